@@ -312,4 +312,102 @@ int verify_greedy_compact(int b, int n, int S, int V, int dtype, const void* log
                           int32_t* predict, int32_t* accept_index, int32_t* accept_lens, int32_t* accepted_tokens,
                           int32_t* next_root, void* ws, size_t ws_bytes, void* stream);
 
+// Pages for new tokens out of the free list: block table, slot table, slot map.
+struct AllocParams {
+  int b, page_size, max_new;
+  const int32_t* req_pool_idx;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  const int32_t* free_ids;
+  int free_cap;
+  const int32_t* n_free;
+  long long num_pages;
+  int32_t* page_table;
+  int req_rows, row_pages;
+  int32_t* req_to_token;  // nullable
+  int row_w;
+  int32_t* cu_new;
+  int32_t* slot_map;
+  int32_t* positions;
+  int slot_cap;
+  int32_t* n_left;
+  uint32_t* error;
+  uint32_t* counters;
+};
+constexpr int kAllocMaxB = 16384;  // the per-CTA scan keeps two prefix sums a request in shared memory
+int launch_alloc_slots(const AllocParams& p, cudaStream_t stream);
+
+// K/V rows quantised into e4m3 pages.
+struct CommitQ8Params {
+  int b, Hkv, D, num_layers, page_size, max_len;
+  const void* k_new[kMaxLayers];
+  const void* v_new[kMaxLayers];
+  void* k_pages[kMaxLayers];
+  void* v_pages[kMaxLayers];
+  uint8_t* k_scales[kMaxLayers];
+  uint8_t* v_scales[kMaxLayers];
+  long long num_rows, new_ld;
+  long long num_pages;
+  const int32_t* page_table;
+  int req_rows, row_pages;
+  const int32_t* req_pool_idx;
+  const int32_t* seq_lens;
+  const int32_t* src_index;  // [b, max_len], or null:
+  const int32_t* src_start;  // [b] first row of each request
+  const int32_t* lens;
+  int32_t* new_seq_lens;
+  uint32_t* error;
+};
+int launch_commit_kv_q8(const CommitQ8Params& p, cudaStream_t stream);
+
+// Verify attention over e4m3 pages and the step's own bf16 rows.
+struct AttentionQ8Params {
+  int b, n, Hq, Hkv, D, page_size;
+  const void* q;
+  long long q_ld;
+  const void* k_new;
+  const void* v_new;
+  long long new_ld;
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  long long num_pages;
+  const int32_t* page_table;
+  int req_rows, row_pages;
+  const int32_t* req_pool_idx;
+  const int32_t* seq_lens;
+  int max_seq_len;
+  const uint64_t* mask_bits;
+  float scale;
+  void* out;
+  float* lse;
+  uint32_t* error;
+  uint32_t* counters;
+  unsigned char* partials;
+};
+// the kernel keeps the tiles before each request in shared memory
+constexpr int kAttentionQ8MaxB = 2048;
+int launch_attention_q8(const AttentionQ8Params& p, cudaStream_t stream);
+size_t attention_q8_partial_bytes();
+
+// Log probabilities of given tokens, entropy and the k best of logit rows.
+struct LogprobParams {
+  int b, n, W, V, dtype, k;
+  const void* logits;
+  const int32_t* row_index;    // [b, W] or null
+  const int32_t* tokens;       // [b, W]
+  const float* temperatures;   // [b] or null
+  float* logprobs;
+  float* entropy;              // nullable
+  int32_t* top_ids;            // [b, W, k]
+  float* top_logprobs;
+  uint32_t* error;
+  uint32_t* counters;          // one a request (zero between calls)
+  unsigned char* partials;
+};
+constexpr int kLogprobMaxK = 32;  // alternatives of a row
+size_t logprob_partial_bytes(long rows, int V);
+int launch_token_logprobs(const LogprobParams& p, cudaStream_t stream);
+
 }  // namespace spec

@@ -99,6 +99,10 @@ size_t partial_bytes(int op, int b, int n, int k, int V, int Hq, int Hkv, int ma
       return attention_partial_bytes();
     case SPEC_OP_COMMIT_KV:
       return commit_partial_bytes(b, n);
+    case SPEC_OP_VERIFY_ATTENTION_Q8:
+      return attention_q8_partial_bytes();
+    case SPEC_OP_TOKEN_LOGPROBS:
+      return logprob_partial_bytes(long(b) * n, V);
     default:
       return 0;
   }
@@ -427,8 +431,9 @@ int spec_build_full_mask(int b, int n, const int32_t* seq_lens, const uint64_t* 
 size_t spec_workspace_size(int op, int b, int n, int k, int V, int Hq, int Hkv, int max_seq_len) {
   if (b < 0 || op < 0 || op > SPEC_OP_LAST) return 0;
   if (b == 0) return kHeaderBytes + counters_bytes(0);
-  if (n < 1 || n > kMaxN || k < 1 || k > kMaxK || V < 1) return 0;
-  if (op == SPEC_OP_VERIFY_ATTENTION && (Hq < 1 || Hkv < 1 || Hq % Hkv || max_seq_len < 0)) return 0;
+  const bool logprobs = op == SPEC_OP_TOKEN_LOGPROBS;
+  if (n < 1 || n > (logprobs ? kMaxN + 1 : kMaxN) || k < 1 || k > (logprobs ? kLogprobMaxK : kMaxK) || V < 1) return 0;
+  if ((op == SPEC_OP_VERIFY_ATTENTION || op == SPEC_OP_VERIFY_ATTENTION_Q8) && (Hq < 1 || Hkv < 1 || Hq % Hkv || max_seq_len < 0)) return 0;
   return kHeaderBytes + counters_bytes(b) + partial_bytes(op, b, n, k, V, Hq, Hkv, max_seq_len);
 }
 
@@ -791,6 +796,204 @@ int spec_commit_kv(int b, int n, int W, int Hkv, int D, int num_layers, int page
   p.counters = v.counters;
   p.partials = v.partials;
   return launch_commit_kv(p, as_stream(stream));
+}
+
+int spec_alloc_slots(int b, int page_size, const int32_t* req_pool_idx, const int32_t* seq_lens,
+                     const int32_t* new_lens, int max_new, const int32_t* free_ids, int free_cap,
+                     const int32_t* n_free, int64_t num_pages, int32_t* page_table, int req_rows, int row_pages,
+                     int32_t* req_to_token, int row_w, int32_t* cu_new, int32_t* slot_map, int32_t* positions,
+                     int slot_cap, int32_t* n_left, void* ws, size_t ws_bytes, void* stream) {
+  if (b < 0 || b > kAllocMaxB || page_size < 1 || max_new < 0 || free_cap < 0 || slot_cap < 0 || req_rows < 1 ||
+      row_pages < 1 || num_pages < 1 || (req_to_token && row_w < 1))
+    return SPEC_ERR_ARG;
+  // slots and positions are int32
+  if (num_pages > (int64_t(1) << 31) / page_size || int64_t(row_pages) * page_size >= (int64_t(1) << 31))
+    return SPEC_ERR_ARG;
+  if (b == 0) return SPEC_OK;
+  if (!req_pool_idx || !seq_lens || !new_lens || !n_free || !page_table || !cu_new || !n_left ||
+      (!free_ids && free_cap > 0) || ((!slot_map || !positions) && slot_cap > 0))
+    return SPEC_ERR_ARG;
+  if (!aligned(slot_map, 16) || !aligned(positions, 16)) return SPEC_ERR_ARG;
+  if (int rc = check_ws(ws, ws_bytes, kHeaderBytes + counters_bytes(b))) return rc;
+  note_other(ws);
+  const WsView v = ws_view(ws, b);
+  AllocParams p{};
+  p.b = b;
+  p.page_size = page_size;
+  p.max_new = max_new;
+  p.req_pool_idx = req_pool_idx;
+  p.seq_lens = seq_lens;
+  p.new_lens = new_lens;
+  p.free_ids = free_ids;
+  p.free_cap = free_cap;
+  p.n_free = n_free;
+  p.num_pages = num_pages;
+  p.page_table = page_table;
+  p.req_rows = req_rows;
+  p.row_pages = row_pages;
+  p.req_to_token = req_to_token;
+  p.row_w = row_w;
+  p.cu_new = cu_new;
+  p.slot_map = slot_map;
+  p.positions = positions;
+  p.slot_cap = slot_cap;
+  p.n_left = n_left;
+  p.error = v.error;
+  p.counters = v.counters;
+  return launch_alloc_slots(p, as_stream(stream));
+}
+
+int spec_commit_kv_q8(int b, int Hkv, int D, int page_size, int num_layers, const void* const* k_new,
+                      const void* const* v_new, int64_t num_rows, int64_t new_ld, void* const* k_pages,
+                      void* const* v_pages, uint8_t* const* k_scales, uint8_t* const* v_scales, int64_t num_pages,
+                      const int32_t* page_table, int req_rows, int row_pages, const int32_t* req_pool_idx,
+                      const int32_t* seq_lens, const int32_t* src_index, const int32_t* src_start,
+                      const int32_t* lens, int max_len, int32_t* new_seq_lens, void* ws, size_t ws_bytes,
+                      void* stream) {
+  if (b < 0 || Hkv < 1 || max_len < 1 || num_rows < 1 || num_pages < 1 || req_rows < 1 || row_pages < 1 ||
+      num_layers < 1 || num_layers > kMaxLayers)
+    return SPEC_ERR_ARG;
+  if ((D != 64 && D != 128) || (page_size != 16 && page_size != 32 && page_size != 64)) return SPEC_ERR_UNSUPPORTED;
+  if (new_ld < int64_t(Hkv) * D || new_ld % 8 || int64_t(row_pages) * page_size >= (int64_t(1) << 31)) return SPEC_ERR_ARG;
+  if (int64_t(b) * ((int64_t(max_len) + page_size - 2) / page_size + 1) >= (int64_t(1) << 31) || Hkv > 65535)
+    return SPEC_ERR_ARG;
+  if (b == 0) return SPEC_OK;
+  if (!k_new || !v_new || !k_pages || !v_pages || !k_scales || !v_scales || !page_table || !req_pool_idx || !seq_lens ||
+      !lens || !new_seq_lens || (!src_index && !src_start))
+    return SPEC_ERR_ARG;
+  if (int rc = check_ws(ws, ws_bytes, kHeaderBytes)) return rc;
+  CommitQ8Params p{};
+  p.b = b;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.num_layers = num_layers;
+  p.page_size = page_size;
+  p.max_len = max_len;
+  for (int i = 0; i < num_layers; ++i) {
+    if (!k_new[i] || !v_new[i] || !k_pages[i] || !v_pages[i] || !k_scales[i] || !v_scales[i]) return SPEC_ERR_ARG;
+    if (!aligned(k_new[i], 16) || !aligned(v_new[i], 16) || !aligned(k_pages[i], 16) || !aligned(v_pages[i], 16))
+      return SPEC_ERR_ARG;
+    p.k_new[i] = k_new[i];
+    p.v_new[i] = v_new[i];
+    p.k_pages[i] = k_pages[i];
+    p.v_pages[i] = v_pages[i];
+    p.k_scales[i] = k_scales[i];
+    p.v_scales[i] = v_scales[i];
+  }
+  note_other(ws);
+  p.num_rows = num_rows;
+  p.new_ld = new_ld;
+  p.num_pages = num_pages;
+  p.page_table = page_table;
+  p.req_rows = req_rows;
+  p.row_pages = row_pages;
+  p.req_pool_idx = req_pool_idx;
+  p.seq_lens = seq_lens;
+  p.src_index = src_index;
+  p.src_start = src_start;
+  p.lens = lens;
+  p.new_seq_lens = new_seq_lens;
+  p.error = ws_view(ws, b).error;
+  return launch_commit_kv_q8(p, as_stream(stream));
+}
+
+int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size, const void* q, int64_t q_ld,
+                             const void* k_new, const void* v_new, int64_t new_ld, const void* k_pages,
+                             const void* v_pages, const uint8_t* k_scales, const uint8_t* v_scales,
+                             int64_t num_pages, const int32_t* page_table, int req_rows, int row_pages,
+                             const int32_t* req_pool_idx, const int32_t* seq_lens, int max_seq_len,
+                             const uint64_t* mask_bits, float scale, void* out, float* lse, void* ws,
+                             size_t ws_bytes, void* stream) {
+  if (b < 0 || b > kAttentionQ8MaxB || n < 1 || n > kMaxN || Hq < 1 || Hkv < 1 || Hq % Hkv || max_seq_len < 0 ||
+      num_pages < 1 || req_rows < 1 || row_pages < 1)
+    return SPEC_ERR_ARG;
+  if ((D != 64 && D != 128) || (page_size != 16 && page_size != 32 && page_size != 64)) return SPEC_ERR_UNSUPPORTED;
+  if (q_ld < int64_t(Hq) * D || q_ld % 8 || new_ld < int64_t(Hkv) * D || new_ld % 8) return SPEC_ERR_ARG;
+  // (page, kv head) units, output rows and 16-key tiles are counted in int32
+  const int64_t tiles = int64_t(max_seq_len) / 16 + 1 + (n + 15) / 16;
+  if (num_pages * Hkv >= (int64_t(1) << 31) || int64_t(b) * n * Hq >= (int64_t(1) << 31) ||
+      int64_t(row_pages) * page_size >= (int64_t(1) << 31) ||
+      int64_t(b) * tiles * Hkv * ((int64_t(n) * (Hq / Hkv) + 15) / 16) >= (int64_t(1) << 31))
+    return SPEC_ERR_ARG;
+  if (b == 0) return SPEC_OK;
+  if (!q || !k_new || !v_new || !k_pages || !v_pages || !k_scales || !v_scales || !page_table || !req_pool_idx ||
+      !seq_lens || !mask_bits || !out)
+    return SPEC_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
+      !aligned(out, 16))
+    return SPEC_ERR_ARG;
+  const size_t need = spec_workspace_size(SPEC_OP_VERIFY_ATTENTION_Q8, b, n, 1, 1, Hq, Hkv, max_seq_len);
+  if (int rc = check_ws(ws, ws_bytes, need)) return rc;
+  note_other(ws);
+  const WsView v = ws_view(ws, b);
+  AttentionQ8Params p{};
+  p.b = b;
+  p.n = n;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.page_size = page_size;
+  p.q = q;
+  p.q_ld = q_ld;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.new_ld = new_ld;
+  p.k_pages = static_cast<const uint8_t*>(k_pages);
+  p.v_pages = static_cast<const uint8_t*>(v_pages);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.num_pages = num_pages;
+  p.page_table = page_table;
+  p.req_rows = req_rows;
+  p.row_pages = row_pages;
+  p.req_pool_idx = req_pool_idx;
+  p.seq_lens = seq_lens;
+  p.max_seq_len = max_seq_len;
+  p.mask_bits = mask_bits;
+  p.scale = scale;
+  p.out = out;
+  p.lse = lse;
+  p.error = v.error;
+  p.counters = v.counters;
+  p.partials = v.partials;
+  return launch_attention_q8(p, as_stream(stream));
+}
+
+int spec_token_logprobs(int b, int n, int W, int V, int dtype, const void* logits, const int32_t* row_index,
+                        const int32_t* tokens, const float* temperatures, int k, float* logprobs,
+                        float* entropy, int32_t* top_ids, float* top_logprobs, void* ws, size_t ws_bytes,
+                        void* stream) {
+  if (b < 0 || n < 1 || n > kMaxN || W < 1 || W > kMaxN + 1 || V < 1 || k < 0 || k > kLogprobMaxK || k > V ||
+      (!row_index && W > n))
+    return SPEC_ERR_ARG;
+  if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || V > (1 << 22)) return SPEC_ERR_UNSUPPORTED;
+  if (int64_t(b) * n >= (int64_t(1) << 31) || int64_t(b) * W * kMaxChunks >= (int64_t(1) << 31)) return SPEC_ERR_ARG;
+  if (b == 0) return SPEC_OK;
+  if (!logits || !tokens || !logprobs || (k > 0 && (!top_ids || !top_logprobs))) return SPEC_ERR_ARG;
+  if (!aligned(logits, size_t(elem_bytes(dtype)))) return SPEC_ERR_ARG;
+  const size_t need = spec_workspace_size(SPEC_OP_TOKEN_LOGPROBS, b, W, k > 0 ? k : 1, V, 0, 0, 0);
+  if (int rc = check_ws(ws, ws_bytes, need)) return rc;
+  note_other(ws);
+  const WsView v = ws_view(ws, b);
+  LogprobParams p{};
+  p.b = b;
+  p.n = n;
+  p.W = W;
+  p.V = V;
+  p.dtype = dtype;
+  p.k = k;
+  p.logits = logits;
+  p.row_index = row_index;
+  p.tokens = tokens;
+  p.temperatures = temperatures;
+  p.logprobs = logprobs;
+  p.entropy = entropy;
+  p.top_ids = top_ids;
+  p.top_logprobs = top_logprobs;
+  p.error = v.error;
+  p.counters = v.counters;
+  p.partials = v.partials;
+  return launch_token_logprobs(p, as_stream(stream));
 }
 
 }  // extern "C"

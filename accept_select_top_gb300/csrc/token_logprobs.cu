@@ -1,0 +1,422 @@
+// token_logprobs.cu -- log probabilities of given tokens, entropy and the k best
+// alternatives of verify rows, in one pass over the logits.
+//
+// With M the row's maximum and y = (x - M) c, c = log2(e) / T:
+//   s = sum 2^y,  t = sum y 2^y,
+//   log p(v) = ln 2 (y_v - log2 s),  H = ln 2 (log2 s - t / s).
+// The difference comes before the factor: x c alone would overflow for masks of
+// the type's lowest value, and its rounding would not cancel.
+//
+// A CTA takes one chunk of one row (a whole row when there are rows enough to
+// fill the GPU).  A thread reads batches of 64 bytes a load group, 32 logits:
+// the batch maximum first (kept in shared memory), then the exponentials
+// relative to the thread's running maximum.  The k best come out of the batch
+// maxima: the CTA's 256 threads form 32 groups (by lane, so that short rows
+// fill all of them), and the k-th largest of the 32 group maxima is a value
+// that at least k logits reach; only the batches whose
+// maximum reaches it are read again (from L2), their logits that reach it are
+// ranked by counting.  Rows need no alignment: the logits before a row's first
+// 16-byte boundary and behind its last are one more batch.
+//   Chunks leave (M, s, t) and their k best; the CTA that arrives last of a
+// request joins the request's rows, one warp a row.
+//
+// Bound: the logits' bytes, read once.
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace spec {
+
+namespace {
+
+constexpr int kLpThreads = 256;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kMaxBatches = 16;  // of a chunk: at most 131072 logits
+constexpr int kListCap = 512;    // batches read again, and logits ranked; more (long ties) take the slow path
+constexpr size_t kLpPartBytes = 16 + size_t(kLogprobMaxK) * 8;
+
+struct LpArgs {
+  LogprobParams p;
+  int chunks, vpc;  // chunks of a row, 16-byte vectors of a chunk
+};
+struct LpPart {
+  float M, s, t;
+  int count;
+};
+
+template <typename T>
+struct LpRow {
+  const T* row;
+  int V, head, nvec, tail;
+  __device__ LpRow(const void* logits, long long idx, int v) : V(v) {
+    constexpr int E = VecOps<T>::E;
+    row = static_cast<const T*>(logits) + idx * (long long)v;
+    const int off = int(reinterpret_cast<uintptr_t>(row) & 15) / int(sizeof(T));
+    head = off ? min(E - off, v) : 0;
+    nvec = (v - head) / E;
+    tail = v - head - nvec * E;
+  }
+  __device__ const uint4* vecs() const { return reinterpret_cast<const uint4*>(row + head); }
+  // the element that thread t < head + tail holds of the edge batch
+  __device__ int edge(int t) const { return t < head ? t : V - tail + (t - head); }
+};
+
+__device__ __forceinline__ float scale_of_row(const LogprobParams& a, long long idx) {
+  const float T = a.temperatures ? a.temperatures[idx / a.n] : 1.f;
+  return T > 0.f ? 1.4426950408889634f / T : 1.4426950408889634f;
+}
+
+// Results of one row from its joined statistics and its k best (count of them
+// with a value above -inf, in order); one warp.
+template <typename T>
+__device__ void finish_row(const LogprobParams& a, int out_row, long long idx, float M, float s, float t,
+                           float c, int count, const float* tv, int* ti) {
+  const int lane = threadIdx.x & 31;
+  const float ls = log2f(s);
+  const T* row = static_cast<const T*>(a.logits) + idx * (long long)a.V;
+  auto logp = [&](float x) {
+    return M == -INFINITY || !(x > -INFINITY) ? -INFINITY : ((x - M) * c - ls) * 0.6931471805599453f;
+  };
+  if (lane == 0) {
+    const int tok = a.tokens[out_row];
+    float lp = 0.f;
+    if (tok >= a.V) raise_error(a.error, SPEC_DEV_INDEX);
+    else if (tok >= 0) lp = logp(LogitTraits<T>::load(row, tok));
+    a.logprobs[out_row] = lp;
+    if (a.entropy) a.entropy[out_row] = M == -INFINITY ? 0.f : (ls - t / s) * 0.6931471805599453f;
+  }
+  if (a.k > 0) {
+    // fewer than k logits above -inf: the lowest other indices follow
+    for (int base = 0; count < a.k && base < a.V; base += 32) {
+      const int i = base + lane;
+      bool other = i < a.V;
+      for (int q = 0; q < count; ++q) other = other && ti[q] != i;
+      const unsigned who = __ballot_sync(0xffffffffu, other);
+      const int at = count + __popc(who & ((1u << lane) - 1u));
+      __syncwarp();
+      if (other && at < a.k) ti[at] = i;
+      count = min(a.k, count + __popc(who));
+      __syncwarp();
+    }
+    if (lane < a.k) {
+      const int i = ti[lane];
+      a.top_ids[size_t(out_row) * a.k + lane] = i;
+      a.top_logprobs[size_t(out_row) * a.k + lane] = logp(LogitTraits<T>::load(row, i));
+    }
+  }
+}
+
+__device__ void blank_row(const LogprobParams& a, int out_row) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) {
+    a.logprobs[out_row] = 0.f;
+    if (a.entropy) a.entropy[out_row] = 0.f;
+  }
+  if (lane < a.k) {
+    a.top_ids[size_t(out_row) * a.k + lane] = -1;
+    a.top_logprobs[size_t(out_row) * a.k + lane] = 0.f;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(LpArgs args) {
+  constexpr int E = VecOps<T>::E, U = kBatch / E;
+  const LogprobParams& a = args.p;
+  __shared__ float bmax[kMaxBatches + 1][kLpThreads];
+  __shared__ float gmax[kLpWarps][32], red[2][kLpWarps];
+  __shared__ float cv[kListCap];
+  __shared__ int ci[kListCap], list[kListCap];
+  __shared__ int n_list, n_cand;
+  __shared__ float tv[kLpWarps][kLogprobMaxK];
+  __shared__ int ti[kLpWarps][kLogprobMaxK];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int out_row = blockIdx.x / args.chunks, ch = blockIdx.x % args.chunks, req = out_row / a.W;
+  auto row_at = [&](int r, bool report) {
+    long long i = a.row_index ? a.row_index[r] : (long long)(r / a.W) * a.n + r % a.W;
+    if (i >= (long long)a.b * a.n) {
+      if (report) raise_error(a.error, SPEC_DEV_INDEX);
+      i = -1;
+    }
+    return i;
+  };
+  const long long idx = row_at(out_row, ch == 0 && tid == 0);
+  if (idx < 0 && args.chunks == 1) {
+    if (w == 0) blank_row(a, out_row);
+    return;
+  }
+  float M = -INFINITY, s = 0.f, t = 0.f, c = 0.f;
+  int count = 0;
+  if (idx >= 0) {
+    if (tid == 0) n_list = n_cand = 0;
+    c = scale_of_row(a, idx);
+    const LpRow<T> row(a.logits, idx, a.V);
+    const uint4* vp = row.vecs();
+    const int v0 = ch * args.vpc, v1 = min(row.nvec, v0 + args.vpc);
+    const int nb = v1 > v0 ? (v1 - v0 + U * kLpThreads - 1) / (U * kLpThreads) : 0;
+    // ---- one pass: batch maxima, running maximum, s and t ----
+    float m = -INFINITY;
+    auto raise = [&](float bm) {  // the thread's maximum moves to bm
+      if (s > 0.f) {
+        const float d = fmaxf((m - bm) * c, -150.f), f = fast_exp2(d);
+        t = f * fmaf(d, s, t);
+        s *= f;
+      }
+      m = bm;
+    };
+    for (int q = 0; q < nb; ++q) {
+      uint4 x[U];
+      const int vb = v0 + q * U * kLpThreads + tid;
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[u] = vb + u * kLpThreads < v1 ? ld_stream(vp + vb + u * kLpThreads) : VecOps<T>::neg_inf();
+      float bm = VecOps<T>::vmax(x[0]);
+#pragma unroll
+      for (int u = 1; u < U; ++u) bm = fmaxf(bm, VecOps<T>::vmax(x[u]));
+      bmax[q][tid] = bm;
+      if (bm > m) raise(bm);
+      if (m > -INFINITY) {
+        float s2[2] = {0.f, 0.f}, t2[2] = {0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            // (-inf, and NaN, count as 0: 2^-150 flushes)
+            const float y = fmaxf((VecOps<T>::at(x[u], e) - m) * c, -150.f);
+            const float p = fast_exp2(y);
+            s2[e & 1] += p;
+            t2[e & 1] = fmaf(y, p, t2[e & 1]);
+          }
+        s += s2[0] + s2[1];
+        t += t2[0] + t2[1];
+      }
+    }
+    const bool edges = ch == 0 && row.head + row.tail > 0;
+    if (edges) {
+      const float x = tid < row.head + row.tail ? LogitTraits<T>::load(row.row, row.edge(tid)) : -INFINITY;
+      bmax[nb][tid] = x == x ? x : -INFINITY;
+      if (x > m) raise(x);
+      if (x > -INFINITY) {
+        const float y = fmaxf((x - m) * c, -150.f), p = fast_exp2(y);
+        s += p;
+        t = fmaf(y, p, t);
+      }
+    }
+    // ---- the chunk's maximum and sums; the 32 group maxima ----
+    gmax[w][lane] = m;
+    __syncthreads();
+    float gv = gmax[0][lane];
+#pragma unroll
+    for (int q = 1; q < kLpWarps; ++q) gv = fmaxf(gv, gmax[q][lane]);
+    M = warp_max(gv);
+    raise(M);
+    s = warp_sum(s);
+    t = warp_sum(t);
+    if (lane == 0) {
+      red[0][w] = s;
+      red[1][w] = t;
+    }
+    float theta = -INFINITY;
+    if (a.k > 0) {
+      // the k-th largest group maximum (counting; ties by lane)
+      int rank = 0;
+#pragma unroll
+      for (int o = 0; o < 32; ++o) {
+        const float v = __shfl_sync(0xffffffffu, gv, o);
+        rank += v > gv || (v == gv && o < lane);
+      }
+      const unsigned who = __ballot_sync(0xffffffffu, rank == a.k - 1);
+      theta = __shfl_sync(0xffffffffu, gv, __ffs(who) - 1);
+      const int all = nb + (edges ? 1 : 0);
+      if (m >= theta)
+        for (int q = 0; q < all; ++q) {
+          const float bm = bmax[q][tid];
+          if (bm >= theta && bm > -INFINITY) {
+            const int at = atomicAdd(&n_list, 1);
+            if (at < kListCap) list[at] = q * kLpThreads + tid;
+          }
+        }
+    }
+    __syncthreads();
+    s = t = 0.f;
+#pragma unroll
+    for (int q = 0; q < kLpWarps; ++q) {
+      s += red[0][q];
+      t += red[1][q];
+    }
+    if (a.k > 0) {
+      const int nl = n_list;
+      if (nl <= kListCap) {
+        for (int e = w; e < nl; e += kLpWarps) {
+          const int q = list[e] / kLpThreads, th = list[e] % kLpThreads;
+          int i = -1;
+          if (q == nb) {
+            if (lane == 0) i = row.edge(th);
+          } else {
+            const int v = v0 + (q * U + lane / E) * kLpThreads + th;
+            if (v < v1) i = row.head + v * E + lane % E;
+          }
+          const float x = i >= 0 ? LogitTraits<T>::load(row.row, i) : -INFINITY;
+          if (x >= theta && x > -INFINITY) {
+            const int at = atomicAdd(&n_cand, 1);
+            if (at < kListCap) {
+              cv[at] = x;
+              ci[at] = i;
+            }
+          }
+        }
+        __syncthreads();
+      }
+      const int nc = n_cand;
+      if (nl <= kListCap && nc <= kListCap) {
+        count = min(a.k, nc);
+        for (int i = tid; i < nc; i += kLpThreads) {
+          int rank = 0;
+          for (int q = 0; q < nc; ++q) rank += better(cv[q], ci[q], cv[i], ci[i]);
+          if (rank < a.k) {
+            tv[0][rank] = cv[i];
+            ti[0][rank] = ci[i];
+          }
+        }
+      } else {
+        // long ties: k rounds, each the best logit after the last one's
+        float pv = INFINITY;
+        int pi = -1;
+        for (count = 0; count < a.k; ++count) {
+          float bv = -INFINITY;
+          int bi = INT_MAX;
+          const int n_edge = edges ? row.head + row.tail : 0;
+          const int elems = (v1 - v0) * E + n_edge;
+          for (int q = tid; q < elems; q += kLpThreads) {
+            const int i = q < n_edge ? row.edge(q) : row.head + v0 * E + (q - n_edge);
+            const float x = LogitTraits<T>::load(row.row, i);
+            if (x > -INFINITY && better(pv, pi, x, i) && better(x, i, bv, bi)) {
+              bv = x;
+              bi = i;
+            }
+          }
+          warp_argmax(bv, bi);
+          __syncthreads();
+          if (lane == 0) {
+            red[0][w] = bv;
+            list[w] = bi;
+          }
+          __syncthreads();
+          for (int q = 0; q < kLpWarps; ++q)
+            if (better(red[0][q], list[q], bv, bi)) {
+              bv = red[0][q];
+              bi = list[q];
+            }
+          if (bi == INT_MAX) break;
+          if (tid == 0) {
+            tv[0][count] = bv;
+            ti[0][count] = bi;
+          }
+          pv = bv;
+          pi = bi;
+        }
+      }
+      __syncthreads();
+    }
+    if (args.chunks == 1) {
+      if (w == 0) finish_row<T>(a, out_row, idx, M, s, t, c, count, tv[0], ti[0]);
+      return;
+    }
+    unsigned char* part = a.partials + size_t(blockIdx.x) * kLpPartBytes;
+    if (tid == 0) *reinterpret_cast<LpPart*>(part) = LpPart{M, s, t, count};
+    if (tid < count) reinterpret_cast<float2*>(part + 16)[tid] = make_float2(tv[0][tid], __int_as_float(ti[0][tid]));
+  }
+  // ---- the last CTA of the request joins its rows, one warp a row, one lane a chunk ----
+  if (!arrive_last(a.counters + req, uint32_t(a.W) * uint32_t(args.chunks))) return;
+  for (int r = w; r < a.W; r += kLpWarps) {
+    const int orow = req * a.W + r;
+    const long long ix = row_at(orow, false);
+    if (ix < 0) {
+      blank_row(a, orow);
+      continue;
+    }
+    const float cc = scale_of_row(a, ix);
+    const unsigned char* part = a.partials + (size_t(orow) * args.chunks + lane) * kLpPartBytes;
+    float pM = -INFINITY, ps = 0.f, pt = 0.f;
+    int pc = 0;
+    if (lane < args.chunks) {
+      const float4 h = __ldcg(reinterpret_cast<const float4*>(part));
+      pM = h.x;
+      ps = h.y;
+      pt = h.z;
+      pc = __float_as_int(h.w);
+    }
+    const float jM = warp_max(pM);
+    const float d = fmaxf((pM - jM) * cc, -150.f), f = fast_exp2(d);
+    const float js = warp_sum(ps > 0.f ? f * ps : 0.f), jt = warp_sum(ps > 0.f ? f * fmaf(d, ps, pt) : 0.f);
+    int got = 0, head = 0;
+    if (a.k > 0) {
+      // the chunks' sorted lists: k times the best head
+      auto fetch = [&](int at, float& v, int& i) {
+        v = -INFINITY;
+        i = INT_MAX;
+        if (at < pc) {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(part + 16) + at);
+          v = x.x;
+          i = __float_as_int(x.y);
+        }
+      };
+      float hv, nv;
+      int hi, ni;
+      fetch(0, hv, hi);
+      fetch(1, nv, ni);
+      for (; got < a.k; ++got) {
+        float bv = hv;
+        int bi = hi;
+        warp_argmax(bv, bi);
+        if (bi == INT_MAX || !(bv > -INFINITY)) break;
+        if (lane == 0) {
+          tv[w][got] = bv;
+          ti[w][got] = bi;
+        }
+        if (hi == bi) {
+          hv = nv;
+          hi = ni;
+          ++head;
+          fetch(head + 1, nv, ni);
+        }
+      }
+      __syncwarp();
+    }
+    finish_row<T>(a, orow, ix, jM, js, jt, cc, got, tv[w], ti[w]);
+    __syncwarp();
+  }
+  __syncthreads();
+  counter_reset(a.counters + req);
+}
+
+// Chunks of a row: about six CTAs a SM in all, at least 2048 logits and at most
+// kMaxBatches batches a chunk.
+int lp_chunks(long rows, int V) {
+  long want = (6 * 152 + rows - 1) / rows;
+  const long by_size = V / 2048 > 1 ? V / 2048 : 1;
+  if (want > by_size) want = by_size;
+  if (want > kMaxChunks) want = kMaxChunks;
+  const long need = (long(V) + kMaxBatches * kBatch * kLpThreads - 1) / (kMaxBatches * kBatch * kLpThreads);
+  if (want < need) want = need;
+  return int(want);
+}
+
+}  // namespace
+
+size_t logprob_partial_bytes(long rows, int V) { return align256(size_t(rows) * lp_chunks(rows, V) * kLpPartBytes); }
+
+int launch_token_logprobs(const LogprobParams& p, cudaStream_t stream) {
+  const long rows = long(p.b) * p.W;
+  LpArgs args{p, lp_chunks(rows, p.V), 0};
+  if (args.chunks > kMaxChunks) return SPEC_ERR_UNSUPPORTED;
+  const int E = p.dtype == SPEC_F32 ? 4 : 8;
+  args.vpc = (p.V / E + args.chunks - 1) / args.chunks;
+  if (args.vpc < 1) args.vpc = 1;
+  const dim3 grid(unsigned(rows * args.chunks));
+  const cudaError_t e =
+      p.dtype == SPEC_F32 ? launch_pdl(token_logprobs_kernel<float>, grid, dim3(kLpThreads), 0, stream, args)
+                          : launch_pdl(token_logprobs_kernel<uint16_t>, grid, dim3(kLpThreads), 0, stream, args);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+}
+
+}  // namespace spec

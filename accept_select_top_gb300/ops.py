@@ -21,8 +21,9 @@ LIB_PATH = os.path.join(_HERE, "_build", "libspecdec.so")
 SPEC_OK = 0
 SPEC_F32, SPEC_BF16 = 0, 1
 (OP_SELECT_TOPK, OP_BUILD_TREE, OP_VERIFY_ATTENTION, OP_VERIFY_GREEDY, OP_VERIFY_SAMPLING, OP_COMMIT_KV,
- OP_VERIFY_TARGET_ONLY) = range(7)
-DEV_INDEX, DEV_INVARIANT, DEV_LENGTH = 1, 2, 4
+ OP_VERIFY_TARGET_ONLY, OP_ALLOC_SLOTS, OP_COMMIT_KV_Q8, OP_VERIFY_ATTENTION_Q8, OP_TOKEN_LOGPROBS) = range(11)
+DEV_INDEX, DEV_INVARIANT, DEV_LENGTH, DEV_TIMEOUT, DEV_SPACE = 1, 2, 4, 8, 16
+Q8_EXP_MIN = 16  # smallest scale exponent byte the library writes (the scale is 2^(e - 127))
 _ERRORS = {-1: "bad argument", -2: "workspace too small or misaligned", -3: "CUDA launch failed",
            -4: "unsupported dtype or head size"}
 
@@ -31,7 +32,8 @@ EXPORTS = ["spec_workspace_size", "spec_workspace_init", "spec_workspace_set_ove
            "spec_verify_greedy", "spec_verify_sampling", "spec_verify_target_only", "spec_build_chain_tree",
            "spec_verify_chain_greedy", "spec_assign_draft_locs", "spec_duplicate_prefix_tail",
            "spec_build_full_mask", "spec_add_penalties", "spec_renorm_probs", "spec_verify_sampling_probs",
-           "spec_verify_target_only_probs", "spec_commit_kv", "spec_verify_greedy_noalloc",
+           "spec_verify_target_only_probs", "spec_commit_kv", "spec_alloc_slots", "spec_commit_kv_q8",
+           "spec_verify_attention_q8", "spec_token_logprobs", "spec_verify_greedy_noalloc",
            "spec_noalloc_last_error"]
 
 
@@ -66,6 +68,11 @@ def _load() -> ctypes.CDLL:
         "spec_verify_sampling_probs": (I, [I, I, I, I, P, P, P, P, P, P, P, P, P, P, P, P, P, P, Z, P]),
         "spec_verify_target_only_probs": (I, [I, I, I, I, P, P, P, F, F, P, P, P, P, P, P, P, P, P, P, Z, P]),
         "spec_commit_kv": (I, [I, I, I, I, I, I, I, P, P, L, P, I, I, P, P, P, P, P, P, P, P, P, Z, P]),
+        "spec_alloc_slots": (I, [I, I, P, P, P, I, P, I, P, L, P, I, I, P, I, P, P, P, I, P, P, Z, P]),
+        "spec_commit_kv_q8": (I, [I, I, I, I, I, P, P, L, L, P, P, P, P, L, P, I, I, P, P, P, P, P, I, P, P, Z, P]),
+        "spec_verify_attention_q8": (I, [I, I, I, I, I, I, P, L, P, P, L, P, P, P, P, L, P, I, I, P, P, I, P, F, P, P,
+                                         P, Z, P]),
+        "spec_token_logprobs": (I, [I, I, I, I, I, P, P, P, P, I, P, P, P, P, P, Z, P]),
         "spec_verify_greedy_noalloc": (I, [I, I, I, I, I, P, P, P, P, P, P, P, P, P, P, P]),
         "spec_noalloc_last_error": (I, [P]),
     }
@@ -115,6 +122,7 @@ class Workspace:
         self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=device or "cuda")
         # zero-filled through the C ABI, which also forgets any earlier
         # workspace that lived at this address
+        self.address = self.tensor.data_ptr()
         _check(LIB.spec_workspace_init(self.ptr, ctypes.c_size_t(self.nbytes), _stream(stream)),
                "spec_workspace_init")
 
@@ -305,6 +313,192 @@ def spec_commit_kv(b: int, n: int, W: int, Hkv: int, D: int, page_size: int, k_l
                               req_to_token.shape[0], req_to_token.shape[1], _ptr(req_pool_idx), _ptr(seq_lens),
                               _ptr(verify_loc), _ptr(accept_index), _ptr(accept_lens), _ptr(new_seq_lens),
                               _ptr(free_ids), _ptr(n_free), ws.ptr, ws.nbytes, _stream(stream)), "spec_commit_kv")
+
+
+# ------------------------------------------------ the 8-bit paged cache, token log probabilities
+#
+# These calls check what a wrong tensor would turn into a stray access: type,
+# device, contiguity and the number of elements the sizes call for.
+
+_I32, _F32, _I64, _BF16 = torch.int32, torch.float32, torch.int64, torch.bfloat16
+_E4M3 = torch.float8_e4m3fn
+
+
+def _in(t: torch.Tensor, dtype, least: int, dev: int, what: str) -> int:
+    """Address of a contiguous tensor of `dtype` with at least `least` elements on device `dev`."""
+    if t.dtype is not dtype:
+        raise SpecError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise SpecError(f"{what}: expected a tensor on the current CUDA device")
+    if not t.is_contiguous():
+        raise SpecError(f"{what}: expected a contiguous tensor")
+    if t.numel() < least:
+        raise SpecError(f"{what}: {t.numel()} elements, {least} are needed")
+    return t.data_ptr()
+
+
+def _pages_in(t: torch.Tensor, shape, dev: int, what: str) -> int:
+    """Address of e4m3 pages [num_pages, Hkv, page_size, D] (float8_e4m3fn, or their bytes)."""
+    if t.dtype is not _E4M3 and t.dtype is not torch.uint8:
+        raise SpecError(f"{what}: expected float8_e4m3fn or uint8, got {t.dtype}")
+    if t.shape[1:] != shape:
+        raise SpecError(f"{what}: expected [num_pages, {', '.join(map(str, shape))}], got {tuple(t.shape)}")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise SpecError(f"{what}: expected a contiguous tensor on the current CUDA device")
+    return t.data_ptr()
+
+
+def _rows_in(t: torch.Tensor, heads: int, D: int, least: int, dev: int, what: str):
+    """Address and row stride of bf16 rows [rows, heads, D]; the rows may be a view of wider ones."""
+    if t.dtype is not _BF16:
+        raise SpecError(f"{what}: expected {_BF16}, got {t.dtype}")
+    rows, h, d = t.shape
+    if h != heads or d != D or rows < least:
+        raise SpecError(f"{what}: expected at least {least} rows [{heads}, {D}], got {tuple(t.shape)}")
+    ld, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != D and h > 1) or (rows > 1 and ld < heads * D):
+        raise SpecError(f"{what}: expected each row's [{heads}, {D}] contiguous")
+    if t.get_device() != dev:
+        raise SpecError(f"{what}: expected a tensor on the current CUDA device")
+    return t.data_ptr(), (ld if rows > 1 else heads * D)
+
+
+def _device() -> int:
+    return torch.cuda.current_device()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+class LayerList:
+    """One tensor a layer, all of one shape, type and strides, with the host array of their
+    addresses that the calls over every layer take (built once; the tensors are kept alive)."""
+
+    def __init__(self, tensors: Sequence[torch.Tensor]):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise SpecError("a layer list needs at least one layer")
+        t0 = self.tensors[0]
+        for t in self.tensors[1:]:
+            if t.shape != t0.shape or t.dtype != t0.dtype or t.stride() != t0.stride() or t.device != t0.device:
+                raise SpecError("the layers of a list must have one shape, type, stride and device")
+        self.first = t0
+        self.array = (ctypes.c_void_p * len(self.tensors))(*[t.data_ptr() for t in self.tensors])
+        self.ptr = ctypes.addressof(self.array)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _layers(x) -> LayerList:
+    return x if isinstance(x, LayerList) else LayerList(x)
+
+
+def spec_alloc_slots(b: int, page_size: int, req_pool_idx, seq_lens, new_lens, max_new: int, free_ids, n_free,
+                     num_slots: int, page_table, req_to_token, cu_new, slot_map, positions, n_left, ws: Workspace,
+                     stream=None):
+    """Pages for new_lens[b] more tokens a request from the free list (a stack: n_free[0] ids); see
+    the header.  num_slots is the pool's size in tokens; req_to_token may be None; n_left may be n_free."""
+    dev = _device()
+    slots = min(slot_map.numel(), positions.numel())
+    width = 0
+    if req_to_token is not None:
+        width = req_to_token.shape[1]
+        if req_to_token.shape[0] != page_table.shape[0]:
+            raise SpecError("req_to_token and page_table must have the same rows")
+    rows, row_pages = page_table.shape
+    _check(LIB.spec_alloc_slots(
+        b, page_size, _in(req_pool_idx, _I32, b, dev, "req_pool_idx"), _in(seq_lens, _I32, b, dev, "seq_lens"),
+        _in(new_lens, _I32, b, dev, "new_lens"), max_new, _in(free_ids, _I32, 0, dev, "free_ids"), free_ids.numel(),
+        _in(n_free, _I32, 1, dev, "n_free"), num_slots // page_size if page_size > 0 else 0,
+        _in(page_table, _I32, 1, dev, "page_table"), rows, row_pages,
+        None if req_to_token is None else _in(req_to_token, _I32, 1, dev, "req_to_token"), width,
+        _in(cu_new, _I32, b + 1, dev, "cu_new"), _in(slot_map, _I32, 0, dev, "slot_map"),
+        _in(positions, _I32, 0, dev, "positions"), slots, _in(n_left, _I32, 1, dev, "n_left"), ws.address, ws.nbytes,
+        _raw_stream(stream, dev)), "spec_alloc_slots")
+
+
+def spec_commit_kv_q8(b: int, Hkv: int, D: int, page_size: int, k_new, v_new, k_pages, v_pages, k_scales, v_scales,
+                      page_table, req_pool_idx, seq_lens, src_index, src_start, lens, max_len: int, new_seq_lens,
+                      ws: Workspace, stream=None):
+    """Quantises bf16 rows into the e4m3 pages of every layer.  k_new .. v_scales: one tensor a layer
+    (a sequence, or a LayerList kept by the caller).  src_index [b, max_len] (accept_index) or
+    src_start [b]; the other may be None."""
+    dev = _device()
+    k_new, v_new, k_pages, v_pages = _layers(k_new), _layers(v_new), _layers(k_pages), _layers(v_pages)
+    k_scales, v_scales = _layers(k_scales), _layers(v_scales)
+    layers = len(k_new)
+    if not all(len(x) == layers for x in (v_new, k_pages, v_pages, k_scales, v_scales)):
+        raise SpecError("every layer list must have the same length")
+    num_rows, num_pages = k_new.first.shape[0], k_pages.first.shape[0]
+    _, ld = _rows_in(k_new.first, Hkv, D, 1, dev, "k_new")
+    _, ldv = _rows_in(v_new.first, Hkv, D, num_rows, dev, "v_new")
+    if ldv != ld:
+        raise SpecError("k_new and v_new must have one row stride")
+    shape = (Hkv, page_size, D)
+    _pages_in(k_pages.first, shape, dev, "k_pages")
+    _pages_in(v_pages.first, shape, dev, "v_pages")
+    if v_pages.first.shape[0] != num_pages:
+        raise SpecError("k_pages and v_pages must have as many pages")
+    _in(k_scales.first, torch.uint8, num_pages * Hkv, dev, "k_scales")
+    _in(v_scales.first, torch.uint8, num_pages * Hkv, dev, "v_scales")
+    rows, row_pages = page_table.shape
+    _check(LIB.spec_commit_kv_q8(
+        b, Hkv, D, page_size, layers, k_new.ptr, v_new.ptr, num_rows, ld, k_pages.ptr, v_pages.ptr, k_scales.ptr,
+        v_scales.ptr, num_pages, _in(page_table, _I32, 1, dev, "page_table"), rows, row_pages,
+        _in(req_pool_idx, _I32, b, dev, "req_pool_idx"), _in(seq_lens, _I32, b, dev, "seq_lens"),
+        None if src_index is None else _in(src_index, _I32, b * max_len, dev, "src_index"),
+        None if src_start is None else _in(src_start, _I32, b, dev, "src_start"), _in(lens, _I32, b, dev, "lens"),
+        max_len, _in(new_seq_lens, _I32, b, dev, "new_seq_lens"), ws.address, ws.nbytes, _raw_stream(stream, dev)),
+        "spec_commit_kv_q8")
+
+
+def spec_verify_attention_q8(b: int, n: int, Hq: int, Hkv: int, D: int, page_size: int, q, k_new, v_new, k_pages,
+                             v_pages, k_scales, v_scales, page_table, req_pool_idx, seq_lens, max_seq_len: int,
+                             mask_bits, scale: float, out, lse, ws: Workspace, stream=None):
+    """Verify attention over the e4m3 pages and the step's own bf16 rows; q, k_new and v_new
+    ([b*n, heads, D]) may be views of one packed projection.  lse may be None."""
+    dev = _device()
+    rows = b * n
+    qp, q_ld = _rows_in(q, Hq, D, rows, dev, "q")
+    kp, ld = _rows_in(k_new, Hkv, D, rows, dev, "k_new")
+    vp, ldv = _rows_in(v_new, Hkv, D, rows, dev, "v_new")
+    if ldv != ld:
+        raise SpecError("k_new and v_new must have one row stride")
+    num_pages = k_pages.shape[0]
+    if v_pages.shape[0] != num_pages:
+        raise SpecError("k_pages and v_pages must have as many pages")
+    shape = (Hkv, page_size, D)
+    table_rows, row_pages = page_table.shape
+    _check(LIB.spec_verify_attention_q8(
+        b, n, Hq, Hkv, D, page_size, qp, q_ld, kp, vp, ld, _pages_in(k_pages, shape, dev, "k_pages"),
+        _pages_in(v_pages, shape, dev, "v_pages"), _in(k_scales, torch.uint8, num_pages * Hkv, dev, "k_scales"),
+        _in(v_scales, torch.uint8, num_pages * Hkv, dev, "v_scales"), num_pages,
+        _in(page_table, _I32, 1, dev, "page_table"), table_rows, row_pages,
+        _in(req_pool_idx, _I32, b, dev, "req_pool_idx"), _in(seq_lens, _I32, b, dev, "seq_lens"), max_seq_len,
+        _in(mask_bits, _I64, rows, dev, "mask_bits"), scale, _in(out, _BF16, rows * Hq * D, dev, "out"),
+        None if lse is None else _in(lse, _F32, rows * Hq, dev, "lse"), ws.address, ws.nbytes,
+        _raw_stream(stream, dev)), "spec_verify_attention_q8")
+
+
+def spec_token_logprobs(b: int, n: int, W: int, logits, row_index, tokens, temperatures, k: int, logprobs, entropy,
+                        top_ids, top_logprobs, ws: Workspace, stream=None):
+    """Log probabilities of tokens [b, W] at verify rows row_index [b, W] (accept_index; None: b*n + j),
+    entropy (None: not wanted) and the k best alternatives."""
+    dev = _device()
+    V = logits.shape[-1]
+    rows = b * W
+    _check(LIB.spec_token_logprobs(
+        b, n, W, V, _dtype_code(logits), _in(logits, logits.dtype, b * n * V, dev, "logits"),
+        None if row_index is None else _in(row_index, _I32, rows, dev, "row_index"),
+        _in(tokens, _I32, rows, dev, "tokens"),
+        None if temperatures is None else _in(temperatures, _F32, b, dev, "temperatures"), k,
+        _in(logprobs, _F32, rows, dev, "logprobs"),
+        None if entropy is None else _in(entropy, _F32, rows, dev, "entropy"),
+        None if top_ids is None else _in(top_ids, _I32, rows * k, dev, "top_ids"),
+        None if top_logprobs is None else _in(top_logprobs, _F32, rows * k, dev, "top_logprobs"), ws.address, ws.nbytes,
+        _raw_stream(stream, dev)), "spec_token_logprobs")
 
 
 def spec_verify_greedy_noalloc(b: int, n: int, S: int, logits, draft_tokens, retrieve_index, next_token,

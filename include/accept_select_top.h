@@ -72,6 +72,7 @@ extern "C" {
 #define SPEC_DEV_INDEX 1u      /* an index read from an input array was out of range */
 #define SPEC_DEV_INVARIANT 2u  /* a selected node's parent was not selected (build_tree) */
 #define SPEC_DEV_LENGTH 4u     /* a length (seq_len, accept_len) outside its valid range */
+#define SPEC_DEV_SPACE 16u     /* the free list or the slot map is too small (alloc_slots); nothing was handed out */
 #define SPEC_DEV_TIMEOUT 8u    /* a bounded device-side wait ran out; the kernel stopped cleanly */
 
 /* operation ids for spec_workspace_size */
@@ -82,7 +83,11 @@ extern "C" {
 #define SPEC_OP_VERIFY_SAMPLING 4
 #define SPEC_OP_COMMIT_KV 5
 #define SPEC_OP_VERIFY_TARGET_ONLY 6
-#define SPEC_OP_LAST SPEC_OP_VERIFY_TARGET_ONLY
+#define SPEC_OP_ALLOC_SLOTS 7
+#define SPEC_OP_COMMIT_KV_Q8 8
+#define SPEC_OP_VERIFY_ATTENTION_Q8 9
+#define SPEC_OP_TOKEN_LOGPROBS 10 /* n: rows a request (W, up to 65), k: alternatives (up to 32) */
+#define SPEC_OP_LAST SPEC_OP_TOKEN_LOGPROBS
 
 /* Bytes of workspace the operation needs for these sizes (b requests, n tree
  * nodes, k = topk, V vocabulary, Hq query heads, Hkv kv heads, max_seq_len an
@@ -455,6 +460,121 @@ int spec_commit_kv(int b, int n, int W, int Hkv, int D, int num_layers, int page
                    const int32_t* accept_lens, int32_t* new_seq_lens,
                    int32_t* free_ids, int32_t* n_free,
                    void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit paged KV cache.  The pages have no counterpart; it is the verify
+ * step's cache at half the bytes of the bf16 pools.
+ *
+ * A layer's K (and its V) is [num_pages, Hkv, page_size, D] e4m3 bytes: a page
+ * holds page_size (16, 32 or 64) consecutive tokens of one request, each kv
+ * head's block of it contiguous.  Its scales are [num_pages, Hkv] bytes e, one
+ * for each page and kv head: a stored value stands for e4m3 * 2^(e - 127)
+ * (e in [1, 254]; the library writes SPEC_Q8_EXP_MIN to 247).  page_table is
+ * [req_rows, row_pages] int32: position x of request b lies in page
+ * page_table[req_pool_idx[b]][x / page_size] at x % page_size.  Pools are
+ * 16-byte aligned.  A request's tree rows never enter the cache before they are
+ * accepted: the attention reads them as the step's own bf16 rows, so nothing
+ * is quantised twice and nothing rejected has to be taken back.  One step:
+ *   spec_verify_attention_q8 (each layer)   accept   spec_alloc_slots with the
+ *   accepted lengths   spec_commit_kv_q8
+ * ------------------------------------------------------------------------- */
+#define SPEC_Q8_EXP_MIN 16
+
+/* spec_alloc_slots -- pages for new tokens from a free list, and the tables that
+ * follow from the lengths.  With L = seq_lens[b] cached tokens and m =
+ * new_lens[b] (0 <= m <= max_new) to come, request b gets the pages
+ * [ceil(L / page_size), ceil((L + m) / page_size)) of its table row; in
+ * request order, then page order, the j-th page of the call is
+ * free_ids[n_free[0] - 1 - j] (the list is a stack: spec_commit_kv's free_ids
+ * and n_free are one, where page_size is that call's).
+ * Outputs: page_table entries of the new pages; req_to_token (nullable,
+ *   [req_rows, row_w], the slot table the other calls read) entries [L, L + m);
+ *   cu_new [b+1] = new tokens before each request; slot_map and positions
+ *   [slot_cap]: for token j of request b, at cu_new[b] + j, the slot page *
+ *   page_size + (L + j) % page_size and the position L + j (entries past the
+ *   last token stay as they are; both 16-byte aligned); n_left [1] = n_free
+ *   less the pages taken (may be n_free itself).
+ * A page_size of 1 makes page_table the slot table (any page_size >= 1 whose
+ * slots stay below 2^31).  A request with a bad length or row gets nothing
+ * (SPEC_DEV_LENGTH / SPEC_DEV_INDEX).  A free list or a slot map that is too
+ * small sets SPEC_DEV_SPACE, and the call hands out nothing: cu_new is 0, n_left
+ * = n_free.  A page id outside [0, num_pages) gives slot -1 and SPEC_DEV_INDEX.
+ * b <= 16384.  Latency of one launch; prompts: 8 bytes a token. */
+int spec_alloc_slots(int b, int page_size, const int32_t* req_pool_idx, const int32_t* seq_lens,
+                     const int32_t* new_lens, int max_new, const int32_t* free_ids, int free_cap,
+                     const int32_t* n_free, int64_t num_pages, int32_t* page_table, int req_rows, int row_pages,
+                     int32_t* req_to_token, int row_w, int32_t* cu_new, int32_t* slot_map, int32_t* positions,
+                     int slot_cap, int32_t* n_left, void* ws, size_t ws_bytes, void* stream);
+
+/* spec_commit_kv_q8 -- quantises bf16 K/V rows into the 8-bit cache: for
+ * request b and j < lens[b] <= max_len, row r of the new rows becomes token
+ * seq_lens[b] + j, with r = src_index[b * max_len + j] (accept_index of a
+ * verify step, max_len its width) or, src_index NULL, src_start[b] + j (cu_new
+ * of prompts).  k_new / v_new: num_rows rows [Hkv, D] bf16, new_ld elements
+ * apart (a multiple of 8, at least Hkv * D: a view of a packed projection).
+ * Every layer, K and V.  The pages have to be in page_table already; no page
+ * that receives a row may belong to two requests of the call.
+ *   With x = the largest finite magnitude among the rows a (page, kv head)
+ * receives, need = the smallest e >= SPEC_Q8_EXP_MIN with x <= 448 * 2^(e-127).
+ * A page that holds earlier tokens keeps e = max(its e, need), and its held
+ * values move to it (round to nearest even; exact unless they fall below
+ * e4m3's normal range); a page without takes e = need.  Each new value is x
+ * 2^(127-e) rounded once to nearest even; +-inf saturates to +-448, NaN stays
+ * NaN.  Bytes behind a request's last token stay as they are.
+ * new_seq_lens[b] = seq_lens[b] + lens[b].  The layer arrays are HOST arrays of
+ * num_layers (<= 128) device pointers.  A bad length or table row leaves its
+ * request untouched; a bad page id or row index skips that page or row. */
+int spec_commit_kv_q8(int b, int Hkv, int D, int page_size, int num_layers, const void* const* k_new,
+                      const void* const* v_new, int64_t num_rows, int64_t new_ld, void* const* k_pages,
+                      void* const* v_pages, uint8_t* const* k_scales, uint8_t* const* v_scales, int64_t num_pages,
+                      const int32_t* page_table, int req_rows, int row_pages, const int32_t* req_pool_idx,
+                      const int32_t* seq_lens, const int32_t* src_index, const int32_t* src_start,
+                      const int32_t* lens, int max_len, int32_t* new_seq_lens, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* spec_verify_attention_q8 -- spec_verify_attention over the 8-bit cache.  Keys
+ * of row b*n+i: positions 0..seq_lens[b]-1 of the cache, then the tree nodes j
+ * with mask bit (i, j) set, whose K and V are rows b*n+j of k_new / v_new
+ * ([Hkv, D] bf16, new_ld elements apart).  n = 1 with mask 1 is plain decoding.
+ * q: rows [Hq, D] bf16, q_ld elements apart; q_ld and new_ld are multiples of
+ * 8, so that q, k_new and v_new can be views of one packed projection.  out:
+ * [b*n, Hq, D] bf16; lse: [b*n, Hq] fp32 (nullable), natural log.  A row that
+ * sees no key gives out 0 and lse -inf.  An inf or NaN in a node's V reaches
+ * only the rows that see the node.  max_seq_len bounds every seq_len (a larger
+ * one sets SPEC_DEV_LENGTH and is clamped).  A page id out of range sets
+ * SPEC_DEV_INDEX and its keys do not count.  b <= 2048.  The workspace holds the
+ * merge slots (about 51 MB, independent of the sizes). */
+int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size, const void* q, int64_t q_ld,
+                             const void* k_new, const void* v_new, int64_t new_ld, const void* k_pages,
+                             const void* v_pages, const uint8_t* k_scales, const uint8_t* v_scales,
+                             int64_t num_pages, const int32_t* page_table, int req_rows, int row_pages,
+                             const int32_t* req_pool_idx, const int32_t* seq_lens, int max_seq_len,
+                             const uint64_t* mask_bits, float scale, void* out, float* lse, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * spec_token_logprobs -- log probabilities of given tokens, entropy and the k
+ * best alternatives of verify rows, what a serving engine returns next to the
+ * accepted tokens.  The pages have no counterpart.
+ *
+ * logits: [b*n, V] (SPEC_F32 or SPEC_BF16, any V).  Output row (b, j), j < W,
+ * reads verify row row_index[b*W+j] (accept_index; -1: no row, outputs 0 and
+ * ids -1), or b*n+j when row_index is NULL (W <= n).  With p = softmax(row /
+ * T_b) (temperatures NULL, or T_b <= 0 as for greedy requests: T = 1):
+ *   logprobs [b, W]      ln p(tokens[b*W+j]) (token -1: 0; >= V: 0 and
+ *                        SPEC_DEV_INDEX)
+ *   entropy [b, W]       -sum p ln p (nullable)
+ *   top_ids [b, W, k], top_logprobs [b, W, k]   the k largest logits in
+ *                        descending order (ties: lowest index) and their ln p;
+ *                        0 <= k <= 32, k <= V (k = 0: both may be NULL)
+ * -inf logits have ln p = -inf and no share in the entropy; NaN counts as -inf;
+ * a row without any other logit gives ln p -inf everywhere and entropy 0; a row
+ * with +inf gives NaN.  W <= 65, V <= 4194304.  HBM-bound: one pass.
+ * ------------------------------------------------------------------------- */
+int spec_token_logprobs(int b, int n, int W, int V, int dtype, const void* logits, const int32_t* row_index,
+                        const int32_t* tokens, const float* temperatures, int k, float* logprobs,
+                        float* entropy, int32_t* top_ids, float* top_logprobs, void* ws, size_t ws_bytes,
+                        void* stream);
 
 /* ---------------------------------------------------------------------------
  * spec_verify_greedy_noalloc -- spec_verify_greedy without a caller workspace.
