@@ -43,6 +43,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kQ8AttThreads = 32 * kWarps;
+constexpr int kRowsMost = 32;  // query rows a kv head up to which this kernel is taken
 constexpr int kTile = 16;    // keys of a tile
 constexpr int kRowTile = 16; // query rows of a unit
 constexpr int kRing = 4;     // tiles in a warp's ring
@@ -706,6 +707,7 @@ int launch_rows(const AttentionQ8Params& p, cudaStream_t stream) {
 size_t attention_q8_partial_bytes() { return kQ8SlotMlBytes + size_t(2) * kQ8MaxCtas * kQ8SlotRows * 128 * 4; }
 
 int launch_attention_q8(const AttentionQ8Params& p, cudaStream_t stream) {
+  if (p.n * (p.Hq / p.Hkv) > kRowsMost) return launch_attention_q8_tc(p, stream);
   return p.D == 128 ? launch_rows<128>(p, stream) : launch_rows<64>(p, stream);
 }
 

@@ -10,8 +10,10 @@ namespace spec {
 constexpr float kLazyLog2 = 8.f;  // O is rescaled only when a row's maximum grows by more than 2^8
 constexpr float kPBaseLog2 = 6.f; // P's row maximum when the reference is set: 2^6, so P <= 2^14 < 65504
 constexpr int kQ8MaxCtas = 192;   // upper bound of a grid of one CTA a SM; sizes the partial slots
-constexpr int kQ8SlotRows = 128;  // query rows of a slot at most
+constexpr int kQ8SlotRows = 256;  // query rows of a slot at most
 constexpr size_t kQ8SlotMlBytes = size_t(2) * kQ8MaxCtas * kQ8SlotRows * 2 * 4;
+
+int launch_attention_q8_tc(const AttentionQ8Params& p, cudaStream_t stream);
 
 // History length and table row of a request, validated: a bad length is
 // clamped, a bad row leaves no history.

@@ -1,0 +1,1141 @@
+// attention_q8_tc.cu -- tree-masked verify attention over the 8-bit paged cache on
+// the tcgen05 tensor cores, for units of more query rows than the register
+// kernel of attention_q8.cu takes (the mathematics is described there).
+//
+// A unit is (request, kv head, up to 256 query rows); row r is (node r / G, q
+// head g G + r % G).  Its keys come in tiles: 128 history keys, then one tile of
+// the (at most 64) tree nodes.  One CTA a SM takes an equal contiguous range of
+// all tiles (units laid end to end, the row blocks of one kv head next to one
+// another, so that the second finds its keys in L2).  Warps:
+//   0-3, 4-7  two softmax groups, one query row a thread.  More than 128 rows:
+//             group w has rows 128 w .. and both see every tile; fewer: the
+//             groups take turns at the tiles (two partial results, joined).
+//   13        loader: bulk copies of the raw tiles (16 keys of a page are
+//             contiguous) into shared memory.  Loads through registers kept
+//             about 11 KB in flight a SM, as little L1 is left beside the
+//             operands, and took three times the MMAs' time.
+//   8-11      converters: raw tile to f16 (one instruction for two values),
+//             stored as 128B-swizzled operand tiles, K and V double buffered.
+//             Tree nodes are bf16 rows divided by their own power of two, and
+//             stored the same way.
+//   12        issues the MMAs: S = Q K^T (M 128, N 128, K D, both
+//             from shared memory) and O += P V (A = P from TMEM).
+// TMEM: O0 O1 | S0 S1; P (f16, two to a column) takes the place of its S.  S of the
+// next tile is issued once P V of this one is complete, while the other
+// group's products run, so each group's softmax overlaps the other's MMAs.
+//   A row reads its scores from TMEM twice, for the maximum and for the
+// exponentials, 16 at a time: holding them, or P, in between took 236 registers
+// and spilled.
+//
+// Bound: 2 x 1024 cycles of MMA for 128 keys and 256 rows (f16 at 4096
+// multiply-adds a cycle).  Per tile shared memory moves 64 KB of converted
+// operands in, 128 KB for S (A and B) and 64 KB for P V; P through shared
+// memory would add 128 KB, which is why it goes through TMEM (an MMA with A
+// from TMEM measured the same 64 cycles as one with both operands in shared
+// memory, once its descriptors are precomputed).
+//   Every wait is bounded: on timeout the CTA sets SPEC_DEV_TIMEOUT, stops,
+// drains its MMAs and frees its TMEM.
+#include "common.cuh"
+#include "kernels.cuh"
+
+#include "attention_q8.cuh"
+#include "e4m3.cuh"
+
+namespace spec {
+
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kKeys = 128;       // history keys of a tile
+constexpr int kTreeKeys = 64;    // nodes of the tree tile
+constexpr int kGroup = 16;       // keys with one page at least
+constexpr int kGroups = kKeys / kGroup;
+constexpr int kTcThreads = 14 * 32;
+constexpr int kConvThreads = 128;
+constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wait
+__host__ __device__ constexpr uint32_t col_o(int w) { return 128u * uint32_t(w); }
+__host__ __device__ constexpr uint32_t col_s(int w) { return 256u + 128u * uint32_t(w); }
+
+// What the softmax needs of a tile: of a history tile, for each group of 16
+// keys, {K scale, V exponent relative to the unit's base, its inverse factor in
+// l, keys that count}; of the tree tile, each node's K and V exponent byte.
+struct TileMeta {
+  union {
+    float4 group[kGroups];
+    uint16_t node[kTreeKeys];
+  };
+  unsigned long long nonfinite[4];  // tree nodes whose V row holds an inf or a NaN, a word a converter warp
+  int base;                         // the unit's V exponent base
+  int pad[3];
+};
+
+template <int D>
+struct TcSmem {
+  static constexpr int kBlock = kRows * 128;       // [128 rows x 64 f16], 128B-swizzled
+  static constexpr int kTile = (D / 64) * kBlock;  // an operand tile
+  static constexpr int kRaw = kKeys * D;           // a tile as it is in memory (also 64 bf16 rows)
+  static constexpr int kQ = 0;                     // two
+  static constexpr int kK = 2 * kTile;             // two
+  static constexpr int kV = 4 * kTile;             // two
+  static constexpr int kRawK = 6 * kTile;
+  static constexpr int kRawV = kRawK + kRaw;
+  static constexpr int kMeta = kRawV + kRaw;       // four
+  static constexpr int kInfo = kMeta + 4 * int(sizeof(TileMeta));  // [2][8]: scale bytes and keys of a raw tile's groups
+  static constexpr int kBars = kInfo + 64;
+  static constexpr int kBytes = kBars + 384;
+  // the tiles before each request are summed up in what will hold operands
+  static_assert(4 * (kAttentionQ8MaxB + 1) <= 2 * kTile, "scan space");
+};
+static_assert(TcSmem<128>::kBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
+
+enum {
+  kKFull0 = 0,  // + buffer: converters stored the K tile (and the tile's meta)
+  kKEmpty0 = 2, // + buffer: the S products that read it are complete (two arrivals)
+  kVFull0 = 4,
+  kVEmpty0 = 6,
+  kQFull0 = 8,  // + group
+  kSFull0 = 10,
+  kPReady0 = 12,
+  kPvDone0 = 14,
+  kOFree0 = 16,  // the epilogue has read O
+  kFragFull = 18,  // group 1 stored its half of a unit that this CTA finishes
+  kFragFree = 19,  // group 0 has read it
+  kDrain = 20,
+  kRawFull0 = 21,   // + (K, V): the raw tile has landed
+  kRawEmpty0 = 23,  // the converters have read it
+  kNumBars = 25
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity), "r"(20000u)
+               : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try(bar, parity)) return true;
+  const long long start = clock64();
+  while (clock64() - start < kWaitCycles && !*abort_flag)
+    if (mbar_try(bar, parity)) return true;
+  return false;
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// `bytes` (a multiple of 16) of global memory into shared memory, counted in on `bar`
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, const uint4& x) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+// one byte; the load stays ahead of the waits that follow it
+__device__ __forceinline__ uint32_t ld_nc8(const uint8_t* p) {
+  uint32_t x;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// shared-memory matrix descriptor: 128B swizzle, descriptor version 1
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
+         (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// instruction descriptor of kind::f16: f16 A and B, f32 accumulator, M = 128
+__host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(kRows >> 4) << 24);
+}
+// the lane of a converged warp that issues (always the same one)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+#define SPEC_R32(r)                                                                                                  \
+  "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),        \
+      "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),         \
+      "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),        \
+      "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+
+// 32 consecutive TMEM columns of this thread's lane, waited for
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : SPEC_R32(r)
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 16 columns: the load is issued (tmem_ld_wait completes it)
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// 8 / 16 columns stored (tmem_st_wait completes them)
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n"
+      " mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+struct TcArgs {
+  AttentionQ8Params p;
+  int blocks;          // 256-row blocks of a kv head's n * G rows
+  uint32_t* counters;  // [CTA]: arrivals on the unit that CTA begins and does not finish
+  float* slot_o;       // [2 * CTA + i][group][128][D]
+  float* slot_ml;      // [2 * CTA + i][group][128][2]
+};
+
+// a position in the tile space
+struct Pos {
+  int r, j, t, Tr;  // request, (kv head, row block), tile, tiles of the request
+  int len, row;     // the request's history and table row (-1: none)
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __grid_constant__ TcArgs args) {
+  using L = TcSmem<D>;
+  constexpr unsigned FULL = 0xffffffffu;
+  const AttentionQ8Params& a = args.p;
+  const int G = a.Hq / a.Hkv, M = a.n * G, J = a.Hkv * args.blocks;
+  const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
+
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
+  unsigned char* sp = smem_raw + (sbase - raw);
+  TileMeta* metas = reinterpret_cast<TileMeta*>(sp + L::kMeta);
+  const uint32_t bars = sbase + L::kBars;
+  auto bar = [&](int i) { return bars + 8u * uint32_t(i); };
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sp + L::kBars + 8 * kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + L::kBars + 8 * kNumBars + 4);
+  int* wsum = reinterpret_cast<int*>(sp + L::kBars + 8 * kNumBars + 8);  // [14]
+  int* s_last = wsum + 14;
+  uint32_t* infos = reinterpret_cast<uint32_t*>(sp + L::kInfo);
+  int* pre = reinterpret_cast<int*>(sp);  // [b + 1] tiles of one (kv head, row block) before request r (until the roles start)
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kKFull0 + i), kConvThreads);
+      mbar_init(bar(kKEmpty0 + i), 2);
+      mbar_init(bar(kVFull0 + i), kConvThreads);
+      mbar_init(bar(kVEmpty0 + i), 2);
+      mbar_init(bar(kQFull0 + i), kRows);
+      mbar_init(bar(kSFull0 + i), 1);
+      mbar_init(bar(kPReady0 + i), kRows);
+      mbar_init(bar(kPvDone0 + i), 1);
+      mbar_init(bar(kOFree0 + i), kRows);
+    }
+    mbar_init(bar(kFragFull), kRows);
+    mbar_init(bar(kFragFree), kRows);
+    mbar_init(bar(kDrain), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kRawFull0 + i), 1);
+      mbar_init(bar(kRawEmpty0 + i), kConvThreads);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_holder)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();  // nothing above reads global memory
+  pdl_trigger();
+
+  // ---- tiles before each request; this CTA's range ----
+  {
+    int run = 0;
+    for (int r0 = 0; r0 < a.b; r0 += kTcThreads) {
+      const int r = r0 + tid;
+      int t = 0;
+      if (r < a.b) {
+        const ReqQ8 q = req_q8(a, a.seq_lens[r], a.req_pool_idx[r], blockIdx.x == 0);
+        t = (q.len + kKeys - 1) / kKeys + 1;
+      }
+      int incl = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(FULL, incl, o);
+        if (lane >= o) incl += y;
+      }
+      __syncthreads();
+      if (lane == 31) wsum[warp] = incl;
+      __syncthreads();
+      int before = run;
+      for (int q = 0; q < kTcThreads / 32; ++q) {
+        if (q < warp) before += wsum[q];
+        run += wsum[q];
+      }
+      if (r < a.b) pre[r] = before + incl - t;
+    }
+    if (tid == 0) pre[a.b] = run;
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *tmem_holder;
+  const long long T = (long long)pre[a.b] * J;
+  const long long ctas = T < gridDim.x ? T : gridDim.x;
+  const bool part = blockIdx.x < ctas;
+  const int S = part ? int(blockIdx.x * T / ctas) : 0, E = part ? int((blockIdx.x + 1ll) * T / ctas) : 0;
+  auto cta_of = [&](long long x) { return int(((x + 1) * ctas - 1) / T); };  // the CTA whose range holds tile x
+  Pos start;
+  {
+    int lo = 0, hi = a.b;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((long long)pre[mid] * J <= S) lo = mid;
+      else hi = mid;
+    }
+    start.r = lo;
+    start.Tr = pre[lo + 1] - pre[lo];
+    const int rem = S - pre[lo] * J;
+    start.j = rem / start.Tr;
+    start.t = rem - start.j * start.Tr;
+  }
+  auto request = [&](Pos& p) {
+    const ReqQ8 q = req_q8(a, a.seq_lens[p.r], a.req_pool_idx[p.r], false);
+    p.len = q.len;
+    p.row = q.row;
+    p.Tr = (q.len + kKeys - 1) / kKeys + 1;
+  };
+  request(start);
+  __syncthreads();  // the scan's space becomes operand tiles
+  auto advance = [&](Pos& p) {
+    if (++p.t == p.Tr) {
+      p.t = 0;
+      if (++p.j == J) {
+        p.j = 0;
+        if (++p.r < a.b) request(p);
+      }
+    }
+  };
+  // the piece of a unit that begins at position p, tile f of the range: its tiles
+  auto piece_tiles = [&](const Pos& p, int f) { return min(p.Tr - p.t, E - f); };
+  auto unit_rows = [&](int j) { return min(2 * kRows, M - 2 * kRows * (j % args.blocks)); };
+  auto fail = [&]() {
+    raise_error(a.error, SPEC_DEV_TIMEOUT);
+    *abort_flag = 1;
+  };
+
+  if (warp == 13) {
+    // ============================ loader ============================
+    // One bulk copy a group of 16 keys (16 D contiguous bytes of a page), a
+    // lane each; the tree tile: one a node's row.  Page ids are read two tiles
+    // ahead, scale bytes one.
+    const int SHIFT = a.page_size == 16 ? 0 : a.page_size == 32 ? 1 : 2;  // log2(groups a page)
+    auto fetch = [&](const Pos& p) {  // the page id of the lane's group
+      const int g0 = p.t * kGroups + lane;
+      if (lane < kGroups && p.t < p.Tr - 1 && g0 * kGroup < p.len) return a.page_table[size_t(p.row) * a.row_pages + (g0 >> SHIFT)];
+      return 0;
+    };
+    auto resolve = [&](const Pos& p, int pid, int& unit, int& cnt) {  // its (page, kv head), -1 if none; keys that count
+      const int left = p.len - (p.t * kGroups + lane) * kGroup;
+      unit = -1;
+      cnt = 0;
+      if (lane < kGroups && p.t < p.Tr - 1 && left > 0) {
+        if (pid < 0 || pid >= a.num_pages) {
+          raise_error(a.error, SPEC_DEV_INDEX);
+        } else {
+          unit = pid * a.Hkv + p.j / args.blocks;
+          cnt = min(kGroup, left);
+        }
+      }
+    };
+    uint32_t ks = 0, vs = 0;
+    auto load_scales = [&](int unit) {
+      ks = unit >= 0 ? ld_nc8(a.k_scales + unit) : 0u;
+      vs = unit >= 0 ? ld_nc8(a.v_scales + unit) : 0u;
+    };
+    auto copy = [&](const Pos& p, int unit, int cnt, int which) {
+      const uint32_t dst = sbase + (which ? L::kRawV : L::kRawK), full = bar(kRawFull0 + which);
+      const uint8_t* pages = which ? a.v_pages : a.k_pages;
+      const void* fresh = which ? a.v_new : a.k_new;
+      if (p.t < p.Tr - 1) {
+        const uint32_t bytes = uint32_t(cnt) * D;
+        const uint32_t all = __reduce_add_sync(FULL, bytes);
+        if (lane == 0) mbar_expect(full, all);
+        __syncwarp();
+        if (bytes) {
+          const int off = ((p.t * kGroups + lane) & ((1 << SHIFT) - 1)) * kGroup;
+          bulk_copy(dst + uint32_t(lane * kGroup * D), pages + (size_t(unit) * a.page_size + off) * D, bytes, full);
+        }
+      } else {
+        if (lane == 0) mbar_expect(full, uint32_t(a.n) * D * 2u);
+        __syncwarp();
+        for (int i = lane; i < a.n; i += 32)
+          bulk_copy(dst + uint32_t(i * D * 2),
+                    static_cast<const uint16_t*>(fresh) + (size_t(p.r) * a.n + i) * a.new_ld + size_t(p.j / args.blocks) * D,
+                    uint32_t(D) * 2u, full);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full);
+    };
+    Pos p = start, p1 = start, p2 = start;  // the tile at hand, the next, the one after
+    int unit0 = -1, cnt0 = 0, unit1 = -1, cnt1 = 0, pid1 = 0, pid2 = 0;
+    uint32_t ks1 = 0, vs1 = 0;
+    if (S < E) {
+      resolve(p, fetch(p), unit0, cnt0);
+      load_scales(unit0);
+      if (S + 1 < E) {
+        advance(p1);
+        pid1 = fetch(p1);
+        p2 = p1;
+        if (S + 2 < E) {
+          advance(p2);
+          pid2 = fetch(p2);
+        }
+      }
+    }
+    int ct = 0;
+    for (int f = S; f < E; ++f, ++ct) {
+      const bool k_ok = (ct < 1 || mbar_wait(bar(kRawEmpty0), (ct - 1) & 1, abort_flag)) && !*abort_flag;
+      if (!__all_sync(FULL, k_ok)) break;
+      if (lane < kGroups) infos[(ct & 1) * kGroups + lane] = ks | (vs << 8) | (uint32_t(cnt0) << 16);
+      copy(p, unit0, cnt0, 0);
+      if (f + 1 < E) {
+        resolve(p1, pid1, unit1, cnt1);
+        ks1 = unit1 >= 0 ? ld_nc8(a.k_scales + unit1) : 0u;
+        vs1 = unit1 >= 0 ? ld_nc8(a.v_scales + unit1) : 0u;
+      }
+      const bool v_ok = (ct < 1 || mbar_wait(bar(kRawEmpty0 + 1), (ct - 1) & 1, abort_flag)) && !*abort_flag;
+      if (!__all_sync(FULL, v_ok)) break;
+      copy(p, unit0, cnt0, 1);
+      p = p1;
+      unit0 = unit1;
+      cnt0 = cnt1;
+      ks = ks1;
+      vs = vs1;
+      p1 = p2;
+      pid1 = pid2;
+      if (f + 3 < E) {
+        advance(p2);
+        pid2 = fetch(p2);
+      }
+    }
+    // every copy has landed before the CTA can end (tile ct - 1's, or both of an interrupted one's)
+    if (ct > 0) {
+      for (int i = 0; i < 2; ++i)
+        for (int k = 0; k < 1000 && !mbar_try(bar(kRawFull0 + i), (ct - 1) & 1); ++k) {
+        }
+    }
+    if (*abort_flag && S < E) {
+      for (int k = 0; k < 50 && !mbar_try(bar(kRawFull0), ct & 1); ++k) {
+      }
+    }
+  } else if (warp >= 8 && warp < 12) {
+    // ============================ converters ============================
+    const int cw = warp - 8, ct_id = tid - 256;
+    constexpr int kLoads = D / 16;               // 16-byte words a thread of a raw tile
+    constexpr int kLanesKey = D / 16;            // lanes a history key
+    constexpr int kLanesRow = D / 8;             // lanes a tree row
+    constexpr int kRowsLoad = kConvThreads / kLanesRow, kTreeLoads = kTreeKeys / kRowsLoad;
+    // group and key (in the tile) of a thread's word i of a history tile
+    auto hist_key = [&](int i) { return D == 128 ? 16 * i + 4 * cw + lane / kLanesKey : 32 * i + 8 * cw + lane / kLanesKey; };
+    auto tree_key = [&](int i) { return i * kRowsLoad + ct_id / kLanesRow; };
+    // word i of the thread, zeros where there is no key
+    auto read = [&](uint4 (&x)[kLoads], uint32_t rawt, bool tree, const uint32_t* info) {
+      if (!tree) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int key = hist_key(i);
+          x[i] = lds16(rawt + uint32_t(key * D + (lane % kLanesKey) * 16));
+          if (uint32_t(key & 15) >= info[key >> 4] >> 16) x[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTreeLoads; ++i) {
+          const int key = tree_key(i);
+          x[i] = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
+          if (key >= a.n) x[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    };
+    // 16 e4m3 values -> two 16-byte chunks of their key's swizzled row
+    auto store_hist = [&](uint32_t tile, const uint4 (&x)[kLoads]) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int key = hist_key(i);
+        const int ch = lane % kLanesKey;  // elements 16 ch ..
+        const uint32_t row = tile + uint32_t(ch >> 2) * L::kBlock + uint32_t(key) * 128u;
+        const uint32_t c0 = uint32_t(2 * (ch & 3));
+        const uint4 lo = make_uint4(e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16), e4m3x2_to_f16x2(x[i].y),
+                                    e4m3x2_to_f16x2(x[i].y >> 16));
+        const uint4 hi = make_uint4(e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16), e4m3x2_to_f16x2(x[i].w),
+                                    e4m3x2_to_f16x2(x[i].w >> 16));
+        // the second half's lanes store their upper chunk first: no two lanes of a phase share banks
+        const bool swap = ch >= 4;
+        sts16(row + (((c0 + (swap ? 1u : 0u)) ^ uint32_t(key & 7)) << 4), swap ? hi : lo);
+        sts16(row + (((c0 + (swap ? 0u : 1u)) ^ uint32_t(key & 7)) << 4), swap ? lo : hi);
+      }
+    };
+    auto row_exp = [&](const uint4& x) {  // exponent byte of a tree row's power of two, from its lanes
+      uint32_t mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(0u, x.x), x.y), x.z), x.w);
+      mx = max(mx & 0xffffu, mx >> 16);
+#pragma unroll
+      for (int o = 1; o < kLanesRow; o <<= 1) mx = max(mx, __shfl_xor_sync(FULL, mx, o));
+      return norm_exp(mx);
+    };
+    auto store_tree = [&](uint32_t tile, uint4 x, int i, int e, bool finite) {
+      if (finite) {
+        x.x = finite_bf16(x.x);
+        x.y = finite_bf16(x.y);
+        x.z = finite_bf16(x.z);
+        x.w = finite_bf16(x.w);
+      }
+      const float inv = exp_scale(2 * kExpBias - e);
+      auto cv = [&](uint32_t w) { return pack_f16(bf16_lo(w) * inv, bf16_hi(w) * inv); };
+      const int key = tree_key(i), ch = ct_id % kLanesRow;
+      sts16(tile + uint32_t(ch >> 3) * L::kBlock + uint32_t(key) * 128u + ((uint32_t(ch & 7) ^ uint32_t(key & 7)) << 4),
+            make_uint4(cv(x.x), cv(x.y), cv(x.z), cv(x.w)));
+    };
+    Pos p = start;
+    int base = 113;
+    bool ok = true;
+    for (int f = S, ct = 0; f < E; ++f, ++ct) {
+      const int buf = ct & 1;
+      const bool tree = p.t == p.Tr - 1, first = f == S || p.t == 0;
+      const uint32_t ktile = sbase + L::kK + uint32_t(buf) * L::kTile, vtile = sbase + L::kV + uint32_t(buf) * L::kTile;
+      const uint32_t* info = infos + buf * kGroups;
+      TileMeta& mt = metas[ct & 3];
+      uint4 x[kLoads];
+      // ---- K ----
+      bool go = mbar_wait(bar(kRawFull0), ct & 1, abort_flag) && !*abort_flag;
+      if (!__all_sync(FULL, go)) {
+        ok = false;
+        break;
+      }
+      read(x, sbase + L::kRawK, tree, info);
+      if (first) {
+        const int v0 = int(info[0] >> 8) & 255;
+        base = tree || v0 == 0 ? 113 : v0;
+      }
+      mbar_arrive(bar(kRawEmpty0));
+      go = (ct < 2 || mbar_wait(bar(kKEmpty0 + buf), ((ct >> 1) - 1) & 1, abort_flag)) && !*abort_flag;
+      if (!__all_sync(FULL, go)) {
+        ok = false;
+        break;
+      }
+      if (!tree) {
+        if (cw == 0 && lane < kGroups) {
+          const int ks = int(info[lane] & 255u), vs = int(info[lane] >> 8) & 255, cnt = int(info[lane] >> 16);
+          mt.group[lane] = cnt > 0 ? make_float4(exp_scale(ks), float(vs - base), ratio_scale(base - vs), float(cnt))
+                                   : make_float4(1.f, 0.f, 0.f, 0.f);
+        }
+        store_hist(ktile, x);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTreeLoads; ++i) {
+          const int e = row_exp(x[i]);
+          if (ct_id % kLanesRow == 0) reinterpret_cast<uint8_t*>(&mt.node[tree_key(i)])[0] = uint8_t(e);
+          store_tree(ktile, x[i], i, e, false);
+        }
+        // (the V rows' exponents are wanted with the scores, before V itself)
+        go = mbar_wait(bar(kRawFull0 + 1), ct & 1, abort_flag) && !*abort_flag;
+        if (!__all_sync(FULL, go)) {
+          ok = false;
+          break;
+        }
+        read(x, sbase + L::kRawV, true, info);
+        unsigned long long nf = 0;
+#pragma unroll
+        for (int i = 0; i < kTreeLoads; ++i) {
+          const int e = row_exp(x[i]);
+          if (ct_id % kLanesRow == 0) reinterpret_cast<uint8_t*>(&mt.node[tree_key(i)])[1] = uint8_t(e);
+          const unsigned who = __ballot_sync(FULL, nonfinite_bf16(x[i].x) || nonfinite_bf16(x[i].y) ||
+                                                       nonfinite_bf16(x[i].z) || nonfinite_bf16(x[i].w));
+          if (who) {
+#pragma unroll
+            for (int q = 0; q < 32 / kLanesRow; ++q)
+              if ((who >> (q * kLanesRow)) & ((1u << kLanesRow) - 1u))
+                nf |= 1ull << (i * kRowsLoad + cw * (32 / kLanesRow) + q);
+          }
+        }
+        if (lane == 0) mt.nonfinite[cw] = nf;
+      }
+      if (ct_id == 0) mt.base = base;
+      fence_async();
+      mbar_arrive(bar(kKFull0 + buf));
+      // ---- V ----
+      if (!tree) {
+        go = mbar_wait(bar(kRawFull0 + 1), ct & 1, abort_flag) && !*abort_flag;
+        if (!__all_sync(FULL, go)) {
+          ok = false;
+          break;
+        }
+        read(x, sbase + L::kRawV, false, info);
+      }
+      mbar_arrive(bar(kRawEmpty0 + 1));
+      go = (ct < 2 || mbar_wait(bar(kVEmpty0 + buf), ((ct >> 1) - 1) & 1, abort_flag)) && !*abort_flag;
+      if (!__all_sync(FULL, go)) {
+        ok = false;
+        break;
+      }
+      if (!tree) {
+        store_hist(vtile, x);
+      } else {
+        __syncwarp();  // what other lanes wrote of the tile's meta
+        const bool bad = mt.nonfinite[cw] != 0ull;
+#pragma unroll
+        for (int i = 0; i < kTreeLoads; ++i) store_tree(vtile, x[i], i, int(mt.node[tree_key(i)] >> 8), bad);
+      }
+      fence_async();
+      mbar_arrive(bar(kVFull0 + buf));
+      advance(p);
+    }
+    if (!ok && !*abort_flag) fail();
+  } else if (warp == 12) {
+    // ============================ MMA issuer ============================
+    // The whole warp runs this role, so that its addresses and descriptors stay
+    // uniform (one lane alone spent more time forming them than the MMAs take);
+    // one elected lane issues.
+    {
+      constexpr uint32_t id_s = idesc_f16(kKeys, false), id_st = idesc_f16(kTreeKeys, false), id_o = idesc_f16(D, true);
+      const uint32_t ub = __shfl_sync(FULL, sbase, 0), ut = __shfl_sync(FULL, tmem, 0);
+      const uint64_t dq0 = sdesc(ub + L::kQ, 16, 1024), dk0 = sdesc(ub + L::kK, 16, 1024),
+                     dv0 = sdesc(ub + L::kV, L::kBlock, 1024);
+      constexpr uint64_t kTileStep = uint64_t(L::kTile >> 4);
+      bool ok = true;
+      int cs[2] = {0, 0};  // products S (and P V) issued for the group
+      auto wait = [&](int b, int parity) {
+        return __all_sync(FULL, mbar_wait(bar(b), uint32_t(parity), abort_flag) && !*abort_flag) != 0;
+      };
+      // S = Q K^T of group w for CTA tile ct
+      auto issue_s = [&](int w, int ct, bool tree, bool twice) -> bool {
+        if (cs[w] > 0 && !wait(kPvDone0 + w, (cs[w] - 1) & 1)) return false;
+        if (!wait(kKFull0 + (ct & 1), (ct >> 1) & 1)) return false;
+        tc_after();
+        const uint64_t dq = dq0 + uint64_t(w) * kTileStep, dk = dk0 + uint64_t(ct & 1) * kTileStep;
+        const uint32_t d = ut + col_s(w), id = tree ? id_st : id_s;
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t o = uint64_t(((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4);
+            mma_ss(d, dq + o, dk + o, id, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(bar(kSFull0 + w));
+          mma_commit(bar(kKEmpty0 + (ct & 1)));
+          if (twice) mma_commit(bar(kKEmpty0 + (ct & 1)));  // the other group does not read this tile
+        }
+        __syncwarp();
+        ++cs[w];
+        return true;
+      };
+      // O += P V of group w
+      auto issue_pv = [&](int w, int ct, bool tree, bool twice, bool zero, int piece) -> bool {
+        if (!wait(kVFull0 + (ct & 1), (ct >> 1) & 1)) return false;
+        if (zero && piece > 0 && !wait(kOFree0 + w, (piece - 1) & 1)) return false;
+        if (!wait(kPReady0 + w, (cs[w] - 1) & 1)) return false;
+        tc_after();
+        const uint64_t dv = dv0 + uint64_t(ct & 1) * kTileStep;
+        const uint32_t d = ut + col_o(w), pa = ut + col_s(w);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kTreeKeys / 16; ++kk)
+            mma_ts(d, pa + kk * 8, dv + uint64_t((kk * 16 * 128) >> 4), id_o, !zero || kk > 0 ? 1u : 0u);
+          if (!tree) {
+#pragma unroll
+            for (int kk = kTreeKeys / 16; kk < kKeys / 16; ++kk)
+              mma_ts(d, pa + kk * 8, dv + uint64_t((kk * 16 * 128) >> 4), id_o, 1u);
+          }
+          mma_commit(bar(kPvDone0 + w));
+          mma_commit(bar(kVEmpty0 + (ct & 1)));
+          if (twice) mma_commit(bar(kVEmpty0 + (ct & 1)));
+        }
+        __syncwarp();
+        return true;
+      };
+      Pos p = start;
+      int ct = 0, piece = 0;
+      for (int f = S; ok && f < E; ++piece) {
+        const int n = piece_tiles(p, f);
+        const bool split = unit_rows(p.j) <= kRows;
+        const bool has_tree = p.t + n == p.Tr;
+        const int stride = split ? 2 : 1;
+        // group w's tiles: first(w), first(w) + stride, ..
+        const int first[2] = {0, split ? 1 : 0};
+        for (int w = 0; ok && w < 2; ++w)
+          if (first[w] < n) {
+            ok = wait(kQFull0 + w, piece & 1) && issue_s(w, ct + first[w], has_tree && first[w] == n - 1, split);
+          }
+        for (int s = 0; ok && s * stride < n; ++s) {
+          const int t0 = first[0] + s * stride, t1 = first[1] + s * stride;
+          const bool has1 = t1 < n;
+          auto pv = [&](int w, int t) { return issue_pv(w, ct + t, has_tree && t == n - 1, split, s == 0, piece); };
+          auto nx = [&](int w, int t) {
+            const int u = t + stride;
+            return u >= n || issue_s(w, ct + u, has_tree && u == n - 1, split);
+          };
+          ok = pv(0, t0);
+          // group 1's P V goes in behind group 0's at once if its P is there already
+          bool early = false;
+          if (ok && has1 && __all_sync(FULL, mbar_test(bar(kPReady0 + 1), (cs[1] - 1) & 1))) {
+            ok = pv(1, t1);
+            early = true;
+          }
+          ok = ok && nx(0, t0);
+          if (ok && has1) ok = (early || pv(1, t1)) && nx(1, t1);
+        }
+        ct += n;
+        f += n;
+        p.t += n - 1;
+        advance(p);
+      }
+      if (!ok && !*abort_flag) fail();
+      // every MMA issued has completed before TMEM is released
+      __syncwarp();
+      if (elect_one()) mma_commit(bar(kDrain));
+      for (int i = 0; i < 1000 && !mbar_try(bar(kDrain), 0); ++i) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // ============================ softmax groups ============================
+    // (every tcgen05.ld / st and every exit around them is warp-uniform)
+    const int w = warp >> 2, r = tid & 127;
+    const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
+    const uint32_t ts = tl + col_s(w), to = tl + col_o(w);
+    Pos p = start;
+    int piece = 0, cs = 0, nfrag = 0, ct0 = 0;
+    bool ok = true;
+    for (int f = S; ok && f < E; ++piece) {
+      const int n = piece_tiles(p, f);
+      const int rows = unit_rows(p.j);
+      const bool split = rows <= kRows, complete = p.t == 0 && n == p.Tr;
+      const int stride = split ? 2 : 1, first = split ? w : 0;
+      const int h = p.j / args.blocks;
+      const int rg = 2 * kRows * (p.j % args.blocks) + (split ? 0 : kRows * w) + r;  // row among the kv head's n * G
+      const bool valid = rg < M;
+      const int node = valid ? rg / G : 0, head = h * G + (valid ? rg % G : 0);
+      const bool mine = first < n;
+      float m = -INFINITY, l = 0.f, xf = 0.f;
+      unsigned long long mask = 0, nonfinite = 0;
+      int base = kExpBias;
+      if (mine) {
+        // ---- the row of Q, divided by its power of two, as f16 ----
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (size_t(p.r) * a.n + node) * a.q_ld + size_t(head) * D);
+        uint4 x[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = valid ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        mask = valid ? a.mask_bits[size_t(p.r) * a.n + node] : 0ull;
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, x[i].x), x[i].y), x[i].z), x[i].w);
+        const int e = norm_exp(max(mx & 0xffffu, mx >> 16));
+        // the sign of the scale goes into Q, so that a larger score is a larger exponent
+        const float inv = copysignf(exp_scale(2 * kExpBias - e), a.scale);
+        xf = fabsf(a.scale) * 1.4426950408889634f * exp_scale(e);
+        auto cv = [&](uint32_t u) { return pack_f16(bf16_lo(u) * inv, bf16_hi(u) * inv); };
+        const uint32_t qrow = sbase + L::kQ + uint32_t(w) * L::kTile + uint32_t(r) * 128u;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qrow + uint32_t(i >> 3) * L::kBlock + ((uint32_t(i & 7) ^ uint32_t(r & 7)) << 4)),
+                       "r"(cv(x[i].x)), "r"(cv(x[i].y)), "r"(cv(x[i].z)), "r"(cv(x[i].w))
+                       : "memory");
+        fence_async();
+      }
+      mbar_arrive(bar(kQFull0 + w));
+      for (int t = first; t < n; t += stride, ++cs) {
+        const bool s_ok = mbar_wait(bar(kSFull0 + w), cs & 1, abort_flag) && !*abort_flag;
+        if (!__all_sync(FULL, s_ok)) {
+          ok = false;
+          break;
+        }
+        tc_after();
+        const TileMeta& mt = metas[(ct0 + t) & 3];
+        base = mt.base;
+        const bool tree = p.t + t == p.Tr - 1;
+        // ---- the row's maximum of x + e ----
+        float mx = -INFINITY;
+        auto max_group = [&](const uint32_t* u, int g) {
+          const float4 e = mt.group[g];
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+          if (e.w < float(kGroup)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (float(i) >= e.w) v[i] = -INFINITY;
+          }
+          float q[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q[i] = fmaxf(fmaxf(v[4 * i], v[4 * i + 1]), fmaxf(v[4 * i + 2], v[4 * i + 3]));
+          mx = fmaxf(mx, fmaf(fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3])), xf * e.x, e.y));
+        };
+        auto tree_score = [&](uint32_t u, int k, int e) {  // e: the node's exponent bytes
+          return k < a.n && ((mask >> k) & 1ull) ? fmaf(__uint_as_float(u), xf * exp_scale(e & 255), float((e >> 8) - base))
+                                                : -INFINITY;
+        };
+        uint32_t ua[16], ub[16];  // groups in flight: one is loaded while the other is worked on
+        tmem_ld16(ts, ua);
+        tmem_ld_wait();
+        if (!tree) {
+#pragma unroll 1
+          for (int c = 0; c < kGroups; c += 2) {
+            tmem_ld16(ts + 16 * (c + 1), ub);
+            max_group(ua, c);
+            tmem_ld_wait();
+            tmem_ld16(ts + 16 * (c + 2 < kGroups ? c + 2 : 0), ua);  // (at the end: the first again, for the next pass)
+            max_group(ub, c + 1);
+            tmem_ld_wait();
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kTreeKeys / 16; ++c) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, tree_score(ua[i], 16 * c + i, mt.node[16 * c + i]));
+            tmem_ld16(ts + 16 * (c + 1 < kTreeKeys / 16 ? c + 1 : 0), ua);
+            tmem_ld_wait();
+          }
+        }
+        // ---- the reference moves only when P would pass 2^kLazyLog2 times its value at the maximum; O is
+        // rescaled then (P V of the tile before is complete: S of this one was issued after it) ----
+        if (__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2))) {
+          const bool up = mx > m + (kLazyLog2 + kPBaseLog2);
+          const float fac = up ? fast_exp2(m + kPBaseLog2 - mx) : 1.f;
+          l *= fac;
+          if (up) m = mx - kPBaseLog2;
+          if (t > first) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              tmem_ld16(to + 16 * c, ub);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) ub[i] = __float_as_uint(__uint_as_float(ub[i]) * fac);
+              tmem_st16(to + 16 * c, ub);
+            }
+          }
+        }
+        // ---- P and its sum; P of a group goes over scores that have been read ----
+        const float mr = m == -INFINITY ? 0.f : m;
+        float lt = 0.f;
+        auto exp_group = [&](const uint32_t* u, int g) {
+          const float4 e = mt.group[g];
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+          if (e.w < float(kGroup)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (float(i) >= e.w) v[i] = -INFINITY;
+          }
+          const float xk = xf * e.x, off = e.y - mr;
+          float2 s0 = make_float2(0.f, 0.f);
+          const float2 k2 = make_float2(xk, xk), o2 = make_float2(off, off);
+          uint32_t pk[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 y = fma2(make_float2(v[2 * i], v[2 * i + 1]), k2, o2);
+            const float2 q = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            s0 = add2(s0, q);
+            pk[i] = pack_f16(q.x, q.y);
+          }
+          lt = fmaf(s0.x + s0.y, e.z, lt);
+          tmem_st8(ts + 8 * g, pk);
+        };
+        if (!tree) {
+#pragma unroll 1
+          for (int c = 0; c < kGroups; c += 2) {
+            tmem_ld16(ts + 16 * (c + 1), ub);
+            exp_group(ua, c);
+            tmem_ld_wait();
+            if (c + 2 < kGroups) tmem_ld16(ts + 16 * (c + 2), ua);
+            exp_group(ub, c + 1);
+            tmem_ld_wait();
+          }
+        } else {
+          nonfinite = mt.nonfinite[0] | mt.nonfinite[1] | mt.nonfinite[2] | mt.nonfinite[3];
+#pragma unroll 1
+          for (int c = 0; c < kTreeKeys / 16; ++c) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const int e0 = mt.node[16 * c + i], e1 = mt.node[16 * c + i + 1];
+              const float q0 = fast_exp2(tree_score(ua[i], 16 * c + i, e0) - mr);
+              const float q1 = fast_exp2(tree_score(ua[i + 1], 16 * c + i + 1, e1) - mr);
+              lt = fmaf(q0, ratio_scale(base - (e0 >> 8)), fmaf(q1, ratio_scale(base - (e1 >> 8)), lt));
+              pk[i / 2] = pack_f16(q0, q1);
+            }
+            if (c + 1 < kTreeKeys / 16) tmem_ld16(ts + 16 * (c + 1), ua);
+            tmem_ld_wait();
+            tmem_st8(ts + 8 * c, pk);
+          }
+        }
+        l += lt;
+        tmem_st_wait();
+        tc_before();
+        mbar_arrive(bar(kPReady0 + w));
+      }
+      if (!ok) break;
+      // ---- the piece's result ----
+      if (mine) {
+        const bool d_ok = mbar_wait(bar(kPvDone0 + w), (cs - 1) & 1, abort_flag) && !*abort_flag;
+        if (!__all_sync(FULL, d_ok)) {
+          ok = false;
+          break;
+        }
+        tc_after();
+      }
+      const float vs = exp_scale(base < 1 ? 1 : base);
+      const bool direct = complete && !split;
+      const int slot = 2 * int(blockIdx.x) + (complete || p.t == 0 ? 1 : 0);  // (0: a unit that an earlier CTA began)
+      const bool local = complete && split;
+      float* so = args.slot_o + ((size_t(slot) * 2 + w) * kRows + r) * D;
+      float2* sm = reinterpret_cast<float2*>(args.slot_ml) + (size_t(slot) * 2 + w) * kRows + r;
+      const size_t orow = (size_t(p.r) * a.n + node) * a.Hq + head;
+      float om = -INFINITY, ol = 0.f;  // group 1's half of a unit that group 0 finishes
+      // (group 1 without a tile may be here before group 0 has read its last half)
+      if (split && w == 1 && nfrag > 0 && !__all_sync(FULL, mbar_wait(bar(kFragFree), (nfrag - 1) & 1, abort_flag))) {
+        ok = false;
+        break;
+      }
+      if (local) {
+        if (w == 0) {
+          if (!__all_sync(FULL, mbar_wait(bar(kFragFull), nfrag & 1, abort_flag))) {
+            ok = false;
+            break;
+          }
+          const float2 x = __ldcg(sm + kRows);
+          om = x.x;
+          ol = x.y;
+        }
+        ++nfrag;
+      }
+      const unsigned long long nf = nonfinite & mask;
+      const bool any_nf = __any_sync(FULL, nf != 0ull);
+      // out = (O 2^base [+ the other half, both relative to the larger reference]) / l
+      const bool has_o = ol > 0.f || ol != ol;
+      const float M2 = has_o ? fmaxf(m, om) : m;
+      const float wa = has_o && m != M2 ? fast_exp2(m - M2) : 1.f, wb = has_o ? fast_exp2(om - M2) : 0.f;
+      const float Ls = has_o ? l * wa + ol * wb : l;
+      const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float v[32];
+        if (mine) {
+          tmem_ld32(to + 32 * c, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= vs;
+        if (any_nf && nf) {
+          for (int q = 0; q < a.n; ++q)
+            if ((nf >> q) & 1ull) {
+              const uint16_t* vr = static_cast<const uint16_t*>(a.v_new) + (size_t(p.r) * a.n + q) * a.new_ld + size_t(h) * D + 32 * c;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float y = __uint_as_float(uint32_t(vr[i]) << 16);
+                if (!(fabsf(y) < INFINITY)) v[i] += y;
+              }
+            }
+        }
+        if (direct || (local && w == 0)) {
+          if (has_o) {
+            const float4* oo = reinterpret_cast<const float4*>(so + size_t(kRows) * D) + 8 * c;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 y = __ldcg(oo + i);
+              v[4 * i] = v[4 * i] * wa + y.x * wb;
+              v[4 * i + 1] = v[4 * i + 1] * wa + y.y * wb;
+              v[4 * i + 2] = v[4 * i + 2] * wa + y.z * wb;
+              v[4 * i + 3] = v[4 * i + 3] * wa + y.w * wb;
+            }
+          }
+          if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D) + 4 * c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                                  pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+          }
+        } else if (valid) {
+          float4* dst = reinterpret_cast<float4*>(so) + 8 * c;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+      if (direct || (local && w == 0)) {
+        if (valid && a.lse) a.lse[orow] = lse_of(M2, Ls);
+      } else if (valid) {
+        *sm = make_float2(m, l);
+      } else {
+        *sm = make_float2(-INFINITY, 0.f);
+      }
+      if (local) mbar_arrive(bar(w == 1 ? kFragFull : kFragFree));
+      tc_before();
+      mbar_arrive(bar(kOFree0 + w));  // the next piece may write O
+      ct0 += n;
+      f += n;
+      p.t += n - 1;
+      advance(p);
+    }
+    if (!ok && !*abort_flag) fail();
+  }
+
+  // ---- teardown ----
+  tc_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+  if (*abort_flag || S >= E) return;
+
+  // ---- units shared with other CTAs: count in, and join those that are last ----
+  Pos last = start;
+  int last_f = S;
+  {  // the first position of the range's last piece
+    int f = S;
+    Pos q = start;
+    while (true) {
+      const int n = piece_tiles(q, f);
+      last = q;
+      last_f = f;
+      if (f + n >= E) break;
+      f += n;
+      q.t += n - 1;
+      advance(q);
+    }
+  }
+  for (int x = 0; x < 2; ++x) {
+    const Pos& q = x == 0 ? start : last;
+    if (x == 1 && last.r == start.r && last.j == start.j) break;  // one unit only
+    const long long us = (x == 0 ? S : last_f) - q.t;  // the unit's first tile
+    const int ca = cta_of(us), cb = cta_of(us + q.Tr - 1);
+    if (ca == cb) continue;
+    __syncthreads();
+    if (tid == 0) *s_last = atom_add_acq_rel(args.counters + ca) == uint32_t(cb - ca);
+    __syncthreads();
+    if (!*s_last) continue;
+    const int rows = unit_rows(q.j), h = q.j / args.blocks;
+    const bool split = rows <= kRows;
+    constexpr int C4 = D / 4;
+    for (int i = tid; i < rows * C4; i += kTcThreads) {
+      const int row = i / C4, c = i % C4;
+      float Mx = -INFINITY, Ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int y = 0; y < (cb - ca + 1) * (split ? 2 : 1); ++y) {
+        const int cta = ca + (split ? y >> 1 : y);
+        const size_t at = (size_t(2 * cta + (cta == ca ? 1 : 0)) * 2 + (split ? y & 1 : row / kRows)) * kRows + row % kRows;
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(args.slot_ml) + at);
+        const float4 o4 = __ldcg(reinterpret_cast<const float4*>(args.slot_o) + at * C4 + c);
+        const float v[4] = {o4.x, o4.y, o4.z, o4.w};
+        join<4>(Mx, Ls, acc, ml.x, ml.y, v);
+      }
+      const int rg = 2 * kRows * (q.j % args.blocks) + row;
+      const size_t orow = (size_t(q.r) * a.n + rg / G) * a.Hq + h * G + rg % G;
+      const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + 4 * c) =
+          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+      if (c == 0 && a.lse) a.lse[orow] = lse_of(Mx, Ls);
+    }
+    if (tid == 0) atomicExch(args.counters + ca, 0u);
+  }
+}
+
+template <int D>
+int launch_tc(const AttentionQ8Params& p, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return SPEC_ERR_LAUNCH;
+  // at least 120 KB, so that two CTAs never share a SM (each holds all of TMEM)
+  size_t smem = TcSmem<D>::kBytes + 1024;
+  if (smem < 120 * 1024) smem = 120 * 1024;
+  if (cudaFuncSetAttribute(attention_q8_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+    return SPEC_ERR_LAUNCH;
+  TcArgs args{p, (p.n * (p.Hq / p.Hkv) + 2 * kRows - 1) / (2 * kRows), p.counters,
+              reinterpret_cast<float*>(p.partials + kQ8SlotMlBytes), reinterpret_cast<float*>(p.partials)};
+  const int grid = sms < kQ8MaxCtas ? sms : kQ8MaxCtas;
+  const cudaError_t e = launch_pdl(attention_q8_tc_kernel<D>, dim3(grid), dim3(kTcThreads), smem, stream, args);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+}
+
+}  // namespace
+
+int launch_attention_q8_tc(const AttentionQ8Params& p, cudaStream_t stream) {
+  return p.D == 128 ? launch_tc<128>(p, stream) : launch_tc<64>(p, stream);
+}
+
+}  // namespace spec
