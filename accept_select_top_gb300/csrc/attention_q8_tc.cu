@@ -18,14 +18,15 @@
 //             stored as 128B-swizzled operand tiles, K and V double buffered.
 //             Tree nodes are bf16 rows divided by their own power of two, and
 //             stored the same way.
-//   12        issues the MMAs: S = Q K^T (M 128, N 128, K D, both
+//   12, 13    issue each group's MMAs: S = Q K^T (M 128, N 128, K D, both
 //             from shared memory) and O += P V (A = P from TMEM).
 // TMEM: O0 O1 | S0 S1; P (f16, two to a column) takes the place of its S.  S of the
 // next tile is issued once P V of this one is complete, while the other
 // group's products run, so each group's softmax overlaps the other's MMAs.
-//   A row reads its scores from TMEM twice, for the maximum and for the
-// exponentials, 16 at a time: holding them, or P, in between took 236 registers
-// and spilled.
+//   A softmax thread takes its row's scores 32 at a time, each once: maximum,
+// exponentials and P of a chunk while the next one is loaded.  Holding the whole
+// row in between (or P) spilled, and a spill costs an L2 access here, as the
+// operands leave almost no L1.
 //
 // Bound: 2 x 1024 cycles of MMA for 128 keys and 256 rows (f16 at 4096
 // multiply-adds a cycle).  Per tile shared memory moves 64 KB of converted
@@ -50,8 +51,12 @@ constexpr int kKeys = 128;       // history keys of a tile
 constexpr int kTreeKeys = 64;    // nodes of the tree tile
 constexpr int kGroup = 16;       // keys with one page at least
 constexpr int kGroups = kKeys / kGroup;
-constexpr int kTcThreads = 14 * 32;
-constexpr int kConvThreads = 128;
+constexpr int kTcThreads = 16 * 32;
+// Registers a thread, by warp group: the CTA is launched with kRegs each, and
+// the groups trade (sums of four warps: 2 kRegsSoft + kRegsConv + kRegsIssue <= 4 kRegs).
+constexpr int kRegs = 128, kRegsSoft = 168, kRegsConv = 96, kRegsIssue = 80;
+static_assert(2 * kRegsSoft + kRegsConv + kRegsIssue <= 4 * kRegs, "register split");
+constexpr int kConvThreads = 128, kSoftThreads = 256;
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wait
 __host__ __device__ constexpr uint32_t col_o(int w) { return 128u * uint32_t(w); }
 __host__ __device__ constexpr uint32_t col_s(int w) { return 256u + 128u * uint32_t(w); }
@@ -82,6 +87,8 @@ struct TcSmem {
   static constexpr int kMeta = kRawV + kRaw;       // four
   static constexpr int kInfo = kMeta + 4 * int(sizeof(TileMeta));  // [2][8]: scale bytes and keys of a raw tile's groups
   static constexpr int kBars = kInfo + 64;
+  static constexpr int kAbort = kBars + 8 * 26 + 4;  // (after the barriers: TMEM address, abort flag)
+  static constexpr int kKeep = kAbort + 4 + 4 * 17;  // 16 words of the scan and one before it
   static constexpr int kBytes = kBars + 384;
   // the tiles before each request are summed up in what will hold operands
   static_assert(4 * (kAttentionQ8MaxB + 1) <= 2 * kTile, "scan space");
@@ -100,10 +107,10 @@ enum {
   kOFree0 = 16,  // the epilogue has read O
   kFragFull = 18,  // group 1 stored its half of a unit that this CTA finishes
   kFragFree = 19,  // group 0 has read it
-  kDrain = 20,
-  kRawFull0 = 21,   // + (K, V): the raw tile has landed
-  kRawEmpty0 = 23,  // the converters have read it
-  kNumBars = 25
+  kDrain0 = 20,     // + group
+  kRawFull0 = 22,   // + (K, V): the raw tile has landed
+  kRawEmpty0 = 24,  // the converters have read it
+  kNumBars = 26
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -113,14 +120,6 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-               : "=r"(ok)
-               : "r"(bar), "r"(parity)
-               : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
@@ -129,12 +128,19 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
                : "memory");
   return ok != 0;
 }
+// Bounded wait for the phase of the given parity: false once kWaitCycles have
+// passed or another warp has given up.  The bound is looked at every 64 polls, so
+// that a waiting warp takes few issue slots from the others.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try(bar, parity)) return true;
-  const long long start = clock64();
-  while (clock64() - start < kWaitCycles && !*abort_flag)
+  long long start = 0;
+  for (uint32_t i = 0;; ++i) {
     if (mbar_try(bar, parity)) return true;
-  return false;
+    if ((i & 63u) == 63u) {
+      const long long now = clock64();
+      if (i == 63u) start = now;
+      if (*abort_flag || now - start > kWaitCycles) return false;
+    }
+  }
 }
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -144,6 +150,10 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
+}
+// 16-byte global -> shared copy; 0 bytes: zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 x;
@@ -163,10 +173,17 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// shared-memory matrix descriptor: 128B swizzle, descriptor version 1
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
-         (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+// Shared-memory matrix descriptor (128B swizzle, descriptor version 1) in two
+// words: address and leading-dimension offset, then stride offset and flags.  The
+// address is stepped in the low word alone.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1024 bytes apart
+__device__ __forceinline__ uint64_t desc(uint32_t lo) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kDescHi));
+  return d;
 }
 // instruction descriptor of kind::f16: f16 A and B, f32 accumulator, M = 128
 __host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn_major) {
@@ -200,18 +217,14 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
       "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),        \
       "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
 
-// 32 consecutive TMEM columns of this thread's lane, waited for
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
+// 32 consecutive TMEM columns of this thread's lane (tmem_ld_wait completes the load)
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
-      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : SPEC_R32(r)
       : "r"(taddr)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 // 16 columns: the load is issued (tmem_ld_wait completes it)
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -223,11 +236,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// 8 / 16 columns stored (tmem_st_wait completes them)
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+// 32 / 16 columns stored (tmem_st_wait completes them)
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -256,11 +274,22 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+// a barrier of the softmax warps, and one that tells whether any of them says yes
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
+__device__ __forceinline__ bool soft_any(bool x) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(r)
+               : "r"(int(x)), "n"(kSoftThreads)
+               : "memory");
+  return r != 0;
+}
+
 struct TcArgs {
   AttentionQ8Params p;
   int blocks;          // 256-row blocks of a kv head's n * G rows
   uint32_t* counters;  // [CTA]: arrivals on the unit that CTA begins and does not finish
-  float* slot_o;       // [2 * CTA + i][group][128][D]
+  float* slot_o;       // [2 * CTA + i][group][D / 4][128][4]
   float* slot_ml;      // [2 * CTA + i][group][128][2]
 };
 
@@ -269,6 +298,22 @@ struct Pos {
   int r, j, t, Tr;  // request, (kv head, row block), tile, tiles of the request
   int len, row;     // the request's history and table row (-1: none)
 };
+
+__device__ __forceinline__ void request_of(const AttentionQ8Params& a, Pos& p) {
+  const ReqQ8 q = req_q8(a, a.seq_lens[p.r], a.req_pool_idx[p.r], false);
+  p.len = q.len;
+  p.row = q.row;
+  p.Tr = (q.len + kKeys - 1) / kKeys + 1;
+}
+__device__ __forceinline__ void next_pos(const AttentionQ8Params& a, int J, Pos& p) {
+  if (++p.t == p.Tr) {
+    p.t = 0;
+    if (++p.j == J) {
+      p.j = 0;
+      if (++p.r < a.b) request_of(a, p);
+    }
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __grid_constant__ TcArgs args) {
@@ -285,9 +330,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
   const uint32_t bars = sbase + L::kBars;
   auto bar = [&](int i) { return bars + 8u * uint32_t(i); };
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sp + L::kBars + 8 * kNumBars);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + L::kBars + 8 * kNumBars + 4);
-  int* wsum = reinterpret_cast<int*>(sp + L::kBars + 8 * kNumBars + 8);  // [14]
-  int* s_last = wsum + 14;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + L::kAbort);
+  static_assert(L::kAbort == L::kBars + 8 * kNumBars + 4 && L::kKeep + 32 <= L::kBytes, "layout");
+  int* wsum = reinterpret_cast<int*>(sp + L::kBars + 8 * kNumBars + 8);  // [16]
+  int* keep = reinterpret_cast<int*>(sp + L::kKeep);  // [8]: what the joining at the end needs (kept here, it costs the roles no registers)
   uint32_t* infos = reinterpret_cast<uint32_t*>(sp + L::kInfo);
   int* pre = reinterpret_cast<int*>(sp);  // [b + 1] tiles of one (kv head, row block) before request r (until the roles start)
 
@@ -305,8 +351,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     }
     mbar_init(bar(kFragFull), kRows);
     mbar_init(bar(kFragFree), kRows);
-    mbar_init(bar(kDrain), 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kDrain0 + i), 1);
       mbar_init(bar(kRawFull0 + i), 1);
       mbar_init(bar(kRawEmpty0 + i), kConvThreads);
     }
@@ -356,7 +402,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
   const long long ctas = T < gridDim.x ? T : gridDim.x;
   const bool part = blockIdx.x < ctas;
   const int S = part ? int(blockIdx.x * T / ctas) : 0, E = part ? int((blockIdx.x + 1ll) * T / ctas) : 0;
-  auto cta_of = [&](long long x) { return int(((x + 1) * ctas - 1) / T); };  // the CTA whose range holds tile x
   Pos start;
   {
     int lo = 0, hi = a.b;
@@ -371,23 +416,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     start.j = rem / start.Tr;
     start.t = rem - start.j * start.Tr;
   }
-  auto request = [&](Pos& p) {
-    const ReqQ8 q = req_q8(a, a.seq_lens[p.r], a.req_pool_idx[p.r], false);
-    p.len = q.len;
-    p.row = q.row;
-    p.Tr = (q.len + kKeys - 1) / kKeys + 1;
-  };
-  request(start);
+  request_of(a, start);
+  if (tid == 0) {
+    keep[0] = S;
+    keep[1] = E;
+    keep[2] = int(T);
+    keep[3] = start.r;
+    keep[4] = start.j;
+    keep[5] = start.t;
+  }
   __syncthreads();  // the scan's space becomes operand tiles
-  auto advance = [&](Pos& p) {
-    if (++p.t == p.Tr) {
-      p.t = 0;
-      if (++p.j == J) {
-        p.j = 0;
-        if (++p.r < a.b) request(p);
-      }
-    }
-  };
+  auto advance = [&](Pos& p) { next_pos(a, J, p); };
   // the piece of a unit that begins at position p, tile f of the range: its tiles
   auto piece_tiles = [&](const Pos& p, int f) { return min(p.Tr - p.t, E - f); };
   auto unit_rows = [&](int j) { return min(2 * kRows, M - 2 * kRows * (j % args.blocks)); };
@@ -396,7 +435,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     *abort_flag = 1;
   };
 
-  if (warp == 13) {
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 14) {
     // ============================ loader ============================
     // One bulk copy a group of 16 keys (16 D contiguous bytes of a page), a
     // lane each; the tree tile: one a node's row.  Page ids are read two tiles
@@ -501,7 +542,87 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       for (int k = 0; k < 50 && !mbar_try(bar(kRawFull0), ct & 1); ++k) {
       }
     }
-  } else if (warp >= 8 && warp < 12) {
+    } else if (warp < 14) {
+    // ============================ MMA issuers ============================
+    // One warp a softmax group, so that one's waits do not hold up the other's
+    // products.  The whole warp runs the role, so that its addresses and
+    // descriptors stay uniform (one lane alone spent more time forming them
+    // than the MMAs take); one elected lane issues.
+      const int w = warp - 12;
+      constexpr uint32_t id_s = idesc_f16(kKeys, false), id_st = idesc_f16(kTreeKeys, false), id_o = idesc_f16(D, true);
+      const uint32_t ub = __shfl_sync(FULL, sbase, 0), ut = __shfl_sync(FULL, tmem, 0);
+      const uint32_t dq = desc_lo(ub + L::kQ + uint32_t(w) * L::kTile, 16), dk0 = desc_lo(ub + L::kK, 16),
+                     dv0 = desc_lo(ub + L::kV, L::kBlock);
+      const uint32_t ds = ut + col_s(w), dp = ut + col_o(w);
+      bool ok = true;
+      auto wait = [&](int b, int parity) { return mbar_wait(bar(b), uint32_t(parity), abort_flag); };
+      Pos p = start;
+      int ct0 = 0, piece = 0, cs = 0;  // cs: S products issued
+      for (int f = S; ok && f < E; ++piece) {
+        const int n = piece_tiles(p, f);
+        const bool split = unit_rows(p.j) <= kRows;
+        const bool has_tree = p.t + n == p.Tr;
+        const int stride = split ? 2 : 1, first = split ? w : 0;
+        for (int t = first; t < n; t += stride) {
+          const int ct = ct0 + t, buf = ct & 1, ph = (ct >> 1) & 1;
+          const bool tree = has_tree && t == n - 1;
+          // S = Q K^T, over the P that the last P V has read
+          ok = (t > first || wait(kQFull0 + w, piece & 1)) && wait(kKFull0 + buf, ph) && (cs == 0 || wait(kPvDone0 + w, (cs - 1) & 1));
+          if (!__all_sync(FULL, ok && !*abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_after();
+          const uint32_t dk = dk0 + uint32_t(buf) * (L::kTile >> 4), dv = dv0 + uint32_t(buf) * (L::kTile >> 4);
+          if (elect_one()) {
+            const uint32_t id = tree ? id_st : id_s;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = uint32_t(((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4);
+              mma_ss(ds, desc(dq + o), desc(dk + o), id, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(bar(kSFull0 + w));
+            mma_commit(bar(kKEmpty0 + buf));
+            if (split) mma_commit(bar(kKEmpty0 + buf));  // the other group does not read this tile
+          }
+          __syncwarp();
+          // O += P V
+          ok = wait(kVFull0 + buf, ph) && (t > first || piece == 0 || wait(kOFree0 + w, (piece - 1) & 1)) && wait(kPReady0 + w, cs & 1);
+          ++cs;
+          if (!__all_sync(FULL, ok && !*abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_after();
+          if (elect_one()) {
+            const int steps = tree ? kTreeKeys / 16 : kKeys / 16;
+#pragma unroll 1
+            for (int kk = 0; kk < steps; kk += 4) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                mma_ts(dp, ds + (kk + q) * 8, desc(dv + uint32_t(((kk + q) * 16 * 128) >> 4)), id_o, t > first || kk + q > 0 ? 1u : 0u);
+            }
+            mma_commit(bar(kPvDone0 + w));
+            mma_commit(bar(kVEmpty0 + buf));
+            if (split) mma_commit(bar(kVEmpty0 + buf));
+          }
+          __syncwarp();
+        }
+        ct0 += n;
+        f += n;
+        p.t += n - 1;
+        advance(p);
+      }
+      if (!ok && !*abort_flag) fail();
+      // every MMA issued has completed before TMEM is released
+      __syncwarp();
+      if (elect_one()) mma_commit(bar(kDrain0 + w));
+      for (int i = 0; i < 1000 && !mbar_try(bar(kDrain0 + w), 0); ++i) {
+      }
+      __syncwarp();
+    }
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
     // ============================ converters ============================
     const int cw = warp - 8, ct_id = tid - 256;
     constexpr int kLoads = D / 16;               // 16-byte words a thread of a raw tile
@@ -511,23 +632,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     // group and key (in the tile) of a thread's word i of a history tile
     auto hist_key = [&](int i) { return D == 128 ? 16 * i + 4 * cw + lane / kLanesKey : 32 * i + 8 * cw + lane / kLanesKey; };
     auto tree_key = [&](int i) { return i * kRowsLoad + ct_id / kLanesRow; };
-    // word i of the thread, zeros where there is no key
-    auto read = [&](uint4 (&x)[kLoads], uint32_t rawt, bool tree, const uint32_t* info) {
-      if (!tree) {
+    // the thread's words of a history tile, zeros where there is no key
+    auto read = [&](uint4 (&x)[kLoads], uint32_t rawt, const uint32_t* info) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int key = hist_key(i);
-          x[i] = lds16(rawt + uint32_t(key * D + (lane % kLanesKey) * 16));
-          if (uint32_t(key & 15) >= info[key >> 4] >> 16) x[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kTreeLoads; ++i) {
-          const int key = tree_key(i);
-          x[i] = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
-          if (key >= a.n) x[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
+      for (int i = 0; i < kLoads; ++i) {
+        const int key = hist_key(i);
+        x[i] = lds16(rawt + uint32_t(key * D + (lane % kLanesKey) * 16));
+        if (uint32_t(key & 15) >= info[key >> 4] >> 16) x[i] = make_uint4(0u, 0u, 0u, 0u);
       }
+    };
+    // its word of a tree row
+    auto tree_row = [&](uint32_t rawt, int key) {
+      const uint4 x = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
+      return key < a.n ? x : make_uint4(0u, 0u, 0u, 0u);
     };
     // 16 e4m3 values -> two 16-byte chunks of their key's swizzled row
     auto store_hist = [&](uint32_t tile, const uint4 (&x)[kLoads]) {
@@ -537,14 +654,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         const int ch = lane % kLanesKey;  // elements 16 ch ..
         const uint32_t row = tile + uint32_t(ch >> 2) * L::kBlock + uint32_t(key) * 128u;
         const uint32_t c0 = uint32_t(2 * (ch & 3));
-        const uint4 lo = make_uint4(e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16), e4m3x2_to_f16x2(x[i].y),
-                                    e4m3x2_to_f16x2(x[i].y >> 16));
-        const uint4 hi = make_uint4(e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16), e4m3x2_to_f16x2(x[i].w),
-                                    e4m3x2_to_f16x2(x[i].w >> 16));
         // the second half's lanes store their upper chunk first: no two lanes of a phase share banks
         const bool swap = ch >= 4;
-        sts16(row + (((c0 + (swap ? 1u : 0u)) ^ uint32_t(key & 7)) << 4), swap ? hi : lo);
-        sts16(row + (((c0 + (swap ? 0u : 1u)) ^ uint32_t(key & 7)) << 4), swap ? lo : hi);
+        const uint32_t a0 = swap ? x[i].z : x[i].x, a1 = swap ? x[i].w : x[i].y, b0 = swap ? x[i].x : x[i].z, b1 = swap ? x[i].y : x[i].w;
+        const uint32_t at = row + (((c0 + (swap ? 1u : 0u)) ^ uint32_t(key & 7)) << 4);
+        sts16(at, make_uint4(e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(a1 >> 16)));
+        sts16(at ^ 16u, make_uint4(e4m3x2_to_f16x2(b0), e4m3x2_to_f16x2(b0 >> 16), e4m3x2_to_f16x2(b1), e4m3x2_to_f16x2(b1 >> 16)));
       }
     };
     auto row_exp = [&](const uint4& x) {  // exponent byte of a tree row's power of two, from its lanes
@@ -554,7 +669,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       for (int o = 1; o < kLanesRow; o <<= 1) mx = max(mx, __shfl_xor_sync(FULL, mx, o));
       return norm_exp(mx);
     };
-    auto store_tree = [&](uint32_t tile, uint4 x, int i, int e, bool finite) {
+    // (an inf or a NaN of V is left out here and added to the rows that see it at the end)
+    auto store_tree = [&](uint32_t tile, uint4 x, int key, int e, bool finite) {
       if (finite) {
         x.x = finite_bf16(x.x);
         x.y = finite_bf16(x.y);
@@ -563,211 +679,79 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       }
       const float inv = exp_scale(2 * kExpBias - e);
       auto cv = [&](uint32_t w) { return pack_f16(bf16_lo(w) * inv, bf16_hi(w) * inv); };
-      const int key = tree_key(i), ch = ct_id % kLanesRow;
+      const int ch = ct_id % kLanesRow;
       sts16(tile + uint32_t(ch >> 3) * L::kBlock + uint32_t(key) * 128u + ((uint32_t(ch & 7) ^ uint32_t(key & 7)) << 4),
             make_uint4(cv(x.x), cv(x.y), cv(x.z), cv(x.w)));
     };
     Pos p = start;
     int base = 113;
     bool ok = true;
-    for (int f = S, ct = 0; f < E; ++f, ++ct) {
+    auto wait = [&](int b, int parity) {
+      return __all_sync(FULL, mbar_wait(bar(b), uint32_t(parity), abort_flag) && !*abort_flag) != 0;
+    };
+    for (int f = S, ct = 0; ok && f < E; ++f, ++ct) {
       const int buf = ct & 1;
       const bool tree = p.t == p.Tr - 1, first = f == S || p.t == 0;
-      const uint32_t ktile = sbase + L::kK + uint32_t(buf) * L::kTile, vtile = sbase + L::kV + uint32_t(buf) * L::kTile;
       const uint32_t* info = infos + buf * kGroups;
       TileMeta& mt = metas[ct & 3];
-      uint4 x[kLoads];
-      // ---- K ----
-      bool go = mbar_wait(bar(kRawFull0), ct & 1, abort_flag) && !*abort_flag;
-      if (!__all_sync(FULL, go)) {
-        ok = false;
-        break;
-      }
-      read(x, sbase + L::kRawK, tree, info);
-      if (first) {
-        const int v0 = int(info[0] >> 8) & 255;
-        base = tree || v0 == 0 ? 113 : v0;
-      }
-      mbar_arrive(bar(kRawEmpty0));
-      go = (ct < 2 || mbar_wait(bar(kKEmpty0 + buf), ((ct >> 1) - 1) & 1, abort_flag)) && !*abort_flag;
-      if (!__all_sync(FULL, go)) {
-        ok = false;
-        break;
-      }
-      if (!tree) {
-        if (cw == 0 && lane < kGroups) {
-          const int ks = int(info[lane] & 255u), vs = int(info[lane] >> 8) & 255, cnt = int(info[lane] >> 16);
-          mt.group[lane] = cnt > 0 ? make_float4(exp_scale(ks), float(vs - base), ratio_scale(base - vs), float(cnt))
-                                   : make_float4(1.f, 0.f, 0.f, 0.f);
-        }
-        store_hist(ktile, x);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kTreeLoads; ++i) {
-          const int e = row_exp(x[i]);
-          if (ct_id % kLanesRow == 0) reinterpret_cast<uint8_t*>(&mt.node[tree_key(i)])[0] = uint8_t(e);
-          store_tree(ktile, x[i], i, e, false);
-        }
-        // (the V rows' exponents are wanted with the scores, before V itself)
-        go = mbar_wait(bar(kRawFull0 + 1), ct & 1, abort_flag) && !*abort_flag;
-        if (!__all_sync(FULL, go)) {
-          ok = false;
-          break;
-        }
-        read(x, sbase + L::kRawV, true, info);
-        unsigned long long nf = 0;
-#pragma unroll
-        for (int i = 0; i < kTreeLoads; ++i) {
-          const int e = row_exp(x[i]);
-          if (ct_id % kLanesRow == 0) reinterpret_cast<uint8_t*>(&mt.node[tree_key(i)])[1] = uint8_t(e);
-          const unsigned who = __ballot_sync(FULL, nonfinite_bf16(x[i].x) || nonfinite_bf16(x[i].y) ||
-                                                       nonfinite_bf16(x[i].z) || nonfinite_bf16(x[i].w));
-          if (who) {
-#pragma unroll
-            for (int q = 0; q < 32 / kLanesRow; ++q)
-              if ((who >> (q * kLanesRow)) & ((1u << kLanesRow) - 1u))
-                nf |= 1ull << (i * kRowsLoad + cw * (32 / kLanesRow) + q);
+#pragma unroll 1
+      for (int kv = 0; ok && kv < 2; ++kv) {  // K, V
+        const uint32_t tile = sbase + (kv ? L::kV : L::kK) + uint32_t(buf) * L::kTile, rawt = sbase + (kv ? L::kRawV : L::kRawK);
+        const int empty = (kv ? kVEmpty0 : kKEmpty0) + buf;
+        ok = wait(kRawFull0 + kv, ct & 1);
+        if (!ok) break;
+        if (kv == 0) {
+          if (first) {
+            const int v0 = int(info[0] >> 8) & 255;
+            base = tree || v0 == 0 ? 113 : v0;
           }
         }
-        if (lane == 0) mt.nonfinite[cw] = nf;
-      }
-      if (ct_id == 0) mt.base = base;
-      fence_async();
-      mbar_arrive(bar(kKFull0 + buf));
-      // ---- V ----
-      if (!tree) {
-        go = mbar_wait(bar(kRawFull0 + 1), ct & 1, abort_flag) && !*abort_flag;
-        if (!__all_sync(FULL, go)) {
-          ok = false;
-          break;
+        if (!tree) {
+          uint4 x[kLoads];
+          read(x, rawt, info);
+          mbar_arrive(bar(kRawEmpty0 + kv));
+          ok = ct < 2 || wait(empty, ((ct >> 1) - 1) & 1);
+          if (!ok) break;
+          if (kv == 0 && cw == 0 && lane < kGroups) {
+            const int ks = int(info[lane] & 255u), vs = int(info[lane] >> 8) & 255, cnt = int(info[lane] >> 16);
+            mt.group[lane] = cnt > 0 ? make_float4(exp_scale(ks), float(vs - base), ratio_scale(base - vs), float(cnt))
+                                     : make_float4(1.f, 0.f, 0.f, 0.f);
+          }
+          store_hist(tile, x);
+        } else {
+          ok = (ct < 2 || wait(empty, ((ct >> 1) - 1) & 1)) && (kv == 1 || wait(kRawFull0 + 1, ct & 1));
+          if (!ok) break;
+          // (the V rows' exponents are wanted with the scores, before V itself)
+          unsigned long long nf = 0;
+#pragma unroll 1
+          for (int i = 0; i < kTreeLoads; ++i) {
+            const int key = tree_key(i);
+            const uint4 x = tree_row(rawt, key);
+            const int e = row_exp(x);
+            if (kv == 0) {
+              const uint4 v = tree_row(sbase + L::kRawV, key);
+              const int ev = row_exp(v);
+              if (ct_id % kLanesRow == 0) mt.node[key] = uint16_t(e | (ev << 8));
+              const unsigned who = __ballot_sync(FULL, nonfinite_bf16(v.x) || nonfinite_bf16(v.y) || nonfinite_bf16(v.z) || nonfinite_bf16(v.w));
+#pragma unroll 1
+              for (int q = 0; q < 32 / kLanesRow; ++q)
+                if ((who >> (q * kLanesRow)) & ((1u << kLanesRow) - 1u))
+                  nf |= 1ull << (i * kRowsLoad + cw * (32 / kLanesRow) + q);
+            }
+            store_tree(tile, x, key, e, kv == 1);
+          }
+          if (kv == 0 && lane == 0) mt.nonfinite[cw] = nf;
+          mbar_arrive(bar(kRawEmpty0 + kv));
         }
-        read(x, sbase + L::kRawV, false, info);
+        if (kv == 0 && ct_id == 0) mt.base = base;
+        fence_async();
+        mbar_arrive(bar((kv ? kVFull0 : kKFull0) + buf));
       }
-      mbar_arrive(bar(kRawEmpty0 + 1));
-      go = (ct < 2 || mbar_wait(bar(kVEmpty0 + buf), ((ct >> 1) - 1) & 1, abort_flag)) && !*abort_flag;
-      if (!__all_sync(FULL, go)) {
-        ok = false;
-        break;
-      }
-      if (!tree) {
-        store_hist(vtile, x);
-      } else {
-        __syncwarp();  // what other lanes wrote of the tile's meta
-        const bool bad = mt.nonfinite[cw] != 0ull;
-#pragma unroll
-        for (int i = 0; i < kTreeLoads; ++i) store_tree(vtile, x[i], i, int(mt.node[tree_key(i)] >> 8), bad);
-      }
-      fence_async();
-      mbar_arrive(bar(kVFull0 + buf));
       advance(p);
     }
     if (!ok && !*abort_flag) fail();
-  } else if (warp == 12) {
-    // ============================ MMA issuer ============================
-    // The whole warp runs this role, so that its addresses and descriptors stay
-    // uniform (one lane alone spent more time forming them than the MMAs take);
-    // one elected lane issues.
-    {
-      constexpr uint32_t id_s = idesc_f16(kKeys, false), id_st = idesc_f16(kTreeKeys, false), id_o = idesc_f16(D, true);
-      const uint32_t ub = __shfl_sync(FULL, sbase, 0), ut = __shfl_sync(FULL, tmem, 0);
-      const uint64_t dq0 = sdesc(ub + L::kQ, 16, 1024), dk0 = sdesc(ub + L::kK, 16, 1024),
-                     dv0 = sdesc(ub + L::kV, L::kBlock, 1024);
-      constexpr uint64_t kTileStep = uint64_t(L::kTile >> 4);
-      bool ok = true;
-      int cs[2] = {0, 0};  // products S (and P V) issued for the group
-      auto wait = [&](int b, int parity) {
-        return __all_sync(FULL, mbar_wait(bar(b), uint32_t(parity), abort_flag) && !*abort_flag) != 0;
-      };
-      // S = Q K^T of group w for CTA tile ct
-      auto issue_s = [&](int w, int ct, bool tree, bool twice) -> bool {
-        if (cs[w] > 0 && !wait(kPvDone0 + w, (cs[w] - 1) & 1)) return false;
-        if (!wait(kKFull0 + (ct & 1), (ct >> 1) & 1)) return false;
-        tc_after();
-        const uint64_t dq = dq0 + uint64_t(w) * kTileStep, dk = dk0 + uint64_t(ct & 1) * kTileStep;
-        const uint32_t d = ut + col_s(w), id = tree ? id_st : id_s;
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t o = uint64_t(((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4);
-            mma_ss(d, dq + o, dk + o, id, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(bar(kSFull0 + w));
-          mma_commit(bar(kKEmpty0 + (ct & 1)));
-          if (twice) mma_commit(bar(kKEmpty0 + (ct & 1)));  // the other group does not read this tile
-        }
-        __syncwarp();
-        ++cs[w];
-        return true;
-      };
-      // O += P V of group w
-      auto issue_pv = [&](int w, int ct, bool tree, bool twice, bool zero, int piece) -> bool {
-        if (!wait(kVFull0 + (ct & 1), (ct >> 1) & 1)) return false;
-        if (zero && piece > 0 && !wait(kOFree0 + w, (piece - 1) & 1)) return false;
-        if (!wait(kPReady0 + w, (cs[w] - 1) & 1)) return false;
-        tc_after();
-        const uint64_t dv = dv0 + uint64_t(ct & 1) * kTileStep;
-        const uint32_t d = ut + col_o(w), pa = ut + col_s(w);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < kTreeKeys / 16; ++kk)
-            mma_ts(d, pa + kk * 8, dv + uint64_t((kk * 16 * 128) >> 4), id_o, !zero || kk > 0 ? 1u : 0u);
-          if (!tree) {
-#pragma unroll
-            for (int kk = kTreeKeys / 16; kk < kKeys / 16; ++kk)
-              mma_ts(d, pa + kk * 8, dv + uint64_t((kk * 16 * 128) >> 4), id_o, 1u);
-          }
-          mma_commit(bar(kPvDone0 + w));
-          mma_commit(bar(kVEmpty0 + (ct & 1)));
-          if (twice) mma_commit(bar(kVEmpty0 + (ct & 1)));
-        }
-        __syncwarp();
-        return true;
-      };
-      Pos p = start;
-      int ct = 0, piece = 0;
-      for (int f = S; ok && f < E; ++piece) {
-        const int n = piece_tiles(p, f);
-        const bool split = unit_rows(p.j) <= kRows;
-        const bool has_tree = p.t + n == p.Tr;
-        const int stride = split ? 2 : 1;
-        // group w's tiles: first(w), first(w) + stride, ..
-        const int first[2] = {0, split ? 1 : 0};
-        for (int w = 0; ok && w < 2; ++w)
-          if (first[w] < n) {
-            ok = wait(kQFull0 + w, piece & 1) && issue_s(w, ct + first[w], has_tree && first[w] == n - 1, split);
-          }
-        for (int s = 0; ok && s * stride < n; ++s) {
-          const int t0 = first[0] + s * stride, t1 = first[1] + s * stride;
-          const bool has1 = t1 < n;
-          auto pv = [&](int w, int t) { return issue_pv(w, ct + t, has_tree && t == n - 1, split, s == 0, piece); };
-          auto nx = [&](int w, int t) {
-            const int u = t + stride;
-            return u >= n || issue_s(w, ct + u, has_tree && u == n - 1, split);
-          };
-          ok = pv(0, t0);
-          // group 1's P V goes in behind group 0's at once if its P is there already
-          bool early = false;
-          if (ok && has1 && __all_sync(FULL, mbar_test(bar(kPReady0 + 1), (cs[1] - 1) & 1))) {
-            ok = pv(1, t1);
-            early = true;
-          }
-          ok = ok && nx(0, t0);
-          if (ok && has1) ok = (early || pv(1, t1)) && nx(1, t1);
-        }
-        ct += n;
-        f += n;
-        p.t += n - 1;
-        advance(p);
-      }
-      if (!ok && !*abort_flag) fail();
-      // every MMA issued has completed before TMEM is released
-      __syncwarp();
-      if (elect_one()) mma_commit(bar(kDrain));
-      for (int i = 0; i < 1000 && !mbar_try(bar(kDrain), 0); ++i) {
-      }
-    }
-    __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     // ============================ softmax groups ============================
     // (every tcgen05.ld / st and every exit around them is warp-uniform)
     const int w = warp >> 2, r = tid & 127;
@@ -776,27 +760,57 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     Pos p = start;
     int piece = 0, cs = 0, nfrag = 0, ct0 = 0;
     bool ok = true;
+    // row of the thread (and of its warp's others) in a unit: among the kv head's n * G
+    auto row_of = [&](const Pos& q, int rr) {
+      return 2 * kRows * (q.j % args.blocks) + (unit_rows(q.j) <= kRows ? 0 : kRows * w) + rr;
+    };
+    // A piece's Q rows go straight into their places of the operand tile (16
+    // lanes a row, coalesced; each warp its own 32 rows) and are divided and
+    // converted in place when the piece begins.  They are asked for as soon as
+    // the piece before has its last scores.
+    const uint32_t qtile = sbase + L::kQ + uint32_t(w) * L::kTile;
+    auto ask_q = [&](const Pos& q) {
+      constexpr int kChunks = D / 8, kRowsOp = 32 / kChunks;
+      const int h = q.j / args.blocks, ch = lane % kChunks;
+      int rr = 32 * (warp & 3) + lane / kChunks, g = row_of(q, rr);
+      int tok = g / G, hq = g - tok * G;  // (stepped: no division a row)
+#pragma unroll 1
+      for (int i = 0; i < 32 / kRowsOp; ++i, rr += kRowsOp, g += kRowsOp) {
+        const bool on = g < M;
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (size_t(q.r) * a.n + (on ? tok : 0)) * a.q_ld +
+                              size_t(h * G + (on ? hq : 0)) * D + ch * 8;
+        cp_async16(qtile + uint32_t(ch >> 3) * L::kBlock + uint32_t(rr) * 128u + ((uint32_t(ch & 7) ^ uint32_t(rr & 7)) << 4), src, on ? 16u : 0u);
+        for (hq += kRowsOp; hq >= G; hq -= G) ++tok;
+      }
+    };
+    if (S < E) ask_q(p);
     for (int f = S; ok && f < E; ++piece) {
       const int n = piece_tiles(p, f);
       const int rows = unit_rows(p.j);
       const bool split = rows <= kRows, complete = p.t == 0 && n == p.Tr;
       const int stride = split ? 2 : 1, first = split ? w : 0;
       const int h = p.j / args.blocks;
-      const int rg = 2 * kRows * (p.j % args.blocks) + (split ? 0 : kRows * w) + r;  // row among the kv head's n * G
+      const int rg = row_of(p, r);
       const bool valid = rg < M;
       const int node = valid ? rg / G : 0, head = h * G + (valid ? rg % G : 0);
       const bool mine = first < n;
       float m = -INFINITY, l = 0.f, xf = 0.f;
-      unsigned long long mask = 0, nonfinite = 0;
+      const unsigned long long mask = valid ? a.mask_bits[size_t(p.r) * a.n + node] : 0ull;
+      unsigned long long nonfinite = 0;
       int base = kExpBias;
-      if (mine) {
+      Pos pn = p;  // the next piece's position
+      pn.t += n - 1;
+      if (f + n < E) advance(pn);
+      {
         // ---- the row of Q, divided by its power of two, as f16 ----
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (size_t(p.r) * a.n + node) * a.q_ld + size_t(head) * D);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        const uint32_t qrow = qtile + uint32_t(r) * 128u;
+        auto chunk = [&](int i) { return qrow + uint32_t(i >> 3) * L::kBlock + ((uint32_t(i & 7) ^ uint32_t(r & 7)) << 4); };
         uint4 x[D / 8];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = valid ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-        mask = valid ? a.mask_bits[size_t(p.r) * a.n + node] : 0ull;
         uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = lds16(chunk(i));
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
           mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, x[i].x), x[i].y), x[i].z), x[i].w);
@@ -805,15 +819,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         const float inv = copysignf(exp_scale(2 * kExpBias - e), a.scale);
         xf = fabsf(a.scale) * 1.4426950408889634f * exp_scale(e);
         auto cv = [&](uint32_t u) { return pack_f16(bf16_lo(u) * inv, bf16_hi(u) * inv); };
-        const uint32_t qrow = sbase + L::kQ + uint32_t(w) * L::kTile + uint32_t(r) * 128u;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qrow + uint32_t(i >> 3) * L::kBlock + ((uint32_t(i & 7) ^ uint32_t(r & 7)) << 4)),
-                       "r"(cv(x[i].x)), "r"(cv(x[i].y)), "r"(cv(x[i].z)), "r"(cv(x[i].w))
-                       : "memory");
+        for (int i = 0; i < D / 8; ++i) sts16(chunk(i), make_uint4(cv(x[i].x), cv(x[i].y), cv(x[i].z), cv(x[i].w)));
         fence_async();
       }
       mbar_arrive(bar(kQFull0 + w));
+      if (!mine && f + n < E) ask_q(pn);  // (no product reads it)
       for (int t = first; t < n; t += stride, ++cs) {
         const bool s_ok = mbar_wait(bar(kSFull0 + w), cs & 1, abort_flag) && !*abort_flag;
         if (!__all_sync(FULL, s_ok)) {
@@ -824,120 +835,125 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         const TileMeta& mt = metas[(ct0 + t) & 3];
         base = mt.base;
         const bool tree = p.t + t == p.Tr - 1;
-        // ---- the row's maximum of x + e ----
-        float mx = -INFINITY;
-        auto max_group = [&](const uint32_t* u, int g) {
-          const float4 e = mt.group[g];
-          float v[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
-          if (e.w < float(kGroup)) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (float(i) >= e.w) v[i] = -INFINITY;
-          }
-          float q[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) q[i] = fmaxf(fmaxf(v[4 * i], v[4 * i + 1]), fmaxf(v[4 * i + 2], v[4 * i + 3]));
-          mx = fmaxf(mx, fmaf(fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3])), xf * e.x, e.y));
-        };
-        auto tree_score = [&](uint32_t u, int k, int e) {  // e: the node's exponent bytes
-          return k < a.n && ((mask >> k) & 1ull) ? fmaf(__uint_as_float(u), xf * exp_scale(e & 255), float((e >> 8) - base))
-                                                : -INFINITY;
-        };
-        uint32_t ua[16], ub[16];  // groups in flight: one is loaded while the other is worked on
-        tmem_ld16(ts, ua);
-        tmem_ld_wait();
-        if (!tree) {
-#pragma unroll 1
-          for (int c = 0; c < kGroups; c += 2) {
-            tmem_ld16(ts + 16 * (c + 1), ub);
-            max_group(ua, c);
-            tmem_ld_wait();
-            tmem_ld16(ts + 16 * (c + 2 < kGroups ? c + 2 : 0), ua);  // (at the end: the first again, for the next pass)
-            max_group(ub, c + 1);
-            tmem_ld_wait();
-          }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < kTreeKeys / 16; ++c) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, tree_score(ua[i], 16 * c + i, mt.node[16 * c + i]));
-            tmem_ld16(ts + 16 * (c + 1 < kTreeKeys / 16 ? c + 1 : 0), ua);
-            tmem_ld_wait();
-          }
-        }
-        // ---- the reference moves only when P would pass 2^kLazyLog2 times its value at the maximum; O is
-        // rescaled then (P V of the tile before is complete: S of this one was issued after it) ----
-        if (__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2))) {
+        float lt = 0.f;
+        // The reference m is moved, to a whole number, when a score would put P
+        // above 2^(kPBaseLog2 + kLazyLog2).  O, l and what the tile has stored of
+        // P so far (`done` chunks) are multiplied by that power of two, exactly.
+        // (P V of the tile before is complete: S of this one was issued after it.)
+        auto move = [&](float mx, int done) {
           const bool up = mx > m + (kLazyLog2 + kPBaseLog2);
-          const float fac = up ? fast_exp2(m + kPBaseLog2 - mx) : 1.f;
+          const float mn = ceilf(mx) - kPBaseLog2;
+          const float fac = !up ? 1.f : m == -INFINITY ? 0.f : ratio_scale(int(fmaxf(m - mn, -126.f)));
           l *= fac;
-          if (up) m = mx - kPBaseLog2;
+          lt *= fac;
+          if (up) m = mn;
+          tmem_st_wait();
+#pragma unroll 1
+          for (int c = 0; c < done; ++c) {
+            uint32_t o[16];
+            tmem_ld16(ts + 16 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 q = __half22float2(*reinterpret_cast<__half2*>(&o[i]));
+              o[i] = pack_f16(q.x * fac, q.y * fac);
+            }
+            tmem_st16(ts + 16 * c, o);
+          }
           if (t > first) {
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
-              tmem_ld16(to + 16 * c, ub);
+              uint32_t o[16];
+              tmem_ld16(to + 16 * c, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) ub[i] = __float_as_uint(__uint_as_float(ub[i]) * fac);
-              tmem_st16(to + 16 * c, ub);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
+              tmem_st16(to + 16 * c, o);
             }
           }
-        }
-        // ---- P and its sum; P of a group goes over scores that have been read ----
-        const float mr = m == -INFINITY ? 0.f : m;
-        float lt = 0.f;
-        auto exp_group = [&](const uint32_t* u, int g) {
-          const float4 e = mt.group[g];
-          float v[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
-          if (e.w < float(kGroup)) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (float(i) >= e.w) v[i] = -INFINITY;
-          }
-          const float xk = xf * e.x, off = e.y - mr;
-          float2 s0 = make_float2(0.f, 0.f);
-          const float2 k2 = make_float2(xk, xk), o2 = make_float2(off, off);
-          uint32_t pk[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 y = fma2(make_float2(v[2 * i], v[2 * i + 1]), k2, o2);
-            const float2 q = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-            s0 = add2(s0, q);
-            pk[i] = pack_f16(q.x, q.y);
-          }
-          lt = fmaf(s0.x + s0.y, e.z, lt);
-          tmem_st8(ts + 8 * g, pk);
+          tmem_st_wait();
         };
+        if (t + stride >= n && f + n < E) ask_q(pn);  // every product that reads this piece's Q is complete
         if (!tree) {
+          // Half a tile at a time (its P goes over scores that have been read), in
+          // a short loop: unrolled, or with the tree's case inside, the roles' code
+          // outran the instruction caches and half of the warps' time went to
+          // fetching it; with quarters the latencies of a step were not covered.
 #pragma unroll 1
-          for (int c = 0; c < kGroups; c += 2) {
-            tmem_ld16(ts + 16 * (c + 1), ub);
-            exp_group(ua, c);
+          for (int c = 0; c < 4; c += 2) {
+            uint32_t u[64];
+            tmem_ld32(ts + 32 * c, u);
+            tmem_ld32(ts + 32 * c + 32, u + 32);
+            float4 e[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) e[g] = mt.group[2 * c + g];
             tmem_ld_wait();
-            if (c + 2 < kGroups) tmem_ld16(ts + 16 * (c + 2), ua);
-            exp_group(ub, c + 1);
-            tmem_ld_wait();
+            if (e[0].w + e[1].w + e[2].w + e[3].w < float(4 * kGroup)) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (float(i) >= e[g].w) u[16 * g + i] = 0xff800000u;
+            }
+            float mx = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              float q[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                q[i] = fmaxf(fmaxf(__uint_as_float(u[16 * g + 4 * i]), __uint_as_float(u[16 * g + 4 * i + 1])),
+                             fmaxf(__uint_as_float(u[16 * g + 4 * i + 2]), __uint_as_float(u[16 * g + 4 * i + 3])));
+              e[g].x *= xf;
+              mx = fmaxf(mx, fmaf(fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3])), e[g].x, e[g].y));
+            }
+            if (__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2))) move(mx, c);
+            const float mr = m == -INFINITY ? 0.f : m;
+            uint32_t pk[32];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const float off = e[g].y - mr;
+              const float2 k2 = make_float2(e[g].x, e[g].x), o2 = make_float2(off, off);
+              float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 y = fma2(make_float2(__uint_as_float(u[16 * g + 2 * i]), __uint_as_float(u[16 * g + 2 * i + 1])), k2, o2);
+                const float2 q = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                if (i & 1) s1 = add2(s1, q);
+                else s0 = add2(s0, q);
+                pk[8 * g + i] = pack_f16(q.x, q.y);
+              }
+              s0 = add2(s0, s1);
+              lt = fmaf(s0.x + s0.y, e[g].z, lt);
+            }
+            tmem_st32(ts + 16 * c, pk);
           }
         } else {
           nonfinite = mt.nonfinite[0] | mt.nonfinite[1] | mt.nonfinite[2] | mt.nonfinite[3];
 #pragma unroll 1
-          for (int c = 0; c < kTreeKeys / 16; ++c) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const int e0 = mt.node[16 * c + i], e1 = mt.node[16 * c + i + 1];
-              const float q0 = fast_exp2(tree_score(ua[i], 16 * c + i, e0) - mr);
-              const float q1 = fast_exp2(tree_score(ua[i + 1], 16 * c + i + 1, e1) - mr);
-              lt = fmaf(q0, ratio_scale(base - (e0 >> 8)), fmaf(q1, ratio_scale(base - (e1 >> 8)), lt));
-              pk[i / 2] = pack_f16(q0, q1);
-            }
-            if (c + 1 < kTreeKeys / 16) tmem_ld16(ts + 16 * (c + 1), ua);
+          for (int c = 0; c < kTreeKeys / 32; ++c) {
+            uint32_t u[32], pk[16];
+            tmem_ld32(ts + 32 * c, u);
             tmem_ld_wait();
-            tmem_st8(ts + 8 * c, pk);
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {  // (scores become x + e)
+              const int k = 32 * c + i, e = mt.node[k];
+              const float x = k < a.n && ((mask >> k) & 1ull)
+                                  ? fmaf(__uint_as_float(u[i]), xf * exp_scale(e & 255), float((e >> 8) - base))
+                                  : -INFINITY;
+              u[i] = __float_as_uint(x);
+              mx = fmaxf(mx, x);
+            }
+            if (__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2))) move(mx, c);
+            const float mr = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int k = 32 * c + 2 * i;
+              const float q0 = fast_exp2(__uint_as_float(u[2 * i]) - mr), q1 = fast_exp2(__uint_as_float(u[2 * i + 1]) - mr);
+              lt = fmaf(q0, ratio_scale(base - (mt.node[k] >> 8)), fmaf(q1, ratio_scale(base - (mt.node[k + 1] >> 8)), lt));
+              pk[i] = pack_f16(q0, q1);
+            }
+            tmem_st16(ts + 16 * c, pk);
           }
         }
         l += lt;
@@ -959,12 +975,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       const bool direct = complete && !split;
       const int slot = 2 * int(blockIdx.x) + (complete || p.t == 0 ? 1 : 0);  // (0: a unit that an earlier CTA began)
       const bool local = complete && split;
-      float* so = args.slot_o + ((size_t(slot) * 2 + w) * kRows + r) * D;
+      // a slot's O: 16-byte words [4 columns][row], so that a warp stores 512 contiguous bytes
+      float4* so = reinterpret_cast<float4*>(args.slot_o) + (size_t(slot) * 2 + w) * kRows * (D / 4) + r;
       float2* sm = reinterpret_cast<float2*>(args.slot_ml) + (size_t(slot) * 2 + w) * kRows + r;
       const size_t orow = (size_t(p.r) * a.n + node) * a.Hq + head;
       float om = -INFINITY, ol = 0.f;  // group 1's half of a unit that group 0 finishes
-      // (group 1 without a tile may be here before group 0 has read its last half)
-      if (split && w == 1 && nfrag > 0 && !__all_sync(FULL, mbar_wait(bar(kFragFree), (nfrag - 1) & 1, abort_flag))) {
+      // (group 0 may not have read the last half that group 1 left in the slot)
+      if (!direct && w == 1 && nfrag > 0 && !__all_sync(FULL, mbar_wait(bar(kFragFree), (nfrag - 1) & 1, abort_flag))) {
         ok = false;
         break;
       }
@@ -988,17 +1005,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       const float wa = has_o && m != M2 ? fast_exp2(m - M2) : 1.f, wb = has_o ? fast_exp2(om - M2) : 0.f;
       const float Ls = has_o ? l * wa + ol * wb : l;
       const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float v[32];
         if (mine) {
-          tmem_ld32(to + 32 * c, v);
+          uint32_t o[32];
+          tmem_ld32(to + 32 * c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * vs;
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= vs;
         if (any_nf && nf) {
           for (int q = 0; q < a.n; ++q)
             if ((nf >> q) & 1ull) {
@@ -1012,10 +1031,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         }
         if (direct || (local && w == 0)) {
           if (has_o) {
-            const float4* oo = reinterpret_cast<const float4*>(so + size_t(kRows) * D) + 8 * c;
+            const float4* oo = so + size_t(kRows) * (D / 4) + size_t(8 * c) * kRows;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float4 y = __ldcg(oo + i);
+              const float4 y = __ldcg(oo + i * kRows);
               v[4 * i] = v[4 * i] * wa + y.x * wb;
               v[4 * i + 1] = v[4 * i + 1] * wa + y.y * wb;
               v[4 * i + 2] = v[4 * i + 2] * wa + y.z * wb;
@@ -1030,9 +1049,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
                                   pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
           }
         } else if (valid) {
-          float4* dst = reinterpret_cast<float4*>(so) + 8 * c;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          for (int i = 0; i < 8; ++i) so[(8 * c + i) * kRows] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
       }
       if (direct || (local && w == 0)) {
@@ -1047,10 +1065,113 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       mbar_arrive(bar(kOFree0 + w));  // the next piece may write O
       ct0 += n;
       f += n;
-      p.t += n - 1;
-      advance(p);
+      p = pn;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok && !*abort_flag) fail();
+    // The softmax groups join what the CTA shares with others (here, not at the
+    // kernel's end, where every warp would have to hold the registers for it, and
+    // what it needs comes out of shared memory, for the same reason).  The vote
+    // makes the decision one for all of them.
+    if (!soft_any(!ok || *abort_flag) && S < E) {
+      auto kept = [&](int i) {
+        int v;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(smem_u32(keep + i)) : "memory");
+        return v;
+      };
+      const int S2 = kept(0), E2 = kept(1);
+      const long long T2 = kept(2), ctas2 = T2 < gridDim.x ? T2 : gridDim.x;
+      auto cta_of = [&](long long x) { return int(((x + 1) * ctas2 - 1) / T2); };  // the CTA whose range holds tile x
+
+      // ---- units shared with other CTAs: count in, and join those that are last ----
+      Pos head;
+      head.r = kept(3);
+      head.j = kept(4);
+      head.t = kept(5);
+      request_of(a, head);
+      Pos last = head;
+      int last_f = S2;
+      {  // the first position of the range's last piece
+        int f = S2;
+        Pos q = head;
+        while (true) {
+          const int n = min(q.Tr - q.t, E2 - f);
+          last = q;
+          last_f = f;
+          if (f + n >= E2) break;
+          f += n;
+          q.t += n - 1;
+          next_pos(a, J, q);
+        }
+      }
+      for (int x = 0; x < 2; ++x) {
+        const Pos& q = x == 0 ? head : last;
+        if (x == 1 && last.r == head.r && last.j == head.j) break;  // one unit only
+        const long long us = (x == 0 ? S2 : last_f) - q.t;  // the unit's first tile
+        const int ca = cta_of(us), cb = cta_of(us + q.Tr - 1);
+        if (ca == cb) continue;
+        soft_sync();
+        if (tid == 0) keep[-1] = atom_add_acq_rel(args.counters + ca) == uint32_t(cb - ca);
+        soft_sync();
+        if (!keep[-1]) continue;
+        const int rows = unit_rows(q.j), h = q.j / args.blocks;
+        const bool split = rows <= kRows;
+        // a thread a row (two a row when the unit has one row tile: half of the
+        // columns each)
+        constexpr int C4 = D / 4;
+        const int row = split ? tid & 127 : tid, c0 = split && tid >= kRows ? C4 / 2 : 0, c1 = split && tid < kRows ? C4 / 2 : C4;
+        const int nf = (cb - ca + 1) * (split ? 2 : 1);
+        auto at = [&](int y) {
+          const int cta = ca + (split ? y >> 1 : y);
+          return size_t(2 * cta + (cta == ca ? 1 : 0)) * 2 + (split ? y & 1 : row / kRows);
+        };
+        const bool on = row < rows;
+        float Mx = -INFINITY, Ls = 0.f;
+        if (on) {
+#pragma unroll 4
+          for (int y = 0; y < nf; ++y) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(args.slot_ml) + at(y) * kRows + row % kRows);
+            const bool has = ml.y > 0.f || ml.y != ml.y;  // (else it saw nothing, and its O is not read)
+            const float M2 = has ? fmaxf(Mx, ml.x) : Mx;
+            const float wa = Ls > 0.f || Ls != Ls ? exp2f(Mx - M2) : 0.f;
+            Ls = has ? Ls * wa + ml.y * exp2f(ml.x - M2) : Ls;
+            Mx = M2;
+          }
+          const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+          const int rg = 2 * kRows * (q.j % args.blocks) + row;
+          const size_t orow = (size_t(q.r) * a.n + rg / G) * a.Hq + h * G + rg % G;
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D);
+          for (int c = c0; c < c1; c += 8) {  // 32 columns, all their loads of a fragment in flight
+            float4 acc[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int y = 0; y < nf; ++y) {
+              const float4* src = reinterpret_cast<const float4*>(args.slot_o) + (at(y) * C4 + c) * kRows + row % kRows;
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(args.slot_ml) + at(y) * kRows + row % kRows);
+              float4 o4[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o4[e] = __ldcg(src + e * kRows);
+              if (!(ml.y > 0.f || ml.y != ml.y)) continue;
+              const float k = exp2f(ml.x - Mx) * inv;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                acc[e].x = fmaf(o4[e].x, k, acc[e].x);
+                acc[e].y = fmaf(o4[e].y, k, acc[e].y);
+                acc[e].z = fmaf(o4[e].z, k, acc[e].z);
+                acc[e].w = fmaf(o4[e].w, k, acc[e].w);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 2)
+              dst[(c + e) / 2] = make_uint4(pack_bf16x2(acc[e].x, acc[e].y), pack_bf16x2(acc[e].z, acc[e].w),
+                                            pack_bf16x2(acc[e + 1].x, acc[e + 1].y), pack_bf16x2(acc[e + 1].z, acc[e + 1].w));
+          }
+          if (c0 == 0 && a.lse) a.lse[orow] = lse_of(Mx, Ls);
+        }
+        if (tid == 0) atomicExch(args.counters + ca, 0u);
+      }
+    }
   }
 
   // ---- teardown ----
@@ -1060,58 +1181,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
-  if (*abort_flag || S >= E) return;
-
-  // ---- units shared with other CTAs: count in, and join those that are last ----
-  Pos last = start;
-  int last_f = S;
-  {  // the first position of the range's last piece
-    int f = S;
-    Pos q = start;
-    while (true) {
-      const int n = piece_tiles(q, f);
-      last = q;
-      last_f = f;
-      if (f + n >= E) break;
-      f += n;
-      q.t += n - 1;
-      advance(q);
-    }
-  }
-  for (int x = 0; x < 2; ++x) {
-    const Pos& q = x == 0 ? start : last;
-    if (x == 1 && last.r == start.r && last.j == start.j) break;  // one unit only
-    const long long us = (x == 0 ? S : last_f) - q.t;  // the unit's first tile
-    const int ca = cta_of(us), cb = cta_of(us + q.Tr - 1);
-    if (ca == cb) continue;
-    __syncthreads();
-    if (tid == 0) *s_last = atom_add_acq_rel(args.counters + ca) == uint32_t(cb - ca);
-    __syncthreads();
-    if (!*s_last) continue;
-    const int rows = unit_rows(q.j), h = q.j / args.blocks;
-    const bool split = rows <= kRows;
-    constexpr int C4 = D / 4;
-    for (int i = tid; i < rows * C4; i += kTcThreads) {
-      const int row = i / C4, c = i % C4;
-      float Mx = -INFINITY, Ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-      for (int y = 0; y < (cb - ca + 1) * (split ? 2 : 1); ++y) {
-        const int cta = ca + (split ? y >> 1 : y);
-        const size_t at = (size_t(2 * cta + (cta == ca ? 1 : 0)) * 2 + (split ? y & 1 : row / kRows)) * kRows + row % kRows;
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(args.slot_ml) + at);
-        const float4 o4 = __ldcg(reinterpret_cast<const float4*>(args.slot_o) + at * C4 + c);
-        const float v[4] = {o4.x, o4.y, o4.z, o4.w};
-        join<4>(Mx, Ls, acc, ml.x, ml.y, v);
-      }
-      const int rg = 2 * kRows * (q.j % args.blocks) + row;
-      const size_t orow = (size_t(q.r) * a.n + rg / G) * a.Hq + h * G + rg % G;
-      const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + 4 * c) =
-          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-      if (c == 0 && a.lse) a.lse[orow] = lse_of(Mx, Ls);
-    }
-    if (tid == 0) atomicExch(args.counters + ca, 0u);
-  }
 }
 
 template <int D>
@@ -1120,6 +1189,9 @@ int launch_tc(const AttentionQ8Params& p, cudaStream_t stream) {
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return SPEC_ERR_LAUNCH;
+  // the register split assumes what the CTA is launched with
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, attention_q8_tc_kernel<D>) != cudaSuccess || attr.numRegs != kRegs) return SPEC_ERR_LAUNCH;
   // at least 120 KB, so that two CTAs never share a SM (each holds all of TMEM)
   size_t smem = TcSmem<D>::kBytes + 1024;
   if (smem < 120 * 1024) smem = 120 * 1024;
