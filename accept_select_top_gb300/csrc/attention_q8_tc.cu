@@ -49,6 +49,7 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kKeys = 128;       // history keys of a tile
 constexpr int kTreeKeys = 64;    // nodes of the tree tile
+constexpr int kStep = 64;        // keys of a step of S, softmax and P V
 constexpr int kGroup = 16;       // keys with one page at least
 constexpr int kGroups = kKeys / kGroup;
 constexpr int kTcThreads = 16 * 32;
@@ -59,7 +60,7 @@ static_assert(2 * kRegsSoft + kRegsConv + kRegsIssue <= 4 * kRegs, "register spl
 constexpr int kConvThreads = 128, kSoftThreads = 256;
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wait
 __host__ __device__ constexpr uint32_t col_o(int w) { return 128u * uint32_t(w); }
-__host__ __device__ constexpr uint32_t col_s(int w) { return 256u + 128u * uint32_t(w); }
+__host__ __device__ constexpr uint32_t col_s(int w, int b) { return 256u + 128u * uint32_t(w) + 64u * uint32_t(b); }
 
 // What the softmax needs of a tile: of a history tile, for each group of 16
 // keys, {K scale, V exponent relative to the unit's base, its inverse factor in
@@ -87,9 +88,9 @@ struct TcSmem {
   static constexpr int kMeta = kRawV + kRaw;       // four
   static constexpr int kInfo = kMeta + 4 * int(sizeof(TileMeta));  // [2][8]: scale bytes and keys of a raw tile's groups
   static constexpr int kBars = kInfo + 64;
-  static constexpr int kAbort = kBars + 8 * 26 + 4;  // (after the barriers: TMEM address, abort flag)
+  static constexpr int kAbort = kBars + 8 * 30 + 4;  // (after the barriers: TMEM address, abort flag)
   static constexpr int kKeep = kAbort + 4 + 4 * 17;  // 16 words of the scan and one before it
-  static constexpr int kBytes = kBars + 384;
+  static constexpr int kBytes = kBars + 448;
   // the tiles before each request are summed up in what will hold operands
   static_assert(4 * (kAttentionQ8MaxB + 1) <= 2 * kTile, "scan space");
 };
@@ -101,16 +102,16 @@ enum {
   kVFull0 = 4,
   kVEmpty0 = 6,
   kQFull0 = 8,  // + group
-  kSFull0 = 10,
-  kPReady0 = 12,
-  kPvDone0 = 14,
-  kOFree0 = 16,  // the epilogue has read O
-  kFragFull = 18,  // group 1 stored its half of a unit that this CTA finishes
-  kFragFree = 19,  // group 0 has read it
-  kDrain0 = 20,     // + group
-  kRawFull0 = 22,   // + (K, V): the raw tile has landed
-  kRawEmpty0 = 24,  // the converters have read it
-  kNumBars = 26
+  kPvDone0 = 10,
+  kOFree0 = 12,    // the epilogue has read O
+  kFragFull = 14,  // group 1 stored its half of a unit that this CTA finishes
+  kFragFree = 15,  // group 0 has read it
+  kDrain0 = 16,    // + group
+  kRawFull0 = 18,  // + (K, V): the raw tile has landed
+  kRawEmpty0 = 20, // the converters have read it
+  kSFull0 = 22,    // + 2 group + S buffer
+  kPReady0 = 26,   // + 2 group + S buffer (the next step's P may be there before this one's is waited for)
+  kNumBars = 30
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -236,7 +237,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// 32 / 16 columns stored (tmem_st_wait completes them)
+// 8, 16, 32 columns stored (tmem_st_wait completes them)
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
@@ -344,8 +350,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       mbar_init(bar(kVFull0 + i), kConvThreads);
       mbar_init(bar(kVEmpty0 + i), 2);
       mbar_init(bar(kQFull0 + i), kRows);
-      mbar_init(bar(kSFull0 + i), 1);
-      mbar_init(bar(kPReady0 + i), kRows);
+      mbar_init(bar(kSFull0 + 2 * i), 1);
+      mbar_init(bar(kSFull0 + 2 * i + 1), 1);
+      mbar_init(bar(kPReady0 + 2 * i), kRows);
+      mbar_init(bar(kPReady0 + 2 * i + 1), kRows);
       mbar_init(bar(kPvDone0 + i), 1);
       mbar_init(bar(kOFree0 + i), kRows);
     }
@@ -549,64 +557,83 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     // descriptors stay uniform (one lane alone spent more time forming them
     // than the MMAs take); one elected lane issues.
       const int w = warp - 12;
-      constexpr uint32_t id_s = idesc_f16(kKeys, false), id_st = idesc_f16(kTreeKeys, false), id_o = idesc_f16(D, true);
       const uint32_t ub = __shfl_sync(FULL, sbase, 0), ut = __shfl_sync(FULL, tmem, 0);
       const uint32_t dq = desc_lo(ub + L::kQ + uint32_t(w) * L::kTile, 16), dk0 = desc_lo(ub + L::kK, 16),
                      dv0 = desc_lo(ub + L::kV, L::kBlock);
-      const uint32_t ds = ut + col_s(w), dp = ut + col_o(w);
+      const uint32_t dp = ut + col_o(w);
       bool ok = true;
       auto wait = [&](int b, int parity) { return mbar_wait(bar(b), uint32_t(parity), abort_flag); };
       Pos p = start;
-      int ct0 = 0, piece = 0, cs = 0;  // cs: S products issued
+      // Steps of 64 keys, counted over the whole range: ns products S issued, np
+      // products P V, seen of these known to be complete (each phase is waited for
+      // in turn, and P V of step k only issued once that of step k - 1 is seen).
+      int ct0 = 0, piece = 0, ns = 0, np = 0, seen = 0;
       for (int f = S; ok && f < E; ++piece) {
         const int n = piece_tiles(p, f);
         const bool split = unit_rows(p.j) <= kRows;
-        const bool has_tree = p.t + n == p.Tr;
-        const int stride = split ? 2 : 1, first = split ? w : 0;
-        for (int t = first; t < n; t += stride) {
-          const int ct = ct0 + t, buf = ct & 1, ph = (ct >> 1) & 1;
-          const bool tree = has_tree && t == n - 1;
-          // S = Q K^T, over the P that the last P V has read
-          ok = (t > first || wait(kQFull0 + w, piece & 1)) && wait(kKFull0 + buf, ph) && (cs == 0 || wait(kPvDone0 + w, (cs - 1) & 1));
-          if (!__all_sync(FULL, ok && !*abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_after();
-          const uint32_t dk = dk0 + uint32_t(buf) * (L::kTile >> 4), dv = dv0 + uint32_t(buf) * (L::kTile >> 4);
-          if (elect_one()) {
-            const uint32_t id = tree ? id_st : id_s;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t o = uint32_t(((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4);
-              mma_ss(ds, desc(dq + o), desc(dk + o), id, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(bar(kSFull0 + w));
-            mma_commit(bar(kKEmpty0 + buf));
-            if (split) mma_commit(bar(kKEmpty0 + buf));  // the other group does not read this tile
-          }
-          __syncwarp();
-          // O += P V
-          ok = wait(kVFull0 + buf, ph) && (t > first || piece == 0 || wait(kOFree0 + w, (piece - 1) & 1)) && wait(kPReady0 + w, cs & 1);
-          ++cs;
-          if (!__all_sync(FULL, ok && !*abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_after();
-          if (elect_one()) {
-            const int steps = tree ? kTreeKeys / 16 : kKeys / 16;
+        const int tree_at = p.t + n == p.Tr ? n - 1 : n, stride = split ? 2 : 1, first = split ? w : 0;
+        int ts = first, hs = 0, tp = first, hp = 0;  // the tile and half that S and P V are at
+        // The next step's S goes into the other buffer as soon as P V of the step
+        // before has read it, so that the softmax of a step runs beside the
+        // products of its neighbours.
+        for (bool begin = true; ok && tp < n; begin = false) {
 #pragma unroll 1
-            for (int kk = 0; kk < steps; kk += 4) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                mma_ts(dp, ds + (kk + q) * 8, desc(dv + uint32_t(((kk + q) * 16 * 128) >> 4)), id_o, t > first || kk + q > 0 ? 1u : 0u);
+          while (ok && ts < n && ns < np + 2) {
+            const int ct = ct0 + ts, buf = ct & 1;
+            const bool tree = ts == tree_at, last = tree || hs == 1;
+            ok = (ts > first || hs == 1 || wait(kQFull0 + w, piece & 1)) && (hs == 1 || wait(kKFull0 + buf, (ct >> 1) & 1));
+            if (ok && seen < ns - 1) {
+              ok = wait(kPvDone0 + w, seen & 1);
+              ++seen;
             }
+            ok = __all_sync(FULL, ok && !*abort_flag) != 0;
+            if (!ok) break;
+            tc_after();
+            const uint32_t dk = dk0 + uint32_t(buf) * (L::kTile >> 4) + uint32_t(hs) * (kStep * 128 >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t o = uint32_t(((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4);
+                mma_ss(ut + col_s(w, ns & 1), desc(dq + o), desc(dk + o), idesc_f16(kStep, false), kk > 0 ? 1u : 0u);
+              }
+              mma_commit(bar(kSFull0 + 2 * w + (ns & 1)));
+              if (last) {
+                mma_commit(bar(kKEmpty0 + buf));
+                if (split) mma_commit(bar(kKEmpty0 + buf));  // the other group does not read this tile
+              }
+            }
+            __syncwarp();
+            ++ns;
+            hs = last ? 0 : 1;
+            ts += last ? stride : 0;
+          }
+          if (!ok) break;
+          const int ct = ct0 + tp, buf = ct & 1;
+          const bool tree = tp == tree_at, last = tree || hp == 1;
+          ok = (hp == 1 || wait(kVFull0 + buf, (ct >> 1) & 1)) && (!begin || piece == 0 || wait(kOFree0 + w, (piece - 1) & 1));
+          if (ok && seen < np) {
+            ok = wait(kPvDone0 + w, seen & 1);
+            ++seen;
+          }
+          ok = ok && wait(kPReady0 + 2 * w + (np & 1), (np >> 1) & 1);
+          ok = __all_sync(FULL, ok && !*abort_flag) != 0;
+          if (!ok) break;
+          tc_after();
+          const uint32_t dv = dv0 + uint32_t(buf) * (L::kTile >> 4) + uint32_t(hp) * (kStep * 128 >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kStep / 16; ++kk)
+              mma_ts(dp, ut + col_s(w, np & 1) + kk * 8, desc(dv + uint32_t((kk * 16 * 128) >> 4)), idesc_f16(D, true), !begin || kk > 0 ? 1u : 0u);
             mma_commit(bar(kPvDone0 + w));
-            mma_commit(bar(kVEmpty0 + buf));
-            if (split) mma_commit(bar(kVEmpty0 + buf));
+            if (last) {
+              mma_commit(bar(kVEmpty0 + buf));
+              if (split) mma_commit(bar(kVEmpty0 + buf));
+            }
           }
           __syncwarp();
+          ++np;
+          hp = last ? 0 : 1;
+          tp += last ? stride : 0;
         }
         ct0 += n;
         f += n;
@@ -756,7 +783,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     // (every tcgen05.ld / st and every exit around them is warp-uniform)
     const int w = warp >> 2, r = tid & 127;
     const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
-    const uint32_t ts = tl + col_s(w), to = tl + col_o(w);
+    const uint32_t to = tl + col_o(w);
     Pos p = start;
     int piece = 0, cs = 0, nfrag = 0, ct0 = 0;
     bool ok = true;
@@ -825,95 +852,81 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       }
       mbar_arrive(bar(kQFull0 + w));
       if (!mine && f + n < E) ask_q(pn);  // (no product reads it)
-      for (int t = first; t < n; t += stride, ++cs) {
-        const bool s_ok = mbar_wait(bar(kSFull0 + w), cs & 1, abort_flag) && !*abort_flag;
+      // The reference m is moved, to a whole number, when a score would put P above
+      // 2^(kPBaseLog2 + kLazyLog2); O and l are multiplied by that power of two,
+      // exactly, once the products so far are complete.
+      auto move = [&](float mx, bool o_live) {
+        const bool up = mx > m + (kLazyLog2 + kPBaseLog2);
+        const float mn = ceilf(mx) - kPBaseLog2;
+        const float fac = !up ? 1.f : m == -INFINITY ? 0.f : ratio_scale(int(fmaxf(m - mn, -126.f)));
+        l *= fac;
+        if (up) m = mn;
+        if (!o_live) return true;
+        if (!__all_sync(FULL, mbar_wait(bar(kPvDone0 + w), (cs - 1) & 1, abort_flag))) return false;
+        tc_after();
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          tmem_ld16(to + 16 * c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
+          tmem_st16(to + 16 * c, o);
+        }
+        tmem_st_wait();
+        return true;
+      };
+      const int cs0 = cs;
+      int t = first, hf = 0;
+      while (t < n) {
+        // One step: 64 keys (half of a history tile, or the tree tile); P goes over
+        // scores that have been read.  A short loop: unrolled, or with the tree's
+        // case inside, the roles' code outran the instruction caches and half of
+        // the warps' time went to fetching it.
+        const bool s_ok = mbar_wait(bar(kSFull0 + 2 * w + (cs & 1)), (cs >> 1) & 1, abort_flag) && !*abort_flag;
         if (!__all_sync(FULL, s_ok)) {
           ok = false;
           break;
         }
         tc_after();
         const TileMeta& mt = metas[(ct0 + t) & 3];
+        const bool tree = p.t + t == p.Tr - 1, last = tree || hf == 1;
+        const uint32_t ts = tl + col_s(w, cs & 1);
         base = mt.base;
-        const bool tree = p.t + t == p.Tr - 1;
-        float lt = 0.f;
-        // The reference m is moved, to a whole number, when a score would put P
-        // above 2^(kPBaseLog2 + kLazyLog2).  O, l and what the tile has stored of
-        // P so far (`done` chunks) are multiplied by that power of two, exactly.
-        // (P V of the tile before is complete: S of this one was issued after it.)
-        auto move = [&](float mx, int done) {
-          const bool up = mx > m + (kLazyLog2 + kPBaseLog2);
-          const float mn = ceilf(mx) - kPBaseLog2;
-          const float fac = !up ? 1.f : m == -INFINITY ? 0.f : ratio_scale(int(fmaxf(m - mn, -126.f)));
-          l *= fac;
-          lt *= fac;
-          if (up) m = mn;
-          tmem_st_wait();
-#pragma unroll 1
-          for (int c = 0; c < done; ++c) {
-            uint32_t o[16];
-            tmem_ld16(ts + 16 * c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 q = __half22float2(*reinterpret_cast<__half2*>(&o[i]));
-              o[i] = pack_f16(q.x * fac, q.y * fac);
-            }
-            tmem_st16(ts + 16 * c, o);
-          }
-          if (t > first) {
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(to + 16 * c, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
-              tmem_st16(to + 16 * c, o);
-            }
-          }
-          tmem_st_wait();
-        };
-        if (t + stride >= n && f + n < E) ask_q(pn);  // every product that reads this piece's Q is complete
+        if (last && t + stride >= n && f + n < E) ask_q(pn);  // every product that reads this piece's Q is complete
         if (!tree) {
-          // Half a tile at a time (its P goes over scores that have been read), in
-          // a short loop: unrolled, or with the tree's case inside, the roles' code
-          // outran the instruction caches and half of the warps' time went to
-          // fetching it; with quarters the latencies of a step were not covered.
+          // The exponentials are taken against the reference as it is, next to the
+          // maximum; in the rare case that it passes what P may hold, the reference
+          // moves and the step is taken again.
 #pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            uint32_t u[64];
-            tmem_ld32(ts + 32 * c, u);
-            tmem_ld32(ts + 32 * c + 32, u + 32);
+          for (int again = 0;; again = 1) {
+            uint32_t u[kStep];
+            tmem_ld32(ts, u);
+            tmem_ld32(ts + 32, u + 32);
+            const float mr = m == -INFINITY ? 0.f : m;
             float4 e[4];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) e[g] = mt.group[2 * c + g];
+            for (int g = 0; g < 4; ++g) e[g] = mt.group[4 * hf + g];
             tmem_ld_wait();
-            if (e[0].w + e[1].w + e[2].w + e[3].w < float(4 * kGroup)) {
+            if (e[0].w + e[1].w + e[2].w + e[3].w < float(kStep)) {
 #pragma unroll
               for (int g = 0; g < 4; ++g)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                   if (float(i) >= e[g].w) u[16 * g + i] = 0xff800000u;
             }
-            float mx = -INFINITY;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              float q[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                q[i] = fmaxf(fmaxf(__uint_as_float(u[16 * g + 4 * i]), __uint_as_float(u[16 * g + 4 * i + 1])),
-                             fmaxf(__uint_as_float(u[16 * g + 4 * i + 2]), __uint_as_float(u[16 * g + 4 * i + 3])));
-              e[g].x *= xf;
-              mx = fmaxf(mx, fmaf(fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3])), e[g].x, e[g].y));
-            }
-            if (__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2))) move(mx, c);
-            const float mr = m == -INFINITY ? 0.f : m;
+            float mx = -INFINITY, ls = 0.f;
             uint32_t pk[32];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              const float off = e[g].y - mr;
-              const float2 k2 = make_float2(e[g].x, e[g].x), o2 = make_float2(off, off);
+              const float xk = xf * e[g].x, off = e[g].y - mr;
+              const float2 k2 = make_float2(xk, xk), o2 = make_float2(off, off);
               float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+              float q4[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                q4[i] = fmaxf(fmaxf(__uint_as_float(u[16 * g + 4 * i]), __uint_as_float(u[16 * g + 4 * i + 1])),
+                              fmaxf(__uint_as_float(u[16 * g + 4 * i + 2]), __uint_as_float(u[16 * g + 4 * i + 3])));
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const float2 y = fma2(make_float2(__uint_as_float(u[16 * g + 2 * i]), __uint_as_float(u[16 * g + 2 * i + 1])), k2, o2);
@@ -922,44 +935,59 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
                 else s0 = add2(s0, q);
                 pk[8 * g + i] = pack_f16(q.x, q.y);
               }
+              mx = fmaxf(mx, fmaf(fmaxf(fmaxf(q4[0], q4[1]), fmaxf(q4[2], q4[3])), xk, e[g].y));
               s0 = add2(s0, s1);
-              lt = fmaf(s0.x + s0.y, e[g].z, lt);
+              ls = fmaf(s0.x + s0.y, e[g].z, ls);
             }
-            tmem_st32(ts + 16 * c, pk);
+            if (again || !__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2))) {
+              l += ls;
+              tmem_st32(ts, pk);
+              break;
+            }
+            if (!move(mx, cs > cs0)) {
+              ok = false;
+              break;
+            }
           }
         } else {
           nonfinite = mt.nonfinite[0] | mt.nonfinite[1] | mt.nonfinite[2] | mt.nonfinite[3];
+          auto score = [&](uint32_t v, int k) {  // x + e of node k
+            const int e = mt.node[k];
+            return k < a.n && ((mask >> k) & 1ull) ? fmaf(__uint_as_float(v), xf * exp_scale(e & 255), float((e >> 8) - base)) : -INFINITY;
+          };
+          float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < kTreeKeys / 32; ++c) {
-            uint32_t u[32], pk[16];
-            tmem_ld32(ts + 32 * c, u);
+          for (int c = 0; c < kTreeKeys / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld16(ts + 16 * c, v);
             tmem_ld_wait();
-            float mx = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {  // (scores become x + e)
-              const int k = 32 * c + i, e = mt.node[k];
-              const float x = k < a.n && ((mask >> k) & 1ull)
-                                  ? fmaf(__uint_as_float(u[i]), xf * exp_scale(e & 255), float((e >> 8) - base))
-                                  : -INFINITY;
-              u[i] = __float_as_uint(x);
-              mx = fmaxf(mx, x);
-            }
-            if (__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2))) move(mx, c);
-            const float mr = m == -INFINITY ? 0.f : m;
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, score(v[i], 16 * c + i));
+          }
+          if (__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2))) ok = move(mx, cs > cs0);
+          const float mr = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+          for (int c = 0; ok && c < kTreeKeys / 16; ++c) {
+            uint32_t v[16], pk[8];
+            tmem_ld16(ts + 16 * c, v);
+            tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int k = 32 * c + 2 * i;
-              const float q0 = fast_exp2(__uint_as_float(u[2 * i]) - mr), q1 = fast_exp2(__uint_as_float(u[2 * i + 1]) - mr);
-              lt = fmaf(q0, ratio_scale(base - (mt.node[k] >> 8)), fmaf(q1, ratio_scale(base - (mt.node[k + 1] >> 8)), lt));
+            for (int i = 0; i < 8; ++i) {
+              const int k = 16 * c + 2 * i;
+              const float q0 = fast_exp2(score(v[2 * i], k) - mr), q1 = fast_exp2(score(v[2 * i + 1], k + 1) - mr);
+              l = fmaf(q0, ratio_scale(base - (mt.node[k] >> 8)), fmaf(q1, ratio_scale(base - (mt.node[k + 1] >> 8)), l));
               pk[i] = pack_f16(q0, q1);
             }
-            tmem_st16(ts + 16 * c, pk);
+            tmem_st8(ts + 8 * c, pk);
           }
         }
-        l += lt;
+        if (!ok) break;
         tmem_st_wait();
         tc_before();
-        mbar_arrive(bar(kPReady0 + w));
+        mbar_arrive(bar(kPReady0 + 2 * w + (cs & 1)));
+        ++cs;
+        hf = last ? 0 : 1;
+        t += last ? stride : 0;
       }
       if (!ok) break;
       // ---- the piece's result ----
