@@ -50,6 +50,7 @@ constexpr int kRows = 128;
 constexpr int kKeys = 128;       // history keys of a tile
 constexpr int kTreeKeys = 64;    // nodes of the tree tile
 constexpr int kStep = 64;        // keys of a step of S, softmax and P V
+constexpr float kPMost = 60000.f; // a sum of P below this holds no value that f16 does not
 constexpr int kGroup = 16;       // keys with one page at least
 constexpr int kGroups = kKeys / kGroup;
 constexpr int kTcThreads = 16 * 32;
@@ -895,11 +896,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         base = mt.base;
         if (last && t + stride >= n && f + n < E) ask_q(pn);  // every product that reads this piece's Q is complete
         if (!tree) {
-          // The exponentials are taken against the reference as it is, next to the
-          // maximum; in the rare case that it passes what P may hold, the reference
-          // moves and the step is taken again.
+          // The exponentials are taken against the reference as it is.  Their sum
+          // tells whether P holds them (none is larger than the sum, and f16 goes
+          // to 65504); in the rare case that it may not, the maximum is looked
+          // for, the reference moves and the step is taken again.
 #pragma unroll 1
-          for (int again = 0;; again = 1) {
+          for (bool again = false;; again = true) {
             uint32_t u[kStep];
             tmem_ld32(ts, u);
             tmem_ld32(ts + 32, u + 32);
@@ -915,18 +917,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
                 for (int i = 0; i < 16; ++i)
                   if (float(i) >= e[g].w) u[16 * g + i] = 0xff800000u;
             }
-            float mx = -INFINITY, ls = 0.f;
+            float all = 0.f, ls = 0.f;
             uint32_t pk[32];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               const float xk = xf * e[g].x, off = e[g].y - mr;
               const float2 k2 = make_float2(xk, xk), o2 = make_float2(off, off);
               float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-              float q4[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                q4[i] = fmaxf(fmaxf(__uint_as_float(u[16 * g + 4 * i]), __uint_as_float(u[16 * g + 4 * i + 1])),
-                              fmaxf(__uint_as_float(u[16 * g + 4 * i + 2]), __uint_as_float(u[16 * g + 4 * i + 3])));
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const float2 y = fma2(make_float2(__uint_as_float(u[16 * g + 2 * i]), __uint_as_float(u[16 * g + 2 * i + 1])), k2, o2);
@@ -935,16 +932,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
                 else s0 = add2(s0, q);
                 pk[8 * g + i] = pack_f16(q.x, q.y);
               }
-              mx = fmaxf(mx, fmaf(fmaxf(fmaxf(q4[0], q4[1]), fmaxf(q4[2], q4[3])), xk, e[g].y));
               s0 = add2(s0, s1);
+              all += s0.x + s0.y;
               ls = fmaf(s0.x + s0.y, e[g].z, ls);
             }
-            if (again || !__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2))) {
+            if (again || __all_sync(FULL, all < kPMost && m > -INFINITY)) {
               l += ls;
               tmem_st32(ts, pk);
               break;
             }
-            if (!move(mx, cs > cs0)) {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int g = 0; g < kStep / kGroup; ++g) {
+              uint32_t v[16];
+              tmem_ld16(ts + 16 * g, v);
+              const float4 eg = mt.group[4 * hf + g];
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (float(i) < eg.w) mx = fmaxf(mx, fmaf(__uint_as_float(v[i]), xf * eg.x, eg.y));
+            }
+            if (__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2)) && !move(mx, cs > cs0)) {
               ok = false;
               break;
             }
