@@ -10,23 +10,16 @@
 //   0-3, 4-7  two softmax groups, one query row a thread.  More than 128 rows:
 //             group w has rows 128 w .. and both see every tile; fewer: the
 //             groups take turns at the tiles (two partial results, joined).
-//   13        loader: bulk copies of the raw tiles (16 keys of a page are
-//             contiguous) into shared memory.  Loads through registers kept
-//             about 11 KB in flight a SM, as little L1 is left beside the
-//             operands, and took three times the MMAs' time.
-//   8-11      converters: raw tile to f16 (one instruction for two values),
-//             stored as 128B-swizzled operand tiles, K and V double buffered.
+//   8-11, 12-15  converters of K and of V: bulk copies bring a tile's pages into
+//             shared memory as they are, then e4m3 becomes f16 (one instruction
+//             for two values) in 128B-swizzled operand tiles, double buffered.
 //             Tree nodes are bf16 rows divided by their own power of two, and
 //             stored the same way.
-//   12, 13    issue each group's MMAs: S = Q K^T (M 128, N 128, K D, both
-//             from shared memory) and O += P V (A = P from TMEM).
-// TMEM: O0 O1 | S0 S1; P (f16, two to a column) takes the place of its S.  S of the
-// next tile is issued once P V of this one is complete, while the other
-// group's products run, so each group's softmax overlaps the other's MMAs.
-//   A softmax thread takes its row's scores 32 at a time, each once: maximum,
-// exponentials and P of a chunk while the next one is loaded.  Holding the whole
-// row in between (or P) spilled, and a spill costs an L2 access here, as the
-// operands leave almost no L1.
+//   16-19     issue the MMAs: S = Q K^T (M 128, N 64, K D, both from shared
+//             memory) and O += P V (A = P from TMEM), a warp each for each group.
+// TMEM: O0 O1 | two S buffers a group; P (f16, two to a column) takes the place of
+// its S.  A step is 64 keys: the scores of the next one are computed, and the
+// products of the last one added up, while a step's softmax runs.
 //
 // Bound: 2 x 1024 cycles of MMA for 128 keys and 256 rows (f16 at 4096
 // multiply-adds a cycle).  Per tile shared memory moves 64 KB of converted
@@ -53,11 +46,11 @@ constexpr int kStep = 64;        // keys of a step of S, softmax and P V
 constexpr float kPMost = 60000.f; // a sum of P below this holds no value that f16 does not
 constexpr int kGroup = 16;       // keys with one page at least
 constexpr int kGroups = kKeys / kGroup;
-constexpr int kTcThreads = 16 * 32;
+constexpr int kTcThreads = 20 * 32;
 // Registers a thread, by warp group: the CTA is launched with kRegs each, and
-// the groups trade (sums of four warps: 2 kRegsSoft + kRegsConv + kRegsIssue <= 4 kRegs).
-constexpr int kRegs = 128, kRegsSoft = 168, kRegsConv = 96, kRegsIssue = 80;
-static_assert(2 * kRegsSoft + kRegsConv + kRegsIssue <= 4 * kRegs, "register split");
+// the groups trade (sums of four warps: what they take may not pass what was launched).
+constexpr int kRegs = 96, kRegsSoft = 144, kRegsConv = 72, kRegsIssue = 48;
+static_assert(2 * kRegsSoft + 2 * kRegsConv + kRegsIssue <= 5 * kRegs, "register split");
 constexpr int kConvThreads = 128, kSoftThreads = 256;
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wait
 __host__ __device__ constexpr uint32_t col_o(int w) { return 128u * uint32_t(w); }
@@ -87,10 +80,10 @@ struct TcSmem {
   static constexpr int kRawK = 6 * kTile;
   static constexpr int kRawV = kRawK + kRaw;
   static constexpr int kMeta = kRawV + kRaw;       // four
-  static constexpr int kInfo = kMeta + 4 * int(sizeof(TileMeta));  // [2][8]: scale bytes and keys of a raw tile's groups
-  static constexpr int kBars = kInfo + 64;
-  static constexpr int kAbort = kBars + 8 * 30 + 4;  // (after the barriers: TMEM address, abort flag)
-  static constexpr int kKeep = kAbort + 4 + 4 * 17;  // 16 words of the scan and one before it
+  static constexpr int kInfo = kMeta + 4 * int(sizeof(TileMeta));  // [K, V][2][8]: keys of a raw tile's groups
+  static constexpr int kBars = kInfo + 128;
+  static constexpr int kAbort = kBars + 8 * 34 + 4;  // (after the barriers: TMEM address, abort flag)
+  static constexpr int kKeep = kAbort + 4 + 4 * 21;  // 20 words of the scan and one before it
   static constexpr int kBytes = kBars + 448;
   // the tiles before each request are summed up in what will hold operands
   static_assert(4 * (kAttentionQ8MaxB + 1) <= 2 * kTile, "scan space");
@@ -103,16 +96,17 @@ enum {
   kVFull0 = 4,
   kVEmpty0 = 6,
   kQFull0 = 8,  // + group
-  kPvDone0 = 10,
-  kOFree0 = 12,    // the epilogue has read O
-  kFragFull = 14,  // group 1 stored its half of a unit that this CTA finishes
-  kFragFree = 15,  // group 0 has read it
-  kDrain0 = 16,    // + group
+  kOFree0 = 10,    // the epilogue has read O
+  kFragFull = 12,  // group 1 stored its half of a unit that this CTA finishes
+  kFragFree = 13,  // group 0 has read it
+  kDrain0 = 14,    // + issuing warp
   kRawFull0 = 18,  // + (K, V): the raw tile has landed
   kRawEmpty0 = 20, // the converters have read it
-  kSFull0 = 22,    // + 2 group + S buffer
-  kPReady0 = 26,   // + 2 group + S buffer (the next step's P may be there before this one's is waited for)
-  kNumBars = 30
+  // + 2 group + S buffer: by buffer, so that nothing is ever two phases ahead of who waits for it
+  kSFull0 = 22,
+  kPReady0 = 26,
+  kPvDone0 = 30,
+  kNumBars = 34
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -339,9 +333,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sp + L::kBars + 8 * kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + L::kAbort);
   static_assert(L::kAbort == L::kBars + 8 * kNumBars + 4 && L::kKeep + 32 <= L::kBytes, "layout");
-  int* wsum = reinterpret_cast<int*>(sp + L::kBars + 8 * kNumBars + 8);  // [16]
+  int* wsum = reinterpret_cast<int*>(sp + L::kBars + 8 * kNumBars + 8);  // [20]
   int* keep = reinterpret_cast<int*>(sp + L::kKeep);  // [8]: what the joining at the end needs (kept here, it costs the roles no registers)
-  uint32_t* infos = reinterpret_cast<uint32_t*>(sp + L::kInfo);
   int* pre = reinterpret_cast<int*>(sp);  // [b + 1] tiles of one (kv head, row block) before request r (until the roles start)
 
   if (tid == 0) {
@@ -351,24 +344,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       mbar_init(bar(kVFull0 + i), kConvThreads);
       mbar_init(bar(kVEmpty0 + i), 2);
       mbar_init(bar(kQFull0 + i), kRows);
-      mbar_init(bar(kSFull0 + 2 * i), 1);
-      mbar_init(bar(kSFull0 + 2 * i + 1), 1);
-      mbar_init(bar(kPReady0 + 2 * i), kRows);
-      mbar_init(bar(kPReady0 + 2 * i + 1), kRows);
-      mbar_init(bar(kPvDone0 + i), 1);
       mbar_init(bar(kOFree0 + i), kRows);
-    }
-    mbar_init(bar(kFragFull), kRows);
-    mbar_init(bar(kFragFree), kRows);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kDrain0 + i), 1);
       mbar_init(bar(kRawFull0 + i), 1);
       mbar_init(bar(kRawEmpty0 + i), kConvThreads);
     }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(kSFull0 + i), 1);
+      mbar_init(bar(kPReady0 + i), kRows);
+      mbar_init(bar(kPvDone0 + i), 1);
+      mbar_init(bar(kDrain0 + i), 1);
+    }
+    mbar_init(bar(kFragFull), kRows);
+    mbar_init(bar(kFragFree), kRows);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_holder)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -444,13 +435,101 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     *abort_flag = 1;
   };
 
-  if (warp >= 12) {
+  if (warp >= 16) {
+    // ============================ MMA issuers ============================
+    // Warps 16, 17: S = Q K^T of softmax groups 0, 1; warps 18, 19: O += P V.  A
+    // step is 64 keys; its S goes into one of two buffers, as soon as P V of the
+    // step before last has read it, so that the softmax of a step runs beside the
+    // products of its neighbours.  Four warps, because a product's waits and
+    // issue take one warp about as long as the product itself.  A whole warp runs
+    // the role, so that its addresses and descriptors stay uniform (one lane
+    // alone spent more time forming them than the MMAs take); one elected lane
+    // issues.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 14) {
-    // ============================ loader ============================
-    // One bulk copy a group of 16 keys (16 D contiguous bytes of a page), a
-    // lane each; the tree tile: one a node's row.  Page ids are read two tiles
-    // ahead, scale bytes one.
+    const int w = warp & 1;
+    const bool pv = warp >= 18;
+    const uint32_t ub = __shfl_sync(FULL, sbase, 0), ut = __shfl_sync(FULL, tmem, 0);
+    const uint32_t dq = desc_lo(ub + L::kQ + uint32_t(w) * L::kTile, 16);
+    const uint32_t db = pv ? desc_lo(ub + L::kV, L::kBlock) : desc_lo(ub + L::kK, 16);
+    const int full0 = pv ? kVFull0 : kKFull0, empty0 = pv ? kVEmpty0 : kKEmpty0;
+    bool ok = true;
+    auto wait = [&](int b, int parity) { return mbar_wait(bar(b), uint32_t(parity), abort_flag); };
+    Pos p = start;
+    int ct0 = 0, piece = 0, cs = 0;  // cs: steps issued
+    for (int f = S; ok && f < E; ++piece) {
+      const int n = piece_tiles(p, f);
+      const bool split = unit_rows(p.j) <= kRows;
+      const int tree_at = p.t + n == p.Tr ? n - 1 : n, stride = split ? 2 : 1, first = split ? w : 0;
+      for (int t = first, hf = 0; t < n;) {
+        const int ct = ct0 + t, buf = ct & 1, sb = 2 * w + (cs & 1), ph = (cs >> 1) & 1;
+        const bool last = hf == 1 || t == tree_at, begin = t == first && hf == 0;
+        const uint32_t ts = ut + col_s(w, cs & 1);
+        const uint32_t dt = db + uint32_t(buf) * (L::kTile >> 4) + uint32_t(hf) * (kStep * 128 >> 4);
+        ok = hf == 1 || wait(full0 + buf, (ct >> 1) & 1);
+        if (!pv) {
+          ok = ok && (!begin || wait(kQFull0 + w, piece & 1)) && (cs < 2 || wait(kPvDone0 + sb, ph ^ 1));
+        } else {
+          ok = ok && (!begin || piece == 0 || wait(kOFree0 + w, (piece - 1) & 1)) && wait(kPReady0 + sb, ph);
+        }
+        if (!__all_sync(FULL, ok && !*abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_after();
+        if (elect_one()) {
+          if (!pv) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = uint32_t(((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4);
+              mma_ss(ts, desc(dq + o), desc(dt + o), idesc_f16(kStep, false), kk > 0 ? 1u : 0u);
+            }
+            mma_commit(bar(kSFull0 + sb));
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < kStep / 16; ++kk)
+              mma_ts(ut + col_o(w), ts + kk * 8, desc(dt + uint32_t((kk * 16 * 128) >> 4)), idesc_f16(D, true), !begin || kk > 0 ? 1u : 0u);
+            mma_commit(bar(kPvDone0 + sb));
+          }
+          if (last) {
+            mma_commit(bar(empty0 + buf));
+            if (split) mma_commit(bar(empty0 + buf));  // the other group does not read this tile
+          }
+        }
+        __syncwarp();
+        ++cs;
+        hf = last ? 0 : 1;
+        t += last ? stride : 0;
+      }
+      ct0 += n;
+      f += n;
+      p.t += n - 1;
+      advance(p);
+    }
+    if (!ok && !*abort_flag) fail();
+    // every MMA issued has completed before TMEM is released
+    __syncwarp();
+    if (elect_one()) mma_commit(bar(kDrain0 + (warp & 3)));
+    for (int i = 0; i < 1000 && !mbar_try(bar(kDrain0 + (warp & 3)), 0); ++i) {
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ============================ converters ============================
+    // Warps 8-11 K, 12-15 V: raw tile -> f16 operand tile.  The first warp of each
+    // also asks for the raw tiles: one bulk copy a group of 16 keys (16 D
+    // contiguous bytes of a page), a lane each; of the tree tile, one a node's
+    // row.  Page ids are read two tiles ahead, scale bytes one.  (Loads through
+    // registers kept about 11 KB in flight a SM, as little L1 is left beside the
+    // operands, and took three times the MMAs' time.)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
+    const int kv = warp >= 12 ? 1 : 0, cw = warp & 3, ct_id = tid & 127;
+    const uint32_t rawt = sbase + (kv ? L::kRawV : L::kRawK);
+    uint32_t* infos = reinterpret_cast<uint32_t*>(sp + L::kInfo) + kv * 2 * kGroups;
+    const int full0 = kv ? kVFull0 : kKFull0, empty0 = kv ? kVEmpty0 : kKEmpty0;
+    auto wait = [&](int b, int parity) {
+      return __all_sync(FULL, mbar_wait(bar(b), uint32_t(parity), abort_flag) && !*abort_flag) != 0;
+    };
+
+    // ---- asking for raw tiles ----
     const int SHIFT = a.page_size == 16 ? 0 : a.page_size == 32 ? 1 : 2;  // log2(groups a page)
     auto fetch = [&](const Pos& p) {  // the page id of the lane's group
       const int g0 = p.t * kGroups + lane;
@@ -470,15 +549,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         }
       }
     };
-    uint32_t ks = 0, vs = 0;
-    auto load_scales = [&](int unit) {
-      ks = unit >= 0 ? ld_nc8(a.k_scales + unit) : 0u;
-      vs = unit >= 0 ? ld_nc8(a.v_scales + unit) : 0u;
-    };
-    auto copy = [&](const Pos& p, int unit, int cnt, int which) {
-      const uint32_t dst = sbase + (which ? L::kRawV : L::kRawK), full = bar(kRawFull0 + which);
-      const uint8_t* pages = which ? a.v_pages : a.k_pages;
-      const void* fresh = which ? a.v_new : a.k_new;
+    auto copy = [&](const Pos& p, int unit, int cnt, int slot) {
+      const uint32_t full = bar(kRawFull0 + kv);
+      const uint8_t* pages = kv ? a.v_pages : a.k_pages;
+      if (lane < kGroups) infos[slot * kGroups + lane] = uint32_t(cnt);
       if (p.t < p.Tr - 1) {
         const uint32_t bytes = uint32_t(cnt) * D;
         const uint32_t all = __reduce_add_sync(FULL, bytes);
@@ -486,194 +560,49 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         __syncwarp();
         if (bytes) {
           const int off = ((p.t * kGroups + lane) & ((1 << SHIFT) - 1)) * kGroup;
-          bulk_copy(dst + uint32_t(lane * kGroup * D), pages + (size_t(unit) * a.page_size + off) * D, bytes, full);
+          bulk_copy(rawt + uint32_t(lane * kGroup * D), pages + (size_t(unit) * a.page_size + off) * D, bytes, full);
         }
       } else {
         if (lane == 0) mbar_expect(full, uint32_t(a.n) * D * 2u);
         __syncwarp();
         for (int i = lane; i < a.n; i += 32)
-          bulk_copy(dst + uint32_t(i * D * 2),
-                    static_cast<const uint16_t*>(fresh) + (size_t(p.r) * a.n + i) * a.new_ld + size_t(p.j / args.blocks) * D,
+          bulk_copy(rawt + uint32_t(i * D * 2),
+                    static_cast<const uint16_t*>(kv ? a.v_new : a.k_new) + (size_t(p.r) * a.n + i) * a.new_ld + size_t(p.j / args.blocks) * D,
                     uint32_t(D) * 2u, full);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
     };
-    Pos p = start, p1 = start, p2 = start;  // the tile at hand, the next, the one after
-    int unit0 = -1, cnt0 = 0, unit1 = -1, cnt1 = 0, pid1 = 0, pid2 = 0;
-    uint32_t ks1 = 0, vs1 = 0;
-    if (S < E) {
-      resolve(p, fetch(p), unit0, cnt0);
-      load_scales(unit0);
+    // (warp cw 0) the tile asked for next, the lane's page id of it, and its scale
+    // bytes of the tile asked for last: each is loaded a tile before it is used
+    Pos p = start, p1 = start;
+    int pid1 = 0;
+    uint32_t ks = 0, vs = 0;
+    auto ask = [&](int slot) {
+      int unit, cnt;
+      resolve(p1, pid1, unit, cnt);
+      copy(p1, unit, cnt, slot);
+      if (kv == 0) {
+        ks = unit >= 0 ? ld_nc8(a.k_scales + unit) : 0u;
+        vs = unit >= 0 ? ld_nc8(a.v_scales + unit) : 0u;
+      }
+    };
+    if (cw == 0 && S < E) {
+      pid1 = fetch(p1);
+      ask(0);
       if (S + 1 < E) {
         advance(p1);
         pid1 = fetch(p1);
-        p2 = p1;
-        if (S + 2 < E) {
-          advance(p2);
-          pid2 = fetch(p2);
-        }
       }
     }
-    int ct = 0;
-    for (int f = S; f < E; ++f, ++ct) {
-      const bool k_ok = (ct < 1 || mbar_wait(bar(kRawEmpty0), (ct - 1) & 1, abort_flag)) && !*abort_flag;
-      if (!__all_sync(FULL, k_ok)) break;
-      if (lane < kGroups) infos[(ct & 1) * kGroups + lane] = ks | (vs << 8) | (uint32_t(cnt0) << 16);
-      copy(p, unit0, cnt0, 0);
-      if (f + 1 < E) {
-        resolve(p1, pid1, unit1, cnt1);
-        ks1 = unit1 >= 0 ? ld_nc8(a.k_scales + unit1) : 0u;
-        vs1 = unit1 >= 0 ? ld_nc8(a.v_scales + unit1) : 0u;
-      }
-      const bool v_ok = (ct < 1 || mbar_wait(bar(kRawEmpty0 + 1), (ct - 1) & 1, abort_flag)) && !*abort_flag;
-      if (!__all_sync(FULL, v_ok)) break;
-      copy(p, unit0, cnt0, 1);
-      p = p1;
-      unit0 = unit1;
-      cnt0 = cnt1;
-      ks = ks1;
-      vs = vs1;
-      p1 = p2;
-      pid1 = pid2;
-      if (f + 3 < E) {
-        advance(p2);
-        pid2 = fetch(p2);
-      }
-    }
-    // every copy has landed before the CTA can end (tile ct - 1's, or both of an interrupted one's)
-    if (ct > 0) {
-      for (int i = 0; i < 2; ++i)
-        for (int k = 0; k < 1000 && !mbar_try(bar(kRawFull0 + i), (ct - 1) & 1); ++k) {
-        }
-    }
-    if (*abort_flag && S < E) {
-      for (int k = 0; k < 50 && !mbar_try(bar(kRawFull0), ct & 1); ++k) {
-      }
-    }
-    } else if (warp < 14) {
-    // ============================ MMA issuers ============================
-    // One warp a softmax group, so that one's waits do not hold up the other's
-    // products.  The whole warp runs the role, so that its addresses and
-    // descriptors stay uniform (one lane alone spent more time forming them
-    // than the MMAs take); one elected lane issues.
-      const int w = warp - 12;
-      const uint32_t ub = __shfl_sync(FULL, sbase, 0), ut = __shfl_sync(FULL, tmem, 0);
-      const uint32_t dq = desc_lo(ub + L::kQ + uint32_t(w) * L::kTile, 16), dk0 = desc_lo(ub + L::kK, 16),
-                     dv0 = desc_lo(ub + L::kV, L::kBlock);
-      const uint32_t dp = ut + col_o(w);
-      bool ok = true;
-      auto wait = [&](int b, int parity) { return mbar_wait(bar(b), uint32_t(parity), abort_flag); };
-      Pos p = start;
-      // Steps of 64 keys, counted over the whole range: ns products S issued, np
-      // products P V, seen of these known to be complete (each phase is waited for
-      // in turn, and P V of step k only issued once that of step k - 1 is seen).
-      int ct0 = 0, piece = 0, ns = 0, np = 0, seen = 0;
-      for (int f = S; ok && f < E; ++piece) {
-        const int n = piece_tiles(p, f);
-        const bool split = unit_rows(p.j) <= kRows;
-        const int tree_at = p.t + n == p.Tr ? n - 1 : n, stride = split ? 2 : 1, first = split ? w : 0;
-        int ts = first, hs = 0, tp = first, hp = 0;  // the tile and half that S and P V are at
-        // The next step's S goes into the other buffer as soon as P V of the step
-        // before has read it, so that the softmax of a step runs beside the
-        // products of its neighbours.
-        for (bool begin = true; ok && tp < n; begin = false) {
-#pragma unroll 1
-          while (ok && ts < n && ns < np + 2) {
-            const int ct = ct0 + ts, buf = ct & 1;
-            const bool tree = ts == tree_at, last = tree || hs == 1;
-            ok = (ts > first || hs == 1 || wait(kQFull0 + w, piece & 1)) && (hs == 1 || wait(kKFull0 + buf, (ct >> 1) & 1));
-            if (ok && seen < ns - 1) {
-              ok = wait(kPvDone0 + w, seen & 1);
-              ++seen;
-            }
-            ok = __all_sync(FULL, ok && !*abort_flag) != 0;
-            if (!ok) break;
-            tc_after();
-            const uint32_t dk = dk0 + uint32_t(buf) * (L::kTile >> 4) + uint32_t(hs) * (kStep * 128 >> 4);
-            if (elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t o = uint32_t(((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4);
-                mma_ss(ut + col_s(w, ns & 1), desc(dq + o), desc(dk + o), idesc_f16(kStep, false), kk > 0 ? 1u : 0u);
-              }
-              mma_commit(bar(kSFull0 + 2 * w + (ns & 1)));
-              if (last) {
-                mma_commit(bar(kKEmpty0 + buf));
-                if (split) mma_commit(bar(kKEmpty0 + buf));  // the other group does not read this tile
-              }
-            }
-            __syncwarp();
-            ++ns;
-            hs = last ? 0 : 1;
-            ts += last ? stride : 0;
-          }
-          if (!ok) break;
-          const int ct = ct0 + tp, buf = ct & 1;
-          const bool tree = tp == tree_at, last = tree || hp == 1;
-          ok = (hp == 1 || wait(kVFull0 + buf, (ct >> 1) & 1)) && (!begin || piece == 0 || wait(kOFree0 + w, (piece - 1) & 1));
-          if (ok && seen < np) {
-            ok = wait(kPvDone0 + w, seen & 1);
-            ++seen;
-          }
-          ok = ok && wait(kPReady0 + 2 * w + (np & 1), (np >> 1) & 1);
-          ok = __all_sync(FULL, ok && !*abort_flag) != 0;
-          if (!ok) break;
-          tc_after();
-          const uint32_t dv = dv0 + uint32_t(buf) * (L::kTile >> 4) + uint32_t(hp) * (kStep * 128 >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < kStep / 16; ++kk)
-              mma_ts(dp, ut + col_s(w, np & 1) + kk * 8, desc(dv + uint32_t((kk * 16 * 128) >> 4)), idesc_f16(D, true), !begin || kk > 0 ? 1u : 0u);
-            mma_commit(bar(kPvDone0 + w));
-            if (last) {
-              mma_commit(bar(kVEmpty0 + buf));
-              if (split) mma_commit(bar(kVEmpty0 + buf));
-            }
-          }
-          __syncwarp();
-          ++np;
-          hp = last ? 0 : 1;
-          tp += last ? stride : 0;
-        }
-        ct0 += n;
-        f += n;
-        p.t += n - 1;
-        advance(p);
-      }
-      if (!ok && !*abort_flag) fail();
-      // every MMA issued has completed before TMEM is released
-      __syncwarp();
-      if (elect_one()) mma_commit(bar(kDrain0 + w));
-      for (int i = 0; i < 1000 && !mbar_try(bar(kDrain0 + w), 0); ++i) {
-      }
-      __syncwarp();
-    }
-  } else if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-    // ============================ converters ============================
-    const int cw = warp - 8, ct_id = tid - 256;
+
     constexpr int kLoads = D / 16;               // 16-byte words a thread of a raw tile
     constexpr int kLanesKey = D / 16;            // lanes a history key
     constexpr int kLanesRow = D / 8;             // lanes a tree row
     constexpr int kRowsLoad = kConvThreads / kLanesRow, kTreeLoads = kTreeKeys / kRowsLoad;
-    // group and key (in the tile) of a thread's word i of a history tile
+    // key (in the tile) of a thread's word i of a history tile, of the tree tile
     auto hist_key = [&](int i) { return D == 128 ? 16 * i + 4 * cw + lane / kLanesKey : 32 * i + 8 * cw + lane / kLanesKey; };
     auto tree_key = [&](int i) { return i * kRowsLoad + ct_id / kLanesRow; };
-    // the thread's words of a history tile, zeros where there is no key
-    auto read = [&](uint4 (&x)[kLoads], uint32_t rawt, const uint32_t* info) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int key = hist_key(i);
-        x[i] = lds16(rawt + uint32_t(key * D + (lane % kLanesKey) * 16));
-        if (uint32_t(key & 15) >= info[key >> 4] >> 16) x[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    // its word of a tree row
-    auto tree_row = [&](uint32_t rawt, int key) {
-      const uint4 x = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
-      return key < a.n ? x : make_uint4(0u, 0u, 0u, 0u);
-    };
     // 16 e4m3 values -> two 16-byte chunks of their key's swizzled row
     auto store_hist = [&](uint32_t tile, const uint4 (&x)[kLoads]) {
 #pragma unroll
@@ -711,73 +640,83 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       sts16(tile + uint32_t(ch >> 3) * L::kBlock + uint32_t(key) * 128u + ((uint32_t(ch & 7) ^ uint32_t(key & 7)) << 4),
             make_uint4(cv(x.x), cv(x.y), cv(x.z), cv(x.w)));
     };
-    Pos p = start;
-    int base = 113;
+    int base = 113, ct = 0;
     bool ok = true;
-    auto wait = [&](int b, int parity) {
-      return __all_sync(FULL, mbar_wait(bar(b), uint32_t(parity), abort_flag) && !*abort_flag) != 0;
-    };
-    for (int f = S, ct = 0; ok && f < E; ++f, ++ct) {
+    for (int f = S; f < E; ++f, ++ct) {
       const int buf = ct & 1;
-      const bool tree = p.t == p.Tr - 1, first = f == S || p.t == 0;
+      const bool tree = p.t == p.Tr - 1, first = f == S || p.t == 0, more = f + 1 < E;
       const uint32_t* info = infos + buf * kGroups;
+      const uint32_t tile = sbase + (kv ? L::kV : L::kK) + uint32_t(buf) * L::kTile;
       TileMeta& mt = metas[ct & 3];
-#pragma unroll 1
-      for (int kv = 0; ok && kv < 2; ++kv) {  // K, V
-        const uint32_t tile = sbase + (kv ? L::kV : L::kK) + uint32_t(buf) * L::kTile, rawt = sbase + (kv ? L::kRawV : L::kRawK);
-        const int empty = (kv ? kVEmpty0 : kKEmpty0) + buf;
-        ok = wait(kRawFull0 + kv, ct & 1);
-        if (!ok) break;
-        if (kv == 0) {
-          if (first) {
-            const int v0 = int(info[0] >> 8) & 255;
-            base = tree || v0 == 0 ? 113 : v0;
-          }
-        }
-        if (!tree) {
-          uint4 x[kLoads];
-          read(x, rawt, info);
-          mbar_arrive(bar(kRawEmpty0 + kv));
-          ok = ct < 2 || wait(empty, ((ct >> 1) - 1) & 1);
-          if (!ok) break;
-          if (kv == 0 && cw == 0 && lane < kGroups) {
-            const int ks = int(info[lane] & 255u), vs = int(info[lane] >> 8) & 255, cnt = int(info[lane] >> 16);
-            mt.group[lane] = cnt > 0 ? make_float4(exp_scale(ks), float(vs - base), ratio_scale(base - vs), float(cnt))
-                                     : make_float4(1.f, 0.f, 0.f, 0.f);
-          }
-          store_hist(tile, x);
-        } else {
-          ok = (ct < 2 || wait(empty, ((ct >> 1) - 1) & 1)) && (kv == 1 || wait(kRawFull0 + 1, ct & 1));
-          if (!ok) break;
-          // (the V rows' exponents are wanted with the scores, before V itself)
-          unsigned long long nf = 0;
-#pragma unroll 1
-          for (int i = 0; i < kTreeLoads; ++i) {
-            const int key = tree_key(i);
-            const uint4 x = tree_row(rawt, key);
-            const int e = row_exp(x);
-            if (kv == 0) {
-              const uint4 v = tree_row(sbase + L::kRawV, key);
-              const int ev = row_exp(v);
-              if (ct_id % kLanesRow == 0) mt.node[key] = uint16_t(e | (ev << 8));
-              const unsigned who = __ballot_sync(FULL, nonfinite_bf16(v.x) || nonfinite_bf16(v.y) || nonfinite_bf16(v.z) || nonfinite_bf16(v.w));
-#pragma unroll 1
-              for (int q = 0; q < 32 / kLanesRow; ++q)
-                if ((who >> (q * kLanesRow)) & ((1u << kLanesRow) - 1u))
-                  nf |= 1ull << (i * kRowsLoad + cw * (32 / kLanesRow) + q);
-            }
-            store_tree(tile, x, key, e, kv == 1);
-          }
-          if (kv == 0 && lane == 0) mt.nonfinite[cw] = nf;
-          mbar_arrive(bar(kRawEmpty0 + kv));
-        }
-        if (kv == 0 && ct_id == 0) mt.base = base;
-        fence_async();
-        mbar_arrive(bar((kv ? kVFull0 : kKFull0) + buf));
+      ok = wait(kRawFull0 + kv, ct & 1);
+      if (!ok) break;
+      const int ks0 = int(ks), vs0 = int(vs);  // this tile's (the next one's are asked for below)
+      if (first && cw == 0) {
+        const int v0 = __shfl_sync(FULL, vs0, 0);
+        base = tree || v0 == 0 ? 113 : v0;
       }
+      // the next raw tile is asked for once every converter has read this one
+      auto ask_next = [&]() {
+        if (cw != 0 || !more) return true;
+        if (!wait(kRawEmpty0 + kv, ct & 1)) return false;
+        ask(buf ^ 1);
+        if (f + 2 < E) {
+          advance(p1);
+          pid1 = fetch(p1);
+        }
+        return true;
+      };
+      if (!tree) {
+        uint4 x[kLoads];  // the thread's words, zeros where there is no key
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int key = hist_key(i);
+          x[i] = lds16(rawt + uint32_t(key * D + (lane % kLanesKey) * 16));
+          if (uint32_t(key & 15) >= info[key >> 4]) x[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        const int cnt = lane < kGroups ? int(info[lane]) : 0;
+        mbar_arrive(bar(kRawEmpty0 + kv));
+        ok = ask_next() && (ct < 2 || wait(empty0 + buf, ((ct >> 1) - 1) & 1));
+        if (!ok) break;
+        if (kv == 0 && cw == 0 && lane < kGroups) {
+          mt.group[lane] = cnt > 0 ? make_float4(exp_scale(ks0), float(vs0 - base), ratio_scale(base - vs0), float(cnt))
+                                   : make_float4(1.f, 0.f, 0.f, 0.f);
+        }
+        store_hist(tile, x);
+      } else {
+        ok = ct < 2 || wait(empty0 + buf, ((ct >> 1) - 1) & 1);
+        if (!ok) break;
+        unsigned long long nf = 0;
+#pragma unroll 1
+        for (int i = 0; i < kTreeLoads; ++i) {
+          const int key = tree_key(i);
+          uint4 x = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
+          if (key >= a.n) x = make_uint4(0u, 0u, 0u, 0u);
+          const int e = row_exp(x);
+          if (ct_id % kLanesRow == 0) reinterpret_cast<uint8_t*>(&mt.node[key])[kv] = uint8_t(e);
+          if (kv == 1) {
+            const unsigned who = __ballot_sync(FULL, nonfinite_bf16(x.x) || nonfinite_bf16(x.y) || nonfinite_bf16(x.z) || nonfinite_bf16(x.w));
+#pragma unroll 1
+            for (int q = 0; q < 32 / kLanesRow; ++q)
+              if ((who >> (q * kLanesRow)) & ((1u << kLanesRow) - 1u))
+                nf |= 1ull << (i * kRowsLoad + cw * (32 / kLanesRow) + q);
+          }
+          store_tree(tile, x, key, e, kv == 1);
+        }
+        if (kv == 1 && lane == 0) mt.nonfinite[cw] = nf;
+        mbar_arrive(bar(kRawEmpty0 + kv));
+        ok = ask_next();
+        if (!ok) break;
+      }
+      if (kv == 0 && ct_id == 0) mt.base = base;
+      fence_async();
+      mbar_arrive(bar(full0 + buf));
       advance(p);
     }
     if (!ok && !*abort_flag) fail();
+    // every copy has landed before the CTA can end (each tile was waited for, but for one when giving up)
+    if (cw == 0 && *abort_flag)
+      for (int k = 0; k < 100; ++k) mbar_try(bar(kRawFull0 + kv), (ct + (k & 1)) & 1);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     // ============================ softmax groups ============================
@@ -835,20 +774,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         __syncwarp();
         const uint32_t qrow = qtile + uint32_t(r) * 128u;
         auto chunk = [&](int i) { return qrow + uint32_t(i >> 3) * L::kBlock + ((uint32_t(i & 7) ^ uint32_t(r & 7)) << 4); };
-        uint4 x[D / 8];
         uint32_t mx = 0;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = lds16(chunk(i));
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, x[i].x), x[i].y), x[i].z), x[i].w);
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = lds16(chunk(i));
+          mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, x.x), x.y), x.z), x.w);
+        }
         const int e = norm_exp(max(mx & 0xffffu, mx >> 16));
         // the sign of the scale goes into Q, so that a larger score is a larger exponent
         const float inv = copysignf(exp_scale(2 * kExpBias - e), a.scale);
         xf = fabsf(a.scale) * 1.4426950408889634f * exp_scale(e);
         auto cv = [&](uint32_t u) { return pack_f16(bf16_lo(u) * inv, bf16_hi(u) * inv); };
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) sts16(chunk(i), make_uint4(cv(x[i].x), cv(x[i].y), cv(x[i].z), cv(x[i].w)));
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = lds16(chunk(i));
+          sts16(chunk(i), make_uint4(cv(x.x), cv(x.y), cv(x.z), cv(x.w)));
+        }
         fence_async();
       }
       mbar_arrive(bar(kQFull0 + w));
@@ -857,13 +798,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       // 2^(kPBaseLog2 + kLazyLog2); O and l are multiplied by that power of two,
       // exactly, once the products so far are complete.
       auto move = [&](float mx, bool o_live) {
-        const bool up = mx > m + (kLazyLog2 + kPBaseLog2);
+        const bool up = mx > m + kPBaseLog2;
         const float mn = ceilf(mx) - kPBaseLog2;
         const float fac = !up ? 1.f : m == -INFINITY ? 0.f : ratio_scale(int(fmaxf(m - mn, -126.f)));
         l *= fac;
         if (up) m = mn;
         if (!o_live) return true;
-        if (!__all_sync(FULL, mbar_wait(bar(kPvDone0 + w), (cs - 1) & 1, abort_flag))) return false;
+        if (!__all_sync(FULL, mbar_wait(bar(kPvDone0 + 2 * w + ((cs - 1) & 1)), ((cs - 1) >> 1) & 1, abort_flag))) return false;
         tc_after();
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
@@ -952,12 +893,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
               for (int i = 0; i < 16; ++i)
                 if (float(i) < eg.w) mx = fmaxf(mx, fmaf(__uint_as_float(v[i]), xf * eg.x, eg.y));
             }
-            if (__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2)) && !move(mx, cs > cs0)) {
+            if (__any_sync(FULL, mx > m + kPBaseLog2) && !move(mx, cs > cs0)) {
               ok = false;
               break;
             }
           }
         } else {
+          // (the V rows' exponents come with V)
+          if (!__all_sync(FULL, mbar_wait(bar(kVFull0 + ((ct0 + t) & 1)), ((ct0 + t) >> 1) & 1, abort_flag))) {
+            ok = false;
+            break;
+          }
           nonfinite = mt.nonfinite[0] | mt.nonfinite[1] | mt.nonfinite[2] | mt.nonfinite[3];
           auto score = [&](uint32_t v, int k) {  // x + e of node k
             const int e = mt.node[k];
@@ -1000,7 +946,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       if (!ok) break;
       // ---- the piece's result ----
       if (mine) {
-        const bool d_ok = mbar_wait(bar(kPvDone0 + w), (cs - 1) & 1, abort_flag) && !*abort_flag;
+        const bool d_ok = mbar_wait(bar(kPvDone0 + 2 * w + ((cs - 1) & 1)), ((cs - 1) >> 1) & 1, abort_flag) && !*abort_flag;
         if (!__all_sync(FULL, d_ok)) {
           ok = false;
           break;
@@ -1042,24 +988,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       const float Ls = has_o ? l * wa + ol * wb : l;
       const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float v[32];
+      for (int c = 0; c < D / 16; ++c) {
+        float v[16];
         if (mine) {
-          uint32_t o[32];
-          tmem_ld32(to + 32 * c, o);
+          uint32_t o[16];
+          tmem_ld16(to + 16 * c, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * vs;
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * vs;
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          for (int i = 0; i < 16; ++i) v[i] = 0.f;
         }
         if (any_nf && nf) {
           for (int q = 0; q < a.n; ++q)
             if ((nf >> q) & 1ull) {
-              const uint16_t* vr = static_cast<const uint16_t*>(a.v_new) + (size_t(p.r) * a.n + q) * a.new_ld + size_t(h) * D + 32 * c;
+              const uint16_t* vr = static_cast<const uint16_t*>(a.v_new) + (size_t(p.r) * a.n + q) * a.new_ld + size_t(h) * D + 16 * c;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
+              for (int i = 0; i < 16; ++i) {
                 const float y = __uint_as_float(uint32_t(vr[i]) << 16);
                 if (!(fabsf(y) < INFINITY)) v[i] += y;
               }
@@ -1067,9 +1013,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         }
         if (direct || (local && w == 0)) {
           if (has_o) {
-            const float4* oo = so + size_t(kRows) * (D / 4) + size_t(8 * c) * kRows;
+            const float4* oo = so + size_t(kRows) * (D / 4) + size_t(4 * c) * kRows;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
               const float4 y = __ldcg(oo + i * kRows);
               v[4 * i] = v[4 * i] * wa + y.x * wb;
               v[4 * i + 1] = v[4 * i + 1] * wa + y.y * wb;
@@ -1078,15 +1024,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
             }
           }
           if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D) + 4 * c;
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D) + 2 * c;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
               dst[i] = make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
                                   pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
           }
         } else if (valid) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) so[(8 * c + i) * kRows] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          for (int i = 0; i < 4; ++i) so[(4 * c + i) * kRows] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
       }
       if (direct || (local && w == 0)) {
@@ -1181,7 +1127,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
             float4 acc[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 1
             for (int y = 0; y < nf; ++y) {
               const float4* src = reinterpret_cast<const float4*>(args.slot_o) + (at(y) * C4 + c) * kRows + row % kRows;
               const float2 ml = __ldcg(reinterpret_cast<const float2*>(args.slot_ml) + at(y) * kRows + row % kRows);
@@ -1213,7 +1159,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
   // ---- teardown ----
   tc_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
