@@ -51,7 +51,7 @@ constexpr int kTcThreads = 20 * 32;
 // the groups trade (sums of four warps: what they take may not pass what was launched).
 constexpr int kRegs = 96, kRegsSoft = 144, kRegsConv = 72, kRegsIssue = 48;
 static_assert(2 * kRegsSoft + 2 * kRegsConv + kRegsIssue <= 5 * kRegs, "register split");
-constexpr int kConvThreads = 128, kSoftThreads = 256;
+constexpr int kConvThreads = 128;
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wait
 __host__ __device__ constexpr uint32_t col_o(int w) { return 128u * uint32_t(w); }
 __host__ __device__ constexpr uint32_t col_s(int w, int b) { return 256u + 128u * uint32_t(w) + 64u * uint32_t(b); }
@@ -83,7 +83,7 @@ struct TcSmem {
   static constexpr int kInfo = kMeta + 4 * int(sizeof(TileMeta));  // [K, V][2][8]: keys of a raw tile's groups
   static constexpr int kBars = kInfo + 128;
   static constexpr int kAbort = kBars + 8 * 34 + 4;  // (after the barriers: TMEM address, abort flag)
-  static constexpr int kKeep = kAbort + 4 + 4 * 21;  // 20 words of the scan and one before it
+  static constexpr int kKeep = kAbort + 4 + 4 * 20;  // behind the scan's 20 words
   static constexpr int kBytes = kBars + 448;
   // the tiles before each request are summed up in what will hold operands
   static_assert(4 * (kAttentionQ8MaxB + 1) <= 2 * kTile, "scan space");
@@ -275,21 +275,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// a barrier of the softmax warps, and one that tells whether any of them says yes
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
-__device__ __forceinline__ bool soft_any(bool x) {
-  uint32_t r;
-  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
-               : "=r"(r)
-               : "r"(int(x)), "n"(kSoftThreads)
-               : "memory");
-  return r != 0;
-}
-
 struct TcArgs {
   AttentionQ8Params p;
   int blocks;          // 256-row blocks of a kv head's n * G rows
-  uint32_t* counters;  // [CTA]: arrivals on the unit that CTA begins and does not finish
+  int4* begun;         // [CTA]: the unit that the CTA begins and does not finish {last CTA of it (-1: none), request, (head, block), -}
   float* slot_o;       // [2 * CTA + i][group][D / 4][128][4]
   float* slot_ml;      // [2 * CTA + i][group][128][2]
 };
@@ -332,9 +321,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
   auto bar = [&](int i) { return bars + 8u * uint32_t(i); };
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sp + L::kBars + 8 * kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + L::kAbort);
-  static_assert(L::kAbort == L::kBars + 8 * kNumBars + 4 && L::kKeep + 32 <= L::kBytes, "layout");
+  static_assert(L::kAbort == L::kBars + 8 * kNumBars + 4 && L::kKeep + 4 <= L::kBytes, "layout");
   int* wsum = reinterpret_cast<int*>(sp + L::kBars + 8 * kNumBars + 8);  // [20]
-  int* keep = reinterpret_cast<int*>(sp + L::kKeep);  // [8]: what the joining at the end needs (kept here, it costs the roles no registers)
+  int* keep = reinterpret_cast<int*>(sp + L::kKeep);  // the tiles in all
   int* pre = reinterpret_cast<int*>(sp);  // [b + 1] tiles of one (kv head, row block) before request r (until the roles start)
 
   if (tid == 0) {
@@ -417,14 +406,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     start.t = rem - start.j * start.Tr;
   }
   request_of(a, start);
-  if (tid == 0) {
-    keep[0] = S;
-    keep[1] = E;
-    keep[2] = int(T);
-    keep[3] = start.r;
-    keep[4] = start.j;
-    keep[5] = start.t;
-  }
+  if (tid == 0) *keep = int(T);
   __syncthreads();  // the scan's space becomes operand tiles
   auto advance = [&](Pos& p) { next_pos(a, J, p); };
   // the piece of a unit that begins at position p, tile f of the range: its tiles
@@ -751,6 +733,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       }
     };
     if (S < E) ask_q(p);
+    if (tid == 0) args.begun[blockIdx.x] = make_int4(-1, 0, 0, 0);
     for (int f = S; ok && f < E; ++piece) {
       const int n = piece_tiles(p, f);
       const int rows = unit_rows(p.j);
@@ -1042,6 +1025,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       } else {
         *sm = make_float2(-INFINITY, 0.f);
       }
+      // (a unit that goes on in later CTAs is joined by the second kernel)
+      if (tid == 0 && !complete && p.t == 0) {
+        const long long Tk = *keep, ck = Tk < gridDim.x ? Tk : gridDim.x;  // (the tiles in all, and the CTAs that share them)
+        args.begun[blockIdx.x] = make_int4(int(((f + p.Tr) * ck - 1) / Tk), p.r, p.j, 0);
+      }
       if (local) mbar_arrive(bar(w == 1 ? kFragFull : kFragFree));
       tc_before();
       mbar_arrive(bar(kOFree0 + w));  // the next piece may write O
@@ -1051,109 +1039,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok && !*abort_flag) fail();
-    // The softmax groups join what the CTA shares with others (here, not at the
-    // kernel's end, where every warp would have to hold the registers for it, and
-    // what it needs comes out of shared memory, for the same reason).  The vote
-    // makes the decision one for all of them.
-    if (!soft_any(!ok || *abort_flag) && S < E) {
-      auto kept = [&](int i) {
-        int v;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(smem_u32(keep + i)) : "memory");
-        return v;
-      };
-      const int S2 = kept(0), E2 = kept(1);
-      const long long T2 = kept(2), ctas2 = T2 < gridDim.x ? T2 : gridDim.x;
-      auto cta_of = [&](long long x) { return int(((x + 1) * ctas2 - 1) / T2); };  // the CTA whose range holds tile x
-
-      // ---- units shared with other CTAs: count in, and join those that are last ----
-      Pos head;
-      head.r = kept(3);
-      head.j = kept(4);
-      head.t = kept(5);
-      request_of(a, head);
-      Pos last = head;
-      int last_f = S2;
-      {  // the first position of the range's last piece
-        int f = S2;
-        Pos q = head;
-        while (true) {
-          const int n = min(q.Tr - q.t, E2 - f);
-          last = q;
-          last_f = f;
-          if (f + n >= E2) break;
-          f += n;
-          q.t += n - 1;
-          next_pos(a, J, q);
-        }
-      }
-      for (int x = 0; x < 2; ++x) {
-        const Pos& q = x == 0 ? head : last;
-        if (x == 1 && last.r == head.r && last.j == head.j) break;  // one unit only
-        const long long us = (x == 0 ? S2 : last_f) - q.t;  // the unit's first tile
-        const int ca = cta_of(us), cb = cta_of(us + q.Tr - 1);
-        if (ca == cb) continue;
-        soft_sync();
-        if (tid == 0) keep[-1] = atom_add_acq_rel(args.counters + ca) == uint32_t(cb - ca);
-        soft_sync();
-        if (!keep[-1]) continue;
-        const int rows = unit_rows(q.j), h = q.j / args.blocks;
-        const bool split = rows <= kRows;
-        // a thread a row (two a row when the unit has one row tile: half of the
-        // columns each)
-        constexpr int C4 = D / 4;
-        const int row = split ? tid & 127 : tid, c0 = split && tid >= kRows ? C4 / 2 : 0, c1 = split && tid < kRows ? C4 / 2 : C4;
-        const int nf = (cb - ca + 1) * (split ? 2 : 1);
-        auto at = [&](int y) {
-          const int cta = ca + (split ? y >> 1 : y);
-          return size_t(2 * cta + (cta == ca ? 1 : 0)) * 2 + (split ? y & 1 : row / kRows);
-        };
-        const bool on = row < rows;
-        float Mx = -INFINITY, Ls = 0.f;
-        if (on) {
-#pragma unroll 4
-          for (int y = 0; y < nf; ++y) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(args.slot_ml) + at(y) * kRows + row % kRows);
-            const bool has = ml.y > 0.f || ml.y != ml.y;  // (else it saw nothing, and its O is not read)
-            const float M2 = has ? fmaxf(Mx, ml.x) : Mx;
-            const float wa = Ls > 0.f || Ls != Ls ? exp2f(Mx - M2) : 0.f;
-            Ls = has ? Ls * wa + ml.y * exp2f(ml.x - M2) : Ls;
-            Mx = M2;
-          }
-          const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
-          const int rg = 2 * kRows * (q.j % args.blocks) + row;
-          const size_t orow = (size_t(q.r) * a.n + rg / G) * a.Hq + h * G + rg % G;
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D);
-          for (int c = c0; c < c1; c += 8) {  // 32 columns, all their loads of a fragment in flight
-            float4 acc[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-            for (int y = 0; y < nf; ++y) {
-              const float4* src = reinterpret_cast<const float4*>(args.slot_o) + (at(y) * C4 + c) * kRows + row % kRows;
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(args.slot_ml) + at(y) * kRows + row % kRows);
-              float4 o4[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o4[e] = __ldcg(src + e * kRows);
-              if (!(ml.y > 0.f || ml.y != ml.y)) continue;
-              const float k = exp2f(ml.x - Mx) * inv;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                acc[e].x = fmaf(o4[e].x, k, acc[e].x);
-                acc[e].y = fmaf(o4[e].y, k, acc[e].y);
-                acc[e].z = fmaf(o4[e].z, k, acc[e].z);
-                acc[e].w = fmaf(o4[e].w, k, acc[e].w);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; e += 2)
-              dst[(c + e) / 2] = make_uint4(pack_bf16x2(acc[e].x, acc[e].y), pack_bf16x2(acc[e].z, acc[e].w),
-                                            pack_bf16x2(acc[e + 1].x, acc[e + 1].y), pack_bf16x2(acc[e + 1].z, acc[e + 1].w));
-          }
-          if (c0 == 0 && a.lse) a.lse[orow] = lse_of(Mx, Ls);
-        }
-        if (tid == 0) atomicExch(args.counters + ca, 0u);
-      }
-    }
   }
 
   // ---- teardown ----
@@ -1163,6 +1048,75 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
+}
+
+// Joins the units that the kernel above left in fragments: block (c, slice) 32 rows
+// of the unit that CTA c began and did not finish, a lane a row, a quarter of
+// the columns a warp.  A launch of its own, because it wants the whole GPU: the last
+// CTA of a unit, alone and with hardly any L1 beside its operands, took 23 us for
+// the trees' 1.2 MB and 54 us for the long contexts'.
+constexpr int kJoinThreads = 128, kJoinRows = 32;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attention_q8_join_kernel(const __grid_constant__ TcArgs args) {
+  pdl_wait();
+  pdl_trigger();
+  const AttentionQ8Params& a = args.p;
+  const int ca = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int4 unit = args.begun[ca];
+  const int cb = unit.x, r = unit.y, j = unit.z;
+  if (cb < 0) return;
+  const int G = a.Hq / a.Hkv, M = a.n * G;
+  const int rows = min(2 * kRows, M - 2 * kRows * (j % args.blocks)), h = j / args.blocks;
+  const bool split = rows <= kRows;
+  const int row = blockIdx.y * kJoinRows + lane;
+  if (row >= rows) return;
+  const int nf = (cb - ca + 1) * (split ? 2 : 1);
+  auto at = [&](int y) {
+    const int cta = ca + (split ? y >> 1 : y);
+    return size_t(2 * cta + (cta == ca ? 1 : 0)) * 2 + (split ? y & 1 : row / kRows);
+  };
+  const float2* ml2 = reinterpret_cast<const float2*>(args.slot_ml) + row % kRows;
+  float Mx = -INFINITY, Ls = 0.f;
+#pragma unroll 4
+  for (int y = 0; y < nf; ++y) {
+    const float2 ml = __ldcg(ml2 + at(y) * kRows);
+    const bool has = ml.y > 0.f || ml.y != ml.y;  // (else it saw nothing, and its O is not read)
+    const float M2 = has ? fmaxf(Mx, ml.x) : Mx;
+    const float wa = Ls > 0.f || Ls != Ls ? exp2f(Mx - M2) : 0.f;
+    Ls = has ? Ls * wa + ml.y * exp2f(ml.x - M2) : Ls;
+    Mx = M2;
+  }
+  const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+  constexpr int C4 = D / 4, C = C4 / (kJoinThreads / 32);  // 16-byte words a thread
+  const int c = warp * C;
+  float4 acc[C];
+#pragma unroll
+  for (int e = 0; e < C; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int y = 0; y < nf; ++y) {
+    const float4* src = reinterpret_cast<const float4*>(args.slot_o) + (at(y) * C4 + c) * kRows + row % kRows;
+    const float2 ml = __ldcg(ml2 + at(y) * kRows);
+    float4 o4[C];
+#pragma unroll
+    for (int e = 0; e < C; ++e) o4[e] = __ldcg(src + e * kRows);
+    if (!(ml.y > 0.f || ml.y != ml.y)) continue;
+    const float k = exp2f(ml.x - Mx) * inv;
+#pragma unroll
+    for (int e = 0; e < C; ++e) {
+      acc[e].x = fmaf(o4[e].x, k, acc[e].x);
+      acc[e].y = fmaf(o4[e].y, k, acc[e].y);
+      acc[e].z = fmaf(o4[e].z, k, acc[e].z);
+      acc[e].w = fmaf(o4[e].w, k, acc[e].w);
+    }
+  }
+  const int rg = 2 * kRows * (j % args.blocks) + row;
+  const size_t orow = (size_t(r) * a.n + rg / G) * a.Hq + h * G + rg % G;
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + 4 * c);
+#pragma unroll
+  for (int e = 0; e < C; e += 2)
+    dst[e / 2] = make_uint4(pack_bf16x2(acc[e].x, acc[e].y), pack_bf16x2(acc[e].z, acc[e].w),
+                            pack_bf16x2(acc[e + 1].x, acc[e + 1].y), pack_bf16x2(acc[e + 1].z, acc[e + 1].w));
+  if (warp == 0 && a.lse) a.lse[orow] = lse_of(Mx, Ls);
 }
 
 template <int D>
@@ -1179,11 +1133,15 @@ int launch_tc(const AttentionQ8Params& p, cudaStream_t stream) {
   if (smem < 120 * 1024) smem = 120 * 1024;
   if (cudaFuncSetAttribute(attention_q8_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
     return SPEC_ERR_LAUNCH;
-  TcArgs args{p, (p.n * (p.Hq / p.Hkv) + 2 * kRows - 1) / (2 * kRows), p.counters,
+  TcArgs args{p, (p.n * (p.Hq / p.Hkv) + 2 * kRows - 1) / (2 * kRows),
+              reinterpret_cast<int4*>(p.partials + kQ8SlotMlBytes - kQ8BegunBytes),
               reinterpret_cast<float*>(p.partials + kQ8SlotMlBytes), reinterpret_cast<float*>(p.partials)};
   const int grid = sms < kQ8MaxCtas ? sms : kQ8MaxCtas;
   const cudaError_t e = launch_pdl(attention_q8_tc_kernel<D>, dim3(grid), dim3(kTcThreads), smem, stream, args);
-  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+  if (e != cudaSuccess) return SPEC_ERR_LAUNCH;
+  const dim3 join(unsigned(grid), 2 * kRows / kJoinRows);
+  return launch_pdl(attention_q8_join_kernel<D>, join, dim3(kJoinThreads), 0, stream, args) == cudaSuccess ? SPEC_OK
+                                                                                                         : SPEC_ERR_LAUNCH;
 }
 
 }  // namespace
