@@ -19,18 +19,23 @@
 // Bound: the cache's bytes.  A warp owns its work end to end: it takes an
 // equal, contiguous range of 16-key tiles of all (request, kv head, 16-row
 // tile) units laid end to end, copies each tile's K and V (2 x 16 x D bytes,
-// contiguous in a page) into a private four-stage ring with 16-byte cp.async, and
+// contiguous in a page) into a private three-stage ring with 16-byte cp.async, and
 // runs S = Q K^T and O += P V as register fragments (mma.sync m16n8k16: with at
 // most 16 rows the tensor work of a 4 KB tile is 64 K multiply-adds, a third of
 // the time the tile takes to arrive, and no operand passes through shared
 // memory twice; a 128-row tcgen05 tile would be mostly padding).  The order of
 // the head dimension inside a fragment is free as long as Q has the same, and
 // that of the keys as long as P has the same, so both K and V fragments are
-// read as whole 16-byte words.
-//   There is no barrier before the end of the range.  Units cut by a range
-// boundary leave fragments (O, m, l) in shared memory; the CTA joins those of
-// its warps, and a unit cut over CTAs is joined by the CTA that arrives last on
-// it (acquire-release counter).
+// read as whole 16-byte words.  What limits a warp is the issue of its ~340
+// instructions a tile, so the history's loop is one short body.
+//   There is no barrier.  Units cut by a range boundary leave fragments (O, m, l)
+// in the workspace, and a second, dependent launch joins them (a join by the CTA's own
+// warps behind a barrier and by the last CTA of a unit took 20 us on average, 57 us at
+// most, of a 275 us call).  Only where all the warps of a CTA lie inside one unit does
+// the CTA join its own first, so that a long context leaves few.
+//   256 chains of four, contexts 256 to 4096, 32 / 8 heads of 128: 215 us (1.13 GB
+// of cache at 5.3 TB/s).  A deeper ring is slower (four stages 232 us): with more
+// bytes in flight than the memory needs, the dependent reads at a unit's ends only wait longer.
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -41,32 +46,56 @@ namespace spec {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 12;
 constexpr int kQ8AttThreads = 32 * kWarps;
 constexpr int kRowsMost = 32;  // query rows a kv head up to which this kernel is taken
 constexpr int kTile = 16;    // keys of a tile
 constexpr int kRowTile = 16; // query rows of a unit
-constexpr int kRing = 4;     // tiles in a warp's ring
-constexpr int kMinTiles = 2; // a warp gets at least this many tiles before another warp is used
+constexpr int kRing = 3;     // tiles in a warp's ring
+constexpr int kMinTicks = 2; // a warp gets at least this many ticks before another warp is used
+// Ticks of a tree tile in the division of the work; a history tile is one.  A tree tile and the
+// ends of its unit cost a warp some ten history tiles, nearly all latency; by 2, 4, 8 and 12 ticks the
+// chains above took 254, 236, 232 and 228 us (with four stages), and a single token 1 us more by 12 than by 8.
+constexpr int kTreeTicks = 8;
 
 template <int D>
 struct RowsSmem {
   static constexpr int kHalf = kTile * D;         // K (or V) bytes of a tile
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kFrag = kRowTile * D * 4;  // fp32 O of a fragment
-  static constexpr int kWarp = kRing * kStage + kFrag + 2 * kRowTile * 8;  // ring | first fragment's O | (m, l) of both
-  static_assert(kRing * kStage >= kFrag, "the last fragment's O takes the idle ring");
-  static constexpr int kDesc = kWarps * kWarp;    // fragment descriptors: [warp][2] unit (-1: none)
-  static constexpr int kScan = kDesc + 256;
+  static constexpr int kWarp = kRing * kStage;
+  static_assert(kWarp >= kFrag, "a fragment takes the idle ring");
+  static constexpr int kMl = kWarps * kWarp;      // [warp][16] (m, l)
+  static constexpr int kMeta = kMl + kWarps * kRowTile * 8;  // [warp][stage] the tile's word
+  static constexpr int kScan = kMeta + kWarps * kRing * 4;
   static size_t bytes(int b) { return size_t(kScan) + 12u * size_t(b + 1); }
 };
 
+// What the kernel leaves for the joining one: table[0] = {warps, warps a CTA},
+// table[1 + warp] = the unit that the warp begins and does not finish
+// {last warp on it (-1: none), request, (kv head, row tile)}.
 struct RowsArgs {
   AttentionQ8Params p;
-  int m_tiles;      // 16-row tiles of a kv head's n * G rows
-  uint32_t* counters;  // [CTA]: arrivals on the unit that CTA begins and does not finish
-  float* slot_o;    // [2 * CTA + i][16][D]
-  float* slot_ml;   // [2 * CTA + i][16][2]
+  int m_tiles;    // 16-row tiles of a kv head's n * G rows
+  int4* table;
+  float4* slot_o; // [2 * warp + i][D / 8][32], i = 1: the unit that the warp begins
+  float2* slot_ml;  // [2 * warp + i][16]
+};
+static_assert((size_t(kQ8MaxCtas) * kWarps + 1) * 16 <= kQ8BegunBytes && 2 * kWarps * kRowTile <= 2 * kQ8SlotRows, "slots");
+
+// The fragments of a unit on warps [wa, wb], wpc of them a CTA: a CTA whose warps lie
+// strictly between has joined its own into its first warp's slot.
+struct Fragments {
+  int wa, wb, wpc, before, solid;  // warps before the first such CTA, and those CTAs
+  __device__ Fragments(int a, int b, int c) : wa(a), wb(b), wpc(c) {
+    const int k1 = wa / wpc + 1, k2 = wb / wpc - 1;
+    solid = k2 >= k1 ? k2 - k1 + 1 : 0;
+    before = solid ? k1 * wpc - wa : wb - wa + 1;
+  }
+  __device__ int count() const { return wb - wa + 1 - solid * (wpc - 1); }
+  __device__ int warp(int i) const {
+    return i < before ? wa + i : i < before + solid ? wa + before + (i - before) * wpc : wa + i + solid * (wpc - 1);
+  }
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -99,19 +128,17 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
   constexpr int NT = D / 8;    // 8-column tiles of O
   const AttentionQ8Params& a = args.p;
   extern __shared__ __align__(128) unsigned char smem[];
-  int* desc = reinterpret_cast<int*>(smem + L::kDesc);
-  int* pre = reinterpret_cast<int*>(smem + L::kScan);  // [b + 1] tiles of one (kv head, row tile) before request r
+  int* pre = reinterpret_cast<int*>(smem + L::kScan);  // [b + 1] ticks of one (kv head, row tile) before request r
   int* slen = pre + a.b + 1;                           // [b]
   int* srow = slen + a.b + 1;                          // [b] table row, -1 if bad
   __shared__ int wsum[kWarps];
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int G = a.Hq / a.Hkv, M = a.n * G, J = a.Hkv * args.m_tiles;
-  const int tree_tiles = (a.n + kTile - 1) / kTile;
-  if (tid < 2 * kWarps) desc[tid] = -1;
+  const int tree_tiles = (a.n + kTile - 1) / kTile, tree_ticks = kTreeTicks * tree_tiles;
 
   pdl_wait();
   pdl_trigger();
-  // ---- tiles before each request ----
+  // ---- ticks before each request ----
   {
     int run = 0;
     for (int r0 = 0; r0 < a.b; r0 += kQ8AttThreads) {
@@ -122,7 +149,7 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
         const ReqQ8 q = req_q8(a, Lp, rq, blockIdx.x == 0);
         slen[r] = q.len;
         srow[r] = q.row;
-        t = (q.len + kTile - 1) / kTile + tree_tiles;
+        t = (q.len + kTile - 1) / kTile + tree_ticks;
       }
       int incl = t;
 #pragma unroll
@@ -144,546 +171,561 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
     __syncthreads();
   }
   const long long T = (long long)pre[a.b] * J;  // (the host keeps it below 2^31)
-  // wpc warps a CTA over `ctas` CTAs, every warp with at least one tile
+  // wpc warps a CTA over `ctas` CTAs, every warp with at least one tick
   const long long grid = gridDim.x;
-  int wpc = int((T + grid * kMinTiles - 1) / (grid * kMinTiles));
+  int wpc = int((T + grid * kMinTicks - 1) / (grid * kMinTicks));
   wpc = wpc < 1 ? 1 : wpc > kWarps ? kWarps : wpc;
-  long long ctas = (T + (long long)wpc * kMinTiles - 1) / ((long long)wpc * kMinTiles);
+  long long ctas = (T + (long long)wpc * kMinTicks - 1) / ((long long)wpc * kMinTicks);
   if (ctas > grid) ctas = grid;
   const long long NW = ctas * wpc < T ? ctas * wpc : T;
-  if (blockIdx.x * (long long)wpc >= NW) return;
-  const long long me = blockIdx.x * (long long)wpc + w;
-  const bool active = w < wpc && me < NW;
-  const int S = active ? int(me * T / NW) : 0, E = active ? int((me + 1) * T / NW) : 0;
-  auto warp_of = [&](long long x) { return ((x + 1) * NW - 1) / T; };  // the warp whose range holds tile x
+  if (blockIdx.x == 0 && tid == 0) args.table[0] = make_int4(int(NW), wpc, 0, 0);
+  const int me0 = int(blockIdx.x) * wpc, me = me0 + w;
+  if (w >= wpc || me >= NW) return;
+  int S = int(me * T / NW);
+  const int E = int((me + 1) * T / NW);
+  auto req_of = [&](int f) {
+    int lo = 0, hi = a.b;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((long long)pre[mid] * J <= f) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  };
+  int r = req_of(S), Tr = pre[r + 1] - pre[r];
+  int j, t;
+  {
+    const int rem = S - pre[r] * J;
+    j = rem / Tr;
+    t = rem - j * Tr;
+  }
+  // whether all of the CTA's warps lie strictly between the first and the last of one unit
+  bool solid = false;
+  if (me0 + wpc < NW) {
+    const long long u0 = S - t, c0 = me0 * T / NW, c1 = (long long)(me0 + wpc) * T / NW;
+    solid = u0 < c0 && c1 < u0 + Tr;
+  }
+  if (t > Tr - tree_ticks && (t - (Tr - tree_ticks)) % kTreeTicks) {  // inside a tree tile, which is the warp's that holds its first tick
+    const int skip = kTreeTicks - (t - (Tr - tree_ticks)) % kTreeTicks;
+    if (lane < kRowTile) args.slot_ml[size_t(2 * me) * kRowTile + lane] = make_float2(-INFINITY, 0.f);
+    __syncwarp();
+    S += skip;
+    t += skip;
+    if (t == Tr) {
+      t = 0;
+      if (++j == J) {
+        j = 0;
+        ++r;
+        if (r < a.b) Tr = pre[r + 1] - pre[r];
+      }
+    }
+  }
+  if (lane == 0) args.table[1 + me] = make_int4(-1, 0, 0, 0);
 
   unsigned char* mine = smem + size_t(w) * L::kWarp;
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
-  float* ffrag = reinterpret_cast<float*>(mine + kRing * L::kStage);
-  float* fml = reinterpret_cast<float*>(mine + kRing * L::kStage + L::kFrag);  // [2][16][2]
+  float2* fml = reinterpret_cast<float2*>(smem + L::kMl) + w * kRowTile;
+  uint32_t* meta = reinterpret_cast<uint32_t*>(smem + L::kMeta) + w * kRing;
+  if (lane < kRowTile) fml[lane] = make_float2(-INFINITY, 0.f);
 
-  if (active) {
-    auto req_of = [&](int f) {
-      int lo = 0, hi = a.b;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((long long)pre[mid] * J <= f) lo = mid;
-        else hi = mid;
-      }
-      return lo;
-    };
-    // lane l looks up tile mb + l of the range: page, kv head, first key in
-    // the page, keys that count; a tree tile (or a bad page) has page -1
-    const int SHIFT = a.page_size == 16 ? 0 : a.page_size == 32 ? 1 : 2;  // log2(tiles a page)
-    int mb = S - 32, l_unit = 0, l_off = 0, l_cnt = 0, l_exp = 0, p_exp = 0;
-    auto load_meta = [&](int f0) {
-      p_exp = l_exp;
-      mb = f0;
-      const int f = f0 + lane;
-      l_unit = -1;
-      l_off = l_cnt = l_exp = 0;
-      if (f < E) {
-        const int r = req_of(f), Tr = pre[r + 1] - pre[r];
-        const int rem = f - pre[r] * J, j = rem / Tr, t = rem - j * Tr, h = j / args.m_tiles;
-        if (t < Tr - tree_tiles && srow[r] >= 0) {
-          const int pid = a.page_table[size_t(srow[r]) * a.row_pages + (t >> SHIFT)];
-          if (pid < 0 || pid >= a.num_pages) {
-            raise_error(a.error, SPEC_DEV_INDEX);
-          } else {
-            l_unit = pid * a.Hkv + h;
-            l_off = (t & ((1 << SHIFT) - 1)) * kTile;
-            l_cnt = min(kTile, slen[r] - t * kTile);
-            l_exp = int(a.k_scales[l_unit]) | (int(a.v_scales[l_unit]) << 8) | 0x10000;
-          }
+  // Lane l looks up tick mb + l of the range: its (page, kv head) unit (-1: a tree
+  // tile's), and in one word the first key in the page, the keys that count and the
+  // exponents of the K and V scales.  A bad page has no key that counts.
+  const int SHIFT = a.page_size == 16 ? 0 : a.page_size == 32 ? 1 : 2;  // log2(tiles a page)
+  int mb = S - 32, l_unit = 0;
+  uint32_t l_word = 0;
+  auto load_meta = [&](int f0) {
+    mb = f0;
+    const int f = f0 + lane;
+    l_unit = -1;
+    l_word = 0;
+    if (f < E) {
+      const int fr = req_of(f), fT = pre[fr + 1] - pre[fr];
+      const int rem = f - pre[fr] * J, fj = rem / fT, ft = rem - fj * fT;
+      if (ft < fT - tree_ticks && srow[fr] >= 0) {
+        const int pid = a.page_table[size_t(srow[fr]) * a.row_pages + (ft >> SHIFT)];
+        if (pid < 0 || pid >= a.num_pages) {
+          raise_error(a.error, SPEC_DEV_INDEX);
+          l_unit = 0;
+          l_word = uint32_t(kExpBias) << 16 | uint32_t(kExpBias) << 24;
+        } else {
+          l_unit = pid * a.Hkv + fj / args.m_tiles;
+          l_word = uint32_t(ft & ((1 << SHIFT) - 1)) * kTile | uint32_t(min(kTile, slen[fr] - ft * kTile)) << 8 |
+                   uint32_t(a.k_scales[l_unit]) << 16 | uint32_t(a.v_scales[l_unit]) << 24;
         }
       }
-    };
-    constexpr int kChunks = D / 16;        // 16-byte chunks of a key
-    constexpr int kCopies = kTile * kChunks / 32;
-    auto issue = [&](int f) {
-      if (f < E) {
-        if (f - mb >= 32) load_meta(f);
-        const int unit = __shfl_sync(FULL, l_unit, f - mb), off = __shfl_sync(FULL, l_off, f - mb),
-                  cnt = __shfl_sync(FULL, l_cnt, f - mb);
-        if (unit >= 0) {
-          const size_t at = (size_t(unit) * a.page_size + off) * D;
-          const uint32_t st = ring + uint32_t(f % kRing) * L::kStage;
-#pragma unroll
-          for (int i = 0; i < kCopies; ++i) {
-            const int ch = i * 32 + lane, key = ch / kChunks, x = ch % kChunks;
-            const int kx = D == 128 ? x ^ (4 * (key & 1)) : x;
-            const int vx = D == 128 ? x ^ (((key >> 1) & 3) << 1) : x ^ (((key >> 1) & 1) << 1);
-            const uint32_t nb = key < cnt ? 16u : 0u;  // (a key past the history reads as zeros)
-            const size_t so = at + (key < cnt ? size_t(ch) * 16 : 0);
-            cp16(st + uint32_t(key * D + kx * 16), a.k_pages + so, nb);
-            cp16(st + L::kHalf + uint32_t(key * D + vx * 16), a.v_pages + so, nb);
-          }
-        }
-      }
-      cp_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kRing - 1; ++i) issue(S + i);
-
-    // ---- consumer state: the current unit and its running results ----
-    int r = req_of(S), Tr = pre[r + 1] - pre[r];
-    int j, t;
-    {
-      const int rem = S - pre[r] * J;
-      j = rem / Tr;
-      t = rem - j * Tr;
     }
-    int t_first = t;
+  };
+  constexpr int kChunks = D / 16;  // 16-byte chunks of a key
+  constexpr int kCopies = kTile * kChunks / 32, kKeys = 32 / kChunks;
+  // where this lane's chunk of a copy goes: the K chunk order turns with the key's
+  // parity, V's with the pair of keys, so that the fragment reads below meet no bank twice
+  const int ckey = lane / kChunks, cx = lane % kChunks;
+  const uint32_t kdst = ckey * D + (D == 128 ? cx ^ (4 * (ckey & 1)) : cx) * 16;
+  auto vdst = [&](int i) {
+    const int key = i * kKeys + ckey;
+    return uint32_t(L::kHalf + ckey * D + (D == 128 ? cx ^ (((key >> 1) & 3) << 1) : cx ^ (((key >> 1) & 1) << 1)) * 16);
+  };
+  auto issue = [&](int f) {
+    if (f < E) {
+      if (f - mb >= 32) load_meta(f);
+      const int unit = __shfl_sync(FULL, l_unit, f - mb);
+      const uint32_t word = __shfl_sync(FULL, l_word, f - mb);
+      if (unit >= 0) {
+        const int cnt = (word >> 8) & 31;
+        const size_t at = (size_t(unit) * a.page_size + (word & 63)) * D + lane * 16;
+        const uint32_t st = ring + uint32_t(f % kRing) * L::kStage;
+        const uint8_t *ks = a.k_pages + at, *vs = a.v_pages + at;
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const uint32_t nb = i * kKeys + ckey < cnt ? 16u : 0u;  // (a key past the history reads as zeros)
+          cp16(st + kdst + i * 512, ks + i * 512, nb);
+          cp16(st + vdst(i) + i * 512, vs + i * 512, nb);
+        }
+        if (lane == 0) meta[f % kRing] = word;
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) issue(S + i);
+
+  const int kread = g * D + (D == 128 ? c ^ (4 * (g & 1)) : c) * 16;
+  const int vread = L::kHalf + 2 * c * D + (D == 128 ? (g ^ (c << 1)) * 16 : ((g >> 1) ^ ((c & 1) << 1)) * 16 + (g & 1) * 8);
+  for (int f = S; f < E;) {
+    // ---- a unit, or the part of it in this range: its Q rows as f16 fragments, masks, empty results ----
+    const int h = j / args.m_tiles, mt = j - h * args.m_tiles;
+    const int t_first = t, f_first = f, Th = Tr - tree_ticks;
     uint32_t qf[KS][4];
     float xf[2];                // softmax factor of rows g, g + 8: scale * log2e * the row's power of two
-    unsigned long long mask[2];
     float o[NT][4], m[2], l[2];
-    int evb = 0;                // the exponent byte that the unit's value scales are taken relative to (its first tile's)
+    int evb = -1;               // the exponent byte that the unit's value scales are taken relative to (its first tile's)
     unsigned long long nonfinite = 0;  // tree nodes whose V row holds an inf or a NaN
-    bool fresh = true;
-    for (int f = S; f < E; ++f) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int rg = mt * kRowTile + g + 8 * i;
+      const bool on = rg < M;
+      const int node = on ? rg / G : 0, hq = h * G + (on ? rg % G : 0);
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                        (size_t(r) * a.n + node) * a.q_ld + size_t(hq) * D);
+      uint4 x[D / 32];
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u)  // 16 elements from 16 c, and 64 + 16 c
+        x[u] = on ? __ldg(src + (u >> 1) * 8 + 2 * c + (u & 1)) : make_uint4(0, 0, 0, 0);
+      uint32_t mx = 0;
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u)
+        mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, x[u].x), x[u].y), x[u].z), x[u].w);
+      mx = max(mx & 0xffffu, mx >> 16);
+      mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
+      mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
+      const int e = norm_exp(mx);
+      const float inv = exp_scale(2 * kExpBias - e);
+      xf[i] = a.scale * 1.4426950408889634f * exp_scale(e);
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {  // words 2 kk, 2 kk + 1 of the thread's words
+        const uint4& y = x[kk >> 1];
+        qf[kk][i] = scaled_f16(word_of(y, (kk & 1) * 2), inv);
+        qf[kk][2 + i] = scaled_f16(word_of(y, (kk & 1) * 2 + 1), inv);
+      }
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[q][i] = 0.f;
+    // The reference m of a row: P is 2^kPBaseLog2 at the row's maximum when it is set,
+    // and it moves only when P would pass 2^kLazyLog2 times that.
+    constexpr float kMost = kLazyLog2 + kPBaseLog2;
+    auto move = [&](const float (&x)[2][4]) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+        if (mx > m[i] + kMost) {
+          const float fac = fast_exp2(m[i] + kPBaseLog2 - mx);  // (0 from an empty row)
+          l[i] *= fac;
+#pragma unroll
+          for (int q = 0; q < NT; ++q) {
+            o[q][2 * i] *= fac;
+            o[q][2 * i + 1] *= fac;
+          }
+          m[i] = mx - kPBaseLog2;
+        }
+      }
+    };
+
+    // ---- history ----
+    for (const int fh = min(E, f + (t < Th ? Th - t : 0)); f < fh; ++f) {
       cp_wait<kRing - 2>();
       __syncwarp();
       issue(f + kRing - 1);
-      const int h = j / args.m_tiles, mt = j - h * args.m_tiles;
-      if (fresh) {  // a unit begins: its Q rows as f16 fragments, masks, empty results
-        fresh = false;
-        t_first = t;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int rg = mt * kRowTile + g + 8 * i;
-          const bool on = rg < M;
-          const int node = on ? rg / G : 0, hq = h * G + (on ? rg % G : 0);
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                            (size_t(r) * a.n + node) * a.q_ld + size_t(hq) * D);
-          uint4 x[D / 32];
-#pragma unroll
-          for (int u = 0; u < D / 32; ++u)  // 16 elements from 16 c, and 64 + 16 c
-            x[u] = on ? __ldg(src + (u >> 1) * 8 + 2 * c + (u & 1)) : make_uint4(0, 0, 0, 0);
-          mask[i] = on ? a.mask_bits[size_t(r) * a.n + node] : 0ull;
-          uint32_t mx = 0;
-#pragma unroll
-          for (int u = 0; u < D / 32; ++u)
-            mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, x[u].x), x[u].y), x[u].z), x[u].w);
-          mx = max(mx & 0xffffu, mx >> 16);
-          mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
-          mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
-          const int e = norm_exp(mx);
-          const float inv = exp_scale(2 * kExpBias - e);
-          xf[i] = a.scale * 1.4426950408889634f * exp_scale(e);
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk) {  // words 2 kk, 2 kk + 1 of the thread's words
-            const uint4& y = x[kk >> 1];
-            qf[kk][i] = scaled_f16(word_of(y, (kk & 1) * 2), inv);
-            qf[kk][2 + i] = scaled_f16(word_of(y, (kk & 1) * 2 + 1), inv);
-          }
-          m[i] = -INFINITY;
-          l[i] = 0.f;
-        }
-#pragma unroll
-        for (int q = 0; q < NT; ++q)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[q][i] = 0.f;
-        evb = -1;
-        nonfinite = 0;
-      }
-
+      const unsigned char* st = mine + (f % kRing) * L::kStage;
+      const uint32_t word = meta[f % kRing];
+      const int cnt = (word >> 8) & 31, ev = word >> 24;
+      const float kf = exp_scale((word >> 16) & 255);
+      if (evb < 0) evb = ev;
       float s[2][4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[q][i] = 0.f;
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) {  // key 8 q + g: chunks c and c + 4
+          const uint4 y = *reinterpret_cast<const uint4*>(st + (kread ^ (64 * u)) + 8 * q * D);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t b0, b1;
+            e4m3x4_to_f16x4(word_of(y, i), b0, b1);
+            mma_f16(s[q], qf[4 * u + i], b0, b1);
+          }
+        }
+      }
+      // y = x - m with x = s * factor + (e - evb); a row without a reference yet has y = inf
+      const float de = float(ev - evb), x0 = xf[0] * kf, x1 = xf[1] * kf, d0 = de - m[0], d1 = de - m[1];
+      float y[2][4];
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[q][i] = 0.f;
-      uint32_t vb[NT][2];  // V fragments: b0 (keys 2c, 2c+1), b1 (keys 2c+8, 2c+9) of column tile nt
-      float dl[2][2];      // P's columns in l: 2^(evb - e) of key 8q + 2c + i
-      const bool hist = t < Tr - tree_tiles;
-      if (hist) {
-        const int src = f - mb >= 0 ? f - mb : f - mb + 32;
-        const int cur = __shfl_sync(FULL, l_exp, src & 31), prv = __shfl_sync(FULL, p_exp, src & 31);
-        const int ex = f >= mb ? cur : prv;
-        const float kf = exp_scale(ex & 255);
-        const int ev = (ex >> 8) & 255;
-        if (evb < 0) evb = ev;
-        const float de = float(ev - evb);
-        dl[0][0] = dl[0][1] = dl[1][0] = dl[1][1] = ratio_scale(evb - ev);
-        const unsigned char* st = mine + (f % kRing) * L::kStage;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int key = 8 * q + g;
-#pragma unroll
-          for (int u = 0; u < D / 64; ++u) {
-            const int x = c + 4 * u, kx = D == 128 ? x ^ (4 * (key & 1)) : x;
-            const uint4 y = *reinterpret_cast<const uint4*>(st + key * D + kx * 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t wd = word_of(y, i);
-              mma_f16(s[q], qf[4 * u + i], e4m3x2_to_f16x2(wd), e4m3x2_to_f16x2(wd >> 16));
-            }
-          }
+        for (int i = 0; i < 2; ++i) {
+          y[q][i] = fmaf(s[q][i], x0, d0);
+          y[q][2 + i] = fmaf(s[q][2 + i], x1, d1);
         }
-        const int cnt = min(kTile, slen[r] - t * kTile);
-        const float x0 = xf[0] * kf, x1 = xf[1] * kf;
-        const bool pageless = ex < 0x10000;  // (a page out of range: its keys do not count)
+      if (cnt < kTile) {  // keys past the history
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const bool on = 8 * q + 2 * c + i < cnt && !pageless;
-            s[q][i] = on ? fmaf(s[q][i], x0, de) : -INFINITY;
-            s[q][2 + i] = on ? fmaf(s[q][2 + i], x1, de) : -INFINITY;
-          }
-        const unsigned char* sv = st + L::kHalf;
-        uint32_t v[4][D / 32];  // keys 2c, 2c+1, 2c+8, 2c+9; D / 8 bytes each
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = 2 * c + (i & 1) + 8 * (i >> 1);
-          if (D == 128) {
-            const int vx = g ^ (((key >> 1) & 3) << 1);
-            const uint4 y = *reinterpret_cast<const uint4*>(sv + key * D + vx * 16);
-            v[i][0] = y.x;
-            v[i][1] = y.y;
-            v[i][D / 32 - 2] = y.z;
-            v[i][D / 32 - 1] = y.w;
-          } else {
-            const int vx = (g >> 1) ^ (((key >> 1) & 1) << 1);
-            const uint2 y = *reinterpret_cast<const uint2*>(sv + key * D + vx * 16 + (g & 1) * 8);
-            v[i][0] = y.x;
-            v[i][1] = y.y;
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < D / 32; ++u)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t t0 = __byte_perm(v[0][u], v[1][u], hf ? 0x7362 : 0x5140);
-            const uint32_t t1 = __byte_perm(v[2][u], v[3][u], hf ? 0x7362 : 0x5140);
-            vb[4 * u + 2 * hf][0] = e4m3x2_to_f16x2(t0);
-            vb[4 * u + 2 * hf][1] = e4m3x2_to_f16x2(t1);
-            vb[4 * u + 2 * hf + 1][0] = e4m3x2_to_f16x2(t0 >> 16);
-            vb[4 * u + 2 * hf + 1][1] = e4m3x2_to_f16x2(t1 >> 16);
-          }
-        if (pageless) {  // (the ring stage holds nothing of this tile)
-#pragma unroll
-          for (int q = 0; q < NT; ++q) vb[q][0] = vb[q][1] = 0u;
-        }
-      } else {
-        // ---- tree nodes: the step's bf16 rows, each divided by its own power of two ----
-        const int nb = (t - (Tr - tree_tiles)) * kTile;  // first node of the tile
-        const uint16_t* kn = static_cast<const uint16_t*>(a.k_new) + size_t(h) * D;
-        const uint16_t* vn = static_cast<const uint16_t*>(a.v_new) + size_t(h) * D;
-        uint4 kx[2][D / 32];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int node = nb + 8 * q + g;
-          const uint4* src = reinterpret_cast<const uint4*>(kn + (size_t(r) * a.n + (node < a.n ? node : 0)) * a.new_ld);
-#pragma unroll
-          for (int u = 0; u < D / 32; ++u)
-            kx[q][u] = node < a.n ? __ldg(src + (u >> 1) * 8 + 2 * c + (u & 1)) : make_uint4(0, 0, 0, 0);
-        }
-        float kf[2][2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t mx = 0;
-#pragma unroll
-          for (int u = 0; u < D / 32; ++u)
-            mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, kx[q][u].x), kx[q][u].y), kx[q][u].z), kx[q][u].w);
-          mx = max(mx & 0xffffu, mx >> 16);
-          mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
-          mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
-          const int e = norm_exp(mx);
-          const float inv = exp_scale(2 * kExpBias - e);
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk) {
-            const uint4& y = kx[q][kk >> 1];
-            mma_f16(s[q], qf[kk], scaled_f16(word_of(y, (kk & 1) * 2), inv), scaled_f16(word_of(y, (kk & 1) * 2 + 1), inv));
-          }
-          kf[q][0] = exp_scale(__shfl_sync(FULL, e, 8 * c));
-          kf[q][1] = exp_scale(__shfl_sync(FULL, e, 8 * c + 4));
-        }
-        uint4 vx[4][D / 64];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int node = nb + 2 * c + (i & 1) + 8 * (i >> 1);
-          const uint4* src = reinterpret_cast<const uint4*>(vn + (size_t(r) * a.n + (node < a.n ? node : 0)) * a.new_ld);
-#pragma unroll
-          for (int u = 0; u < D / 64; ++u)
-            vx[i][u] = node < a.n ? __ldg(src + g * (D / 64) + u) : make_uint4(0, 0, 0, 0);
-        }
-        int evk[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t mx = 0;
-          bool nf = false;
-#pragma unroll
-          for (int u = 0; u < D / 64; ++u) {
-            nf = nf || nonfinite_bf16(vx[i][u].x) || nonfinite_bf16(vx[i][u].y) || nonfinite_bf16(vx[i][u].z) ||
-                 nonfinite_bf16(vx[i][u].w);
-            mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, vx[i][u].x), vx[i][u].y), vx[i][u].z), vx[i][u].w);
-          }
-          mx = max(mx & 0xffffu, mx >> 16);
-          mx = max(mx, __shfl_xor_sync(FULL, mx, 4));
-          mx = max(mx, __shfl_xor_sync(FULL, mx, 8));
-          mx = max(mx, __shfl_xor_sync(FULL, mx, 16));
-          evk[i] = norm_exp(mx);
-          // an inf or a NaN must reach the rows that see the node and no
-          // other: it is left out of the product and added at the end
-          const unsigned who = __ballot_sync(FULL, nf);
-          if (who) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (who & (0x11111111u << q)) {
-                const int node = nb + 2 * q + (i & 1) + 8 * (i >> 1);
-                if (node < kMaxN) nonfinite |= 1ull << node;
-              }
-#pragma unroll
-            for (int u = 0; u < D / 64; ++u) {
-              vx[i][u].x = finite_bf16(vx[i][u].x);
-              vx[i][u].y = finite_bf16(vx[i][u].y);
-              vx[i][u].z = finite_bf16(vx[i][u].z);
-              vx[i][u].w = finite_bf16(vx[i][u].w);
-            }
-          }
-        }
-        if (evb < 0) {
-          evb = max(max(evk[0], evk[1]), max(evk[2], evk[3]));
-          evb = max(evb, __shfl_xor_sync(FULL, evb, 1));
-          evb = max(evb, __shfl_xor_sync(FULL, evb, 2));
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int node = nb + 8 * q + 2 * c + i;
-            const bool in = node < a.n;
-            const int d = evk[2 * q + i] - evb;
-            s[q][i] = in && ((mask[0] >> (node & 63)) & 1) ? fmaf(s[q][i], xf[0] * kf[q][i], float(d)) : -INFINITY;
-            s[q][2 + i] = in && ((mask[1] >> (node & 63)) & 1) ? fmaf(s[q][2 + i], xf[1] * kf[q][i], float(d)) : -INFINITY;
-            dl[q][i] = ratio_scale(-d);
-          }
-        // the columns: element e of the thread's D / 8 is column tile e
-#pragma unroll
-        for (int e = 0; e < NT; ++e) {
-          auto el = [&](int i) {
-            const uint32_t wd = word_of(vx[i][e >> 3], (e & 7) >> 1);
-            return ((e & 1) ? bf16_hi(wd) : bf16_lo(wd)) * exp_scale(2 * kExpBias - evk[i]);
-          };
-          vb[e][0] = pack_f16(el(0), el(1));
-          vb[e][1] = pack_f16(el(2), el(3));
-        }
+          for (int i = 0; i < 4; ++i)
+            if (8 * q + 2 * c + (i & 1) >= cnt) y[q][i] = s[q][i] = -INFINITY;
       }
-
-      // ---- running reference: P is kPBase at the row's maximum when it is
-      // set, and it is moved only when P would pass 2^kLazyLog2 times that ----
-      const float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-      const float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-      if (__any_sync(FULL, x0 > m[0] + (kLazyLog2 + kPBaseLog2) || x1 > m[1] + (kLazyLog2 + kPBaseLog2))) {
-        float fac[2];
+      const float ym = fmaxf(fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[0][2], y[0][3])), fmaxf(fmaxf(y[1][0], y[1][1]), fmaxf(y[1][2], y[1][3])));
+      const bool unset = m[0] == -INFINITY || m[1] == -INFINITY;
+      if (__any_sync(FULL, ym > kMost || unset)) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[q][i] = 8 * q + 2 * c + (i & 1) < cnt ? fmaf(s[q][i], i < 2 ? x0 : x1, de) : -INFINITY;
+        move(y);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[q][i] -= m[i >> 1] == -INFINITY ? 0.f : m[i >> 1];
+      }
+      uint32_t pa[4];
+      float sum[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float mx = i ? x1 : x0;
-          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
-          const bool up = mx > m[i] + (kLazyLog2 + kPBaseLog2);
-          fac[i] = up ? fast_exp2(m[i] + kPBaseLog2 - mx) : 1.f;  // (0 from an empty row)
-          l[i] *= fac[i];
-          if (up) m[i] = mx - kPBaseLog2;
+          const float p0 = fast_exp2(y[q][2 * i]), p1 = fast_exp2(y[q][2 * i + 1]);
+          sum[i] = q == 0 ? p0 + p1 : sum[i] + (p0 + p1);
+          pa[2 * q + i] = pack_f16(p0, p1);
         }
+      const float dl = ratio_scale(evb - ev);
+      l[0] = fmaf(sum[0], dl, l[0]);
+      l[1] = fmaf(sum[1], dl, l[1]);
+      // O += P V: b0 holds keys 2c, 2c+1, b1 keys 2c+8, 2c+9 of a column
+      uint32_t v[4][D / 32];  // D / 8 bytes of each of the four keys
 #pragma unroll
-        for (int q = 0; q < NT; ++q) {
-          o[q][0] *= fac[0];
-          o[q][1] *= fac[0];
-          o[q][2] *= fac[1];
-          o[q][3] *= fac[1];
+      for (int i = 0; i < 4; ++i) {
+        const unsigned char* sv = st + vread + ((i & 1) + 8 * (i >> 1)) * D;
+        if (D == 128) {
+          const uint4 w4 = *reinterpret_cast<const uint4*>(sv);
+          v[i][0] = w4.x;
+          v[i][1] = w4.y;
+          v[i][D / 32 - 2] = w4.z;
+          v[i][D / 32 - 1] = w4.w;
+        } else {
+          const uint2 w2 = *reinterpret_cast<const uint2*>(sv);
+          v[i][0] = w2.x;
+          v[i][1] = w2.y;
         }
       }
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t a0, a1, c0, c1;
+          e4m3x4_to_f16x4(__byte_perm(v[0][u], v[1][u], hf ? 0x7362 : 0x5140), a0, a1);
+          e4m3x4_to_f16x4(__byte_perm(v[2][u], v[3][u], hf ? 0x7362 : 0x5140), c0, c1);
+          mma_f16(o[4 * u + 2 * hf], pa, a0, c0);
+          mma_f16(o[4 * u + 2 * hf + 1], pa, a1, c1);
+        }
+    }
+
+    // ---- tree nodes: the step's bf16 rows, each divided by its own power of two ----
+    const int f_end = f_first + (Tr - t_first);  // the tick behind the unit
+    for (; f < E && f < f_end; f += kTreeTicks) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kTreeTicks; ++i) issue(f + kRing - 1 + i);
+      const int nb = (t_first + (f - f_first) - Th) / kTreeTicks * kTile;  // first node of the tile
+      unsigned long long mask[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int rg = mt * kRowTile + g + 8 * i;
+        mask[i] = rg < M ? a.mask_bits[size_t(r) * a.n + rg / G] : 0ull;
+      }
+      const uint16_t* kn = static_cast<const uint16_t*>(a.k_new) + size_t(h) * D;
+      float s[2][4], kf[2][2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int node = nb + 8 * q + g;
+        const uint4* src = reinterpret_cast<const uint4*>(kn + (size_t(r) * a.n + (node < a.n ? node : 0)) * a.new_ld);
+        uint4 kx[D / 32];
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u)
+          kx[u] = node < a.n ? __ldg(src + (u >> 1) * 8 + 2 * c + (u & 1)) : make_uint4(0, 0, 0, 0);
+        uint32_t mx = 0;
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u)
+          mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, kx[u].x), kx[u].y), kx[u].z), kx[u].w);
+        mx = max(mx & 0xffffu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
+        mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
+        const int e = norm_exp(mx);
+        const float inv = exp_scale(2 * kExpBias - e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[q][i] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) {
+          const uint4& y = kx[kk >> 1];
+          mma_f16(s[q], qf[kk], scaled_f16(word_of(y, (kk & 1) * 2), inv), scaled_f16(word_of(y, (kk & 1) * 2 + 1), inv));
+        }
+        kf[q][0] = exp_scale(__shfl_sync(FULL, e, 8 * c));
+        kf[q][1] = exp_scale(__shfl_sync(FULL, e, 8 * c + 4));
+      }
+      auto vrow = [&](int node) {  // the thread's D / 8 elements of a node's V row
+        return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v_new) + size_t(h) * D +
+                                              (size_t(r) * a.n + (node < a.n ? node : 0)) * a.new_ld) + g * (D / 64);
+      };
+      // V's exponents; the rows themselves are read again for the product
+      int evk[4];  // of nodes 2c, 2c+1, 2c+8, 2c+9
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int node = nb + 2 * c + (i & 1) + 8 * (i >> 1);
+        const uint4* src = vrow(node);
+        uint32_t mx = 0;
+        bool nf = false;
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) {
+          const uint4 x = node < a.n ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+          nf = nf || nonfinite_bf16(x.x) || nonfinite_bf16(x.y) || nonfinite_bf16(x.z) || nonfinite_bf16(x.w);
+          mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, x.x), x.y), x.z), x.w);
+        }
+        mx = max(mx & 0xffffu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(FULL, mx, 4));
+        mx = max(mx, __shfl_xor_sync(FULL, mx, 8));
+        mx = max(mx, __shfl_xor_sync(FULL, mx, 16));
+        evk[i] = norm_exp(mx);
+        // an inf or a NaN must reach the rows that see the node and no
+        // other: it is left out of the product and added at the end
+        const unsigned who = __ballot_sync(FULL, nf);
+        if (who) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (who & (0x11111111u << q)) {
+              const int at = nb + 2 * q + (i & 1) + 8 * (i >> 1);
+              if (at < kMaxN) nonfinite |= 1ull << at;
+            }
+        }
+      }
+      if (evb < 0) {
+        evb = max(max(evk[0], evk[1]), max(evk[2], evk[3]));
+        evb = max(evb, __shfl_xor_sync(FULL, evb, 1));
+        evb = max(evb, __shfl_xor_sync(FULL, evb, 2));
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int node = nb + 8 * q + 2 * c + i;
+          const bool in = node < a.n;
+          const int d = evk[2 * q + i] - evb;
+          s[q][i] = in && ((mask[0] >> (node & 63)) & 1) ? fmaf(s[q][i], xf[0] * kf[q][i], float(d)) : -INFINITY;
+          s[q][2 + i] = in && ((mask[1] >> (node & 63)) & 1) ? fmaf(s[q][2 + i], xf[1] * kf[q][i], float(d)) : -INFINITY;
+        }
+      move(s);
       const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
       uint32_t pa[4];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const float p00 = fast_exp2(s[q][0] - m0), p01 = fast_exp2(s[q][1] - m0);
         const float p10 = fast_exp2(s[q][2] - m1), p11 = fast_exp2(s[q][3] - m1);
-        l[0] = fmaf(p00, dl[q][0], fmaf(p01, dl[q][1], l[0]));
-        l[1] = fmaf(p10, dl[q][0], fmaf(p11, dl[q][1], l[1]));
+        const float dl0 = ratio_scale(evb - evk[2 * q]), dl1 = ratio_scale(evb - evk[2 * q + 1]);
+        l[0] = fmaf(p00, dl0, fmaf(p01, dl1, l[0]));
+        l[1] = fmaf(p10, dl0, fmaf(p11, dl1, l[1]));
         pa[2 * q] = pack_f16(p00, p01);
         pa[2 * q + 1] = pack_f16(p10, p11);
       }
+      float inv[4];
 #pragma unroll
-      for (int q = 0; q < NT; ++q) mma_f16(o[q], pa, vb[q][0], vb[q][1]);
+      for (int i = 0; i < 4; ++i) inv[i] = exp_scale(2 * kExpBias - evk[i]);
+#pragma unroll
+      for (int u = 0; u < D / 64; ++u) {  // eight column tiles: element e of the thread's D / 8 is column tile e
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int node = nb + 2 * c + (i & 1) + 8 * (i >> 1);
+          x[i] = node < a.n ? __ldg(vrow(node) + u) : make_uint4(0, 0, 0, 0);
+        }
+        if (nonfinite) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = make_uint4(finite_bf16(x[i].x), finite_bf16(x[i].y), finite_bf16(x[i].z), finite_bf16(x[i].w));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          auto el = [&](int i) {
+            const uint32_t wd = word_of(x[i], e >> 1);
+            return ((e & 1) ? bf16_hi(wd) : bf16_lo(wd)) * inv[i];
+          };
+          mma_f16(o[8 * u + e], pa, pack_f16(el(0), el(1)), pack_f16(el(2), el(3)));
+        }
+      }
+    }
 
-      // ---- the unit's or the range's end ----
-      ++t;
-      const bool unit_end = t == Tr;
-      if (unit_end || f + 1 == E) {
-        // rows g, g + 8; columns c D/4 .. + D/4: [0, D/8) from fragment columns 2c, [D/8, D/4) from 2c + 1
-        float lt[2];
-        const float vs = exp_scale(evb < 1 ? 1 : evb);
+    // ---- the unit's or the range's end ----
+    const bool unit_end = f == f_end && f <= E;  // (past E: the last ticks are another warp's, which has nothing to add)
+    // rows g, g + 8; columns c D/4 .. + D/4: [0, D/8) from fragment columns 2c, [D/8, D/4) from 2c + 1
+    float lt[2];
+    const float vs = exp_scale(evb < 1 ? 1 : evb);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          lt[i] = l[i] + __shfl_xor_sync(FULL, l[i], 1);
-          lt[i] += __shfl_xor_sync(FULL, lt[i], 2);
+    for (int i = 0; i < 2; ++i) {
+      lt[i] = l[i] + __shfl_xor_sync(FULL, l[i], 1);
+      lt[i] += __shfl_xor_sync(FULL, lt[i], 2);
 #pragma unroll
-          for (int q = 0; q < NT; ++q) {
-            o[q][2 * i] *= vs;
-            o[q][2 * i + 1] *= vs;
-          }
-          if (nonfinite & mask[i])
-            for (int node = 0; node < a.n; ++node)
-              if ((nonfinite & mask[i]) >> node & 1) {
-                const uint16_t* src = static_cast<const uint16_t*>(a.v_new) + (size_t(r) * a.n + node) * a.new_ld +
-                                      size_t(h) * D + c * (D / 4);
+      for (int q = 0; q < NT; ++q) {
+        o[q][2 * i] *= vs;
+        o[q][2 * i + 1] *= vs;
+      }
+      if (nonfinite) {
+        const int rg = mt * kRowTile + g + 8 * i;
+        const unsigned long long seen = rg < M ? nonfinite & a.mask_bits[size_t(r) * a.n + rg / G] : 0ull;
+        for (int node = 0; node < a.n; ++node)
+          if (seen >> node & 1) {
+            const uint16_t* src = static_cast<const uint16_t*>(a.v_new) + (size_t(r) * a.n + node) * a.new_ld +
+                                  size_t(h) * D + c * (D / 4);
 #pragma unroll
-                for (int q = 0; q < NT; ++q)
+            for (int q = 0; q < NT; ++q)
 #pragma unroll
-                  for (int u = 0; u < 2; ++u) {
-                    const float v = __uint_as_float(uint32_t(src[u * NT + q]) << 16);
-                    if (!(fabsf(v) < INFINITY)) o[q][2 * i + u] += v;
-                  }
+              for (int u = 0; u < 2; ++u) {
+                const float v = __uint_as_float(uint32_t(src[u * NT + q]) << 16);
+                if (!(fabsf(v) < INFINITY)) o[q][2 * i + u] += v;
               }
-        }
-        if (unit_end && t_first == 0) {  // the whole unit
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int rg = mt * kRowTile + g + 8 * i;
-            if (rg < M) {
-              const size_t orow = (size_t(r) * a.n + rg / G) * a.Hq + h * G + rg % G;
-              const float inv = lt[i] > 0.f || lt[i] != lt[i] ? 1.f / lt[i] : 0.f;
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + c * (D / 4));
-#pragma unroll
-              for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int q = 0; q < NT; q += 8) {
-                  auto pk = [&](int e) { return pack_bf16x2(o[q + e][2 * i + u] * inv, o[q + e + 1][2 * i + u] * inv); };
-                  dst[(u * NT + q) / 8] = make_uint4(pk(0), pk(2), pk(4), pk(6));
-                }
-              if (c == 0 && a.lse) a.lse[orow] = lse_of(m[i], lt[i]);
-            }
           }
-        } else {
-          // a fragment: of a unit begun by an earlier warp (its own place), or one that goes on in a later one (the ring)
-          const int which = unit_end ? 0 : 1;
-          if (which == 1) {
-            cp_wait<0>();
-            __syncwarp();
-          }
-          float* fo = which == 0 ? ffrag : reinterpret_cast<float*>(mine);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float4* dst = reinterpret_cast<float4*>(fo + (g + 8 * i) * D + c * (D / 4));
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int q = 0; q < NT; q += 4)
-                dst[(u * NT + q) / 4] = make_float4(o[q][2 * i + u], o[q + 1][2 * i + u], o[q + 2][2 * i + u], o[q + 3][2 * i + u]);
-            if (c == 0) {
-              fml[(which * 16 + g + 8 * i) * 2] = m[i];
-              fml[(which * 16 + g + 8 * i) * 2 + 1] = lt[i];
-            }
-          }
-          if (lane == 0) desc[2 * w + which] = r * J + j;  // (below 2^31: a unit has at least one tile)
-        }
-        fresh = true;
-        if (unit_end) {
-          t = 0;
-          if (++j == J) {
-            j = 0;
-            ++r;
-            if (r < a.b) Tr = pre[r + 1] - pre[r];
-          }
-        }
       }
     }
-    cp_wait<0>();
-  }
-  __syncthreads();
-
-  // ---- join the fragments: thread -> row tid / 16, D / 16 columns ----
-  constexpr int CW = D / 16;  // 8 or 4 columns a thread
-  const int row = tid >> 4, col = (tid & 15) * CW;
-  int posted[2] = {-1, -1};  // units of this CTA that other CTAs share
-  long long pstart[2] = {0, 0};
-  int np = 0;
-  auto finish = [&](int unit, float Mx, float Ls, const float (&acc)[CW]) {
-    const int ur = unit / J, uj = unit - ur * J, uh = uj / args.m_tiles, um = uj - uh * args.m_tiles;
-    const int rg = um * kRowTile + row;
-    if (rg < M) {
-      const size_t orow = (size_t(ur) * a.n + rg / G) * a.Hq + uh * G + rg % G;
-      const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
-      uint32_t pk[CW / 2];
+    if (unit_end && t_first == 0) {  // the whole unit
 #pragma unroll
-      for (int e = 0; e < CW / 2; ++e) pk[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * D + col);
-      if (CW == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(pk[0], pk[1], pk[CW / 2 - 2], pk[CW / 2 - 1]);
-      else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
-      if (col == 0 && a.lse) a.lse[orow] = lse_of(Mx, Ls);
-    }
-  };
-  for (int i = 0; i < 2 * kWarps;) {
-    const int unit = desc[i];
-    if (unit < 0) {
-      ++i;
-      continue;
-    }
-    int e = i + 1;  // fragments [i, e) of this unit (in tile order; absent ones are -1)
-    while (e < 2 * kWarps && (desc[e] == unit || desc[e] < 0)) ++e;
-    float Mx = -INFINITY, Ls = 0.f, acc[CW];
+      for (int i = 0; i < 2; ++i) {
+        const int rg = mt * kRowTile + g + 8 * i;
+        if (rg < M) {
+          const size_t orow = (size_t(r) * a.n + rg / G) * a.Hq + h * G + rg % G;
+          const float inv = lt[i] > 0.f || lt[i] != lt[i] ? 1.f / lt[i] : 0.f;
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + c * (D / 4));
 #pragma unroll
-    for (int q = 0; q < CW; ++q) acc[q] = 0.f;
-    for (int x = i; x < e; ++x) {
-      if (desc[x] < 0) continue;
-      const unsigned char* base = smem + size_t(x >> 1) * L::kWarp;
-      const float* ml = reinterpret_cast<const float*>(base + kRing * L::kStage + L::kFrag) + ((x & 1) * 16 + row) * 2;
-      const float* fo = reinterpret_cast<const float*>(base + ((x & 1) ? 0 : kRing * L::kStage)) + row * D + col;
-      join<CW>(Mx, Ls, acc, ml[0], ml[1], fo);
-    }
-    const int ur = unit / J, uj = unit - ur * J, Tu = pre[ur + 1] - pre[ur];
-    const long long us = (long long)pre[ur] * J + (long long)uj * Tu;
-    const long long ca = warp_of(us) / wpc, cb = warp_of(us + Tu - 1) / wpc;
-    if (ca == cb) {
-      finish(unit, Mx, Ls, acc);
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int q = 0; q < NT; q += 8) {
+              auto pk = [&](int e) { return pack_bf16x2(o[q + e][2 * i + u] * inv, o[q + e + 1][2 * i + u] * inv); };
+              dst[(u * NT + q) / 8] = make_uint4(pk(0), pk(2), pk(4), pk(6));
+            }
+          if (c == 0 && a.lse) a.lse[orow] = lse_of(m[i], lt[i]);
+        }
+      }
     } else {
-      const int slot = 2 * int(blockIdx.x) + (ca < blockIdx.x ? 0 : 1);
-      float* so = args.slot_o + (size_t(slot) * kRowTile + row) * D + col;
-#pragma unroll
-      for (int q = 0; q < CW; q += 4) *reinterpret_cast<float4*>(so + q) = make_float4(acc[q], acc[q + 1], acc[q + 2], acc[q + 3]);
-      if (col == 0) {
-        args.slot_ml[(size_t(slot) * kRowTile + row) * 2] = Mx;
-        args.slot_ml[(size_t(slot) * kRowTile + row) * 2 + 1] = Ls;
+      // a fragment, as the registers hold it: word e of a lane is columns
+      // c D/4 + 4 (e % (D/16)) .. + 3 of row g + 8 (e / (D/16))
+      const size_t slot = size_t(2 * me) + (t_first == 0 ? 1 : 0);
+      if (solid) {
+        cp_wait<0>();
+        __syncwarp();
       }
-      posted[np] = unit;  // (the CTA's first and last unit at most)
-      pstart[np] = us;
-      ++np;
-    }
-    i = e;
-  }
-  __shared__ int s_last;
-  for (int x = 0; x < np; ++x) {
-    const int unit = posted[x], ur = unit / J, Tu = pre[ur + 1] - pre[ur];
-    const int ca = int(warp_of(pstart[x]) / wpc), cb = int(warp_of(pstart[x] + Tu - 1) / wpc);
-    __syncthreads();
-    if (tid == 0) s_last = atom_add_acq_rel(args.counters + ca) == uint32_t(cb - ca);
-    __syncthreads();
-    if (!s_last) continue;
-    float Mx = -INFINITY, Ls = 0.f, acc[CW];
+      float4* dst = (solid ? reinterpret_cast<float4*>(mine) : args.slot_o + slot * (32 * NT)) + lane;
 #pragma unroll
-    for (int q = 0; q < CW; ++q) acc[q] = 0.f;
-#pragma unroll 4
-    for (int q = ca; q <= cb; ++q) {
-      const int slot = 2 * q + (q == ca ? 1 : 0);
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(args.slot_ml) + size_t(slot) * kRowTile + row);
-      const float4* so = reinterpret_cast<const float4*>(args.slot_o + (size_t(slot) * kRowTile + row) * D + col);
-      float v[CW];
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int u = 0; u < CW / 4; ++u) {
-        const float4 y = __ldcg(so + u);
-        v[4 * u] = y.x;
-        v[4 * u + 1] = y.y;
-        v[4 * u + 2] = y.z;
-        v[4 * u + 3] = y.w;
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int q = 0; q < NT; q += 4)
+            dst[((i * 2 + u) * (NT / 4) + q / 4) * 32] = make_float4(o[q][2 * i + u], o[q + 1][2 * i + u], o[q + 2][2 * i + u], o[q + 3][2 * i + u]);
+      float2* ml = solid ? fml : args.slot_ml + slot * kRowTile;
+      if (c == 0) {
+        ml[g] = make_float2(m[0], lt[0]);
+        ml[g + 8] = make_float2(m[1], lt[1]);
       }
-      join<CW>(Mx, Ls, acc, ml.x, ml.y, v);
+      if (lane == 0 && t_first == 0) args.table[1 + me] = make_int4(int(((long long)f_end * NW - 1) / T), r, j, 0);
     }
-    finish(unit, Mx, Ls, acc);
-    if (tid == 0) atomicExch(args.counters + ca, 0u);
+    if (unit_end) {
+      t = 0;
+      if (++j == J) {
+        j = 0;
+        ++r;
+        if (r < a.b) Tr = pre[r + 1] - pre[r];
+      }
+    }
   }
+  cp_wait<0>();
+  if (!solid) return;
+  // ---- the CTA's fragments are all of one unit: joined here, so that few are left of a long context ----
+  __syncthreads();
+  for (int x = tid; x < 32 * NT; x += 32 * wpc) {
+    const int row = ((x & 31) >> 2) + 8 * (x / (16 * NT));
+    const float2* ml = reinterpret_cast<const float2*>(smem + L::kMl) + row;
+    float Mx = -INFINITY, Ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < wpc; ++q) {
+      const float4 y = reinterpret_cast<const float4*>(smem + size_t(q) * L::kWarp)[x];
+      const float v[4] = {y.x, y.y, y.z, y.w};
+      join<4>(Mx, Ls, acc, ml[q * kRowTile].x, ml[q * kRowTile].y, v);
+    }
+    args.slot_o[size_t(2 * me0) * (32 * NT) + x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if ((x & 3) == 0 && (x / 32) % (NT / 2) == 0) args.slot_ml[size_t(2 * me0) * kRowTile + row] = make_float2(Mx, Ls);
+  }
+}
+
+// Joins the units cut over warps: a block the unit that warp blockIdx.x begins and does not
+// finish; a thread one 16-byte word of the fragments' layout.
+template <int D>
+__global__ void __launch_bounds__(4 * D, 3) attention_q8_rows_join_kernel(const __grid_constant__ RowsArgs args) {
+  constexpr int NT = D / 8, kBatch4 = 4;
+  pdl_wait();
+  pdl_trigger();
+  const AttentionQ8Params& a = args.p;
+  const int4 head = __ldcg(args.table), unit = __ldcg(args.table + 1 + blockIdx.x);
+  if (int(blockIdx.x) >= head.x || unit.x < 0) return;  // (an entry behind the warps that ran is not looked at)
+  const Fragments fr(blockIdx.x, unit.x, head.y);
+  const int nf = fr.count(), r = unit.y, j = unit.z, h = j / args.m_tiles, mt = j - h * args.m_tiles;
+  const int G = a.Hq / a.Hkv, M = a.n * G, lane = threadIdx.x & 31, e = threadIdx.x >> 5;
+  const int row = (lane >> 2) + 8 * (e / (NT / 2)), rg = mt * kRowTile + row;
+  if (rg >= M) return;
+  float Mx = -INFINITY, Ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int i0 = 0; i0 < nf; i0 += kBatch4) {
+    float2 ml[kBatch4];
+    float4 o[kBatch4];
+#pragma unroll
+    for (int i = 0; i < kBatch4; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (i0 + i < nf) {
+        const int slot = 2 * fr.warp(i0 + i) + (i0 + i == 0 ? 1 : 0);
+        ml[i] = __ldcg(args.slot_ml + slot * kRowTile + row);
+        o[i] = __ldcg(args.slot_o + size_t(slot) * (32 * NT) + threadIdx.x);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch4; ++i) {
+      const float v[4] = {o[i].x, o[i].y, o[i].z, o[i].w};
+      join<4>(Mx, Ls, acc, ml[i].x, ml[i].y, v);
+    }
+  }
+  const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+  const size_t orow = (size_t(r) * a.n + rg / G) * a.Hq + h * G + rg % G;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + (lane & 3) * (D / 4) + 4 * (e % (NT / 2))) =
+      make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  if (a.lse && (lane & 3) == 0 && e % (NT / 2) == 0) a.lse[orow] = lse_of(Mx, Ls);
 }
 
 template <int D>
@@ -695,11 +737,17 @@ int launch_rows(const AttentionQ8Params& p, cudaStream_t stream) {
   const size_t smem = RowsSmem<D>::bytes(p.b);
   if (cudaFuncSetAttribute(attention_q8_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
     return SPEC_ERR_LAUNCH;
-  RowsArgs args{p, (p.n * (p.Hq / p.Hkv) + kRowTile - 1) / kRowTile, p.counters,
-                reinterpret_cast<float*>(p.partials + kQ8SlotMlBytes), reinterpret_cast<float*>(p.partials)};
+  RowsArgs args{p, (p.n * (p.Hq / p.Hkv) + kRowTile - 1) / kRowTile,
+                reinterpret_cast<int4*>(p.partials + kQ8SlotMlBytes - kQ8BegunBytes),
+                reinterpret_cast<float4*>(p.partials + kQ8SlotMlBytes), reinterpret_cast<float2*>(p.partials)};
   const int grid = sms < kQ8MaxCtas ? sms : kQ8MaxCtas;
-  const cudaError_t e = launch_pdl(attention_q8_rows_kernel<D>, dim3(grid), dim3(kQ8AttThreads), smem, stream, args);
-  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+  if (launch_pdl(attention_q8_rows_kernel<D>, dim3(grid), dim3(kQ8AttThreads), smem, stream, args) != cudaSuccess)
+    return SPEC_ERR_LAUNCH;
+  // (warps there can be at most: the second kernel's blocks beyond those that run leave at once)
+  const long long most = ((long long)(p.max_seq_len / kTile) + 1 + kTreeTicks * ((p.n + kTile - 1) / kTile)) * p.b * p.Hkv * args.m_tiles / kMinTicks + kWarps;
+  const int warps = most < grid * kWarps ? int(most) : grid * kWarps;
+  return launch_pdl(attention_q8_rows_join_kernel<D>, dim3(warps), dim3(4 * D), 0, stream, args) == cudaSuccess ? SPEC_OK
+                                                                                                           : SPEC_ERR_LAUNCH;
 }
 
 }  // namespace

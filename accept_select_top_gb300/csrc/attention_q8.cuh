@@ -11,8 +11,8 @@ constexpr float kLazyLog2 = 8.f;  // O is rescaled only when a row's maximum gro
 constexpr float kPBaseLog2 = 6.f; // P's row maximum when the reference is set: 2^6, so P <= 2^14 < 65504
 constexpr int kQ8MaxCtas = 192;   // upper bound of a grid of one CTA a SM; sizes the partial slots
 constexpr int kQ8SlotRows = 256;  // query rows of a slot at most
-// the partial area: (m, l) of each slot's rows, the table of units cut over CTAs, O of the slots
-constexpr size_t kQ8BegunBytes = size_t(kQ8MaxCtas) * 16;
+// the partial area: (m, l) of each slot's rows, the table of units cut over CTAs or warps, O of the slots
+constexpr size_t kQ8BegunBytes = (size_t(kQ8MaxCtas) * 12 + 16) * 16;
 constexpr size_t kQ8SlotMlBytes = size_t(2) * kQ8MaxCtas * kQ8SlotRows * 2 * 4 + kQ8BegunBytes;
 
 int launch_attention_q8_tc(const AttentionQ8Params& p, cudaStream_t stream);

@@ -33,6 +33,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(w)));
   return r;
 }
+// four e4m3 bytes to two f16x2 (one asm, so that the halves of w need no instructions of their own)
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 // two floats to e4m3 (nearest even; +-inf and anything past 448 saturates, NaN stays NaN); lo in the low byte
 __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
   uint16_t r;

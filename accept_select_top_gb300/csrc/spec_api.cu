@@ -909,8 +909,8 @@ int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size
     return SPEC_ERR_ARG;
   if ((D != 64 && D != 128) || (page_size != 16 && page_size != 32 && page_size != 64)) return SPEC_ERR_UNSUPPORTED;
   if (q_ld < int64_t(Hq) * D || q_ld % 8 || new_ld < int64_t(Hkv) * D || new_ld % 8) return SPEC_ERR_ARG;
-  // (page, kv head) units, output rows and 16-key tiles are counted in int32
-  const int64_t tiles = int64_t(max_seq_len) / 16 + 1 + (n + 15) / 16;
+  // (page, kv head) units, output rows and 16-key tiles (a tree's count eight times) are counted in int32
+  const int64_t tiles = int64_t(max_seq_len) / 16 + 1 + 8 * ((n + 15) / 16);
   if (num_pages * Hkv >= (int64_t(1) << 31) || int64_t(b) * n * Hq >= (int64_t(1) << 31) ||
       int64_t(row_pages) * page_size >= (int64_t(1) << 31) ||
       int64_t(b) * tiles * Hkv * ((int64_t(n) * (Hq / Hkv) + 15) / 16) >= (int64_t(1) << 31))
