@@ -20,7 +20,10 @@
 //   Chunks leave (M, s, t) and their k best; the CTA that arrives last of a
 // request joins the request's rows, one warp a row.
 //
-// Bound: the logits' bytes, read once.
+// Bound: the logits' bytes, read once, for many rows: 1024 fp32 rows of 129280 with 20
+// alternatives take 94 us (5.7 TB/s).  Few rows are latency: 32 requests' 224 rows of
+// 128256 bf16 logits, about half of them counting, 17.8 us, of which the selection, the
+// arrival and the join take some 8; four rows of 50257 8.3 us.
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -32,6 +35,7 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxBatches = 16;  // of a chunk: at most 131072 logits
 constexpr int kListCap = 512;    // batches read again, and logits ranked; more (long ties) take the slow path
+constexpr int kJoinCap = kListCap / kLpWarps;  // entries ranked when chunks are joined; more take the slow path
 constexpr size_t kLpPartBytes = 16 + size_t(kLogprobMaxK) * 8;
 
 struct LpArgs {
@@ -65,26 +69,35 @@ __device__ __forceinline__ float scale_of_row(const LogprobParams& a, long long 
   return T > 0.f ? 1.4426950408889634f / T : 1.4426950408889634f;
 }
 
+// A row's token and its logit, read before the row's statistics are there.
+struct LpToken {
+  int tok;
+  float x;
+};
+template <typename T>
+__device__ __forceinline__ LpToken token_of(const LogprobParams& a, int tok, long long idx) {
+  const bool on = idx >= 0 && tok >= 0 && tok < a.V;
+  return LpToken{tok, on ? LogitTraits<T>::load(static_cast<const T*>(a.logits) + idx * (long long)a.V, tok) : -INFINITY};
+}
+
 // Results of one row from its joined statistics and its k best (count of them
 // with a value above -inf, in order); one warp.
-template <typename T>
-__device__ void finish_row(const LogprobParams& a, int out_row, long long idx, float M, float s, float t,
+__device__ void finish_row(const LogprobParams& a, int out_row, LpToken token, float M, float s, float t,
                            float c, int count, const float* tv, int* ti) {
   const int lane = threadIdx.x & 31;
   const float ls = log2f(s);
-  const T* row = static_cast<const T*>(a.logits) + idx * (long long)a.V;
   auto logp = [&](float x) {
     return M == -INFINITY || !(x > -INFINITY) ? -INFINITY : ((x - M) * c - ls) * 0.6931471805599453f;
   };
   if (lane == 0) {
-    const int tok = a.tokens[out_row];
     float lp = 0.f;
-    if (tok >= a.V) raise_error(a.error, SPEC_DEV_INDEX);
-    else if (tok >= 0) lp = logp(LogitTraits<T>::load(row, tok));
+    if (token.tok >= a.V) raise_error(a.error, SPEC_DEV_INDEX);
+    else if (token.tok >= 0) lp = logp(token.x);
     a.logprobs[out_row] = lp;
     if (a.entropy) a.entropy[out_row] = M == -INFINITY ? 0.f : (ls - t / s) * 0.6931471805599453f;
   }
   if (a.k > 0) {
+    const float best = lane < count ? logp(tv[lane]) : -INFINITY;
     // fewer than k logits above -inf: the lowest other indices follow
     for (int base = 0; count < a.k && base < a.V; base += 32) {
       const int i = base + lane;
@@ -98,9 +111,8 @@ __device__ void finish_row(const LogprobParams& a, int out_row, long long idx, f
       __syncwarp();
     }
     if (lane < a.k) {
-      const int i = ti[lane];
-      a.top_ids[size_t(out_row) * a.k + lane] = i;
-      a.top_logprobs[size_t(out_row) * a.k + lane] = logp(LogitTraits<T>::load(row, i));
+      a.top_ids[size_t(out_row) * a.k + lane] = ti[lane];
+      a.top_logprobs[size_t(out_row) * a.k + lane] = best;
     }
   }
 }
@@ -117,8 +129,10 @@ __device__ void blank_row(const LogprobParams& a, int out_row) {
   }
 }
 
+// (four CTAs a SM for fp32: the compiler's own choice, five with 48 registers, keeps fewer loads
+// in flight, 103 against 94 us; for bf16 three with 72 registers, 17.8 against 19.6 us by four)
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(LpArgs args) {
+__global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 1) token_logprobs_kernel(LpArgs args) {
   constexpr int E = VecOps<T>::E, U = kBatch / E;
   const LogprobParams& a = args.p;
   __shared__ float bmax[kMaxBatches + 1][kLpThreads];
@@ -131,7 +145,8 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(LpArgs args)
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int out_row = blockIdx.x / args.chunks, ch = blockIdx.x % args.chunks, req = out_row / a.W;
+  // (the first row of every request, then the second: where only some count, those start together)
+  const int rw = blockIdx.x / args.chunks, ch = blockIdx.x % args.chunks, req = rw % a.b, out_row = req * a.W + rw / a.b;
   auto row_at = [&](int r, bool report) {
     long long i = a.row_index ? a.row_index[r] : (long long)(r / a.W) * a.n + r % a.W;
     if (i >= (long long)a.b * a.n) {
@@ -201,6 +216,8 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(LpArgs args)
         t = fmaf(y, p, t);
       }
     }
+    LpToken token{-1, 0.f};
+    if (args.chunks == 1 && tid == 0) token = token_of<T>(a, a.tokens[out_row], idx);
     // ---- the chunk's maximum and sums; the 32 group maxima ----
     gmax[w][lane] = m;
     __syncthreads();
@@ -318,10 +335,10 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(LpArgs args)
       __syncthreads();
     }
     if (args.chunks == 1) {
-      if (w == 0) finish_row<T>(a, out_row, idx, M, s, t, c, count, tv[0], ti[0]);
+      if (w == 0) finish_row(a, out_row, token, M, s, t, c, count, tv[0], ti[0]);
       return;
     }
-    unsigned char* part = a.partials + size_t(blockIdx.x) * kLpPartBytes;
+    unsigned char* part = a.partials + (size_t(out_row) * args.chunks + ch) * kLpPartBytes;
     if (tid == 0) *reinterpret_cast<LpPart*>(part) = LpPart{M, s, t, count};
     if (tid < count) reinterpret_cast<float2*>(part + 16)[tid] = make_float2(tv[0][tid], __int_as_float(ti[0][tid]));
   }
@@ -334,65 +351,100 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(LpArgs args)
       blank_row(a, orow);
       continue;
     }
+    const int tok = a.tokens[orow];
     const float cc = scale_of_row(a, ix);
-    const unsigned char* part = a.partials + (size_t(orow) * args.chunks + lane) * kLpPartBytes;
+    const unsigned char* parts = a.partials + size_t(orow) * args.chunks * kLpPartBytes;
+    const unsigned char* part = parts + lane * kLpPartBytes;
+    auto entry = [&](const unsigned char* p, int at) { return __ldcg(reinterpret_cast<const float2*>(p + 16) + at); };
+    const int all = args.chunks * a.k;
+    float4 h = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    float kth = 0.f;
+    if (lane < args.chunks) {
+      h = __ldcg(reinterpret_cast<const float4*>(part));
+      if (a.k > 0) kth = entry(part, a.k - 1).x;
+    }
+    const LpToken token = token_of<T>(a, tok, ix);
     float pM = -INFINITY, ps = 0.f, pt = 0.f;
     int pc = 0;
+    float theta = -INFINITY;  // at least k logits reach it: the largest of the chunks' k-th best
     if (lane < args.chunks) {
-      const float4 h = __ldcg(reinterpret_cast<const float4*>(part));
       pM = h.x;
       ps = h.y;
       pt = h.z;
       pc = __float_as_int(h.w);
+      if (pc == a.k) theta = kth;  // (else it was not written)
     }
     const float jM = warp_max(pM);
     const float d = fmaxf((pM - jM) * cc, -150.f), f = fast_exp2(d);
     const float js = warp_sum(ps > 0.f ? f * ps : 0.f), jt = warp_sum(ps > 0.f ? f * fmaf(d, ps, pt) : 0.f);
-    int got = 0, head = 0;
+    int got = 0;
     if (a.k > 0) {
-      // the chunks' sorted lists: k times the best head
-      auto fetch = [&](int at, float& v, int& i) {
-        v = -INFINITY;
-        i = INT_MAX;
-        if (at < pc) {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(part + 16) + at);
-          v = x.x;
-          i = __float_as_int(x.y);
+      theta = warp_max(theta);
+      // the entries that reach theta, ranked by counting
+      float* qv = cv + w * kJoinCap;
+      int* qi = ci + w * kJoinCap;
+      int nc = 0;
+#pragma unroll 4
+      for (int base = 0; base < all; base += 32) {
+        const int p = base + lane, pch = min(p / a.k, args.chunks - 1), at = p - pch * a.k;
+        const int cnt = __shfl_sync(0xffffffffu, pc, pch);
+        float2 x = make_float2(-INFINITY, 0.f);
+        if (at < cnt) x = entry(parts + pch * kLpPartBytes, at);
+        const bool in = at < cnt && x.x >= theta;
+        const unsigned who = __ballot_sync(0xffffffffu, in);
+        const int to = nc + __popc(who & ((1u << lane) - 1u));
+        if (in && to < kJoinCap) {
+          qv[to] = x.x;
+          qi[to] = __float_as_int(x.y);
         }
-      };
-      float hv, nv;
-      int hi, ni;
-      fetch(0, hv, hi);
-      fetch(1, nv, ni);
-      for (; got < a.k; ++got) {
-        float bv = hv;
-        int bi = hi;
-        warp_argmax(bv, bi);
-        if (bi == INT_MAX || !(bv > -INFINITY)) break;
-        if (lane == 0) {
-          tv[w][got] = bv;
-          ti[w][got] = bi;
+        nc += __popc(who);
+      }
+      __syncwarp();
+      if (nc <= kJoinCap) {
+        got = min(a.k, nc);
+        for (int i = lane; i < nc; i += 32) {
+          int rank = 0;
+          for (int q = 0; q < nc; ++q) rank += better(qv[q], qi[q], qv[i], qi[i]);
+          if (rank < a.k) {
+            tv[w][rank] = qv[i];
+            ti[w][rank] = qi[i];
+          }
         }
-        if (hi == bi) {
-          hv = nv;
-          hi = ni;
-          ++head;
-          fetch(head + 1, nv, ni);
+      } else {
+        // long ties: the chunks' sorted lists, k times the best head
+        int head = 0;
+        for (; got < a.k; ++got) {
+          float bv = -INFINITY;
+          int bi = INT_MAX;
+          if (head < pc) {
+            const float2 x = entry(part, head);
+            bv = x.x;
+            bi = __float_as_int(x.y);
+          }
+          const int hi = bi;
+          warp_argmax(bv, bi);
+          if (bi == INT_MAX || !(bv > -INFINITY)) break;
+          if (lane == 0) {
+            tv[w][got] = bv;
+            ti[w][got] = bi;
+          }
+          if (hi == bi) ++head;
         }
       }
       __syncwarp();
     }
-    finish_row<T>(a, orow, ix, jM, js, jt, cc, got, tv[w], ti[w]);
+    finish_row(a, orow, token, jM, js, jt, cc, got, tv[w], ti[w]);
     __syncwarp();
   }
   __syncthreads();
   counter_reset(a.counters + req);
 }
 
-// Chunks of a row: about six CTAs a SM in all, at least 2048 logits and at most
+// Chunks of a row: about four CTAs a SM in all (each chunk ends in some 4 us of selection and
+// arrival: the 224 rows below took 17.8 us so, 20.3 by five and 23.1 by six), at least 2048 logits and at most
 // kMaxBatches batches a chunk.
 int lp_chunks(long rows, int V) {
-  long want = (6 * 152 + rows - 1) / rows;
+  long want = (4 * 152 + rows - 1) / rows;
   const long by_size = V / 2048 > 1 ? V / 2048 : 1;
   if (want > by_size) want = by_size;
   if (want > kMaxChunks) want = kMaxChunks;
