@@ -386,6 +386,15 @@ class LayerList:
         self.first = t0
         self.array = (ctypes.c_void_p * len(self.tensors))(*[t.data_ptr() for t in self.tensors])
         self.ptr = ctypes.addressof(self.array)
+        self.rows = t0.shape[0] if t0.dim() else 0
+        self._checked = {}
+
+    def check(self, fn, *args):
+        """fn(first layer, *args), once for each args: addresses and layouts are those of the list's making."""
+        got = self._checked.get(args)
+        if got is None:
+            got = self._checked[args] = fn(self.first, *args)
+        return got
 
     def __len__(self):
         return len(self.tensors)
@@ -431,18 +440,18 @@ def spec_commit_kv_q8(b: int, Hkv: int, D: int, page_size: int, k_new, v_new, k_
     layers = len(k_new)
     if not all(len(x) == layers for x in (v_new, k_pages, v_pages, k_scales, v_scales)):
         raise SpecError("every layer list must have the same length")
-    num_rows, num_pages = k_new.first.shape[0], k_pages.first.shape[0]
-    _, ld = _rows_in(k_new.first, Hkv, D, 1, dev, "k_new")
-    _, ldv = _rows_in(v_new.first, Hkv, D, num_rows, dev, "v_new")
+    num_rows, num_pages = k_new.rows, k_pages.rows
+    _, ld = k_new.check(_rows_in, Hkv, D, 1, dev, "k_new")
+    _, ldv = v_new.check(_rows_in, Hkv, D, num_rows, dev, "v_new")
     if ldv != ld:
         raise SpecError("k_new and v_new must have one row stride")
     shape = (Hkv, page_size, D)
-    _pages_in(k_pages.first, shape, dev, "k_pages")
-    _pages_in(v_pages.first, shape, dev, "v_pages")
-    if v_pages.first.shape[0] != num_pages:
+    k_pages.check(_pages_in, shape, dev, "k_pages")
+    v_pages.check(_pages_in, shape, dev, "v_pages")
+    if v_pages.rows != num_pages:
         raise SpecError("k_pages and v_pages must have as many pages")
-    _in(k_scales.first, torch.uint8, num_pages * Hkv, dev, "k_scales")
-    _in(v_scales.first, torch.uint8, num_pages * Hkv, dev, "v_scales")
+    k_scales.check(_in, torch.uint8, num_pages * Hkv, dev, "k_scales")
+    v_scales.check(_in, torch.uint8, num_pages * Hkv, dev, "v_scales")
     rows, row_pages = page_table.shape
     _check(LIB.spec_commit_kv_q8(
         b, Hkv, D, page_size, layers, k_new.ptr, v_new.ptr, num_rows, ld, k_pages.ptr, v_pages.ptr, k_scales.ptr,
