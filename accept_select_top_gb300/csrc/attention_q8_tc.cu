@@ -58,11 +58,12 @@ __host__ __device__ constexpr uint32_t col_s(int w, int b) { return 256u + 128u 
 
 // What the softmax needs of a tile: of a history tile, for each group of 16
 // keys, {K scale, V exponent relative to the unit's base, its inverse factor in
-// l, keys that count}; of the tree tile, each node's K and V exponent byte.
+// l, keys that count}; of the tree tile, each node's K and V exponent
+// bytes, as the halves that hold 2^(K's - 127) and float(V's) in bf16.
 struct TileMeta {
   union {
     float4 group[kGroups];
-    uint16_t node[kTreeKeys];
+    uint32_t node[kTreeKeys];
   };
   unsigned long long nonfinite[4];  // tree nodes whose V row holds an inf or a NaN, a word a converter warp
   int base;                         // the unit's V exponent base
@@ -597,8 +598,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         const bool swap = ch >= 4;
         const uint32_t a0 = swap ? x[i].z : x[i].x, a1 = swap ? x[i].w : x[i].y, b0 = swap ? x[i].x : x[i].z, b1 = swap ? x[i].y : x[i].w;
         const uint32_t at = row + (((c0 + (swap ? 1u : 0u)) ^ uint32_t(key & 7)) << 4);
-        sts16(at, make_uint4(e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(a1 >> 16)));
-        sts16(at ^ 16u, make_uint4(e4m3x2_to_f16x2(b0), e4m3x2_to_f16x2(b0 >> 16), e4m3x2_to_f16x2(b1), e4m3x2_to_f16x2(b1 >> 16)));
+        auto put = [&](uint32_t to, uint32_t w0, uint32_t w1) {
+          uint4 y;
+          e4m3x4_to_f16x4(w0, y.x, y.y);
+          e4m3x4_to_f16x4(w1, y.z, y.w);
+          sts16(to, y);
+        };
+        put(at, a0, a1);
+        put(at ^ 16u, b0, b1);
       }
     };
     auto row_exp = [&](const uint4& x) {  // exponent byte of a tree row's power of two, from its lanes
@@ -675,7 +682,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
           uint4 x = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
           if (key >= a.n) x = make_uint4(0u, 0u, 0u, 0u);
           const int e = row_exp(x);
-          if (ct_id % kLanesRow == 0) reinterpret_cast<uint8_t*>(&mt.node[key])[kv] = uint8_t(e);
+          if (ct_id % kLanesRow == 0) reinterpret_cast<uint16_t*>(&mt.node[key])[kv] = uint16_t(kv == 0 ? uint32_t(e) << 7 : __float_as_uint(float(e)) >> 16);
           if (kv == 1) {
             const unsigned who = __ballot_sync(FULL, nonfinite_bf16(x.x) || nonfinite_bf16(x.y) || nonfinite_bf16(x.z) || nonfinite_bf16(x.w));
 #pragma unroll 1
@@ -745,7 +752,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       const int node = valid ? rg / G : 0, head = h * G + (valid ? rg % G : 0);
       const bool mine = first < n;
       float m = -INFINITY, l = 0.f, xf = 0.f;
-      const unsigned long long mask = valid ? a.mask_bits[size_t(p.r) * a.n + node] : 0ull;
+      const unsigned long long mask = valid ? a.mask_bits[size_t(p.r) * a.n + node] & (~0ull >> (kTreeKeys - a.n)) : 0ull;
       unsigned long long nonfinite = 0;
       int base = kExpBias;
       Pos pn = p;  // the next piece's position
@@ -888,32 +895,46 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
             break;
           }
           nonfinite = mt.nonfinite[0] | mt.nonfinite[1] | mt.nonfinite[2] | mt.nonfinite[3];
-          auto score = [&](uint32_t v, int k) {  // x + e of node k
-            const int e = mt.node[k];
-            return k < a.n && ((mask >> k) & 1ull) ? fmaf(__uint_as_float(v), xf * exp_scale(e & 255), float((e >> 8) - base)) : -INFINITY;
+          const float b0 = float(base);
+          // x + e - against of node k, from its word; chunk: the mask's bits from the chunk's first node on
+          auto score = [&](uint32_t v, uint32_t word, uint32_t chunk, int i, float against) {
+            const float x = fmaf(__uint_as_float(v), xf * bf16_lo(word), bf16_hi(word) - against);
+            return chunk & (1u << i) ? x : -INFINITY;
           };
           float mx = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < kTreeKeys / 16; ++c) {
             uint32_t v[16];
             tmem_ld16(ts + 16 * c, v);
+            const uint32_t bits = uint32_t(mask >> (16 * c));
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, score(v[i], 16 * c + i));
+            for (int q = 0; q < 4; ++q) {
+              const uint4 wd = *reinterpret_cast<const uint4*>(mt.node + 16 * c + 4 * q);
+              mx = fmaxf(mx, fmaxf(score(v[4 * q], wd.x, bits, 4 * q, b0), score(v[4 * q + 1], wd.y, bits, 4 * q + 1, b0)));
+              mx = fmaxf(mx, fmaxf(score(v[4 * q + 2], wd.z, bits, 4 * q + 2, b0), score(v[4 * q + 3], wd.w, bits, 4 * q + 3, b0)));
+            }
           }
           if (__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2))) ok = move(mx, cs > cs0);
-          const float mr = m == -INFINITY ? 0.f : m;
+          const float bm = b0 + (m == -INFINITY ? 0.f : m);  // (whole numbers)
 #pragma unroll 1
           for (int c = 0; ok && c < kTreeKeys / 16; ++c) {
             uint32_t v[16], pk[8];
             tmem_ld16(ts + 16 * c, v);
+            const uint32_t bits = uint32_t(mask >> (16 * c));
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int k = 16 * c + 2 * i;
-              const float q0 = fast_exp2(score(v[2 * i], k) - mr), q1 = fast_exp2(score(v[2 * i + 1], k + 1) - mr);
-              l = fmaf(q0, ratio_scale(base - (mt.node[k] >> 8)), fmaf(q1, ratio_scale(base - (mt.node[k + 1] >> 8)), l));
-              pk[i] = pack_f16(q0, q1);
+            for (int q = 0; q < 4; ++q) {
+              const uint4 wd = *reinterpret_cast<const uint4*>(mt.node + 16 * c + 4 * q);
+              auto p_of = [&](uint32_t vv, uint32_t word, int i) {
+                const float y = fast_exp2(score(vv, word, bits, i, bm));
+                l = fmaf(y, fast_exp2(fminf(b0 - bf16_hi(word), 126.f)), l);
+                return y;
+              };
+              const float q0 = p_of(v[4 * q], wd.x, 4 * q), q1 = p_of(v[4 * q + 1], wd.y, 4 * q + 1);
+              const float q2 = p_of(v[4 * q + 2], wd.z, 4 * q + 2), q3 = p_of(v[4 * q + 3], wd.w, 4 * q + 3);
+              pk[2 * q] = pack_f16(q0, q1);
+              pk[2 * q + 1] = pack_f16(q2, q3);
             }
             tmem_st8(ts + 8 * c, pk);
           }
