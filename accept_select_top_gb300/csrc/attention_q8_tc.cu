@@ -442,17 +442,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     for (int f = S; ok && f < E; ++piece) {
       const int n = piece_tiles(p, f);
       const bool split = unit_rows(p.j) <= kRows;
-      const int tree_at = p.t + n == p.Tr ? n - 1 : n, stride = split ? 2 : 1, first = split ? w : 0;
-      for (int t = first, hf = 0; t < n;) {
+      const int tree_at = p.t + n == p.Tr ? n - 1 : n, first = split ? w : 0;
+      // (every piece's and every tile's barrier is waited for, read or not: a phase that is
+      // let pass makes the next one's parity the wrong one)
+      ok = __all_sync(FULL, pv ? piece == 0 || wait(kOFree0 + w, (piece - 1) & 1) : wait(kQFull0 + w, piece & 1)) != 0;
+      for (int t = 0, hf = 0; ok && t < n;) {
         const int ct = ct0 + t, buf = ct & 1, sb = 2 * w + (cs & 1), ph = (cs >> 1) & 1;
+        if (split && (t & 1) != w) {  // the other group's tile
+          ok = wait(full0 + buf, (ct >> 1) & 1);
+          if (!__all_sync(FULL, ok && !*abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (elect_one()) mbar_arrive(bar(empty0 + buf));
+          __syncwarp();
+          ++t;
+          continue;
+        }
         const bool last = hf == 1 || t == tree_at, begin = t == first && hf == 0;
         const uint32_t ts = ut + col_s(w, cs & 1);
         const uint32_t dt = db + uint32_t(buf) * (L::kTile >> 4) + uint32_t(hf) * (kStep * 128 >> 4);
         ok = hf == 1 || wait(full0 + buf, (ct >> 1) & 1);
         if (!pv) {
-          ok = ok && (!begin || wait(kQFull0 + w, piece & 1)) && (cs < 2 || wait(kPvDone0 + sb, ph ^ 1));
+          ok = ok && (cs < 2 || wait(kPvDone0 + sb, ph ^ 1));
+          // (the tree tile is one step, so its S alone does not tell that the softmax is through with the
+          // group's tile before, whose place in the ring of metas the converters take once it is read)
+          if (split && t == tree_at && cs > 0) ok = ok && wait(kPvDone0 + 2 * w + ((cs - 1) & 1), ((cs - 1) >> 1) & 1);
         } else {
-          ok = ok && (!begin || piece == 0 || wait(kOFree0 + w, (piece - 1) & 1)) && wait(kPReady0 + sb, ph);
+          ok = ok && wait(kPReady0 + sb, ph);
         }
         if (!__all_sync(FULL, ok && !*abort_flag)) {
           ok = false;
@@ -473,15 +490,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
               mma_ts(ut + col_o(w), ts + kk * 8, desc(dt + uint32_t((kk * 16 * 128) >> 4)), idesc_f16(D, true), !begin || kk > 0 ? 1u : 0u);
             mma_commit(bar(kPvDone0 + sb));
           }
-          if (last) {
-            mma_commit(bar(empty0 + buf));
-            if (split) mma_commit(bar(empty0 + buf));  // the other group does not read this tile
-          }
+          if (last) mma_commit(bar(empty0 + buf));
         }
         __syncwarp();
         ++cs;
         hf = last ? 0 : 1;
-        t += last ? stride : 0;
+        t += last ? 1 : 0;
       }
       ct0 += n;
       f += n;
