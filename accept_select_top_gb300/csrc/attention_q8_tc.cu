@@ -438,14 +438,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     bool ok = true;
     auto wait = [&](int b, int parity) { return mbar_wait(bar(b), uint32_t(parity), abort_flag); };
     Pos p = start;
-    int ct0 = 0, piece = 0, cs = 0;  // cs: steps issued
-    for (int f = S; ok && f < E; ++piece) {
+    int ct0 = 0, own = 0, cs = 0;  // pieces in which the group has a tile; steps issued
+    for (int f = S; ok && f < E;) {
       const int n = piece_tiles(p, f);
       const bool split = unit_rows(p.j) <= kRows;
       const int tree_at = p.t + n == p.Tr ? n - 1 : n, first = split ? w : 0;
-      // (every piece's and every tile's barrier is waited for, read or not: a phase that is
-      // let pass makes the next one's parity the wrong one)
-      ok = __all_sync(FULL, pv ? piece == 0 || wait(kOFree0 + w, (piece - 1) & 1) : wait(kQFull0 + w, piece & 1)) != 0;
+      // Q and O have a phase for each piece in which the group has a tile, K and V one
+      // for each tile, read or not: a phase let pass makes the next one's parity the wrong one.
+      // Before S goes on to another piece, P V has to be through with the last: the softmax
+      // then reads no more of its tiles' metas, whose places the converters take.
+      if (!pv) ok = cs == 0 || wait(kPvDone0 + 2 * w + ((cs - 1) & 1), ((cs - 1) >> 1) & 1);
+      if (first < n) {
+        ok = ok && (pv ? own == 0 || wait(kOFree0 + w, (own - 1) & 1) : wait(kQFull0 + w, own & 1));
+        ++own;
+      }
+      ok = __all_sync(FULL, ok) != 0;
       for (int t = 0, hf = 0; ok && t < n;) {
         const int ct = ct0 + t, buf = ct & 1, sb = 2 * w + (cs & 1), ph = (cs >> 1) & 1;
         if (split && (t & 1) != w) {  // the other group's tile
@@ -689,22 +696,38 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       } else {
         ok = ct < 2 || wait(empty0 + buf, ((ct >> 1) - 1) & 1);
         if (!ok) break;
+        constexpr int kAtOnce = 4;  // (eight take more registers than there are)
         unsigned long long nf = 0;
 #pragma unroll 1
-        for (int i = 0; i < kTreeLoads; ++i) {
-          const int key = tree_key(i);
-          uint4 x = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
-          if (key >= a.n) x = make_uint4(0u, 0u, 0u, 0u);
-          const int e = row_exp(x);
-          if (ct_id % kLanesRow == 0) reinterpret_cast<uint16_t*>(&mt.node[key])[kv] = uint16_t(kv == 0 ? uint32_t(e) << 7 : __float_as_uint(float(e)) >> 16);
-          if (kv == 1) {
-            const unsigned who = __ballot_sync(FULL, nonfinite_bf16(x.x) || nonfinite_bf16(x.y) || nonfinite_bf16(x.z) || nonfinite_bf16(x.w));
-#pragma unroll 1
-            for (int q = 0; q < 32 / kLanesRow; ++q)
-              if ((who >> (q * kLanesRow)) & ((1u << kLanesRow) - 1u))
-                nf |= 1ull << (i * kRowsLoad + cw * (32 / kLanesRow) + q);
+        for (int i0 = 0; i0 < kTreeLoads; i0 += kAtOnce) {
+          uint4 x[kAtOnce];
+          bool odd = false;
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const int key = tree_key(i0 + i);
+            x[i] = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
+            if (key >= a.n) x[i] = make_uint4(0u, 0u, 0u, 0u);
           }
-          store_tree(tile, x, key, e, kv == 1);
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const int key = tree_key(i0 + i), e = row_exp(x[i]);
+            if (ct_id % kLanesRow == 0) reinterpret_cast<uint16_t*>(&mt.node[key])[kv] = uint16_t(kv == 0 ? uint32_t(e) << 7 : __float_as_uint(float(e)) >> 16);
+            odd = odd || nonfinite_bf16(x[i].x) || nonfinite_bf16(x[i].y) || nonfinite_bf16(x[i].z) || nonfinite_bf16(x[i].w);
+            store_tree(tile, x[i], key, e, kv == 1);
+          }
+          if (kv == 1 && __any_sync(FULL, odd)) {  // (the words are read again: few rows hold such)
+#pragma unroll 1
+            for (int i = 0; i < kAtOnce; ++i) {
+              const int key = tree_key(i0 + i);
+              const uint4 y = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
+              const bool bad = key < a.n && (nonfinite_bf16(y.x) || nonfinite_bf16(y.y) || nonfinite_bf16(y.z) || nonfinite_bf16(y.w));
+              const unsigned who = __ballot_sync(FULL, bad);
+#pragma unroll 1
+              for (int q = 0; q < 32 / kLanesRow; ++q)
+                if ((who >> (q * kLanesRow)) & ((1u << kLanesRow) - 1u))
+                  nf |= 1ull << ((i0 + i) * kRowsLoad + cw * (32 / kLanesRow) + q);
+            }
+          }
         }
         if (kv == 1 && lane == 0) mt.nonfinite[cw] = nf;
         mbar_arrive(bar(kRawEmpty0 + kv));
@@ -728,7 +751,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t to = tl + col_o(w);
     Pos p = start;
-    int piece = 0, cs = 0, nfrag = 0, ct0 = 0;
+    int cs = 0, nfrag = 0, ct0 = 0;
     bool ok = true;
     // row of the thread (and of its warp's others) in a unit: among the kv head's n * G
     auto row_of = [&](const Pos& q, int rr) {
@@ -753,51 +776,185 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         for (hq += kRowsOp; hq >= G; hq -= G) ++tok;
       }
     };
-    if (S < E) ask_q(p);
-    if (tid == 0) args.begun[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    for (int f = S; ok && f < E; ++piece) {
-      const int n = piece_tiles(p, f);
-      const int rows = unit_rows(p.j);
-      const bool split = rows <= kRows, complete = p.t == 0 && n == p.Tr;
-      const int stride = split ? 2 : 1, first = split ? w : 0;
-      const int h = p.j / args.blocks;
-      const int rg = row_of(p, r);
-      const bool valid = rg < M;
-      const int node = valid ? rg / G : 0, head = h * G + (valid ? rg % G : 0);
-      const bool mine = first < n;
-      float m = -INFINITY, l = 0.f, xf = 0.f;
-      const unsigned long long mask = valid ? a.mask_bits[size_t(p.r) * a.n + node] & (~0ull >> (kTreeKeys - a.n)) : 0ull;
-      unsigned long long nonfinite = 0;
-      int base = kExpBias;
-      Pos pn = p;  // the next piece's position
-      pn.t += n - 1;
-      if (f + n < E) advance(pn);
-      {
-        // ---- the row of Q, divided by its power of two, as f16 ----
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncwarp();
-        const uint32_t qrow = qtile + uint32_t(r) * 128u;
-        auto chunk = [&](int i) { return qrow + uint32_t(i >> 3) * L::kBlock + ((uint32_t(i & 7) ^ uint32_t(r & 7)) << 4); };
-        uint32_t mx = 0;
-#pragma unroll 4
+    // A piece's row of Q, divided by its power of two, as f16.
+    float xf_next = 0.f;
+    auto normalise_q = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      const uint32_t qrow = qtile + uint32_t(r) * 128u;
+      auto chunk = [&](int i) { return qrow + uint32_t(i >> 3) * L::kBlock + ((uint32_t(i & 7) ^ uint32_t(r & 7)) << 4); };
+      uint32_t mx = 0;
+#pragma unroll 8
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = lds16(chunk(i));
+        mx = __vmaxu2(__vmaxu2(__vmaxu2(__vmaxu2(mx, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu), x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
+      }
+      if (max(mx & 0xffffu, mx >> 16) >= 0x7f80u) {  // an inf or a NaN: the largest of the others
+        mx = 0;
+#pragma unroll 1
         for (int i = 0; i < D / 8; ++i) {
           const uint4 x = lds16(chunk(i));
           mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, x.x), x.y), x.z), x.w);
         }
-        const int e = norm_exp(max(mx & 0xffffu, mx >> 16));
-        // the sign of the scale goes into Q, so that a larger score is a larger exponent
-        const float inv = copysignf(exp_scale(2 * kExpBias - e), a.scale);
-        xf = fabsf(a.scale) * 1.4426950408889634f * exp_scale(e);
-        auto cv = [&](uint32_t u) { return pack_f16(bf16_lo(u) * inv, bf16_hi(u) * inv); };
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = lds16(chunk(i));
-          sts16(chunk(i), make_uint4(cv(x.x), cv(x.y), cv(x.z), cv(x.w)));
-        }
-        fence_async();
       }
+      const int e = norm_exp(max(mx & 0xffffu, mx >> 16));
+      // the sign of the scale goes into Q, so that a larger score is a larger exponent
+      const float inv = copysignf(exp_scale(2 * kExpBias - e), a.scale);
+      xf_next = fabsf(a.scale) * 1.4426950408889634f * exp_scale(e);
+      auto cv = [&](uint32_t u) { return pack_f16(bf16_lo(u) * inv, bf16_hi(u) * inv); };
+#pragma unroll 8
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = lds16(chunk(i));
+        sts16(chunk(i), make_uint4(cv(x.x), cv(x.y), cv(x.z), cv(x.w)));
+      }
+      fence_async();
       mbar_arrive(bar(kQFull0 + w));
-      if (!mine && f + n < E) ask_q(pn);  // (no product reads it)
+    };
+    auto has_tile = [&](const Pos& q, int f) { return unit_rows(q.j) > kRows || w < piece_tiles(q, f); };  // (the groups take tiles in turn, or all)
+    if (S < E && has_tile(p, S)) ask_q(p);
+    if (tid == 0) args.begun[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    // the piece at hand: tiles [f, f + n) of the range, from position p, and the next one's position
+    Pos pn = start;
+    int n = 0, node = 0, head = 0, h = 0, base = kExpBias;
+    bool split = false, complete = false, mine = false, valid = false;
+    float m = -INFINITY, l = 0.f;
+    unsigned long long mask = 0, nonfinite = 0;
+    for (int f = S;;) {
+      // The next piece's Q comes before this one's result, so that its first scores are
+      // computed while the result is written.
+      const bool more = f + n < E;
+      const bool next = more && has_tile(pn, f + n);
+      if (next) normalise_q();
+      if (n > 0) {
+        // ---- the piece's result ----
+        if (mine) {
+          const bool d_ok = mbar_wait(bar(kPvDone0 + 2 * w + ((cs - 1) & 1)), ((cs - 1) >> 1) & 1, abort_flag) && !*abort_flag;
+          if (!__all_sync(FULL, d_ok)) {
+            ok = false;
+            break;
+          }
+          tc_after();
+        }
+        const float vs = exp_scale(base < 1 ? 1 : base);
+        const bool direct = complete && !split;
+        const int slot = 2 * int(blockIdx.x) + (complete || p.t == 0 ? 1 : 0);  // (0: a unit that an earlier CTA began)
+        const bool local = complete && split;
+        // a slot's O: 16-byte words [4 columns][row], so that a warp stores 512 contiguous bytes
+        float4* so = reinterpret_cast<float4*>(args.slot_o) + (size_t(slot) * 2 + w) * kRows * (D / 4) + r;
+        float2* sm = reinterpret_cast<float2*>(args.slot_ml) + (size_t(slot) * 2 + w) * kRows + r;
+        const size_t orow = (size_t(p.r) * a.n + node) * a.Hq + head;
+        float om = -INFINITY, ol = 0.f;  // group 1's half of a unit that group 0 finishes
+        // (group 0 may not have read the last half that group 1 left in the slot)
+        if (!direct && w == 1 && nfrag > 0 && !__all_sync(FULL, mbar_wait(bar(kFragFree), (nfrag - 1) & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        if (local) {
+          if (w == 0) {
+            if (!__all_sync(FULL, mbar_wait(bar(kFragFull), nfrag & 1, abort_flag))) {
+              ok = false;
+              break;
+            }
+            const float2 x = __ldcg(sm + kRows);
+            om = x.x;
+            ol = x.y;
+          }
+          ++nfrag;
+        }
+        const unsigned long long nf = nonfinite & mask;
+        const bool any_nf = __any_sync(FULL, nf != 0ull);
+        // out = (O 2^base [+ the other half, both relative to the larger reference]) / l
+        const bool has_o = ol > 0.f || ol != ol;
+        const float M2 = has_o ? fmaxf(m, om) : m;
+        const float wa = has_o && m != M2 ? fast_exp2(m - M2) : 1.f, wb = has_o ? fast_exp2(om - M2) : 0.f;
+        const float Ls = has_o ? l * wa + ol * wb : l;
+        const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          float v[16];
+          if (mine) {
+            uint32_t o[16];
+            tmem_ld16(to + 16 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * vs;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = 0.f;
+          }
+          if (any_nf && nf) {
+            for (int q = 0; q < a.n; ++q)
+              if ((nf >> q) & 1ull) {
+                const uint16_t* vr = static_cast<const uint16_t*>(a.v_new) + (size_t(p.r) * a.n + q) * a.new_ld + size_t(h) * D + 16 * c;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float y = __uint_as_float(uint32_t(vr[i]) << 16);
+                  if (!(fabsf(y) < INFINITY)) v[i] += y;
+                }
+              }
+          }
+          if (direct || (local && w == 0)) {
+            if (has_o) {
+              const float4* oo = so + size_t(kRows) * (D / 4) + size_t(4 * c) * kRows;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 y = __ldcg(oo + i * kRows);
+                v[4 * i] = v[4 * i] * wa + y.x * wb;
+                v[4 * i + 1] = v[4 * i + 1] * wa + y.y * wb;
+                v[4 * i + 2] = v[4 * i + 2] * wa + y.z * wb;
+                v[4 * i + 3] = v[4 * i + 3] * wa + y.w * wb;
+              }
+            }
+            if (valid) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D) + 2 * c;
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                dst[i] = make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                                    pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) so[(4 * c + i) * kRows] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        }
+        if (direct || (local && w == 0)) {
+          if (valid && a.lse) a.lse[orow] = lse_of(M2, Ls);
+        } else if (valid) {
+          *sm = make_float2(m, l);
+        } else {
+          *sm = make_float2(-INFINITY, 0.f);
+        }
+        // (a unit that goes on in later CTAs is joined by the second kernel)
+        if (tid == 0 && !complete && p.t == 0) {
+          const long long Tk = *keep, ck = Tk < gridDim.x ? Tk : gridDim.x;  // (the tiles in all, and the CTAs that share them)
+          args.begun[blockIdx.x] = make_int4(int(((f + p.Tr) * ck - 1) / Tk), p.r, p.j, 0);
+        }
+        if (local) mbar_arrive(bar(w == 1 ? kFragFull : kFragFree));
+        tc_before();
+        if (mine) mbar_arrive(bar(kOFree0 + w));  // the next piece may write O
+      }
+      if (!more) break;
+      ct0 += n;
+      f += n;
+      p = pn;
+      n = piece_tiles(p, f);
+      const int rows = unit_rows(p.j);
+      split = rows <= kRows, complete = p.t == 0 && n == p.Tr;
+      const int stride = split ? 2 : 1, first = split ? w : 0;
+      const int rg = row_of(p, r);
+      h = p.j / args.blocks;
+      valid = rg < M;
+      node = valid ? rg / G : 0, head = h * G + (valid ? rg % G : 0);
+      mine = first < n;
+      m = -INFINITY, l = 0.f;
+      const float xf = xf_next;
+      mask = valid ? a.mask_bits[size_t(p.r) * a.n + node] & (~0ull >> (kTreeKeys - a.n)) : 0ull;
+      nonfinite = 0;
+      base = kExpBias;
+      pn.t += n - 1;
+      if (f + n < E) advance(pn);
+      const bool ask = f + n < E && has_tile(pn, f + n);
+      if (!mine && ask) ask_q(pn);  // (no product reads it)
       // The reference m is moved, to a whole number, when a score would put P above
       // 2^(kPBaseLog2 + kLazyLog2); O and l are multiplied by that power of two,
       // exactly, once the products so far are complete.
@@ -839,7 +996,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         const bool tree = p.t + t == p.Tr - 1, last = tree || hf == 1;
         const uint32_t ts = tl + col_s(w, cs & 1);
         base = mt.base;
-        if (last && t + stride >= n && f + n < E) ask_q(pn);  // every product that reads this piece's Q is complete
+        if (last && t + stride >= n && ask) ask_q(pn);  // every product that reads this piece's Q is complete
         if (!tree) {
           // The exponentials are taken against the reference as it is.  Their sum
           // tells whether P holds them (none is larger than the sum, and f16 goes
@@ -962,115 +1119,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         t += last ? stride : 0;
       }
       if (!ok) break;
-      // ---- the piece's result ----
-      if (mine) {
-        const bool d_ok = mbar_wait(bar(kPvDone0 + 2 * w + ((cs - 1) & 1)), ((cs - 1) >> 1) & 1, abort_flag) && !*abort_flag;
-        if (!__all_sync(FULL, d_ok)) {
-          ok = false;
-          break;
-        }
-        tc_after();
-      }
-      const float vs = exp_scale(base < 1 ? 1 : base);
-      const bool direct = complete && !split;
-      const int slot = 2 * int(blockIdx.x) + (complete || p.t == 0 ? 1 : 0);  // (0: a unit that an earlier CTA began)
-      const bool local = complete && split;
-      // a slot's O: 16-byte words [4 columns][row], so that a warp stores 512 contiguous bytes
-      float4* so = reinterpret_cast<float4*>(args.slot_o) + (size_t(slot) * 2 + w) * kRows * (D / 4) + r;
-      float2* sm = reinterpret_cast<float2*>(args.slot_ml) + (size_t(slot) * 2 + w) * kRows + r;
-      const size_t orow = (size_t(p.r) * a.n + node) * a.Hq + head;
-      float om = -INFINITY, ol = 0.f;  // group 1's half of a unit that group 0 finishes
-      // (group 0 may not have read the last half that group 1 left in the slot)
-      if (!direct && w == 1 && nfrag > 0 && !__all_sync(FULL, mbar_wait(bar(kFragFree), (nfrag - 1) & 1, abort_flag))) {
-        ok = false;
-        break;
-      }
-      if (local) {
-        if (w == 0) {
-          if (!__all_sync(FULL, mbar_wait(bar(kFragFull), nfrag & 1, abort_flag))) {
-            ok = false;
-            break;
-          }
-          const float2 x = __ldcg(sm + kRows);
-          om = x.x;
-          ol = x.y;
-        }
-        ++nfrag;
-      }
-      const unsigned long long nf = nonfinite & mask;
-      const bool any_nf = __any_sync(FULL, nf != 0ull);
-      // out = (O 2^base [+ the other half, both relative to the larger reference]) / l
-      const bool has_o = ol > 0.f || ol != ol;
-      const float M2 = has_o ? fmaxf(m, om) : m;
-      const float wa = has_o && m != M2 ? fast_exp2(m - M2) : 1.f, wb = has_o ? fast_exp2(om - M2) : 0.f;
-      const float Ls = has_o ? l * wa + ol * wb : l;
-      const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
-#pragma unroll 1
-      for (int c = 0; c < D / 16; ++c) {
-        float v[16];
-        if (mine) {
-          uint32_t o[16];
-          tmem_ld16(to + 16 * c, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * vs;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0.f;
-        }
-        if (any_nf && nf) {
-          for (int q = 0; q < a.n; ++q)
-            if ((nf >> q) & 1ull) {
-              const uint16_t* vr = static_cast<const uint16_t*>(a.v_new) + (size_t(p.r) * a.n + q) * a.new_ld + size_t(h) * D + 16 * c;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float y = __uint_as_float(uint32_t(vr[i]) << 16);
-                if (!(fabsf(y) < INFINITY)) v[i] += y;
-              }
-            }
-        }
-        if (direct || (local && w == 0)) {
-          if (has_o) {
-            const float4* oo = so + size_t(kRows) * (D / 4) + size_t(4 * c) * kRows;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 y = __ldcg(oo + i * kRows);
-              v[4 * i] = v[4 * i] * wa + y.x * wb;
-              v[4 * i + 1] = v[4 * i + 1] * wa + y.y * wb;
-              v[4 * i + 2] = v[4 * i + 2] * wa + y.z * wb;
-              v[4 * i + 3] = v[4 * i + 3] * wa + y.w * wb;
-            }
-          }
-          if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D) + 2 * c;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              dst[i] = make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
-                                  pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
-          }
-        } else if (valid) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) so[(4 * c + i) * kRows] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        }
-      }
-      if (direct || (local && w == 0)) {
-        if (valid && a.lse) a.lse[orow] = lse_of(M2, Ls);
-      } else if (valid) {
-        *sm = make_float2(m, l);
-      } else {
-        *sm = make_float2(-INFINITY, 0.f);
-      }
-      // (a unit that goes on in later CTAs is joined by the second kernel)
-      if (tid == 0 && !complete && p.t == 0) {
-        const long long Tk = *keep, ck = Tk < gridDim.x ? Tk : gridDim.x;  // (the tiles in all, and the CTAs that share them)
-        args.begun[blockIdx.x] = make_int4(int(((f + p.Tr) * ck - 1) / Tk), p.r, p.j, 0);
-      }
-      if (local) mbar_arrive(bar(w == 1 ? kFragFull : kFragFree));
-      tc_before();
-      mbar_arrive(bar(kOFree0 + w));  // the next piece may write O
-      ct0 += n;
-      f += n;
-      p = pn;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok && !*abort_flag) fail();
