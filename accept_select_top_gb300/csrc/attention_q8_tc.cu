@@ -46,11 +46,11 @@ constexpr int kStep = 64;        // keys of a step of S, softmax and P V
 constexpr float kPMost = 60000.f; // a sum of P below this holds no value that f16 does not
 constexpr int kGroup = 16;       // keys with one page at least
 constexpr int kGroups = kKeys / kGroup;
-constexpr int kTcThreads = 20 * 32;
+constexpr int kTcThreads = 24 * 32;
 // Registers a thread, by warp group: the CTA is launched with kRegs each, and
 // the groups trade (sums of four warps: what they take may not pass what was launched).
-constexpr int kRegs = 96, kRegsSoft = 144, kRegsConv = 72, kRegsIssue = 48;
-static_assert(2 * kRegsSoft + 2 * kRegsConv + kRegsIssue <= 5 * kRegs, "register split");
+constexpr int kRegs = 80, kRegsSoft = 136, kRegsConv = 64, kRegsIssue = 40, kRegsAsk = 40;
+static_assert(2 * kRegsSoft + 2 * kRegsConv + kRegsIssue + kRegsAsk <= 6 * kRegs, "register split");
 constexpr int kConvThreads = 128;
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wait
 __host__ __device__ constexpr uint32_t col_o(int w) { return 128u * uint32_t(w); }
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sp + L::kBars + 8 * kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + L::kAbort);
   static_assert(L::kAbort == L::kBars + 8 * kNumBars + 4 && L::kKeep + 4 <= L::kBytes, "layout");
-  int* wsum = reinterpret_cast<int*>(sp + L::kBars + 8 * kNumBars + 8);  // [20]
+  int* wsum = reinterpret_cast<int*>(sp + L::kBars + 8 * kNumBars + 8);  // [24]
   int* keep = reinterpret_cast<int*>(sp + L::kKeep);  // the tiles in all
   int* pre = reinterpret_cast<int*>(sp);  // [b + 1] tiles of one (kv head, row block) before request r (until the roles start)
 
@@ -418,7 +418,81 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     *abort_flag = 1;
   };
 
-  if (warp >= 16) {
+  if (warp >= 20) {
+    // ============================ asking for raw tiles ============================
+    // Warp 20 K, 21 V (22 and 23 make up the warp group): one bulk copy a group of 16
+    // keys (16 D contiguous bytes of a page), a lane each; of the tree tile, one a
+    // node's row.  Page ids are read two tiles ahead, scale bytes one.  (Loads
+    // through registers kept about 11 KB in flight a SM, as little L1 is left beside
+    // the operands, and took three times the MMAs' time; asked for by the converters'
+    // own first warps, the tiles came 2000 cycles later and bounded everything.)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsAsk));
+    const int kv = warp & 1;
+    const uint32_t rawt = sbase + (kv ? L::kRawV : L::kRawK);
+    uint32_t* infos = reinterpret_cast<uint32_t*>(sp + L::kInfo) + kv * 2 * kGroups;
+    const int SHIFT = a.page_size == 16 ? 0 : a.page_size == 32 ? 1 : 2;  // log2(groups a page)
+    auto fetch = [&](const Pos& p) {  // the page id of the lane's group
+      const int g0 = p.t * kGroups + lane;
+      if (lane < kGroups && p.t < p.Tr - 1 && g0 * kGroup < p.len) return a.page_table[size_t(p.row) * a.row_pages + (g0 >> SHIFT)];
+      return 0;
+    };
+    if (warp < 22 && S < E) {
+      // the tile asked for next: where the lane's group (of the tree tile: row 0) lies, its bytes, its info word
+      const uint8_t* src = nullptr;
+      uint32_t bytes = 0, word = 0;
+      bool tree = false;
+      Pos p = start;  // and the one after
+      int pid = fetch(p);
+      auto prepare = [&]() {
+        tree = p.t == p.Tr - 1;
+        bytes = word = 0;
+        if (tree) {
+          src = static_cast<const uint8_t*>(kv ? a.v_new : a.k_new) + 2 * (size_t(p.r) * a.n * a.new_ld + size_t(p.j / args.blocks) * D);
+        } else {
+          const int g = p.t * kGroups + lane, left = p.len - g * kGroup;
+          if (lane < kGroups && left > 0) {
+            if (pid < 0 || pid >= a.num_pages) {
+              raise_error(a.error, SPEC_DEV_INDEX);
+            } else {
+              const int unit = pid * a.Hkv + p.j / args.blocks, cnt = min(kGroup, left);
+              bytes = uint32_t(cnt) * D;
+              src = (kv ? a.v_pages : a.k_pages) + (size_t(unit) * a.page_size + (g & ((1 << SHIFT) - 1)) * kGroup) * D;
+              word = uint32_t(cnt);
+              if (kv == 0) word |= ld_nc8(a.k_scales + unit) << 8 | ld_nc8(a.v_scales + unit) << 16;
+            }
+          }
+        }
+      };
+      const uint32_t full = bar(kRawFull0 + kv);
+      bool ok = true;
+      for (int ct = -1;;) {
+        if (ct >= 0) {
+          if (ct > 0) {
+            ok = __all_sync(FULL, mbar_wait(bar(kRawEmpty0 + kv), (ct - 1) & 1, abort_flag) && !*abort_flag) != 0;
+            if (!ok) break;
+          }
+          if (lane < kGroups) infos[(ct & 1) * kGroups + lane] = word;
+          const uint32_t all = tree ? uint32_t(a.n) * D * 2u : __reduce_add_sync(FULL, bytes);
+          if (lane == 0) mbar_expect(full, all);
+          __syncwarp();
+          if (tree) {
+            for (int i = lane; i < a.n; i += 32) bulk_copy(rawt + uint32_t(i * D * 2), src + size_t(i) * a.new_ld * 2, uint32_t(D) * 2u, full);
+          } else if (bytes) {
+            bulk_copy(rawt + uint32_t(lane * kGroup * D), src, bytes, full);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+        }
+        if (++ct == E - S) break;
+        prepare();
+        if (ct + 1 < E - S) {
+          advance(p);
+          pid = fetch(p);
+        }
+      }
+      if (!ok && !*abort_flag) fail();
+    }
+  } else if (warp >= 16) {
     // ============================ MMA issuers ============================
     // Warps 16, 17: S = Q K^T of softmax groups 0, 1; warps 18, 19: O += P V.  A
     // step is 64 keys; its S goes into one of two buffers, as soon as P V of the
@@ -518,12 +592,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     __syncwarp();
   } else if (warp >= 8) {
     // ============================ converters ============================
-    // Warps 8-11 K, 12-15 V: raw tile -> f16 operand tile.  The first warp of each
-    // also asks for the raw tiles: one bulk copy a group of 16 keys (16 D
-    // contiguous bytes of a page), a lane each; of the tree tile, one a node's
-    // row.  Page ids are read two tiles ahead, scale bytes one.  (Loads through
-    // registers kept about 11 KB in flight a SM, as little L1 is left beside the
-    // operands, and took three times the MMAs' time.)
+    // Warps 8-11 K, 12-15 V: raw tile -> f16 operand tile.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
     const int kv = warp >= 12 ? 1 : 0, cw = warp & 3, ct_id = tid & 127;
     const uint32_t rawt = sbase + (kv ? L::kRawV : L::kRawK);
@@ -533,73 +602,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       return __all_sync(FULL, mbar_wait(bar(b), uint32_t(parity), abort_flag) && !*abort_flag) != 0;
     };
 
-    // ---- asking for raw tiles ----
-    const int SHIFT = a.page_size == 16 ? 0 : a.page_size == 32 ? 1 : 2;  // log2(groups a page)
-    auto fetch = [&](const Pos& p) {  // the page id of the lane's group
-      const int g0 = p.t * kGroups + lane;
-      if (lane < kGroups && p.t < p.Tr - 1 && g0 * kGroup < p.len) return a.page_table[size_t(p.row) * a.row_pages + (g0 >> SHIFT)];
-      return 0;
-    };
-    auto resolve = [&](const Pos& p, int pid, int& unit, int& cnt) {  // its (page, kv head), -1 if none; keys that count
-      const int left = p.len - (p.t * kGroups + lane) * kGroup;
-      unit = -1;
-      cnt = 0;
-      if (lane < kGroups && p.t < p.Tr - 1 && left > 0) {
-        if (pid < 0 || pid >= a.num_pages) {
-          raise_error(a.error, SPEC_DEV_INDEX);
-        } else {
-          unit = pid * a.Hkv + p.j / args.blocks;
-          cnt = min(kGroup, left);
-        }
-      }
-    };
-    auto copy = [&](const Pos& p, int unit, int cnt, int slot) {
-      const uint32_t full = bar(kRawFull0 + kv);
-      const uint8_t* pages = kv ? a.v_pages : a.k_pages;
-      if (lane < kGroups) infos[slot * kGroups + lane] = uint32_t(cnt);
-      if (p.t < p.Tr - 1) {
-        const uint32_t bytes = uint32_t(cnt) * D;
-        const uint32_t all = __reduce_add_sync(FULL, bytes);
-        if (lane == 0) mbar_expect(full, all);
-        __syncwarp();
-        if (bytes) {
-          const int off = ((p.t * kGroups + lane) & ((1 << SHIFT) - 1)) * kGroup;
-          bulk_copy(rawt + uint32_t(lane * kGroup * D), pages + (size_t(unit) * a.page_size + off) * D, bytes, full);
-        }
-      } else {
-        if (lane == 0) mbar_expect(full, uint32_t(a.n) * D * 2u);
-        __syncwarp();
-        for (int i = lane; i < a.n; i += 32)
-          bulk_copy(rawt + uint32_t(i * D * 2),
-                    static_cast<const uint16_t*>(kv ? a.v_new : a.k_new) + (size_t(p.r) * a.n + i) * a.new_ld + size_t(p.j / args.blocks) * D,
-                    uint32_t(D) * 2u, full);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full);
-    };
-    // (warp cw 0) the tile asked for next, the lane's page id of it, and its scale
-    // bytes of the tile asked for last: each is loaded a tile before it is used
-    Pos p = start, p1 = start;
-    int pid1 = 0;
-    uint32_t ks = 0, vs = 0;
-    auto ask = [&](int slot) {
-      int unit, cnt;
-      resolve(p1, pid1, unit, cnt);
-      copy(p1, unit, cnt, slot);
-      if (kv == 0) {
-        ks = unit >= 0 ? ld_nc8(a.k_scales + unit) : 0u;
-        vs = unit >= 0 ? ld_nc8(a.v_scales + unit) : 0u;
-      }
-    };
-    if (cw == 0 && S < E) {
-      pid1 = fetch(p1);
-      ask(0);
-      if (S + 1 < E) {
-        advance(p1);
-        pid1 = fetch(p1);
-      }
-    }
-
+    Pos p = start;
     constexpr int kLoads = D / 16;               // 16-byte words a thread of a raw tile
     constexpr int kLanesKey = D / 16;            // lanes a history key
     constexpr int kLanesRow = D / 8;             // lanes a tree row
@@ -654,39 +657,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     bool ok = true;
     for (int f = S; f < E; ++f, ++ct) {
       const int buf = ct & 1;
-      const bool tree = p.t == p.Tr - 1, first = f == S || p.t == 0, more = f + 1 < E;
+      const bool tree = p.t == p.Tr - 1, first = f == S || p.t == 0;
       const uint32_t* info = infos + buf * kGroups;
       const uint32_t tile = sbase + (kv ? L::kV : L::kK) + uint32_t(buf) * L::kTile;
       TileMeta& mt = metas[ct & 3];
       ok = wait(kRawFull0 + kv, ct & 1);
       if (!ok) break;
-      const int ks0 = int(ks), vs0 = int(vs);  // this tile's (the next one's are asked for below)
+      // (K) the lane's group: keys that count, scale bytes
+      const uint32_t word = lane < kGroups ? info[lane] : 0u;
+      const int cnt = word & 255, ks0 = (word >> 8) & 255, vs0 = word >> 16;
       if (first && cw == 0) {
         const int v0 = __shfl_sync(FULL, vs0, 0);
         base = tree || v0 == 0 ? 113 : v0;
       }
-      // the next raw tile is asked for once every converter has read this one
-      auto ask_next = [&]() {
-        if (cw != 0 || !more) return true;
-        if (!wait(kRawEmpty0 + kv, ct & 1)) return false;
-        ask(buf ^ 1);
-        if (f + 2 < E) {
-          advance(p1);
-          pid1 = fetch(p1);
-        }
-        return true;
-      };
       if (!tree) {
         uint4 x[kLoads];  // the thread's words, zeros where there is no key
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           const int key = hist_key(i);
           x[i] = lds16(rawt + uint32_t(key * D + (lane % kLanesKey) * 16));
-          if (uint32_t(key & 15) >= info[key >> 4]) x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (uint32_t(key & 15) >= (info[key >> 4] & 255u)) x[i] = make_uint4(0u, 0u, 0u, 0u);
         }
-        const int cnt = lane < kGroups ? int(info[lane]) : 0;
         mbar_arrive(bar(kRawEmpty0 + kv));
-        ok = ask_next() && (ct < 2 || wait(empty0 + buf, ((ct >> 1) - 1) & 1));
+        ok = ct < 2 || wait(empty0 + buf, ((ct >> 1) - 1) & 1);
         if (!ok) break;
         if (kv == 0 && cw == 0 && lane < kGroups) {
           mt.group[lane] = cnt > 0 ? make_float4(exp_scale(ks0), float(vs0 - base), ratio_scale(base - vs0), float(cnt))
@@ -731,8 +724,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         }
         if (kv == 1 && lane == 0) mt.nonfinite[cw] = nf;
         mbar_arrive(bar(kRawEmpty0 + kv));
-        ok = ask_next();
-        if (!ok) break;
       }
       if (kv == 0 && ct_id == 0) mt.base = base;
       fence_async();
