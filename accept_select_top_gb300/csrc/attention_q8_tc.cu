@@ -125,19 +125,29 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
                : "memory");
   return ok != 0;
 }
+// Up to 128 tries, in a loop of four instructions and without a time hint: the warps that wait
+// took a quarter of the issue slots with a loop of ten (long contexts 282 us; 279 so, 286
+// with a hint of 20 us, 285 by test_wait, 288 where the converters sleep between their tries).
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 128;\nAGAIN:\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
+      " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra AGAIN;\nDONE:\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Bounded wait for the phase of the given parity: false once kWaitCycles have
-// passed or another warp has given up.  The bound is looked at every 64 polls, so
-// that a waiting warp takes few issue slots from the others.
+// passed or another warp has given up.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  long long start = 0;
-  for (uint32_t i = 0;; ++i) {
-    if (mbar_try(bar, parity)) return true;
-    if ((i & 63u) == 63u) {
-      const long long now = clock64();
-      if (i == 63u) start = now;
-      if (*abort_flag || now - start > kWaitCycles) return false;
-    }
-  }
+  if (mbar_poll(bar, parity)) return true;
+  const long long start = clock64();
+  do {
+    if (mbar_poll(bar, parity)) return true;
+  } while (!*abort_flag && clock64() - start <= kWaitCycles);
+  return false;
 }
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -790,8 +800,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       }
       const int e = norm_exp(max(mx & 0xffffu, mx >> 16));
       // the sign of the scale goes into Q, so that a larger score is a larger exponent
-      const float inv = copysignf(exp_scale(2 * kExpBias - e), a.scale);
-      xf_next = fabsf(a.scale) * 1.4426950408889634f * exp_scale(e);
+      const float inv = a.scale == 0.f ? 0.f : copysignf(exp_scale(2 * kExpBias - e), a.scale);
+      // (a factor of 0 would take the -inf of a key that does not count to NaN: then Q is 0)
+      xf_next = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f * exp_scale(e);
       auto cv = [&](uint32_t u) { return pack_f16(bf16_lo(u) * inv, bf16_hi(u) * inv); };
 #pragma unroll 8
       for (int i = 0; i < D / 8; ++i) {

@@ -130,9 +130,10 @@ def test_attention_under_load(n, Hq, Hkv, D, page, lens):
     assert x.ws.last_error() == 0
 
 
+@pytest.mark.parametrize("scale", [-0.11, 0.0])
 @pytest.mark.parametrize("n, Hq, Hkv", [(4, 32, 8), (64, 16, 8), (64, 32, 8)])
-def test_attention_negative_scale_under_load(n, Hq, Hkv):
-    x = Load(n, Hq, Hkv, 128, 32, mixed(30, 200, 1500, 9), seed=8, scale=-0.11)
+def test_attention_scale_below_or_at_zero_under_load(n, Hq, Hkv, scale):
+    x = Load(n, Hq, Hkv, 128, 32, mixed(30, 200, 1500, 9), seed=8, scale=scale)
     x.launch()
     assert x.ws.last_error() == 0
     x.check(x.reference())
