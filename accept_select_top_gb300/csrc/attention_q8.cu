@@ -48,7 +48,11 @@ namespace {
 
 constexpr int kWarps = 12;
 constexpr int kQ8AttThreads = 32 * kWarps;
-constexpr int kRowsMost = 32;  // query rows a kv head up to which this kernel is taken
+// Query rows a kv head up to which this kernel is taken: its time goes with the 16-row tiles, the tcgen05
+// kernel's hardly (in us, this one / that one; 8 kv heads of 128): 32 rows, eight contexts of 16384 109 / 104,
+// 64 ragged ones to 4096 110 / 236; 48 rows, 16 of 4096 83 / 70, 32 of 2048 86 / 94; 64 rows, 16 of 4096
+// 97 / 70, eight of 16384 177 / 105.
+constexpr int kRowsMost = 32;
 constexpr int kTile = 16;    // keys of a tile
 constexpr int kRowTile = 16; // query rows of a unit
 constexpr int kRing = 3;     // tiles in a warp's ring

@@ -699,20 +699,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       } else {
         ok = ct < 2 || wait(empty0 + buf, ((ct >> 1) - 1) & 1);
         if (!ok) break;
-        constexpr int kAtOnce = 4;  // (eight take more registers than there are)
+        constexpr int kRowsOnce = 4;  // (eight take more registers than there are)
         unsigned long long nf = 0;
 #pragma unroll 1
-        for (int i0 = 0; i0 < kTreeLoads; i0 += kAtOnce) {
-          uint4 x[kAtOnce];
+        for (int i0 = 0; i0 < kTreeLoads; i0 += kRowsOnce) {
+          uint4 x[kRowsOnce];
           bool odd = false;
 #pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) {
+          for (int i = 0; i < kRowsOnce; ++i) {
             const int key = tree_key(i0 + i);
             x[i] = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
             if (key >= a.n) x[i] = make_uint4(0u, 0u, 0u, 0u);
           }
 #pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) {
+          for (int i = 0; i < kRowsOnce; ++i) {
             const int key = tree_key(i0 + i), e = row_exp(x[i]);
             if (ct_id % kLanesRow == 0) reinterpret_cast<uint16_t*>(&mt.node[key])[kv] = uint16_t(kv == 0 ? uint32_t(e) << 7 : __float_as_uint(float(e)) >> 16);
             odd = odd || nonfinite_bf16(x[i].x) || nonfinite_bf16(x[i].y) || nonfinite_bf16(x[i].z) || nonfinite_bf16(x[i].w);
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
           }
           if (kv == 1 && __any_sync(FULL, odd)) {  // (the words are read again: few rows hold such)
 #pragma unroll 1
-            for (int i = 0; i < kAtOnce; ++i) {
+            for (int i = 0; i < kRowsOnce; ++i) {
               const int key = tree_key(i0 + i);
               const uint4 y = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
               const bool bad = key < a.n && (nonfinite_bf16(y.x) || nonfinite_bf16(y.y) || nonfinite_bf16(y.z) || nonfinite_bf16(y.w));
@@ -1136,13 +1136,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
 }
 
 // Joins the units that the kernel above left in fragments: block (c, slice) 32 rows
-// of the unit that CTA c began and did not finish, a lane a row, a quarter of
+// of the unit that CTA c began and did not finish, a lane a row, an eighth of
 // the columns a warp.  A launch of its own, because it wants the whole GPU: the last
 // CTA of a unit, alone and with hardly any L1 beside its operands, took 23 us for
 // the trees' 1.2 MB and 54 us for the long contexts'.
-constexpr int kJoinThreads = 128, kJoinRows = 32;
+constexpr int kJoinThreads = 256, kJoinRows = 32;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attention_q8_join_kernel(const __grid_constant__ TcArgs args) {
+__global__ void __launch_bounds__(kJoinThreads, 4) attention_q8_join_kernel(const __grid_constant__ TcArgs args) {
   pdl_wait();
   pdl_trigger();
   const AttentionQ8Params& a = args.p;
@@ -1162,14 +1162,21 @@ __global__ void __launch_bounds__(kJoinThreads) attention_q8_join_kernel(const _
   };
   const float2* ml2 = reinterpret_cast<const float2*>(args.slot_ml) + row % kRows;
   float Mx = -INFINITY, Ls = 0.f;
-#pragma unroll 4
-  for (int y = 0; y < nf; ++y) {
-    const float2 ml = __ldcg(ml2 + at(y) * kRows);
-    const bool has = ml.y > 0.f || ml.y != ml.y;  // (else it saw nothing, and its O is not read)
-    const float M2 = has ? fmaxf(Mx, ml.x) : Mx;
-    const float wa = Ls > 0.f || Ls != Ls ? exp2f(Mx - M2) : 0.f;
-    Ls = has ? Ls * wa + ml.y * exp2f(ml.x - M2) : Ls;
-    Mx = M2;
+  // (fragments two at a time: with four, fewer blocks fit a SM, and the trees take 103 us, not 100)
+  constexpr int kAtOnce = 2;
+#pragma unroll 1
+  for (int y0 = 0; y0 < nf; y0 += 2 * kAtOnce) {
+    float2 ml[2 * kAtOnce];
+#pragma unroll
+    for (int y = 0; y < 2 * kAtOnce; ++y) ml[y] = y0 + y < nf ? __ldcg(ml2 + at(y0 + y) * kRows) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int y = 0; y < 2 * kAtOnce; ++y) {
+      const bool has = ml[y].y > 0.f || ml[y].y != ml[y].y;  // (else it saw nothing, and its O is not read)
+      const float M2 = has ? fmaxf(Mx, ml[y].x) : Mx;
+      const float wa = Ls > 0.f || Ls != Ls ? exp2f(Mx - M2) : 0.f;
+      Ls = has ? Ls * wa + ml[y].y * exp2f(ml[y].x - M2) : Ls;
+      Mx = M2;
+    }
   }
   const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
   constexpr int C4 = D / 4, C = C4 / (kJoinThreads / 32);  // 16-byte words a thread
@@ -1177,22 +1184,33 @@ __global__ void __launch_bounds__(kJoinThreads) attention_q8_join_kernel(const _
   float4 acc[C];
 #pragma unroll
   for (int e = 0; e < C; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int y = 0; y < nf; ++y) {
-    const float4* src = reinterpret_cast<const float4*>(args.slot_o) + (at(y) * C4 + c) * kRows + row % kRows;
-    const float2 ml = __ldcg(ml2 + at(y) * kRows);
-    float4 o4[C];
+#pragma unroll 1
+  for (int y0 = 0; y0 < nf; y0 += kAtOnce) {
+    float4 o4[kAtOnce][C];
+    float2 ml[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < C; ++e) o4[e] = __ldcg(src + e * kRows);
-    if (!(ml.y > 0.f || ml.y != ml.y)) continue;
-    const float k = exp2f(ml.x - Mx) * inv;
+    for (int y = 0; y < kAtOnce; ++y) {
+      ml[y] = make_float2(-INFINITY, 0.f);
+      if (y0 + y < nf) {
+        const size_t slot = at(y0 + y);
+        const float4* src = reinterpret_cast<const float4*>(args.slot_o) + (slot * C4 + c) * kRows + row % kRows;
+        ml[y] = __ldcg(ml2 + slot * kRows);
 #pragma unroll
-    for (int e = 0; e < C; ++e) {
-      acc[e].x = fmaf(o4[e].x, k, acc[e].x);
-      acc[e].y = fmaf(o4[e].y, k, acc[e].y);
-      acc[e].z = fmaf(o4[e].z, k, acc[e].z);
-      acc[e].w = fmaf(o4[e].w, k, acc[e].w);
+        for (int e = 0; e < C; ++e) o4[y][e] = __ldcg(src + e * kRows);
+      }
     }
+#pragma unroll
+    for (int y = 0; y < kAtOnce; ++y)
+      if (ml[y].y > 0.f || ml[y].y != ml[y].y) {
+        const float k = exp2f(ml[y].x - Mx) * inv;
+#pragma unroll
+        for (int e = 0; e < C; ++e) {
+          acc[e].x = fmaf(o4[y][e].x, k, acc[e].x);
+          acc[e].y = fmaf(o4[y][e].y, k, acc[e].y);
+          acc[e].z = fmaf(o4[y][e].z, k, acc[e].z);
+          acc[e].w = fmaf(o4[y][e].w, k, acc[e].w);
+        }
+      }
   }
   const int rg = 2 * kRows * (j % args.blocks) + row;
   const size_t orow = (size_t(r) * a.n + rg / G) * a.Hq + h * G + rg % G;
