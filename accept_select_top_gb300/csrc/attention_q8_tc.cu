@@ -10,16 +10,19 @@
 //   0-3, 4-7  two softmax groups, one query row a thread.  More than 128 rows:
 //             group w has rows 128 w .. and both see every tile; fewer: the
 //             groups take turns at the tiles (two partial results, joined).
-//   8-11, 12-15  converters of K and of V: bulk copies bring a tile's pages into
-//             shared memory as they are, then e4m3 becomes f16 (one instruction
-//             for two values) in 128B-swizzled operand tiles, double buffered.
-//             Tree nodes are bf16 rows divided by their own power of two, and
-//             stored the same way.
+//   8-11, 12-15  converters of K and of V: e4m3 becomes f16 (one instruction for
+//             two values) in 128B-swizzled operand tiles, double buffered.  Tree
+//             nodes are bf16 rows divided by their own power of two, and stored the
+//             same way.
 //   16-19     issue the MMAs: S = Q K^T (M 128, N 64, K D, both from shared
 //             memory) and O += P V (A = P from TMEM), a warp each for each group.
+//   20, 21    ask for the tiles: bulk copies bring their pages into shared memory as
+//             they are.
 // TMEM: O0 O1 | two S buffers a group; P (f16, two to a column) takes the place of
 // its S.  A step is 64 keys: the scores of the next one are computed, and the
-// products of the last one added up, while a step's softmax runs.
+// products of the last one added up, while a step's softmax runs.  (One S buffer with
+// places of their own for P made S always ready, but its softmax, which then has to
+// settle a half's reference before S is gone, 500 cycles longer: 333 us, not 282.)
 //
 // Bound: 2 x 1024 cycles of MMA for 128 keys and 256 rows (f16 at 4096
 // multiply-adds a cycle).  Per tile shared memory moves 64 KB of converted
@@ -27,6 +30,13 @@
 // memory would add 128 KB, which is why it goes through TMEM (an MMA with A
 // from TMEM measured the same 64 cycles as one with both operands in shared
 // memory, once its descriptors are precomputed).
+//   Measured: two contexts of 32768 to 131072, 64 nodes, 64 / 8 heads of 128: 273 us
+// (1.26 PF/s); 32 requests of 2048, 64 nodes, 32 / 8 heads: 95 us (0.72 PF/s).  In the
+// history a step of 64 keys takes a group some 1960 cycles, of which the softmax is 1500
+// (two warps of it and two converters share a scheduler) and the MMAs of both groups
+// 1280.  A unit's end costs about 25000 cycles more: the tree's rows are converted
+// late, its softmax looks at masks and exponents node by node, and O leaves as 128 KB
+// of fragments where a CTA's range cuts the unit.
 //   Every wait is bounded: on timeout the CTA sets SPEC_DEV_TIMEOUT, stops,
 // drains its MMAs and frees its TMEM.
 #include "common.cuh"
@@ -475,7 +485,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       };
       const uint32_t full = bar(kRawFull0 + kv);
       bool ok = true;
-      for (int ct = -1;;) {
+      int ct = -1;
+      for (;;) {
         if (ct >= 0) {
           if (ct > 0) {
             ok = __all_sync(FULL, mbar_wait(bar(kRawEmpty0 + kv), (ct - 1) & 1, abort_flag) && !*abort_flag) != 0;
@@ -501,6 +512,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         }
       }
       if (!ok && !*abort_flag) fail();
+      // the last copy has landed before the CTA can end, whoever gave up
+      for (int k = 0; k < 100 && !mbar_try(full, (ct - 1) & 1); ++k) {
+      }
     }
   } else if (warp >= 16) {
     // ============================ MMA issuers ============================
@@ -642,21 +656,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         put(at ^ 16u, b0, b1);
       }
     };
-    auto row_exp = [&](const uint4& x) {  // exponent byte of a tree row's power of two, from its lanes
+    auto row_max = [&](const uint4& x) {  // a tree row's largest finite magnitude, from its lanes
       uint32_t mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(0u, x.x), x.y), x.z), x.w);
       mx = max(mx & 0xffffu, mx >> 16);
 #pragma unroll
       for (int o = 1; o < kLanesRow; o <<= 1) mx = max(mx, __shfl_xor_sync(FULL, mx, o));
-      return norm_exp(mx);
+      return mx;
     };
-    // (an inf or a NaN of V is left out here and added to the rows that see it at the end)
-    auto store_tree = [&](uint32_t tile, uint4 x, int key, int e, bool finite) {
-      if (finite) {
-        x.x = finite_bf16(x.x);
-        x.y = finite_bf16(x.y);
-        x.z = finite_bf16(x.z);
-        x.w = finite_bf16(x.w);
-      }
+    auto store_tree = [&](uint32_t tile, const uint4& x, int key, int e) {
       const float inv = exp_scale(2 * kExpBias - e);
       auto cv = [&](uint32_t w) { return pack_f16(bf16_lo(w) * inv, bf16_hi(w) * inv); };
       const int ch = ct_id % kLanesRow;
@@ -704,32 +711,45 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
 #pragma unroll 1
         for (int i0 = 0; i0 < kTreeLoads; i0 += kRowsOnce) {
           uint4 x[kRowsOnce];
-          bool odd = false;
 #pragma unroll
           for (int i = 0; i < kRowsOnce; ++i) {
             const int key = tree_key(i0 + i);
             x[i] = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
             if (key >= a.n) x[i] = make_uint4(0u, 0u, 0u, 0u);
           }
+          // the rows' largest magnitudes; an inf or a NaN anywhere shows in them
+          uint32_t top[kRowsOnce];
 #pragma unroll
           for (int i = 0; i < kRowsOnce; ++i) {
-            const int key = tree_key(i0 + i), e = row_exp(x[i]);
-            if (ct_id % kLanesRow == 0) reinterpret_cast<uint16_t*>(&mt.node[key])[kv] = uint16_t(kv == 0 ? uint32_t(e) << 7 : __float_as_uint(float(e)) >> 16);
-            odd = odd || nonfinite_bf16(x[i].x) || nonfinite_bf16(x[i].y) || nonfinite_bf16(x[i].z) || nonfinite_bf16(x[i].w);
-            store_tree(tile, x[i], key, e, kv == 1);
+            const uint32_t m2 = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu), __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+            top[i] = max(m2 & 0xffffu, m2 >> 16);
           }
-          if (kv == 1 && __any_sync(FULL, odd)) {  // (the words are read again: few rows hold such)
-#pragma unroll 1
+#pragma unroll
+          for (int o = 1; o < kLanesRow; o <<= 1)
+#pragma unroll
+            for (int i = 0; i < kRowsOnce; ++i) top[i] = max(top[i], __shfl_xor_sync(FULL, top[i], o));
+          bool odd = false;
+#pragma unroll
+          for (int i = 0; i < kRowsOnce; ++i) odd = odd || top[i] >= 0x7f80u;
+          if (__any_sync(FULL, odd)) {
+#pragma unroll
             for (int i = 0; i < kRowsOnce; ++i) {
-              const int key = tree_key(i0 + i);
-              const uint4 y = lds16(rawt + uint32_t(key * D * 2 + (ct_id % kLanesRow) * 16));
-              const bool bad = key < a.n && (nonfinite_bf16(y.x) || nonfinite_bf16(y.y) || nonfinite_bf16(y.z) || nonfinite_bf16(y.w));
-              const unsigned who = __ballot_sync(FULL, bad);
+              const unsigned who = __ballot_sync(FULL, top[i] >= 0x7f80u);
+              top[i] = row_max(x[i]);
+              if (kv == 1) {
+                // (an inf or a NaN of V is left out here and added to the rows that see it at the end)
+                x[i] = make_uint4(finite_bf16(x[i].x), finite_bf16(x[i].y), finite_bf16(x[i].z), finite_bf16(x[i].w));
 #pragma unroll 1
-              for (int q = 0; q < 32 / kLanesRow; ++q)
-                if ((who >> (q * kLanesRow)) & ((1u << kLanesRow) - 1u))
-                  nf |= 1ull << ((i0 + i) * kRowsLoad + cw * (32 / kLanesRow) + q);
+                for (int q = 0; q < 32 / kLanesRow; ++q)
+                  if ((who >> (q * kLanesRow)) & 1u) nf |= 1ull << ((i0 + i) * kRowsLoad + cw * (32 / kLanesRow) + q);
+              }
             }
+          }
+#pragma unroll
+          for (int i = 0; i < kRowsOnce; ++i) {
+            const int key = tree_key(i0 + i), e = norm_exp(top[i]);
+            if (ct_id % kLanesRow == 0) reinterpret_cast<uint16_t*>(&mt.node[key])[kv] = uint16_t(kv == 0 ? uint32_t(e) << 7 : __float_as_uint(float(e)) >> 16);
+            store_tree(tile, x[i], key, e);
           }
         }
         if (kv == 1 && lane == 0) mt.nonfinite[cw] = nf;
@@ -741,9 +761,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       advance(p);
     }
     if (!ok && !*abort_flag) fail();
-    // every copy has landed before the CTA can end (each tile was waited for, but for one when giving up)
-    if (cw == 0 && *abort_flag)
-      for (int k = 0; k < 100; ++k) mbar_try(bar(kRawFull0 + kv), (ct + (k & 1)) & 1);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     // ============================ softmax groups ============================

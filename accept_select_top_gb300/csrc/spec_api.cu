@@ -850,8 +850,8 @@ int spec_commit_kv_q8(int b, int Hkv, int D, int page_size, int num_layers, cons
                       const int32_t* seq_lens, const int32_t* src_index, const int32_t* src_start,
                       const int32_t* lens, int max_len, int32_t* new_seq_lens, void* ws, size_t ws_bytes,
                       void* stream) {
-  if (b < 0 || Hkv < 1 || max_len < 1 || num_rows < 1 || num_pages < 1 || req_rows < 1 || row_pages < 1 ||
-      num_layers < 1 || num_layers > kMaxLayers)
+  if (b < 0 || Hkv < 1 || max_len < 1 || num_rows < 1 || num_rows >= (int64_t(1) << 31) || num_pages < 1 || req_rows < 1 ||
+      row_pages < 1 || num_layers < 1 || num_layers > kMaxLayers)
     return SPEC_ERR_ARG;
   if ((D != 64 && D != 128) || (page_size != 16 && page_size != 32 && page_size != 64)) return SPEC_ERR_UNSUPPORTED;
   if (new_ld < int64_t(Hkv) * D || new_ld % 8 || int64_t(row_pages) * page_size >= (int64_t(1) << 31)) return SPEC_ERR_ARG;
@@ -913,7 +913,7 @@ int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size
   const int64_t tiles = int64_t(max_seq_len) / 16 + 1 + 8 * ((n + 15) / 16);
   if (num_pages * Hkv >= (int64_t(1) << 31) || int64_t(b) * n * Hq >= (int64_t(1) << 31) ||
       int64_t(row_pages) * page_size >= (int64_t(1) << 31) ||
-      int64_t(b) * tiles * Hkv * ((int64_t(n) * (Hq / Hkv) + 15) / 16) >= (int64_t(1) << 31))
+      int64_t(b) * tiles * Hkv * ((int64_t(n) * (Hq / Hkv) + 15) / 16) >= (int64_t(1) << 31) - 1024)
     return SPEC_ERR_ARG;
   if (b == 0) return SPEC_OK;
   if (!q || !k_new || !v_new || !k_pages || !v_pages || !k_scales || !v_scales || !page_table || !req_pool_idx ||

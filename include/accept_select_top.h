@@ -512,7 +512,7 @@ int spec_alloc_slots(int b, int page_size, const int32_t* req_pool_idx, const in
  * verify step, max_len its width) or, src_index NULL, src_start[b] + j (cu_new
  * of prompts).  k_new / v_new: num_rows rows [Hkv, D] bf16, new_ld elements
  * apart (a multiple of 8, at least Hkv * D: a view of a packed projection).
- * Every layer, K and V.  The pages have to be in page_table already; no page
+ * Every layer, K and V; num_rows is below 2^31.  The pages have to be in page_table already; no page
  * that receives a row may belong to two requests of the call.
  *   With x = the largest finite magnitude among the rows a (page, kv head)
  * receives, need = the smallest e >= SPEC_Q8_EXP_MIN with x <= 448 * 2^(e-127).

@@ -150,3 +150,9 @@ def test_reference_scale():
     for a, e in ((448.0, 127), (449.0, 128), (224.0, 126), (1.75, 119), (1.0, 119), (1.7578125, 120), (0.0, 16), (1e-38, 16),
                  (float(torch.finfo(torch.bfloat16).max), 247)):
         assert R.need_exp(torch.tensor([a, -a / 2, math.inf, math.nan], dtype=torch.float64)) == e, a
+
+
+def test_commit_refuses_rows_past_32_bits(lib):
+    """A row number is kept in 32 bits: one past them would have been dropped without a word."""
+    args, keep = _commit(num_rows=1 << 31)
+    assert lib.spec_commit_kv_q8(*args) == -1
