@@ -153,3 +153,44 @@ def test_attention_on_two_streams_at_once():
     for x, w in zip(both, want):
         assert x.ws.last_error() == 0
         x.check(w)
+
+
+def test_commit_of_more_pages_than_get_a_cta_for_each_layer():
+    """A CTA takes K and V of several layers in turn: bytes and scales of whole prompts, against torch's own e4m3."""
+    ops = _ops()
+    b, page, Hkv, D, layers = 120, 16, 8, 64, 3
+    gen = torch.Generator().manual_seed(12)
+    lens = torch.randint(1, 700, (b,), generator=gen).tolist()
+    lens[3], lens[50] = 0, 699
+    start = [sum(lens[:r]) for r in range(b)]
+    need = [-(-x // page) for x in lens]
+    ids = torch.randperm(sum(need), generator=gen).tolist()
+    table = torch.full((b, max(need)), -1, dtype=torch.int32)
+    owner = []  # (page id, first row, rows) of every page
+    for r in range(b):
+        for p in range(need[r]):
+            table[r, p] = ids.pop()
+            owner.append((int(table[r, p]), start[r] + p * page, min(page, lens[r] - p * page)))
+    on = torch.Generator(device=DEV).manual_seed(13)
+    x = [[(torch.randn(sum(lens), Hkv, D, generator=on, device=DEV) * torch.exp2(torch.randint(-9, 10, (sum(lens), 1, 1), generator=on, device=DEV))).bfloat16()
+          for _ in range(layers)] for _ in "kv"]
+    pools = [[torch.full((sum(need), Hkv, page, D), 0x55, dtype=torch.uint8, device=DEV) for _ in range(layers)] for _ in "kv"]
+    scales = [[torch.zeros(sum(need), Hkv, dtype=torch.uint8, device=DEV) for _ in range(layers)] for _ in "kv"]
+    after, ws = torch.empty(b, dtype=torch.int32, device=DEV), ops.Workspace(ops.spec_workspace_size(ops.OP_COMMIT_KV_Q8, b, 1, 1, 1))
+    ops.spec_commit_kv_q8(b, Hkv, D, page, x[0], x[1], pools[0], pools[1], scales[0], scales[1], table.to(DEV), i32(list(range(b))), i32([0] * b),
+                          None, i32(start), i32(lens), 699, after, ws)
+    assert ws.last_error() == 0 and after.tolist() == lens
+    pid = torch.tensor([o[0] for o in owner], device=DEV)
+    rows = torch.tensor([o[1] for o in owner], device=DEV)[:, None] + torch.arange(page, device=DEV)
+    held = torch.arange(page, device=DEV) < torch.tensor([o[2] for o in owner], device=DEV)[:, None]
+    for kv in range(2):
+        for layer in range(layers):
+            y = x[kv][layer].float()[torch.where(held, rows, 0)].transpose(1, 2)  # [pages, Hkv, page, D]
+            there = held[:, None, :, None].expand_as(y)
+            most = torch.where(there, y, 0.0).abs().amax((2, 3)).double()
+            e = torch.full_like(most, 16.0)
+            for k in range(100, 150):
+                e = torch.where(most > 448 * 2.0 ** (k - 127), k + 1.0, e)
+            assert torch.equal(scales[kv][layer][pid].double(), e)
+            want = (y * torch.exp2(127 - e)[..., None, None].float()).to(torch.float8_e4m3fn).view(torch.uint8)
+            assert torch.equal(pools[kv][layer][pid], torch.where(there, want, 0x55))
