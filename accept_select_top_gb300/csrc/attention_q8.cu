@@ -28,7 +28,10 @@
 // that of the keys as long as P has the same, so both K and V fragments are
 // read as whole 16-byte words.  What limits a warp is the issue of its ~340
 // instructions a tile, so the history's loop is one short body.
-//   There is no barrier.  Units cut by a range boundary leave fragments (O, m, l)
+//   Few units: a cluster of CTAs takes each, its warps equal shares of the unit's
+// tiles, and joins it through distributed shared memory.
+//   Many: the warps of the whole GPU share all the tiles, and there is no
+// barrier.  Units cut by a range boundary leave fragments (O, m, l)
 // in the workspace, and a second, dependent launch joins them (a join by the CTA's own
 // warps behind a barrier and by the last CTA of a unit took 20 us on average, 57 us at
 // most, of a 275 us call).  Only where all the warps of a CTA lie inside one unit does
@@ -62,6 +65,17 @@ constexpr int kMinTicks = 2; // a warp gets at least this many ticks before anot
 // chains above took 254, 236, 232 and 228 us (with four stages), and a single token 1 us more by 12 than by 8.
 constexpr int kTreeTicks = 8;
 
+// A cluster takes a unit and joins it by itself, in one launch, where the units are few enough for
+// all of them to run at once (a GB300 holds 15 clusters of eight such CTAs, 36 of four, 76 of two) and a
+// warp gets at most so many ticks; else the warps of the whole GPU share the work, and a second
+// launch joins it.  In us, cluster / whole GPU, 32 / 8 heads of 128: one request, one token, 1000 keys 10.6 /
+// 18.8, 8000 15.6 / 27.5, 32000 28.6 / 35.4, 60000 (39 ticks) 44.5 / 45.4; 16 requests of 4000 31.1 / 47.1.
+constexpr int kClusterTicks = 32;
+constexpr int kLargestCluster = 8;
+inline int cluster_of(long long units, int sms) {
+  return units <= 14 ? 8 : units <= 34 ? 4 : units <= 72 ? 2 : units <= sms ? 1 : 0;
+}
+
 template <int D>
 struct RowsSmem {
   static constexpr int kHalf = kTile * D;         // K (or V) bytes of a tile
@@ -73,6 +87,8 @@ struct RowsSmem {
   static constexpr int kMeta = kMl + kWarps * kRowTile * 8;  // [warp][stage] the tile's word
   static constexpr int kScan = kMeta + kWarps * kRing * 4;
   static size_t bytes(int b) { return size_t(kScan) + 12u * size_t(b + 1); }
+  // (a cluster a unit: no scan, there the CTA's joined fragment: O, then (m, l))
+  static constexpr int kUnitBytes = kScan + kFrag + kRowTile * 8;
 };
 
 // What the kernel leaves for the joining one: table[0] = {warps, warps a CTA},
@@ -124,7 +140,28 @@ struct Raw16 {
 __device__ __forceinline__ uint32_t scaled_f16(uint32_t w, float inv) { return pack_f16(bf16_lo(w) * inv, bf16_hi(w) * inv); }
 __device__ __forceinline__ uint32_t word_of(const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
 
-template <int D>
+// Distributed shared memory: the address of `p` in CTA `rank` of the cluster, and reads of it.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// CLUSTER: a cluster of CTAs takes one unit (grid: cluster, units) and joins it by itself.
+template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(const __grid_constant__ RowsArgs args) {
   using L = RowsSmem<D>;
   constexpr unsigned FULL = 0xffffffffu;
@@ -142,51 +179,11 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
 
   pdl_wait();
   pdl_trigger();
-  // ---- ticks before each request ----
-  {
-    int run = 0;
-    for (int r0 = 0; r0 < a.b; r0 += kQ8AttThreads) {
-      const int r = r0 + tid;
-      int t = 0;
-      if (r < a.b) {
-        int Lp = a.seq_lens[r], rq = a.req_pool_idx[r];
-        const ReqQ8 q = req_q8(a, Lp, rq, blockIdx.x == 0);
-        slen[r] = q.len;
-        srow[r] = q.row;
-        t = (q.len + kTile - 1) / kTile + tree_ticks;
-      }
-      int incl = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(FULL, incl, o);
-        if (lane >= o) incl += y;
-      }
-      __syncthreads();
-      if (lane == 31) wsum[w] = incl;
-      __syncthreads();
-      int before = run;
-      for (int q = 0; q < kWarps; ++q) {
-        if (q < w) before += wsum[q];
-        run += wsum[q];
-      }
-      if (r < a.b) pre[r] = before + incl - t;
-    }
-    if (tid == 0) pre[a.b] = run;
-    __syncthreads();
-  }
-  const long long T = (long long)pre[a.b] * J;  // (the host keeps it below 2^31)
-  // wpc warps a CTA over `ctas` CTAs, every warp with at least one tick
-  const long long grid = gridDim.x;
-  int wpc = int((T + grid * kMinTicks - 1) / (grid * kMinTicks));
-  wpc = wpc < 1 ? 1 : wpc > kWarps ? kWarps : wpc;
-  long long ctas = (T + (long long)wpc * kMinTicks - 1) / ((long long)wpc * kMinTicks);
-  if (ctas > grid) ctas = grid;
-  const long long NW = ctas * wpc < T ? ctas * wpc : T;
-  if (blockIdx.x == 0 && tid == 0) args.table[0] = make_int4(int(NW), wpc, 0, 0);
-  const int me0 = int(blockIdx.x) * wpc, me = me0 + w;
-  if (w >= wpc || me >= NW) return;
-  int S = int(me * T / NW);
-  const int E = int((me + 1) * T / NW);
+  // The warp's range of ticks [S, E) of T; its first unit (r, j), whose ticks are Tr, and tick t of it.
+  long long T = 0, NW = 0;
+  int wpc = kWarps, me0 = 0, me = 0, S = 0, E = 0, r = 0, Tr = 0, j = 0, t = 0;
+  bool solid = CLUSTER;  // whether all of the CTA's warps lie (strictly between the first and the last of) one unit
+  ReqQ8 own{0, -1};      // CLUSTER: the request's history
   auto req_of = [&](int f) {
     int lo = 0, hi = a.b;
     while (hi - lo > 1) {
@@ -196,26 +193,82 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
     }
     return lo;
   };
-  int r = req_of(S), Tr = pre[r + 1] - pre[r];
-  int j, t;
-  {
-    const int rem = S - pre[r] * J;
-    j = rem / Tr;
-    t = rem - j * Tr;
-  }
-  // whether all of the CTA's warps lie strictly between the first and the last of one unit
-  bool solid = false;
-  if (me0 + wpc < NW) {
-    const long long u0 = S - t, c0 = me0 * T / NW, c1 = (long long)(me0 + wpc) * T / NW;
-    solid = u0 < c0 && c1 < u0 + Tr;
+  if (CLUSTER) {
+    r = blockIdx.y / J;
+    j = blockIdx.y - r * J;
+    own = req_q8(a, a.seq_lens[r], a.req_pool_idx[r], blockIdx.x == 0 && j == 0 && tid == 0);
+    Tr = (own.len + kTile - 1) / kTile + tree_ticks;
+    me = blockIdx.x * kWarps + w;
+    const long long warps = gridDim.x * kWarps;
+    S = t = int(me * (long long)Tr / warps);
+    E = int((me + 1) * (long long)Tr / warps);
+  } else {
+    // ---- ticks before each request ----
+    {
+      int run = 0;
+      for (int r0 = 0; r0 < a.b; r0 += kQ8AttThreads) {
+        const int r = r0 + tid;
+        int t = 0;
+        if (r < a.b) {
+          int Lp = a.seq_lens[r], rq = a.req_pool_idx[r];
+          const ReqQ8 q = req_q8(a, Lp, rq, blockIdx.x == 0);
+          slen[r] = q.len;
+          srow[r] = q.row;
+          t = (q.len + kTile - 1) / kTile + tree_ticks;
+        }
+        int incl = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(FULL, incl, o);
+          if (lane >= o) incl += y;
+        }
+        __syncthreads();
+        if (lane == 31) wsum[w] = incl;
+        __syncthreads();
+        int before = run;
+        for (int q = 0; q < kWarps; ++q) {
+          if (q < w) before += wsum[q];
+          run += wsum[q];
+        }
+        if (r < a.b) pre[r] = before + incl - t;
+      }
+      if (tid == 0) pre[a.b] = run;
+      __syncthreads();
+    }
+    T = (long long)pre[a.b] * J;  // (the host keeps it below 2^31)
+    // wpc warps a CTA over `ctas` CTAs, every warp with at least one tick
+    const long long grid = gridDim.x;
+    wpc = int((T + grid * kMinTicks - 1) / (grid * kMinTicks));
+    wpc = wpc < 1 ? 1 : wpc > kWarps ? kWarps : wpc;
+    long long ctas = (T + (long long)wpc * kMinTicks - 1) / ((long long)wpc * kMinTicks);
+    if (ctas > grid) ctas = grid;
+    NW = ctas * wpc < T ? ctas * wpc : T;
+    if (blockIdx.x == 0 && tid == 0) args.table[0] = make_int4(int(NW), wpc, 0, 0);
+    me0 = int(blockIdx.x) * wpc;
+    me = me0 + w;
+    if (w >= wpc || me >= NW) return;
+    S = int(me * T / NW);
+    E = int((me + 1) * T / NW);
+    r = req_of(S);
+    Tr = pre[r + 1] - pre[r];
+    {
+      const int rem = S - pre[r] * J;
+      j = rem / Tr;
+      t = rem - j * Tr;
+    }
+    // whether all of the CTA's warps lie strictly between the first and the last of one unit
+    if (me0 + wpc < NW) {
+      const long long u0 = S - t, c0 = me0 * T / NW, c1 = (long long)(me0 + wpc) * T / NW;
+      solid = u0 < c0 && c1 < u0 + Tr;
+    }
   }
   if (t > Tr - tree_ticks && (t - (Tr - tree_ticks)) % kTreeTicks) {  // inside a tree tile, which is the warp's that holds its first tick
     const int skip = kTreeTicks - (t - (Tr - tree_ticks)) % kTreeTicks;
-    if (lane < kRowTile) args.slot_ml[size_t(2 * me) * kRowTile + lane] = make_float2(-INFINITY, 0.f);
+    if (!CLUSTER && lane < kRowTile) args.slot_ml[size_t(2 * me) * kRowTile + lane] = make_float2(-INFINITY, 0.f);
     __syncwarp();
     S += skip;
     t += skip;
-    if (t == Tr) {
+    if (!CLUSTER && t == Tr) {
       t = 0;
       if (++j == J) {
         j = 0;
@@ -224,7 +277,7 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
       }
     }
   }
-  if (lane == 0) args.table[1 + me] = make_int4(-1, 0, 0, 0);
+  if (!CLUSTER && lane == 0) args.table[1 + me] = make_int4(-1, 0, 0, 0);
 
   unsigned char* mine = smem + size_t(w) * L::kWarp;
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
@@ -244,17 +297,18 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
     l_unit = -1;
     l_word = 0;
     if (f < E) {
-      const int fr = req_of(f), fT = pre[fr + 1] - pre[fr];
-      const int rem = f - pre[fr] * J, fj = rem / fT, ft = rem - fj * fT;
-      if (ft < fT - tree_ticks && srow[fr] >= 0) {
-        const int pid = a.page_table[size_t(srow[fr]) * a.row_pages + (ft >> SHIFT)];
+      const int fr = CLUSTER ? r : req_of(f), fT = CLUSTER ? Tr : pre[fr + 1] - pre[fr];
+      const int rem = CLUSTER ? f : f - pre[fr] * J, fj = CLUSTER ? j : rem / fT, ft = CLUSTER ? f : rem - fj * fT;
+      const int row = CLUSTER ? own.row : srow[fr], len = CLUSTER ? own.len : slen[fr];
+      if (ft < fT - tree_ticks && row >= 0) {
+        const int pid = a.page_table[size_t(row) * a.row_pages + (ft >> SHIFT)];
         if (pid < 0 || pid >= a.num_pages) {
           raise_error(a.error, SPEC_DEV_INDEX);
           l_unit = 0;
           l_word = uint32_t(kExpBias) << 16 | uint32_t(kExpBias) << 24;
         } else {
           l_unit = pid * a.Hkv + fj / args.m_tiles;
-          l_word = uint32_t(ft & ((1 << SHIFT) - 1)) * kTile | uint32_t(min(kTile, slen[fr] - ft * kTile)) << 8 |
+          l_word = uint32_t(ft & ((1 << SHIFT) - 1)) * kTile | uint32_t(min(kTile, len - ft * kTile)) << 8 |
                    uint32_t(a.k_scales[l_unit]) << 16 | uint32_t(a.v_scales[l_unit]) << 24;
         }
       }
@@ -622,7 +676,7 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
           }
       }
     }
-    if (unit_end && t_first == 0) {  // the whole unit
+    if (!CLUSTER && unit_end && t_first == 0) {  // the whole unit
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int rg = mt * kRowTile + g + 8 * i;
@@ -661,9 +715,9 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
         ml[g] = make_float2(m[0], lt[0]);
         ml[g + 8] = make_float2(m[1], lt[1]);
       }
-      if (lane == 0 && t_first == 0) args.table[1 + me] = make_int4(int(((long long)f_end * NW - 1) / T), r, j, 0);
+      if (!CLUSTER && lane == 0 && t_first == 0) args.table[1 + me] = make_int4(int(((long long)f_end * NW - 1) / T), r, j, 0);
     }
-    if (unit_end) {
+    if (!CLUSTER && unit_end) {
       t = 0;
       if (++j == J) {
         j = 0;
@@ -685,8 +739,47 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
       const float v[4] = {y.x, y.y, y.z, y.w};
       join<4>(Mx, Ls, acc, ml[q * kRowTile].x, ml[q * kRowTile].y, v);
     }
-    args.slot_o[size_t(2 * me0) * (32 * NT) + x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    if ((x & 3) == 0 && (x / 32) % (NT / 2) == 0) args.slot_ml[size_t(2 * me0) * kRowTile + row] = make_float2(Mx, Ls);
+    const bool first = (x & 3) == 0 && (x / 32) % (NT / 2) == 0;
+    if (CLUSTER) {
+      reinterpret_cast<float4*>(smem + L::kScan)[x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (first) reinterpret_cast<float2*>(smem + L::kScan + L::kFrag)[row] = make_float2(Mx, Ls);
+    } else {
+      args.slot_o[size_t(2 * me0) * (32 * NT) + x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (first) args.slot_ml[size_t(2 * me0) * kRowTile + row] = make_float2(Mx, Ls);
+    }
+  }
+  if (CLUSTER) {
+    // ---- and the cluster's CTAs each a share of the words ----
+    cluster_sync();
+    const int share = 32 * NT / gridDim.x;  // (gridDim.x: 1, 2, 4 or 8 CTAs)
+    for (int i = tid; i < share; i += kQ8AttThreads) {
+      const int x = blockIdx.x * share + i, e = x >> 5, l = x & 31;
+      const int row = (l >> 2) + 8 * (e / (NT / 2)), rg = (j % args.m_tiles) * kRowTile + row, h = j / args.m_tiles;
+      float Mx = -INFINITY, Ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+      float4 o[kLargestCluster];
+      float2 ml[kLargestCluster];
+#pragma unroll
+      for (int q = 0; q < kLargestCluster; ++q) {
+        ml[q] = make_float2(-INFINITY, 0.f);
+        if (q < int(gridDim.x)) {
+          ml[q] = cluster_ld2(cluster_addr(smem + L::kScan + L::kFrag + row * 8, q));
+          o[q] = cluster_ld4(cluster_addr(smem + L::kScan + x * 16, q));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kLargestCluster; ++q) {
+        const float v[4] = {o[q].x, o[q].y, o[q].z, o[q].w};
+        join<4>(Mx, Ls, acc, ml[q].x, ml[q].y, v);
+      }
+      if (rg < M) {
+        const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+        const size_t orow = (size_t(r) * a.n + rg / G) * a.Hq + h * G + rg % G;
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + (l & 3) * (D / 4) + 4 * (e % (NT / 2))) =
+            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+        if (a.lse && (l & 3) == 0 && e % (NT / 2) == 0) a.lse[orow] = lse_of(Mx, Ls);
+      }
+    }
+    cluster_sync();  // (no CTA ends while another reads its shared memory)
   }
 }
 
@@ -738,17 +831,39 @@ int launch_rows(const AttentionQ8Params& p, cudaStream_t stream) {
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return SPEC_ERR_LAUNCH;
-  const size_t smem = RowsSmem<D>::bytes(p.b);
-  if (cudaFuncSetAttribute(attention_q8_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
-    return SPEC_ERR_LAUNCH;
   RowsArgs args{p, (p.n * (p.Hq / p.Hkv) + kRowTile - 1) / kRowTile,
                 reinterpret_cast<int4*>(p.partials + kQ8SlotMlBytes - kQ8BegunBytes),
                 reinterpret_cast<float4*>(p.partials + kQ8SlotMlBytes), reinterpret_cast<float2*>(p.partials)};
+  const long long units = (long long)p.b * p.Hkv * args.m_tiles;
+  const long long ticks = (long long)(p.max_seq_len / kTile) + 1 + kTreeTicks * ((p.n + kTile - 1) / kTile);  // of a unit at most
+  const int cluster = cluster_of(units, sms);
+  if (cluster > 0 && ticks <= kClusterTicks * cluster * kWarps) {
+    constexpr int bytes = RowsSmem<D>::kUnitBytes;
+    if (cudaFuncSetAttribute(attention_q8_rows_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return SPEC_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster, unsigned(units));
+    cfg.blockDim = dim3(kQ8AttThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, attention_q8_rows_kernel<D, true>, args) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+  }
+  const size_t smem = RowsSmem<D>::bytes(p.b);
+  if (cudaFuncSetAttribute(attention_q8_rows_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+    return SPEC_ERR_LAUNCH;
   const int grid = sms < kQ8MaxCtas ? sms : kQ8MaxCtas;
-  if (launch_pdl(attention_q8_rows_kernel<D>, dim3(grid), dim3(kQ8AttThreads), smem, stream, args) != cudaSuccess)
+  if (launch_pdl(attention_q8_rows_kernel<D, false>, dim3(grid), dim3(kQ8AttThreads), smem, stream, args) != cudaSuccess)
     return SPEC_ERR_LAUNCH;
   // (warps there can be at most: the second kernel's blocks beyond those that run leave at once)
-  const long long most = ((long long)(p.max_seq_len / kTile) + 1 + kTreeTicks * ((p.n + kTile - 1) / kTile)) * p.b * p.Hkv * args.m_tiles / kMinTicks + kWarps;
+  const long long most = ticks * units / kMinTicks + kWarps;
   const int warps = most < grid * kWarps ? int(most) : grid * kWarps;
   return launch_pdl(attention_q8_rows_join_kernel<D>, dim3(warps), dim3(4 * D), 0, stream, args) == cudaSuccess ? SPEC_OK
                                                                                                            : SPEC_ERR_LAUNCH;

@@ -22,7 +22,7 @@ def i32(v):
 
 
 class Load:
-    def __init__(self, n, Hq, Hkv, D, page, lens, seed, scale=None, lo=110, hi=122):
+    def __init__(self, n, Hq, Hkv, D, page, lens, seed, scale=None, lo=110, hi=122, bound=None):
         ops = _ops()
         gen = torch.Generator(device=DEV).manual_seed(seed)
         self.b, self.n, self.Hq, self.Hkv, self.D, self.page, self.lens = len(lens), n, Hq, Hkv, D, page, lens
@@ -51,7 +51,7 @@ class Load:
         self.see = see
         bits = (see.long() << torch.arange(n, device=DEV)).sum(-1)
         self.scale = 1 / math.sqrt(D) if scale is None else scale
-        most = max(lens)
+        most = max(lens) if bound is None else bound
         self.ws = ops.Workspace(ops.spec_workspace_size(ops.OP_VERIFY_ATTENTION_Q8, self.b, n, 1, 1, Hq, Hkv, most))
         self.out = torch.empty(self.b * n, Hq, D, dtype=torch.bfloat16, device=DEV)
         self.lse = torch.empty(self.b * n, Hq, device=DEV)
@@ -128,6 +128,26 @@ def test_attention_under_load(n, Hq, Hkv, D, page, lens):
         x.launch()
         assert torch.equal(first, x.out) and torch.equal(z, x.lse)
     assert x.ws.last_error() == 0
+
+
+@pytest.mark.parametrize("bound", [None, 1 << 20])
+@pytest.mark.parametrize("n, Hq, Hkv, D, page, lens", [
+    (1, 1, 1, 64, 16, [0, 1, 65, 130]), (1, 8, 8, 128, 32, [40, 0, 700]), (2, 6, 2, 128, 64, [0, 1, 65, 130]), (3, 5, 1, 64, 16, [2000]),
+    (4, 32, 8, 128, 16, [1000]), (7, 16, 4, 64, 32, [1, 900, 16, 15]), (16, 8, 4, 128, 64, [300, 0, 17]), (32, 4, 4, 64, 16, [129, 1500]),
+    (1, 16, 2, 128, 32, [30000, 5, 0, 17000]), (5, 12, 2, 128, 64, [12000]), (1, 8, 1, 64, 16, [0] * 15 + [4000]), (4, 8, 2, 128, 16, [333] * 36),
+    (4, 8, 2, 64, 32, [100, 0, 3] * 25)])
+def test_attention_by_clusters_and_by_the_whole_gpu(n, Hq, Hkv, D, page, lens, bound):
+    """Few units: a cluster of CTAs takes each (of 8, 4, 2, 1), unless the bound of the lengths allows long ones; then
+    the GPU's warps share the work, and long contexts are joined by CTA first."""
+    x = Load(n, Hq, Hkv, D, page, lens, seed=3 * n + len(lens), bound=bound)
+    x.launch()
+    assert x.ws.last_error() == 0
+    x.check(x.reference())
+    first, z = x.out.clone(), x.lse.clone()
+    for _ in range(5):
+        x.out.fill_(3.0)
+        x.launch()
+        assert torch.equal(first, x.out) and torch.equal(z, x.lse)
 
 
 @pytest.mark.parametrize("scale", [-0.11, 0.0])
