@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_slots_kernel(AllocParams 
 
 int launch_alloc_slots(const AllocParams& p, cudaStream_t stream) {
   const size_t smem = size_t(2) * (p.b + 1) * 4;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(alloc_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+  // (the most, so that calls of two threads agree)
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(alloc_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               2 * (kAllocMaxB + 1) * 4) != cudaSuccess)
     return SPEC_ERR_LAUNCH;
   // as many CTAs as the largest possible call has shares, up to four a SM
   const long long most = (long long)p.b * p.max_new < p.slot_cap ? (long long)p.b * p.max_new : p.slot_cap;

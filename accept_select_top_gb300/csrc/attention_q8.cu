@@ -51,7 +51,7 @@ namespace {
 
 constexpr int kWarps = 12;
 constexpr int kQ8AttThreads = 32 * kWarps;
-// Query rows a kv head up to which this kernel is taken: its time goes with the 16-row tiles, the tcgen05
+// Query rows a kv head up to which this kernel is taken (more, where clusters take the units): its time goes with the 16-row tiles, the tcgen05
 // kernel's hardly (in us, this one / that one; 8 kv heads of 128): 32 rows, eight contexts of 16384 109 / 104,
 // 64 ragged ones to 4096 110 / 236; 48 rows, 16 of 4096 83 / 70, 32 of 2048 86 / 94; 64 rows, 16 of 4096
 // 97 / 70, eight of 16384 177 / 105.
@@ -70,7 +70,9 @@ constexpr int kTreeTicks = 8;
 // warp gets at most so many ticks; else the warps of the whole GPU share the work, and a second
 // launch joins it.  In us, cluster / whole GPU, 32 / 8 heads of 128: one request, one token, 1000 keys 10.6 /
 // 18.8, 8000 15.6 / 27.5, 32000 28.6 / 35.4, 60000 (39 ticks) 44.5 / 45.4; 16 requests of 4000 31.1 / 47.1.
-constexpr int kClusterTicks = 32;
+// With more than kRowsMost query rows, against the tcgen05 kernel: one request of 2000 keys, 64 rows 14.9 / 29.1, 256 rows
+// 22.1 / 26.4; of 4000, 256 rows (24 ticks) 30.9 / 29.8; two of 4000, 128 rows 29.8 / 32.8.
+constexpr int kClusterTicks = 32, kClusterTicksTall = 20;
 constexpr int kLargestCluster = 8;
 inline int cluster_of(long long units, int sms) {
   return units <= 14 ? 8 : units <= 34 ? 4 : units <= 72 ? 2 : units <= sms ? 1 : 0;
@@ -825,24 +827,31 @@ __global__ void __launch_bounds__(4 * D, 3) attention_q8_rows_join_kernel(const 
   if (a.lse && (lane & 3) == 0 && e % (NT / 2) == 0) a.lse[orow] = lse_of(Mx, Ls);
 }
 
+// The units of a call, the ticks of one at most, and the CTAs of a cluster that takes one (0: none does).
+struct RowsPlan {
+  int m_tiles, cluster;
+  long long units, ticks;
+  RowsPlan(const AttentionQ8Params& p, int sms) {
+    const int rows = p.n * (p.Hq / p.Hkv);
+    m_tiles = (rows + kRowTile - 1) / kRowTile;
+    units = (long long)p.b * p.Hkv * m_tiles;
+    ticks = (long long)(p.max_seq_len / kTile) + 1 + kTreeTicks * ((p.n + kTile - 1) / kTile);
+    cluster = cluster_of(units, sms);
+    if (ticks > (long long)(rows <= kRowsMost ? kClusterTicks : kClusterTicksTall) * cluster * kWarps) cluster = 0;
+  }
+};
+
 template <int D>
-int launch_rows(const AttentionQ8Params& p, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return SPEC_ERR_LAUNCH;
-  RowsArgs args{p, (p.n * (p.Hq / p.Hkv) + kRowTile - 1) / kRowTile,
+int launch_rows(const AttentionQ8Params& p, const RowsPlan& plan, int sms, cudaStream_t stream) {
+  RowsArgs args{p, plan.m_tiles,
                 reinterpret_cast<int4*>(p.partials + kQ8SlotMlBytes - kQ8BegunBytes),
                 reinterpret_cast<float4*>(p.partials + kQ8SlotMlBytes), reinterpret_cast<float2*>(p.partials)};
-  const long long units = (long long)p.b * p.Hkv * args.m_tiles;
-  const long long ticks = (long long)(p.max_seq_len / kTile) + 1 + kTreeTicks * ((p.n + kTile - 1) / kTile);  // of a unit at most
-  const int cluster = cluster_of(units, sms);
-  if (cluster > 0 && ticks <= kClusterTicks * cluster * kWarps) {
+  if (plan.cluster > 0) {
     constexpr int bytes = RowsSmem<D>::kUnitBytes;
     if (cudaFuncSetAttribute(attention_q8_rows_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
       return SPEC_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(cluster, unsigned(units));
+    cfg.gridDim = dim3(plan.cluster, unsigned(plan.units));
     cfg.blockDim = dim3(kQ8AttThreads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = stream;
@@ -850,20 +859,21 @@ int launch_rows(const AttentionQ8Params& p, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.x = plan.cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, attention_q8_rows_kernel<D, true>, args) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
   }
   const size_t smem = RowsSmem<D>::bytes(p.b);
-  if (cudaFuncSetAttribute(attention_q8_rows_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+  if (cudaFuncSetAttribute(attention_q8_rows_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           int(RowsSmem<D>::bytes(kAttentionQ8MaxB))) != cudaSuccess)  // (the most, so that calls of two threads agree)
     return SPEC_ERR_LAUNCH;
   const int grid = sms < kQ8MaxCtas ? sms : kQ8MaxCtas;
   if (launch_pdl(attention_q8_rows_kernel<D, false>, dim3(grid), dim3(kQ8AttThreads), smem, stream, args) != cudaSuccess)
     return SPEC_ERR_LAUNCH;
   // (warps there can be at most: the second kernel's blocks beyond those that run leave at once)
-  const long long most = ticks * units / kMinTicks + kWarps;
+  const long long most = plan.ticks * plan.units / kMinTicks + kWarps;
   const int warps = most < grid * kWarps ? int(most) : grid * kWarps;
   return launch_pdl(attention_q8_rows_join_kernel<D>, dim3(warps), dim3(4 * D), 0, stream, args) == cudaSuccess ? SPEC_OK
                                                                                                            : SPEC_ERR_LAUNCH;
@@ -874,8 +884,13 @@ int launch_rows(const AttentionQ8Params& p, cudaStream_t stream) {
 size_t attention_q8_partial_bytes() { return kQ8SlotMlBytes + size_t(2) * kQ8MaxCtas * kQ8SlotRows * 128 * 4; }
 
 int launch_attention_q8(const AttentionQ8Params& p, cudaStream_t stream) {
-  if (p.n * (p.Hq / p.Hkv) > kRowsMost) return launch_attention_q8_tc(p, stream);
-  return p.D == 128 ? launch_rows<128>(p, stream) : launch_rows<64>(p, stream);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return SPEC_ERR_LAUNCH;
+  const RowsPlan plan(p, sms);
+  if (p.n * (p.Hq / p.Hkv) > kRowsMost && plan.cluster == 0) return launch_attention_q8_tc(p, stream);
+  return p.D == 128 ? launch_rows<128>(p, plan, sms, stream) : launch_rows<64>(p, plan, sms, stream);
 }
 
 }  // namespace spec

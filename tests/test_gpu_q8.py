@@ -266,7 +266,14 @@ def test_commit_bad_input_is_skipped():
 
 # -------------------------------------------------------------- attention
 
+@pytest.fixture(params=[0, 1 << 20], ids=["tight", "loose"])
+def bounds(request, monkeypatch):
+    monkeypatch.setattr(Att, "bound", request.param)
+
+
 class Att:
+    bound = 0  # of the lengths, at least: a loose one keeps a few short units from being taken by clusters
+
     def __init__(self, b, n, Hq, Hkv, D, page, lens, seed=0, masks=None, packed=False, scale=None, **kw):
         self.n, self.Hq, self.Hkv, self.D, self.page, self.lens = n, Hq, Hkv, D, page, lens
         gen = _gen(seed)
@@ -294,7 +301,7 @@ class Att:
             q, k, v = x[:, :self.Hq], x[:, self.Hq:self.Hq + self.Hkv], x[:, self.Hq + self.Hkv:self.Hq + 2 * self.Hkv]
         else:
             q, k, v = (t.contiguous().to(DEV) for t in (self.q, self.k, self.v))
-        most = max(self.lens + [0])
+        most = max(self.lens + [self.bound])
         masks = torch.tensor([m - (1 << 64) if m >> 63 else m for m in self.masks], dtype=torch.int64, device=DEV)
         self.ws = ops.Workspace(ops.spec_workspace_size(ops.OP_VERIFY_ATTENTION_Q8, self.b, self.n, 1, 1, self.Hq, self.Hkv, most))
         self.out = torch.full((self.b * self.n, self.Hq, self.D), 7.0, dtype=torch.bfloat16, device=DEV)
@@ -327,6 +334,7 @@ class Att:
         return self
 
 
+@pytest.mark.usefixtures("bounds")
 @pytest.mark.parametrize("page", [16, 32, 64])
 @pytest.mark.parametrize("n, Hq, Hkv, D", [
     (1, 1, 1, 64), (1, 8, 8, 128), (1, 32, 4, 128), (2, 6, 2, 128), (3, 5, 1, 64), (4, 32, 8, 128), (7, 12, 4, 64), (16, 8, 2, 128), (17, 3, 3, 64),
@@ -335,6 +343,7 @@ def test_attention_sizes(page, n, Hq, Hkv, D):
     Att(4, n, Hq, Hkv, D, page, [0, 1, 65, 130], seed=n * Hq + page, packed=n % 2 == 0).run()
 
 
+@pytest.mark.usefixtures("bounds")
 @pytest.mark.parametrize("n, Hq, Hkv", [(1, 4, 1), (4, 4, 1), (20, 4, 1), (64, 4, 1)])
 @pytest.mark.parametrize("lens", [[1500], [2047, 3, 0, 17, 16, 15], [0, 0, 0], [31] * 40 + [900]])
 def test_attention_ragged(n, Hq, Hkv, lens):
@@ -342,12 +351,14 @@ def test_attention_ragged(n, Hq, Hkv, lens):
     Att(len(lens), n, Hq, Hkv, 128, 16, lens, seed=len(lens) + n).run()
 
 
+@pytest.mark.usefixtures("bounds")
 @pytest.mark.parametrize("n, Hq, Hkv, D", [(1, 8, 1, 128), (4, 16, 4, 64), (64, 4, 1, 128)])
 def test_attention_many_requests(n, Hq, Hkv, D):
     lens = [(37 * i) % 200 for i in range(90)]
     Att(90, n, Hq, Hkv, D, 32, lens, seed=1).run()
 
 
+@pytest.mark.usefixtures("bounds")
 @pytest.mark.parametrize("n", [1, 5, 40, 64])
 def test_attention_masks_that_leave_rows_empty(n):
     masks = [0, 0, 1, 0][:3] * 60 if n == 1 else None
@@ -356,6 +367,7 @@ def test_attention_masks_that_leave_rows_empty(n):
     Att(b, n, 8, 2, 128, 16, [0, 0, 20], masks=masks, seed=n).run()
 
 
+@pytest.mark.usefixtures("bounds")
 @pytest.mark.parametrize("n", [1, 4, 33, 64])
 @pytest.mark.parametrize("D", [64, 128])
 def test_attention_scales_of_every_size(n, D):
@@ -369,12 +381,14 @@ def test_attention_scales_of_every_size(n, D):
     a.run()
 
 
+@pytest.mark.usefixtures("bounds")
 @pytest.mark.parametrize("n", [1, 4, 33, 64])
 def test_attention_peaked_rows(n):
     """Large logits: most rows are one key; the running maximum moves often."""
     Att(2, n, 8, 2, 128, 16, [300, 5], seed=9, scale=1.0, lo=112, hi=114).run()
 
 
+@pytest.mark.usefixtures("bounds")
 @pytest.mark.parametrize("n", [4, 20, 64])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 def test_attention_nonfinite_values_in_masked_nodes(n, value):
@@ -408,6 +422,7 @@ def test_attention_nonfinite_values_in_masked_nodes(n, value):
     a.check(got, lse, clean)
 
 
+@pytest.mark.usefixtures("bounds")
 @pytest.mark.parametrize("n", [1, 4, 64])
 def test_attention_nan_in_history(n):
     a = Att(2, n, 4, 1, 64, 16, [40, 40], seed=11)
@@ -417,6 +432,7 @@ def test_attention_nan_in_history(n):
     assert bad[:n, :, 9].all() and bad.sum() == n * 4
 
 
+@pytest.mark.usefixtures("bounds")
 def test_attention_bad_input():
     """Wrong lengths, rows and page ids are reported; nothing is read out of range and the other requests keep their results
     (within the bars: another total of keys splits the work elsewhere)."""
@@ -448,6 +464,7 @@ def test_attention_bad_input():
         call(0, (0, 1, 2))
 
 
+@pytest.mark.usefixtures("bounds")
 @pytest.mark.parametrize("n, lens", [(1, [1000, 3]), (4, [700, 50, 0]), (64, [700, 50])])
 def test_attention_captured_twice_and_on_another_stream(n, lens):
     """Two graphs that share one workspace, replayed in turn, and an eager call on a side stream: the same bits each time."""
@@ -483,6 +500,7 @@ def test_attention_captured_twice_and_on_another_stream(n, lens):
     assert a.ws.last_error() == 0
 
 
+@pytest.mark.usefixtures("bounds")
 def test_attention_without_lse_and_idle_batch():
     ops = _ops()
     a = Att(2, 4, 8, 2, 64, 16, [20, 33], seed=15)

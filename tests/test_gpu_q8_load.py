@@ -135,7 +135,8 @@ def test_attention_under_load(n, Hq, Hkv, D, page, lens):
     (1, 1, 1, 64, 16, [0, 1, 65, 130]), (1, 8, 8, 128, 32, [40, 0, 700]), (2, 6, 2, 128, 64, [0, 1, 65, 130]), (3, 5, 1, 64, 16, [2000]),
     (4, 32, 8, 128, 16, [1000]), (7, 16, 4, 64, 32, [1, 900, 16, 15]), (16, 8, 4, 128, 64, [300, 0, 17]), (32, 4, 4, 64, 16, [129, 1500]),
     (1, 16, 2, 128, 32, [30000, 5, 0, 17000]), (5, 12, 2, 128, 64, [12000]), (1, 8, 1, 64, 16, [0] * 15 + [4000]), (4, 8, 2, 128, 16, [333] * 36),
-    (4, 8, 2, 64, 32, [100, 0, 3] * 25)])
+    (4, 8, 2, 64, 32, [100, 0, 3] * 25), (33, 7, 1, 128, 16, [200, 0, 1000]), (63, 4, 1, 64, 64, [65, 1]), (64, 10, 2, 128, 32, [0, 300]),
+    (48, 8, 8, 64, 16, [129]), (64, 16, 2, 64, 16, [1500])])
 def test_attention_by_clusters_and_by_the_whole_gpu(n, Hq, Hkv, D, page, lens, bound):
     """Few units: a cluster of CTAs takes each (of 8, 4, 2, 1), unless the bound of the lengths allows long ones; then
     the GPU's warps share the work, and long contexts are joined by CTA first."""
