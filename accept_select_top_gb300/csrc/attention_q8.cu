@@ -43,6 +43,7 @@
 #include "kernels.cuh"
 
 #include "attention_q8.cuh"
+#include "cluster.cuh"
 #include "e4m3.cuh"
 
 namespace spec {
@@ -141,26 +142,6 @@ struct Raw16 {
 };
 __device__ __forceinline__ uint32_t scaled_f16(uint32_t w, float inv) { return pack_f16(bf16_lo(w) * inv, bf16_hi(w) * inv); }
 __device__ __forceinline__ uint32_t word_of(const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
-
-// Distributed shared memory: the address of `p` in CTA `rank` of the cluster, and reads of it.
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 cluster_ld4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ float2 cluster_ld2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // CLUSTER: a cluster of CTAs takes one unit (grid: cluster, units) and joins it by itself.
 template <int D, bool CLUSTER>
@@ -850,20 +831,10 @@ int launch_rows(const AttentionQ8Params& p, const RowsPlan& plan, int sms, cudaS
     constexpr int bytes = RowsSmem<D>::kUnitBytes;
     if (cudaFuncSetAttribute(attention_q8_rows_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
       return SPEC_ERR_LAUNCH;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(plan.cluster, unsigned(plan.units));
-    cfg.blockDim = dim3(kQ8AttThreads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = plan.cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, attention_q8_rows_kernel<D, true>, args) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+    return launch_cluster(attention_q8_rows_kernel<D, true>, plan.cluster, dim3(plan.cluster, unsigned(plan.units)), dim3(kQ8AttThreads), bytes,
+                          stream, args) == cudaSuccess
+               ? SPEC_OK
+               : SPEC_ERR_LAUNCH;
   }
   const size_t smem = RowsSmem<D>::bytes(p.b);
   if (cudaFuncSetAttribute(attention_q8_rows_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,

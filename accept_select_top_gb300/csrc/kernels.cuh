@@ -403,11 +403,8 @@ struct LogprobParams {
   int32_t* top_ids;            // [b, W, k]
   float* top_logprobs;
   uint32_t* error;
-  uint32_t* counters;          // one a request (zero between calls)
-  unsigned char* partials;
 };
 constexpr int kLogprobMaxK = 32;  // alternatives of a row
-size_t logprob_partial_bytes(long rows, int V);
 int launch_token_logprobs(const LogprobParams& p, cudaStream_t stream);
 
 }  // namespace spec

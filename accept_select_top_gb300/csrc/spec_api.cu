@@ -101,8 +101,6 @@ size_t partial_bytes(int op, int b, int n, int k, int V, int Hq, int Hkv, int ma
       return commit_partial_bytes(b, n);
     case SPEC_OP_VERIFY_ATTENTION_Q8:
       return attention_q8_partial_bytes();
-    case SPEC_OP_TOKEN_LOGPROBS:
-      return logprob_partial_bytes(long(b) * n, V);
     default:
       return 0;
   }
@@ -966,8 +964,8 @@ int spec_token_logprobs(int b, int n, int W, int V, int dtype, const void* logit
   if (b < 0 || n < 1 || n > kMaxN || W < 1 || W > kMaxN + 1 || V < 1 || k < 0 || k > kLogprobMaxK || k > V ||
       (!row_index && W > n))
     return SPEC_ERR_ARG;
-  if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || V > (1 << 22)) return SPEC_ERR_UNSUPPORTED;
-  if (int64_t(b) * n >= (int64_t(1) << 31) || int64_t(b) * W * kMaxChunks >= (int64_t(1) << 31)) return SPEC_ERR_ARG;
+  if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || V > (1 << 20)) return SPEC_ERR_UNSUPPORTED;
+  if (int64_t(b) * n >= (int64_t(1) << 31) || int64_t(b) * W * 8 >= (int64_t(1) << 31)) return SPEC_ERR_ARG;
   if (b == 0) return SPEC_OK;
   if (!logits || !tokens || !logprobs || (k > 0 && (!top_ids || !top_logprobs))) return SPEC_ERR_ARG;
   if (!aligned(logits, size_t(elem_bytes(dtype)))) return SPEC_ERR_ARG;
@@ -991,8 +989,6 @@ int spec_token_logprobs(int b, int n, int W, int V, int dtype, const void* logit
   p.top_ids = top_ids;
   p.top_logprobs = top_logprobs;
   p.error = v.error;
-  p.counters = v.counters;
-  p.partials = v.partials;
   return launch_token_logprobs(p, as_stream(stream));
 }
 

@@ -17,13 +17,15 @@
 // maximum reaches it are read again (from L2), their logits that reach it are
 // ranked by counting.  Rows need no alignment: the logits before a row's first
 // 16-byte boundary and behind its last are one more batch.
-//   Chunks leave (M, s, t) and their k best; the CTA that arrives last of a
-// request joins the request's rows, one warp a row.
+//   The chunks of a row are a cluster: each leaves (M, s, t) and its k best in its
+// shared memory, and the first CTA joins them.
 //
 // Bound: the logits' bytes, read once, for many rows: 1024 fp32 rows of 129280 with 20
-// alternatives take 94 us (5.7 TB/s).  Few rows are latency: 32 requests' 224 rows of
-// 128256 bf16 logits, about half of them counting, 17.8 us, of which the selection, the
-// arrival and the join take some 8; four rows of 50257 8.3 us.
+// alternatives take 90 us (5.9 TB/s).  Few rows are latency: 32 requests' 224 rows of
+// 128256 bf16 logits, about half of them counting, 15 us, of which the selection and
+// the join take some 5; four rows of 50257 6.5 us (8.3 us where the chunks met through
+// the workspace and an arrival counter).
+#include "cluster.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -35,8 +37,9 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxBatches = 16;  // of a chunk: at most 131072 logits
 constexpr int kListCap = 512;    // batches read again, and logits ranked; more (long ties) take the slow path
-constexpr int kJoinCap = kListCap / kLpWarps;  // entries ranked when chunks are joined; more take the slow path
-constexpr size_t kLpPartBytes = 16 + size_t(kLogprobMaxK) * 8;
+constexpr int kLpCluster = 8;    // chunks of a row at most: a cluster of CTAs
+constexpr long kLpCtas = 912;    // CTAs up to which rows are cut
+constexpr int kJoinCap = 128;  // entries ranked when chunks are joined; more take the slow path
 
 struct LpArgs {
   LogprobParams p;
@@ -129,8 +132,8 @@ __device__ void blank_row(const LogprobParams& a, int out_row) {
   }
 }
 
-// (four CTAs a SM for fp32: the compiler's own choice, five with 48 registers, keeps fewer loads
-// in flight, 103 against 94 us; for bf16 three with 72 registers, 17.8 against 19.6 us by four)
+// (four CTAs a SM for fp32: with five, the compiler's own choice of 48 registers, fewer loads are in
+// flight, 99 against 91 us)
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 1) token_logprobs_kernel(LpArgs args) {
   constexpr int E = VecOps<T>::E, U = kBatch / E;
@@ -140,29 +143,26 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 1) token_logp
   __shared__ float cv[kListCap];
   __shared__ int ci[kListCap], list[kListCap];
   __shared__ int n_list, n_cand;
-  __shared__ float tv[kLpWarps][kLogprobMaxK];
-  __shared__ int ti[kLpWarps][kLogprobMaxK];
+  __shared__ float tv[2][kLogprobMaxK];  // the chunk's best, the row's
+  __shared__ int ti[2][kLogprobMaxK];
+  __shared__ __align__(16) LpPart part;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   // (the first row of every request, then the second: where only some count, those start together)
-  const int rw = blockIdx.x / args.chunks, ch = blockIdx.x % args.chunks, req = rw % a.b, out_row = req * a.W + rw / a.b;
-  auto row_at = [&](int r, bool report) {
-    long long i = a.row_index ? a.row_index[r] : (long long)(r / a.W) * a.n + r % a.W;
-    if (i >= (long long)a.b * a.n) {
-      if (report) raise_error(a.error, SPEC_DEV_INDEX);
-      i = -1;
-    }
-    return i;
-  };
-  const long long idx = row_at(out_row, ch == 0 && tid == 0);
-  if (idx < 0 && args.chunks == 1) {
-    if (w == 0) blank_row(a, out_row);
+  const int rw = blockIdx.x / args.chunks, ch = blockIdx.x % args.chunks, out_row = rw % a.b * a.W + rw / a.b;
+  long long idx = a.row_index ? a.row_index[out_row] : (long long)(out_row / a.W) * a.n + out_row % a.W;
+  if (idx >= (long long)a.b * a.n) {
+    if (ch == 0 && tid == 0) raise_error(a.error, SPEC_DEV_INDEX);
+    idx = -1;
+  }
+  if (idx < 0) {  // (the whole cluster)
+    if (ch == 0 && w == 0) blank_row(a, out_row);
     return;
   }
   float M = -INFINITY, s = 0.f, t = 0.f, c = 0.f;
   int count = 0;
-  if (idx >= 0) {
+  {
     if (tid == 0) n_list = n_cand = 0;
     c = scale_of_row(a, idx);
     const LpRow<T> row(a.logits, idx, a.V);
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 1) token_logp
       }
     }
     LpToken token{-1, 0.f};
-    if (args.chunks == 1 && tid == 0) token = token_of<T>(a, a.tokens[out_row], idx);
+    if (ch == 0 && tid == 0) token = token_of<T>(a, a.tokens[out_row], idx);
     // ---- the chunk's maximum and sums; the 32 group maxima ----
     gmax[w][lane] = m;
     __syncthreads();
@@ -338,136 +338,119 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 1) token_logp
       if (w == 0) finish_row(a, out_row, token, M, s, t, c, count, tv[0], ti[0]);
       return;
     }
-    unsigned char* part = a.partials + (size_t(out_row) * args.chunks + ch) * kLpPartBytes;
-    if (tid == 0) *reinterpret_cast<LpPart*>(part) = LpPart{M, s, t, count};
-    if (tid < count) reinterpret_cast<float2*>(part + 16)[tid] = make_float2(tv[0][tid], __int_as_float(ti[0][tid]));
-  }
-  // ---- the last CTA of the request joins its rows, one warp a row, one lane a chunk ----
-  if (!arrive_last(a.counters + req, uint32_t(a.W) * uint32_t(args.chunks))) return;
-  for (int r = w; r < a.W; r += kLpWarps) {
-    const int orow = req * a.W + r;
-    const long long ix = row_at(orow, false);
-    if (ix < 0) {
-      blank_row(a, orow);
-      continue;
-    }
-    const int tok = a.tokens[orow];
-    const float cc = scale_of_row(a, ix);
-    const unsigned char* parts = a.partials + size_t(orow) * args.chunks * kLpPartBytes;
-    const unsigned char* part = parts + lane * kLpPartBytes;
-    auto entry = [&](const unsigned char* p, int at) { return __ldcg(reinterpret_cast<const float2*>(p + 16) + at); };
-    const int all = args.chunks * a.k;
-    float4 h = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    float kth = 0.f;
-    if (lane < args.chunks) {
-      h = __ldcg(reinterpret_cast<const float4*>(part));
-      if (a.k > 0) kth = entry(part, a.k - 1).x;
-    }
-    const LpToken token = token_of<T>(a, tok, ix);
-    float pM = -INFINITY, ps = 0.f, pt = 0.f;
-    int pc = 0;
-    float theta = -INFINITY;  // at least k logits reach it: the largest of the chunks' k-th best
-    if (lane < args.chunks) {
-      pM = h.x;
-      ps = h.y;
-      pt = h.z;
-      pc = __float_as_int(h.w);
-      if (pc == a.k) theta = kth;  // (else it was not written)
-    }
-    const float jM = warp_max(pM);
-    const float d = fmaxf((pM - jM) * cc, -150.f), f = fast_exp2(d);
-    const float js = warp_sum(ps > 0.f ? f * ps : 0.f), jt = warp_sum(ps > 0.f ? f * fmaf(d, ps, pt) : 0.f);
-    int got = 0;
-    if (a.k > 0) {
-      theta = warp_max(theta);
-      // the entries that reach theta, ranked by counting
-      float* qv = cv + w * kJoinCap;
-      int* qi = ci + w * kJoinCap;
-      int nc = 0;
+    if (tid == 0) part = LpPart{M, s, t, count};
+    // ---- the row's first CTA joins the chunks, a lane a chunk ----
+    cluster_sync();
+    if (ch == 0 && w == 0) {
+      const uint32_t heads = cluster_addr(&part, lane < args.chunks ? lane : 0);
+      auto entry = [&](int q, int at) {
+        return make_float2(cluster_ldf(cluster_addr(&tv[0][at], q)), cluster_ldf(cluster_addr(&ti[0][at], q)));
+      };
+      const int all = args.chunks * a.k;
+      float4 h = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      float kth = 0.f;
+      if (lane < args.chunks) {
+        h = cluster_ld4(heads);
+        if (a.k > 0) kth = entry(lane, a.k - 1).x;
+      }
+      float pM = -INFINITY, ps = 0.f, pt = 0.f;
+      int pc = 0;
+      float theta = -INFINITY;  // at least k logits reach it: the largest of the chunks' k-th best
+      if (lane < args.chunks) {
+        pM = h.x;
+        ps = h.y;
+        pt = h.z;
+        pc = __float_as_int(h.w);
+        if (pc == a.k) theta = kth;  // (else it was not written)
+      }
+      const float jM = warp_max(pM);
+      const float d = fmaxf((pM - jM) * c, -150.f), f = fast_exp2(d);
+      const float js = warp_sum(ps > 0.f ? f * ps : 0.f), jt = warp_sum(ps > 0.f ? f * fmaf(d, ps, pt) : 0.f);
+      int got = 0;
+      if (a.k > 0) {
+        theta = warp_max(theta);
+        // the entries that reach theta, ranked by counting
+        float* qv = cv;
+        int* qi = ci;
+        int nc = 0;
 #pragma unroll 4
-      for (int base = 0; base < all; base += 32) {
-        const int p = base + lane, pch = min(p / a.k, args.chunks - 1), at = p - pch * a.k;
-        const int cnt = __shfl_sync(0xffffffffu, pc, pch);
-        float2 x = make_float2(-INFINITY, 0.f);
-        if (at < cnt) x = entry(parts + pch * kLpPartBytes, at);
-        const bool in = at < cnt && x.x >= theta;
-        const unsigned who = __ballot_sync(0xffffffffu, in);
-        const int to = nc + __popc(who & ((1u << lane) - 1u));
-        if (in && to < kJoinCap) {
-          qv[to] = x.x;
-          qi[to] = __float_as_int(x.y);
+        for (int base = 0; base < all; base += 32) {
+          const int p = base + lane, pch = min(p / a.k, args.chunks - 1), at = p - pch * a.k;
+          const int cnt = __shfl_sync(0xffffffffu, pc, pch);
+          float2 x = make_float2(-INFINITY, 0.f);
+          if (at < cnt) x = entry(pch, at);
+          const bool in = at < cnt && x.x >= theta;
+          const unsigned who = __ballot_sync(0xffffffffu, in);
+          const int to = nc + __popc(who & ((1u << lane) - 1u));
+          if (in && to < kJoinCap) {
+            qv[to] = x.x;
+            qi[to] = __float_as_int(x.y);
+          }
+          nc += __popc(who);
         }
-        nc += __popc(who);
+        __syncwarp();
+        if (nc <= kJoinCap) {
+          got = min(a.k, nc);
+          for (int i = lane; i < nc; i += 32) {
+            int rank = 0;
+            for (int q = 0; q < nc; ++q) rank += better(qv[q], qi[q], qv[i], qi[i]);
+            if (rank < a.k) {
+              tv[1][rank] = qv[i];
+              ti[1][rank] = qi[i];
+            }
+          }
+        } else {
+          // long ties: the chunks' sorted lists, k times the best head
+          int head = 0;
+          for (; got < a.k; ++got) {
+            float bv = -INFINITY;
+            int bi = INT_MAX;
+            if (head < pc) {
+              const float2 x = entry(lane, head);
+              bv = x.x;
+              bi = __float_as_int(x.y);
+            }
+            const int hi = bi;
+            warp_argmax(bv, bi);
+            if (bi == INT_MAX || !(bv > -INFINITY)) break;
+            if (lane == 0) {
+              tv[1][got] = bv;
+              ti[1][got] = bi;
+            }
+            if (hi == bi) ++head;
+          }
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      if (nc <= kJoinCap) {
-        got = min(a.k, nc);
-        for (int i = lane; i < nc; i += 32) {
-          int rank = 0;
-          for (int q = 0; q < nc; ++q) rank += better(qv[q], qi[q], qv[i], qi[i]);
-          if (rank < a.k) {
-            tv[w][rank] = qv[i];
-            ti[w][rank] = qi[i];
-          }
-        }
-      } else {
-        // long ties: the chunks' sorted lists, k times the best head
-        int head = 0;
-        for (; got < a.k; ++got) {
-          float bv = -INFINITY;
-          int bi = INT_MAX;
-          if (head < pc) {
-            const float2 x = entry(part, head);
-            bv = x.x;
-            bi = __float_as_int(x.y);
-          }
-          const int hi = bi;
-          warp_argmax(bv, bi);
-          if (bi == INT_MAX || !(bv > -INFINITY)) break;
-          if (lane == 0) {
-            tv[w][got] = bv;
-            ti[w][got] = bi;
-          }
-          if (hi == bi) ++head;
-        }
-      }
-      __syncwarp();
+      finish_row(a, out_row, token, jM, js, jt, c, got, tv[1], ti[1]);
     }
-    finish_row(a, orow, token, jM, js, jt, cc, got, tv[w], ti[w]);
-    __syncwarp();
+    cluster_sync();  // (no CTA ends while its shared memory is read)
   }
-  __syncthreads();
-  counter_reset(a.counters + req);
 }
 
-// Chunks of a row: about four CTAs a SM in all (each chunk ends in some 4 us of selection and
-// arrival: the 224 rows below took 17.8 us so, 20.3 by five and 23.1 by six), at least 2048 logits and at most
-// kMaxBatches batches a chunk.
+// Chunks of a row: a power of two, for at most kLpCtas CTAs in all (the 224 rows of the header's
+// example in four chunks 15.2 us, in two 20.4, in eight 22.6), of 2048 logits at least
+// and kMaxBatches batches at most.
 int lp_chunks(long rows, int V) {
-  long want = (4 * 152 + rows - 1) / rows;
-  const long by_size = V / 2048 > 1 ? V / 2048 : 1;
-  if (want > by_size) want = by_size;
-  if (want > kMaxChunks) want = kMaxChunks;
-  const long need = (long(V) + kMaxBatches * kBatch * kLpThreads - 1) / (kMaxBatches * kBatch * kLpThreads);
-  if (want < need) want = need;
-  return int(want);
+  int chunks = 1;
+  while (chunks < kLpCluster && 2 * chunks * rows <= kLpCtas && 2 * chunks <= V / 2048) chunks *= 2;
+  while (long(chunks) * kMaxBatches * kBatch * kLpThreads < V) chunks *= 2;  // (the API's largest V takes eight)
+  return chunks;
 }
 
 }  // namespace
 
-size_t logprob_partial_bytes(long rows, int V) { return align256(size_t(rows) * lp_chunks(rows, V) * kLpPartBytes); }
-
 int launch_token_logprobs(const LogprobParams& p, cudaStream_t stream) {
   const long rows = long(p.b) * p.W;
   LpArgs args{p, lp_chunks(rows, p.V), 0};
-  if (args.chunks > kMaxChunks) return SPEC_ERR_UNSUPPORTED;
+  if (args.chunks > kLpCluster) return SPEC_ERR_UNSUPPORTED;
   const int E = p.dtype == SPEC_F32 ? 4 : 8;
   args.vpc = (p.V / E + args.chunks - 1) / args.chunks;
   if (args.vpc < 1) args.vpc = 1;
   const dim3 grid(unsigned(rows * args.chunks));
   const cudaError_t e =
-      p.dtype == SPEC_F32 ? launch_pdl(token_logprobs_kernel<float>, grid, dim3(kLpThreads), 0, stream, args)
-                          : launch_pdl(token_logprobs_kernel<uint16_t>, grid, dim3(kLpThreads), 0, stream, args);
+      p.dtype == SPEC_F32 ? launch_cluster(token_logprobs_kernel<float>, args.chunks, grid, dim3(kLpThreads), 0, stream, args)
+                          : launch_cluster(token_logprobs_kernel<uint16_t>, args.chunks, grid, dim3(kLpThreads), 0, stream, args);
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 

@@ -569,7 +569,7 @@ int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size
  *                        0 <= k <= 32, k <= V (k = 0: both may be NULL)
  * -inf logits have ln p = -inf and no share in the entropy; NaN counts as -inf;
  * a row without any other logit gives ln p -inf everywhere and entropy 0; a row
- * with +inf gives NaN.  W <= 65, V <= 4194304.  HBM-bound: one pass.
+ * with +inf gives NaN.  W <= 65, V <= 1048576.  HBM-bound: one pass.
  * ------------------------------------------------------------------------- */
 int spec_token_logprobs(int b, int n, int W, int V, int dtype, const void* logits, const int32_t* row_index,
                         const int32_t* tokens, const float* temperatures, int k, float* logprobs,
