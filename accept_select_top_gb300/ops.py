@@ -326,23 +326,28 @@ _E4M3 = torch.float8_e4m3fn
 
 def _in(t: torch.Tensor, dtype, least: int, dev: int, what: str) -> int:
     """Address of a contiguous tensor of `dtype` with at least `least` elements on device `dev`."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= least:
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise SpecError(f"{what}: expected {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise SpecError(f"{what}: expected a tensor on the current CUDA device")
     if not t.is_contiguous():
         raise SpecError(f"{what}: expected a contiguous tensor")
-    if t.numel() < least:
-        raise SpecError(f"{what}: {t.numel()} elements, {least} are needed")
-    return t.data_ptr()
+    raise SpecError(f"{what}: {t.numel()} elements, {least} are needed")
 
 
 def _pages_in(t: torch.Tensor, shape, dev: int, what: str) -> int:
     """Address of e4m3 pages [num_pages, Hkv, page_size, D] (float8_e4m3fn, or their bytes)."""
+    if t.dim() != 4 or t.shape[1:] != shape:
+        raise SpecError(f"{what}: expected [num_pages, {', '.join(map(str, shape))}], got {tuple(t.shape)}")
+    return _bytes_in(t, dev, what)
+
+
+def _bytes_in(t: torch.Tensor, dev: int, what: str) -> int:
+    """Address of e4m3 values (or their bytes) of a shape that is known to be right."""
     if t.dtype is not _E4M3 and t.dtype is not torch.uint8:
         raise SpecError(f"{what}: expected float8_e4m3fn or uint8, got {t.dtype}")
-    if t.shape[1:] != shape:
-        raise SpecError(f"{what}: expected [num_pages, {', '.join(map(str, shape))}], got {tuple(t.shape)}")
     if t.get_device() != dev or not t.is_contiguous():
         raise SpecError(f"{what}: expected a contiguous tensor on the current CUDA device")
     return t.data_ptr()
@@ -364,7 +369,7 @@ def _rows_in(t: torch.Tensor, heads: int, D: int, least: int, dev: int, what: st
 
 
 def _device() -> int:
-    return torch.cuda.current_device()
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -475,14 +480,17 @@ def spec_verify_attention_q8(b: int, n: int, Hq: int, Hkv: int, D: int, page_siz
     vp, ldv = _rows_in(v_new, Hkv, D, rows, dev, "v_new")
     if ldv != ld:
         raise SpecError("k_new and v_new must have one row stride")
-    num_pages = k_pages.shape[0]
-    if v_pages.shape[0] != num_pages:
+    pages = k_pages.shape
+    if v_pages.shape != pages:
         raise SpecError("k_pages and v_pages must have as many pages")
-    shape = (Hkv, page_size, D)
+    num_pages = pages[0] if pages else 0
+    shape = (num_pages, Hkv, page_size, D)
+    if pages != shape:
+        raise SpecError(f"k_pages: expected [num_pages, {Hkv}, {page_size}, {D}], got {tuple(pages)}")
     table_rows, row_pages = page_table.shape
     _check(LIB.spec_verify_attention_q8(
-        b, n, Hq, Hkv, D, page_size, qp, q_ld, kp, vp, ld, _pages_in(k_pages, shape, dev, "k_pages"),
-        _pages_in(v_pages, shape, dev, "v_pages"), _in(k_scales, torch.uint8, num_pages * Hkv, dev, "k_scales"),
+        b, n, Hq, Hkv, D, page_size, qp, q_ld, kp, vp, ld, _bytes_in(k_pages, dev, "k_pages"),
+        _bytes_in(v_pages, dev, "v_pages"), _in(k_scales, torch.uint8, num_pages * Hkv, dev, "k_scales"),
         _in(v_scales, torch.uint8, num_pages * Hkv, dev, "v_scales"), num_pages,
         _in(page_table, _I32, 1, dev, "page_table"), table_rows, row_pages,
         _in(req_pool_idx, _I32, b, dev, "req_pool_idx"), _in(seq_lens, _I32, b, dev, "seq_lens"), max_seq_len,

@@ -178,3 +178,25 @@ def test_captured_and_repeated():
     again = run(3, 3, x, None, tok, None, 9, stream=side)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(again[:4], (lp, ent, ids, top)))
+
+
+@pytest.mark.parametrize("V", [1 << 20, (1 << 20) - 5])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_largest_vocabulary(V, dtype):
+    """A row in chunks of as many batches as a chunk may have."""
+    gen = torch.Generator().manual_seed(V)
+    logits = (4 * torch.randn(2, V, generator=gen)).to(dtype)
+    tokens = torch.tensor([[V - 1, 17]], dtype=torch.int32)
+    check(2, 2, logits, None, tokens, None, 32)
+
+
+@pytest.mark.parametrize("b, V", [(1, 5000), (1, 9000), (3, 20000), (40, 70000), (120, 20000), (230, 9001)])
+def test_rows_in_clusters_of_every_size(b, V):
+    """Rows cut into 1, 2, 4 and 8 chunks; some rows left out, in the middle of others."""
+    gen = torch.Generator().manual_seed(b)
+    n, W = 3, 4
+    logits = torch.randn(b * n, V, generator=gen).bfloat16()
+    index = torch.randint(0, b * n, (b, W), generator=gen).to(torch.int32)
+    index[torch.rand(b, W, generator=gen) < 0.3] = -1
+    tokens = torch.randint(0, V, (b, W), generator=gen).to(torch.int32)
+    check(n, W, logits, index, tokens, None, 7)

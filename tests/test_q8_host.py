@@ -156,3 +156,7 @@ def test_commit_refuses_rows_past_32_bits(lib):
     """A row number is kept in 32 bits: one past them would have been dropped without a word."""
     args, keep = _commit(num_rows=1 << 31)
     assert lib.spec_commit_kv_q8(*args) == -1
+
+
+def test_logprobs_refuse_a_vocabulary_past_the_chunks(lib):
+    assert lib.spec_token_logprobs(*_logprobs(V=(1 << 20) + 1)) == -4
