@@ -143,6 +143,16 @@ struct Raw16 {
 __device__ __forceinline__ uint32_t scaled_f16(uint32_t w, float inv) { return pack_f16(bf16_lo(w) * inv, bf16_hi(w) * inv); }
 __device__ __forceinline__ uint32_t word_of(const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
 
+// The larger magnitude halfword by halfword, whatever it is: an inf or a NaN shows as 0x7f80 or
+// more, and only then the finite ones are looked for (a third of the instructions).
+__device__ __forceinline__ uint32_t raw_max(uint32_t m, const uint4& x) {
+  m = __vmaxu2(__vmaxu2(m, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
+  return __vmaxu2(__vmaxu2(m, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
+}
+__device__ __forceinline__ uint32_t finite_max(uint32_t m, const uint4& x) {
+  return max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(m, x.x), x.y), x.z), x.w);
+}
+
 // CLUSTER: a cluster of CTAs takes one unit (grid: cluster, units) and joins it by itself.
 template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(const __grid_constant__ RowsArgs args) {
@@ -353,13 +363,21 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
 #pragma unroll
       for (int u = 0; u < D / 32; ++u)  // 16 elements from 16 c, and 64 + 16 c
         x[u] = on ? __ldg(src + (u >> 1) * 8 + 2 * c + (u & 1)) : make_uint4(0, 0, 0, 0);
+      auto over_row = [&](uint32_t mx) {
+        mx = max(mx & 0xffffu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
+        return max(mx, __shfl_xor_sync(FULL, mx, 2));
+      };
       uint32_t mx = 0;
 #pragma unroll
-      for (int u = 0; u < D / 32; ++u)
-        mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, x[u].x), x[u].y), x[u].z), x[u].w);
-      mx = max(mx & 0xffffu, mx >> 16);
-      mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
-      mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
+      for (int u = 0; u < D / 32; ++u) mx = raw_max(mx, x[u]);
+      mx = over_row(mx);
+      if (__any_sync(FULL, mx >= 0x7f80u)) {
+        mx = 0;
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) mx = finite_max(mx, x[u]);
+        mx = over_row(mx);
+      }
       const int e = norm_exp(mx);
       const float inv = exp_scale(2 * kExpBias - e);
       xf[i] = a.scale * 1.4426950408889634f * exp_scale(e);
@@ -519,13 +537,21 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
 #pragma unroll
         for (int u = 0; u < D / 32; ++u)
           kx[u] = node < a.n ? __ldg(src + (u >> 1) * 8 + 2 * c + (u & 1)) : make_uint4(0, 0, 0, 0);
+        auto over_row = [&](uint32_t mx) {
+          mx = max(mx & 0xffffu, mx >> 16);
+          mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
+          return max(mx, __shfl_xor_sync(FULL, mx, 2));
+        };
         uint32_t mx = 0;
 #pragma unroll
-        for (int u = 0; u < D / 32; ++u)
-          mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, kx[u].x), kx[u].y), kx[u].z), kx[u].w);
-        mx = max(mx & 0xffffu, mx >> 16);
-        mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
-        mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
+        for (int u = 0; u < D / 32; ++u) mx = raw_max(mx, kx[u]);
+        mx = over_row(mx);
+        if (__any_sync(FULL, mx >= 0x7f80u)) {
+          mx = 0;
+#pragma unroll
+          for (int u = 0; u < D / 32; ++u) mx = finite_max(mx, kx[u]);
+          mx = over_row(mx);
+        }
         const int e = norm_exp(mx);
         const float inv = exp_scale(2 * kExpBias - e);
 #pragma unroll
@@ -548,22 +574,30 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
       for (int i = 0; i < 4; ++i) {
         const int node = nb + 2 * c + (i & 1) + 8 * (i >> 1);
         const uint4* src = vrow(node);
+        auto over_row = [&](uint32_t mx) {
+          mx = max(mx & 0xffffu, mx >> 16);
+          mx = max(mx, __shfl_xor_sync(FULL, mx, 4));
+          mx = max(mx, __shfl_xor_sync(FULL, mx, 8));
+          return max(mx, __shfl_xor_sync(FULL, mx, 16));
+        };
+        uint4 x[D / 64];
         uint32_t mx = 0;
-        bool nf = false;
 #pragma unroll
         for (int u = 0; u < D / 64; ++u) {
-          const uint4 x = node < a.n ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-          nf = nf || nonfinite_bf16(x.x) || nonfinite_bf16(x.y) || nonfinite_bf16(x.z) || nonfinite_bf16(x.w);
-          mx = max_abs_bf16(max_abs_bf16(max_abs_bf16(max_abs_bf16(mx, x.x), x.y), x.z), x.w);
+          x[u] = node < a.n ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+          mx = raw_max(mx, x[u]);
         }
-        mx = max(mx & 0xffffu, mx >> 16);
-        mx = max(mx, __shfl_xor_sync(FULL, mx, 4));
-        mx = max(mx, __shfl_xor_sync(FULL, mx, 8));
-        mx = max(mx, __shfl_xor_sync(FULL, mx, 16));
-        evk[i] = norm_exp(mx);
+        mx = over_row(mx);
         // an inf or a NaN must reach the rows that see the node and no
         // other: it is left out of the product and added at the end
-        const unsigned who = __ballot_sync(FULL, nf);
+        const unsigned who = __ballot_sync(FULL, mx >= 0x7f80u);
+        if (who) {
+          mx = 0;
+#pragma unroll
+          for (int u = 0; u < D / 64; ++u) mx = finite_max(mx, x[u]);
+          mx = over_row(mx);
+        }
+        evk[i] = norm_exp(mx);
         if (who) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
