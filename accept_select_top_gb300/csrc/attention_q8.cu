@@ -528,9 +528,16 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
         mask[i] = rg < M ? a.mask_bits[size_t(r) * a.n + rg / G] : 0ull;
       }
       const uint16_t* kn = static_cast<const uint16_t*>(a.k_new) + size_t(h) * D;
+      const bool upper = nb + 8 < a.n;  // whether the tile's second eight rows hold a node
       float s[2][4], kf[2][2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
+        if (q == 1 && !upper) {
+          kf[1][0] = kf[1][1] = 1.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[1][i] = 0.f;
+          continue;
+        }
         const int node = nb + 8 * q + g;
         const uint4* src = reinterpret_cast<const uint4*>(kn + (size_t(r) * a.n + (node < a.n ? node : 0)) * a.new_ld);
         uint4 kx[D / 32];
@@ -572,6 +579,10 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
       int evk[4];  // of nodes 2c, 2c+1, 2c+8, 2c+9
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if (i >= 2 && !upper) {
+          evk[i] = 1;
+          continue;
+        }
         const int node = nb + 2 * c + (i & 1) + 8 * (i >> 1);
         const uint4* src = vrow(node);
         auto over_row = [&](uint32_t mx) {
@@ -657,7 +668,7 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
             const uint32_t wd = word_of(x[i], e >> 1);
             return ((e & 1) ? bf16_hi(wd) : bf16_lo(wd)) * inv[i];
           };
-          mma_f16(o[8 * u + e], pa, pack_f16(el(0), el(1)), pack_f16(el(2), el(3)));
+          mma_f16(o[8 * u + e], pa, pack_f16(el(0), el(1)), upper ? pack_f16(el(2), el(3)) : 0u);
         }
       }
     }
