@@ -27,7 +27,8 @@
 // the head dimension inside a fragment is free as long as Q has the same, and
 // that of the keys as long as P has the same, so both K and V fragments are
 // read as whole 16-byte words.  What limits a warp is the issue of its ~340
-// instructions a tile, so the history's loop is one short body.
+// instructions a tile, so the history's loop is one short body, and what a unit's
+// ends execute counts as much as what they read.
 //   Few units: a cluster of CTAs takes each, its warps equal shares of the unit's
 // tiles, and joins it through distributed shared memory.
 //   Many: the warps of the whole GPU share all the tiles, and there is no
@@ -36,9 +37,10 @@
 // warps behind a barrier and by the last CTA of a unit took 20 us on average, 57 us at
 // most, of a 275 us call).  Only where all the warps of a CTA lie inside one unit does
 // the CTA join its own first, so that a long context leaves few.
-//   256 chains of four, contexts 256 to 4096, 32 / 8 heads of 128: 215 us (1.13 GB
-// of cache at 5.3 TB/s).  A deeper ring is slower (four stages 232 us): with more
-// bytes in flight than the memory needs, the dependent reads at a unit's ends only wait longer.
+//   256 chains of four, contexts 256 to 4096, 32 / 8 heads of 128: 200 us (1.13 GB
+// of cache at 5.6 TB/s); one token over 1000 keys 8.6 us.  A deeper ring is slower (four stages
+// 208 us): with more bytes in flight than the memory needs, the dependent reads at a
+// unit's ends only wait longer.
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -52,27 +54,27 @@ namespace {
 
 constexpr int kWarps = 12;
 constexpr int kQ8AttThreads = 32 * kWarps;
-// Query rows a kv head up to which this kernel is taken (more, where clusters take the units): its time goes with the 16-row tiles, the tcgen05
-// kernel's hardly (in us, this one / that one; 8 kv heads of 128): 32 rows, eight contexts of 16384 109 / 104,
-// 64 ragged ones to 4096 110 / 236; 48 rows, 16 of 4096 83 / 70, 32 of 2048 86 / 94; 64 rows, 16 of 4096
-// 97 / 70, eight of 16384 177 / 105.
+// Query rows a kv head up to which this kernel is taken (more, where clusters take the units): its time goes with
+// the 16-row tiles, the tcgen05 kernel's hardly (in us, this one / that one; 8 kv heads of 128, no clusters): 32 rows,
+// eight contexts of 16384 103 / 104, 64 ragged ones to 4096 100 / 214; 48 rows, 16 of 4096 78 / 70, 32 of 2048
+// 82 / 86; 64 rows, 16 of 4096 92 / 70, eight of 16384 172 / 105.
 constexpr int kRowsMost = 32;
 constexpr int kTile = 16;    // keys of a tile
 constexpr int kRowTile = 16; // query rows of a unit
 constexpr int kRing = 3;     // tiles in a warp's ring
 constexpr int kMinTicks = 2; // a warp gets at least this many ticks before another warp is used
 // Ticks of a tree tile in the division of the work; a history tile is one.  A tree tile and the
-// ends of its unit cost a warp some ten history tiles, nearly all latency; by 2, 4, 8 and 12 ticks the
-// chains above took 254, 236, 232 and 228 us (with four stages), and a single token 1 us more by 12 than by 8.
+// ends of its unit cost a warp some eight history tiles, nearly all latency: by 4, 6, 8 and 10 ticks the
+// chains above take 211, 205, 200 and 198 us, 512 single tokens over 100 to 600 keys 105, 107, 110 and 115.
 constexpr int kTreeTicks = 8;
 
 // A cluster takes a unit and joins it by itself, in one launch, where the units are few enough for
 // all of them to run at once (a GB300 holds 15 clusters of eight such CTAs, 36 of four, 76 of two) and a
 // warp gets at most so many ticks; else the warps of the whole GPU share the work, and a second
-// launch joins it.  In us, cluster / whole GPU, 32 / 8 heads of 128: one request, one token, 1000 keys 10.6 /
-// 18.8, 8000 15.6 / 27.5, 32000 28.6 / 35.4, 60000 (39 ticks) 44.5 / 45.4; 16 requests of 4000 31.1 / 47.1.
-// With more than kRowsMost query rows, against the tcgen05 kernel: one request of 2000 keys, 64 rows 14.9 / 29.1, 256 rows
-// 22.1 / 26.4; of 4000, 256 rows (24 ticks) 30.9 / 29.8; two of 4000, 128 rows 29.8 / 32.8.
+// launch joins it.  In us, cluster / whole GPU, 32 / 8 heads of 128: one request, one token, 1000 keys 8.9 /
+// 17.0, 8000 13.4 / 25.3, 32000 27.2 / 34.1, 60000 (39 ticks) 42.4 / 43.3; 16 requests of 4000 30.1 / 42.0.
+// With more than kRowsMost query rows, against the tcgen05 kernel: one request of 2000 keys, 64 rows 13.8 / 29.1, 256 rows
+// 20.2 / 26.2; of 4000, 256 rows (24 ticks) 29.1 / 29.8; two of 4000, 128 rows 28.1 / 32.3.
 constexpr int kClusterTicks = 32, kClusterTicksTall = 20;
 constexpr int kLargestCluster = 8;
 inline int cluster_of(long long units, int sms) {
