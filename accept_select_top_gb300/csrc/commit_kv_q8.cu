@@ -14,9 +14,9 @@
 // lanes a row), so a unit of a 16-, 32- or 64-token page is 1, 2 or 4 warps
 // that share their maxima through shared memory: the rows are read once.
 // Bound: bytes for prompts (2 read + 1 written a value): five of 4099 rows, four layers, 8 heads of 128,
-// take 66 us (5.7 TB/s).  A verify step is the chain of dependent reads (lengths, table
-// and row indices, rows, the held rows of a page whose scale grows): 32 trees, eight layers 6.5 us, 256
-// chains, two layers 11.3 us.
+// take 58 us (6.5 TB/s; 66 us when every value was looked at for infs and NaNs).  A verify step
+// is the chain of dependent reads (lengths, table and row indices, rows, the held rows of a
+// page whose scale grows): 32 trees, eight layers 5.1 us, 256 chains, two layers 8.2 us.
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -29,8 +29,7 @@ namespace {
 constexpr int kQ8Threads = 256;
 constexpr int kRowsPerWarp = 16;
 // CTAs up to which K and V of every layer have one of their own; past it a CTA takes several in turn and
-// looks up its rows once.  Five prompts of 4099 rows in four layers: 66 us by 4864, 81 us by 9728 and without a limit;
-// 74 us by 2432 and fewer (the last wave is not full).
+// looks up its rows once.  Five prompts of 4099 rows in four layers: 58 us by 4864, 61 us by 9728, 60 us by 2432.
 constexpr long kMostCtas = 4864;
 
 // the larger of |a| and |b| halfword by halfword, non-finite halves counting as 0
@@ -48,7 +47,6 @@ __global__ void __launch_bounds__(kQ8Threads, 4) commit_kv_q8_kernel(const __gri
   __shared__ uint32_t s_max[2][kQ8Threads / 32];
   pdl_wait();
   pdl_trigger();
-  const int pages = (a.max_len + PS - 2) / PS + 1;  // most pages that max_len rows touch
   // (every request's first page, then the second: the pages that are not touched come last)
   const int req = blockIdx.x % a.b, j = blockIdx.x / a.b;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -105,9 +103,17 @@ __global__ void __launch_bounds__(kQ8Threads, 4) commit_kv_q8_kernel(const __gri
     for (int i = 0; i < kLoads; ++i)
       x[i] = rows[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + size_t(rows[i]) * a.new_ld * 2) + c)
                           : make_uint4(0u, 0u, 0u, 0u);
+    // (an inf or a NaN shows as 0x7f80 or more; only then the finite ones are looked for)
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) mx = max_abs2(max_abs2(max_abs2(max_abs2(mx, x[i].x), x[i].y), x[i].z), x[i].w);
+    for (int i = 0; i < kLoads; ++i)
+      mx = __vmaxu2(__vmaxu2(__vmaxu2(__vmaxu2(mx, x[i].x & 0x7fff7fffu), x[i].y & 0x7fff7fffu), x[i].z & 0x7fff7fffu), x[i].w & 0x7fff7fffu);
     mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+    if (mx >= 0x7f80u) {
+      mx = 0u;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) mx = max_abs2(max_abs2(max_abs2(max_abs2(mx, x[i].x), x[i].y), x[i].z), x[i].w);
+      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+    }
     if (WU > 1) {
       uint32_t* sm = s_max[(z / gridDim.z) & 1];  // (the other one next time: one barrier is enough)
       if (lane == 0) sm[w] = mx;
