@@ -495,7 +495,8 @@ int spec_commit_kv(int b, int n, int W, int Hkv, int D, int num_layers, int page
  *   last token stay as they are; both 16-byte aligned); n_left [1] = n_free
  *   less the pages taken (may be n_free itself).
  * A page_size of 1 makes page_table the slot table (any page_size >= 1 whose
- * slots stay below 2^31).  A request with a bad length or row gets nothing
+ * slots stay below 2^31).  The requests of a call have different table rows.
+ * A request with a bad length or row gets nothing
  * (SPEC_DEV_LENGTH / SPEC_DEV_INDEX).  A free list or a slot map that is too
  * small sets SPEC_DEV_SPACE, and the call hands out nothing: cu_new is 0, n_left
  * = n_free.  A page id outside [0, num_pages) gives slot -1 and SPEC_DEV_INDEX.
@@ -541,7 +542,8 @@ int spec_commit_kv_q8(int b, int Hkv, int D, int page_size, int num_layers, cons
  * [b*n, Hq, D] bf16; lse: [b*n, Hq] fp32 (nullable), natural log.  A row that
  * sees no key gives out 0 and lse -inf.  An inf or NaN in a node's V reaches
  * only the rows that see the node.  max_seq_len bounds every seq_len (a larger
- * one sets SPEC_DEV_LENGTH and is clamped).  A page id out of range sets
+ * one sets SPEC_DEV_LENGTH and is clamped); a close bound is quicker where
+ * there are few requests.  A page id out of range sets
  * SPEC_DEV_INDEX and its keys do not count.  b <= 2048.  The workspace holds the
  * merge slots (about 51 MB, independent of the sizes). */
 int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size, const void* q, int64_t q_ld,
