@@ -30,8 +30,8 @@
 // memory would add 128 KB, which is why it goes through TMEM (an MMA with A
 // from TMEM measured the same 64 cycles as one with both operands in shared
 // memory, once its descriptors are precomputed).
-//   Measured: two contexts of 32768 to 131072, 64 nodes, 64 / 8 heads of 128: 273 us
-// (1.26 PF/s); 32 requests of 2048, 64 nodes, 32 / 8 heads: 95 us (0.72 PF/s).  In the
+//   Measured: two contexts of 32768 to 131072, 64 nodes, 64 / 8 heads of 128: 263 us
+// (1.31 PF/s); 32 requests of 2048, 64 nodes, 32 / 8 heads: 94 us (0.73 PF/s).  In the
 // history a step of 64 keys takes a group some 1960 cycles, of which the softmax is 1500
 // (two warps of it and two converters share a scheduler) and the MMAs of both groups
 // 1280.  A unit's end costs about 25000 cycles more: the tree's rows are converted
@@ -150,7 +150,8 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Bounded wait for the phase of the given parity: false once kWaitCycles have
-// passed or another warp has given up.
+// passed or another warp has given up.  (That is looked at only where the phase does not
+// come: a warp whose waits are still met goes on. A look in every step cost 3%.)
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   if (mbar_poll(bar, parity)) return true;
   const long long start = clock64();
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         const int ct = ct0 + t, buf = ct & 1, sb = 2 * w + (cs & 1), ph = (cs >> 1) & 1;
         if (split && (t & 1) != w) {  // the other group's tile
           ok = wait(full0 + buf, (ct >> 1) & 1);
-          if (!__all_sync(FULL, ok && !*abort_flag)) {
+          if (!__all_sync(FULL, ok)) {
             ok = false;
             break;
           }
@@ -576,7 +577,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         } else {
           ok = ok && wait(kPReady0 + sb, ph);
         }
-        if (!__all_sync(FULL, ok && !*abort_flag)) {
+        if (!__all_sync(FULL, ok)) {
           ok = false;
           break;
         }
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     uint32_t* infos = reinterpret_cast<uint32_t*>(sp + L::kInfo) + kv * 2 * kGroups;
     const int full0 = kv ? kVFull0 : kKFull0, empty0 = kv ? kVEmpty0 : kKEmpty0;
     auto wait = [&](int b, int parity) {
-      return __all_sync(FULL, mbar_wait(bar(b), uint32_t(parity), abort_flag) && !*abort_flag) != 0;
+      return __all_sync(FULL, mbar_wait(bar(b), uint32_t(parity), abort_flag)) != 0;
     };
 
     Pos p = start;
@@ -1005,7 +1006,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         // scores that have been read.  A short loop: unrolled, or with the tree's
         // case inside, the roles' code outran the instruction caches and half of
         // the warps' time went to fetching it.
-        const bool s_ok = mbar_wait(bar(kSFull0 + 2 * w + (cs & 1)), (cs >> 1) & 1, abort_flag) && !*abort_flag;
+        const bool s_ok = mbar_wait(bar(kSFull0 + 2 * w + (cs & 1)), (cs >> 1) & 1, abort_flag);
         if (!__all_sync(FULL, s_ok)) {
           ok = false;
           break;
