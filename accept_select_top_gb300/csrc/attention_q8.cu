@@ -13,8 +13,9 @@
 // the scales stay outside the products: a key's multiplies its column of S, and
 // a value's, 2^e, is an exponent added to x: P_j = 2^(x_j + e_j - m), rounded
 // once to f16 (2^-11), against a running maximum m of x + e.  So what P loses
-// below f16's range is 2^-30 of the row's largest contribution p |v|, however
-// far the value scales lie apart; l = sum P_j 2^-e_j (before the rounding).
+// below f16's range is 2^-24 of the row's largest contribution p |v|; l = sum
+// P_j 2^-e_j (before the rounding), which is why e_j is kept within a span
+// (attention_q8.cuh): alone, e = 1 of a row of zeros would take P below fp32's range.
 //
 // Bound: the cache's bytes.  A warp owns its work end to end: it takes an
 // equal, contiguous range of 16-key tiles of all (request, kv head, 16-row
@@ -418,6 +419,23 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
       }
     };
 
+    auto raise = [&](int top) {  // the base moves up to `top`
+      const int up = evb >= 0 ? top - evb : 0;
+      evb = top;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (up > 0 && m[i] > -INFINITY) {
+          const float mn = floorf(m[i] - float(raised_into_l(up, l[i]))), by = m[i] - mn;  // (exact)
+          const float fac = fast_exp2(by - float(up));
+          l[i] *= fast_exp2(by);
+          m[i] = mn;
+#pragma unroll
+          for (int q = 0; q < NT; ++q) {
+            o[q][2 * i] *= fac;
+            o[q][2 * i + 1] *= fac;
+          }
+        }
+    };
     // ---- history ----
     for (const int fh = min(E, f + (t < Th ? Th - t : 0)); f < fh; ++f) {
       cp_wait<kRing - 2>();
@@ -427,7 +445,7 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
       const uint32_t word = meta[f % kRing];
       const int cnt = (word >> 8) & 31, ev = word >> 24;
       const float kf = exp_scale((word >> 16) & 255);
-      if (evb < 0) evb = ev;
+      if (evb < 0 || ev > evb + kSpanUp) raise(ev);
       float s[2][4];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -445,7 +463,8 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
         }
       }
       // y = x - m with x = s * factor + (e - evb); a row without a reference yet has y = inf
-      const float de = float(ev - evb), x0 = xf[0] * kf, x1 = xf[1] * kf, d0 = de - m[0], d1 = de - m[1];
+      const int e_in = span_of(ev - evb);
+      const float de = float(e_in), x0 = xf[0] * kf, x1 = xf[1] * kf, d0 = de - m[0], d1 = de - m[1];
       float y[2][4];
 #pragma unroll
       for (int q = 0; q < 2; ++q)
@@ -484,9 +503,17 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
           sum[i] = q == 0 ? p0 + p1 : sum[i] + (p0 + p1);
           pa[2 * q + i] = pack_f16(p0, p1);
         }
-      const float dl = ratio_scale(evb - ev);
+      const float dl = exp_scale(kExpBias - e_in);
       l[0] = fmaf(sum[0], dl, l[0]);
       l[1] = fmaf(sum[1], dl, l[1]);
+      if (ev - evb < e_in) {  // (P takes what the values would be smaller by: four products, not sixteen)
+        const __half2 f = __float2half2_rn(ratio_scale(ev - evb - e_in));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 y2 = __hmul2(*reinterpret_cast<const __half2*>(&pa[i]), f);
+          pa[i] = *reinterpret_cast<const uint32_t*>(&y2);
+        }
+      }
       // O += P V: b0 holds keys 2c, 2c+1, b1 keys 2c+8, 2c+9 of a column
       uint32_t v[4][D / 32];  // D / 8 bytes of each of the four keys
 #pragma unroll
@@ -620,11 +647,14 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
             }
         }
       }
-      if (evb < 0) {
-        evb = max(max(evk[0], evk[1]), max(evk[2], evk[3]));
-        evb = max(evb, __shfl_xor_sync(FULL, evb, 1));
-        evb = max(evb, __shfl_xor_sync(FULL, evb, 2));
+      {
+        int top = max(max(evk[0], evk[1]), max(evk[2], evk[3]));
+        top = max(top, __shfl_xor_sync(FULL, top, 1));
+        top = max(top, __shfl_xor_sync(FULL, top, 2));
+        if (evb < 0 || top > evb + kSpanUp) raise(top);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) evk[i] = evb + span_of(evk[i] - evb);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "e4m3.cuh"
 #include "kernels.cuh"
 
 namespace spec {
@@ -53,6 +54,27 @@ __device__ __forceinline__ int norm_exp(uint32_t bits) {
   const int e = int(bits >> 7) - 14;
   return e < 1 ? 1 : e;
 }
+// A key's weight enters P with its value's exponent in it, 2^(x + d - m), d = e - base, and l without,
+// 2^(x - m).  So that neither leaves fp32, however far the values of a kv head lie apart:
+//   - d is at most kSpanUp.  A larger exponent raises the base: m falls by as much, so that P
+//     stays as it was and l grows, while l is below 2^kMostLog2; the rest makes O smaller.
+//   - l is won back from P, as P 2^-d, while d is at least -kSpanDown.  Below (a row or a page of zeros,
+//     above all) l has a sum of its own, or the key counts as one of d = -kSpanDown whose values are
+//     that much smaller.
+//   - m is set against x + max(d, -kSpanDown), so that l stays below 2^78 a key.
+// So l loses weights below 2^-37 of the largest only, and O bits of values 2^-70 below the largest of
+// the kv head's, and those 2^-90 below.
+constexpr int kSpanUp = 16, kSpanDown = 64, kMostLog2 = 64;
+__device__ __forceinline__ int span_of(int d) { return max(d, -kSpanDown); }
+
+// The base once an exponent `top` has come (base -1: none yet).
+__device__ __forceinline__ int raised_base(int base, int top) { return base < 0 || top > base + kSpanUp ? top : base; }
+
+// Of a base raised by `up`, what m falls by in a row of sum l.
+__device__ __forceinline__ int raised_into_l(int up, float l) {
+  return max(0, min(up, kMostLog2 + kExpBias - int(__float_as_uint(l) >> 23)));
+}
+
 // 2^d, d clamped to [-126, 127]
 __device__ __forceinline__ float ratio_scale(int d) {
   d = d < -126 ? -126 : d > 127 ? 127 : d;

@@ -68,15 +68,20 @@ __host__ __device__ constexpr uint32_t col_s(int w, int b) { return 256u + 128u 
 
 // What the softmax needs of a tile: of a history tile, for each group of 16
 // keys, {K scale, V exponent relative to the unit's base, its inverse factor in
-// l, keys that count}; of the tree tile, each node's K and V exponent
-// bytes, as the halves that hold 2^(K's - 127) and float(V's) in bf16.
+// l (0: below the span, l's share is added up apart), keys that count (less kMark in
+// a step's first group: the base has changed, or a group lies below the span)}; of the
+// tree tile, each node's K and V exponent bytes, as the halves that hold 2^(K's - 127)
+// and float(V's) in bf16.
+constexpr float kMark = 1024.f;
+__device__ __forceinline__ float keys_of(float w) { return w < 0.f ? w + kMark : w; }
 struct TileMeta {
   union {
     float4 group[kGroups];
     uint32_t node[kTreeKeys];
   };
   unsigned long long nonfinite[4];  // tree nodes whose V row holds an inf or a NaN, a word a converter warp
-  int base;                         // the unit's V exponent base
+  int top[4];                       // the tree's largest V exponent, a word a converter warp
+  int base;                         // the history's V exponent base
   int pad[3];
 };
 
@@ -94,7 +99,7 @@ struct TcSmem {
   static constexpr int kInfo = kMeta + 4 * int(sizeof(TileMeta));  // [K, V][2][8]: keys of a raw tile's groups
   static constexpr int kBars = kInfo + 128;
   static constexpr int kAbort = kBars + 8 * 34 + 4;  // (after the barriers: TMEM address, abort flag)
-  static constexpr int kKeep = kAbort + 4 + 4 * 20;  // behind the scan's 20 words
+  static constexpr int kKeep = kAbort + 4 + 4 * (kTcThreads / 32);  // behind the scan's words
   static constexpr int kBytes = kBars + 448;
   // the tiles before each request are summed up in what will hold operands
   static_assert(4 * (kAttentionQ8MaxB + 1) <= 2 * kTile, "scan space");
@@ -671,7 +676,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       sts16(tile + uint32_t(ch >> 3) * L::kBlock + uint32_t(key) * 128u + ((uint32_t(ch & 7) ^ uint32_t(key & 7)) << 4),
             make_uint4(cv(x.x), cv(x.y), cv(x.z), cv(x.w)));
     };
-    int base = 113, ct = 0;
+    int base = -1, last2 = -1, ct = 0;
     bool ok = true;
     for (int f = S; f < E; ++f, ++ct) {
       const int buf = ct & 1;
@@ -684,9 +689,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       // (K) the lane's group: keys that count, scale bytes
       const uint32_t word = lane < kGroups ? info[lane] : 0u;
       const int cnt = word & 255, ks0 = (word >> 8) & 255, vs0 = word >> 16;
-      if (first && cw == 0) {
-        const int v0 = __shfl_sync(FULL, vs0, 0);
-        base = tree || v0 == 0 ? 113 : v0;
+      if (first) base = last2 = -1;
+      bool mark = false;
+      if (!tree && kv == 0 && cw == 0) {
+        // (the base of the tile before last: the softmax groups may take the tiles in turn)
+        const int last = base, top = int(__reduce_max_sync(FULL, cnt > 0 ? uint32_t(vs0) : 0u));
+        if (top > 0) base = raised_base(base, top);
+        mark = (last >= 0 && last != base) || (last2 >= 0 && last2 != base) || __any_sync(FULL, cnt > 0 && vs0 < base - kSpanDown);
+        last2 = last;
       }
       if (!tree) {
         uint4 x[kLoads];  // the thread's words, zeros where there is no key
@@ -700,8 +710,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         ok = ct < 2 || wait(empty0 + buf, ((ct >> 1) - 1) & 1);
         if (!ok) break;
         if (kv == 0 && cw == 0 && lane < kGroups) {
-          mt.group[lane] = cnt > 0 ? make_float4(exp_scale(ks0), float(vs0 - base), ratio_scale(base - vs0), float(cnt))
-                                   : make_float4(1.f, 0.f, 0.f, 0.f);
+          float4 y = cnt > 0 ? make_float4(exp_scale(ks0), float(vs0 - base), vs0 < base - kSpanDown ? 0.f : ratio_scale(base - vs0), float(cnt))
+                             : make_float4(1.f, 0.f, 0.f, 0.f);
+          if (mark && lane % (kStep / kGroup) == 0) y.w -= kMark;
+          mt.group[lane] = y;
+          if (lane == 0) mt.base = max(base, 0);
         }
         store_hist(tile, x);
       } else {
@@ -709,6 +722,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         if (!ok) break;
         constexpr int kRowsOnce = 4;  // (eight take more registers than there are)
         unsigned long long nf = 0;
+        int top_e = 0;
 #pragma unroll 1
         for (int i0 = 0; i0 < kTreeLoads; i0 += kRowsOnce) {
           uint4 x[kRowsOnce];
@@ -751,12 +765,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
             const int key = tree_key(i0 + i), e = norm_exp(top[i]);
             if (ct_id % kLanesRow == 0) reinterpret_cast<uint16_t*>(&mt.node[key])[kv] = uint16_t(kv == 0 ? uint32_t(e) << 7 : __float_as_uint(float(e)) >> 16);
             store_tree(tile, x[i], key, e);
+            top_e = max(top_e, e);
           }
         }
-        if (kv == 1 && lane == 0) mt.nonfinite[cw] = nf;
+        if (kv == 1) {
+          top_e = int(__reduce_max_sync(FULL, uint32_t(top_e)));
+          if (lane == 0) {
+            mt.nonfinite[cw] = nf;
+            mt.top[cw] = top_e;
+          }
+        }
         mbar_arrive(bar(kRawEmpty0 + kv));
       }
-      if (kv == 0 && ct_id == 0) mt.base = base;
       fence_async();
       mbar_arrive(bar(full0 + buf));
       advance(p);
@@ -835,7 +855,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
     if (tid == 0) args.begun[blockIdx.x] = make_int4(-1, 0, 0, 0);
     // the piece at hand: tiles [f, f + n) of the range, from position p, and the next one's position
     Pos pn = start;
-    int n = 0, node = 0, head = 0, h = 0, base = kExpBias;
+    int n = 0, node = 0, head = 0, h = 0, base = -1;
     bool split = false, complete = false, mine = false, valid = false;
     float m = -INFINITY, l = 0.f;
     unsigned long long mask = 0, nonfinite = 0;
@@ -970,7 +990,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       const float xf = xf_next;
       mask = valid ? a.mask_bits[size_t(p.r) * a.n + node] & (~0ull >> (kTreeKeys - a.n)) : 0ull;
       nonfinite = 0;
-      base = kExpBias;
+      base = -1;
       pn.t += n - 1;
       if (f + n < E) advance(pn);
       const bool ask = f + n < E && has_tile(pn, f + n);
@@ -978,13 +998,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
       // The reference m is moved, to a whole number, when a score would put P above
       // 2^(kPBaseLog2 + kLazyLog2); O and l are multiplied by that power of two,
       // exactly, once the products so far are complete.
-      auto move = [&](float mx, bool o_live) {
-        const bool up = mx > m + kPBaseLog2;
-        const float mn = ceilf(mx) - kPBaseLog2;
-        const float fac = !up ? 1.f : m == -INFINITY ? 0.f : ratio_scale(int(fmaxf(m - mn, -126.f)));
-        l *= fac;
-        if (up) m = mn;
-        if (!o_live) return true;
+      // A base that has been raised (to `now`) moves it too.
+      auto move = [&](float mx, int now, bool o_live) {
+        float fac = 1.f;
+        if (now != base) {
+          const int d = m > -INFINITY ? now - base : 0, by = raised_into_l(d, l);
+          l *= ratio_scale(by);
+          m -= float(by);
+          fac = ratio_scale(by - d);
+          base = now;
+        }
+        if (mx > m + kPBaseLog2) {
+          const float mn = ceilf(mx) - kPBaseLog2, by = m == -INFINITY ? 0.f : ratio_scale(int(fmaxf(m - mn, -126.f)));
+          l *= by;
+          fac *= by;
+          m = mn;
+        }
+        if (!o_live || !__any_sync(FULL, fac != 1.f)) return true;
         if (!__all_sync(FULL, mbar_wait(bar(kPvDone0 + 2 * w + ((cs - 1) & 1)), ((cs - 1) >> 1) & 1, abort_flag))) return false;
         tc_after();
 #pragma unroll 1
@@ -1015,7 +1045,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         const TileMeta& mt = metas[(ct0 + t) & 3];
         const bool tree = p.t + t == p.Tr - 1, last = tree || hf == 1;
         const uint32_t ts = tl + col_s(w, cs & 1);
-        base = mt.base;
         if (last && t + stride >= n && ask) ask_q(pn);  // every product that reads this piece's Q is complete
         if (!tree) {
           // The exponentials are taken against the reference as it is.  Their sum
@@ -1032,7 +1061,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
 #pragma unroll
             for (int g = 0; g < 4; ++g) e[g] = mt.group[4 * hf + g];
             tmem_ld_wait();
+            bool marked = false;
             if (e[0].w + e[1].w + e[2].w + e[3].w < float(kStep)) {
+              marked = e[0].w < 0.f;
+              e[0].w = keys_of(e[0].w);
 #pragma unroll
               for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -1058,7 +1090,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
               all += s0.x + s0.y;
               ls = fmaf(s0.x + s0.y, e[g].z, ls);
             }
-            if (again || __all_sync(FULL, all < kPMost && m > -INFINITY)) {
+            if (again || __all_sync(FULL, all < kPMost && m > -INFINITY && !marked)) {
               l += ls;
               tmem_st32(ts, pk);
               break;
@@ -1072,11 +1104,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (float(i) < eg.w) mx = fmaxf(mx, fmaf(__uint_as_float(v[i]), xf * eg.x, eg.y));
+                if (float(i) < keys_of(eg.w)) mx = fmaxf(mx, fmaf(__uint_as_float(v[i]), xf * eg.x, fmaxf(eg.y, -float(kSpanDown))));
             }
-            if (__any_sync(FULL, mx > m + kPBaseLog2) && !move(mx, cs > cs0)) {
+            const int now = mt.base;
+            if ((now != base || __any_sync(FULL, mx > m + kPBaseLog2)) && !move(mx, now, cs > cs0)) {
               ok = false;
               break;
+            }
+            if (marked) {
+#pragma unroll 1
+              for (int g = 0; g < kStep / kGroup; ++g) {
+                const float4 eg = mt.group[4 * hf + g];
+                if (eg.z != 0.f) continue;
+                uint32_t v[16];
+                tmem_ld16(ts + 16 * g, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (float(i) < keys_of(eg.w)) l += fast_exp2(fmaf(__uint_as_float(v[i]), xf * eg.x, -m));
+              }
             }
           }
         } else {
@@ -1086,12 +1132,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
             break;
           }
           nonfinite = mt.nonfinite[0] | mt.nonfinite[1] | mt.nonfinite[2] | mt.nonfinite[3];
-          const float b0 = float(base);
-          // x + e - against of node k, from its word; chunk: the mask's bits from the chunk's first node on
-          auto score = [&](uint32_t v, uint32_t word, uint32_t chunk, int i, float against) {
-            const float x = fmaf(__uint_as_float(v), xf * bf16_lo(word), bf16_hi(word) - against);
+          const int now = raised_base(base, max(max(mt.top[0], mt.top[1]), max(mt.top[2], mt.top[3])));
+          const float b0 = float(now);
+          // x + add of node k, from its word; chunk: the mask's bits from the chunk's first node on
+          auto score = [&](uint32_t v, uint32_t word, uint32_t chunk, int i, float add) {
+            const float x = fmaf(__uint_as_float(v), xf * bf16_lo(word), add);
             return chunk & (1u << i) ? x : -INFINITY;
           };
+          // (against which m is set)
+          auto most = [&](uint32_t v, uint32_t word, uint32_t chunk, int i) { return score(v, word, chunk, i, fmaxf(bf16_hi(word) - b0, -float(kSpanDown))); };
           float mx = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < kTreeKeys / 16; ++c) {
@@ -1102,12 +1151,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const uint4 wd = *reinterpret_cast<const uint4*>(mt.node + 16 * c + 4 * q);
-              mx = fmaxf(mx, fmaxf(score(v[4 * q], wd.x, bits, 4 * q, b0), score(v[4 * q + 1], wd.y, bits, 4 * q + 1, b0)));
-              mx = fmaxf(mx, fmaxf(score(v[4 * q + 2], wd.z, bits, 4 * q + 2, b0), score(v[4 * q + 3], wd.w, bits, 4 * q + 3, b0)));
+              mx = fmaxf(mx, fmaxf(most(v[4 * q], wd.x, bits, 4 * q), most(v[4 * q + 1], wd.y, bits, 4 * q + 1)));
+              mx = fmaxf(mx, fmaxf(most(v[4 * q + 2], wd.z, bits, 4 * q + 2), most(v[4 * q + 3], wd.w, bits, 4 * q + 3)));
             }
           }
-          if (__any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2))) ok = move(mx, cs > cs0);
-          const float bm = b0 + (m == -INFINITY ? 0.f : m);  // (whole numbers)
+          if (now != base || __any_sync(FULL, mx > m + (kLazyLog2 + kPBaseLog2))) ok = move(mx, now, cs > cs0);
+          const float mr = m == -INFINITY ? 0.f : m, bm = b0 + mr;  // (whole numbers)
 #pragma unroll 1
           for (int c = 0; ok && c < kTreeKeys / 16; ++c) {
             uint32_t v[16], pk[8];
@@ -1118,9 +1167,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
             for (int q = 0; q < 4; ++q) {
               const uint4 wd = *reinterpret_cast<const uint4*>(mt.node + 16 * c + 4 * q);
               auto p_of = [&](uint32_t vv, uint32_t word, int i) {
-                const float y = fast_exp2(score(vv, word, bits, i, bm));
-                l = fmaf(y, fast_exp2(fminf(b0 - bf16_hi(word), 126.f)), l);
-                return y;
+                l += fast_exp2(score(vv, word, bits, i, -mr));
+                return fast_exp2(score(vv, word, bits, i, bf16_hi(word) - bm));
               };
               const float q0 = p_of(v[4 * q], wd.x, 4 * q), q1 = p_of(v[4 * q + 1], wd.y, 4 * q + 1);
               const float q2 = p_of(v[4 * q + 2], wd.z, 4 * q + 2), q3 = p_of(v[4 * q + 3], wd.w, 4 * q + 3);
