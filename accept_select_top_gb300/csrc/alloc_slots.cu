@@ -31,10 +31,11 @@ __device__ __forceinline__ unsigned ceil_div(unsigned a, unsigned d) { return a 
 __global__ void __launch_bounds__(kAllocThreads) alloc_slots_kernel(AllocParams a) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ int scan[];
-  int* cu = scan;                // [b + 1] tokens before request r
-  int* cp = scan + a.b + 1;      // [b + 1] pages before request r
-  __shared__ long long wsum[2][kAllocThreads / 32];
+  extern __shared__ long long scan[];
+  constexpr int kAllocWarps = kAllocThreads / 32;
+  long long* const wsum[2] = {scan, scan + kAllocWarps};
+  int* cu = reinterpret_cast<int*>(scan + 2 * kAllocWarps);  // [b + 1] tokens before request r
+  int* cp = cu + a.b + 1;                                    // [b + 1] pages before request r
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const unsigned P = unsigned(a.page_size);
   const bool report = blockIdx.x == 0;
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_slots_kernel(AllocParams 
     }
     __syncthreads();
     long long bt = run_t, bp = run_p;
-    for (int q = 0; q < kAllocThreads / 32; ++q) {
+    for (int q = 0; q < kAllocWarps; ++q) {
       if (q < w) {
         bt += wsum[0][q];
         bp += wsum[1][q];
@@ -162,10 +163,12 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_slots_kernel(AllocParams 
 }  // namespace
 
 int launch_alloc_slots(const AllocParams& p, cudaStream_t stream) {
-  const size_t smem = size_t(2) * (p.b + 1) * 4;
+  // (all of the kernel's shared memory is dynamic: 48 KB of it need no leave)
+  auto bytes = [](int b) { return size_t(2) * (kAllocThreads / 32) * sizeof(long long) + size_t(2) * (b + 1) * 4; };
+  const size_t smem = bytes(p.b);
   // (the most, so that calls of two threads agree)
   if (smem > 48 * 1024 && cudaFuncSetAttribute(alloc_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               2 * (kAllocMaxB + 1) * 4) != cudaSuccess)
+                                               int(bytes(kAllocMaxB))) != cudaSuccess)
     return SPEC_ERR_LAUNCH;
   // as many CTAs as the largest possible call has shares, up to four a SM
   const long long most = (long long)p.b * p.max_new < p.slot_cap ? (long long)p.b * p.max_new : p.slot_cap;
