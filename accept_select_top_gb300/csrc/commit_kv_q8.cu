@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kQ8Threads, 4) commit_kv_q8_kernel(const __gri
           *p = make_uint2(move(v.x), move(v.y));
         }
     }
-    const float inv = exp_scale(2 * kExpBias - e);
+    const float inv = inv_scale(e);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       if (rows[i] >= 0) {

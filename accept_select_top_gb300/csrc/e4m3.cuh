@@ -18,6 +18,8 @@ constexpr int kExpMax = 247;  // the largest finite bf16 / 448
 
 // 2^(e - 127) for e in [1, 254]
 __device__ __forceinline__ float exp_scale(int e) { return __uint_as_float(uint32_t(e) << 23); }
+// 2^(127 - e) for e in [1, 254] (of 254, the subnormal 2^-127)
+__device__ __forceinline__ float inv_scale(int e) { return __uint_as_float(e < 254 ? uint32_t(254 - e) << 23 : 1u << 22); }
 
 // Exponent byte of the smallest power-of-two scale at which a bf16 magnitude
 // (its 15 bits below the sign, finite) is at most 448 = 1.75 * 2^8.
