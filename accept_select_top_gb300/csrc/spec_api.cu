@@ -19,6 +19,12 @@ inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// whether two arrays of `bytes` bytes have one in common
+inline bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + bytes && y < x + bytes;
+}
+
 inline int elem_bytes(int dtype) { return dtype == SPEC_F32 ? 4 : 2; }
 inline int vec_elems(int dtype) { return dtype == SPEC_F32 ? 4 : 8; }
 
@@ -860,6 +866,9 @@ int spec_commit_kv_q8(int b, int Hkv, int D, int page_size, int num_layers, cons
       !lens || !new_seq_lens || (!src_index && !src_start))
     return SPEC_ERR_ARG;
   if (int rc = check_ws(ws, ws_bytes, kHeaderBytes)) return rc;
+  // (a request's CTAs read what one of them would overwrite)
+  for (const int32_t* in : {seq_lens, lens, req_pool_idx, src_index ? nullptr : src_start})
+    if (overlap(in, new_seq_lens, size_t(b) * 4)) return SPEC_ERR_ARG;
   CommitQ8Params p{};
   p.b = b;
   p.Hkv = Hkv;

@@ -438,7 +438,7 @@ def spec_commit_kv_q8(b: int, Hkv: int, D: int, page_size: int, k_new, v_new, k_
                       ws: Workspace, stream=None):
     """Quantises bf16 rows into the e4m3 pages of every layer.  k_new .. v_scales: one tensor a layer
     (a sequence, or a LayerList kept by the caller).  src_index [b, max_len] (accept_index) or
-    src_start [b]; the other may be None."""
+    src_start [b]; the other may be None.  new_seq_lens shares no memory with the arrays of lengths."""
     dev = _device()
     k_new, v_new, k_pages, v_pages = _layers(k_new), _layers(v_new), _layers(k_pages), _layers(v_pages)
     k_scales, v_scales = _layers(k_scales), _layers(v_scales)

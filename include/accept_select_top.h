@@ -513,8 +513,8 @@ int spec_alloc_slots(int b, int page_size, const int32_t* req_pool_idx, const in
  * verify step, max_len its width) or, src_index NULL, src_start[b] + j (cu_new
  * of prompts).  k_new / v_new: num_rows rows [Hkv, D] bf16, new_ld elements
  * apart (a multiple of 8, at least Hkv * D: a view of a packed projection).
- * Every layer, K and V; num_rows is below 2^31.  The pages have to be in page_table already; no page
- * that receives a row may belong to two requests of the call.
+ * Every layer, K and V; num_rows is below 2^31.  The pages have to be in page_table
+ * already; no page that receives a row may belong to two requests of the call.
  *   With x = the largest finite magnitude among the rows a (page, kv head)
  * receives, need = the smallest e >= SPEC_Q8_EXP_MIN with x <= 448 * 2^(e-127).
  * A page that holds earlier tokens keeps e = max(its e, need), and its held
@@ -522,9 +522,11 @@ int spec_alloc_slots(int b, int page_size, const int32_t* req_pool_idx, const in
  * e4m3's normal range); a page without takes e = need.  Each new value is x
  * 2^(127-e) rounded once to nearest even; +-inf saturates to +-448, NaN stays
  * NaN.  Bytes behind a request's last token stay as they are.
- * new_seq_lens[b] = seq_lens[b] + lens[b].  The layer arrays are HOST arrays of
- * num_layers (<= 128) device pointers.  A bad length or table row leaves its
- * request untouched; a bad page id or row index skips that page or row. */
+ * new_seq_lens[b] = seq_lens[b] + lens[b]; it is an array of its own (one that
+ * overlaps seq_lens, lens, req_pool_idx or src_start is SPEC_ERR_ARG: the call
+ * reads them to its end).  The layer arrays are HOST arrays of num_layers (<=
+ * 128) device pointers.  A bad length or table row leaves its request untouched;
+ * a bad page id or row index skips that page or row. */
 int spec_commit_kv_q8(int b, int Hkv, int D, int page_size, int num_layers, const void* const* k_new,
                       const void* const* v_new, int64_t num_rows, int64_t new_ld, void* const* k_pages,
                       void* const* v_pages, uint8_t* const* k_scales, uint8_t* const* v_scales, int64_t num_pages,

@@ -160,3 +160,13 @@ def test_commit_refuses_rows_past_32_bits(lib):
 
 def test_logprobs_refuse_a_vocabulary_past_the_chunks(lib):
     assert lib.spec_token_logprobs(*_logprobs(V=(1 << 20) + 1)) == -4
+
+
+@pytest.mark.parametrize("change, code", [
+    (dict(after=FAKE, lens=FAKE), -1), (dict(after=FAKE + 4), -1), (dict(lens=FAKE + 8, after=FAKE + 12, idx=FAKE, new=FAKE), -1),
+    (dict(after=FAKE + 0x1000, new=FAKE + 0x1000), -1), (dict(after=FAKE + 0x1000, idx=FAKE + 0x1000), -1),
+    (dict(after=FAKE + 0x1000, index=None, start=FAKE + 0x1004), -1)])
+def test_commit_refuses_lengths_in_place(lib, change, code):
+    """Some of a request's CTAs would have read the new length for the old one."""
+    args, keep = _commit(**change)
+    assert lib.spec_commit_kv_q8(*args) == code
