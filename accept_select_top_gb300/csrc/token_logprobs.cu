@@ -67,8 +67,9 @@ struct LpRow {
   __device__ int edge(int t) const { return t < head ? t : V - tail + (t - head); }
 };
 
-__device__ __forceinline__ float scale_of_row(const LogprobParams& a, long long idx) {
-  const float T = a.temperatures ? a.temperatures[idx / a.n] : 1.f;
+// (T is the output row's request's, whichever request's verify row it reads)
+__device__ __forceinline__ float scale_of_row(const LogprobParams& a, int out_row) {
+  const float T = a.temperatures ? a.temperatures[out_row / a.W] : 1.f;
   return T > 0.f ? 1.4426950408889634f / T : 1.4426950408889634f;
 }
 
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 1) token_logp
   int count = 0;
   {
     if (tid == 0) n_list = n_cand = 0;
-    c = scale_of_row(a, idx);
+    c = scale_of_row(a, out_row);
     const LpRow<T> row(a.logits, idx, a.V);
     const uint4* vp = row.vecs();
     const int v0 = ch * args.vpc, v1 = min(row.nvec, v0 + args.vpc);

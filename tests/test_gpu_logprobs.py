@@ -200,3 +200,24 @@ def test_rows_in_clusters_of_every_size(b, V):
     index[torch.rand(b, W, generator=gen) < 0.3] = -1
     tokens = torch.randint(0, V, (b, W), generator=gen).to(torch.int32)
     check(n, W, logits, index, tokens, None, 7)
+
+
+@pytest.mark.parametrize("V", [1000, 30000])
+def test_temperatures_are_the_output_rows(V):
+    """Rows of other requests: the temperature is that of the request that asks."""
+    b, n, W = 4, 3, 4
+    x = logits_of(b * n, V, torch.float32, 21)
+    index = torch.tensor([[9, 0, 3, -1], [1, 4, 11, 6], [5, 5, -1, -1], [0, 2, 8, 10]], dtype=torch.int32)
+    tokens = torch.where(index >= 0, tokens_of(b, W, V, 22), -1)
+    temps = torch.tensor([0.5, 1.0, 0.0, 2.5])
+    lp, ent, ids, top, ws = run(n, W, x, index, tokens, temps, 6)
+    assert ws.last_error() == 0
+    for r in range(b):
+        # the request's rows gathered, as a batch of its own
+        at = index[r][index[r] >= 0].long()
+        m = at.numel()
+        want = R.logprobs(m, m, x[at], None, tokens[r:r + 1, :m], temps[r:r + 1], 6)
+        assert torch.equal(ids[r, :m].cpu().long(), want[2][0])
+        near(lp[r, :m], want[0][0], 1)
+        near(ent[r, :m], want[1][0], 2)
+        near(top[r, :m], want[3][0], 1)
