@@ -3,9 +3,10 @@
 //
 // With M the row's maximum and y = (x - M) c, c = log2(e) / T:
 //   s = sum 2^y,  t = sum y 2^y,
-//   log p(v) = ln 2 (y_v - log2 s),  H = ln 2 (log2 s - t / s).
+//   log p(v) = (x_v - M) / T - ln 2 log2 s,  H = ln 2 (log2 s - t / s).
 // The difference comes before the factor: x c alone would overflow for masks of
-// the type's lowest value, and its rounding would not cancel.
+// the type's lowest value, and its rounding would not cancel.  log p has a factor of its
+// own: of such a mask, y is past fp32's range where log p is not.
 //
 // A CTA takes one chunk of one row (a whole row when there are rows enough to
 // fill the GPU).  A thread reads batches of 64 bytes a load group, 32 logits:
@@ -68,9 +69,9 @@ struct LpRow {
 };
 
 // (T is the output row's request's, whichever request's verify row it reads)
-__device__ __forceinline__ float scale_of_row(const LogprobParams& a, int out_row) {
+__device__ __forceinline__ float inverse_temperature(const LogprobParams& a, int out_row) {
   const float T = a.temperatures ? a.temperatures[out_row / a.W] : 1.f;
-  return T > 0.f ? 1.4426950408889634f / T : 1.4426950408889634f;
+  return T > 0.f ? 1.f / T : 1.f;
 }
 
 // A row's token and its logit, read before the row's statistics are there.
@@ -87,11 +88,11 @@ __device__ __forceinline__ LpToken token_of(const LogprobParams& a, int tok, lon
 // Results of one row from its joined statistics and its k best (count of them
 // with a value above -inf, in order); one warp.
 __device__ void finish_row(const LogprobParams& a, int out_row, LpToken token, float M, float s, float t,
-                           float c, int count, const float* tv, int* ti) {
+                           float inv_t, int count, const float* tv, int* ti) {
   const int lane = threadIdx.x & 31;
   const float ls = log2f(s);
   auto logp = [&](float x) {
-    return M == -INFINITY || !(x > -INFINITY) ? -INFINITY : ((x - M) * c - ls) * 0.6931471805599453f;
+    return M == -INFINITY || !(x > -INFINITY) ? -INFINITY : (x - M) * inv_t - ls * 0.6931471805599453f;
   };
   if (lane == 0) {
     float lp = 0.f;
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 1) token_logp
   __shared__ float cv[kListCap];
   __shared__ int ci[kListCap], list[kListCap];
   __shared__ int n_list, n_cand;
+  __shared__ float inv_t;
   __shared__ float tv[2][kLogprobMaxK];  // the chunk's best, the row's
   __shared__ int ti[2][kLogprobMaxK];
   __shared__ __align__(16) LpPart part;
@@ -164,8 +166,12 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 1) token_logp
   float M = -INFINITY, s = 0.f, t = 0.f, c = 0.f;
   int count = 0;
   {
-    if (tid == 0) n_list = n_cand = 0;
-    c = scale_of_row(a, out_row);
+    const float it = inverse_temperature(a, out_row);
+    if (tid == 0) {
+      n_list = n_cand = 0;
+      inv_t = it;
+    }
+    c = 1.4426950408889634f * it;
     const LpRow<T> row(a.logits, idx, a.V);
     const uint4* vp = row.vecs();
     const int v0 = ch * args.vpc, v1 = min(row.nvec, v0 + args.vpc);
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 1) token_logp
       __syncthreads();
     }
     if (args.chunks == 1) {
-      if (w == 0) finish_row(a, out_row, token, M, s, t, c, count, tv[0], ti[0]);
+      if (w == 0) finish_row(a, out_row, token, M, s, t, inv_t, count, tv[0], ti[0]);
       return;
     }
     if (tid == 0) part = LpPart{M, s, t, count};
@@ -423,7 +429,7 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 1) token_logp
         }
         __syncwarp();
       }
-      finish_row(a, out_row, token, jM, js, jt, c, got, tv[1], ti[1]);
+      finish_row(a, out_row, token, jM, js, jt, inv_t, got, tv[1], ti[1]);
     }
     cluster_sync();  // (no CTA ends while its shared memory is read)
   }

@@ -221,3 +221,27 @@ def test_temperatures_are_the_output_rows(V):
         near(lp[r, :m], want[0][0], 1)
         near(ent[r, :m], want[1][0], 2)
         near(top[r, :m], want[3][0], 1)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [40, 1000, 20000])
+def test_tokens_masked_by_the_lowest_value(V, dtype):
+    """Fewer allowed tokens than alternatives, and asked tokens under the mask: their log probability is finite where
+    fp32 holds it."""
+    x = logits_of(4, V, dtype, 31)
+    low = torch.finfo(dtype).min
+    x[0, 3:] = low
+    x[1, : V - 1] = low
+    x[2, V // 2:] = low / 2
+    x[3, 5:] = low
+    x[3, 5:20] = -1e30
+    tokens = torch.tensor([[5, 0, V - 1, V - 1]], dtype=torch.int32)
+    for T in (1.0, 0.75, 2.0):
+        lp, ent, ids, top, ws = run(4, 4, x, None, tokens, torch.tensor([T]), 20)
+        assert ws.last_error() == 0
+        wlp, went, wids, wtop = R.logprobs(4, 4, x, None, tokens, torch.tensor([T]), 20)
+        past = lambda w: torch.where(w < -torch.finfo(torch.float32).max, -math.inf, w)  # noqa: E731
+        assert torch.equal(ids.cpu().long(), wids)
+        near(lp, past(wlp), 1)
+        near(top, past(wtop), 1)
+        near(ent, went, 2)
