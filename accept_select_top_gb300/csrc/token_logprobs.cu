@@ -92,7 +92,8 @@ __device__ void finish_row(const LogprobParams& a, int out_row, LpToken token, f
   const int lane = threadIdx.x & 31;
   const float ls = log2f(s);
   auto logp = [&](float x) {
-    return M == -INFINITY || !(x > -INFINITY) ? -INFINITY : (x - M) * inv_t - ls * 0.6931471805599453f;
+    // (1 / T may be inf: of the maximum itself, 0 / T is 0)
+    return M == -INFINITY || !(x > -INFINITY) ? -INFINITY : (x == M ? x - M : (x - M) * inv_t) - ls * 0.6931471805599453f;
   };
   if (lane == 0) {
     float lp = 0.f;
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 1) token_logp
       n_list = n_cand = 0;
       inv_t = it;
     }
-    c = 1.4426950408889634f * it;
+    c = fminf(1.4426950408889634f * it, 3.402823466e38f);  // (0 inf would be NaN)
     const LpRow<T> row(a.logits, idx, a.V);
     const uint4* vp = row.vecs();
     const int v0 = ch * args.vpc, v1 = min(row.nvec, v0 + args.vpc);

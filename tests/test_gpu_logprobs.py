@@ -245,3 +245,21 @@ def test_tokens_masked_by_the_lowest_value(V, dtype):
         near(lp, past(wlp), 1)
         near(top, past(wtop), 1)
         near(ent, went, 2)
+
+
+@pytest.mark.parametrize("V", [50, 3000, 30000])
+@pytest.mark.parametrize("T", [1e-45, 1e-39, 4e-39, 1e-38, 1e-30, 1e-6, 1e30, 3e38, math.inf])
+def test_temperatures_of_every_size(V, T):
+    """Down to subnormal ones, whose inverse is past fp32's range (all the weight on the maximum), and up to inf (all equal)."""
+    x = logits_of(3, V, torch.float32, 41)
+    x[1, 7:9] = 20.0  # two maxima
+    tokens = torch.tensor([[int(x[0].argmax()), 8, 0]], dtype=torch.int32)
+    temps = torch.tensor([T], dtype=torch.float32)
+    lp, ent, ids, top, ws = run(3, 3, x, None, tokens, temps, 5)
+    assert ws.last_error() == 0
+    wlp, went, wids, wtop = R.logprobs(3, 3, x, None, tokens, temps, 5)
+    past = lambda w: torch.where(w < -torch.finfo(torch.float32).max, -math.inf, w)  # noqa: E731
+    assert torch.equal(ids.cpu().long(), wids)
+    near(lp, past(wlp), 1)
+    near(top, past(wtop), 1)
+    near(ent, went, 2)
