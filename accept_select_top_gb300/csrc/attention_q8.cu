@@ -708,16 +708,18 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
     // ---- the unit's or the range's end ----
     const bool unit_end = f == f_end && f <= E;  // (past E: the last ticks are another warp's, which has nothing to add)
     // rows g, g + 8; columns c D/4 .. + D/4: [0, D/8) from fragment columns 2c, [D/8, D/4) from 2c + 1
+    const bool whole = !CLUSTER && unit_end && t_first == 0;
     float lt[2];
     const float vs = exp_scale(evb < 1 ? 1 : evb);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       lt[i] = l[i] + __shfl_xor_sync(FULL, l[i], 1);
       lt[i] += __shfl_xor_sync(FULL, lt[i], 2);
+      const float inv = whole ? inverse_of(lt[i]) : settle(m[i], lt[i]);
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
-        o[q][2 * i] *= vs;
-        o[q][2 * i + 1] *= vs;
+        o[q][2 * i] = o[q][2 * i] * inv * vs;
+        o[q][2 * i + 1] = o[q][2 * i + 1] * inv * vs;
       }
       if (nonfinite) {
         const int rg = mt * kRowTile + g + 8 * i;
@@ -736,19 +738,18 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
           }
       }
     }
-    if (!CLUSTER && unit_end && t_first == 0) {  // the whole unit
+    if (whole) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int rg = mt * kRowTile + g + 8 * i;
         if (rg < M) {
           const size_t orow = (size_t(r) * a.n + rg / G) * a.Hq + h * G + rg % G;
-          const float inv = lt[i] > 0.f || lt[i] != lt[i] ? 1.f / lt[i] : 0.f;
           uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + c * (D / 4));
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int q = 0; q < NT; q += 8) {
-              auto pk = [&](int e) { return pack_bf16x2(o[q + e][2 * i + u] * inv, o[q + e + 1][2 * i + u] * inv); };
+              auto pk = [&](int e) { return pack_bf16x2(o[q + e][2 * i + u], o[q + e + 1][2 * i + u]); };
               dst[(u * NT + q) / 8] = make_uint4(pk(0), pk(2), pk(4), pk(6));
             }
           if (c == 0 && a.lse) a.lse[orow] = lse_of(m[i], lt[i]);
@@ -799,6 +800,9 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
       const float v[4] = {y.x, y.y, y.z, y.w};
       join<4>(Mx, Ls, acc, ml[q * kRowTile].x, ml[q * kRowTile].y, v);
     }
+    const float f = settle(Mx, Ls) * float(1 << kRoomLog2);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q] *= f;
     const bool first = (x & 3) == 0 && (x / 32) % (NT / 2) == 0;
     if (CLUSTER) {
       reinterpret_cast<float4*>(smem + L::kScan)[x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -832,7 +836,7 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
         join<4>(Mx, Ls, acc, ml[q].x, ml[q].y, v);
       }
       if (rg < M) {
-        const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+        const float inv = settled_inverse(Ls);
         const size_t orow = (size_t(r) * a.n + rg / G) * a.Hq + h * G + rg % G;
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + (l & 3) * (D / 4) + 4 * (e % (NT / 2))) =
             make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
@@ -878,7 +882,7 @@ __global__ void __launch_bounds__(4 * D, 3) attention_q8_rows_join_kernel(const 
       join<4>(Mx, Ls, acc, ml[i].x, ml[i].y, v);
     }
   }
-  const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+  const float inv = settled_inverse(Ls);
   const size_t orow = (size_t(r) * a.n + rg / G) * a.Hq + h * G + rg % G;
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + (lane & 3) * (D / 4) + 4 * (e % (NT / 2))) =
       make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));

@@ -91,6 +91,23 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
+// A partial's reference moves so that l lies in [1/2, 1); returns what O is multiplied by.  O then is an
+// average of values, and 2^-kRoomLog2 of it: the sums of many values near the type's largest would not fit.
+constexpr int kRoomLog2 = 8;
+__device__ __forceinline__ float settle(float& m, float& l) {
+  float f = 1.f;
+  if (l > 0.f) {
+    const int e = int(__float_as_uint(l) >> 23) - (kExpBias - 1);
+    m += float(e);
+    f = ratio_scale(-e);
+    l *= f;
+  }
+  return f * (1.f / (1 << kRoomLog2));
+}
+// 1 / l, and for settled partials' sum
+__device__ __forceinline__ float inverse_of(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }
+__device__ __forceinline__ float settled_inverse(float l) { return l > 0.f || l != l ? float(1 << kRoomLog2) / l : 0.f; }
+
 // (Mx, Ls, acc) joined with another partial (m, l, o) of the same row
 template <int N, typename O>
 __device__ __forceinline__ void join(float& Mx, float& Ls, float (&acc)[N], float m, float l, const O& o) {

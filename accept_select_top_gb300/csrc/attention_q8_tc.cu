@@ -903,12 +903,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
         }
         const unsigned long long nf = nonfinite & mask;
         const bool any_nf = __any_sync(FULL, nf != 0ull);
-        // out = (O 2^base [+ the other half, both relative to the larger reference]) / l
+        // out = O / l 2^base, averaged with the other half by their weights
         const bool has_o = ol > 0.f || ol != ol;
         const float M2 = has_o ? fmaxf(m, om) : m;
-        const float wa = has_o && m != M2 ? fast_exp2(m - M2) : 1.f, wb = has_o ? fast_exp2(om - M2) : 0.f;
-        const float Ls = has_o ? l * wa + ol * wb : l;
-        const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+        const float la = has_o && m != M2 ? l * fast_exp2(m - M2) : l, lb = has_o ? fast_exp2(om - M2) : 0.f;
+        const float Ls = has_o ? fmaf(ol, lb, la) : l;
+        const bool result = direct || (local && w == 0);
+        float fm = m, fl = l;
+        const float inv = result ? inverse_of(l) : settle(fm, fl), wa = has_o ? la / Ls : 1.f, wb = lb * settled_inverse(Ls);
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
           float v[16];
@@ -917,7 +919,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
             tmem_ld16(to + 16 * c, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * vs;
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(o[i]) * inv * vs;
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = 0.f;
@@ -933,7 +935,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
                 }
               }
           }
-          if (direct || (local && w == 0)) {
+          if (result) {
             if (has_o) {
               const float4* oo = so + size_t(kRows) * (D / 4) + size_t(4 * c) * kRows;
 #pragma unroll
@@ -949,18 +951,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_q8_tc_kernel(const __
               uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D) + 2 * c;
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                dst[i] = make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
-                                    pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+                dst[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                    pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
             }
           } else if (valid) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) so[(4 * c + i) * kRows] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
-        if (direct || (local && w == 0)) {
+        if (result) {
           if (valid && a.lse) a.lse[orow] = lse_of(M2, Ls);
         } else if (valid) {
-          *sm = make_float2(m, l);
+          *sm = make_float2(fm, fl);
         } else {
           *sm = make_float2(-INFINITY, 0.f);
         }
@@ -1244,7 +1246,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attention_q8_join_kernel(cons
       Mx = M2;
     }
   }
-  const float inv = Ls > 0.f || Ls != Ls ? 1.f / Ls : 0.f;
+  const float inv = settled_inverse(Ls);
   constexpr int C4 = D / 4, C = C4 / (kJoinThreads / 32);  // 16-byte words a thread
   const int c = warp * C;
   float4 acc[C];

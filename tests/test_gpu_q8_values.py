@@ -166,6 +166,17 @@ def test_all_values_tiny(n, D, low):
 
 
 @pytest.mark.usefixtures("bounds")
+@pytest.mark.parametrize("n, D", [(1, 128), (4, 64), (33, 128), (64, 64), (64, 128)])
+@pytest.mark.parametrize("lens", [[2000, 3, 0], [200] * 40])
+def test_values_near_the_types_largest(n, D, lens):
+    """Values up to 2^122: sums of many stay an average."""
+    a = Att(len(lens), n, 4, 1, D, 16, lens, seed=13, lo=EXP_ONE + 119, hi=EXP_ONE + 121, scale=0.1 / math.sqrt(D))
+    a.ks.fill_(114)
+    a.v.copy_((a.v.float() * 2.0 ** 119).bfloat16())
+    check(a.device())
+
+
+@pytest.mark.usefixtures("bounds")
 @pytest.mark.parametrize("n, Hq", [(4, 8), (33, 4), (64, 8)])
 def test_a_dominant_key_of_zeros(n, Hq):
     """Nearly all the weight on a zero row: what is left of the others is small, not lost, and lse is that row's."""
