@@ -42,6 +42,11 @@ __host__ __device__ inline size_t greedy_counter_base(int b) { return size_t(2 *
 __host__ __device__ inline size_t sampling_queue_word(int b) { return greedy_counter_base(b) + size_t(b); }
 __host__ __device__ inline size_t counters_bytes(int b) { return align256((sampling_queue_word(b) + 1) * 4); }
 
+// The partials start behind the counters of kSharedB requests at least: calls of different batch
+// sizes share a workspace, and the counters of a larger one have to be as zero as they were.
+constexpr int kSharedB = SPEC_WORKSPACE_SHARED_B;
+__host__ __device__ inline size_t partials_offset(int b) { return kHeaderBytes + counters_bytes(b > kSharedB ? b : kSharedB); }
+
 struct WsView {
   uint32_t* error;
   uint32_t* counters;
@@ -51,7 +56,7 @@ struct WsView {
 inline WsView ws_view(void* ws, int b) {
   unsigned char* base = static_cast<unsigned char*>(ws);
   return WsView{reinterpret_cast<uint32_t*>(base), reinterpret_cast<uint32_t*>(base + kHeaderBytes),
-                base + kHeaderBytes + counters_bytes(b)};
+                base + partials_offset(b)};
 }
 
 __device__ inline void raise_error(uint32_t* err, uint32_t bit) { atomicOr(err, bit); }

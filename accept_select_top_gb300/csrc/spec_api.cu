@@ -230,7 +230,7 @@ int greedy_call(bool compact, int b, int n, int S, int V, int dtype, const void*
   p.early = early;
   p.error = v.error;
   p.counters = v.counters + greedy_counter_base(b);
-  p.partials = v.partials + (compact ? 0 : attention_partial_bytes());
+  p.partials = compact ? static_cast<unsigned char*>(ws) + kHeaderBytes + counters_bytes(b) : v.partials + attention_partial_bytes();
   return launch_verify_greedy(p, as_stream(stream));
 }
 
@@ -438,7 +438,7 @@ size_t spec_workspace_size(int op, int b, int n, int k, int V, int Hq, int Hkv, 
   const bool logprobs = op == SPEC_OP_TOKEN_LOGPROBS;
   if (n < 1 || n > (logprobs ? kMaxN + 1 : kMaxN) || k < 1 || k > (logprobs ? kLogprobMaxK : kMaxK) || V < 1) return 0;
   if ((op == SPEC_OP_VERIFY_ATTENTION || op == SPEC_OP_VERIFY_ATTENTION_Q8) && (Hq < 1 || Hkv < 1 || Hq % Hkv || max_seq_len < 0)) return 0;
-  return kHeaderBytes + counters_bytes(b) + partial_bytes(op, b, n, k, V, Hq, Hkv, max_seq_len);
+  return partials_offset(b) + partial_bytes(op, b, n, k, V, Hq, Hkv, max_seq_len);
 }
 
 int spec_workspace_init(void* ws, size_t ws_bytes, void* stream) {

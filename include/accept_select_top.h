@@ -23,8 +23,10 @@
  *     it and never synchronises the host (except spec_last_error).
  *   - `ws` / `ws_bytes` is caller-provided scratch memory sized by
  *     spec_workspace_size() and zero-filled once (spec_workspace_init) before its
- *     first use.  Every call leaves it zero again apart from the error word, so
- *     one workspace serves any sequence of calls on one stream.  Calls that may
+ *     first use.  Every call leaves its counters zero again, so one workspace
+ *     serves any sequence of calls on one stream, of any batch sizes up to
+ *     SPEC_WORKSPACE_SHARED_B (a larger batch needs one of its own: its counters
+ *     lie where smaller ones keep partial results).  Calls that may
  *     run concurrently (different streams) need separate workspaces.  Every
  *     kernel is launched with programmatic dependent launch: by default it
  *     waits for the kernel before it on the stream -- whichever library or
@@ -88,6 +90,9 @@ extern "C" {
 #define SPEC_OP_VERIFY_ATTENTION_Q8 9
 #define SPEC_OP_TOKEN_LOGPROBS 10 /* n: rows a request (W, up to 65), k: alternatives (up to 32) */
 #define SPEC_OP_LAST SPEC_OP_TOKEN_LOGPROBS
+
+/* Batch sizes up to which calls of different sizes may share a workspace. */
+#define SPEC_WORKSPACE_SHARED_B 4096
 
 /* Bytes of workspace the operation needs for these sizes (b requests, n tree
  * nodes, k = topk, V vocabulary, Hq query heads, Hkv kv heads, max_seq_len an

@@ -170,3 +170,11 @@ def test_commit_refuses_lengths_in_place(lib, change, code):
     """Some of a request's CTAs would have read the new length for the old one."""
     args, keep = _commit(**change)
     assert lib.spec_commit_kv_q8(*args) == code
+
+
+def test_workspaces_of_smaller_batches_keep_clear_of_the_counters():
+    """The partial results of any batch size start behind the counters of every size that may share the workspace."""
+    from accept_select_top_gb300 import ops
+    # (an operation of no partial results: header and counters alone)
+    sizes = [ops.spec_workspace_size(ops.OP_BUILD_TREE, b, 4, 1, 1000) for b in (1, 2, 600, 4096)]
+    assert len(set(sizes)) == 1 and ops.spec_workspace_size(ops.OP_BUILD_TREE, 5000, 4, 1, 1000) > sizes[0]
