@@ -122,7 +122,7 @@ class Workspace:
         self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=device or "cuda")
         # zero-filled through the C ABI, which also forgets any earlier
         # workspace that lived at this address
-        self.address = self.tensor.data_ptr()
+        self.address, self.device = self.tensor.data_ptr(), self.tensor.get_device()
         _check(LIB.spec_workspace_init(self.ptr, ctypes.c_size_t(self.nbytes), _stream(stream)),
                "spec_workspace_init")
 
@@ -368,6 +368,13 @@ def _rows_in(t: torch.Tensor, heads: int, D: int, least: int, dev: int, what: st
     return t.data_ptr(), (ld if rows > 1 else heads * D)
 
 
+def _workspace_in(ws: Workspace, dev: int) -> int:
+    """Address of a workspace on device `dev`."""
+    if ws.device != dev:
+        raise SpecError(f"workspace: on device {ws.device}, the current CUDA device is {dev}")
+    return ws.address
+
+
 def _device() -> int:
     return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
 
@@ -429,8 +436,8 @@ def spec_alloc_slots(b: int, page_size: int, req_pool_idx, seq_lens, new_lens, m
         _in(page_table, _I32, 1, dev, "page_table"), rows, row_pages,
         None if req_to_token is None else _in(req_to_token, _I32, 1, dev, "req_to_token"), width,
         _in(cu_new, _I32, b + 1, dev, "cu_new"), _in(slot_map, _I32, 0, dev, "slot_map"),
-        _in(positions, _I32, 0, dev, "positions"), slots, _in(n_left, _I32, 1, dev, "n_left"), ws.address, ws.nbytes,
-        _raw_stream(stream, dev)), "spec_alloc_slots")
+        _in(positions, _I32, 0, dev, "positions"), slots, _in(n_left, _I32, 1, dev, "n_left"),
+        _workspace_in(ws, dev), ws.nbytes, _raw_stream(stream, dev)), "spec_alloc_slots")
 
 
 def spec_commit_kv_q8(b: int, Hkv: int, D: int, page_size: int, k_new, v_new, k_pages, v_pages, k_scales, v_scales,
@@ -464,7 +471,8 @@ def spec_commit_kv_q8(b: int, Hkv: int, D: int, page_size: int, k_new, v_new, k_
         _in(req_pool_idx, _I32, b, dev, "req_pool_idx"), _in(seq_lens, _I32, b, dev, "seq_lens"),
         None if src_index is None else _in(src_index, _I32, b * max_len, dev, "src_index"),
         None if src_start is None else _in(src_start, _I32, b, dev, "src_start"), _in(lens, _I32, b, dev, "lens"),
-        max_len, _in(new_seq_lens, _I32, b, dev, "new_seq_lens"), ws.address, ws.nbytes, _raw_stream(stream, dev)),
+        max_len, _in(new_seq_lens, _I32, b, dev, "new_seq_lens"), _workspace_in(ws, dev), ws.nbytes,
+        _raw_stream(stream, dev)),
         "spec_commit_kv_q8")
 
 
@@ -495,7 +503,7 @@ def spec_verify_attention_q8(b: int, n: int, Hq: int, Hkv: int, D: int, page_siz
         _in(page_table, _I32, 1, dev, "page_table"), table_rows, row_pages,
         _in(req_pool_idx, _I32, b, dev, "req_pool_idx"), _in(seq_lens, _I32, b, dev, "seq_lens"), max_seq_len,
         _in(mask_bits, _I64, rows, dev, "mask_bits"), scale, _in(out, _BF16, rows * Hq * D, dev, "out"),
-        None if lse is None else _in(lse, _F32, rows * Hq, dev, "lse"), ws.address, ws.nbytes,
+        None if lse is None else _in(lse, _F32, rows * Hq, dev, "lse"), _workspace_in(ws, dev), ws.nbytes,
         _raw_stream(stream, dev)), "spec_verify_attention_q8")
 
 
@@ -514,8 +522,8 @@ def spec_token_logprobs(b: int, n: int, W: int, logits, row_index, tokens, tempe
         _in(logprobs, _F32, rows, dev, "logprobs"),
         None if entropy is None else _in(entropy, _F32, rows, dev, "entropy"),
         None if top_ids is None else _in(top_ids, _I32, rows * k, dev, "top_ids"),
-        None if top_logprobs is None else _in(top_logprobs, _F32, rows * k, dev, "top_logprobs"), ws.address, ws.nbytes,
-        _raw_stream(stream, dev)), "spec_token_logprobs")
+        None if top_logprobs is None else _in(top_logprobs, _F32, rows * k, dev, "top_logprobs"),
+        _workspace_in(ws, dev), ws.nbytes, _raw_stream(stream, dev)), "spec_token_logprobs")
 
 
 def spec_verify_greedy_noalloc(b: int, n: int, S: int, logits, draft_tokens, retrieve_index, next_token,

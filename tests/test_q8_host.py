@@ -178,3 +178,12 @@ def test_workspaces_of_smaller_batches_keep_clear_of_the_counters():
     # (an operation of no partial results: header and counters alone)
     sizes = [ops.spec_workspace_size(ops.OP_BUILD_TREE, b, 4, 1, 1000) for b in (1, 2, 600, 4096)]
     assert len(set(sizes)) == 1 and ops.spec_workspace_size(ops.OP_BUILD_TREE, 5000, 4, 1, 1000) > sizes[0]
+
+
+def test_binding_refuses_a_workspace_of_another_device():
+    from accept_select_top_gb300 import ops
+    ws = ops.Workspace.__new__(ops.Workspace)
+    ws.address, ws.device = FAKE, 1
+    assert ops._workspace_in(ws, 1) == FAKE
+    with pytest.raises(ops.SpecError, match="device 1"):
+        ops._workspace_in(ws, 0)
