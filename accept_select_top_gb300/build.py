@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -20,6 +21,10 @@ INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
+
+# Registers a thread that a kernel has to be launched with: its warp groups trade them, and the split counts
+# on what the compiler gives it (a launch with fewer would wait for ever, and is refused).
+REGISTERS = {"attention_q8_tc.cu": ("attention_q8_tc_kernel", 80)}
 
 
 def nvcc() -> str:
@@ -46,13 +51,28 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > t for d in [src] + _headers())
 
 
+def check_registers(log: str, kernel: str, want: int) -> None:
+    """Raises unless ptxas' report gives every instance of `kernel` `want` registers."""
+    got = [int(n) for name, n in re.findall(r"Compiling entry function '(\S+)'.*?Used (\d+) registers", log, re.S)
+           if kernel in name]
+    if not got or any(n != want for n in got):
+        raise RuntimeError(f"{kernel} is written for {want} registers a thread at launch; this compiler gives it {got}: "
+                           "its kRegs and the split by role have to follow")
+
+
 def _compile(src: str, extra) -> str:
-    obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
+    name = os.path.basename(src)
+    obj = os.path.join(BUILD, name[:-3] + ".o")
     if _stale(obj, src):
-        cmd = [nvcc(), *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
+        need = REGISTERS.get(name)
+        tmp = obj + f".tmp{os.getpid()}"
+        cmd = [nvcc(), *ARCH, *FLAGS, *(["-Xptxas", "-v"] if need else []), *extra, "-c", src, "-o", tmp]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"nvcc failed for {name}:\n{r.stdout}\n{r.stderr}")
+        if need:
+            check_registers(r.stdout + r.stderr, *need)
+        os.replace(tmp, obj)
     return obj
 
 

@@ -1296,7 +1296,7 @@ int launch_tc(const AttentionQ8Params& p, cudaStream_t stream) {
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return SPEC_ERR_LAUNCH;
-  // the register split assumes what the CTA is launched with
+  // the register split assumes what the CTA is launched with (the build checks it, too)
   cudaFuncAttributes attr;
   if (cudaFuncGetAttributes(&attr, attention_q8_tc_kernel<D>) != cudaSuccess || attr.numRegs != kRegs) return SPEC_ERR_LAUNCH;
   // at least 120 KB, so that two CTAs never share a SM (each holds all of TMEM)
