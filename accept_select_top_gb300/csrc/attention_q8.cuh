@@ -37,14 +37,11 @@ __device__ __forceinline__ ReqQ8 req_q8(const AttentionQ8Params& a, int Lp, int 
   return ReqQ8{Lp, rq};
 }
 
-// The larger magnitude halfword by halfword (15 bits), inf and NaN counting as 0.
+// Two bf16 values, inf and NaN replaced by 0.
 __device__ __forceinline__ uint32_t finite_bf16(uint32_t x) {
   if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
   if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
   return x;
-}
-__device__ __forceinline__ bool nonfinite_bf16(uint32_t x) {
-  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
 __device__ __forceinline__ uint32_t max_abs_bf16(uint32_t m, uint32_t x) { return __vmaxu2(m, finite_bf16(x) & 0x7fff7fffu); }
 
@@ -54,6 +51,7 @@ __device__ __forceinline__ int norm_exp(uint32_t bits) {
   const int e = int(bits >> 7) - 14;
   return e < 1 ? 1 : e;
 }
+
 // A key's weight enters P with its value's exponent in it, 2^(x + d - m), d = e - base, and l without,
 // 2^(x - m).  So that neither leaves fp32, however far the values of a kv head lie apart:
 //   - d is at most kSpanUp.  A larger exponent raises the base: m falls by as much, so that P

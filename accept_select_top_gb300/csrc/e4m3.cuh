@@ -14,7 +14,6 @@ namespace spec {
 
 constexpr int kExpBias = 127;
 constexpr int kExpMin = SPEC_Q8_EXP_MIN;
-constexpr int kExpMax = 247;  // the largest finite bf16 / 448
 
 // 2^(e - 127) for e in [1, 254]
 __device__ __forceinline__ float exp_scale(int e) { return __uint_as_float(uint32_t(e) << 23); }

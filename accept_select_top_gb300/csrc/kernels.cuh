@@ -383,7 +383,6 @@ struct AttentionQ8Params {
   void* out;
   float* lse;
   uint32_t* error;
-  uint32_t* counters;
   unsigned char* partials;
 };
 // the kernel keeps the tiles before each request in shared memory

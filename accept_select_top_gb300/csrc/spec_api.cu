@@ -961,7 +961,6 @@ int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size
   p.out = out;
   p.lse = lse;
   p.error = v.error;
-  p.counters = v.counters;
   p.partials = v.partials;
   return launch_attention_q8(p, as_stream(stream));
 }
