@@ -263,3 +263,13 @@ def test_temperatures_of_every_size(V, T):
     near(lp, past(wlp), 1)
     near(top, past(wtop), 1)
     near(ent, went, 2)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_widest_rows_a_request(dtype):
+    """65 output rows a request of 64 nodes, 32 alternatives, nodes asked for more than once."""
+    b, n, W, V = 3, 64, 65, 5000
+    gen = torch.Generator().manual_seed(51)
+    index = torch.randint(0, n, (b, W), generator=gen).to(torch.int32) + torch.arange(b, dtype=torch.int32)[:, None] * n
+    index[1, 40:] = -1
+    check(n, W, logits_of(b * n, V, dtype, 52), index, tokens_of(b, W, V, 53), torch.tensor([1.0, 0.4, 0.0]), 32)
