@@ -420,9 +420,12 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
       const int up = evb >= 0 ? top - evb : 0;
       evb = top;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        // (the four lanes of a row keep one m: the largest of their sums decides)
+        float most = fmaxf(l[i], __shfl_xor_sync(FULL, l[i], 1));
+        most = fmaxf(most, __shfl_xor_sync(FULL, most, 2));
         if (up > 0 && m[i] > -INFINITY) {
-          const float mn = floorf(m[i] - float(raised_into_l(up, l[i]))), by = m[i] - mn;  // (exact)
+          const float mn = floorf(m[i] - float(raised_into_l(up, most))), by = m[i] - mn;  // (exact)
           const float fac = fast_exp2(by - float(up));
           l[i] *= fast_exp2(by);
           m[i] = mn;
@@ -432,6 +435,7 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
             o[q][2 * i + 1] *= fac;
           }
         }
+      }
     };
     // ---- history ----
     for (const int fh = min(E, f + (t < Th ? Th - t : 0)); f < fh; ++f) {

@@ -166,6 +166,28 @@ def test_all_values_tiny(n, D, low):
 
 
 @pytest.mark.usefixtures("bounds")
+@pytest.mark.parametrize("n, Hq, D", [(1, 4, 128), (4, 8, 64), (16, 4, 128), (33, 4, 128), (64, 4, 64)])
+@pytest.mark.parametrize("ahead", [20, 60, 100, 140])  # log2 of the weight of the small values' keys
+@pytest.mark.parametrize("low", [16, 60, 95])
+def test_small_values_of_great_weight_before_large_ones(n, Hq, D, ahead, low):
+    """The base rises by up to 103 while the sum of weights is all the small values': of keys whose weights differ
+    from one another by 2^12."""
+    b, page = 40, 16
+    a = Att(b, n, Hq, 1, D, page, [120] * b, seed=3, lo=119, hi=120, masks=[1 << i for _ in range(b) for i in range(n)], scale=ahead * math.log(2.0) / 16)
+    a.q[:] = 0
+    a.q[:, :, 0] = 4
+    a.kp[:] = 0
+    a.ks[:] = 127
+    a.k[:] = 0
+    a.v.copy_((a.v.float() * 8).bfloat16())
+    for r in a.rows[:b]:
+        p = int(a.table[r, 0])
+        a.kp[p, 0, :, 0] = torch.tensor([0x48, 0x47, 0x46, 0x45, 0x44, 0x43, 0x42, 0x41] * 2)  # 4, 3.75 .. 2.25
+        a.vs[p] = low
+    check(a.device())
+
+
+@pytest.mark.usefixtures("bounds")
 @pytest.mark.parametrize("n, D", [(1, 128), (4, 64), (33, 128), (64, 64), (64, 128)])
 @pytest.mark.parametrize("lens", [[2000, 3, 0], [200] * 40])
 def test_values_near_the_types_largest(n, D, lens):
