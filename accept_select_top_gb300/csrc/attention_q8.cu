@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
       const uint32_t word = meta[f % kRing];
       const int cnt = (word >> 8) & 31, ev = word >> 24;
       const float kf = exp_scale((word >> 16) & 255);
-      if (evb < 0 || ev > evb + kSpanUp) raise(ev);
+      if (evb < 0) evb = ev;
       float s[2][4];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -464,8 +464,9 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
         }
       }
       // y = x - m with x = s * factor + (e - evb); a row without a reference yet has y = inf
-      const int e_in = span_of(ev - evb);
-      const float de = float(e_in), x0 = xf[0] * kf, x1 = xf[1] * kf, d0 = de - m[0], d1 = de - m[1];
+      float de = float(ev - evb);
+      const float x0 = xf[0] * kf, x1 = xf[1] * kf, d0 = de - m[0], d1 = de - m[1];
+      const bool far = unsigned(ev - evb + kSpanDown) > unsigned(kSpanDown + kSpanUp);
       float y[2][4];
 #pragma unroll
       for (int q = 0; q < 2; ++q)
@@ -483,7 +484,12 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
       }
       const float ym = fmaxf(fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[0][2], y[0][3])), fmaxf(fmaxf(y[1][0], y[1][1]), fmaxf(y[1][2], y[1][3])));
       const bool unset = m[0] == -INFINITY || m[1] == -INFINITY;
-      if (__any_sync(FULL, ym > kMost || unset)) {
+      float dl = ratio_scale(evb - ev);  // l's share of P (a sum of its own below the span)
+      if (__any_sync(FULL, ym > kMost || unset || far)) {
+        if (far) {
+          if (ev > evb) raise(ev);
+          de = float(span_of(ev - evb));
+        }
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -493,6 +499,16 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
         for (int q = 0; q < 2; ++q)
 #pragma unroll
           for (int i = 0; i < 4; ++i) y[q][i] -= m[i >> 1] == -INFINITY ? 0.f : m[i >> 1];
+        if (far) {
+          dl = ev < evb ? 0.f : 1.f;
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (ev < evb) l[i >> 1] = fmaf(fast_exp2(y[q][i]), exp_scale(kExpBias + kSpanDown), l[i >> 1]);
+              y[q][i] += float(ev - evb) - de;
+            }
+        }
       }
       uint32_t pa[4];
       float sum[2];
@@ -504,17 +520,8 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
           sum[i] = q == 0 ? p0 + p1 : sum[i] + (p0 + p1);
           pa[2 * q + i] = pack_f16(p0, p1);
         }
-      const float dl = exp_scale(kExpBias - e_in);
       l[0] = fmaf(sum[0], dl, l[0]);
       l[1] = fmaf(sum[1], dl, l[1]);
-      if (ev - evb < e_in) {  // (P takes what the values would be smaller by: four products, not sixteen)
-        const __half2 f = __float2half2_rn(ratio_scale(ev - evb - e_in));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half2 y2 = __hmul2(*reinterpret_cast<const __half2*>(&pa[i]), f);
-          pa[i] = *reinterpret_cast<const uint32_t*>(&y2);
-        }
-      }
       // O += P V: b0 holds keys 2c, 2c+1, b1 keys 2c+8, 2c+9 of a column
       uint32_t v[4][D / 32];  // D / 8 bytes of each of the four keys
 #pragma unroll
@@ -610,7 +617,7 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i >= 2 && !upper) {
-          evk[i] = 1;
+          evk[i] = evb >= 0 ? evb : 1;
           continue;
         }
         const int node = nb + 2 * c + (i & 1) + 8 * (i >> 1);
@@ -638,7 +645,7 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
           for (int u = 0; u < D / 64; ++u) mx = finite_max(mx, x[u]);
           mx = over_row(mx);
         }
-        evk[i] = norm_exp(mx);
+        evk[i] = mx == 0 && evb >= 0 ? evb : norm_exp(mx);  // (a row of zeros is one whatever its exponent)
         if (who) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -648,14 +655,14 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
             }
         }
       }
-      {
-        int top = max(max(evk[0], evk[1]), max(evk[2], evk[3]));
-        top = max(top, __shfl_xor_sync(FULL, top, 1));
+      const int most = max(max(evk[0], evk[1]), max(evk[2], evk[3])), least = min(min(evk[0], evk[1]), min(evk[2], evk[3]));
+      if (__any_sync(FULL, evb < 0 || most > evb + kSpanUp || least < evb - kSpanDown)) {
+        int top = max(most, __shfl_xor_sync(FULL, most, 1));
         top = max(top, __shfl_xor_sync(FULL, top, 2));
         if (evb < 0 || top > evb + kSpanUp) raise(top);
-      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) evk[i] = evb + span_of(evk[i] - evb);
+        for (int i = 0; i < 4; ++i) evk[i] = evb + span_of(evk[i] - evb);
+      }
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
