@@ -34,13 +34,13 @@
 // tiles, and joins it through distributed shared memory.
 //   Many: the warps of the whole GPU share all the tiles, and there is no
 // barrier.  Units cut by a range boundary leave fragments (O, m, l)
-// in the workspace, and a second, dependent launch joins them (a join by the CTA's own
-// warps behind a barrier and by the last CTA of a unit took 20 us on average, 57 us at
-// most, of a 275 us call).  Only where all the warps of a CTA lie inside one unit does
+// in the workspace, and a second, dependent launch joins them (joined in the same kernel,
+// by the CTA's own warps behind a barrier and by the last CTA of a unit, they held a CTA 20 us
+// on average, 57 us at most).  Only where all the warps of a CTA lie inside one unit does
 // the CTA join its own first, so that a long context leaves few.
-//   256 chains of four, contexts 256 to 4096, 32 / 8 heads of 128: 200 us (1.13 GB
-// of cache at 5.6 TB/s); one token over 1000 keys 8.6 us.  A deeper ring is slower (four stages
-// 208 us): with more bytes in flight than the memory needs, the dependent reads at a
+//   256 chains of four, contexts 256 to 4096, 32 / 8 heads of 128: 205 us (1.13 GB
+// of cache at 5.5 TB/s); one token over 1000 keys 9.0 us.  A deeper ring is slower (four stages
+// 215 us): with more bytes in flight than the memory needs, the dependent reads at a
 // unit's ends only wait longer.
 #include "common.cuh"
 #include "kernels.cuh"
@@ -57,8 +57,8 @@ constexpr int kWarps = 12;
 constexpr int kQ8AttThreads = 32 * kWarps;
 // Query rows a kv head up to which this kernel is taken (more, where clusters take the units): its time goes with
 // the 16-row tiles, the tcgen05 kernel's hardly (in us, this one / that one; 8 kv heads of 128, no clusters): 32 rows,
-// eight contexts of 16384 103 / 104, 64 ragged ones to 4096 100 / 214; 48 rows, 16 of 4096 78 / 70, 32 of 2048
-// 82 / 86; 64 rows, 16 of 4096 92 / 70, eight of 16384 172 / 105.
+// eight contexts of 16384 106 / 107, 64 ragged ones to 4096 104 / 228; 48 rows, 16 of 4096 81 / 72, 32 of 2048
+// 85 / 91; 64 rows, 16 of 4096 96 / 72, eight of 16384 174 / 109.
 constexpr int kRowsMost = 32;
 constexpr int kTile = 16;    // keys of a tile
 constexpr int kRowTile = 16; // query rows of a unit
@@ -66,16 +66,16 @@ constexpr int kRing = 3;     // tiles in a warp's ring
 constexpr int kMinTicks = 2; // a warp gets at least this many ticks before another warp is used
 // Ticks of a tree tile in the division of the work; a history tile is one.  A tree tile and the
 // ends of its unit cost a warp some eight history tiles, nearly all latency: by 4, 6, 8 and 10 ticks the
-// chains above take 211, 205, 200 and 198 us, 512 single tokens over 100 to 600 keys 105, 107, 110 and 115.
+// chains above take 214, 209, 205 and 202 us, 512 single tokens over 100 to 600 keys 115, 114, 121 and 125.
 constexpr int kTreeTicks = 8;
 
 // A cluster takes a unit and joins it by itself, in one launch, where the units are few enough for
 // all of them to run at once (a GB300 holds 15 clusters of eight such CTAs, 36 of four, 76 of two) and a
 // warp gets at most so many ticks; else the warps of the whole GPU share the work, and a second
-// launch joins it.  In us, cluster / whole GPU, 32 / 8 heads of 128: one request, one token, 1000 keys 8.9 /
-// 17.0, 8000 13.4 / 25.3, 32000 27.2 / 34.1, 60000 (39 ticks) 42.4 / 43.3; 16 requests of 4000 30.1 / 42.0.
-// With more than kRowsMost query rows, against the tcgen05 kernel: one request of 2000 keys, 64 rows 13.8 / 29.1, 256 rows
-// 20.2 / 26.2; of 4000, 256 rows (24 ticks) 29.1 / 29.8; two of 4000, 128 rows 28.1 / 32.3.
+// launch joins it.  In us, cluster / whole GPU, 32 / 8 heads of 128: one request, one token, 1000 keys 9.3 /
+// 17.6, 8000 13.8 / 26.0, 32000 27.6 / 34.4, 60000 (39 ticks) 42.6 / 43.4; 16 requests of 4000 30.3 / 44.5.
+// With more than kRowsMost query rows, against the tcgen05 kernel: one request of 2000 keys, 64 rows 14.3 / 29.4, 256 rows
+// 20.6 / 26.5; of 4000, 256 rows (24 ticks) 29.5 / 30.0; two of 4000, 128 rows 28.5 / 33.2.
 constexpr int kClusterTicks = 32, kClusterTicksTall = 20;
 constexpr int kLargestCluster = 8;
 inline int cluster_of(long long units, int sms) {

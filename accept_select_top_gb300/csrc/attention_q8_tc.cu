@@ -22,7 +22,7 @@
 // its S.  A step is 64 keys: the scores of the next one are computed, and the
 // products of the last one added up, while a step's softmax runs.  (One S buffer with
 // places of their own for P made S always ready, but its softmax, which then has to
-// settle a half's reference before S is gone, 500 cycles longer: 333 us, not 282.)
+// settle a half's reference before S is gone, took 500 cycles longer.)
 //
 // Bound: 2 x 1024 cycles of MMA for 128 keys and 256 rows (f16 at 4096
 // multiply-adds a cycle).  Per tile shared memory moves 64 KB of converted
@@ -30,8 +30,8 @@
 // memory would add 128 KB, which is why it goes through TMEM (an MMA with A
 // from TMEM measured the same 64 cycles as one with both operands in shared
 // memory, once its descriptors are precomputed).
-//   Measured: two contexts of 32768 to 131072, 64 nodes, 64 / 8 heads of 128: 263 us
-// (1.31 PF/s); 32 requests of 2048, 64 nodes, 32 / 8 heads: 94 us (0.73 PF/s).  In the
+//   Measured: two contexts of 32768 to 131072, 64 nodes, 64 / 8 heads of 128: 267 us
+// (1.29 PF/s); 32 requests of 2048, 64 nodes, 32 / 8 heads: 97 us (0.71 PF/s).  In the
 // history a step of 64 keys takes a group some 1960 cycles, of which the softmax is 1500
 // (two warps of it and two converters share a scheduler) and the MMAs of both groups
 // 1280.  A unit's end costs about 25000 cycles more: the tree's rows are converted
@@ -141,8 +141,8 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Up to 128 tries, in a loop of four instructions and without a time hint: the warps that wait
-// took a quarter of the issue slots with a loop of ten (long contexts 282 us; 279 so, 286
-// with a hint of 20 us, 285 by test_wait, 288 where the converters sleep between their tries).
+// take issue slots from the others (the long contexts 267 us so, 268 with a hint of 20 us, 275 by
+// test_wait).
 __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -156,7 +156,7 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
 }
 // Bounded wait for the phase of the given parity: false once kWaitCycles have
 // passed or another warp has given up.  (That is looked at only where the phase does not
-// come: a warp whose waits are still met goes on. A look in every step cost 3%.)
+// come: a warp whose waits are still met goes on. With a look in every wait the long contexts take 272 us.)
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   if (mbar_poll(bar, parity)) return true;
   const long long start = clock64();
@@ -1230,7 +1230,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attention_q8_join_kernel(cons
   };
   const float2* ml2 = reinterpret_cast<const float2*>(args.slot_ml) + row % kRows;
   float Mx = -INFINITY, Ls = 0.f;
-  // (fragments two at a time: with four, fewer blocks fit a SM, and the trees take 103 us, not 100)
+  // (fragments two at a time: with four, fewer blocks fit a SM, and the trees take 111 us, not 97)
   constexpr int kAtOnce = 2;
 #pragma unroll 1
   for (int y0 = 0; y0 < nf; y0 += 2 * kAtOnce) {
