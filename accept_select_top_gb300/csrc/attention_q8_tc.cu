@@ -31,7 +31,7 @@
 // from TMEM measured the same 64 cycles as one with both operands in shared
 // memory, once its descriptors are precomputed).
 //   Measured: two contexts of 32768 to 131072, 64 nodes, 64 / 8 heads of 128: 267 us
-// (1.29 PF/s); 32 requests of 2048, 64 nodes, 32 / 8 heads: 97 us (0.71 PF/s).  In the
+// (1.29 PF/s; 277 us by eager calls); 32 requests of 2048, 64 nodes, 32 / 8 heads: 97 us (0.71 PF/s).  In the
 // history a step of 64 keys takes a group some 1960 cycles, of which the softmax is 1500
 // (two warps of it and two converters share a scheduler) and the MMAs of both groups
 // 1280.  A unit's end costs about 25000 cycles more: the tree's rows are converted
