@@ -19,10 +19,10 @@ inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// whether two arrays of `bytes` bytes have one in common
-inline bool overlap(const void* a, const void* b, size_t bytes) {
+// whether an array of `na` bytes and one of `nb` have a byte in common
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + bytes && y < x + bytes;
+  return a && b && x < y + nb && y < x + na;
 }
 
 inline int elem_bytes(int dtype) { return dtype == SPEC_F32 ? 4 : 2; }
@@ -819,6 +819,9 @@ int spec_alloc_slots(int b, int page_size, const int32_t* req_pool_idx, const in
     return SPEC_ERR_ARG;
   if (!aligned(slot_map, 16) || !aligned(positions, 16)) return SPEC_ERR_ARG;
   if (int rc = check_ws(ws, ws_bytes, kHeaderBytes + counters_bytes(b))) return rc;
+  // (one CTA writes cu_new while the others still read the lengths)
+  for (const int32_t* in : {seq_lens, new_lens, req_pool_idx})
+    if (overlap(in, size_t(b) * 4, cu_new, (size_t(b) + 1) * 4)) return SPEC_ERR_ARG;
   note_other(ws);
   const WsView v = ws_view(ws, b);
   AllocParams p{};
@@ -868,7 +871,7 @@ int spec_commit_kv_q8(int b, int Hkv, int D, int page_size, int num_layers, cons
   if (int rc = check_ws(ws, ws_bytes, kHeaderBytes)) return rc;
   // (a request's CTAs read what one of them would overwrite)
   for (const int32_t* in : {seq_lens, lens, req_pool_idx, src_index ? nullptr : src_start})
-    if (overlap(in, new_seq_lens, size_t(b) * 4)) return SPEC_ERR_ARG;
+    if (overlap(in, size_t(b) * 4, new_seq_lens, size_t(b) * 4)) return SPEC_ERR_ARG;
   CommitQ8Params p{};
   p.b = b;
   p.Hkv = Hkv;
@@ -931,6 +934,11 @@ int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size
     return SPEC_ERR_ARG;
   const size_t need = spec_workspace_size(SPEC_OP_VERIFY_ATTENTION_Q8, b, n, 1, 1, Hq, Hkv, max_seq_len);
   if (int rc = check_ws(ws, ws_bytes, need)) return rc;
+  // (a row's results are written while other warps still read the step's rows)
+  const size_t rows = size_t(b) * n, out_bytes = rows * Hq * D * 2;
+  const size_t q_bytes = ((rows - 1) * size_t(q_ld) + size_t(Hq) * D) * 2, new_bytes = ((rows - 1) * size_t(new_ld) + size_t(Hkv) * D) * 2;
+  if (overlap(out, out_bytes, q, q_bytes) || overlap(out, out_bytes, k_new, new_bytes) || overlap(out, out_bytes, v_new, new_bytes))
+    return SPEC_ERR_ARG;
   note_other(ws);
   const WsView v = ws_view(ws, b);
   AttentionQ8Params p{};

@@ -498,7 +498,8 @@ int spec_commit_kv(int b, int n, int W, int Hkv, int D, int num_layers, int page
  *   [slot_cap]: for token j of request b, at cu_new[b] + j, the slot page *
  *   page_size + (L + j) % page_size and the position L + j (entries past the
  *   last token stay as they are; both 16-byte aligned); n_left [1] = n_free
- *   less the pages taken (may be n_free itself).
+ *   less the pages taken (may be n_free itself).  cu_new overlaps none of
+ *   seq_lens, new_lens and req_pool_idx (SPEC_ERR_ARG).
  * A page_size of 1 makes page_table the slot table (any page_size >= 1 whose
  * slots stay below 2^31).  The requests of a call have different table rows.
  * A request with a bad length or row gets nothing
@@ -547,7 +548,8 @@ int spec_commit_kv_q8(int b, int Hkv, int D, int page_size, int num_layers, cons
  * q: rows [Hq, D] bf16, q_ld elements apart; q_ld and new_ld are multiples of
  * 8, so that q, k_new and v_new can be views of one packed projection.  out:
  * [b*n, Hq, D] bf16; lse: [b*n, Hq] fp32 (nullable), natural log.  A row that
- * sees no key gives out 0 and lse -inf.  An inf or NaN in a node's V reaches
+ * sees no key gives out 0 and lse -inf.  out overlaps none of q, k_new and v_new
+ * (SPEC_ERR_ARG).  An inf or NaN in a node's V reaches
  * only the rows that see the node.  max_seq_len bounds every seq_len (a larger
  * one sets SPEC_DEV_LENGTH and is clamped); a close bound is quicker where
  * there are few requests.  A page id out of range sets

@@ -187,3 +187,22 @@ def test_binding_refuses_a_workspace_of_another_device():
     assert ops._workspace_in(ws, 1) == FAKE
     with pytest.raises(ops.SpecError, match="device 1"):
         ops._workspace_in(ws, 0)
+
+
+@pytest.mark.parametrize("change", [
+    dict(out=FAKE), dict(q=FAKE + 0x100000, kn=FAKE), dict(q=FAKE + 0x100000, kn=FAKE + 0x100000),
+    # the last bytes of out and of strided rows
+    dict(q=FAKE + 8 * 8 * 128 * 2 - 16, kn=FAKE + 0x100000, vn=FAKE + 0x100000),
+    dict(q=FAKE + 0x100000, kn=FAKE + 0x100000, vn=FAKE - (7 * 2048 + 256) * 2 + 16, ld=2048)])
+def test_attention_refuses_its_output_over_its_rows(lib, change):
+    """out of 8 rows of 8 heads of 128: a warp writes it while others read the step's rows."""
+    a = dict(ws_bytes=1 << 30)
+    a.update(change)
+    assert lib.spec_verify_attention_q8(*_attention(**a)) == -1
+
+
+@pytest.mark.parametrize("change", [dict(cu=FAKE), dict(cu=FAKE - 8, lens=FAKE, new=FAKE + 0x100, idx=FAKE + 0x200),
+                                    dict(cu=FAKE + 0x104, lens=FAKE, new=FAKE + 0x100, idx=FAKE + 0x200),
+                                    dict(cu=FAKE + 0x204, lens=FAKE, new=FAKE + 0x100, idx=FAKE + 0x200)])
+def test_alloc_refuses_offsets_over_its_lengths(lib, change):
+    assert lib.spec_alloc_slots(*_alloc(ws_bytes=1 << 20, **change)) == -1
