@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kQ8AttThreads, 1) attention_q8_rows_kernel(con
           for (int u = 0; u < D / 64; ++u) mx = finite_max(mx, x[u]);
           mx = over_row(mx);
         }
-        evk[i] = mx == 0 && evb >= 0 ? evb : norm_exp(mx);  // (a row of zeros is one whatever its exponent)
+        evk[i] = node >= a.n && evb >= 0 ? evb : norm_exp(mx);
         if (who) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)

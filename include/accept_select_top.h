@@ -549,12 +549,15 @@ int spec_commit_kv_q8(int b, int Hkv, int D, int page_size, int num_layers, cons
  * 8, so that q, k_new and v_new can be views of one packed projection.  out:
  * [b*n, Hq, D] bf16; lse: [b*n, Hq] fp32 (nullable), natural log.  A row that
  * sees no key gives out 0 and lse -inf.  out overlaps none of q, k_new and v_new
- * (SPEC_ERR_ARG).  An inf or NaN in a node's V reaches
- * only the rows that see the node.  max_seq_len bounds every seq_len (a larger
- * one sets SPEC_DEV_LENGTH and is clamped); a close bound is quicker where
- * there are few requests.  A page id out of range sets
- * SPEC_DEV_INDEX and its keys do not count.  b <= 2048.  The workspace holds the
- * merge slots (about 51 MB, independent of the sizes). */
+ * (SPEC_ERR_ARG).  An inf or NaN in a node's V reaches only the rows that see the
+ * node.  Every key counts by its score alone, whatever its value's size; values
+ * 2^-64 and less below the largest of their kv head's may count as zeros.
+ * max_seq_len bounds every seq_len (a larger one sets SPEC_DEV_LENGTH and is
+ * clamped); a close bound is quicker where there are few requests.  A page id out
+ * of range sets SPEC_DEV_INDEX and its keys do not count.  b <= 2048, and the tiles
+ * b * (max_seq_len / 16 + 1 + 8 ceil(n / 16)) * Hkv * ceil(n Hq / Hkv / 16) stay
+ * below 2^31.  The workspace holds the merge slots (about 51 MB, independent of the
+ * sizes). */
 int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size, const void* q, int64_t q_ld,
                              const void* k_new, const void* v_new, int64_t new_ld, const void* k_pages,
                              const void* v_pages, const uint8_t* k_scales, const uint8_t* v_scales,

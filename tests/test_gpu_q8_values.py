@@ -9,7 +9,7 @@ f16 is off by at most 2^-25: out moves by at most
     2^-25 sum_j |v_j| 2^-e_j / kappa <= 2^-30 M sum_j |v_j| 2^-e_j.
 A value whose exponent counts as the base's less 64 (M is taken with those: the base is at most the
 largest exponent) is off by at most 2^-25 in v_j 2^-e_j: out moves by at most 2^-25 M for each of
-the K keys (P_j / kappa <= M)."""
+the K keys (P_j / kappa <= M).  A subnormal bf16 is off by at most 2^-134."""
 import math
 
 import pytest
@@ -55,7 +55,7 @@ def reference(n, q, k_new, v_new, kp, vp, ks, vs, table, rows, lens, see, scale)
         M = (p * torch.exp2(torch.maximum(e, e.amax(-1, keepdim=True) - 64))[:, None]).amax(-1, keepdim=True)
         seen = (~hide).double()[None]
         lost = 2.0 ** -30 * M * (seen @ (v.abs() * torch.exp2(-e)[..., None])) + 2.0 ** -25 * M * seen.sum(-1, keepdim=True)
-        bar = 2.0 ** -8 * out.abs() + (2.0 ** -11 + d)[..., None] * (p @ v.abs()) + lost
+        bar = 2.0 ** -8 * out.abs() + (2.0 ** -11 + d)[..., None] * (p @ v.abs()) + lost + 2.0 ** -134
 
         def back(t):
             return t.reshape(Hkv, n, G, *t.shape[2:]).transpose(0, 1).reshape(n, Hq, *t.shape[2:])
@@ -227,4 +227,16 @@ def test_zeros_and_far_values_under_load(n, Hq, Hkv, D, page, what, bound):
         x.vs.copy_(torch.randint(95, 146, x.vs.shape, generator=gen, device=DEV))
         f = torch.randint(-25, 26, (rows, 1, 1), generator=gen, device=DEV)
         x.v.copy_((x.v.double() * torch.exp2(f.double())).bfloat16())
+    check(x.args)
+
+
+@pytest.mark.parametrize("bound", [None, 1 << 20])
+@pytest.mark.parametrize("n, Hq, Hkv, D", [(2, 10, 2, 128), (4, 12, 4, 128), (8, 6, 2, 64), (16, 2, 2, 128), (64, 4, 2, 64)])
+def test_short_histories_beside_zero_nodes_of_great_weight(n, Hq, Hkv, D, bound):
+    """A zero node with nearly all the weight must not take the others' P below f16's range."""
+    x = Load(n, Hq, Hkv, D, 16, [i % 7 for i in range(300)], seed=n, scale=4 / math.sqrt(D), lo=125, hi=126, bound=bound)
+    x.ks.fill_(113)
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    x.v.copy_((x.v.float() * 2.0 ** 4).bfloat16())
+    x.v[torch.rand(x.v.shape[0], generator=gen, device=DEV) < 0.4] = 0
     check(x.args)
