@@ -406,4 +406,97 @@ struct LogprobParams {
 constexpr int kLogprobMaxK = 32;  // alternatives of a row
 int launch_token_logprobs(const LogprobParams& p, cudaStream_t stream);
 
+// Requests that share pages: forks, pages given back, compaction, copies.
+struct ForkParams {
+  int b, page_size;
+  const int32_t* parents;
+  const int32_t* children;
+  const int32_t* fork_lens;
+  int32_t* share_counts;
+  long long num_pages;
+  const int32_t* free_ids;
+  int free_cap;
+  const int32_t* n_free;
+  int32_t* page_table;
+  int req_rows, row_pages;
+  int32_t* req_to_token;  // nullable
+  int row_w;
+  int vec_slots;  // every page's slots start on 16 bytes
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t* n_copies;
+  int32_t* n_left;
+  uint32_t* error;
+  uint32_t* counters;
+};
+int launch_fork_pages(const ForkParams& p, cudaStream_t stream);
+
+struct ReleaseParams {
+  int b, page_size;
+  const int32_t* req_pool_idx;
+  const int32_t* seq_lens;
+  const int32_t* keep_lens;  // nullable
+  int32_t* share_counts;
+  long long num_pages;
+  int32_t* free_ids;
+  int free_cap;
+  const int32_t* n_free;
+  const int32_t* page_table;
+  int req_rows, row_pages;
+  int32_t* n_left;
+  uint32_t* error;
+  int* totals;  // [8]
+  int2* note;   // [num_pages]
+};
+int launch_release_pages(const ReleaseParams& p, cudaStream_t stream);
+size_t release_partial_bytes(long long pages);
+
+struct CompactParams {
+  int b, page_size;
+  const int32_t* req_pool_idx;
+  const int32_t* seq_lens;
+  long long limit;
+  const int32_t* share_counts;
+  long long num_pages;
+  const int32_t* free_ids;
+  int free_cap;
+  const int32_t* n_free;
+  const int32_t* page_table;
+  int req_rows, row_pages;
+  const int32_t* req_to_token;  // nullable
+  int row_w;
+  int vec_slots;
+  int32_t* new_share_counts;
+  int32_t* new_free_ids;
+  int32_t* n_left;
+  int32_t* new_page_table;
+  int32_t* new_req_to_token;
+  int32_t* move_src;
+  int32_t* move_dst;
+  int32_t* n_moves;
+  uint32_t* error;
+  int4* plan;         // {whether there is one, limit, moves, free pages}
+  int2* totals;       // [16]
+  uint32_t* bits;     // [ceil(num_pages / 32)] free pages
+  int32_t* pre_hole;  // [same] holes and moved pages before each word
+  int32_t* pre_live;
+};
+int launch_compact_pages(const CompactParams& p, cudaStream_t stream);
+size_t compact_partial_bytes(long long pages);
+
+struct CopyParams {
+  int num_layers, max_copies;
+  long long page_bytes, num_pages;
+  int scale_bytes;  // 0: no scales
+  void* k_layers[kMaxLayers];
+  void* v_layers[kMaxLayers];
+  uint8_t* k_scales[kMaxLayers];
+  uint8_t* v_scales[kMaxLayers];
+  const int32_t* src_ids;
+  const int32_t* dst_ids;
+  const int32_t* n_copies;
+  uint32_t* error;
+};
+int launch_copy_pages(const CopyParams& p, int sms, cudaStream_t stream);
+
 }  // namespace spec

@@ -107,6 +107,10 @@ size_t partial_bytes(int op, int b, int n, int k, int V, int Hq, int Hkv, int ma
       return commit_partial_bytes(b, n);
     case SPEC_OP_VERIFY_ATTENTION_Q8:
       return attention_q8_partial_bytes();
+    case SPEC_OP_RELEASE_PAGES:
+      return release_partial_bytes(V);
+    case SPEC_OP_COMPACT_PAGES:
+      return compact_partial_bytes(V);
     default:
       return 0;
   }
@@ -1026,3 +1030,175 @@ int verify_greedy_compact(int b, int n, int S, int V, int dtype, const void* log
 }
 
 }  // namespace spec
+
+namespace {
+
+// What the calls that walk table rows have in common: sizes whose products stay below 2^31.
+bool table_ok(int b, int page_size, int64_t num_pages, int req_rows, int row_pages, const void* slots, int row_w) {
+  return b >= 0 && b <= kAllocMaxB && page_size >= 1 && num_pages >= 1 && req_rows >= 1 && row_pages >= 1 &&
+         (!slots || row_w >= 1) && num_pages <= ((int64_t(1) << 31) - 1) / page_size &&
+         int64_t(row_pages) * page_size < (int64_t(1) << 31) && int64_t(b) * row_pages < (int64_t(1) << 31);
+}
+
+bool vec_slots(const void* slots, int row_w, int page_size) { return page_size % 4 == 0 && row_w % 4 == 0 && aligned(slots, 16); }
+
+}  // namespace
+
+extern "C" {
+
+int spec_fork_pages(int b, int page_size, const int32_t* parents, const int32_t* children, const int32_t* fork_lens,
+                    int32_t* share_counts, int64_t num_pages, const int32_t* free_ids, int free_cap,
+                    const int32_t* n_free, int32_t* page_table, int req_rows, int row_pages, int32_t* req_to_token,
+                    int row_w, int32_t* copy_src, int32_t* copy_dst, int32_t* n_copies, int32_t* n_left, void* ws,
+                    size_t ws_bytes, void* stream) {
+  if (!table_ok(b, page_size, num_pages, req_rows, row_pages, req_to_token, row_w) || free_cap < 0) return SPEC_ERR_ARG;
+  if (b == 0) return SPEC_OK;
+  if (!parents || !children || !fork_lens || !share_counts || !n_free || !page_table || !copy_src || !copy_dst ||
+      !n_copies || !n_left || n_copies == n_left || n_copies == n_free || (!free_ids && free_cap > 0))
+    return SPEC_ERR_ARG;
+  if (int rc = check_ws(ws, ws_bytes, kHeaderBytes + counters_bytes(b))) return rc;
+  note_other(ws);
+  const WsView v = ws_view(ws, b);
+  ForkParams p{};
+  p.b = b;
+  p.page_size = page_size;
+  p.parents = parents;
+  p.children = children;
+  p.fork_lens = fork_lens;
+  p.share_counts = share_counts;
+  p.num_pages = num_pages;
+  p.free_ids = free_ids;
+  p.free_cap = free_cap;
+  p.n_free = n_free;
+  p.page_table = page_table;
+  p.req_rows = req_rows;
+  p.row_pages = row_pages;
+  p.req_to_token = req_to_token;
+  p.row_w = row_w;
+  p.vec_slots = vec_slots(req_to_token, row_w, page_size);
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  p.n_copies = n_copies;
+  p.n_left = n_left;
+  p.error = v.error;
+  p.counters = v.counters;
+  return launch_fork_pages(p, as_stream(stream));
+}
+
+int spec_release_pages(int b, int page_size, const int32_t* req_pool_idx, const int32_t* seq_lens,
+                       const int32_t* keep_lens, int32_t* share_counts, int64_t num_pages, int32_t* free_ids,
+                       int free_cap, const int32_t* n_free, const int32_t* page_table, int req_rows, int row_pages,
+                       int32_t* n_left, void* ws, size_t ws_bytes, void* stream) {
+  if (!table_ok(b, page_size, num_pages, req_rows, row_pages, nullptr, 0) || free_cap < 0) return SPEC_ERR_ARG;
+  if (b == 0) return SPEC_OK;
+  if (!req_pool_idx || !seq_lens || !share_counts || !n_free || !page_table || !n_left || (!free_ids && free_cap > 0))
+    return SPEC_ERR_ARG;
+  if (int rc = check_ws(ws, ws_bytes, spec_workspace_size(SPEC_OP_RELEASE_PAGES, b, 1, 1, int(num_pages), 0, 0, 0))) return rc;
+  note_other(ws);
+  const WsView v = ws_view(ws, b);
+  ReleaseParams p{};
+  p.b = b;
+  p.page_size = page_size;
+  p.req_pool_idx = req_pool_idx;
+  p.seq_lens = seq_lens;
+  p.keep_lens = keep_lens;
+  p.share_counts = share_counts;
+  p.num_pages = num_pages;
+  p.free_ids = free_ids;
+  p.free_cap = free_cap;
+  p.n_free = n_free;
+  p.page_table = page_table;
+  p.req_rows = req_rows;
+  p.row_pages = row_pages;
+  p.n_left = n_left;
+  p.error = v.error;
+  p.totals = reinterpret_cast<int*>(v.partials);
+  p.note = reinterpret_cast<int2*>(v.partials + 256);
+  return launch_release_pages(p, as_stream(stream));
+}
+
+int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const int32_t* seq_lens, int64_t limit,
+                       const int32_t* share_counts, int64_t num_pages, const int32_t* free_ids, int free_cap,
+                       const int32_t* n_free, const int32_t* page_table, int req_rows, int row_pages,
+                       const int32_t* req_to_token, int row_w, int32_t* new_share_counts, int32_t* new_free_ids,
+                       int32_t* n_left, int32_t* new_page_table, int32_t* new_req_to_token, int32_t* move_src,
+                       int32_t* move_dst, int32_t* n_moves, void* ws, size_t ws_bytes, void* stream) {
+  if (!table_ok(b, page_size, num_pages, req_rows, row_pages, req_to_token, row_w) || free_cap < 0 || limit < 0)
+    return SPEC_ERR_ARG;
+  if (b == 0) return SPEC_OK;
+  if (!req_pool_idx || !seq_lens || !share_counts || !n_free || !page_table || !new_share_counts || !n_left ||
+      !new_page_table || !n_moves || n_moves == n_left || n_moves == n_free || (req_to_token && !new_req_to_token) ||
+      ((!free_ids || !new_free_ids || !move_src || !move_dst) && free_cap > 0))
+    return SPEC_ERR_ARG;
+  if (int rc = check_ws(ws, ws_bytes, spec_workspace_size(SPEC_OP_COMPACT_PAGES, b, 1, 1, int(num_pages), 0, 0, 0))) return rc;
+  note_other(ws);
+  const WsView v = ws_view(ws, b);
+  CompactParams p{};
+  p.b = b;
+  p.page_size = page_size;
+  p.req_pool_idx = req_pool_idx;
+  p.seq_lens = seq_lens;
+  p.limit = limit;
+  p.share_counts = share_counts;
+  p.num_pages = num_pages;
+  p.free_ids = free_ids;
+  p.free_cap = free_cap;
+  p.n_free = n_free;
+  p.page_table = page_table;
+  p.req_rows = req_rows;
+  p.row_pages = row_pages;
+  p.req_to_token = req_to_token;
+  p.row_w = row_w;
+  p.vec_slots = vec_slots(new_req_to_token, row_w, page_size);
+  p.new_share_counts = new_share_counts;
+  p.new_free_ids = new_free_ids;
+  p.n_left = n_left;
+  p.new_page_table = new_page_table;
+  p.new_req_to_token = new_req_to_token;
+  p.move_src = move_src;
+  p.move_dst = move_dst;
+  p.n_moves = n_moves;
+  p.error = v.error;
+  const size_t words = align256(size_t(num_pages + 31) / 32 * 4);
+  p.plan = reinterpret_cast<int4*>(v.partials);
+  p.totals = reinterpret_cast<int2*>(v.partials + 16);
+  p.bits = reinterpret_cast<uint32_t*>(v.partials + 256);
+  p.pre_hole = reinterpret_cast<int32_t*>(v.partials + 256 + words);
+  p.pre_live = reinterpret_cast<int32_t*>(v.partials + 256 + 2 * words);
+  return launch_compact_pages(p, as_stream(stream));
+}
+
+int spec_copy_pages(int num_layers, int64_t page_bytes, int scale_bytes, void* const* k_layers, void* const* v_layers,
+                    uint8_t* const* k_scales, uint8_t* const* v_scales, int64_t num_pages, const int32_t* src_ids,
+                    const int32_t* dst_ids, int max_copies, const int32_t* n_copies, void* ws, size_t ws_bytes,
+                    void* stream) {
+  if (num_layers < 1 || num_layers > kMaxLayers || page_bytes < 16 || page_bytes % 16 || scale_bytes < 0 ||
+      num_pages < 1 || num_pages >= (int64_t(1) << 31) || max_copies < 0)
+    return SPEC_ERR_ARG;
+  if (max_copies == 0) return SPEC_OK;
+  if (!k_layers || !v_layers || (scale_bytes && (!k_scales || !v_scales)) || !src_ids || !dst_ids || !n_copies)
+    return SPEC_ERR_ARG;
+  if (int rc = check_ws(ws, ws_bytes, kHeaderBytes)) return rc;
+  CopyParams p{};
+  p.num_layers = num_layers;
+  p.max_copies = max_copies;
+  p.page_bytes = page_bytes;
+  p.num_pages = num_pages;
+  p.scale_bytes = scale_bytes;
+  for (int i = 0; i < num_layers; ++i) {
+    if (!k_layers[i] || !v_layers[i] || !aligned(k_layers[i], 16) || !aligned(v_layers[i], 16)) return SPEC_ERR_ARG;
+    if (scale_bytes && (!k_scales[i] || !v_scales[i])) return SPEC_ERR_ARG;
+    p.k_layers[i] = k_layers[i];
+    p.v_layers[i] = v_layers[i];
+    p.k_scales[i] = scale_bytes ? k_scales[i] : nullptr;
+    p.v_scales[i] = scale_bytes ? v_scales[i] : nullptr;
+  }
+  note_other(ws);
+  p.src_ids = src_ids;
+  p.dst_ids = dst_ids;
+  p.n_copies = n_copies;
+  p.error = ws_view(ws, 1).error;
+  return launch_copy_pages(p, device_sms(), as_stream(stream));
+}
+
+}  // extern "C"

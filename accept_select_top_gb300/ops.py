@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(_HERE, "_build", "libspecdec.so")
 SPEC_OK = 0
 SPEC_F32, SPEC_BF16 = 0, 1
 (OP_SELECT_TOPK, OP_BUILD_TREE, OP_VERIFY_ATTENTION, OP_VERIFY_GREEDY, OP_VERIFY_SAMPLING, OP_COMMIT_KV,
- OP_VERIFY_TARGET_ONLY, OP_ALLOC_SLOTS, OP_COMMIT_KV_Q8, OP_VERIFY_ATTENTION_Q8, OP_TOKEN_LOGPROBS) = range(11)
+ OP_VERIFY_TARGET_ONLY, OP_ALLOC_SLOTS, OP_COMMIT_KV_Q8, OP_VERIFY_ATTENTION_Q8, OP_TOKEN_LOGPROBS,
+ OP_FORK_PAGES, OP_COPY_PAGES, OP_RELEASE_PAGES, OP_COMPACT_PAGES) = range(15)
 DEV_INDEX, DEV_INVARIANT, DEV_LENGTH, DEV_TIMEOUT, DEV_SPACE = 1, 2, 4, 8, 16
 Q8_EXP_MIN = 16  # smallest scale exponent byte the library writes (the scale is 2^(e - 127))
 _ERRORS = {-1: "bad argument", -2: "workspace too small or misaligned", -3: "CUDA launch failed",
@@ -33,7 +34,8 @@ EXPORTS = ["spec_workspace_size", "spec_workspace_init", "spec_workspace_set_ove
            "spec_verify_chain_greedy", "spec_assign_draft_locs", "spec_duplicate_prefix_tail",
            "spec_build_full_mask", "spec_add_penalties", "spec_renorm_probs", "spec_verify_sampling_probs",
            "spec_verify_target_only_probs", "spec_commit_kv", "spec_alloc_slots", "spec_commit_kv_q8",
-           "spec_verify_attention_q8", "spec_token_logprobs", "spec_verify_greedy_noalloc",
+           "spec_verify_attention_q8", "spec_fork_pages", "spec_copy_pages", "spec_release_pages",
+           "spec_compact_pages", "spec_token_logprobs", "spec_verify_greedy_noalloc",
            "spec_noalloc_last_error"]
 
 
@@ -72,6 +74,10 @@ def _load() -> ctypes.CDLL:
         "spec_commit_kv_q8": (I, [I, I, I, I, I, P, P, L, L, P, P, P, P, L, P, I, I, P, P, P, P, P, I, P, P, Z, P]),
         "spec_verify_attention_q8": (I, [I, I, I, I, I, I, P, L, P, P, L, P, P, P, P, L, P, I, I, P, P, I, P, F, P, P,
                                          P, Z, P]),
+        "spec_fork_pages": (I, [I, I, P, P, P, P, L, P, I, P, P, I, I, P, I, P, P, P, P, P, Z, P]),
+        "spec_copy_pages": (I, [I, L, I, P, P, P, P, L, P, P, I, P, P, Z, P]),
+        "spec_release_pages": (I, [I, I, P, P, P, P, L, P, I, P, P, I, I, P, P, Z, P]),
+        "spec_compact_pages": (I, [I, I, P, P, L, P, L, P, I, P, P, I, I, P, I, P, P, P, P, P, P, P, P, P, Z, P]),
         "spec_token_logprobs": (I, [I, I, I, I, I, P, P, P, P, I, P, P, P, P, P, Z, P]),
         "spec_verify_greedy_noalloc": (I, [I, I, I, I, I, P, P, P, P, P, P, P, P, P, P, P]),
         "spec_noalloc_last_error": (I, [P]),
@@ -505,6 +511,116 @@ def spec_verify_attention_q8(b: int, n: int, Hq: int, Hkv: int, D: int, page_siz
         _in(mask_bits, _I64, rows, dev, "mask_bits"), scale, _in(out, _BF16, rows * Hq * D, dev, "out"),
         None if lse is None else _in(lse, _F32, rows * Hq, dev, "lse"), _workspace_in(ws, dev), ws.nbytes,
         _raw_stream(stream, dev)), "spec_verify_attention_q8")
+
+
+def _slots_in(req_to_token, rows: int, dev: int, what: str):
+    """Address and width of a slot table with as many rows as the page table (None: no slot table)."""
+    if req_to_token is None:
+        return None, 0
+    if req_to_token.dim() != 2 or req_to_token.shape[0] != rows:
+        raise SpecError(f"{what} and page_table must have the same rows")
+    return _in(req_to_token, _I32, 1, dev, what), req_to_token.shape[1]
+
+
+def spec_fork_pages(b: int, page_size: int, parents, children, fork_lens, share_counts, free_ids, n_free, page_table,
+                    req_to_token, copy_src, copy_dst, n_copies, n_left, ws: Workspace, stream=None):
+    """Children (table rows) that share their parents' whole pages up to fork_lens[r] tokens, with a page of their
+    own behind them; see the header.  copy_src, copy_dst and n_copies go to spec_copy_pages.  share_counts has one
+    entry a page of the pool; req_to_token may be None; n_left may be n_free."""
+    dev = _device()
+    rows, row_pages = page_table.shape
+    slots, width = _slots_in(req_to_token, rows, dev, "req_to_token")
+    _check(LIB.spec_fork_pages(
+        b, page_size, _in(parents, _I32, b, dev, "parents"), _in(children, _I32, b, dev, "children"),
+        _in(fork_lens, _I32, b, dev, "fork_lens"), _in(share_counts, _I32, 1, dev, "share_counts"), share_counts.numel(),
+        _in(free_ids, _I32, 0, dev, "free_ids"), free_ids.numel(), _in(n_free, _I32, 1, dev, "n_free"),
+        _in(page_table, _I32, 1, dev, "page_table"), rows, row_pages, slots, width, _in(copy_src, _I32, b, dev, "copy_src"),
+        _in(copy_dst, _I32, b, dev, "copy_dst"), _in(n_copies, _I32, 1, dev, "n_copies"), _in(n_left, _I32, 1, dev, "n_left"),
+        _workspace_in(ws, dev), ws.nbytes, _raw_stream(stream, dev)), "spec_fork_pages")
+
+
+def _pool_pages(t: torch.Tensor, page_size: int, dev: int, what: str):
+    """(pages, bytes of a page) of one layer's K or V: bf16 slots [num_slots, Hkv, D] or e4m3 pages
+    [num_pages, Hkv, page_size, D]."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise SpecError(f"{what}: expected a contiguous tensor on the current CUDA device")
+    if t.dtype is _BF16 and t.dim() == 3:
+        slots, heads, D = t.shape
+        if page_size < 1 or slots < page_size:
+            raise SpecError(f"{what}: {slots} slots, pages of {page_size}")
+        return slots // page_size, page_size * heads * D * 2
+    if t.dtype not in (_E4M3, torch.uint8) or t.dim() != 4 or t.shape[2] != page_size:
+        raise SpecError(f"{what}: expected bf16 [num_slots, Hkv, D] or e4m3 [num_pages, Hkv, {page_size}, D], got {t.dtype} {tuple(t.shape)}")
+    return t.shape[0], t.shape[1] * page_size * t.shape[3]
+
+
+def spec_copy_pages(page_size: int, k_layers, v_layers, k_scales, v_scales, src_ids, dst_ids, n_copies, ws: Workspace,
+                    stream=None):
+    """Pages src_ids[i] copied to dst_ids[i], i < n_copies[0], in every layer: one tensor a layer (a sequence, or a
+    LayerList kept by the caller).  k_scales and v_scales: of the 8-bit cache, else None."""
+    dev = _device()
+    k_layers, v_layers = _layers(k_layers), _layers(v_layers)
+    layers = len(k_layers)
+    pages, page_bytes = k_layers.check(_pool_pages, page_size, dev, "k_layers")
+    if len(v_layers) != layers or v_layers.check(_pool_pages, page_size, dev, "v_layers") != (pages, page_bytes):
+        raise SpecError("k_layers and v_layers must have the same layers, pages and page size")
+    quantised = k_layers.first.dim() == 4
+    if quantised != (v_layers.first.dim() == 4) or quantised != (k_scales is not None) or quantised != (v_scales is not None):
+        raise SpecError("scales go with e4m3 pages, and only with them")
+    heads, kp, vp = 0, None, None
+    if quantised:
+        k_scales, v_scales = _layers(k_scales), _layers(v_scales)
+        heads = k_layers.first.shape[1]
+        if len(k_scales) != layers or len(v_scales) != layers:
+            raise SpecError("every layer list must have the same length")
+        k_scales.check(_in, torch.uint8, pages * heads, dev, "k_scales")
+        v_scales.check(_in, torch.uint8, pages * heads, dev, "v_scales")
+        kp, vp = k_scales.ptr, v_scales.ptr
+    copies = min(src_ids.numel(), dst_ids.numel())
+    _check(LIB.spec_copy_pages(
+        layers, page_bytes, heads, k_layers.ptr, v_layers.ptr, kp, vp, pages, _in(src_ids, _I32, 0, dev, "src_ids"),
+        _in(dst_ids, _I32, 0, dev, "dst_ids"), copies, _in(n_copies, _I32, 1, dev, "n_copies"), _workspace_in(ws, dev),
+        ws.nbytes, _raw_stream(stream, dev)), "spec_copy_pages")
+
+
+def spec_release_pages(b: int, page_size: int, req_pool_idx, seq_lens, keep_lens, share_counts, free_ids, n_free,
+                       page_table, n_left, ws: Workspace, stream=None):
+    """Pages behind keep_lens[r] tokens (None: every page) given up; those without another holder are pushed onto
+    free_ids behind its n_free[0] entries.  n_left may be n_free."""
+    dev = _device()
+    rows, row_pages = page_table.shape
+    _check(LIB.spec_release_pages(
+        b, page_size, _in(req_pool_idx, _I32, b, dev, "req_pool_idx"), _in(seq_lens, _I32, b, dev, "seq_lens"),
+        None if keep_lens is None else _in(keep_lens, _I32, b, dev, "keep_lens"),
+        _in(share_counts, _I32, 1, dev, "share_counts"), share_counts.numel(), _in(free_ids, _I32, 0, dev, "free_ids"),
+        free_ids.numel(), _in(n_free, _I32, 1, dev, "n_free"), _in(page_table, _I32, 1, dev, "page_table"), rows, row_pages,
+        _in(n_left, _I32, 1, dev, "n_left"), _workspace_in(ws, dev), ws.nbytes, _raw_stream(stream, dev)),
+        "spec_release_pages")
+
+
+def spec_compact_pages(b: int, page_size: int, req_pool_idx, seq_lens, limit: int, share_counts, free_ids, n_free,
+                       page_table, req_to_token, new_share_counts, new_free_ids, n_left, new_page_table,
+                       new_req_to_token, move_src, move_dst, n_moves, ws: Workspace, stream=None):
+    """Pages in use moved below `limit` (0: as low as they go): new tables, counts and free list, and the moves for
+    spec_copy_pages.  Every output may be its input; req_to_token and new_req_to_token may be None."""
+    dev = _device()
+    rows, row_pages = page_table.shape
+    if new_page_table.shape != page_table.shape:
+        raise SpecError("new_page_table and page_table must have one shape")
+    slots, width = _slots_in(req_to_token, rows, dev, "req_to_token")
+    new_slots, new_width = _slots_in(new_req_to_token, rows, dev, "new_req_to_token")
+    if (slots is None) != (new_slots is None) or width != new_width:
+        raise SpecError("new_req_to_token and req_to_token must have one shape")
+    pages, cap = share_counts.numel(), free_ids.numel()
+    _check(LIB.spec_compact_pages(
+        b, page_size, _in(req_pool_idx, _I32, b, dev, "req_pool_idx"), _in(seq_lens, _I32, b, dev, "seq_lens"), limit,
+        _in(share_counts, _I32, 1, dev, "share_counts"), pages, _in(free_ids, _I32, 0, dev, "free_ids"), cap,
+        _in(n_free, _I32, 1, dev, "n_free"), _in(page_table, _I32, 1, dev, "page_table"), rows, row_pages, slots, width,
+        _in(new_share_counts, _I32, pages, dev, "new_share_counts"), _in(new_free_ids, _I32, cap, dev, "new_free_ids"),
+        _in(n_left, _I32, 1, dev, "n_left"), _in(new_page_table, _I32, 1, dev, "new_page_table"), new_slots,
+        _in(move_src, _I32, cap, dev, "move_src"), _in(move_dst, _I32, cap, dev, "move_dst"),
+        _in(n_moves, _I32, 1, dev, "n_moves"), _workspace_in(ws, dev), ws.nbytes, _raw_stream(stream, dev)),
+        "spec_compact_pages")
 
 
 def spec_token_logprobs(b: int, n: int, W: int, logits, row_index, tokens, temperatures, k: int, logprobs, entropy,

@@ -89,7 +89,11 @@ extern "C" {
 #define SPEC_OP_COMMIT_KV_Q8 8
 #define SPEC_OP_VERIFY_ATTENTION_Q8 9
 #define SPEC_OP_TOKEN_LOGPROBS 10 /* n: rows a request (W, up to 65), k: alternatives (up to 32) */
-#define SPEC_OP_LAST SPEC_OP_TOKEN_LOGPROBS
+#define SPEC_OP_FORK_PAGES 11
+#define SPEC_OP_COPY_PAGES 12
+#define SPEC_OP_RELEASE_PAGES 13 /* V: pages of the pool */
+#define SPEC_OP_COMPACT_PAGES 14 /* V: pages of the pool */
+#define SPEC_OP_LAST SPEC_OP_COMPACT_PAGES
 
 /* Batch sizes up to which calls of different sizes may share a workspace. */
 #define SPEC_WORKSPACE_SHARED_B 4096
@@ -565,6 +569,97 @@ int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size
                              const int32_t* req_pool_idx, const int32_t* seq_lens, int max_seq_len,
                              const uint64_t* mask_bits, float scale, void* out, float* lse, void* ws,
                              size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Requests that share pages: forks, pages given back, copies, compaction.  The
+ * pages have no counterpart; parallel samples of a prompt and beams hold the
+ * prompt's KV once.  They work on page_table and the free list of
+ * spec_alloc_slots (any page_size >= 1) and on the pages of either cache.
+ *
+ * share_counts [num_pages] int32, zero-filled once: the holders of a page beyond
+ * the first (0 for a free page, too), so spec_alloc_slots and the commits need not
+ * know of it.  Only whole pages are shared, and tokens are only appended, so no
+ * shared page is written: a request that goes on from the middle of a page it
+ * shares (cut back to there, for instance) is forked there first.  The rows of a
+ * call hold at most 2^31 - 1 pages (b * row_pages), b <= 16384.  Results do not
+ * depend on the order in which a call's threads run.
+ *
+ * spec_fork_pages -- child r (table row children[r]) starts as the first
+ * fork_lens[r] tokens of its parent (table row parents[r]).  With L = fork_lens[r]:
+ * entries i < L / page_size of the child's row are the parent's, whose
+ * share_counts go up by one; where L % page_size, the entry behind them is a page
+ * of its own: in child order, the j-th of the call is free_ids[n_free[0] - 1 - j],
+ * and (copy_src[j], copy_dst[j]) = (the parent's page, it) is a pair for
+ * spec_copy_pages (arrays of b).  n_copies [1] = those pages, n_left [1] = n_free
+ * less them (may be n_free itself).  req_to_token (nullable): entries [0, L) of
+ * the child's row.  A parent may have many children; the children are distinct
+ * rows, none of them a parent in the call (a child that is its own parent sets
+ * SPEC_DEV_INDEX).  A bad length or row leaves its child as it was
+ * (SPEC_DEV_LENGTH / SPEC_DEV_INDEX); too short a free list sets SPEC_DEV_SPACE and
+ * the call does nothing (n_copies 0, n_left = n_free).  A bad page id gives an entry
+ * (and slots) of -1 and SPEC_DEV_INDEX.
+ * ------------------------------------------------------------------------- */
+int spec_fork_pages(int b, int page_size, const int32_t* parents, const int32_t* children, const int32_t* fork_lens,
+                    int32_t* share_counts, int64_t num_pages, const int32_t* free_ids, int free_cap,
+                    const int32_t* n_free, int32_t* page_table, int req_rows, int row_pages, int32_t* req_to_token,
+                    int row_w, int32_t* copy_src, int32_t* copy_dst, int32_t* n_copies, int32_t* n_left, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* spec_copy_pages -- page src_ids[i] of every layer's K and V copied to page
+ * dst_ids[i], i < n_copies[0] <= max_copies (a device count; more sets
+ * SPEC_DEV_LENGTH and is clamped).  page_bytes: of one page of one layer's K, a
+ * multiple of 16: page_size * Hkv * D * 2 of the bf16 pools, Hkv * page_size * D of
+ * the 8-bit cache, whose scales, scale_bytes = Hkv a page, are copied too
+ * (scale_bytes 0: none; the scale arrays may be NULL).  The layer arrays are HOST
+ * arrays of num_layers (<= 128) device pointers.  The targets are distinct and
+ * none is a source of the call.  A bad id skips its pair and sets SPEC_DEV_INDEX.
+ * Workspace: the error word only. */
+int spec_copy_pages(int num_layers, int64_t page_bytes, int scale_bytes, void* const* k_layers, void* const* v_layers,
+                    uint8_t* const* k_scales, uint8_t* const* v_scales, int64_t num_pages, const int32_t* src_ids,
+                    const int32_t* dst_ids, int max_copies, const int32_t* n_copies, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/* spec_release_pages -- request r of seq_lens[r] tokens gives up its pages
+ * [ceil(keep_lens[r] / page_size), ceil(seq_lens[r] / page_size)); keep_lens NULL:
+ * all of them.  A page given up m times in the call has its share count lowered by
+ * m, and goes back to the free list where that was less than m: the freed pages,
+ * in the order in which they are first given up (request order, then page order),
+ * are pushed last one first, so that what one spec_alloc_slots or spec_fork_pages
+ * took goes back to where it was.  free_ids is changed behind its n_free[0] entries;
+ * n_left [1] = the new count (may be n_free itself).  Table rows keep their
+ * entries.  A bad length or row leaves its request out (SPEC_DEV_LENGTH /
+ * SPEC_DEV_INDEX), a bad page id its page; a page given up more often than it is
+ * held is freed once and sets SPEC_DEV_INVARIANT.  Pages that do not fit into
+ * free_cap set SPEC_DEV_SPACE, and the call does nothing. */
+int spec_release_pages(int b, int page_size, const int32_t* req_pool_idx, const int32_t* seq_lens,
+                       const int32_t* keep_lens, int32_t* share_counts, int64_t num_pages, int32_t* free_ids,
+                       int free_cap, const int32_t* n_free, const int32_t* page_table, int req_rows, int row_pages,
+                       int32_t* n_left, void* ws, size_t ws_bytes, void* stream);
+
+/* spec_compact_pages -- the pages in use move to the ids below `limit` (raised to
+ * their number; 0: as low as they go), so that the pool's upper part is free.  In
+ * use is every page that is not one of free_ids' n_free[0].  Ascending, the i-th
+ * page in use at or above the limit becomes the i-th free one below it:
+ * (move_src[i], move_dst[i]), i < n_moves[0], pairs for spec_copy_pages (arrays of
+ * free_cap).  The new tables name the new pages: entries [0, ceil(seq_lens[r] /
+ * page_size)) of the rows req_pool_idx[r] and, where req_to_token is given, slots
+ * [0, seq_lens[r]); every request that holds a page has to be listed.
+ * new_share_counts [num_pages] follow the pages.  new_free_ids: the n_left[0] free
+ * pages, highest first, so that the lowest are handed out first and a pool cut to
+ * N pages drops the first num_pages - N of them.
+ * Each output may be its input (n_left may be n_free).  Where the tables are arrays of their own, the old
+ * ones stay readable, and so do the moved pages until their ids are handed out.
+ * A bad id on the free list is passed over (SPEC_DEV_INDEX), one listed twice
+ * counts once (SPEC_DEV_INVARIANT), as does a table entry that is on it; a bad table
+ * entry becomes -1 (SPEC_DEV_INDEX); a bad length or row leaves its row out.  n_free
+ * outside [0, free_cap] sets SPEC_DEV_SPACE, and the call does nothing (n_moves 0).
+ * Two launches. */
+int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const int32_t* seq_lens, int64_t limit,
+                       const int32_t* share_counts, int64_t num_pages, const int32_t* free_ids, int free_cap,
+                       const int32_t* n_free, const int32_t* page_table, int req_rows, int row_pages,
+                       const int32_t* req_to_token, int row_w, int32_t* new_share_counts, int32_t* new_free_ids,
+                       int32_t* n_left, int32_t* new_page_table, int32_t* new_req_to_token, int32_t* move_src,
+                       int32_t* move_dst, int32_t* n_moves, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * spec_token_logprobs -- log probabilities of given tokens, entropy and the k
