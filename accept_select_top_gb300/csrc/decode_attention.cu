@@ -1,0 +1,699 @@
+// decode_attention.cu -- attention of one new token a request over the paged bf16
+// cache.  Requests of a group share the pages of their first tokens.
+//
+// For request r and q head h: x_j = scale q . k_j over its tokens, out = sum_j
+// 2^(x_j log2e - m) v_j / l with a running reference m and sum l.  The sums over
+// the shared tokens and over a request's own ones are independent until the end,
+// so a group's shared tokens are read once for all its rows.
+//
+// Bound: the cache's bytes.  A segment is a group's shared tokens (rows: every member's q heads of a kv head) or a
+// request's own tokens; a unit is (segment, kv head, up to 64 rows).  One CTA a SM takes an equal contiguous
+// range of the 64-key tiles of all units laid end to end.
+//   Four producer warps look up the slots of the keys (two tiles ahead) and copy K and V rows with 16-byte
+// cp.async into a ring of five tiles; they do not care where units end, so the memory stays busy while one does.
+//   Eight consumer warps compute on register fragments (mma.sync m16n8k16; rows are few, and a 128-row tcgen05 tile
+// would be padding): up to 16 rows: four warps share a tile's keys, and the two sets of four take turns at the
+// tiles; 32: two row tiles times four shares of the keys; 64: four times two.  The order of the head
+// dimension inside a fragment is free as long as Q has the same, so K fragments are read as 16-byte words.
+// At a unit's end the warps' results are joined through shared memory.
+//   Units cut by a range boundary, and all of a grouped request, leave fp32 results in the workspace; a second,
+// dependent launch joins them.  No atomics: a call's result is always the same.
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.cuh"
+
+#include "decode_attention.cuh"
+
+namespace spec {
+
+namespace {
+
+constexpr int kConsumers = 8, kProducers = 4;
+constexpr int kDecThreads = 32 * (kConsumers + kProducers);
+constexpr int kRing = 5;
+constexpr int kEndTicks = 1;  // what a unit's end costs in the division of the work, in tiles
+constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wait
+
+template <int D>
+struct DecSmem {
+  static constexpr int kRow = 2 * D;               // bytes of a K (or V) row
+  static constexpr int kHalf = kDecTile * kRow;    // K of a tile
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kMerge = kRing * kStage;    // [warp][8 column tiles][32 lanes] float4
+  static constexpr int kMl = kMerge + kConsumers * 8 * 32 * 16;  // [warp][16] (m, l)
+  static constexpr int kMask = kMl + kConsumers * 16 * 8;        // [stage][4] keys that count, 16 bits each
+  static constexpr int kBars = kMask + kRing * 4 * 4;            // full[5], empty[5]
+  static constexpr int kAbort = kBars + 2 * kRing * 8;
+  static constexpr int kScan = kAbort + 16;        // pre [groups + b + 1], len [b], base [b]
+  static size_t bytes(int b, int groups) { return size_t(kScan) + 4u * size_t(groups + 3 * b + 1); }
+};
+static_assert(DecSmem<128>::kScan + 4 * (4 * kDecodeMaxB + 1) + 256 <= 227 * 1024, "shared memory of one CTA");
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// counts as an arrival once the thread's copies so far have landed
+__device__ __forceinline__ void mbar_arrive_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+// Bounded wait for the phase of the given parity: false once kWaitCycles have passed or another warp has given up.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try(bar, parity)) return true;
+  const long long start = clock64();
+  do {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try(bar, parity)) return true;
+  } while (!*abort_flag && clock64() - start <= kWaitCycles);
+  return false;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a) : "memory");
+  return x;
+}
+// four 8x8 matrices of 16-bit values, transposed
+__device__ __forceinline__ uint4 ldsm_t(uint32_t a) {
+  uint4 x;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(a)
+               : "memory");
+  return x;
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory"); }
+
+// A unit of the tick space.  Segments: the groups' shared tokens, then the requests' own.
+struct Unit {
+  int seg, j;        // segment, (kv head, row tile)
+  int tiles, J;      // of the unit; units of the segment
+  int first, last;   // keys [first, last) of the table row that count
+  int rows, r0;      // query rows of the segment; its first request
+};
+
+template <int D>
+__global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const __grid_constant__ DecodeArgs args) {
+  using L = DecSmem<D>;
+  constexpr unsigned FULL = 0xffffffffu;
+  constexpr int NT = D / 8;
+  const DecodeParams& a = args.p;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int ng = a.num_groups, G = a.Hq / a.Hkv;
+  int* pre = reinterpret_cast<int*>(smem + L::kScan);
+  int* slen = pre + ng + a.b + 1;
+  int* sbase = slen + a.b;
+  int* sgroup = reinterpret_cast<int*>(smem);  // (the ring is not in use yet)
+  __shared__ int wsum[kDecThreads / 32];
+  __shared__ int s_bad;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const uint32_t full = smem_u32(smem + L::kBars), empty = full + 8 * kRing;
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(full + 8 * i, kProducers * 33);
+      mbar_init(empty + 8 * i, kConsumers);
+    }
+    *abort_flag = 0;
+    s_bad = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- segments ----
+  const bool report = blockIdx.x == 0;
+  const long long room = (long long)a.row_pages << args.shift;
+  const int most = room < a.max_seq_len ? int(room) : a.max_seq_len;
+  for (int g = tid; g <= ng && ng > 0; g += kDecThreads) sgroup[g] = a.group_start[g];
+  for (int r = tid; r < a.b; r += kDecThreads) {
+    int len = a.seq_lens[r];
+    const int row = a.req_pool_idx[r];
+    if (len < 0 || len > most) {
+      if (report) raise_error(a.error, SPEC_DEV_LENGTH);
+      len = len < 0 ? 0 : most;
+    }
+    if (row < 0 || row >= a.req_rows) {
+      if (report) raise_error(a.error, SPEC_DEV_INDEX);
+      len = 0;
+    }
+    slen[r] = len;
+  }
+  __syncthreads();
+  // groups that overlap or lie outside the batch: nothing is shared
+  for (int g = tid; g < ng; g += kDecThreads)
+    if (sgroup[g] < 0 || sgroup[g] > sgroup[g + 1] || sgroup[g + 1] > a.b) s_bad = 1;
+  __syncthreads();
+  const bool grouped = ng > 0 && !s_bad;
+  if (report && tid == 0 && ng > 0 && s_bad) raise_error(a.error, SPEC_DEV_INDEX);
+  for (int r = tid; r < a.b; r += kDecThreads) {
+    int base = 0, g = -1;
+    if (grouped && r >= sgroup[0] && r < sgroup[ng]) {
+      int lo = 0, hi = ng;  // the last group that begins at or before r (empty ones are passed over)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sgroup[mid] <= r) lo = mid;
+        else hi = mid;
+      }
+      g = lo;
+      const int shared = a.shared_lens[g];
+      if (report && r == sgroup[g] && (shared < 0 || shared > most)) raise_error(a.error, SPEC_DEV_LENGTH);
+      if (shared > 0 && slen[sgroup[g]] >= shared && slen[r] >= shared) base = shared;
+    }
+    sbase[r] = base;
+    if (report) {
+      args.base[r] = base;
+      args.member[r] = make_int2(g, g < 0 ? 0 : r - sgroup[g]);
+    }
+  }
+  __syncthreads();
+  auto ticks_of = [&](int s) {
+    if (s < ng) {
+      const int first = grouped ? sgroup[s] : 0, rows = grouped ? (sgroup[s + 1] - first) * G : 0;
+      const int tiles = rows ? (sbase[first] + kDecTile - 1) / kDecTile : 0;
+      return tiles ? a.Hkv * ((rows + kDecRows - 1) / kDecRows) * (tiles + kEndTicks) : 0;
+    }
+    const int r = s - ng, n = (slen[r] + kDecTile - 1) / kDecTile - sbase[r] / kDecTile;
+    return a.Hkv * args.own_tiles * ((n < 1 ? 1 : n) + kEndTicks);
+  };
+  {
+    const int segs = ng + a.b;
+    int run = 0;
+    for (int s0 = 0; s0 < segs; s0 += kDecThreads) {
+      const int s = s0 + tid, t = s < segs ? ticks_of(s) : 0;
+      int incl = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(FULL, incl, o);
+        if (lane >= o) incl += y;
+      }
+      __syncthreads();
+      if (lane == 31) wsum[w] = incl;
+      __syncthreads();
+      int before = run;
+      for (int q = 0; q < kDecThreads / 32; ++q) {
+        if (q < w) before += wsum[q];
+        run += wsum[q];
+      }
+      if (s < segs) pre[s] = before + incl - t;
+    }
+    if (tid == 0) pre[segs] = run;
+    __syncthreads();
+    if (report)
+      for (int s = tid; s <= segs; s += kDecThreads) args.pre[s] = pre[s];
+  }
+  const int T = pre[ng + a.b];  // (the host keeps it below 2^31)
+  const int ctas = T < int(gridDim.x) ? T : int(gridDim.x);
+  if (report && tid == 0) *args.plan = make_int4(T, ctas, ng, 0);
+  if (int(blockIdx.x) >= ctas) return;
+  const int S = int((long long)blockIdx.x * T / ctas), E = int((long long)(blockIdx.x + 1) * T / ctas);
+
+  auto open = [&](Unit& u, int seg) {  // the first segment from `seg` on that has ticks
+    while (pre[seg + 1] == pre[seg]) ++seg;
+    u.seg = seg;
+    const int n = pre[seg + 1] - pre[seg];
+    if (seg < ng) {
+      u.r0 = __ldg(a.group_start + seg);
+      u.rows = (__ldg(a.group_start + seg + 1) - u.r0) * G;
+      u.first = 0;
+      u.last = sbase[u.r0];
+      u.J = a.Hkv * ((u.rows + kDecRows - 1) / kDecRows);
+    } else {
+      u.r0 = seg - ng;
+      u.rows = G;
+      u.first = sbase[u.r0];
+      u.last = slen[u.r0];
+      u.J = a.Hkv * args.own_tiles;
+    }
+    u.tiles = n / u.J - kEndTicks;
+  };
+  // tick f of the range: its unit and the tile in it (from `tiles` on: the end's ticks)
+  auto locate = [&](int f, Unit& u, int& t) {
+    int lo = 0, hi = ng + a.b;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= f) lo = mid;
+      else hi = mid;
+    }
+    open(u, lo);
+    const int rem = f - pre[u.seg];
+    u.j = rem / (u.tiles + kEndTicks);
+    t = rem - u.j * (u.tiles + kEndTicks);
+  };
+  auto next_unit = [&](Unit& u) {
+    if (++u.j == u.J) {
+      open(u, u.seg + 1);
+      u.j = 0;
+    }
+  };
+  __syncthreads();  // (sgroup is not read any more)
+
+  if (w >= kConsumers) {
+    // ------------------------------------------------------------ producers
+    const int p = w - kConsumers;
+    constexpr int kChunks = D / 8;              // 16-byte chunks of a row
+    constexpr int kKeys = 32 / kChunks;         // rows that a warp's copy spans
+    const int cx = lane % kChunks, ck = lane / kChunks;
+    const size_t slot_bytes = size_t(a.Hkv) * L::kRow;
+    Unit u;
+    int t, f = S;
+    locate(f, u, t);
+    // The next tile of the range, its kv head (-1: none is left); lanes of this half of the warp look up
+    // their key's page id.
+    int x_pos = -1, x_id = -1;
+    auto look = [&](int half) {
+      while (f < E && t >= u.tiles) {  // over a unit's end
+        f += u.tiles + kEndTicks - t;
+        t = 0;
+        if (f < E) next_unit(u);
+      }
+      if (f >= E) return -1;
+      const int row_tiles = u.J / a.Hkv, h = u.j / row_tiles;
+      if ((lane >> 4) == half) {
+        const int x = (u.first / kDecTile + t) * kDecTile + 16 * p + (lane & 15);
+        x_pos = x_id = -1;
+        if (x >= u.first && x < u.last) {
+          x_pos = x;
+          x_id = __ldg(a.page_table + (long long)__ldg(a.req_pool_idx + u.r0) * a.row_pages + (x >> args.shift));
+        }
+      }
+      ++f;
+      ++t;
+      return h;
+    };
+    int stage = 0;
+    uint32_t phase = 1;  // (an empty ring)
+    bool dead = false;
+    int heads[2];
+    heads[0] = look(0);
+    heads[1] = heads[0] >= 0 ? look(1) : -1;
+    while (heads[0] >= 0 && !dead) {
+      const int h0 = heads[0], h1 = heads[1];
+      int slot = -1;
+      if (x_pos >= 0) {
+        if (x_id < 0 || x_id >= a.num_pages) raise_error(a.error, SPEC_DEV_INDEX);
+        else slot = (x_id << args.shift) + (x_pos & ((1 << args.shift) - 1));
+      }
+      const unsigned valid = __ballot_sync(FULL, slot >= 0);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int h = half ? h1 : h0;
+        if (h < 0 || dead) break;
+        if (__any_sync(FULL, !mbar_wait(empty + 8 * stage, phase, abort_flag))) {
+          dead = true;
+          break;
+        }
+        const uint32_t st = smem_u32(smem + stage * L::kStage) + 16 * p * L::kRow;
+#pragma unroll
+        for (int i = 0; i < 16 / kKeys; ++i) {
+          const int key = i * kKeys + ck;
+          const int s = __shfl_sync(FULL, slot, half * 16 + key);
+          const uint32_t n = s >= 0 ? 16u : 0u;  // (a key that does not count reads as zeros)
+          const size_t at = size_t(s >= 0 ? s : 0) * slot_bytes + size_t(h) * L::kRow + cx * 16;
+          cp16(st + key * L::kRow + (cx ^ (4 * (key & 1))) * 16, static_cast<const unsigned char*>(a.k_pool) + at, n);
+          cp16(st + L::kHalf + key * L::kRow + (cx ^ (key & 7)) * 16, static_cast<const unsigned char*>(a.v_pool) + at, n);
+        }
+        if (lane == 0) {
+          reinterpret_cast<volatile uint32_t*>(smem + L::kMask)[stage * 4 + p] = (valid >> (16 * half)) & 0xffffu;
+          mbar_arrive(full + 8 * stage);
+        }
+        mbar_arrive_copies(full + 8 * stage);
+        if (++stage == kRing) {
+          stage = 0;
+          phase ^= 1;
+        }
+        if (half == 0) heads[0] = look(0);
+      }
+      // (the other half's next tile follows, once both of this window have been copied)
+      heads[1] = !dead && h1 >= 0 && heads[0] >= 0 ? look(1) : -1;
+    }
+    if (dead && lane == 0) {
+      raise_error(a.error, SPEC_DEV_TIMEOUT);
+      *abort_flag = 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int g = lane >> 2, c = lane & 3;
+  const float xf = a.scale * 1.4426950408889634f;
+  int stage = 0, count = 0;
+  uint32_t phase = 0;
+  bool dead = false;
+  float4* const merge = reinterpret_cast<float4*>(smem + L::kMerge);
+  float2* const mls = reinterpret_cast<float2*>(smem + L::kMl);
+
+  // One unit's part in the range: n tiles; RT row tiles of 16.
+  auto work = [&](auto rt_const, const Unit& u, int t0, int n) {
+    constexpr int RT = decltype(rt_const)::value;
+    constexpr int KS = kConsumers / RT;             // warps that hold a row tile
+    constexpr int BLOCKS = RT == 4 ? 2 : 1;         // 16-key blocks of a tile that a warp takes
+    const int rt = w % RT, share = RT == 1 ? w & 3 : w / RT, set = w >> 2;
+    const int row_tiles = u.J / a.Hkv, h = u.j / row_tiles, row0 = (u.j - h * row_tiles) * kDecRows;
+    uint32_t qf[D / 16][4];
+    float o[NT][4], m[2], l[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int x = row0 + rt * 16 + g + 8 * i;  // row of the segment
+      const bool on = x < u.rows;
+      const int f = on ? x / G : 0;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (size_t(u.r0) + f) * a.q_ld +
+                                                        size_t(h * G + (on ? x - f * G : 0)) * D);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const uint4 y = on ? __ldg(src + 4 * k + c) : make_uint4(0, 0, 0, 0);
+        qf[2 * k][i] = y.x;
+        qf[2 * k][2 + i] = y.y;
+        qf[2 * k + 1][i] = y.z;
+        qf[2 * k + 1][2 + i] = y.w;
+      }
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[q][i] = 0.f;
+
+    for (int i = 0; i < n; ++i) {
+      if (!dead && __any_sync(FULL, !mbar_wait(full + 8 * stage, phase, abort_flag))) {
+        dead = true;
+        if (lane == 0) {
+          raise_error(a.error, SPEC_DEV_TIMEOUT);
+          *abort_flag = 1;
+        }
+      }
+      if (!dead && (RT > 1 || (count & 1) == set)) {
+        const uint32_t st = smem_u32(smem + stage * L::kStage);
+#pragma unroll
+        for (int blk = 0; blk < BLOCKS; ++blk) {
+          const int part = share * BLOCKS + blk;  // 16 keys of the tile
+          const uint32_t mask = reinterpret_cast<volatile uint32_t*>(smem + L::kMask)[stage * 4 + part];
+          if (mask == 0) continue;
+          float s[2][4];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[q][e] = 0.f;
+            const uint32_t row = st + (16 * part + 8 * q + g) * L::kRow;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              const uint4 y = lds16(row + ((4 * k + c) ^ (4 * (g & 1))) * 16);
+              mma_bf16(s[q], qf[2 * k], y.x, y.y);
+              mma_bf16(s[q], qf[2 * k + 1], y.z, y.w);
+            }
+          }
+          auto masked = [&](float (&v)[2][4]) {
+            if (mask != 0xffffu) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (!(mask >> (8 * q + 2 * c + (e & 1)) & 1)) v[q][e] = -INFINITY;
+            }
+          };
+          // y = x - m; a row without a reference has y = inf (NaN where x is -inf)
+          float y[2][4], top = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[q][e] = fmaf(s[q][e], xf, -m[e >> 1]);
+          masked(y);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, y[q][e]);
+          if (__any_sync(FULL, top > kDecBase + kDecLazy || m[0] == -INFINITY || m[1] == -INFINITY)) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[q][e] *= xf;
+            masked(s);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+              mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+              mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+              const float ref = mx - kDecBase;
+              if (ref > m[r] + kDecLazy || m[r] == -INFINITY) {
+                const float fac = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - ref);
+                l[r] *= fac;
+#pragma unroll
+                for (int q = 0; q < NT; ++q) {
+                  o[q][2 * r] *= fac;
+                  o[q][2 * r + 1] *= fac;
+                }
+                m[r] = ref;
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[q][e] = s[q][e] - (m[e >> 1] == -INFINITY ? 0.f : m[e >> 1]);
+          }
+          uint32_t pa[4];
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float p0 = fast_exp2(y[q][2 * r]), p1 = fast_exp2(y[q][2 * r + 1]);
+              l[r] += p0 + p1;
+              pa[2 * q + r] = dec_pack(p0, p1);
+            }
+          const int vkey = 16 * part + (lane & 15);
+          const uint32_t vrow = st + L::kHalf + vkey * L::kRow;
+#pragma unroll
+          for (int q = 0; q < NT / 2; ++q) {
+            const uint4 v = ldsm_t(vrow + (((2 * q + (lane >> 4)) ^ (vkey & 7)) * 16));
+            mma_bf16(o[2 * q], pa, v.x, v.y);
+            mma_bf16(o[2 * q + 1], pa, v.z, v.w);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * stage);
+      ++count;
+      if (++stage == kRing) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+
+    // ---- the warps' results joined ----
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(FULL, l[r], 1);
+      l[r] += __shfl_xor_sync(FULL, l[r], 2);
+      if (c == 0) mls[w * 16 + g + 8 * r] = make_float2(m[r], l[r]);
+    }
+    const bool own = u.seg >= ng, begun = t0 == 0, whole = begun && n == u.tiles;
+    const bool final = own && whole && u.first == 0;
+#pragma unroll
+    for (int half = 0; half < D / 64; ++half) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        merge[(w * 8 + q) * 32 + lane] = make_float4(o[8 * half + q][0], o[8 * half + q][1], o[8 * half + q][2], o[8 * half + q][3]);
+      consumer_sync();
+      for (int x = tid; x < RT * 256; x += 32 * kConsumers) {
+        const int tile = x >> 8, q = (x >> 5) & 7, ln = x & 31, gg = ln >> 2;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = row0 + tile * 16 + gg + 8 * r;  // of the segment
+          if (row >= u.rows) continue;
+          float M = -INFINITY, Ls = 0.f, s0 = 0.f, s1 = 0.f;
+          // (the warps of a row tile; the two sets of RT 1 count as eight)
+#pragma unroll
+          for (int k = 0; k < KS; ++k) M = fmaxf(M, mls[(RT * k + tile) * 16 + gg + 8 * r].x);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const int ww = RT * k + tile;
+            const float2 ml = mls[ww * 16 + gg + 8 * r];
+            const float wt = dec_weight(ml.x, M);
+            const float2 v = reinterpret_cast<const float2*>(merge + (ww * 8 + q) * 32 + ln)[r];
+            Ls = fmaf(wt, ml.y, Ls);
+            s0 = fmaf(wt, v.x, s0);
+            s1 = fmaf(wt, v.y, s1);
+          }
+          const int col = 64 * half + 8 * q + 2 * (ln & 3);
+          const int f = row / G;
+          const size_t orow = (size_t(u.r0) + f) * a.Hq + h * G + (row - f * G);
+          const bool note = half == 0 && q == 0 && (ln & 3) == 0;
+          if (final) {
+            const float inv = dec_inverse(Ls);
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * D + col) = dec_pack(s0 * inv, s1 * inv);
+            if (note && a.lse) a.lse[orow] = dec_lse(M, Ls);
+          } else {
+            const size_t frow = whole ? orow : size_t(2 * blockIdx.x + (begun ? 1 : 0)) * kDecRows + row - row0;
+            float* fo = whole ? (own ? args.own_o : args.shared_o) : args.frag_o;
+            float2* fm = whole ? (own ? args.own_ml : args.shared_ml) : args.frag_ml;
+            *reinterpret_cast<float2*>(fo + frow * D + col) = make_float2(s0, s1);
+            if (note) fm[frow] = make_float2(M, Ls);
+          }
+        }
+      }
+      consumer_sync();
+    }
+  };
+
+  Unit u;
+  int t, f = S;
+  locate(f, u, t);
+  while (f < E) {
+    const int n = min(u.tiles - t, E - f);
+    if (n > 0) {
+      const int row_tiles = u.J / a.Hkv, left = u.rows - (u.j % row_tiles) * kDecRows;
+      if (left <= 16) work(std::integral_constant<int, 1>{}, u, t, n);
+      else if (left <= 32) work(std::integral_constant<int, 2>{}, u, t, n);
+      else work(std::integral_constant<int, 4>{}, u, t, n);
+    }
+    f += u.tiles + kEndTicks - t;
+    t = 0;
+    if (f < E) next_unit(u);
+  }
+}
+
+// Joins what the first kernel left: a warp an output row.
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __grid_constant__ DecodeArgs args) {
+  pdl_wait();
+  pdl_trigger();
+  const DecodeParams& a = args.p;
+  constexpr int E = D / 32;  // elements a lane
+  const int lane = threadIdx.x & 31, orow = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (orow >= a.b * a.Hq) return;
+  const int r = orow / a.Hq, head = orow - r * a.Hq, G = a.Hq / a.Hkv, h = head / G, i = head - h * G;
+  const int4 plan = __ldcg(args.plan);
+  const int base = __ldcg(args.base + r);
+  const long long T = plan.x, ctas = plan.y;
+  auto cta_of = [&](int f) { return int(((long long)(f + 1) * ctas - 1) / T); };
+  float M = -INFINITY, Ls = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  auto add = [&](const float* o, const float2* ml, size_t row) {
+    const float2 x = __ldcg(ml + row);
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = __ldcg(o + row * D + 32 * e + lane);
+    const float M2 = fmaxf(M, x.x), wa = dec_weight(M, M2), wb = dec_weight(x.x, M2);
+    Ls = Ls * wa + x.y * wb;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * wa + v[e] * wb;
+    M = M2;
+  };
+  // the CTAs on the unit of row x of segment `seg`; false where one CTA holds it whole
+  auto parts = [&](int seg, int row_tiles, int x, int& wa, int& wb) {
+    const int p0 = __ldcg(args.pre + seg), n = (__ldcg(args.pre + seg + 1) - p0) / (a.Hkv * row_tiles);
+    const int u0 = p0 + (h * row_tiles + x / kDecRows) * n;
+    wa = cta_of(u0);
+    wb = cta_of(u0 + n - kEndTicks - 1);
+    return wa != wb;
+  };
+  auto add_parts = [&](int wa, int wb, int x) {
+    for (int q = wa; q <= wb; ++q) add(args.frag_o, args.frag_ml, size_t(2 * q + (q == wa ? 1 : 0)) * kDecRows + x % kDecRows);
+  };
+  int wa, wb;
+  const bool cut = parts(plan.z + r, args.own_tiles, i, wa, wb);
+  if (!cut && base == 0) return;  // (already in out)
+  if (cut) add_parts(wa, wb, i);
+  else add(args.own_o, args.own_ml, orow);
+  if (base > 0) {
+    const int2 mem = __ldcg(args.member + r);
+    const int rows = (__ldg(a.group_start + mem.x + 1) - (r - mem.y)) * G, x = mem.y * G + i;
+    if (parts(mem.x, (rows + kDecRows - 1) / kDecRows, x, wa, wb)) add_parts(wa, wb, x);
+    else add(args.shared_o, args.shared_ml, orow);
+  }
+  const float inv = dec_inverse(Ls);
+  uint16_t* out = static_cast<uint16_t*>(a.out) + size_t(orow) * D;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[32 * e + lane] = uint16_t(dec_pack(acc[e] * inv, 0.f));
+  if (lane == 0 && a.lse) a.lse[orow] = dec_lse(M, Ls);
+}
+
+template <int D>
+int launch_decode(const DecodeArgs& args, int sms, cudaStream_t stream) {
+  const DecodeParams& p = args.p;
+  const size_t smem = DecSmem<D>::bytes(p.b, p.num_groups);
+  if (cudaFuncSetAttribute(decode_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           int(DecSmem<D>::bytes(kDecodeMaxB, kDecodeMaxB))) != cudaSuccess)  // (the most, so that calls of two threads agree)
+    return SPEC_ERR_LAUNCH;
+  const int grid = sms < kDecMaxCtas ? sms : kDecMaxCtas;
+  if (launch_pdl(decode_attention_kernel<D>, dim3(grid), dim3(kDecThreads), smem, stream, args) != cudaSuccess) return SPEC_ERR_LAUNCH;
+  const unsigned blocks = unsigned((size_t(p.b) * p.Hq + kJoinWarps - 1) / kJoinWarps);
+  return launch_pdl(decode_join_kernel<D>, dim3(blocks), dim3(32 * kJoinWarps), 0, stream, args) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+}
+
+// Offsets of the workspace's parts.
+struct DecodeLayout {
+  size_t pre, base, member, frag_ml, own_ml, shared_ml, frag_o, own_o, shared_o, bytes;
+  DecodeLayout(int b, int Hq, int D) {
+    const size_t rows = size_t(b) * Hq, frags = size_t(2) * kDecMaxCtas * kDecRows;
+    size_t at = 256;
+    auto take = [&](size_t n) {
+      const size_t x = at;
+      at += align256(n);
+      return x;
+    };
+    pre = take(size_t(2 * b + 1) * 4);
+    base = take(size_t(b) * 4);
+    member = take(size_t(b) * 8);
+    frag_ml = take(frags * 8);
+    own_ml = take(rows * 8);
+    shared_ml = take(rows * 8);
+    frag_o = take(frags * D * 4);
+    own_o = take(rows * D * 4);
+    shared_o = take(rows * D * 4);
+    bytes = at;
+  }
+};
+
+}  // namespace
+
+size_t decode_partial_bytes(int b, int Hq) { return DecodeLayout(b, Hq, 128).bytes; }
+
+int launch_decode_attention(const DecodeParams& p, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return SPEC_ERR_LAUNCH;
+  const DecodeLayout at(p.b, p.Hq, p.D);
+  unsigned char* ws = p.partials;
+  DecodeArgs args{};
+  args.p = p;
+  for (args.shift = 0; (1 << args.shift) < p.page_size; ++args.shift) {
+  }
+  args.own_tiles = (p.Hq / p.Hkv + kDecRows - 1) / kDecRows;
+  args.plan = reinterpret_cast<int4*>(ws);
+  args.pre = reinterpret_cast<int*>(ws + at.pre);
+  args.base = reinterpret_cast<int*>(ws + at.base);
+  args.member = reinterpret_cast<int2*>(ws + at.member);
+  args.frag_ml = reinterpret_cast<float2*>(ws + at.frag_ml);
+  args.own_ml = reinterpret_cast<float2*>(ws + at.own_ml);
+  args.shared_ml = reinterpret_cast<float2*>(ws + at.shared_ml);
+  args.frag_o = reinterpret_cast<float*>(ws + at.frag_o);
+  args.own_o = reinterpret_cast<float*>(ws + at.own_o);
+  args.shared_o = reinterpret_cast<float*>(ws + at.shared_o);
+  return p.D == 128 ? launch_decode<128>(args, sms, stream) : launch_decode<64>(args, sms, stream);
+}
+
+}  // namespace spec

@@ -1,0 +1,49 @@
+// decode_attention.cuh -- what the kernels of the one-token attention over shared pages have in common.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace spec {
+
+constexpr int kDecTile = 64;    // keys of a tile
+constexpr int kDecRows = 64;    // query rows of a unit
+constexpr int kDecMaxCtas = 192;  // upper bound of a grid of one CTA a SM; sizes the fragment slots
+
+// P at a row's maximum when its reference is set, and how far the maximum may grow before it is set again: P stays below
+// 2^-24, so the sums of any number of values that 32 bits count stay below the largest of them.  (What that costs:
+// products below 2^-126, of values below 2^-94.)
+constexpr float kDecBase = -32.f, kDecLazy = 8.f;
+
+__device__ __forceinline__ uint32_t dec_pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// the weight of a partial result of reference m in one of reference M (an empty one has m = -inf)
+__device__ __forceinline__ float dec_weight(float m, float M) { return m == -INFINITY ? 0.f : exp2f(m - M); }
+__device__ __forceinline__ float dec_inverse(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }
+__device__ __forceinline__ float dec_lse(float m, float l) {
+  return l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+// The workspace of a call.  plan: {ticks, CTAs, groups, -} and, for the joining kernel, what the first CTA of the main
+// kernel found: ticks before each segment, each request's shared length, its group and place in it.
+struct DecodeArgs {
+  DecodeParams p;
+  int shift;       // log2(page_size)
+  int own_tiles;   // 64-row tiles of a kv head's rows of one request
+  int4* plan;
+  int* pre;        // [groups + b + 1]
+  int* base;       // [b]
+  int2* member;    // [b]
+  float2* frag_ml;  // [2 * CTA + i][64], i = 1: the unit that the CTA begins and does not finish
+  float2* own_ml;   // [b * Hq] of units that lie in one CTA
+  float2* shared_ml;
+  float* frag_o;    // [.][D]
+  float* own_o;
+  float* shared_o;
+};
+
+}  // namespace spec

@@ -499,4 +499,31 @@ struct CopyParams {
 };
 int launch_copy_pages(const CopyParams& p, int sms, cudaStream_t stream);
 
+// Attention of one new token a request over the bf16 pools, groups of requests sharing their first tokens.
+struct DecodeParams {
+  int b, Hq, Hkv, D, page_size;
+  const void* q;
+  long long q_ld;
+  const void* k_pool;
+  const void* v_pool;
+  long long num_pages;
+  const int32_t* page_table;
+  int req_rows, row_pages;
+  const int32_t* req_pool_idx;
+  const int32_t* seq_lens;
+  int max_seq_len;
+  int num_groups;
+  const int32_t* group_start;  // [num_groups + 1]
+  const int32_t* shared_lens;  // [num_groups]
+  float scale;
+  void* out;
+  float* lse;
+  uint32_t* error;
+  unsigned char* partials;
+};
+// the kernel keeps the tiles before each segment in shared memory
+constexpr int kDecodeMaxB = 2048;
+int launch_decode_attention(const DecodeParams& p, cudaStream_t stream);
+size_t decode_partial_bytes(int b, int Hq);
+
 }  // namespace spec

@@ -111,6 +111,8 @@ size_t partial_bytes(int op, int b, int n, int k, int V, int Hq, int Hkv, int ma
       return release_partial_bytes(V);
     case SPEC_OP_COMPACT_PAGES:
       return compact_partial_bytes(V);
+    case SPEC_OP_DECODE_ATTENTION:
+      return decode_partial_bytes(b, Hq);
     default:
       return 0;
   }
@@ -441,7 +443,7 @@ size_t spec_workspace_size(int op, int b, int n, int k, int V, int Hq, int Hkv, 
   if (b == 0) return kHeaderBytes + counters_bytes(0);
   const bool logprobs = op == SPEC_OP_TOKEN_LOGPROBS;
   if (n < 1 || n > (logprobs ? kMaxN + 1 : kMaxN) || k < 1 || k > (logprobs ? kLogprobMaxK : kMaxK) || V < 1) return 0;
-  if ((op == SPEC_OP_VERIFY_ATTENTION || op == SPEC_OP_VERIFY_ATTENTION_Q8) && (Hq < 1 || Hkv < 1 || Hq % Hkv || max_seq_len < 0)) return 0;
+  if ((op == SPEC_OP_VERIFY_ATTENTION || op == SPEC_OP_VERIFY_ATTENTION_Q8 || op == SPEC_OP_DECODE_ATTENTION) && (Hq < 1 || Hkv < 1 || Hq % Hkv || max_seq_len < 0)) return 0;
   return partials_offset(b) + partial_bytes(op, b, n, k, V, Hq, Hkv, max_seq_len);
 }
 
@@ -1199,6 +1201,60 @@ int spec_copy_pages(int num_layers, int64_t page_bytes, int scale_bytes, void* c
   p.n_copies = n_copies;
   p.error = ws_view(ws, 1).error;
   return launch_copy_pages(p, device_sms(), as_stream(stream));
+}
+
+int spec_decode_attention(int b, int Hq, int Hkv, int D, int page_size, const void* q, int64_t q_ld,
+                          const void* k_pool, const void* v_pool, int64_t num_slots, const int32_t* page_table,
+                          int req_rows, int row_pages, const int32_t* req_pool_idx, const int32_t* seq_lens,
+                          int max_seq_len, int num_groups, const int32_t* group_start, const int32_t* shared_lens,
+                          float scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (b < 0 || b > kDecodeMaxB || Hq < 1 || Hkv < 1 || Hq % Hkv || max_seq_len < 0 || num_groups < 0 || num_groups > b)
+    return SPEC_ERR_ARG;
+  if ((D != 64 && D != 128) || page_size < 1 || page_size > 128 || (page_size & (page_size - 1))) return SPEC_ERR_UNSUPPORTED;
+  if (q_ld < int64_t(Hq) * D || q_ld % 8 || num_slots < page_size || num_slots >= (int64_t(1) << 31) || req_rows < 1 ||
+      row_pages < 1 || int64_t(row_pages) * page_size >= (int64_t(1) << 31))
+    return SPEC_ERR_ARG;
+  // tiles (an end's ticks among them) of the requests' own tokens and of the shared ones
+  const int64_t G = Hq / Hkv, most = int64_t(max_seq_len) / 64 + 3, row_tiles = (G + 63) / 64;
+  if (int64_t(b) * Hkv >= (int64_t(1) << 31) / row_tiles / most / 2 ||
+      (num_groups && (b * G / 64 + num_groups) * Hkv >= (int64_t(1) << 31) / most / 2) || int64_t(b) * Hq >= (int64_t(1) << 31))
+    return SPEC_ERR_ARG;
+  if (b == 0) return SPEC_OK;
+  if (!q || !k_pool || !v_pool || !page_table || !req_pool_idx || !seq_lens || !out ||
+      (num_groups && (!group_start || !shared_lens)))
+    return SPEC_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16)) return SPEC_ERR_ARG;
+  // (a request's results are written while another's q is still read)
+  if (overlap(q, (size_t(b - 1) * q_ld + size_t(Hq) * D) * 2, out, size_t(b) * Hq * D * 2)) return SPEC_ERR_ARG;
+  if (int rc = check_ws(ws, ws_bytes, spec_workspace_size(SPEC_OP_DECODE_ATTENTION, b, 1, 1, 1, Hq, Hkv, max_seq_len))) return rc;
+  note_other(ws);
+  const WsView v = ws_view(ws, b);
+  DecodeParams p{};
+  p.b = b;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.page_size = page_size;
+  p.q = q;
+  p.q_ld = q_ld;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.num_pages = num_slots / page_size;
+  p.page_table = page_table;
+  p.req_rows = req_rows;
+  p.row_pages = row_pages;
+  p.req_pool_idx = req_pool_idx;
+  p.seq_lens = seq_lens;
+  p.max_seq_len = max_seq_len;
+  p.num_groups = num_groups;
+  p.group_start = group_start;
+  p.shared_lens = shared_lens;
+  p.scale = scale;
+  p.out = out;
+  p.lse = lse;
+  p.error = v.error;
+  p.partials = v.partials;
+  return launch_decode_attention(p, as_stream(stream));
 }
 
 }  // extern "C"

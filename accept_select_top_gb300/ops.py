@@ -22,7 +22,7 @@ SPEC_OK = 0
 SPEC_F32, SPEC_BF16 = 0, 1
 (OP_SELECT_TOPK, OP_BUILD_TREE, OP_VERIFY_ATTENTION, OP_VERIFY_GREEDY, OP_VERIFY_SAMPLING, OP_COMMIT_KV,
  OP_VERIFY_TARGET_ONLY, OP_ALLOC_SLOTS, OP_COMMIT_KV_Q8, OP_VERIFY_ATTENTION_Q8, OP_TOKEN_LOGPROBS,
- OP_FORK_PAGES, OP_COPY_PAGES, OP_RELEASE_PAGES, OP_COMPACT_PAGES) = range(15)
+ OP_FORK_PAGES, OP_COPY_PAGES, OP_RELEASE_PAGES, OP_COMPACT_PAGES, OP_DECODE_ATTENTION) = range(16)
 DEV_INDEX, DEV_INVARIANT, DEV_LENGTH, DEV_TIMEOUT, DEV_SPACE = 1, 2, 4, 8, 16
 Q8_EXP_MIN = 16  # smallest scale exponent byte the library writes (the scale is 2^(e - 127))
 _ERRORS = {-1: "bad argument", -2: "workspace too small or misaligned", -3: "CUDA launch failed",
@@ -35,7 +35,7 @@ EXPORTS = ["spec_workspace_size", "spec_workspace_init", "spec_workspace_set_ove
            "spec_build_full_mask", "spec_add_penalties", "spec_renorm_probs", "spec_verify_sampling_probs",
            "spec_verify_target_only_probs", "spec_commit_kv", "spec_alloc_slots", "spec_commit_kv_q8",
            "spec_verify_attention_q8", "spec_fork_pages", "spec_copy_pages", "spec_release_pages",
-           "spec_compact_pages", "spec_token_logprobs", "spec_verify_greedy_noalloc",
+           "spec_compact_pages", "spec_decode_attention", "spec_token_logprobs", "spec_verify_greedy_noalloc",
            "spec_noalloc_last_error"]
 
 
@@ -78,6 +78,7 @@ def _load() -> ctypes.CDLL:
         "spec_copy_pages": (I, [I, L, I, P, P, P, P, L, P, P, I, P, P, Z, P]),
         "spec_release_pages": (I, [I, I, P, P, P, P, L, P, I, P, P, I, I, P, P, Z, P]),
         "spec_compact_pages": (I, [I, I, P, P, L, P, L, P, I, P, P, I, I, P, I, P, P, P, P, P, P, P, P, P, Z, P]),
+        "spec_decode_attention": (I, [I, I, I, I, I, P, L, P, P, L, P, I, I, P, P, I, I, P, P, F, P, P, P, Z, P]),
         "spec_token_logprobs": (I, [I, I, I, I, I, P, P, P, P, I, P, P, P, P, P, Z, P]),
         "spec_verify_greedy_noalloc": (I, [I, I, I, I, I, P, P, P, P, P, P, P, P, P, P, P]),
         "spec_noalloc_last_error": (I, [P]),
@@ -621,6 +622,30 @@ def spec_compact_pages(b: int, page_size: int, req_pool_idx, seq_lens, limit: in
         _in(move_src, _I32, cap, dev, "move_src"), _in(move_dst, _I32, cap, dev, "move_dst"),
         _in(n_moves, _I32, 1, dev, "n_moves"), _workspace_in(ws, dev), ws.nbytes, _raw_stream(stream, dev)),
         "spec_compact_pages")
+
+
+def spec_decode_attention(b: int, Hq: int, Hkv: int, D: int, page_size: int, q, k_pool, v_pool, page_table,
+                          req_pool_idx, seq_lens, max_seq_len: int, group_start, shared_lens, scale: float, out, lse,
+                          ws: Workspace, stream=None):
+    """Attention of one new token a request over the bf16 pools [num_slots, Hkv, D]; q ([b, Hq, D]) may be a view of a
+    packed projection.  group_start [groups + 1] and shared_lens [groups]: requests whose first tokens lie in the same
+    pages (both None: no groups).  lse may be None."""
+    dev = _device()
+    qp, q_ld = _rows_in(q, Hq, D, b, dev, "q")
+    if k_pool.shape != v_pool.shape or k_pool.dim() != 3 or k_pool.shape[1] != Hkv or k_pool.shape[2] != D:
+        raise SpecError(f"pools: expected [num_slots, {Hkv}, {D}] twice, got {tuple(k_pool.shape)} and {tuple(v_pool.shape)}")
+    if (group_start is None) != (shared_lens is None):
+        raise SpecError("group_start and shared_lens go together")
+    groups = 0 if shared_lens is None else shared_lens.numel()
+    rows, row_pages = page_table.shape
+    _check(LIB.spec_decode_attention(
+        b, Hq, Hkv, D, page_size, qp, q_ld, _in(k_pool, _BF16, 1, dev, "k_pool"), _in(v_pool, _BF16, 1, dev, "v_pool"),
+        k_pool.shape[0], _in(page_table, _I32, 1, dev, "page_table"), rows, row_pages,
+        _in(req_pool_idx, _I32, b, dev, "req_pool_idx"), _in(seq_lens, _I32, b, dev, "seq_lens"), max_seq_len, groups,
+        None if groups == 0 else _in(group_start, _I32, groups + 1, dev, "group_start"),
+        None if groups == 0 else _in(shared_lens, _I32, groups, dev, "shared_lens"), scale,
+        _in(out, _BF16, b * Hq * D, dev, "out"), None if lse is None else _in(lse, _F32, b * Hq, dev, "lse"),
+        _workspace_in(ws, dev), ws.nbytes, _raw_stream(stream, dev)), "spec_decode_attention")
 
 
 def spec_token_logprobs(b: int, n: int, W: int, logits, row_index, tokens, temperatures, k: int, logprobs, entropy,

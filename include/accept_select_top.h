@@ -93,7 +93,8 @@ extern "C" {
 #define SPEC_OP_COPY_PAGES 12
 #define SPEC_OP_RELEASE_PAGES 13 /* V: pages of the pool */
 #define SPEC_OP_COMPACT_PAGES 14 /* V: pages of the pool */
-#define SPEC_OP_LAST SPEC_OP_COMPACT_PAGES
+#define SPEC_OP_DECODE_ATTENTION 15 /* n, k, V: 1 */
+#define SPEC_OP_LAST SPEC_OP_DECODE_ATTENTION
 
 /* Batch sizes up to which calls of different sizes may share a workspace. */
 #define SPEC_WORKSPACE_SHARED_B 4096
@@ -660,6 +661,41 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
                        const int32_t* req_to_token, int row_w, int32_t* new_share_counts, int32_t* new_free_ids,
                        int32_t* n_left, int32_t* new_page_table, int32_t* new_req_to_token, int32_t* move_src,
                        int32_t* move_dst, int32_t* n_moves, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * spec_decode_attention -- attention of one new token a request over the bf16
+ * pools, through page tables.  Requests that share pages (spec_fork_pages) are
+ * told as groups, and what a group shares is read once for all its members.  The
+ * pages have no counterpart.
+ *
+ * q: rows [Hq, D] bf16, q_ld elements apart (a multiple of 8: a view of a packed
+ * projection); k_pool, v_pool: [num_slots, Hkv, D] bf16, a page page_size (a power
+ * of two up to 128; 1: page_table is the slot table) consecutive slots;
+ * page_table: [req_rows, row_pages].  Request r sees its tokens 0 ..
+ * seq_lens[r]-1, the new one's K and V being in the pools already:
+ *   out[r, h] = softmax(scale * q.K^T) V,  lse (nullable) = its natural-log
+ * sum-exp.  out: [b, Hq, D] bf16, lse: [b, Hq] fp32.  A request without a token
+ * gives out 0 and lse -inf.  out does not overlap q (SPEC_ERR_ARG).
+ *   Group g: requests group_start[g] .. group_start[g+1]-1 (ascending, [num_groups
+ * + 1]; requests before the first and behind the last are in none), whose tables
+ * name the same pages for their tokens 0 .. shared_lens[g]-1; these are read
+ * through the first member's row.  A member shorter than that reads all of its
+ * tokens through its own row, and so does every one where the first member is
+ * shorter.  num_groups 0: both arrays may be NULL.  Group bounds that descend or
+ * leave the batch set SPEC_DEV_INDEX, and nothing is shared; a negative shared
+ * length, or one above max_seq_len, sets SPEC_DEV_LENGTH.
+ *   max_seq_len bounds every seq_len (a larger one sets SPEC_DEV_LENGTH and is
+ * clamped).  A page id out of range sets SPEC_DEV_INDEX and its keys do not count;
+ * a bad table row leaves its request without tokens.  What the pools hold behind a
+ * request's last token is not looked at.  A call's results are always the same
+ * bits.  D 64 or 128, b <= 2048, num_groups <= b; the tiles, b * (max_seq_len / 64
+ * + 3) * Hkv * ceil(Hq / Hkv / 64), stay below 2^30.  HBM-bound.
+ * ------------------------------------------------------------------------- */
+int spec_decode_attention(int b, int Hq, int Hkv, int D, int page_size, const void* q, int64_t q_ld,
+                          const void* k_pool, const void* v_pool, int64_t num_slots, const int32_t* page_table,
+                          int req_rows, int row_pages, const int32_t* req_pool_idx, const int32_t* seq_lens,
+                          int max_seq_len, int num_groups, const int32_t* group_start, const int32_t* shared_lens,
+                          float scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * spec_token_logprobs -- log probabilities of given tokens, entropy and the k
