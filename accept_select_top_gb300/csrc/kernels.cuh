@@ -445,9 +445,11 @@ struct ReleaseParams {
   int req_rows, row_pages;
   int32_t* n_left;
   uint32_t* error;
-  int* totals;  // [8]
-  int2* note;   // [num_pages]
+  uint32_t* counters;  // two
+  int* totals;         // a CTA each
+  int2* note;          // [num_pages]
 };
+constexpr size_t kReleaseTotalsBytes = 1024;
 int launch_release_pages(const ReleaseParams& p, cudaStream_t stream);
 size_t release_partial_bytes(long long pages);
 

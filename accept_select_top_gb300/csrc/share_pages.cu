@@ -93,78 +93,150 @@ __global__ void __launch_bounds__(kForkThreads) fork_pages_kernel(ForkParams a) 
 
 // ---------------------------------------------------------------- release
 
-// The occurrences (request, page) of the call, laid end to end, are cut into eight contiguous shares, one a CTA of
-// the cluster.  note[p] = {times given up, first occurrence} is cleared, then filled by atomics; a page is
-// freed where more holders than its count give it up, by its first occurrence.  Freed pages are pushed in
-// descending order of occurrence: what alloc or fork took in one call goes back to where it was.
+// The occurrences (request, page) of the call, laid end to end, are cut into contiguous shares, one a CTA of the
+// cluster, in rows of 1024.  note[p] = {times given up, first occurrence of a page that is freed}: cleared, then
+// counted by atomics; a page is freed where more holders than its count give it up.  (The first occurrence takes
+// atomics only where a page is given up more than once.)  Freed pages are pushed in descending order of
+// occurrence: what alloc or fork took in one call goes back to where it was.
+//   The page ids and what is known of them stay in registers for the first kKept rows of a share.
+//   The CTAs meet four times.  Up to 16 are a cluster (16 of them where the device takes such); a call that may hold
+// more occurrences than their registers is a cooperative launch over all SMs, as a SM's scattered accesses to the
+// notes, one a cycle, are what a large call costs, and its CTAs meet at a counter.  In us, cluster of 16 / all SMs:
+// 133 thousand pages 47 / 20, 328 thousand of 32 holders each 111 / 39 (its atomics meet at the same words);
+// a few hundred pages: cluster of 8 8, all SMs 13.
+constexpr int kKept = 8;
+constexpr int kClusterMost = 16;
+constexpr int kReleaseMostCtas = 192;
+constexpr long long kBarrierCycles = 4000000000ll;  // about 2 s: bound of a wait for the other CTAs
+
+// All CTAs of a cooperative launch; what they wrote before is seen after.  arrivals counts to `ctas` once a meeting.
+// False (in every thread) if they do not come.
+__device__ __forceinline__ bool grid_sync(uint32_t* arrivals, uint32_t until, uint32_t* error) {
+  __shared__ int s_ok;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    bool ok = atom_add_acq_rel(arrivals) + 1 >= until;
+    const long long start = clock64();
+    while (!ok && clock64() - start <= kBarrierCycles) {
+      uint32_t now;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(arrivals) : "memory");
+      ok = now >= until;
+    }
+    if (!ok) raise_error(error, SPEC_DEV_TIMEOUT);
+    s_ok = ok;
+  }
+  __syncthreads();
+  return s_ok;
+}
+
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kClusterThreads) release_pages_kernel(ReleaseParams a) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ int pre[];  // [b + 1]
+  extern __shared__ long long row_at[];  // [b] where the request's first page given up lies in page_table
+  int* pre = reinterpret_cast<int*>(row_at + a.b);  // [b + 1]
   __shared__ int wsum[kClusterThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, me = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, me = blockIdx.x, ctas = gridDim.x;
   const int n_free = *a.n_free;
-  auto first_of = [&](int r) { return a.keep_lens ? pages_of(a.keep_lens[r], a.page_size) : 0; };
+  uint32_t met = 0;
+  auto meet = [&] {
+    if (CLUSTER) {
+      cluster_sync();
+      return true;
+    }
+    return grid_sync(a.counters, ++met * uint32_t(ctas), a.error);
+  };
   const int E = scan_counts<kClusterThreads>(a.b, pre, wsum, [&](int r) {
     const int len = a.seq_lens[r], keep = a.keep_lens ? a.keep_lens[r] : 0, row = a.req_pool_idx[r];
     const bool idx_ok = row >= 0 && row < a.req_rows;
     const bool len_ok = keep >= 0 && keep <= len && len <= (long long)a.row_pages * a.page_size;
     if (me == 0 && !idx_ok) raise_error(a.error, SPEC_DEV_INDEX);
     if (me == 0 && !len_ok) raise_error(a.error, SPEC_DEV_LENGTH);
-    return idx_ok && len_ok ? pages_of(len, a.page_size) - pages_of(keep, a.page_size) : 0;
+    if (!idx_ok || !len_ok) return 0;
+    const int first = pages_of(keep, a.page_size);
+    row_at[r] = (long long)row * a.row_pages + first;
+    return pages_of(len, a.page_size) - first;
   });
-  const int lo = int((long long)E * me / kClusterCtas), hi = int((long long)E * (me + 1) / kClusterCtas);
-  auto page_at = [&](int e) {  // -1 for a bad one
+  const int lo = int((long long)E * me / ctas), hi = int((long long)E * (me + 1) / ctas);
+  const int rows = (hi - lo + kClusterThreads - 1) / kClusterThreads;
+  auto page_at = [&](int e) {  // -1 for a bad one, or none
+    if (e >= hi) return -1;
     const int r = row_of_entry(pre, a.b, e);
-    const int p = a.page_table[(long long)a.req_pool_idx[r] * a.row_pages + first_of(r) + e - pre[r]];
-    return p >= 0 && p < a.num_pages ? p : -1;
+    const int p = __ldg(a.page_table + row_at[r] + (e - pre[r]));
+    if (p >= 0 && p < a.num_pages) return p;
+    raise_error(a.error, SPEC_DEV_INDEX);
+    return -1;
   };
-  for (int e = lo + tid; e < hi; e += kClusterThreads) {
-    const int p = page_at(e);
-    if (p >= 0) a.note[p] = make_int2(0, INT_MAX);
-    else raise_error(a.error, SPEC_DEV_INDEX);
-  }
-  cluster_sync();
-  for (int e = lo + tid; e < hi; e += kClusterThreads) {
-    const int p = page_at(e);
-    if (p >= 0) {
-      atomicAdd(&a.note[p].x, 1);
-      atomicMin(&a.note[p].y, e);
+  int kept[kKept];
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) kept[i] = page_at(lo + i * kClusterThreads + tid);
+  // fn(occurrence, page, row) for the thread's pages
+  auto for_each = [&](auto&& fn) {
+#pragma unroll
+    for (int i = 0; i < kKept; ++i)
+      if (kept[i] >= 0) fn(lo + i * kClusterThreads + tid, kept[i], i);
+    for (int i0 = kKept; i0 < rows; i0 += kKept) {
+      int p[kKept];
+#pragma unroll
+      for (int i = 0; i < kKept; ++i) p[i] = page_at(lo + (i0 + i) * kClusterThreads + tid);
+#pragma unroll
+      for (int i = 0; i < kKept; ++i)
+        if (p[i] >= 0) fn(lo + (i0 + i) * kClusterThreads + tid, p[i], i0 + i);
     }
-  }
-  cluster_sync();
-  // whether occurrence e frees its page; counts are not touched before the list is known to have room
-  auto frees = [&](int e, int& p, int& left) {
-    p = page_at(e);
-    if (p < 0) return false;
-    const int2 n = __ldcg(a.note + p);
-    if (n.y != e) {
-      p = -1;
-      return false;
-    }
-    left = a.share_counts[p] - n.x;
-    return left < 0;
   };
+  for_each([&](int, int p, int) { a.note[p] = make_int2(0, INT_MAX); });
+  if (!meet()) return;
+  for_each([&](int, int p, int) { atomicAdd(&a.note[p].x, 1); });
+  if (!meet()) return;
+  for_each([&](int e, int p, int) {
+    const int times = __ldcg(&a.note[p].x), more = a.share_counts[p];
+    if (times > more) {
+      if (times == 1) a.note[p].y = e;
+      else atomicMin(&a.note[p].y, e);
+      if (times > more + 1) raise_error(a.error, SPEC_DEV_INVARIANT);
+    }
+  });
+  if (!meet()) return;
+  // counts are not touched before the list is known to have room
   int mine = 0;
-  for (int e = lo + tid; e < hi; e += kClusterThreads) {
-    int p, left;
-    mine += frees(e, p, left);
-  }
+  unsigned freed = 0, stays = 0;  // bits: of the kept rows
+  for_each([&](int e, int p, int i) {
+    const int first = __ldcg(&a.note[p].y);
+    mine += first == e;
+    if (i < kKept) {
+      if (first == e) freed |= 1u << i;
+      if (first == INT_MAX) stays |= 1u << i;
+    }
+  });
   mine = __reduce_add_sync(0xffffffffu, mine);
   __syncthreads();
   if (lane == 0) wsum[w] = mine;
   __syncthreads();
-  if (tid == 0) {
-    int sum = 0;
-    for (int q = 0; q < kClusterThreads / 32; ++q) sum += wsum[q];
-    a.totals[me] = sum;
+  if (w == 0) {
+    const int sum = __reduce_add_sync(0xffffffffu, wsum[lane]);
+    if (lane == 0) a.totals[me] = sum;
   }
-  cluster_sync();
-  int total = 0, at = n_free;  // where the next page of this share goes
-  for (int q = 0; q < kClusterCtas; ++q) {
-    const int c = __ldcg(a.totals + q);
-    total += c;
-    if (q > me) at += c;
+  if (!meet()) return;
+  int total = 0, at = n_free;  // `at`: where the next page of this share goes
+  {
+    __syncthreads();
+    int c[kReleaseMostCtas / 32];  // (each warp adds them up by itself)
+    int behind = 0;
+#pragma unroll
+    for (int i = 0; i < kReleaseMostCtas / 32; ++i) {
+      const int q = 32 * i + lane;
+      c[i] = q < ctas ? __ldcg(a.totals + q) : 0;
+      total += c[i];
+      behind += q > me ? c[i] : 0;
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    at += __reduce_add_sync(0xffffffffu, behind);
+    mine = __ldcg(a.totals + me);
+  }
+  // the CTA that leaves last puts the counters back to zero
+  if (!CLUSTER && tid == 0 && atom_add_acq_rel(a.counters + 1) == uint32_t(ctas) - 1) {
+    atomicExch(a.counters, 0u);
+    atomicExch(a.counters + 1, 0u);
   }
   const bool fits = n_free >= 0 && n_free <= a.free_cap && total <= a.free_cap - n_free;
   if (me == 0 && tid == 0) {
@@ -172,25 +244,35 @@ __global__ void __launch_bounds__(kClusterThreads) release_pages_kernel(ReleaseP
     *a.n_left = fits ? n_free + total : n_free;
   }
   if (!fits) return;
-  for (int h = hi; h > lo; h -= kClusterThreads) {
-    const int e = h - 1 - tid;
-    int p = -1, left = 0;
-    const bool go = e >= lo && frees(e, p, left);
-    if (p >= 0) {
-      if (left < -1) raise_error(a.error, SPEC_DEV_INVARIANT);
-      a.share_counts[p] = left < 0 ? 0 : left;
+  for (int i = rows - 1; i >= 0; --i) {
+    const int e = lo + i * kClusterThreads + tid;
+    int p = -1;
+    bool go = false, stay = false;
+    if (i < kKept) {
+#pragma unroll
+      for (int q = 0; q < kKept; ++q)
+        if (q == i) p = kept[q];
+      go = freed >> i & 1;
+      stay = stays >> i & 1;
+    } else {
+      p = page_at(e);
+      if (p >= 0) {
+        const int first = __ldcg(&a.note[p].y);
+        go = first == e;
+        stay = first == INT_MAX;
+      }
     }
+    if (go) a.share_counts[p] = 0;
+    if (stay) atomicSub(a.share_counts + p, 1);
+    if (mine == 0) continue;  // (the CTA frees nothing)
     const unsigned m = __ballot_sync(0xffffffffu, go);
     __syncthreads();
     if (lane == 0) wsum[w] = __popc(m);
     __syncthreads();
-    int before = at;
-#pragma unroll
-    for (int q = 0; q < kClusterThreads / 32; ++q) {
-      if (q < w) before += wsum[q];
-      at += wsum[q];
-    }
-    if (go) a.free_ids[before + __popc(m & ((1u << lane) - 1u))] = p;
+    const int n = wsum[lane];  // (as many warps as lanes)
+    const int behind = __reduce_add_sync(0xffffffffu, lane > w ? n : 0);
+    if (go) a.free_ids[at + behind + __popc(m & ~((2u << lane) - 1u))] = p;
+    at += __reduce_add_sync(0xffffffffu, n);
   }
 }
 
@@ -407,10 +489,32 @@ int launch_fork_pages(const ForkParams& p, cudaStream_t stream) {
 }
 
 int launch_release_pages(const ReleaseParams& p, cudaStream_t stream) {
-  auto bytes = [](int b) { return size_t(b + 1) * 4; };
-  if (!allow_smem(release_pages_kernel, bytes(p.b), bytes(kAllocMaxB))) return SPEC_ERR_LAUNCH;
-  const cudaError_t e = launch_cluster(release_pages_kernel, kClusterCtas, dim3(kClusterCtas), dim3(kClusterThreads), bytes(p.b), stream, p);
-  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+  auto bytes = [](int b) { return size_t(b + 1) * 12; };
+  const size_t smem = bytes(p.b);
+  const long long most = ((long long)p.b * p.row_pages + kKept * kClusterThreads - 1) / (kKept * kClusterThreads);
+  if (most > kClusterMost) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        !allow_smem(release_pages_kernel<false>, smem, bytes(kAllocMaxB)))
+      return SPEC_ERR_LAUNCH;
+    const int ctas = sms < kReleaseMostCtas ? sms : kReleaseMostCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(ctas));
+    cfg.blockDim = dim3(kClusterThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, release_pages_kernel<false>, p) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+  }
+  if (!allow_smem(release_pages_kernel<true>, smem, bytes(kAllocMaxB))) return SPEC_ERR_LAUNCH;
+  const int ctas = most > kClusterCtas && cudaFuncSetAttribute(release_pages_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess
+                       ? kClusterMost
+                       : kClusterCtas;
+  return launch_cluster(release_pages_kernel<true>, ctas, dim3(ctas), dim3(kClusterThreads), smem, stream, p) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 
 int launch_compact_pages(const CompactParams& p, cudaStream_t stream) {
@@ -423,7 +527,7 @@ int launch_compact_pages(const CompactParams& p, cudaStream_t stream) {
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 
-size_t release_partial_bytes(long long pages) { return 256 + align256(size_t(pages) * 8); }
+size_t release_partial_bytes(long long pages) { return kReleaseTotalsBytes + align256(size_t(pages) * 8); }
 size_t compact_partial_bytes(long long pages) { return 256 + 3 * align256(size_t(pages + 31) / 32 * 4); }
 
 }  // namespace spec

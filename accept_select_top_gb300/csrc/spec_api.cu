@@ -1114,8 +1114,9 @@ int spec_release_pages(int b, int page_size, const int32_t* req_pool_idx, const 
   p.row_pages = row_pages;
   p.n_left = n_left;
   p.error = v.error;
+  p.counters = v.counters;
   p.totals = reinterpret_cast<int*>(v.partials);
-  p.note = reinterpret_cast<int2*>(v.partials + 256);
+  p.note = reinterpret_cast<int2*>(v.partials + kReleaseTotalsBytes);
   return launch_release_pages(p, as_stream(stream));
 }
 

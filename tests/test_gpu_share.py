@@ -383,6 +383,34 @@ def test_captured_and_replayed():
             assert torch.equal(_bits(x), _bits(y))
 
 
+def test_wide_release_captured_and_replayed():
+    """Many rows: the release is one launch over many SMs.  Forks of a long prompt given back in one graph, three
+    times; then every holder's pages in one call."""
+    ops = _ops()
+    page, fan, L = 4, 60, 20001
+    c = Cache(page, [L], fan + 1, 5002, fan + 4)
+    ws = _ws(ops, ops.OP_FORK_PAGES, ops.OP_RELEASE_PAGES, b=fan + 1, pages=c.total)
+    r, t = c.rows, c.t
+    before = (list(c.free), c.n_free, list(c.counts))
+    parents, children, lens = i32([r[0]] * fan), i32(r[1:]), i32([L - i for i in range(fan)])
+    src, dst, n, left = i32([-5] * fan), i32([-5] * fan), i32([-5]), i32([-5])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ops.spec_fork_pages(fan, page, parents, children, lens, t["counts"], t["free"], t["n"], t["table"], None, src, dst, n, left, ws)
+        ops.spec_release_pages(fan, page, children, lens, None, t["counts"], t["free"], left, t["table"], left, ws)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert ws.last_error() == 0
+    assert (t["free"].tolist(), left.tolist()[0], t["counts"].tolist()) == before
+    c.fork(ws, [r[0]] * fan, r[1:], [L - i for i in range(fan)])
+    c.release(ws, r, [L] + [L - i for i in range(fan)])
+    assert ws.last_error() == 0
+    c.same()
+    assert c.n_free == c.total
+
+
 def test_engine_run():
     """Prompts admitted, sampled several times, grown, ended in another order, the cache compacted, and what every
     request holds read back after each step: the values written into each token's slot follow the request."""
