@@ -137,7 +137,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     s_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  pdl_wait();
+  // (behind the tcgen05 kernel, which waits for what came before the call, this one starts where CTAs end: it reads
+  // nothing of that kernel's, and waits for it at its own end)
+  if (!args.tall) pdl_wait();
   pdl_trigger();
 
   // ---- segments ----
@@ -177,7 +179,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
       g = lo;
       const int shared = a.shared_lens[g];
       if (report && r == sgroup[g] && (shared < 0 || shared > most)) raise_error(a.error, SPEC_DEV_LENGTH);
-      if (shared > 0 && slen[sgroup[g]] >= shared && slen[r] >= shared) base = shared;
+      const int s = dec_shared(shared, slen[sgroup[g]]);
+      if (slen[r] >= s) base = s;
     }
     sbase[r] = base;
     if (report) {
@@ -189,7 +192,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   auto ticks_of = [&](int s) {
     if (s < ng) {
       const int first = grouped ? sgroup[s] : 0, rows = grouped ? (sgroup[s + 1] - first) * G : 0;
-      const int tiles = rows ? (sbase[first] + kDecTile - 1) / kDecTile : 0;
+      const bool here = rows > 0 && !(args.tall && rows > kDecFlatRows);  // (else it is the tcgen05 kernel's)
+      const int tiles = here ? (sbase[first] + kDecTile - 1) / kDecTile : 0;
       return tiles ? a.Hkv * ((rows + kDecRows - 1) / kDecRows) * (tiles + kEndTicks) : 0;
     }
     const int r = s - ng, n = (slen[r] + kDecTile - 1) / kDecTile - sbase[r] / kDecTile;
@@ -224,7 +228,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   const int T = pre[ng + a.b];  // (the host keeps it below 2^31)
   const int ctas = T < int(gridDim.x) ? T : int(gridDim.x);
   if (report && tid == 0) *args.plan = make_int4(T, ctas, ng, 0);
-  if (int(blockIdx.x) >= ctas) return;
+  if (int(blockIdx.x) >= ctas) {
+    if (args.tall) pdl_wait();
+    return;
+  }
   const int S = int((long long)blockIdx.x * T / ctas), E = int((long long)(blockIdx.x + 1) * T / ctas);
 
   auto open = [&](Unit& u, int seg) {  // the first segment from `seg` on that has ticks
@@ -570,63 +577,145 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     t = 0;
     if (f < E) next_unit(u);
   }
+  if (args.tall) pdl_wait();
 }
 
-// Joins what the first kernel left: a warp an output row.
+// Joins the partial results of a row: a warp an output row, E neighbouring columns a lane.
 constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __grid_constant__ DecodeArgs args) {
   pdl_wait();
   pdl_trigger();
   const DecodeParams& a = args.p;
-  constexpr int E = D / 32;  // elements a lane
+  constexpr int E = D / 32;
+  constexpr unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31, orow = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
   if (orow >= a.b * a.Hq) return;
   const int r = orow / a.Hq, head = orow - r * a.Hq, G = a.Hq / a.Hkv, h = head / G, i = head - h * G;
   const int4 plan = __ldcg(args.plan);
   const int base = __ldcg(args.base + r);
-  const long long T = plan.x, ctas = plan.y;
-  auto cta_of = [&](int f) { return int(((long long)(f + 1) * ctas - 1) / T); };
+  // The parts of a unit: CTAs [wa, wb], or one whole.
+  struct Unit1 {
+    int wa, wb;
+    __device__ bool cut() const { return wa != wb; }
+  };
+  auto unit = [&](const int4& pl, const int* pre, int seg, int units, int j, int end) {
+    const int p0 = __ldcg(pre + seg), n = (__ldcg(pre + seg + 1) - p0) / units, u0 = p0 + j * n;
+    const long long T = pl.x, ctas = pl.y;
+    return Unit1{int(((long long)(u0 + 1) * ctas - 1) / T), int(((long long)(u0 + n - end) * ctas - 1) / T)};
+  };
+  const Unit1 own = unit(plan, args.pre, plan.z + r, a.Hkv * args.own_tiles, h * args.own_tiles + i / kDecRows, kEndTicks);
+  if (!own.cut() && base == 0) return;  // (already in out)
+  const int n_own = own.wb - own.wa + 1;
+  // what the request shares: in the first kernel's fragments, or the tcgen05 kernel's
+  Unit1 sh{0, 0};
+  int n_sh = 0, x = 0, rows = 0, xr = 0;
+  bool tall = false, split = false;
+  size_t unit0 = 0;
+  if (base > 0) {
+    const int2 mem = __ldcg(args.member + r);
+    const int r0 = r - mem.y, all = (__ldg(a.group_start + mem.x + 1) - r0) * G;
+    x = mem.y * G + i;
+    tall = args.tall && all > kDecFlatRows;
+    if (tall) {
+      const int blocks = (all + kDecTallRows - 1) / kDecTallRows, blk = x / kDecTallRows;
+      rows = min(kDecTallRows, all - blk * kDecTallRows);
+      xr = x - blk * kDecTallRows;
+      split = rows <= 128;
+      unit0 = size_t(r0) * a.Hq + size_t(h) * all + size_t(blk) * kDecTallRows;
+      sh = unit(__ldcg(args.tall_plan), args.tall_pre, mem.x, a.Hkv * blocks, h * blocks + blk, kDecTallEnd);
+      n_sh = (sh.wb - sh.wa + 1) * (split ? 2 : 1);
+    } else {
+      const int tiles = (all + kDecRows - 1) / kDecRows;
+      sh = unit(plan, args.pre, mem.x, a.Hkv * tiles, h * tiles + x / kDecRows, kEndTicks);
+      n_sh = sh.wb - sh.wa + 1;
+    }
+  }
+  const int np = n_own + n_sh;
+  // part q: its (m, l), its O (row-major, or words of four columns `step` apart)
+  auto part = [&](int q, const float2*& ml, const float*& o, int& step) {
+    step = 1;
+    const bool mine = q < n_own;
+    if (!mine) q -= n_own;
+    if (!mine && tall) {
+      const int cta = sh.wa + (split ? q >> 1 : q), half = split ? q & 1 : xr >> 7;
+      if (!sh.cut()) {
+        const size_t first = (split ? size_t(half) * a.b * a.Hq : 0) + unit0;
+        ml = args.whole_ml + first + xr;
+        o = reinterpret_cast<const float*>(args.whole_o + first * (D / 4) + xr);
+        step = rows;
+      } else {
+        const size_t slot = (size_t(2) * cta + (cta == sh.wa ? 1 : 0)) * 2 + half;
+        ml = args.tall_ml + slot * 128 + (xr & 127);
+        o = reinterpret_cast<const float*>(args.tall_o + slot * (D / 4) * 128 + (xr & 127));
+        step = 128;
+      }
+      return;
+    }
+    const Unit1& u = mine ? own : sh;
+    const size_t row = u.cut() ? size_t(2 * (u.wa + q) + (q == 0 ? 1 : 0)) * kDecRows + (mine ? i : x) % kDecRows : size_t(orow);
+    ml = (u.cut() ? args.frag_ml : mine ? args.own_ml : args.shared_ml) + row;
+    o = (u.cut() ? args.frag_o : mine ? args.own_o : args.shared_o) + row * D;
+  };
   float M = -INFINITY, Ls = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  auto add = [&](const float* o, const float2* ml, size_t row) {
-    const float2 x = __ldcg(ml + row);
-    float v[E];
+  for (int q0 = 0; q0 < np; q0 += 32) {
+    const float2* ml = nullptr;
+    const float* o = nullptr;
+    int step = 1;
+    float2 v = make_float2(-INFINITY, 0.f);
+    if (q0 + lane < np) {
+      part(q0 + lane, ml, o, step);
+      v = __ldcg(ml);
+    }
+    float M2 = v.x;
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = __ldcg(o + row * D + 32 * e + lane);
-    const float M2 = fmaxf(M, x.x), wa = dec_weight(M, M2), wb = dec_weight(x.x, M2);
-    Ls = Ls * wa + x.y * wb;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * wa + v[e] * wb;
+    for (int k = 16; k > 0; k >>= 1) M2 = fmaxf(M2, __shfl_xor_sync(FULL, M2, k));
+    M2 = fmaxf(M2, M);
+    const float was = dec_weight(M, M2), wt = dec_weight(v.x, M2);
     M = M2;
-  };
-  // the CTAs on the unit of row x of segment `seg`; false where one CTA holds it whole
-  auto parts = [&](int seg, int row_tiles, int x, int& wa, int& wb) {
-    const int p0 = __ldcg(args.pre + seg), n = (__ldcg(args.pre + seg + 1) - p0) / (a.Hkv * row_tiles);
-    const int u0 = p0 + (h * row_tiles + x / kDecRows) * n;
-    wa = cta_of(u0);
-    wb = cta_of(u0 + n - kEndTicks - 1);
-    return wa != wb;
-  };
-  auto add_parts = [&](int wa, int wb, int x) {
-    for (int q = wa; q <= wb; ++q) add(args.frag_o, args.frag_ml, size_t(2 * q + (q == wa ? 1 : 0)) * kDecRows + x % kDecRows);
-  };
-  int wa, wb;
-  const bool cut = parts(plan.z + r, args.own_tiles, i, wa, wb);
-  if (!cut && base == 0) return;  // (already in out)
-  if (cut) add_parts(wa, wb, i);
-  else add(args.own_o, args.own_ml, orow);
-  if (base > 0) {
-    const int2 mem = __ldcg(args.member + r);
-    const int rows = (__ldg(a.group_start + mem.x + 1) - (r - mem.y)) * G, x = mem.y * G + i;
-    if (parts(mem.x, (rows + kDecRows - 1) / kDecRows, x, wa, wb)) add_parts(wa, wb, x);
-    else add(args.shared_o, args.shared_ml, orow);
+    Ls = Ls * was + warp_sum(v.y * wt);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= was;
+    const int n = min(32, np - q0);
+    constexpr int kOnce = 4;
+    for (int k0 = 0; k0 < n; k0 += kOnce) {
+      float y[kOnce][E], wk[kOnce];
+#pragma unroll
+      for (int k = 0; k < kOnce; ++k) {
+        const int src = k0 + k < n ? k0 + k : 0;
+        wk[k] = k0 + k < n ? __shfl_sync(FULL, wt, src) : 0.f;
+        const float* from = reinterpret_cast<const float*>(__shfl_sync(FULL, reinterpret_cast<unsigned long long>(o), src));
+        const int st = __shfl_sync(FULL, step, src);
+        // (the lane's columns E lane ..: word E lane / 4 of four)
+        from += size_t(E * lane / 4) * 4 * st + E * lane % 4;
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[k][e] = 0.f;
+        if (wk[k] != 0.f) {  // (a part that has seen nothing is not read)
+          if (E == 4) {
+            const float4 z = __ldcg(reinterpret_cast<const float4*>(from));
+            y[k][0] = z.x;
+            y[k][1] = z.y;
+            y[k][E - 2] = z.z;
+            y[k][E - 1] = z.w;
+          } else {
+            const float2 z = __ldcg(reinterpret_cast<const float2*>(from));
+            y[k][0] = z.x;
+            y[k][1] = z.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kOnce; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(y[k][e], wk[k], acc[e]);
+    }
   }
   const float inv = dec_inverse(Ls);
-  uint16_t* out = static_cast<uint16_t*>(a.out) + size_t(orow) * D;
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[32 * e + lane] = uint16_t(dec_pack(acc[e] * inv, 0.f));
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + size_t(orow) * D + E * lane);
+  out[0] = dec_pack(acc[0] * inv, acc[1] * inv);
+  if (E == 4) out[E / 2 - 1] = dec_pack(acc[E - 2] * inv, acc[E - 1] * inv);
   if (lane == 0 && a.lse) a.lse[orow] = dec_lse(M, Ls);
 }
 
@@ -638,6 +727,8 @@ int launch_decode(const DecodeArgs& args, int sms, cudaStream_t stream) {
                            int(DecSmem<D>::bytes(kDecodeMaxB, kDecodeMaxB))) != cudaSuccess)  // (the most, so that calls of two threads agree)
     return SPEC_ERR_LAUNCH;
   const int grid = sms < kDecMaxCtas ? sms : kDecMaxCtas;
+  if (args.tall)
+    if (const int rc = launch_decode_tall(args, sms, stream)) return rc;
   if (launch_pdl(decode_attention_kernel<D>, dim3(grid), dim3(kDecThreads), smem, stream, args) != cudaSuccess) return SPEC_ERR_LAUNCH;
   const unsigned blocks = unsigned((size_t(p.b) * p.Hq + kJoinWarps - 1) / kJoinWarps);
   return launch_pdl(decode_join_kernel<D>, dim3(blocks), dim3(32 * kJoinWarps), 0, stream, args) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
@@ -646,8 +737,9 @@ int launch_decode(const DecodeArgs& args, int sms, cudaStream_t stream) {
 // Offsets of the workspace's parts.
 struct DecodeLayout {
   size_t pre, base, member, frag_ml, own_ml, shared_ml, frag_o, own_o, shared_o, bytes;
-  DecodeLayout(int b, int Hq, int D) {
-    const size_t rows = size_t(b) * Hq, frags = size_t(2) * kDecMaxCtas * kDecRows;
+  size_t tall_pre, tall_ml, whole_ml, tall_o, whole_o;
+  DecodeLayout(int b, int Hq, int D, bool tall) {
+    const size_t rows = size_t(b) * Hq, frags = size_t(2) * kDecMaxCtas * kDecRows, tall_frags = size_t(2) * kDecMaxCtas * kDecTallRows;
     size_t at = 256;
     auto take = [&](size_t n) {
       const size_t x = at;
@@ -663,20 +755,32 @@ struct DecodeLayout {
     frag_o = take(frags * D * 4);
     own_o = take(rows * D * 4);
     shared_o = take(rows * D * 4);
+    tall_pre = tall_ml = whole_ml = tall_o = whole_o = at;
+    if (tall) {
+      tall_pre = take(size_t(b + 1) * 4);
+      tall_ml = take(tall_frags * 8);
+      whole_ml = take(2 * rows * 8);
+      tall_o = take(tall_frags * D * 4);
+      whole_o = take(2 * rows * D * 4);
+    }
     bytes = at;
   }
 };
+// whether a group of the batch may have more rows than the register kernel takes
+bool may_be_tall(int b, int Hq, int Hkv) { return (long long)b * (Hq / Hkv) > kDecFlatRows; }
 
 }  // namespace
 
-size_t decode_partial_bytes(int b, int Hq) { return DecodeLayout(b, Hq, 128).bytes; }
+size_t decode_partial_bytes(int b, int Hq, int Hkv) { return DecodeLayout(b, Hq, 128, may_be_tall(b, Hq, Hkv)).bytes; }
 
 int launch_decode_attention(const DecodeParams& p, cudaStream_t stream) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return SPEC_ERR_LAUNCH;
-  const DecodeLayout at(p.b, p.Hq, p.D);
+  // (a scale of zero would take the -inf of a key that does not count to NaN there)
+  const bool tall = p.num_groups > 0 && may_be_tall(p.b, p.Hq, p.Hkv) && p.scale != 0.f;
+  const DecodeLayout at(p.b, p.Hq, p.D, tall);
   unsigned char* ws = p.partials;
   DecodeArgs args{};
   args.p = p;
@@ -693,6 +797,13 @@ int launch_decode_attention(const DecodeParams& p, cudaStream_t stream) {
   args.frag_o = reinterpret_cast<float*>(ws + at.frag_o);
   args.own_o = reinterpret_cast<float*>(ws + at.own_o);
   args.shared_o = reinterpret_cast<float*>(ws + at.shared_o);
+  args.tall = tall;
+  args.tall_plan = reinterpret_cast<int4*>(ws + 128);
+  args.tall_pre = reinterpret_cast<int*>(ws + at.tall_pre);
+  args.tall_ml = reinterpret_cast<float2*>(ws + at.tall_ml);
+  args.tall_o = reinterpret_cast<float4*>(ws + at.tall_o);
+  args.whole_ml = reinterpret_cast<float2*>(ws + at.whole_ml);
+  args.whole_o = reinterpret_cast<float4*>(ws + at.whole_o);
   return p.D == 128 ? launch_decode<128>(args, sms, stream) : launch_decode<64>(args, sms, stream);
 }
 

@@ -28,6 +28,14 @@ __device__ __forceinline__ float dec_lse(float m, float l) {
   return l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
+// Rows of a group's shared tokens (members times q heads of a kv head) above which the tcgen05 kernel takes them.
+constexpr int kDecFlatRows = 64;
+constexpr int kDecTallRows = 256;  // query rows of one of its units
+constexpr int kDecTallEnd = 2;     // what a unit's end costs there in the division of the work, in tiles
+
+// What a group shares, from its bounds and its first member's length (0: nothing).
+__device__ __forceinline__ int dec_shared(int shared, int first_len) { return shared > 0 && first_len >= shared ? shared : 0; }
+
 // The workspace of a call.  plan: {ticks, CTAs, groups, -} and, for the joining kernel, what the first CTA of the main
 // kernel found: ticks before each segment, each request's shared length, its group and place in it.
 struct DecodeArgs {
@@ -44,6 +52,18 @@ struct DecodeArgs {
   float* frag_o;    // [.][D]
   float* own_o;
   float* shared_o;
+  // the tcgen05 kernel's (tall 0: it is not launched): plan {ticks, CTAs, -, -}, ticks before each group, fragments
+  // [2 * CTA + i][half][D / 4][128 rows] and units that lie in one CTA, [half][..][D / 4][rows]; halves: rows 128 .., or
+  // every second tile where there are no more than 128
+  int tall;
+  int4* tall_plan;
+  int* tall_pre;
+  float2* tall_ml;
+  float4* tall_o;
+  float2* whole_ml;  // [half][b * Hq]
+  float4* whole_o;
 };
+
+int launch_decode_tall(const DecodeArgs& args, int sms, cudaStream_t stream);
 
 }  // namespace spec

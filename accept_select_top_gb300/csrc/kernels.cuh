@@ -526,6 +526,6 @@ struct DecodeParams {
 // the kernel keeps the tiles before each segment in shared memory
 constexpr int kDecodeMaxB = 2048;
 int launch_decode_attention(const DecodeParams& p, cudaStream_t stream);
-size_t decode_partial_bytes(int b, int Hq);
+size_t decode_partial_bytes(int b, int Hq, int Hkv);
 
 }  // namespace spec

@@ -112,7 +112,7 @@ size_t partial_bytes(int op, int b, int n, int k, int V, int Hq, int Hkv, int ma
     case SPEC_OP_COMPACT_PAGES:
       return compact_partial_bytes(V);
     case SPEC_OP_DECODE_ATTENTION:
-      return decode_partial_bytes(b, Hq);
+      return decode_partial_bytes(b, Hq, Hkv);
     default:
       return 0;
   }
