@@ -12,8 +12,9 @@
 //   Four producer warps look up the slots of the keys (two tiles ahead) and copy K and V rows with 16-byte
 // cp.async into a ring of five tiles; they do not care where units end, so the memory stays busy while one does.
 //   Eight consumer warps compute on register fragments (mma.sync m16n8k16; rows are few, and a 128-row tcgen05 tile
-// would be padding): up to 16 rows: four warps share a tile's keys, and the two sets of four take turns at the
-// tiles; 32: two row tiles times four shares of the keys; 64: four times two.  The order of the head
+// would be padding).  A unit's part of up to 16 rows belongs to four of them, which share each tile's keys (to one, if it
+// is a single tile), and the parts take turns: what the ends of a part take (its Q, the results) is 3 us of latency,
+// during which the others compute.  32 rows: two row tiles times four shares of the keys; 64: four times two.  The order of the head
 // dimension inside a fragment is free as long as Q has the same, so K fragments are read as 16-byte words.
 // At a unit's end the warps' results are joined through shared memory.
 //   Units cut by a range boundary, and all of a grouped request, leave fp32 results in the workspace; a second,
@@ -32,6 +33,9 @@ namespace {
 constexpr int kConsumers = 8, kProducers = 4;
 constexpr int kDecThreads = 32 * (kConsumers + kProducers);
 constexpr int kRing = 5;
+constexpr int kOwners = kConsumers + 2;  // who may have a part to itself: a warp, or four of them
+// A part of at most so many tiles, where the CTA's range is so many times longer, goes to one warp.
+constexpr int kSoloTiles = 1, kSoloRange = 2;
 constexpr int kEndTicks = 1;  // what a unit's end costs in the division of the work, in tiles
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wait
 
@@ -43,8 +47,8 @@ struct DecSmem {
   static constexpr int kMerge = kRing * kStage;    // [warp][8 column tiles][32 lanes] float4
   static constexpr int kMl = kMerge + kConsumers * 8 * 32 * 16;  // [warp][16] (m, l)
   static constexpr int kMask = kMl + kConsumers * 16 * 8;        // [stage][4] keys that count, 16 bits each
-  static constexpr int kBars = kMask + kRing * 4 * 4;            // full[5], empty[5]
-  static constexpr int kAbort = kBars + 2 * kRing * 8;
+  static constexpr int kBars = kMask + kRing * 4 * 4;            // full[5], empty[5], then [owner][5]
+  static constexpr int kAbort = kBars + (2 + kOwners) * kRing * 8;
   static constexpr int kScan = kAbort + 16;        // pre [groups + b + 1], len [b], base [b]
   static size_t bytes(int b, int groups) { return size_t(kScan) + 4u * size_t(groups + 3 * b + 1); }
 };
@@ -54,8 +58,8 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mbar_arrive(uint32_t bar, uint32_t count = 1) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 // counts as an arrival once the thread's copies so far have landed
 __device__ __forceinline__ void mbar_arrive_copies(uint32_t bar) {
@@ -101,7 +105,7 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory"); }
+__device__ __forceinline__ void part_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 // A unit of the tick space.  Segments: the groups' shared tokens, then the requests' own.
 struct Unit {
@@ -127,12 +131,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   __shared__ int s_bad;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  const uint32_t full = smem_u32(smem + L::kBars), empty = full + 8 * kRing;
+  const uint32_t full = smem_u32(smem + L::kBars), empty = full + 8 * kRing, owned = empty + 8 * kRing;
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(full + 8 * i, kProducers * 33);
       mbar_init(empty + 8 * i, kConsumers);
     }
+    for (int i = 0; i < kOwners * kRing; ++i) mbar_init(owned + 8 * i, kProducers * 33);
     *abort_flag = 0;
     s_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -272,6 +277,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
       u.j = 0;
     }
   };
+  // Who takes a part of n tiles of a unit: a warp (0 .. 7), four (8, 9), or all (-1).  parts: how many of either kind
+  // came before in the range.
+  auto owner_of = [&](const Unit& u, int n, int2& parts) {
+    const int row_tiles = u.J / a.Hkv;
+    if (u.rows - (u.j % row_tiles) * kDecRows > 16) return -1;
+    if (n <= kSoloTiles && E - S > kSoloRange * n) return parts.x++ % kConsumers;
+    return kConsumers + (parts.y++ & 1);
+  };
   __syncthreads();  // (sgroup is not read any more)
 
   if (w >= kConsumers) {
@@ -284,16 +297,23 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     Unit u;
     int t, f = S;
     locate(f, u, t);
-    // The next tile of the range, its kv head (-1: none is left); lanes of this half of the warp look up
-    // their key's page id.
-    int x_pos = -1, x_id = -1;
+    // The next tile of the range, its kv head (-1: none is left) and its owner (-1: all warps);
+    // lanes of this half of the warp look up their key's page id.
+    int x_pos = -1, x_id = -1, owner = -1;
+    int2 parts = make_int2(0, 0);
+    bool entered = false;
     auto look = [&](int half) {
       while (f < E && t >= u.tiles) {  // over a unit's end
         f += u.tiles + kEndTicks - t;
         t = 0;
+        entered = false;
         if (f < E) next_unit(u);
       }
-      if (f >= E) return -1;
+      if (f >= E) return make_int2(-1, -1);
+      if (!entered) {
+        entered = true;
+        owner = owner_of(u, min(u.tiles - t, E - f), parts);
+      }
       const int row_tiles = u.J / a.Hkv, h = u.j / row_tiles;
       if ((lane >> 4) == half) {
         const int x = (u.first / kDecTile + t) * kDecTile + 16 * p + (lane & 15);
@@ -305,16 +325,16 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
       }
       ++f;
       ++t;
-      return h;
+      return make_int2(h, owner);
     };
     int stage = 0;
     uint32_t phase = 1;  // (an empty ring)
     bool dead = false;
-    int heads[2];
+    int2 heads[2];
     heads[0] = look(0);
-    heads[1] = heads[0] >= 0 ? look(1) : -1;
-    while (heads[0] >= 0 && !dead) {
-      const int h0 = heads[0], h1 = heads[1];
+    heads[1] = heads[0].x >= 0 ? look(1) : make_int2(-1, -1);
+    while (heads[0].x >= 0 && !dead) {
+      const int2 h0 = heads[0], h1 = heads[1];
       int slot = -1;
       if (x_pos >= 0) {
         if (x_id < 0 || x_id >= a.num_pages) raise_error(a.error, SPEC_DEV_INDEX);
@@ -323,7 +343,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
       const unsigned valid = __ballot_sync(FULL, slot >= 0);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int h = half ? h1 : h0;
+        const int h = half ? h1.x : h0.x, who = half ? h1.y : h0.y;
         if (h < 0 || dead) break;
         if (__any_sync(FULL, !mbar_wait(empty + 8 * stage, phase, abort_flag))) {
           dead = true;
@@ -339,11 +359,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
           cp16(st + key * L::kRow + (cx ^ (4 * (key & 1))) * 16, static_cast<const unsigned char*>(a.k_pool) + at, n);
           cp16(st + L::kHalf + key * L::kRow + (cx ^ (key & 7)) * 16, static_cast<const unsigned char*>(a.v_pool) + at, n);
         }
+        const uint32_t tell = who < 0 ? full + 8 * stage : owned + 8 * (who * kRing + stage);
         if (lane == 0) {
           reinterpret_cast<volatile uint32_t*>(smem + L::kMask)[stage * 4 + p] = (valid >> (16 * half)) & 0xffffu;
-          mbar_arrive(full + 8 * stage);
+          mbar_arrive(tell);
         }
-        mbar_arrive_copies(full + 8 * stage);
+        mbar_arrive_copies(tell);
         if (++stage == kRing) {
           stage = 0;
           phase ^= 1;
@@ -351,7 +372,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
         if (half == 0) heads[0] = look(0);
       }
       // (the other half's next tile follows, once both of this window have been copied)
-      heads[1] = !dead && h1 >= 0 && heads[0] >= 0 ? look(1) : -1;
+      heads[1] = !dead && h1.x >= 0 && heads[0].x >= 0 ? look(1) : make_int2(-1, -1);
     }
     if (dead && lane == 0) {
       raise_error(a.error, SPEC_DEV_TIMEOUT);
@@ -364,24 +385,29 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, c = lane & 3;
   const float xf = a.scale * 1.4426950408889634f;
-  int stage = 0, count = 0;
-  uint32_t phase = 0;
+  int stage = 0;
+  int2 parts = make_int2(0, 0);
+  uint32_t full_bits = 0, solo_bits = 0, four_bits = 0;  // parity of the next phase of each stage's barriers
   bool dead = false;
   float4* const merge = reinterpret_cast<float4*>(smem + L::kMerge);
   float2* const mls = reinterpret_cast<float2*>(smem + L::kMl);
-
-  // One unit's part in the range: n tiles; RT row tiles of 16.
-  auto work = [&](auto rt_const, const Unit& u, int t0, int n) {
-    constexpr int RT = decltype(rt_const)::value;
-    constexpr int KS = kConsumers / RT;             // warps that hold a row tile
-    constexpr int BLOCKS = RT == 4 ? 2 : 1;         // 16-key blocks of a tile that a warp takes
-    const int rt = w % RT, share = RT == 1 ? w & 3 : w / RT, set = w >> 2;
-    const int row_tiles = u.J / a.Hkv, h = u.j / row_tiles, row0 = (u.j - h * row_tiles) * kDecRows;
-    uint32_t qf[D / 16][4];
-    float o[NT][4], m[2], l[2];
+  uint32_t qf[D / 16][4];
+  float o[NT][4], m[2], l[2];
+  auto wait_tile = [&](uint32_t bar, uint32_t parity) {
+    if (!dead && __any_sync(FULL, !mbar_wait(bar, parity, abort_flag))) {
+      dead = true;
+      if (lane == 0) {
+        raise_error(a.error, SPEC_DEV_TIMEOUT);
+        *abort_flag = 1;
+      }
+    }
+  };
+  auto next_stage = [&] { stage = stage + 1 == kRing ? 0 : stage + 1; };
+  // 16 query rows of the unit, from row x0 of the segment on, and empty results
+  auto begin = [&](const Unit& u, int h, int x0) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int x = row0 + rt * 16 + g + 8 * i;  // row of the segment
+      const int x = x0 + g + 8 * i;
       const bool on = x < u.rows;
       const int f = on ? x / G : 0;
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (size_t(u.r0) + f) * a.q_ld +
@@ -401,139 +427,166 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     for (int q = 0; q < NT; ++q)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[q][i] = 0.f;
-
-    for (int i = 0; i < n; ++i) {
-      if (!dead && __any_sync(FULL, !mbar_wait(full + 8 * stage, phase, abort_flag))) {
-        dead = true;
-        if (lane == 0) {
-          raise_error(a.error, SPEC_DEV_TIMEOUT);
-          *abort_flag = 1;
-        }
-      }
-      if (!dead && (RT > 1 || (count & 1) == set)) {
-        const uint32_t st = smem_u32(smem + stage * L::kStage);
+  };
+  // 16 keys of the tile in `stage`
+  auto block = [&](int part) {
+    const uint32_t st = smem_u32(smem + stage * L::kStage);
+    const uint32_t mask = reinterpret_cast<volatile uint32_t*>(smem + L::kMask)[stage * 4 + part];
+    if (mask == 0) return;
+    float s[2][4];
 #pragma unroll
-        for (int blk = 0; blk < BLOCKS; ++blk) {
-          const int part = share * BLOCKS + blk;  // 16 keys of the tile
-          const uint32_t mask = reinterpret_cast<volatile uint32_t*>(smem + L::kMask)[stage * 4 + part];
-          if (mask == 0) continue;
-          float s[2][4];
+    for (int q = 0; q < 2; ++q) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+      for (int e = 0; e < 4; ++e) s[q][e] = 0.f;
+      const uint32_t row = st + (16 * part + 8 * q + g) * L::kRow;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[q][e] = 0.f;
-            const uint32_t row = st + (16 * part + 8 * q + g) * L::kRow;
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              const uint4 y = lds16(row + ((4 * k + c) ^ (4 * (g & 1))) * 16);
-              mma_bf16(s[q], qf[2 * k], y.x, y.y);
-              mma_bf16(s[q], qf[2 * k + 1], y.z, y.w);
-            }
-          }
-          auto masked = [&](float (&v)[2][4]) {
-            if (mask != 0xffffu) {
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (!(mask >> (8 * q + 2 * c + (e & 1)) & 1)) v[q][e] = -INFINITY;
-            }
-          };
-          // y = x - m; a row without a reference has y = inf (NaN where x is -inf)
-          float y[2][4], top = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[q][e] = fmaf(s[q][e], xf, -m[e >> 1]);
-          masked(y);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = fmaxf(top, y[q][e]);
-          if (__any_sync(FULL, top > kDecBase + kDecLazy || m[0] == -INFINITY || m[1] == -INFINITY)) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) s[q][e] *= xf;
-            masked(s);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-              mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
-              mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
-              const float ref = mx - kDecBase;
-              if (ref > m[r] + kDecLazy || m[r] == -INFINITY) {
-                const float fac = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - ref);
-                l[r] *= fac;
-#pragma unroll
-                for (int q = 0; q < NT; ++q) {
-                  o[q][2 * r] *= fac;
-                  o[q][2 * r + 1] *= fac;
-                }
-                m[r] = ref;
-              }
-            }
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[q][e] = s[q][e] - (m[e >> 1] == -INFINITY ? 0.f : m[e >> 1]);
-          }
-          uint32_t pa[4];
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float p0 = fast_exp2(y[q][2 * r]), p1 = fast_exp2(y[q][2 * r + 1]);
-              l[r] += p0 + p1;
-              pa[2 * q + r] = dec_pack(p0, p1);
-            }
-          const int vkey = 16 * part + (lane & 15);
-          const uint32_t vrow = st + L::kHalf + vkey * L::kRow;
-#pragma unroll
-          for (int q = 0; q < NT / 2; ++q) {
-            const uint4 v = ldsm_t(vrow + (((2 * q + (lane >> 4)) ^ (vkey & 7)) * 16));
-            mma_bf16(o[2 * q], pa, v.x, v.y);
-            mma_bf16(o[2 * q + 1], pa, v.z, v.w);
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty + 8 * stage);
-      ++count;
-      if (++stage == kRing) {
-        stage = 0;
-        phase ^= 1;
+      for (int k = 0; k < D / 32; ++k) {
+        const uint4 y = lds16(row + ((4 * k + c) ^ (4 * (g & 1))) * 16);
+        mma_bf16(s[q], qf[2 * k], y.x, y.y);
+        mma_bf16(s[q], qf[2 * k + 1], y.z, y.w);
       }
     }
-
-    // ---- the warps' results joined ----
+    auto masked = [&](float (&v)[2][4]) {
+      if (mask != 0xffffu) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!(mask >> (8 * q + 2 * c + (e & 1)) & 1)) v[q][e] = -INFINITY;
+      }
+    };
+    // y = x - m; a row without a reference has y = inf (NaN where x is -inf)
+    float y[2][4], top = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[q][e] = fmaf(s[q][e], xf, -m[e >> 1]);
+    masked(y);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, y[q][e]);
+    if (__any_sync(FULL, top > kDecBase + kDecLazy || m[0] == -INFINITY || m[1] == -INFINITY)) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[q][e] *= xf;
+      masked(s);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+        const float ref = mx - kDecBase;
+        if (ref > m[r] + kDecLazy || m[r] == -INFINITY) {
+          const float fac = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - ref);
+          l[r] *= fac;
+#pragma unroll
+          for (int q = 0; q < NT; ++q) {
+            o[q][2 * r] *= fac;
+            o[q][2 * r + 1] *= fac;
+          }
+          m[r] = ref;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[q][e] = s[q][e] - (m[e >> 1] == -INFINITY ? 0.f : m[e >> 1]);
+    }
+    uint32_t pa[4];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float p0 = fast_exp2(y[q][2 * r]), p1 = fast_exp2(y[q][2 * r + 1]);
+        l[r] += p0 + p1;
+        pa[2 * q + r] = dec_pack(p0, p1);
+      }
+    const int vkey = 16 * part + (lane & 15);
+    const uint32_t vrow = st + L::kHalf + vkey * L::kRow;
+#pragma unroll
+    for (int q = 0; q < NT / 2; ++q) {
+      const uint4 v = ldsm_t(vrow + (((2 * q + (lane >> 4)) ^ (vkey & 7)) * 16));
+      mma_bf16(o[2 * q], pa, v.x, v.y);
+      mma_bf16(o[2 * q + 1], pa, v.z, v.w);
+    }
+  };
+  auto sum_l = [&] {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(FULL, l[r], 1);
       l[r] += __shfl_xor_sync(FULL, l[r], 2);
-      if (c == 0) mls[w * 16 + g + 8 * r] = make_float2(m[r], l[r]);
     }
-    const bool own = u.seg >= ng, begun = t0 == 0, whole = begun && n == u.tiles;
-    const bool final = own && whole && u.first == 0;
+  };
+  // Two columns of a row's result (unnormalised, relative to M): out, or a partial result.
+  auto put = [&](const Unit& u, int h, int row0, int row, int col, bool whole, bool begun, float M, float Ls, float s0, float s1, bool note) {
+    const bool own = u.seg >= ng;
+    const int f = row / G;
+    const size_t orow = (size_t(u.r0) + f) * a.Hq + h * G + (row - f * G);
+    if (own && whole && u.first == 0) {
+      const float inv = dec_inverse(Ls);
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * D + col) = dec_pack(s0 * inv, s1 * inv);
+      if (note && a.lse) a.lse[orow] = dec_lse(M, Ls);
+    } else {
+      const size_t frow = whole ? orow : size_t(2 * blockIdx.x + (begun ? 1 : 0)) * kDecRows + row - row0;
+      float* fo = whole ? (own ? args.own_o : args.shared_o) : args.frag_o;
+      float2* fm = whole ? (own ? args.own_ml : args.shared_ml) : args.frag_ml;
+      *reinterpret_cast<float2*>(fo + frow * D + col) = make_float2(s0, s1);
+      if (note) fm[frow] = make_float2(M, Ls);
+    }
+  };
+
+  // A unit's part in the range, n tiles, by `who`: all warps (RT 2 or 4 row tiles of 16), or four of them (RT 1).
+  auto work = [&](auto rt_const, const Unit& u, int t0, int n, int who) {
+    constexpr int RT = decltype(rt_const)::value;
+    constexpr int KS = RT == 1 ? 4 : kConsumers / RT;  // warps that hold a row tile
+    constexpr int kThreads = 32 * RT * KS;
+    const int rt = w % RT, share = RT == 1 ? w & 3 : w / RT, w0 = RT == 1 ? w & 4 : 0, id = RT == 1 ? 2 + (w >> 2) : 1;
+    const int row_tiles = u.J / a.Hkv, h = u.j / row_tiles, row0 = (u.j - h * row_tiles) * kDecRows;
+    uint32_t& bits = RT == 1 ? four_bits : full_bits;
+    begin(u, h, row0 + rt * 16);
+    for (int i = 0; i < n; ++i) {
+      wait_tile(RT == 1 ? owned + 8 * (who * kRing + stage) : full + 8 * stage, bits >> stage & 1u);
+      bits ^= 1u << stage;
+      if (!dead) {
+        if (RT == 4) {
+          block(2 * share);
+          block(2 * share + 1);
+        } else {
+          block(share);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * stage, kConsumers / (RT * KS));
+      next_stage();
+    }
+
+    // ---- the warps' results joined ----
+    sum_l();
+    if (c == 0) {
+      mls[w * 16 + g] = make_float2(m[0], l[0]);
+      mls[w * 16 + g + 8] = make_float2(m[1], l[1]);
+    }
+    const bool begun = t0 == 0, whole = begun && n == u.tiles;
 #pragma unroll
     for (int half = 0; half < D / 64; ++half) {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
         merge[(w * 8 + q) * 32 + lane] = make_float4(o[8 * half + q][0], o[8 * half + q][1], o[8 * half + q][2], o[8 * half + q][3]);
-      consumer_sync();
-      for (int x = tid; x < RT * 256; x += 32 * kConsumers) {
+      part_sync(id, kThreads);
+      for (int x = tid - 32 * w0; x < RT * 256; x += kThreads) {
         const int tile = x >> 8, q = (x >> 5) & 7, ln = x & 31, gg = ln >> 2;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int row = row0 + tile * 16 + gg + 8 * r;  // of the segment
           if (row >= u.rows) continue;
           float M = -INFINITY, Ls = 0.f, s0 = 0.f, s1 = 0.f;
-          // (the warps of a row tile; the two sets of RT 1 count as eight)
 #pragma unroll
-          for (int k = 0; k < KS; ++k) M = fmaxf(M, mls[(RT * k + tile) * 16 + gg + 8 * r].x);
+          for (int k = 0; k < KS; ++k) M = fmaxf(M, mls[(w0 + RT * k + tile) * 16 + gg + 8 * r].x);
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
-            const int ww = RT * k + tile;
+            const int ww = w0 + RT * k + tile;
             const float2 ml = mls[ww * 16 + gg + 8 * r];
             const float wt = dec_weight(ml.x, M);
             const float2 v = reinterpret_cast<const float2*>(merge + (ww * 8 + q) * 32 + ln)[r];
@@ -541,24 +594,35 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
             s0 = fmaf(wt, v.x, s0);
             s1 = fmaf(wt, v.y, s1);
           }
-          const int col = 64 * half + 8 * q + 2 * (ln & 3);
-          const int f = row / G;
-          const size_t orow = (size_t(u.r0) + f) * a.Hq + h * G + (row - f * G);
-          const bool note = half == 0 && q == 0 && (ln & 3) == 0;
-          if (final) {
-            const float inv = dec_inverse(Ls);
-            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * D + col) = dec_pack(s0 * inv, s1 * inv);
-            if (note && a.lse) a.lse[orow] = dec_lse(M, Ls);
-          } else {
-            const size_t frow = whole ? orow : size_t(2 * blockIdx.x + (begun ? 1 : 0)) * kDecRows + row - row0;
-            float* fo = whole ? (own ? args.own_o : args.shared_o) : args.frag_o;
-            float2* fm = whole ? (own ? args.own_ml : args.shared_ml) : args.frag_ml;
-            *reinterpret_cast<float2*>(fo + frow * D + col) = make_float2(s0, s1);
-            if (note) fm[frow] = make_float2(M, Ls);
-          }
+          put(u, h, row0, row, 64 * half + 8 * q + 2 * (ln & 3), whole, begun, M, Ls, s0, s1, half == 0 && q == 0 && (ln & 3) == 0);
         }
       }
-      consumer_sync();
+      part_sync(id, kThreads);
+    }
+  };
+  // The same by one warp.
+  auto work_alone = [&](const Unit& u, int t0, int n) {
+    const int row_tiles = u.J / a.Hkv, h = u.j / row_tiles, row0 = (u.j - h * row_tiles) * kDecRows;
+    begin(u, h, row0);
+    for (int i = 0; i < n; ++i) {
+      wait_tile(owned + 8 * (w * kRing + stage), solo_bits >> stage & 1u);
+      solo_bits ^= 1u << stage;
+      if (!dead) {
+#pragma unroll 1
+        for (int part = 0; part < kDecTile / 16; ++part) block(part);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * stage, kConsumers);
+      next_stage();
+    }
+    sum_l();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = row0 + g + 8 * r;
+      if (row >= u.rows) continue;
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+        put(u, h, row0, row, 8 * q + 2 * c, t0 == 0 && n == u.tiles, t0 == 0, m[r], l[r], o[q][2 * r], o[q][2 * r + 1], q == 0 && c == 0);
     }
   };
 
@@ -568,10 +632,18 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   while (f < E) {
     const int n = min(u.tiles - t, E - f);
     if (n > 0) {
-      const int row_tiles = u.J / a.Hkv, left = u.rows - (u.j % row_tiles) * kDecRows;
-      if (left <= 16) work(std::integral_constant<int, 1>{}, u, t, n);
-      else if (left <= 32) work(std::integral_constant<int, 2>{}, u, t, n);
-      else work(std::integral_constant<int, 4>{}, u, t, n);
+      const int who = owner_of(u, n, parts);
+      if (who < 0) {
+        const int row_tiles = u.J / a.Hkv, left = u.rows - (u.j % row_tiles) * kDecRows;
+        if (left <= 32) work(std::integral_constant<int, 2>{}, u, t, n, who);
+        else work(std::integral_constant<int, 4>{}, u, t, n, who);
+      } else if (who == w) {
+        work_alone(u, t, n);
+      } else if (who == kConsumers + (w >> 2)) {
+        work(std::integral_constant<int, 1>{}, u, t, n, who);
+      } else {
+        stage = (stage + n) % kRing;
+      }
     }
     f += u.tiles + kEndTicks - t;
     t = 0;
