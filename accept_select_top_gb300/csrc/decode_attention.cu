@@ -10,7 +10,7 @@
 // request's own tokens; a unit is (segment, kv head, up to 64 rows).  One CTA a SM takes an equal contiguous
 // range of the 64-key tiles of all units laid end to end.
 //   Four producer warps look up the slots of the keys (two tiles ahead) and copy K and V rows with 16-byte
-// cp.async into a ring of five tiles; they do not care where units end, so the memory stays busy while one does.
+// cp.async into a ring of 160 KB; they do not care where units end, so the memory stays busy while one does.
 //   Eight consumer warps compute on register fragments (mma.sync m16n8k16; rows are few, and a 128-row tcgen05 tile
 // would be padding).  A unit's part of up to 16 rows belongs to four of them, which share each tile's keys (to one, if it
 // is a single tile), and the parts take turns: what the ends of a part take (its Q, the results) is 3 us of latency,
@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kConsumers = 8, kProducers = 4;
 constexpr int kDecThreads = 32 * (kConsumers + kProducers);
-constexpr int kRing = 5;
+constexpr int kRing128 = 5, kRing64 = 10;  // tiles (of D 128, 64) in the ring: 160 KB
 constexpr int kOwners = kConsumers + 2;  // who may have a part to itself: a warp, or four of them
 // A part of at most so many tiles, where the CTA's range is so many times longer, goes to one warp.
 constexpr int kSoloTiles = 1, kSoloRange = 2;
@@ -41,18 +41,19 @@ constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wa
 
 template <int D>
 struct DecSmem {
+  static constexpr int kRing = D == 128 ? kRing128 : kRing64;
   static constexpr int kRow = 2 * D;               // bytes of a K (or V) row
   static constexpr int kHalf = kDecTile * kRow;    // K of a tile
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kMerge = kRing * kStage;    // [warp][8 column tiles][32 lanes] float4
   static constexpr int kMl = kMerge + kConsumers * 8 * 32 * 16;  // [warp][16] (m, l)
   static constexpr int kMask = kMl + kConsumers * 16 * 8;        // [stage][4] keys that count, 16 bits each
-  static constexpr int kBars = kMask + kRing * 4 * 4;            // full[5], empty[5], then [owner][5]
+  static constexpr int kBars = kMask + kRing * 4 * 4;            // full[ring], empty[ring], then [owner][ring]
   static constexpr int kAbort = kBars + (2 + kOwners) * kRing * 8;
   static constexpr int kScan = kAbort + 16;        // pre [groups + b + 1], len [b], base [b]
   static size_t bytes(int b, int groups) { return size_t(kScan) + 4u * size_t(groups + 3 * b + 1); }
 };
-static_assert(DecSmem<128>::kScan + 4 * (4 * kDecodeMaxB + 1) + 256 <= 227 * 1024, "shared memory of one CTA");
+static_assert(DecSmem<128>::kScan + 4 * (4 * kDecodeMaxB + 1) + 256 <= 227 * 1024 && DecSmem<64>::kScan + 4 * (4 * kDecodeMaxB + 1) + 256 <= 227 * 1024, "shared memory of one CTA");
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
@@ -119,7 +120,7 @@ template <int D>
 __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const __grid_constant__ DecodeArgs args) {
   using L = DecSmem<D>;
   constexpr unsigned FULL = 0xffffffffu;
-  constexpr int NT = D / 8;
+  constexpr int NT = D / 8, kRing = L::kRing;
   const DecodeParams& a = args.p;
   extern __shared__ __align__(128) unsigned char smem[];
   const int ng = a.num_groups, G = a.Hq / a.Hkv;
@@ -293,14 +294,19 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     constexpr int kChunks = D / 8;              // 16-byte chunks of a row
     constexpr int kKeys = 32 / kChunks;         // rows that a warp's copy spans
     const int cx = lane % kChunks, ck = lane / kChunks;
-    const size_t slot_bytes = size_t(a.Hkv) * L::kRow;
+    const uint32_t slot_bytes = uint32_t(a.Hkv) * L::kRow;
+    const unsigned char* const k0 = static_cast<const unsigned char*>(a.k_pool) + cx * 16;
+    const long long to_v = static_cast<const unsigned char*>(a.v_pool) - static_cast<const unsigned char*>(a.k_pool);
+    const uint32_t ring0 = smem_u32(smem) + (16 * p + ck) * L::kRow;
+    const uint32_t kdst = (cx ^ (4 * (ck & 1))) * 16, page_mask = (1u << args.shift) - 1u;
     Unit u;
     int t, f = S;
     locate(f, u, t);
-    // The next tile of the range, its kv head (-1: none is left) and its owner (-1: all warps);
-    // lanes of this half of the warp look up their key's page id.
-    int x_pos = -1, x_id = -1, owner = -1;
+    // What look() found: of each of two tiles the kv head (-1: none is left) and the owner (-1: all warps); lanes of a half
+    // of the warp hold their key's position (-1: none that counts) and page id.
+    int x_pos = -1, x_id = -1, owner = -1, h_now = 0, x_now = 0, heads[2], owners[2];
     int2 parts = make_int2(0, 0);
+    const int* row_now = nullptr;
     bool entered = false;
     auto look = [&](int half) {
       while (f < E && t >= u.tiles) {  // over a unit's end
@@ -309,55 +315,65 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
         entered = false;
         if (f < E) next_unit(u);
       }
-      if (f >= E) return make_int2(-1, -1);
+      heads[half] = -1;
+      if (f >= E) return;
       if (!entered) {
         entered = true;
         owner = owner_of(u, min(u.tiles - t, E - f), parts);
+        h_now = u.j / (u.J / a.Hkv);
+        row_now = a.page_table + (long long)__ldg(a.req_pool_idx + u.r0) * a.row_pages;
+        x_now = (u.first / kDecTile + t) * kDecTile + 16 * p + (lane & 15);
       }
-      const int row_tiles = u.J / a.Hkv, h = u.j / row_tiles;
+      heads[half] = h_now;
+      owners[half] = owner;
       if ((lane >> 4) == half) {
-        const int x = (u.first / kDecTile + t) * kDecTile + 16 * p + (lane & 15);
-        x_pos = x_id = -1;
-        if (x >= u.first && x < u.last) {
-          x_pos = x;
-          x_id = __ldg(a.page_table + (long long)__ldg(a.req_pool_idx + u.r0) * a.row_pages + (x >> args.shift));
+        x_pos = -1;
+        if (x_now >= u.first && x_now < u.last) {
+          x_pos = x_now;
+          x_id = __ldg(row_now + (x_now >> args.shift));
         }
       }
+      x_now += kDecTile;
       ++f;
       ++t;
-      return make_int2(h, owner);
     };
     int stage = 0;
     uint32_t phase = 1;  // (an empty ring)
     bool dead = false;
-    int2 heads[2];
-    heads[0] = look(0);
-    heads[1] = heads[0].x >= 0 ? look(1) : make_int2(-1, -1);
-    while (heads[0].x >= 0 && !dead) {
-      const int2 h0 = heads[0], h1 = heads[1];
-      int slot = -1;
-      if (x_pos >= 0) {
-        if (x_id < 0 || x_id >= a.num_pages) raise_error(a.error, SPEC_DEV_INDEX);
-        else slot = (x_id << args.shift) + (x_pos & ((1 << args.shift) - 1));
+    heads[1] = -1;
+    look(0);
+    if (heads[0] >= 0) look(1);
+    while (heads[0] >= 0 && !dead) {
+      const int h1 = heads[1];
+      int slot = 0;
+      bool counts = x_pos >= 0;
+      if (counts) {
+        if (uint32_t(x_id) >= uint32_t(a.num_pages)) {
+          raise_error(a.error, SPEC_DEV_INDEX);
+          counts = false;
+        } else {
+          slot = (x_id << args.shift) + int(uint32_t(x_pos) & page_mask);
+        }
       }
-      const unsigned valid = __ballot_sync(FULL, slot >= 0);
+      const unsigned valid = __ballot_sync(FULL, counts);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int h = half ? h1.x : h0.x, who = half ? h1.y : h0.y;
+        const int h = half ? h1 : heads[0], who = owners[half];
         if (h < 0 || dead) break;
         if (__any_sync(FULL, !mbar_wait(empty + 8 * stage, phase, abort_flag))) {
           dead = true;
           break;
         }
-        const uint32_t st = smem_u32(smem + stage * L::kStage) + 16 * p * L::kRow;
+        const uint32_t st = ring0 + stage * L::kStage;
+        const unsigned char* const from = k0 + uint32_t(h) * uint32_t(L::kRow);
+        const unsigned mine = valid >> (half * 16 + ck);
 #pragma unroll
         for (int i = 0; i < 16 / kKeys; ++i) {
-          const int key = i * kKeys + ck;
-          const int s = __shfl_sync(FULL, slot, half * 16 + key);
-          const uint32_t n = s >= 0 ? 16u : 0u;  // (a key that does not count reads as zeros)
-          const size_t at = size_t(s >= 0 ? s : 0) * slot_bytes + size_t(h) * L::kRow + cx * 16;
-          cp16(st + key * L::kRow + (cx ^ (4 * (key & 1))) * 16, static_cast<const unsigned char*>(a.k_pool) + at, n);
-          cp16(st + L::kHalf + key * L::kRow + (cx ^ (key & 7)) * 16, static_cast<const unsigned char*>(a.v_pool) + at, n);
+          const unsigned char* src = from + (unsigned long long)uint32_t(__shfl_sync(FULL, slot, half * 16 + i * kKeys + ck)) * slot_bytes;
+          const uint32_t n = (mine >> (i * kKeys) & 1u) * 16u;  // (a key that does not count reads as zeros)
+          const uint32_t to = st + i * kKeys * L::kRow;
+          cp16(to + kdst, src, n);
+          cp16(to + L::kHalf + (cx ^ ((i * kKeys + ck) & 7)) * 16, src + to_v, n);
         }
         const uint32_t tell = who < 0 ? full + 8 * stage : owned + 8 * (who * kRing + stage);
         if (lane == 0) {
@@ -369,10 +385,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
           stage = 0;
           phase ^= 1;
         }
-        if (half == 0) heads[0] = look(0);
+        // (the other half's next tile is looked up once both of this window have been copied)
+        if (half == 0) look(0);
       }
-      // (the other half's next tile follows, once both of this window have been copied)
-      heads[1] = !dead && h1.x >= 0 && heads[0].x >= 0 ? look(1) : make_int2(-1, -1);
+      const bool had = h1 >= 0 && heads[0] >= 0 && !dead;
+      heads[1] = -1;
+      if (had) look(1);
     }
     if (dead && lane == 0) {
       raise_error(a.error, SPEC_DEV_TIMEOUT);
@@ -529,11 +547,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
       *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * D + col) = dec_pack(s0 * inv, s1 * inv);
       if (note && a.lse) a.lse[orow] = dec_lse(M, Ls);
     } else {
-      const size_t frow = whole ? orow : size_t(2 * blockIdx.x + (begun ? 1 : 0)) * kDecRows + row - row0;
-      float* fo = whole ? (own ? args.own_o : args.shared_o) : args.frag_o;
-      float2* fm = whole ? (own ? args.own_ml : args.shared_ml) : args.frag_ml;
-      *reinterpret_cast<float2*>(fo + frow * D + col) = make_float2(s0, s1);
-      if (note) fm[frow] = make_float2(M, Ls);
+      const size_t first = whole ? size_t(u.r0) * a.Hq + size_t(h) * u.rows + row0 : size_t(2 * blockIdx.x + (begun ? 1 : 0)) * kDecRows;
+      const int step = whole ? min(kDecRows, u.rows - row0) : kDecRows;
+      float* fo = reinterpret_cast<float*>((whole ? (own ? args.own_o : args.shared_o) : args.frag_o) + first * (D / 4));
+      *reinterpret_cast<float2*>(fo + 4 * ((col >> 2) * step + row - row0) + (col & 3)) = make_float2(s0, s1);
+      if (note) (whole ? (own ? args.own_ml : args.shared_ml) : args.frag_ml)[first + row - row0] = make_float2(M, Ls);
     }
   };
 
@@ -652,143 +670,116 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   if (args.tall) pdl_wait();
 }
 
-// Joins the partial results of a row: a warp an output row, E neighbouring columns a lane.
-constexpr int kJoinWarps = 8;
+// Joins the partial results: a thread a word of four columns of a row.  The rows of a group come in the order of its units,
+// (kv head, member, q head), so that the words of neighbouring threads lie side by side.
+constexpr int kJoinThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __grid_constant__ DecodeArgs args) {
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeArgs args) {
   pdl_wait();
   pdl_trigger();
   const DecodeParams& a = args.p;
-  constexpr int E = D / 32;
-  constexpr unsigned FULL = 0xffffffffu;
-  const int lane = threadIdx.x & 31, orow = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (orow >= a.b * a.Hq) return;
-  const int r = orow / a.Hq, head = orow - r * a.Hq, G = a.Hq / a.Hkv, h = head / G, i = head - h * G;
-  const int4 plan = __ldcg(args.plan);
-  const int base = __ldcg(args.base + r);
-  // The parts of a unit: CTAs [wa, wb], or one whole.
-  struct Unit1 {
+  constexpr int kRows = kJoinThreads / (D / 4);  // rows of a block
+  const int c = threadIdx.x / kRows, at = blockIdx.x * kRows + threadIdx.x % kRows, total = a.b * a.Hq, G = a.Hq / a.Hkv;
+  if (at >= total) return;
+  const int4 plan = __ldcg(args.plan), tall_plan = args.tall ? __ldcg(args.tall_plan) : make_int4(0, 0, 0, 0);
+  int r = at / a.Hq, head = at - r * a.Hq;
+  const int2 mem0 = __ldcg(args.member + r);
+  int r0 = r, all = G;
+  if (mem0.x >= 0) {
+    r0 = r - mem0.y;
+    all = (__ldg(a.group_start + mem0.x + 1) - r0) * G;
+    const int rem = at - r0 * a.Hq, hh = rem / all, x = rem - hh * all, f = x / G;
+    r = r0 + f;
+    head = hh * G + x - f * G;
+  }
+  const int h = head / G, i = head - h * G, x = (r - r0) * G + i, base = __ldcg(args.base + r);
+  const size_t orow = size_t(r) * a.Hq + head;
+  // The CTAs on a unit, the j-th of a segment of so many: [wa, wb].
+  struct Span {
     int wa, wb;
-    __device__ bool cut() const { return wa != wb; }
   };
-  auto unit = [&](const int4& pl, const int* pre, int seg, int units, int j, int end) {
+  auto span = [&](const int4& pl, const int* pre, int seg, int units, int j, int end) {
     const int p0 = __ldcg(pre + seg), n = (__ldcg(pre + seg + 1) - p0) / units, u0 = p0 + j * n;
     const long long T = pl.x, ctas = pl.y;
-    return Unit1{int(((long long)(u0 + 1) * ctas - 1) / T), int(((long long)(u0 + n - end) * ctas - 1) / T)};
+    return Span{int(((long long)(u0 + 1) * ctas - 1) / T), int(((long long)(u0 + n - end) * ctas - 1) / T)};
   };
-  const Unit1 own = unit(plan, args.pre, plan.z + r, a.Hkv * args.own_tiles, h * args.own_tiles + i / kDecRows, kEndTicks);
-  if (!own.cut() && base == 0) return;  // (already in out)
+  const int own0 = i / kDecRows * kDecRows;
+  const Span own = span(plan, args.pre, plan.z + r, a.Hkv * args.own_tiles, h * args.own_tiles + i / kDecRows, kEndTicks);
+  const bool done = own.wa == own.wb && base == 0;  // (already in out)
+  if (done) return;
   const int n_own = own.wb - own.wa + 1;
-  // what the request shares: in the first kernel's fragments, or the tcgen05 kernel's
-  Unit1 sh{0, 0};
-  int n_sh = 0, x = 0, rows = 0, xr = 0;
-  bool tall = false, split = false;
-  size_t unit0 = 0;
+  int n_sh = 0;
+  // what the request shares: the first kernel's partial results, or the tcgen05 kernel's
+  Span sh{0, 0};
+  const bool tall = args.tall && all > kDecFlatRows;
+  const int size = tall ? kDecTallRows : kDecRows, x0 = x / size * size, rows = min(size, all - x0), xr = x - x0;
+  const bool split = tall && rows <= 128;
   if (base > 0) {
-    const int2 mem = __ldcg(args.member + r);
-    const int r0 = r - mem.y, all = (__ldg(a.group_start + mem.x + 1) - r0) * G;
-    x = mem.y * G + i;
-    tall = args.tall && all > kDecFlatRows;
-    if (tall) {
-      const int blocks = (all + kDecTallRows - 1) / kDecTallRows, blk = x / kDecTallRows;
-      rows = min(kDecTallRows, all - blk * kDecTallRows);
-      xr = x - blk * kDecTallRows;
-      split = rows <= 128;
-      unit0 = size_t(r0) * a.Hq + size_t(h) * all + size_t(blk) * kDecTallRows;
-      sh = unit(__ldcg(args.tall_plan), args.tall_pre, mem.x, a.Hkv * blocks, h * blocks + blk, kDecTallEnd);
-      n_sh = (sh.wb - sh.wa + 1) * (split ? 2 : 1);
-    } else {
-      const int tiles = (all + kDecRows - 1) / kDecRows;
-      sh = unit(plan, args.pre, mem.x, a.Hkv * tiles, h * tiles + x / kDecRows, kEndTicks);
-      n_sh = sh.wb - sh.wa + 1;
-    }
+    const int tiles = (all + size - 1) / size;
+    sh = span(tall ? tall_plan : plan, tall ? args.tall_pre : args.pre, mem0.x, a.Hkv * tiles, h * tiles + x / size, tall ? kDecTallEnd : kEndTicks);
+    n_sh = (sh.wb - sh.wa + 1) * (split ? 2 : 1);
   }
-  const int np = n_own + n_sh;
-  // part q: its (m, l), its O (row-major, or words of four columns `step` apart)
-  auto part = [&](int q, const float2*& ml, const float*& o, int& step) {
-    step = 1;
-    const bool mine = q < n_own;
-    if (!mine) q -= n_own;
-    if (!mine && tall) {
-      const int cta = sh.wa + (split ? q >> 1 : q), half = split ? q & 1 : xr >> 7;
-      if (!sh.cut()) {
-        const size_t first = (split ? size_t(half) * a.b * a.Hq : 0) + unit0;
-        ml = args.whole_ml + first + xr;
-        o = reinterpret_cast<const float*>(args.whole_o + first * (D / 4) + xr);
-        step = rows;
-      } else {
-        const size_t slot = (size_t(2) * cta + (cta == sh.wa ? 1 : 0)) * 2 + half;
-        ml = args.tall_ml + slot * 128 + (xr & 127);
-        o = reinterpret_cast<const float*>(args.tall_o + slot * (D / 4) * 128 + (xr & 127));
-        step = 128;
-      }
-      return;
-    }
-    const Unit1& u = mine ? own : sh;
-    const size_t row = u.cut() ? size_t(2 * (u.wa + q) + (q == 0 ? 1 : 0)) * kDecRows + (mine ? i : x) % kDecRows : size_t(orow);
-    ml = (u.cut() ? args.frag_ml : mine ? args.own_ml : args.shared_ml) + row;
-    o = (u.cut() ? args.frag_o : mine ? args.own_o : args.shared_o) + row * D;
+  const size_t sh_first = size_t(r0) * a.Hq + size_t(h) * all + x0;
+  // part q: its (m, l), its first word, and how far its words lie apart
+  struct Part {
+    const float2* ml;
+    const float4* o;
+    int step;
   };
-  float M = -INFINITY, Ls = 0.f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int q0 = 0; q0 < np; q0 += 32) {
-    const float2* ml = nullptr;
-    const float* o = nullptr;
-    int step = 1;
-    float2 v = make_float2(-INFINITY, 0.f);
-    if (q0 + lane < np) {
-      part(q0 + lane, ml, o, step);
-      v = __ldcg(ml);
+  auto part = [&](int q) {
+    if (q < n_own) {
+      const bool cut = own.wa != own.wb;
+      const size_t first = cut ? size_t(2 * (own.wa + q) + (q == 0 ? 1 : 0)) * kDecRows : size_t(r) * a.Hq + h * G + own0;
+      return Part{(cut ? args.frag_ml : args.own_ml) + first + i - own0, (cut ? args.frag_o : args.own_o) + first * (D / 4) + i - own0,
+                  cut ? kDecRows : min(kDecRows, G - own0)};
     }
-    float M2 = v.x;
+    q -= n_own;
+    const bool cut = sh.wa != sh.wb;
+    if (!tall) {
+      const size_t first = cut ? size_t(2 * (sh.wa + q) + (q == 0 ? 1 : 0)) * kDecRows : sh_first;
+      return Part{(cut ? args.frag_ml : args.shared_ml) + first + xr, (cut ? args.frag_o : args.shared_o) + first * (D / 4) + xr, cut ? kDecRows : rows};
+    }
+    const int cta = sh.wa + (split ? q >> 1 : q), half = split ? q & 1 : xr >> 7;
+    const size_t first = cut ? ((size_t(2) * cta + (cta == sh.wa ? 1 : 0)) * 2 + half) * 128 : (split ? size_t(half) * total : 0) + sh_first;
+    const int row = cut ? xr & 127 : xr;
+    return Part{(cut ? args.tall_ml : args.whole_ml) + first + row, (cut ? args.tall_o : args.whole_o) + first * (D / 4) + row, cut ? 128 : rows};
+  };
+  const int np = n_own + n_sh;
+  float M = -INFINITY, Ls = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kOnce = 8;
+#pragma unroll 1
+  for (int q0 = 0; q0 < np; q0 += kOnce) {
+    float2 v[kOnce];
+    float4 y[kOnce];
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) M2 = fmaxf(M2, __shfl_xor_sync(FULL, M2, k));
-    M2 = fmaxf(M2, M);
-    const float was = dec_weight(M, M2), wt = dec_weight(v.x, M2);
-    M = M2;
-    Ls = Ls * was + warp_sum(v.y * wt);
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= was;
-    const int n = min(32, np - q0);
-    constexpr int kOnce = 4;
-    for (int k0 = 0; k0 < n; k0 += kOnce) {
-      float y[kOnce][E], wk[kOnce];
-#pragma unroll
-      for (int k = 0; k < kOnce; ++k) {
-        const int src = k0 + k < n ? k0 + k : 0;
-        wk[k] = k0 + k < n ? __shfl_sync(FULL, wt, src) : 0.f;
-        const float* from = reinterpret_cast<const float*>(__shfl_sync(FULL, reinterpret_cast<unsigned long long>(o), src));
-        const int st = __shfl_sync(FULL, step, src);
-        // (the lane's columns E lane ..: word E lane / 4 of four)
-        from += size_t(E * lane / 4) * 4 * st + E * lane % 4;
-#pragma unroll
-        for (int e = 0; e < E; ++e) y[k][e] = 0.f;
-        if (wk[k] != 0.f) {  // (a part that has seen nothing is not read)
-          if (E == 4) {
-            const float4 z = __ldcg(reinterpret_cast<const float4*>(from));
-            y[k][0] = z.x;
-            y[k][1] = z.y;
-            y[k][E - 2] = z.z;
-            y[k][E - 1] = z.w;
-          } else {
-            const float2 z = __ldcg(reinterpret_cast<const float2*>(from));
-            y[k][0] = z.x;
-            y[k][1] = z.y;
-          }
-        }
+    for (int k = 0; k < kOnce; ++k) {
+      v[k] = make_float2(-INFINITY, 0.f);
+      if (q0 + k < np) {
+        const Part p = part(q0 + k);
+        v[k] = __ldcg(p.ml);
+        y[k] = __ldcg(p.o + size_t(c) * p.step);
       }
+    }
+    float M2 = M;
 #pragma unroll
-      for (int k = 0; k < kOnce; ++k)
+    for (int k = 0; k < kOnce; ++k) M2 = fmaxf(M2, v[k].x);
+    const float was = dec_weight(M, M2);
+    M = M2;
+    Ls *= was;
+    acc = make_float4(acc.x * was, acc.y * was, acc.z * was, acc.w * was);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(y[k][e], wk[k], acc[e]);
+    for (int k = 0; k < kOnce; ++k) {
+      const float wt = dec_weight(v[k].x, M);
+      if (wt == 0.f) continue;  // (a part that has seen nothing may not have been written)
+      Ls = fmaf(v[k].y, wt, Ls);
+      acc = make_float4(fmaf(y[k].x, wt, acc.x), fmaf(y[k].y, wt, acc.y), fmaf(y[k].z, wt, acc.z), fmaf(y[k].w, wt, acc.w));
     }
   }
   const float inv = dec_inverse(Ls);
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + size_t(orow) * D + E * lane);
-  out[0] = dec_pack(acc[0] * inv, acc[1] * inv);
-  if (E == 4) out[E / 2 - 1] = dec_pack(acc[E - 2] * inv, acc[E - 1] * inv);
-  if (lane == 0 && a.lse) a.lse[orow] = dec_lse(M, Ls);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + 4 * c) =
+      make_uint2(dec_pack(acc.x * inv, acc.y * inv), dec_pack(acc.z * inv, acc.w * inv));
+  if (c == 0 && a.lse) a.lse[orow] = dec_lse(M, Ls);
 }
 
 template <int D>
@@ -802,8 +793,9 @@ int launch_decode(const DecodeArgs& args, int sms, cudaStream_t stream) {
   if (args.tall)
     if (const int rc = launch_decode_tall(args, sms, stream)) return rc;
   if (launch_pdl(decode_attention_kernel<D>, dim3(grid), dim3(kDecThreads), smem, stream, args) != cudaSuccess) return SPEC_ERR_LAUNCH;
-  const unsigned blocks = unsigned((size_t(p.b) * p.Hq + kJoinWarps - 1) / kJoinWarps);
-  return launch_pdl(decode_join_kernel<D>, dim3(blocks), dim3(32 * kJoinWarps), 0, stream, args) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+  constexpr int rows = kJoinThreads / (D / 4);
+  const unsigned blocks = unsigned((size_t(p.b) * p.Hq + rows - 1) / rows);
+  return launch_pdl(decode_join_kernel<D>, dim3(blocks), dim3(kJoinThreads), 0, stream, args) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 
 // Offsets of the workspace's parts.
@@ -866,9 +858,9 @@ int launch_decode_attention(const DecodeParams& p, cudaStream_t stream) {
   args.frag_ml = reinterpret_cast<float2*>(ws + at.frag_ml);
   args.own_ml = reinterpret_cast<float2*>(ws + at.own_ml);
   args.shared_ml = reinterpret_cast<float2*>(ws + at.shared_ml);
-  args.frag_o = reinterpret_cast<float*>(ws + at.frag_o);
-  args.own_o = reinterpret_cast<float*>(ws + at.own_o);
-  args.shared_o = reinterpret_cast<float*>(ws + at.shared_o);
+  args.frag_o = reinterpret_cast<float4*>(ws + at.frag_o);
+  args.own_o = reinterpret_cast<float4*>(ws + at.own_o);
+  args.shared_o = reinterpret_cast<float4*>(ws + at.shared_o);
   args.tall = tall;
   args.tall_plan = reinterpret_cast<int4*>(ws + 128);
   args.tall_pre = reinterpret_cast<int*>(ws + at.tall_pre);

@@ -29,7 +29,7 @@ __device__ __forceinline__ float dec_lse(float m, float l) {
 }
 
 // Rows of a group's shared tokens (members times q heads of a kv head) above which the tcgen05 kernel takes them.
-constexpr int kDecFlatRows = 64;
+constexpr int kDecFlatRows = 32;
 constexpr int kDecTallRows = 256;  // query rows of one of its units
 constexpr int kDecTallEnd = 2;     // what a unit's end costs there in the division of the work, in tiles
 
@@ -46,15 +46,18 @@ struct DecodeArgs {
   int* pre;        // [groups + b + 1]
   int* base;       // [b]
   int2* member;    // [b]
-  float2* frag_ml;  // [2 * CTA + i][64], i = 1: the unit that the CTA begins and does not finish
-  float2* own_ml;   // [b * Hq] of units that lie in one CTA
+  // Partial results: (m, l) of each row, and O as words of four columns, [D / 4][rows].  Those of a unit's part:
+  // [2 * CTA + i][..][64], i = 1: the unit that the CTA begins and does not finish.  Those of units that lie in one
+  // CTA: from row r0 * Hq + h * (the segment's rows) + (the unit's first) on, as many rows as the unit has.
+  float2* frag_ml;
+  float2* own_ml;
   float2* shared_ml;
-  float* frag_o;    // [.][D]
-  float* own_o;
-  float* shared_o;
-  // the tcgen05 kernel's (tall 0: it is not launched): plan {ticks, CTAs, -, -}, ticks before each group, fragments
-  // [2 * CTA + i][half][D / 4][128 rows] and units that lie in one CTA, [half][..][D / 4][rows]; halves: rows 128 .., or
-  // every second tile where there are no more than 128
+  float4* frag_o;
+  float4* own_o;
+  float4* shared_o;
+  // the tcgen05 kernel's (tall 0: it is not launched): plan {ticks, CTAs, -, -}, ticks before each group, partial
+  // results [2 * CTA + i][half][..][128], and of units that lie in one CTA, [half] first; halves: rows 128 .., or every
+  // second tile where there are no more than 128
   int tall;
   int4* tall_plan;
   int* tall_pre;

@@ -6,7 +6,7 @@
 // SM takes an equal contiguous range of the 64-key tiles of all units laid end to end.  Warps:
 //   0-3, 4-7  two softmax groups, one query row a thread.  More than 128 rows: group w has rows 128 w .. and both see
 //             every tile; fewer: the groups take turns at the tiles (two partial results).
-//   8-11      copy K and V rows with 16-byte cp.async into a ring of five 128B-swizzled tiles
+//   8-11      copy K and V rows with 16-byte cp.async into a ring of 128B-swizzled tiles
 //   12, 13    issue S = Q K^T (M 128, N 64, K D) of groups 0, 1; 14, 15: O += P V (A = P from TMEM)
 // TMEM: O0 O1 | two S buffers a group; P (bf16, two to a column) takes the place of its S, so that the scores of
 // the next tile are computed, and the products of the last one added up, while a tile's softmax runs.
@@ -24,8 +24,7 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kTallThreads = 16 * 32;
-constexpr int kStages = 5;
-constexpr int kLag = 2;  // tiles whose copies are in flight behind the one being issued
+constexpr int kMostStages = 10;
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wait
 constexpr float kSumMost = 5.9604644775390625e-08f;  // 2^-24
 __host__ __device__ constexpr uint32_t col_o(int w) { return 128u * uint32_t(w); }
@@ -33,6 +32,8 @@ __host__ __device__ constexpr uint32_t col_s(int w, int b) { return 256u + 128u 
 
 template <int D>
 struct TallSmem {
+  static constexpr int kStages = D == 128 ? 5 : 10;  // tiles in the ring
+  static constexpr int kLag = D == 128 ? 2 : 5;      // tiles whose copies are in flight behind the one being issued
   static constexpr int kQBlock = kRows * 128;       // [128 rows x 64 bf16], 128B-swizzled
   static constexpr int kQTile = (D / 64) * kQBlock;
   static constexpr int kBlock = kDecTile * 128;     // [64 keys x 64 bf16]
@@ -40,7 +41,7 @@ struct TallSmem {
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kRing = 2 * kQTile;
   static constexpr int kBars = kRing + kStages * kStage;
-  static constexpr int kNumBars = 2 * kStages + 2 + 2 + 4 + 4 + 4 + 4;
+  static constexpr int kNumBars = 2 * kMostStages + 2 + 2 + 4 + 4 + 4 + 4;
   static constexpr int kMask = kBars + 8 * kNumBars;   // [stage][4] keys that count, 16 bits each
   static constexpr int kWords = kMask + kStages * 16;  // TMEM address, abort flag, bad flag, ticks, then a word a warp
   static constexpr int kBytes = kWords + 16 + 4 * (kTallThreads / 32);
@@ -51,8 +52,8 @@ static_assert(TallSmem<128>::kBytes + 1024 <= 227 * 1024, "shared memory of one 
 
 enum {
   kFull0 = 0,              // + stage: the tile's copies have landed
-  kEmpty0 = kStages,       // + stage: the products that read it are complete (one arrival a group)
-  kQFull0 = 2 * kStages,   // + group
+  kEmpty0 = kMostStages,   // + stage: the products that read it are complete (one arrival a group)
+  kQFull0 = 2 * kMostStages,  // + group
   kOFree0 = kQFull0 + 2,   // + group: the epilogue has read O
   kSFull0 = kOFree0 + 2,   // + 2 group + S buffer
   kPReady0 = kSFull0 + 4,
@@ -210,6 +211,7 @@ template <int D>
 __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(const __grid_constant__ DecodeArgs args) {
   using L = TallSmem<D>;
   constexpr unsigned FULL = 0xffffffffu;
+  constexpr int kStages = L::kStages, kLag = L::kLag;
   const DecodeParams& a = args.p;
   const int G = a.Hq / a.Hkv, ng = a.num_groups;
   const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
@@ -426,59 +428,74 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
     constexpr int kChunks = D / 8;       // 16-byte chunks of a row
     constexpr int kKeys = 32 / kChunks;  // rows that a warp's copy spans
     const int cx = lane % kChunks, ck = lane / kChunks;
-    const size_t slot_bytes = size_t(a.Hkv) * D * 2;
+    const uint32_t slot_bytes = uint32_t(a.Hkv) * D * 2u, page_mask = (1u << args.shift) - 1u;
+    const unsigned char* const k0 = static_cast<const unsigned char*>(a.k_pool) + cx * 16;
+    const long long to_v = static_cast<const unsigned char*>(a.v_pool) - static_cast<const unsigned char*>(a.k_pool);
+    const uint32_t ring0 = sbase + uint32_t(L::kRing) + uint32_t(cx >> 3) * L::kBlock + uint32_t(16 * c + ck) * 128u;
     Place p = start;
     int f = S, n = piece(p, f), i = 0;
-    // The next tile of the range, its kv head (-1: none is left); lanes of this half of the warp look up their key's
-    // page id.
-    int x_pos = -1, x_id = -1;
+    // What look() found: of each of two tiles the kv head (-1: none is left); lanes of a half of the warp hold their
+    // key's position (-1: none that counts) and page id.
+    int x_pos = -1, x_id = -1, h_now = 0, x_now = 0, heads[2];
+    const int* row_now = nullptr;
     auto look = [&](int half) {
       if (i == n) {
         over(p, f, n);
         n = piece(p, f);
         i = 0;
       }
-      if (n == 0) return -1;
+      heads[half] = -1;
+      if (n == 0) return;
+      if (i == 0) {
+        h_now = p.j / p.blocks;
+        row_now = a.page_table + (long long)__ldg(a.req_pool_idx + p.r0) * a.row_pages;
+        x_now = p.t * kDecTile + 16 * c + (lane & 15);
+      }
+      heads[half] = h_now;
       if ((lane >> 4) == half) {
-        const int x = (p.t + i) * kDecTile + 16 * c + (lane & 15);
-        x_pos = x_id = -1;
-        if (x < p.shared) {
-          x_pos = x;
-          x_id = __ldg(a.page_table + (long long)__ldg(a.req_pool_idx + p.r0) * a.row_pages + (x >> args.shift));
+        x_pos = -1;
+        if (x_now < p.shared) {
+          x_pos = x_now;
+          x_id = __ldg(row_now + (x_now >> args.shift));
         }
       }
+      x_now += kDecTile;
       ++i;
-      return p.j / p.blocks;
     };
     int stage = 0, ph = 1, issued = 0, told = 0, told_stage = 0;
     bool ok = true;
-    int heads[2];
-    heads[0] = look(0);
-    heads[1] = heads[0] >= 0 ? look(1) : -1;
+    heads[1] = -1;
+    look(0);
+    if (heads[0] >= 0) look(1);
     while (ok && heads[0] >= 0) {
       const int h1 = heads[1];
-      int slot = -1;
-      if (x_pos >= 0) {
-        if (x_id < 0 || x_id >= a.num_pages) raise_error(a.error, SPEC_DEV_INDEX);
-        else slot = (x_id << args.shift) + (x_pos & ((1 << args.shift) - 1));
+      int slot = 0;
+      bool counts = x_pos >= 0;
+      if (counts) {
+        if (uint32_t(x_id) >= uint32_t(a.num_pages)) {
+          raise_error(a.error, SPEC_DEV_INDEX);
+          counts = false;
+        } else {
+          slot = (x_id << args.shift) + int(uint32_t(x_pos) & page_mask);
+        }
       }
-      const unsigned valid = __ballot_sync(FULL, slot >= 0);
+      const unsigned valid = __ballot_sync(FULL, counts);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int h = half ? h1 : heads[0];
         if (h < 0 || !ok) break;
         ok = __all_sync(FULL, mbar_wait(bar(kEmpty0 + stage), uint32_t(ph), abort_flag)) != 0;
         if (!ok) break;
-        const uint32_t st = sbase + uint32_t(L::kRing) + uint32_t(stage) * L::kStage + uint32_t(cx >> 3) * L::kBlock;
+        const uint32_t st = ring0 + uint32_t(stage) * L::kStage;
+        const unsigned char* const from = k0 + uint32_t(h) * uint32_t(D) * 2u;
+        const unsigned mine = valid >> (half * 16 + ck);
 #pragma unroll
         for (int q = 0; q < 16 / kKeys; ++q) {
-          const int key = 16 * c + q * kKeys + ck;
-          const int s = __shfl_sync(FULL, slot, half * 16 + q * kKeys + ck);
-          const uint32_t bytes = s >= 0 ? 16u : 0u;  // (a key that does not count reads as zeros)
-          const size_t at = size_t(s >= 0 ? s : 0) * slot_bytes + size_t(h) * D * 2 + cx * 16;
-          const uint32_t to = st + uint32_t(key) * 128u + ((uint32_t(cx & 7) ^ uint32_t(key & 7)) << 4);
-          cp16(to, static_cast<const unsigned char*>(a.k_pool) + at, bytes);
-          cp16(to + L::kHalf, static_cast<const unsigned char*>(a.v_pool) + at, bytes);
+          const unsigned char* src = from + (unsigned long long)uint32_t(__shfl_sync(FULL, slot, half * 16 + q * kKeys + ck)) * slot_bytes;
+          const uint32_t bytes = (mine >> (q * kKeys) & 1u) * 16u;  // (a key that does not count reads as zeros)
+          const uint32_t to = st + uint32_t(q * kKeys) * 128u + ((uint32_t(cx & 7) ^ uint32_t((q * kKeys + ck) & 7)) << 4);
+          cp16(to, src, bytes);
+          cp16(to + L::kHalf, src + to_v, bytes);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (lane == 0) masks[stage * 4 + c] = (valid >> (16 * half)) & 0xffffu;
@@ -494,9 +511,12 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
           stage = 0;
           ph ^= 1;
         }
-        if (half == 0) heads[0] = look(0);
+        // (the other half's next tile is looked up once both of this window have been copied)
+        if (half == 0) look(0);
       }
-      heads[1] = ok && h1 >= 0 && heads[0] >= 0 ? look(1) : -1;
+      const bool had = ok && h1 >= 0 && heads[0] >= 0;
+      heads[1] = -1;
+      if (had) look(1);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     fence_async();
