@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kConsumers = 8, kProducers = 4;
 constexpr int kDecThreads = 32 * (kConsumers + kProducers);
-constexpr int kRing128 = 5, kRing64 = 10;  // tiles (of D 128, 64) in the ring: 160 KB
+constexpr int kRing = 5;
 constexpr int kOwners = kConsumers + 2;  // who may have a part to itself: a warp, or four of them
 // A part of at most so many tiles, where the CTA's range is so many times longer, goes to one warp.
 constexpr int kSoloTiles = 1, kSoloRange = 2;
@@ -41,14 +41,16 @@ constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wa
 
 template <int D>
 struct DecSmem {
-  static constexpr int kRing = D == 128 ? kRing128 : kRing64;
   static constexpr int kRow = 2 * D;               // bytes of a K (or V) row
-  static constexpr int kHalf = kDecTile * kRow;    // K of a tile
+  // Keys of a tile: 32 KB of K and V.  (Tiles of 64 keys for D 64, too, bounded it by what a tile costs besides its
+  // bytes: 256 requests of 2048 tokens, 4 kv heads, 112 us, so 99.)
+  static constexpr int kTile = 64 * 128 / D;
+  static constexpr int kHalf = kTile * kRow;       // K of a tile
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kMerge = kRing * kStage;    // [warp][8 column tiles][32 lanes] float4
   static constexpr int kMl = kMerge + kConsumers * 8 * 32 * 16;  // [warp][16] (m, l)
-  static constexpr int kMask = kMl + kConsumers * 16 * 8;        // [stage][4] keys that count, 16 bits each
-  static constexpr int kBars = kMask + kRing * 4 * 4;            // full[ring], empty[ring], then [owner][ring]
+  static constexpr int kMask = kMl + kConsumers * 16 * 8;        // [stage][4] keys that count, of a quarter of the tile each
+  static constexpr int kBars = kMask + kRing * 4 * 4;            // full[5], empty[5], then [owner][5]
   static constexpr int kAbort = kBars + (2 + kOwners) * kRing * 8;
   static constexpr int kScan = kAbort + 16;        // pre [groups + b + 1], len [b], base [b]
   static size_t bytes(int b, int groups) { return size_t(kScan) + 4u * size_t(groups + 3 * b + 1); }
@@ -120,7 +122,7 @@ template <int D>
 __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const __grid_constant__ DecodeArgs args) {
   using L = DecSmem<D>;
   constexpr unsigned FULL = 0xffffffffu;
-  constexpr int NT = D / 8, kRing = L::kRing;
+  constexpr int NT = D / 8, kTile = L::kTile;
   const DecodeParams& a = args.p;
   extern __shared__ __align__(128) unsigned char smem[];
   const int ng = a.num_groups, G = a.Hq / a.Hkv;
@@ -199,10 +201,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     if (s < ng) {
       const int first = grouped ? sgroup[s] : 0, rows = grouped ? (sgroup[s + 1] - first) * G : 0;
       const bool here = rows > 0 && !(args.tall && rows > kDecFlatRows);  // (else it is the tcgen05 kernel's)
-      const int tiles = here ? (sbase[first] + kDecTile - 1) / kDecTile : 0;
+      const int tiles = here ? (sbase[first] + kTile - 1) / kTile : 0;
       return tiles ? a.Hkv * ((rows + kDecRows - 1) / kDecRows) * (tiles + kEndTicks) : 0;
     }
-    const int r = s - ng, n = (slen[r] + kDecTile - 1) / kDecTile - sbase[r] / kDecTile;
+    const int r = s - ng, n = (slen[r] + kTile - 1) / kTile - sbase[r] / kTile;
     return a.Hkv * args.own_tiles * ((n < 1 ? 1 : n) + kEndTicks);
   };
   {
@@ -293,18 +295,19 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     const int p = w - kConsumers;
     constexpr int kChunks = D / 8;              // 16-byte chunks of a row
     constexpr int kKeys = 32 / kChunks;         // rows that a warp's copy spans
+    constexpr int kMine = kTile / kProducers;   // keys of a tile that the warp copies
     const int cx = lane % kChunks, ck = lane / kChunks;
     const uint32_t slot_bytes = uint32_t(a.Hkv) * L::kRow;
     const unsigned char* const k0 = static_cast<const unsigned char*>(a.k_pool) + cx * 16;
     const long long to_v = static_cast<const unsigned char*>(a.v_pool) - static_cast<const unsigned char*>(a.k_pool);
-    const uint32_t ring0 = smem_u32(smem) + (16 * p + ck) * L::kRow;
+    const uint32_t ring0 = smem_u32(smem) + (kMine * p + ck) * L::kRow;
     const uint32_t kdst = (cx ^ (4 * (ck & 1))) * 16, page_mask = (1u << args.shift) - 1u;
     Unit u;
     int t, f = S;
     locate(f, u, t);
-    // What look() found: of each of two tiles the kv head (-1: none is left) and the owner (-1: all warps); lanes of a half
-    // of the warp hold their key's position (-1: none that counts) and page id.
-    int x_pos = -1, x_id = -1, owner = -1, h_now = 0, x_now = 0, heads[2], owners[2];
+    // What look() found: of each of two tiles the kv head (-1: none is left), the owner (-1: all warps), and the lane's key's
+    // position (-1: none that counts) and page id.
+    int x_pos[2] = {-1, -1}, x_id[2] = {-1, -1}, owner = -1, h_now = 0, x_now = 0, heads[2], owners[2];
     int2 parts = make_int2(0, 0);
     const int* row_now = nullptr;
     bool entered = false;
@@ -322,18 +325,16 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
         owner = owner_of(u, min(u.tiles - t, E - f), parts);
         h_now = u.j / (u.J / a.Hkv);
         row_now = a.page_table + (long long)__ldg(a.req_pool_idx + u.r0) * a.row_pages;
-        x_now = (u.first / kDecTile + t) * kDecTile + 16 * p + (lane & 15);
+        x_now = (u.first / kTile + t) * kTile + kMine * p + lane;
       }
       heads[half] = h_now;
       owners[half] = owner;
-      if ((lane >> 4) == half) {
-        x_pos = -1;
-        if (x_now >= u.first && x_now < u.last) {
-          x_pos = x_now;
-          x_id = __ldg(row_now + (x_now >> args.shift));
-        }
+      x_pos[half] = -1;
+      if (lane < kMine && x_now >= u.first && x_now < u.last) {
+        x_pos[half] = x_now;
+        x_id[half] = __ldg(row_now + (x_now >> args.shift));
       }
-      x_now += kDecTile;
+      x_now += kTile;
       ++f;
       ++t;
     };
@@ -345,20 +346,26 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     if (heads[0] >= 0) look(1);
     while (heads[0] >= 0 && !dead) {
       const int h1 = heads[1];
-      int slot = 0;
-      bool counts = x_pos >= 0;
-      if (counts) {
-        if (uint32_t(x_id) >= uint32_t(a.num_pages)) {
-          raise_error(a.error, SPEC_DEV_INDEX);
-          counts = false;
-        } else {
-          slot = (x_id << args.shift) + int(uint32_t(x_pos) & page_mask);
-        }
-      }
-      const unsigned valid = __ballot_sync(FULL, counts);
+      int slots[2];
+      unsigned valids[2];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int h = half ? h1 : heads[0], who = owners[half];
+        slots[half] = 0;
+        bool counts = x_pos[half] >= 0;
+        if (counts) {
+          if (uint32_t(x_id[half]) >= uint32_t(a.num_pages)) {
+            raise_error(a.error, SPEC_DEV_INDEX);
+            counts = false;
+          } else {
+            slots[half] = (x_id[half] << args.shift) + int(uint32_t(x_pos[half]) & page_mask);
+          }
+        }
+        valids[half] = __ballot_sync(FULL, counts);
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int h = half ? h1 : heads[0], who = owners[half], slot = slots[half];
+        const unsigned valid = valids[half];
         if (h < 0 || dead) break;
         if (__any_sync(FULL, !mbar_wait(empty + 8 * stage, phase, abort_flag))) {
           dead = true;
@@ -366,10 +373,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
         }
         const uint32_t st = ring0 + stage * L::kStage;
         const unsigned char* const from = k0 + uint32_t(h) * uint32_t(L::kRow);
-        const unsigned mine = valid >> (half * 16 + ck);
+        const unsigned mine = valid >> ck;
 #pragma unroll
-        for (int i = 0; i < 16 / kKeys; ++i) {
-          const unsigned char* src = from + (unsigned long long)uint32_t(__shfl_sync(FULL, slot, half * 16 + i * kKeys + ck)) * slot_bytes;
+        for (int i = 0; i < kMine / kKeys; ++i) {
+          const unsigned char* src = from + (unsigned long long)uint32_t(__shfl_sync(FULL, slot, i * kKeys + ck)) * slot_bytes;
           const uint32_t n = (mine >> (i * kKeys) & 1u) * 16u;  // (a key that does not count reads as zeros)
           const uint32_t to = st + i * kKeys * L::kRow;
           cp16(to + kdst, src, n);
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
         }
         const uint32_t tell = who < 0 ? full + 8 * stage : owned + 8 * (who * kRing + stage);
         if (lane == 0) {
-          reinterpret_cast<volatile uint32_t*>(smem + L::kMask)[stage * 4 + p] = (valid >> (16 * half)) & 0xffffu;
+          reinterpret_cast<volatile uint32_t*>(smem + L::kMask)[stage * 4 + p] = valid;
           mbar_arrive(tell);
         }
         mbar_arrive_copies(tell);
@@ -385,7 +392,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
           stage = 0;
           phase ^= 1;
         }
-        // (the other half's next tile is looked up once both of this window have been copied)
         if (half == 0) look(0);
       }
       const bool had = h1 >= 0 && heads[0] >= 0 && !dead;
@@ -446,53 +452,58 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[q][i] = 0.f;
   };
-  // 16 keys of the tile in `stage`
+  // Keys [16 NB part, 16 NB (part + 1)) of the tile in `stage`.
+  constexpr int NB = kTile / 64;
   auto block = [&](int part) {
     const uint32_t st = smem_u32(smem + stage * L::kStage);
+    constexpr uint32_t kAll = NB == 2 ? 0xffffffffu : 0xffffu;
     const uint32_t mask = reinterpret_cast<volatile uint32_t*>(smem + L::kMask)[stage * 4 + part];
     if (mask == 0) return;
-    float s[2][4];
+    float s[2 * NB][4];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < 2 * NB; ++q)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[q][e] = 0.f;
-      const uint32_t row = st + (16 * part + 8 * q + g) * L::kRow;
+    const uint32_t krow = st + (16 * NB * part + g) * L::kRow;
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        const uint4 y = lds16(row + ((4 * k + c) ^ (4 * (g & 1))) * 16);
+    for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+      for (int q = 0; q < 2 * NB; ++q) {
+        const uint4 y = lds16(krow + 8 * q * L::kRow + ((4 * k + c) ^ (4 * (g & 1))) * 16);
         mma_bf16(s[q], qf[2 * k], y.x, y.y);
         mma_bf16(s[q], qf[2 * k + 1], y.z, y.w);
       }
-    }
-    auto masked = [&](float (&v)[2][4]) {
-      if (mask != 0xffffu) {
+    auto masked = [&](float (&v)[2 * NB][4]) {
+      if (mask != kAll) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < 2 * NB; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (!(mask >> (8 * q + 2 * c + (e & 1)) & 1)) v[q][e] = -INFINITY;
       }
     };
     // y = x - m; a row without a reference has y = inf (NaN where x is -inf)
-    float y[2][4], top = -INFINITY;
+    float y[2 * NB][4], top = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int q = 0; q < 2 * NB; ++q)
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[q][e] = fmaf(s[q][e], xf, -m[e >> 1]);
     masked(y);
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int q = 0; q < 2 * NB; ++q)
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = fmaxf(top, y[q][e]);
     if (__any_sync(FULL, top > kDecBase + kDecLazy || m[0] == -INFINITY || m[1] == -INFINITY)) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int q = 0; q < 2 * NB; ++q)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[q][e] *= xf;
       masked(s);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+        float mx = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 2 * NB; ++q) mx = fmaxf(mx, fmaxf(s[q][2 * r], s[q][2 * r + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
         const float ref = mx - kDecBase;
@@ -508,26 +519,29 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
         }
       }
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int q = 0; q < 2 * NB; ++q)
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[q][e] = s[q][e] - (m[e >> 1] == -INFINITY ? 0.f : m[e >> 1]);
     }
-    uint32_t pa[4];
+    uint32_t pa[NB][4];
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int q = 0; q < 2 * NB; ++q)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float p0 = fast_exp2(y[q][2 * r]), p1 = fast_exp2(y[q][2 * r + 1]);
         l[r] += p0 + p1;
-        pa[2 * q + r] = dec_pack(p0, p1);
+        pa[q >> 1][2 * (q & 1) + r] = dec_pack(p0, p1);
       }
-    const int vkey = 16 * part + (lane & 15);
-    const uint32_t vrow = st + L::kHalf + vkey * L::kRow;
 #pragma unroll
-    for (int q = 0; q < NT / 2; ++q) {
-      const uint4 v = ldsm_t(vrow + (((2 * q + (lane >> 4)) ^ (vkey & 7)) * 16));
-      mma_bf16(o[2 * q], pa, v.x, v.y);
-      mma_bf16(o[2 * q + 1], pa, v.z, v.w);
+    for (int b = 0; b < NB; ++b) {
+      const int vkey = 16 * (NB * part + b) + (lane & 15);
+      const uint32_t vrow = st + L::kHalf + vkey * L::kRow;
+#pragma unroll
+      for (int q = 0; q < NT / 2; ++q) {
+        const uint4 v = ldsm_t(vrow + (((2 * q + (lane >> 4)) ^ (vkey & 7)) * 16));
+        mma_bf16(o[2 * q], pa[b], v.x, v.y);
+        mma_bf16(o[2 * q + 1], pa[b], v.z, v.w);
+      }
     }
   };
   auto sum_l = [&] {
@@ -627,7 +641,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
       solo_bits ^= 1u << stage;
       if (!dead) {
 #pragma unroll 1
-        for (int part = 0; part < kDecTile / 16; ++part) block(part);
+        for (int part = 0; part < 4; ++part) block(part);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + 8 * stage, kConsumers);
