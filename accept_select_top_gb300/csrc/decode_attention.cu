@@ -36,7 +36,9 @@ constexpr int kRing = 5;
 constexpr int kOwners = kConsumers + 2;  // who may have a part to itself: a warp, or four of them
 // A part of at most so many tiles, where the CTA's range is so many times longer, goes to one warp.
 constexpr int kSoloTiles = 1, kSoloRange = 2;
-constexpr int kEndTicks = 1;  // what a unit's end costs in the division of the work, in tiles
+// The work is divided in ticks of a quarter of a tile, so that short parts count by their keys; a tile belongs to the CTA
+// that has its first tick.  A unit's end counts as so many.
+constexpr int kEndTicks = 3;
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wait
 
 template <int D>
@@ -45,6 +47,7 @@ struct DecSmem {
   // Keys of a tile: 32 KB of K and V.  (Tiles of 64 keys for D 64, too, bounded it by what a tile costs besides its
   // bytes: 256 requests of 2048 tokens, 4 kv heads, 112 us, so 99.)
   static constexpr int kTile = 64 * 128 / D;
+  static constexpr int kTick = kTile / 4;
   static constexpr int kHalf = kTile * kRow;       // K of a tile
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kMerge = kRing * kStage;    // [warp][8 column tiles][32 lanes] float4
@@ -112,17 +115,20 @@ __device__ __forceinline__ void part_sync(int id, int threads) { asm volatile("b
 
 // A unit of the tick space.  Segments: the groups' shared tokens, then the requests' own.
 struct Unit {
-  int seg, j;        // segment, (kv head, row tile)
-  int tiles, J;      // of the unit; units of the segment
-  int first, last;   // keys [first, last) of the table row that count
-  int rows, r0;      // query rows of the segment; its first request
+  int seg, h, rt;        // segment, kv head, 64-row tile
+  int row_tiles, ticks;  // of the segment; of the unit, without its end's
+  int first, last;       // keys [first, last) of the table row that count
+  int rows, r0;          // query rows of the segment; its first request
+  int u0;                // the unit's first tick
+  __device__ int tiles() const { return (ticks + 3) >> 2; }
+  __device__ int row0() const { return rt * kDecRows; }
 };
 
 template <int D>
 __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const __grid_constant__ DecodeArgs args) {
   using L = DecSmem<D>;
   constexpr unsigned FULL = 0xffffffffu;
-  constexpr int NT = D / 8, kTile = L::kTile;
+  constexpr int NT = D / 8, kTile = L::kTile, kTick = L::kTick;
   const DecodeParams& a = args.p;
   extern __shared__ __align__(128) unsigned char smem[];
   const int ng = a.num_groups, G = a.Hq / a.Hkv;
@@ -192,20 +198,19 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     }
     sbase[r] = base;
     if (report) {
-      args.base[r] = base;
-      args.member[r] = make_int2(g, g < 0 ? 0 : r - sgroup[g]);
+      args.member[r] = g < 0 ? make_int4(-1, r, 1, 0) : make_int4(g, sgroup[g], sgroup[g + 1] - sgroup[g], base);
     }
   }
   __syncthreads();
+  // ticks of a unit over keys [first, last), without its end's
+  auto unit_ticks = [&](int first, int last) { return max(1, (last - first / kTile * kTile + kTick - 1) / kTick); };
   auto ticks_of = [&](int s) {
     if (s < ng) {
       const int first = grouped ? sgroup[s] : 0, rows = grouped ? (sgroup[s + 1] - first) * G : 0;
-      const bool here = rows > 0 && !(args.tall && rows > kDecFlatRows);  // (else it is the tcgen05 kernel's)
-      const int tiles = here ? (sbase[first] + kTile - 1) / kTile : 0;
-      return tiles ? a.Hkv * ((rows + kDecRows - 1) / kDecRows) * (tiles + kEndTicks) : 0;
+      const bool here = rows > 0 && sbase[first] > 0 && !(args.tall && rows > kDecFlatRows);  // (else it is the tcgen05 kernel's)
+      return here ? a.Hkv * ((rows + kDecRows - 1) / kDecRows) * (unit_ticks(0, sbase[first]) + kEndTicks) : 0;
     }
-    const int r = s - ng, n = (slen[r] + kTile - 1) / kTile - sbase[r] / kTile;
-    return a.Hkv * args.own_tiles * ((n < 1 ? 1 : n) + kEndTicks);
+    return a.Hkv * args.own_tiles * (unit_ticks(sbase[s - ng], slen[s - ng]) + kEndTicks);
   };
   {
     const int segs = ng + a.b;
@@ -234,7 +239,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
       for (int s = tid; s <= segs; s += kDecThreads) args.pre[s] = pre[s];
   }
   const int T = pre[ng + a.b];  // (the host keeps it below 2^31)
-  const int ctas = T < int(gridDim.x) ? T : int(gridDim.x);
+  // (at least four ticks a CTA: each on a unit has one of its tiles)
+  const int ctas = max(1, min(T >> 2, int(gridDim.x)));
   if (report && tid == 0) *args.plan = make_int4(T, ctas, ng, 0);
   if (int(blockIdx.x) >= ctas) {
     if (args.tall) pdl_wait();
@@ -242,50 +248,57 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   }
   const int S = int((long long)blockIdx.x * T / ctas), E = int((long long)(blockIdx.x + 1) * T / ctas);
 
-  auto open = [&](Unit& u, int seg) {  // the first segment from `seg` on that has ticks
-    while (pre[seg + 1] == pre[seg]) ++seg;
+  auto open = [&](Unit& u, int seg) {  // the first unit of the first segment from `seg` on that has ticks
+    while (seg < ng && pre[seg + 1] == pre[seg]) ++seg;
     u.seg = seg;
-    const int n = pre[seg + 1] - pre[seg];
+    u.h = u.rt = 0;
     if (seg < ng) {
       u.r0 = __ldg(a.group_start + seg);
       u.rows = (__ldg(a.group_start + seg + 1) - u.r0) * G;
       u.first = 0;
       u.last = sbase[u.r0];
-      u.J = a.Hkv * ((u.rows + kDecRows - 1) / kDecRows);
+      u.row_tiles = (u.rows + kDecRows - 1) / kDecRows;
     } else {
       u.r0 = seg - ng;
       u.rows = G;
       u.first = sbase[u.r0];
       u.last = slen[u.r0];
-      u.J = a.Hkv * args.own_tiles;
+      u.row_tiles = args.own_tiles;
     }
-    u.tiles = n / u.J - kEndTicks;
+    u.ticks = unit_ticks(u.first, u.last);
   };
-  // tick f of the range: its unit and the tile in it (from `tiles` on: the end's ticks)
-  auto locate = [&](int f, Unit& u, int& t) {
+  // the range's first unit, and the first of its tiles that is the CTA's
+  auto locate = [&](Unit& u, int& t) {
     int lo = 0, hi = ng + a.b;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= f) lo = mid;
+      if (pre[mid] <= S) lo = mid;
       else hi = mid;
     }
     open(u, lo);
-    const int rem = f - pre[u.seg];
-    u.j = rem / (u.tiles + kEndTicks);
-    t = rem - u.j * (u.tiles + kEndTicks);
+    const int n = u.ticks + kEndTicks, j = (S - pre[u.seg]) / n;
+    u.h = j / u.row_tiles;
+    u.rt = j - u.h * u.row_tiles;
+    u.u0 = pre[u.seg] + j * n;
+    t = (S - u.u0 + 3) >> 2;
   };
+  // the next unit; false behind the range
   auto next_unit = [&](Unit& u) {
-    if (++u.j == u.J) {
-      open(u, u.seg + 1);
-      u.j = 0;
+    u.u0 += u.ticks + kEndTicks;
+    if (u.u0 >= E) return false;
+    if (++u.rt == u.row_tiles) {
+      u.rt = 0;
+      if (++u.h == a.Hkv) open(u, u.seg + 1);
     }
+    return true;
   };
+  // tiles of the unit in the range, from tile t on
+  auto tiles_from = [&](const Unit& u, int t) { return min(u.tiles(), (E - u.u0 + 3) >> 2) - t; };
   // Who takes a part of n tiles of a unit: a warp (0 .. 7), four (8, 9), or all (-1).  parts: how many of either kind
   // came before in the range.
   auto owner_of = [&](const Unit& u, int n, int2& parts) {
-    const int row_tiles = u.J / a.Hkv;
-    if (u.rows - (u.j % row_tiles) * kDecRows > 16) return -1;
-    if (n <= kSoloTiles && E - S > kSoloRange * n) return parts.x++ % kConsumers;
+    if (u.rows - u.row0() > 16) return -1;
+    if (n <= kSoloTiles && E - S > kSoloRange * 4 * n) return parts.x++ % kConsumers;
     return kConsumers + (parts.y++ & 1);
   };
   __syncthreads();  // (sgroup is not read any more)
@@ -303,27 +316,27 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     const uint32_t ring0 = smem_u32(smem) + (kMine * p + ck) * L::kRow;
     const uint32_t kdst = (cx ^ (4 * (ck & 1))) * 16, page_mask = (1u << args.shift) - 1u;
     Unit u;
-    int t, f = S;
-    locate(f, u, t);
+    int t, n;
+    locate(u, t);
+    n = tiles_from(u, t);
     // What look() found: of each of two tiles the kv head (-1: none is left), the owner (-1: all warps), and the lane's key's
     // position (-1: none that counts) and page id.
     int x_pos[2] = {-1, -1}, x_id[2] = {-1, -1}, owner = -1, h_now = 0, x_now = 0, heads[2], owners[2];
     int2 parts = make_int2(0, 0);
     const int* row_now = nullptr;
-    bool entered = false;
+    bool entered = false, more = true;
     auto look = [&](int half) {
-      while (f < E && t >= u.tiles) {  // over a unit's end
-        f += u.tiles + kEndTicks - t;
-        t = 0;
-        entered = false;
-        if (f < E) next_unit(u);
-      }
       heads[half] = -1;
-      if (f >= E) return;
+      while (n <= 0) {  // over a unit's end
+        if (!more || !(more = next_unit(u))) return;
+        t = 0;
+        n = tiles_from(u, 0);
+        entered = false;
+      }
       if (!entered) {
         entered = true;
-        owner = owner_of(u, min(u.tiles - t, E - f), parts);
-        h_now = u.j / (u.J / a.Hkv);
+        owner = owner_of(u, n, parts);
+        h_now = u.h;
         row_now = a.page_table + (long long)__ldg(a.req_pool_idx + u.r0) * a.row_pages;
         x_now = (u.first / kTile + t) * kTile + kMine * p + lane;
       }
@@ -335,8 +348,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
         x_id[half] = __ldg(row_now + (x_now >> args.shift));
       }
       x_now += kTile;
-      ++f;
-      ++t;
+      --n;
     };
     int stage = 0;
     uint32_t phase = 1;  // (an empty ring)
@@ -552,7 +564,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     }
   };
   // Two columns of a row's result (unnormalised, relative to M): out, or a partial result.
-  auto put = [&](const Unit& u, int h, int row0, int row, int col, bool whole, bool begun, float M, float Ls, float s0, float s1, bool note) {
+  auto put = [&](const Unit& u, int row, int col, bool whole, bool begun, float M, float Ls, float s0, float s1, bool note) {
+    const int h = u.h, row0 = u.row0();
     const bool own = u.seg >= ng;
     const int f = row / G;
     const size_t orow = (size_t(u.r0) + f) * a.Hq + h * G + (row - f * G);
@@ -575,7 +588,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     constexpr int KS = RT == 1 ? 4 : kConsumers / RT;  // warps that hold a row tile
     constexpr int kThreads = 32 * RT * KS;
     const int rt = w % RT, share = RT == 1 ? w & 3 : w / RT, w0 = RT == 1 ? w & 4 : 0, id = RT == 1 ? 2 + (w >> 2) : 1;
-    const int row_tiles = u.J / a.Hkv, h = u.j / row_tiles, row0 = (u.j - h * row_tiles) * kDecRows;
+    const int h = u.h, row0 = u.row0();
     uint32_t& bits = RT == 1 ? four_bits : full_bits;
     begin(u, h, row0 + rt * 16);
     for (int i = 0; i < n; ++i) {
@@ -600,7 +613,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
       mls[w * 16 + g] = make_float2(m[0], l[0]);
       mls[w * 16 + g + 8] = make_float2(m[1], l[1]);
     }
-    const bool begun = t0 == 0, whole = begun && n == u.tiles;
+    const bool begun = t0 == 0, whole = begun && n == u.tiles();
 #pragma unroll
     for (int half = 0; half < D / 64; ++half) {
 #pragma unroll
@@ -626,7 +639,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
             s0 = fmaf(wt, v.x, s0);
             s1 = fmaf(wt, v.y, s1);
           }
-          put(u, h, row0, row, 64 * half + 8 * q + 2 * (ln & 3), whole, begun, M, Ls, s0, s1, half == 0 && q == 0 && (ln & 3) == 0);
+          put(u, row, 64 * half + 8 * q + 2 * (ln & 3), whole, begun, M, Ls, s0, s1, half == 0 && q == 0 && (ln & 3) == 0);
         }
       }
       part_sync(id, kThreads);
@@ -634,7 +647,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   };
   // The same by one warp.
   auto work_alone = [&](const Unit& u, int t0, int n) {
-    const int row_tiles = u.J / a.Hkv, h = u.j / row_tiles, row0 = (u.j - h * row_tiles) * kDecRows;
+    const int h = u.h, row0 = u.row0();
     begin(u, h, row0);
     for (int i = 0; i < n; ++i) {
       wait_tile(owned + 8 * (w * kRing + stage), solo_bits >> stage & 1u);
@@ -654,20 +667,19 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
       if (row >= u.rows) continue;
 #pragma unroll
       for (int q = 0; q < NT; ++q)
-        put(u, h, row0, row, 8 * q + 2 * c, t0 == 0 && n == u.tiles, t0 == 0, m[r], l[r], o[q][2 * r], o[q][2 * r + 1], q == 0 && c == 0);
+        put(u, row, 8 * q + 2 * c, t0 == 0 && n == u.tiles(), t0 == 0, m[r], l[r], o[q][2 * r], o[q][2 * r + 1], q == 0 && c == 0);
     }
   };
 
   Unit u;
-  int t, f = S;
-  locate(f, u, t);
-  while (f < E) {
-    const int n = min(u.tiles - t, E - f);
+  int t;
+  locate(u, t);
+  do {
+    const int n = tiles_from(u, t);
     if (n > 0) {
       const int who = owner_of(u, n, parts);
       if (who < 0) {
-        const int row_tiles = u.J / a.Hkv, left = u.rows - (u.j % row_tiles) * kDecRows;
-        if (left <= 32) work(std::integral_constant<int, 2>{}, u, t, n, who);
+        if (u.rows - u.row0() <= 32) work(std::integral_constant<int, 2>{}, u, t, n, who);
         else work(std::integral_constant<int, 4>{}, u, t, n, who);
       } else if (who == w) {
         work_alone(u, t, n);
@@ -677,10 +689,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
         stage = (stage + n) % kRing;
       }
     }
-    f += u.tiles + kEndTicks - t;
     t = 0;
-    if (f < E) next_unit(u);
-  }
+  } while (next_unit(u));
   if (args.tall) pdl_wait();
 }
 
@@ -697,28 +707,28 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   if (at >= total) return;
   const int4 plan = __ldcg(args.plan), tall_plan = args.tall ? __ldcg(args.tall_plan) : make_int4(0, 0, 0, 0);
   int r = at / a.Hq, head = at - r * a.Hq;
-  const int2 mem0 = __ldcg(args.member + r);
-  int r0 = r, all = G;
-  if (mem0.x >= 0) {
-    r0 = r - mem0.y;
-    all = (__ldg(a.group_start + mem0.x + 1) - r0) * G;
+  const int4 mem = __ldcg(args.member + r);
+  const int r0 = mem.y, all = mem.z * G;  // (all: the rows of a kv head)
+  int base = mem.w;
+  if (mem.x >= 0) {
     const int rem = at - r0 * a.Hq, hh = rem / all, x = rem - hh * all, f = x / G;
     r = r0 + f;
     head = hh * G + x - f * G;
+    base = __ldcg(args.member + r).w;
   }
-  const int h = head / G, i = head - h * G, x = (r - r0) * G + i, base = __ldcg(args.base + r);
+  const int h = head / G, i = head - h * G, x = (r - r0) * G + i;
   const size_t orow = size_t(r) * a.Hq + head;
   // The CTAs on a unit, the j-th of a segment of so many: [wa, wb].
   struct Span {
     int wa, wb;
   };
-  auto span = [&](const int4& pl, const int* pre, int seg, int units, int j, int end) {
-    const int p0 = __ldcg(pre + seg), n = (__ldcg(pre + seg + 1) - p0) / units, u0 = p0 + j * n;
+  auto span = [&](const int4& pl, const int* pre, int seg, int units, int j, int end, int tile) {  // tile: its ticks
+    const int p0 = __ldcg(pre + seg), n = (__ldcg(pre + seg + 1) - p0) / units, u0 = p0 + j * n, last = u0 + (n - end - 1) / tile * tile;
     const long long T = pl.x, ctas = pl.y;
-    return Span{int(((long long)(u0 + 1) * ctas - 1) / T), int(((long long)(u0 + n - end) * ctas - 1) / T)};
+    return Span{int(((long long)(u0 + 1) * ctas - 1) / T), int(((long long)(last + 1) * ctas - 1) / T)};
   };
   const int own0 = i / kDecRows * kDecRows;
-  const Span own = span(plan, args.pre, plan.z + r, a.Hkv * args.own_tiles, h * args.own_tiles + i / kDecRows, kEndTicks);
+  const Span own = span(plan, args.pre, plan.z + r, a.Hkv * args.own_tiles, h * args.own_tiles + i / kDecRows, kEndTicks, 4);
   const bool done = own.wa == own.wb && base == 0;  // (already in out)
   if (done) return;
   const int n_own = own.wb - own.wa + 1;
@@ -730,7 +740,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   const bool split = tall && rows <= 128;
   if (base > 0) {
     const int tiles = (all + size - 1) / size;
-    sh = span(tall ? tall_plan : plan, tall ? args.tall_pre : args.pre, mem0.x, a.Hkv * tiles, h * tiles + x / size, tall ? kDecTallEnd : kEndTicks);
+    sh = span(tall ? tall_plan : plan, tall ? args.tall_pre : args.pre, mem.x, a.Hkv * tiles, h * tiles + x / size, tall ? kDecTallEnd : kEndTicks, tall ? 1 : 4);
     n_sh = (sh.wb - sh.wa + 1) * (split ? 2 : 1);
   }
   const size_t sh_first = size_t(r0) * a.Hq + size_t(h) * all + x0;
@@ -814,7 +824,7 @@ int launch_decode(const DecodeArgs& args, int sms, cudaStream_t stream) {
 
 // Offsets of the workspace's parts.
 struct DecodeLayout {
-  size_t pre, base, member, frag_ml, own_ml, shared_ml, frag_o, own_o, shared_o, bytes;
+  size_t pre, member, frag_ml, own_ml, shared_ml, frag_o, own_o, shared_o, bytes;
   size_t tall_pre, tall_ml, whole_ml, tall_o, whole_o;
   DecodeLayout(int b, int Hq, int D, bool tall) {
     const size_t rows = size_t(b) * Hq, frags = size_t(2) * kDecMaxCtas * kDecRows, tall_frags = size_t(2) * kDecMaxCtas * kDecTallRows;
@@ -825,8 +835,7 @@ struct DecodeLayout {
       return x;
     };
     pre = take(size_t(2 * b + 1) * 4);
-    base = take(size_t(b) * 4);
-    member = take(size_t(b) * 8);
+    member = take(size_t(b) * 16);
     frag_ml = take(frags * 8);
     own_ml = take(rows * 8);
     shared_ml = take(rows * 8);
@@ -856,8 +865,11 @@ int launch_decode_attention(const DecodeParams& p, cudaStream_t stream) {
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return SPEC_ERR_LAUNCH;
-  // (a scale of zero would take the -inf of a key that does not count to NaN there)
-  const bool tall = p.num_groups > 0 && may_be_tall(p.b, p.Hq, p.Hkv) && p.scale != 0.f;
+  // The groups are not known here, but their mean is: where it is far below what the tcgen05 kernel takes, its launch
+  // (5 us) is left out, and a large group among small ones takes the other kernel's tiles of 64 rows.
+  // (A scale of zero would take the -inf of a key that does not count to NaN there.)
+  const bool tall = p.num_groups > 0 && may_be_tall(p.b, p.Hq, p.Hkv) && (long long)p.b * (p.Hq / p.Hkv) > kDecFlatRows / 2 * (long long)p.num_groups &&
+                    p.scale != 0.f;
   const DecodeLayout at(p.b, p.Hq, p.D, tall);
   unsigned char* ws = p.partials;
   DecodeArgs args{};
@@ -867,8 +879,7 @@ int launch_decode_attention(const DecodeParams& p, cudaStream_t stream) {
   args.own_tiles = (p.Hq / p.Hkv + kDecRows - 1) / kDecRows;
   args.plan = reinterpret_cast<int4*>(ws);
   args.pre = reinterpret_cast<int*>(ws + at.pre);
-  args.base = reinterpret_cast<int*>(ws + at.base);
-  args.member = reinterpret_cast<int2*>(ws + at.member);
+  args.member = reinterpret_cast<int4*>(ws + at.member);
   args.frag_ml = reinterpret_cast<float2*>(ws + at.frag_ml);
   args.own_ml = reinterpret_cast<float2*>(ws + at.own_ml);
   args.shared_ml = reinterpret_cast<float2*>(ws + at.shared_ml);

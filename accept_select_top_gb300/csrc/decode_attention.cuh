@@ -6,7 +6,7 @@
 
 namespace spec {
 
-constexpr int kDecTile = 64;    // keys of a tile
+constexpr int kDecTile = 64;    // keys of a tile of the tcgen05 kernel
 constexpr int kDecRows = 64;    // query rows of a unit
 constexpr int kDecMaxCtas = 192;  // upper bound of a grid of one CTA a SM; sizes the fragment slots
 
@@ -37,15 +37,14 @@ constexpr int kDecTallEnd = 2;     // what a unit's end costs there in the divis
 __device__ __forceinline__ int dec_shared(int shared, int first_len) { return shared > 0 && first_len >= shared ? shared : 0; }
 
 // The workspace of a call.  plan: {ticks, CTAs, groups, -} and, for the joining kernel, what the first CTA of the main
-// kernel found: ticks before each segment, each request's shared length, its group and place in it.
+// kernel found: ticks before each segment, and each request's group.
 struct DecodeArgs {
   DecodeParams p;
   int shift;       // log2(page_size)
   int own_tiles;   // 64-row tiles of a kv head's rows of one request
   int4* plan;
   int* pre;        // [groups + b + 1]
-  int* base;       // [b]
-  int2* member;    // [b]
+  int4* member;    // [b]: {group (-1: none), its first request, its members, tokens shared}
   // Partial results: (m, l) of each row, and O as words of four columns, [D / 4][rows].  Those of a unit's part:
   // [2 * CTA + i][..][64], i = 1: the unit that the CTA begins and does not finish.  Those of units that lie in one
   // CTA: from row r0 * Hq + h * (the segment's rows) + (the unit's first) on, as many rows as the unit has.

@@ -1215,8 +1215,8 @@ int spec_decode_attention(int b, int Hq, int Hkv, int D, int page_size, const vo
   if (q_ld < int64_t(Hq) * D || q_ld % 8 || num_slots < page_size || num_slots >= (int64_t(1) << 31) || req_rows < 1 ||
       row_pages < 1 || int64_t(row_pages) * page_size >= (int64_t(1) << 31))
     return SPEC_ERR_ARG;
-  // tiles (an end's ticks among them) of the requests' own tokens and of the shared ones
-  const int64_t G = Hq / Hkv, most = int64_t(max_seq_len) / 64 + 3, row_tiles = (G + 63) / 64;
+  // ticks (16 keys, and a unit's end) of the requests' own tokens and of the shared ones
+  const int64_t G = Hq / Hkv, most = int64_t(max_seq_len) / 16 + 8, row_tiles = (G + 63) / 64;
   if (int64_t(b) * Hkv >= (int64_t(1) << 31) / row_tiles / most / 2 ||
       (num_groups && (b * G / 64 + num_groups) * Hkv >= (int64_t(1) << 31) / most / 2) || int64_t(b) * Hq >= (int64_t(1) << 31))
     return SPEC_ERR_ARG;

@@ -688,8 +688,8 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
  * clamped).  A page id out of range sets SPEC_DEV_INDEX and its keys do not count;
  * a bad table row leaves its request without tokens.  What the pools hold behind a
  * request's last token is not looked at.  A call's results are always the same
- * bits.  D 64 or 128, b <= 2048, num_groups <= b; the tiles, b * (max_seq_len / 64
- * + 3) * Hkv * ceil(Hq / Hkv / 64), stay below 2^30.  HBM-bound.
+ * bits.  D 64 or 128, b <= 2048, num_groups <= b; the ticks, b * (max_seq_len / 16
+ * + 8) * Hkv * ceil(Hq / Hkv / 64), stay below 2^30.  HBM-bound.
  * ------------------------------------------------------------------------- */
 int spec_decode_attention(int b, int Hq, int Hkv, int D, int page_size, const void* q, int64_t q_ld,
                           const void* k_pool, const void* v_pool, int64_t num_slots, const int32_t* page_table,
