@@ -37,8 +37,8 @@ constexpr int kOwners = kConsumers + 2;  // who may have a part to itself: a war
 // A part of at most so many tiles, where the CTA's range is so many times longer, goes to one warp.
 constexpr int kSoloTiles = 1, kSoloRange = 2;
 // The work is divided in ticks of a quarter of a tile, so that short parts count by their keys; a tile belongs to the CTA
-// that has its first tick.  A unit's end counts as so many.
-constexpr int kEndTicks = 3;
+// that has its first tick.  A unit's end counts as kEndTicks.
+constexpr int kEndTicks = kDecEndTicks;
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wait
 
 template <int D>
@@ -47,7 +47,6 @@ struct DecSmem {
   // Keys of a tile: 32 KB of K and V.  (Tiles of 64 keys for D 64, too, bounded it by what a tile costs besides its
   // bytes: 256 requests of 2048 tokens, 4 kv heads, 112 us, so 99.)
   static constexpr int kTile = 64 * 128 / D;
-  static constexpr int kTick = kTile / 4;
   static constexpr int kHalf = kTile * kRow;       // K of a tile
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kMerge = kRing * kStage;    // [warp][8 column tiles][32 lanes] float4
@@ -128,7 +127,8 @@ template <int D>
 __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const __grid_constant__ DecodeArgs args) {
   using L = DecSmem<D>;
   constexpr unsigned FULL = 0xffffffffu;
-  constexpr int NT = D / 8, kTile = L::kTile, kTick = L::kTick;
+  constexpr int NT = D / 8, kTile = L::kTile;
+  static_assert(kTile == 4 * kDecTickKeys128 * 128 / D, "four ticks a tile");
   const DecodeParams& a = args.p;
   extern __shared__ __align__(128) unsigned char smem[];
   const int ng = a.num_groups, G = a.Hq / a.Hkv;
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   int* sbase = slen + a.b;
   int* sgroup = reinterpret_cast<int*>(smem);  // (the ring is not in use yet)
   __shared__ int wsum[kDecThreads / 32];
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_tall;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const uint32_t full = smem_u32(smem + L::kBars), empty = full + 8 * kRing, owned = empty + 8 * kRing;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     }
     for (int i = 0; i < kOwners * kRing; ++i) mbar_init(owned + 8 * i, kProducers * 33);
     *abort_flag = 0;
-    s_bad = 0;
+    s_bad = s_tall = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // (behind the tcgen05 kernel, which waits for what came before the call, this one starts where CTAs end: it reads
@@ -202,8 +202,17 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     }
   }
   __syncthreads();
-  // ticks of a unit over keys [first, last), without its end's
-  auto unit_ticks = [&](int first, int last) { return max(1, (last - first / kTile * kTile + kTick - 1) / kTick); };
+  auto unit_ticks = [](int first, int last) { return dec_unit_ticks<D>(first, last); };
+  // the tcgen05 kernel's ticks
+  int tall = 0;
+  if (args.tall && grouped)
+    for (int g = tid; g < ng; g += kDecThreads) {
+      const int first = sgroup[g], rows = (sgroup[g + 1] - first) * G;
+      if (rows > kDecFlatRows && sbase[first] > 0)
+        tall += a.Hkv * ((rows + kDecTallRows - 1) / kDecTallRows) * ((sbase[first] + kDecTile - 1) / kDecTile + kDecTallEnd);
+    }
+  tall = __reduce_add_sync(FULL, tall);
+  if (args.tall && lane == 0 && tall) atomicAdd(&s_tall, tall);
   auto ticks_of = [&](int s) {
     if (s < ng) {
       const int first = grouped ? sgroup[s] : 0, rows = grouped ? (sgroup[s + 1] - first) * G : 0;
@@ -240,7 +249,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   }
   const int T = pre[ng + a.b];  // (the host keeps it below 2^31)
   // (at least four ticks a CTA: each on a unit has one of its tiles)
-  const int ctas = max(1, min(T >> 2, int(gridDim.x)));
+  const int ctas = max(1, min(T >> 2, int(gridDim.x) - dec_tall_ctas(s_tall, T, gridDim.x)));
   if (report && tid == 0) *args.plan = make_int4(T, ctas, ng, 0);
   if (int(blockIdx.x) >= ctas) {
     if (args.tall) pdl_wait();

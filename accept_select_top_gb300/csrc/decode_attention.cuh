@@ -33,6 +33,26 @@ constexpr int kDecFlatRows = 32;
 constexpr int kDecTallRows = 256;  // query rows of one of its units
 constexpr int kDecTallEnd = 2;     // what a unit's end costs there in the division of the work, in tiles
 
+// The two kernels of a call run side by side: of `ctas` SMs the tcgen05 kernel takes so many, by the ticks of both (one
+// of its tiles takes as long as so many of the other's ticks), and the rest of its CTAs leave at once, so that the other
+// kernel's, launched behind them, find their SMs free.
+constexpr int kDecTallCost = 4;
+__device__ __forceinline__ int dec_tall_ctas(int tall, int flat, int ctas) {
+  if (tall == 0) return 0;
+  const long long cost = (long long)tall * kDecTallCost;
+  const int n = int((cost * ctas + (cost + flat) / 2) / (cost + flat));
+  return n < 1 || ctas == 1 ? 1 : n > ctas - 1 ? ctas - 1 : n;
+}
+constexpr int kDecTickKeys128 = 16;  // keys of a tick of the other kernel, of D 128 (64: twice as many)
+constexpr int kDecEndTicks = 3;      // what a unit's end costs there
+// ticks of a unit over keys [first, last), without its end's
+template <int D>
+__device__ __forceinline__ int dec_unit_ticks(int first, int last) {
+  constexpr int kTick = kDecTickKeys128 * 128 / D, kTile = 4 * kTick;
+  const int n = (last - first / kTile * kTile + kTick - 1) / kTick;
+  return n < 1 ? 1 : n;
+}
+
 // What a group shares, from its bounds and its first member's length (0: nothing).
 __device__ __forceinline__ int dec_shared(int shared, int first_len) { return shared > 0 && first_len >= shared ? shared : 0; }
 

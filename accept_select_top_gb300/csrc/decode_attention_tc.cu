@@ -43,7 +43,7 @@ struct TallSmem {
   static constexpr int kBars = kRing + kStages * kStage;
   static constexpr int kNumBars = 2 * kMostStages + 2 + 2 + 4 + 4 + 4 + 4;
   static constexpr int kMask = kBars + 8 * kNumBars;   // [stage][4] keys that count, 16 bits each
-  static constexpr int kWords = kMask + kStages * 16;  // TMEM address, abort flag, bad flag, ticks, then a word a warp
+  static constexpr int kWords = kMask + kStages * 16;  // TMEM address, abort flag, bad flag, the other kernel's ticks, then a word a warp
   static constexpr int kBytes = kWords + 16 + 4 * (kTallThreads / 32);
   // the ticks before each group are summed up where the ring will be
   static_assert(4 * (2 * kDecodeMaxB + 2) <= kStages * kStage, "scan space");
@@ -224,8 +224,10 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sp + L::kWords);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + L::kWords + 4);
   volatile int* bad = reinterpret_cast<volatile int*>(sp + L::kWords + 8);
+  int* s_flat = reinterpret_cast<int*>(sp + L::kWords + 12);
   int* wsum = reinterpret_cast<int*>(sp + L::kWords + 16);
   int* pre = reinterpret_cast<int*>(sp + L::kRing);  // [groups + 1] ticks before each group, until the roles start
+  int* sgroup = pre + ng + 1;                        // [groups + 1]
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -244,6 +246,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
     }
     *abort_flag = 0;
     *bad = 0;
+    *s_flat = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 12) {
@@ -257,9 +260,10 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
   const long long room = (long long)a.row_pages << args.shift;
   const int most = room < a.max_seq_len ? int(room) : a.max_seq_len;
   __syncthreads();
-  for (int g = tid; g < ng; g += kTallThreads) {
-    const int s = a.group_start[g], e = a.group_start[g + 1];
-    if (s < 0 || s > e || e > a.b) *bad = 1;
+  for (int g = tid; g <= ng; g += kTallThreads) {
+    const int s = a.group_start[g], e = g < ng ? a.group_start[g + 1] : a.b;
+    if (g < ng && (s < 0 || s > e || e > a.b)) *bad = 1;
+    sgroup[g] = s;
   }
   __syncthreads();
   const bool grouped = *bad == 0;  // (the other kernel tells)
@@ -278,6 +282,32 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
     p.tiles = (p.shared + kDecTile - 1) / kDecTile;
   };
   auto ticks_of = [&](const Place& p) { return p.tiles ? a.Hkv * p.blocks * (p.tiles + kDecTallEnd) : 0; };
+  if (grouped) {  // the other kernel's ticks: each request's own tokens, and what smaller groups share
+    const int own_tiles = args.own_tiles;
+    auto len_of = [&](int r) {
+      const int row = __ldg(a.req_pool_idx + r);
+      return row < 0 || row >= a.req_rows ? 0 : min(max(__ldg(a.seq_lens + r), 0), most);
+    };
+    int flat = 0;
+    for (int r = tid; r < a.b; r += kTallThreads) {
+      const int len = len_of(r);
+      int base = 0;
+      if (r >= sgroup[0] && r < sgroup[ng]) {
+        int lo = 0, hi = ng;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (sgroup[mid] <= r) lo = mid;
+          else hi = mid;
+        }
+        const int first = sgroup[lo], rows = (sgroup[lo + 1] - first) * G, s = dec_shared(__ldg(a.shared_lens + lo), len_of(first));
+        base = len >= s ? s : 0;
+        if (r == first && s > 0 && rows <= kDecFlatRows) flat += a.Hkv * ((rows + kDecRows - 1) / kDecRows) * (dec_unit_ticks<D>(0, s) + kDecEndTicks);
+      }
+      flat += a.Hkv * own_tiles * (dec_unit_ticks<D>(base, len) + kDecEndTicks);
+    }
+    flat = __reduce_add_sync(FULL, flat);
+    if (lane == 0) atomicAdd(s_flat, flat);
+  }
   {
     int run = 0;
     for (int g0 = 0; g0 < ng; g0 += kTallThreads) {
@@ -308,7 +338,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
   tc_after();
   const uint32_t tmem = *tmem_holder;
   const int T = pre[ng];
-  const int ctas = T < int(gridDim.x) ? T : int(gridDim.x);
+  const int ctas = min(T, dec_tall_ctas(T, *s_flat, gridDim.x));
   const bool part = int(blockIdx.x) < ctas;
   const int S = part ? int((long long)blockIdx.x * T / ctas) : 0, E = part ? int((blockIdx.x + 1ll) * T / ctas) : 0;
   if (blockIdx.x == 0) {
