@@ -18,12 +18,15 @@
 // dimension inside a fragment is free as long as Q has the same, so K fragments are read as 16-byte words.
 // At a unit's end the warps' results are joined through shared memory.
 //   Units cut by a range boundary, and all of a grouped request, leave fp32 results in the workspace; a second,
-// dependent launch joins them.  No atomics: a call's result is always the same.
+// dependent launch joins them.  Where units are few and short, a cluster of CTAs takes each, an equal share of its tiles a
+// CTA, and joins it through distributed shared memory in the same launch.  No atomics: a call's result is always the
+// same.
 #include <type_traits>
 
 #include "common.cuh"
 #include "kernels.cuh"
 
+#include "cluster.cuh"
 #include "decode_attention.cuh"
 
 namespace spec {
@@ -33,6 +36,10 @@ namespace {
 constexpr int kConsumers = 8, kProducers = 4;
 constexpr int kDecThreads = 32 * (kConsumers + kProducers);
 constexpr int kRing = 5;
+// A cluster takes a unit where all of them run at once (a GB300 holds 15 clusters of eight CTAs of a SM each, 36 of four,
+// 76 of two) and a CTA gets at most so many tiles; else the SMs share the work, and a second launch joins it.
+constexpr int kClusterMost = 8, kClusterTiles = 8;
+inline int cluster_of(long long units, int sms) { return units <= 14 ? 8 : units <= 34 ? 4 : units <= 72 ? 2 : units <= sms ? 1 : 0; }
 constexpr int kOwners = kConsumers + 2;  // who may have a part to itself: a warp, or four of them
 // A part of at most so many tiles, where the CTA's range is so many times longer, goes to one warp.
 constexpr int kSoloTiles = 1, kSoloRange = 2;
@@ -123,7 +130,8 @@ struct Unit {
   __device__ int row0() const { return rt * kDecRows; }
 };
 
-template <int D>
+// CLUSTER: a cluster of CTAs takes one unit (grid: cluster, units) and joins it by itself.
+template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const __grid_constant__ DecodeArgs args) {
   using L = DecSmem<D>;
   constexpr unsigned FULL = 0xffffffffu;
@@ -158,104 +166,131 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
 
   // ---- segments ----
   const bool report = blockIdx.x == 0;
+  Unit unit{};  // CLUSTER: the unit, and its tiles [S, E) of this CTA
+  int S = 0, E = 0;
   const long long room = (long long)a.row_pages << args.shift;
   const int most = room < a.max_seq_len ? int(room) : a.max_seq_len;
-  for (int g = tid; g <= ng && ng > 0; g += kDecThreads) sgroup[g] = a.group_start[g];
-  for (int r = tid; r < a.b; r += kDecThreads) {
+  auto unit_ticks = [](int first, int last) { return dec_unit_ticks<D>(first, last); };
+  if (CLUSTER) {
+    const int r = blockIdx.y / a.Hkv;
     int len = a.seq_lens[r];
     const int row = a.req_pool_idx[r];
+    unit.h = blockIdx.y - r * a.Hkv;
+    const bool tell = report && unit.h == 0 && tid == 0;
     if (len < 0 || len > most) {
-      if (report) raise_error(a.error, SPEC_DEV_LENGTH);
+      if (tell) raise_error(a.error, SPEC_DEV_LENGTH);
       len = len < 0 ? 0 : most;
     }
     if (row < 0 || row >= a.req_rows) {
-      if (report) raise_error(a.error, SPEC_DEV_INDEX);
+      if (tell) raise_error(a.error, SPEC_DEV_INDEX);
       len = 0;
     }
-    slen[r] = len;
-  }
-  __syncthreads();
-  // groups that overlap or lie outside the batch: nothing is shared
-  for (int g = tid; g < ng; g += kDecThreads)
-    if (sgroup[g] < 0 || sgroup[g] > sgroup[g + 1] || sgroup[g + 1] > a.b) s_bad = 1;
-  __syncthreads();
-  const bool grouped = ng > 0 && !s_bad;
-  if (report && tid == 0 && ng > 0 && s_bad) raise_error(a.error, SPEC_DEV_INDEX);
-  for (int r = tid; r < a.b; r += kDecThreads) {
-    int base = 0, g = -1;
-    if (grouped && r >= sgroup[0] && r < sgroup[ng]) {
-      int lo = 0, hi = ng;  // the last group that begins at or before r (empty ones are passed over)
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sgroup[mid] <= r) lo = mid;
-        else hi = mid;
+    unit.r0 = r;
+    unit.rows = G;
+    unit.row_tiles = 1;
+    unit.last = len;
+    const int tiles = (len + kTile - 1) / kTile;
+    S = int((long long)blockIdx.x * tiles / gridDim.x);
+    E = int((blockIdx.x + 1ll) * tiles / gridDim.x);
+    __syncthreads();  // (the barriers)
+  } else {
+    for (int g = tid; g <= ng && ng > 0; g += kDecThreads) sgroup[g] = a.group_start[g];
+    for (int r = tid; r < a.b; r += kDecThreads) {
+      int len = a.seq_lens[r];
+      const int row = a.req_pool_idx[r];
+      if (len < 0 || len > most) {
+        if (report) raise_error(a.error, SPEC_DEV_LENGTH);
+        len = len < 0 ? 0 : most;
       }
-      g = lo;
-      const int shared = a.shared_lens[g];
-      if (report && r == sgroup[g] && (shared < 0 || shared > most)) raise_error(a.error, SPEC_DEV_LENGTH);
-      const int s = dec_shared(shared, slen[sgroup[g]]);
-      if (slen[r] >= s) base = s;
-    }
-    sbase[r] = base;
-    if (report) {
-      args.member[r] = g < 0 ? make_int4(-1, r, 1, 0) : make_int4(g, sgroup[g], sgroup[g + 1] - sgroup[g], base);
-    }
-  }
-  __syncthreads();
-  auto unit_ticks = [](int first, int last) { return dec_unit_ticks<D>(first, last); };
-  // the tcgen05 kernel's ticks
-  int tall = 0;
-  if (args.tall && grouped)
-    for (int g = tid; g < ng; g += kDecThreads) {
-      const int first = sgroup[g], rows = (sgroup[g + 1] - first) * G;
-      if (rows > kDecFlatRows && sbase[first] > 0)
-        tall += a.Hkv * ((rows + kDecTallRows - 1) / kDecTallRows) * ((sbase[first] + kDecTile - 1) / kDecTile + kDecTallEnd);
-    }
-  tall = __reduce_add_sync(FULL, tall);
-  if (args.tall && lane == 0 && tall) atomicAdd(&s_tall, tall);
-  auto ticks_of = [&](int s) {
-    if (s < ng) {
-      const int first = grouped ? sgroup[s] : 0, rows = grouped ? (sgroup[s + 1] - first) * G : 0;
-      const bool here = rows > 0 && sbase[first] > 0 && !(args.tall && rows > kDecFlatRows);  // (else it is the tcgen05 kernel's)
-      return here ? a.Hkv * ((rows + kDecRows - 1) / kDecRows) * (unit_ticks(0, sbase[first]) + kEndTicks) : 0;
-    }
-    return a.Hkv * args.own_tiles * (unit_ticks(sbase[s - ng], slen[s - ng]) + kEndTicks);
-  };
-  {
-    const int segs = ng + a.b;
-    int run = 0;
-    for (int s0 = 0; s0 < segs; s0 += kDecThreads) {
-      const int s = s0 + tid, t = s < segs ? ticks_of(s) : 0;
-      int incl = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(FULL, incl, o);
-        if (lane >= o) incl += y;
+      if (row < 0 || row >= a.req_rows) {
+        if (report) raise_error(a.error, SPEC_DEV_INDEX);
+        len = 0;
       }
-      __syncthreads();
-      if (lane == 31) wsum[w] = incl;
-      __syncthreads();
-      int before = run;
-      for (int q = 0; q < kDecThreads / 32; ++q) {
-        if (q < w) before += wsum[q];
-        run += wsum[q];
-      }
-      if (s < segs) pre[s] = before + incl - t;
+      slen[r] = len;
     }
-    if (tid == 0) pre[segs] = run;
     __syncthreads();
-    if (report)
-      for (int s = tid; s <= segs; s += kDecThreads) args.pre[s] = pre[s];
+    // groups that overlap or lie outside the batch: nothing is shared
+    for (int g = tid; g < ng; g += kDecThreads)
+      if (sgroup[g] < 0 || sgroup[g] > sgroup[g + 1] || sgroup[g + 1] > a.b) s_bad = 1;
+    __syncthreads();
+    const bool grouped = ng > 0 && !s_bad;
+    if (report && tid == 0 && ng > 0 && s_bad) raise_error(a.error, SPEC_DEV_INDEX);
+    for (int r = tid; r < a.b; r += kDecThreads) {
+      int base = 0, g = -1;
+      if (grouped && r >= sgroup[0] && r < sgroup[ng]) {
+        int lo = 0, hi = ng;  // the last group that begins at or before r (empty ones are passed over)
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (sgroup[mid] <= r) lo = mid;
+          else hi = mid;
+        }
+        g = lo;
+        const int shared = a.shared_lens[g];
+        if (report && r == sgroup[g] && (shared < 0 || shared > most)) raise_error(a.error, SPEC_DEV_LENGTH);
+        const int s = dec_shared(shared, slen[sgroup[g]]);
+        if (slen[r] >= s) base = s;
+      }
+      sbase[r] = base;
+      if (report) {
+        args.member[r] = g < 0 ? make_int4(-1, r, 1, 0) : make_int4(g, sgroup[g], sgroup[g + 1] - sgroup[g], base);
+      }
+    }
+    __syncthreads();
+    // the tcgen05 kernel's ticks
+    int tall = 0;
+    if (args.tall && grouped)
+      for (int g = tid; g < ng; g += kDecThreads) {
+        const int first = sgroup[g], rows = (sgroup[g + 1] - first) * G;
+        if (rows > kDecFlatRows && sbase[first] > 0)
+          tall += a.Hkv * ((rows + kDecTallRows - 1) / kDecTallRows) * ((sbase[first] + kDecTile - 1) / kDecTile + kDecTallEnd);
+      }
+    tall = __reduce_add_sync(FULL, tall);
+    if (args.tall && lane == 0 && tall) atomicAdd(&s_tall, tall);
+    auto ticks_of = [&](int s) {
+      if (s < ng) {
+        const int first = grouped ? sgroup[s] : 0, rows = grouped ? (sgroup[s + 1] - first) * G : 0;
+        const bool here = rows > 0 && sbase[first] > 0 && !(args.tall && rows > kDecFlatRows);  // (else it is the tcgen05 kernel's)
+        return here ? a.Hkv * ((rows + kDecRows - 1) / kDecRows) * (unit_ticks(0, sbase[first]) + kEndTicks) : 0;
+      }
+      return a.Hkv * args.own_tiles * (unit_ticks(sbase[s - ng], slen[s - ng]) + kEndTicks);
+    };
+    {
+      const int segs = ng + a.b;
+      int run = 0;
+      for (int s0 = 0; s0 < segs; s0 += kDecThreads) {
+        const int s = s0 + tid, t = s < segs ? ticks_of(s) : 0;
+        int incl = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(FULL, incl, o);
+          if (lane >= o) incl += y;
+        }
+        __syncthreads();
+        if (lane == 31) wsum[w] = incl;
+        __syncthreads();
+        int before = run;
+        for (int q = 0; q < kDecThreads / 32; ++q) {
+          if (q < w) before += wsum[q];
+          run += wsum[q];
+        }
+        if (s < segs) pre[s] = before + incl - t;
+      }
+      if (tid == 0) pre[segs] = run;
+      __syncthreads();
+      if (report)
+        for (int s = tid; s <= segs; s += kDecThreads) args.pre[s] = pre[s];
+    }
+    const int T = pre[ng + a.b];  // (the host keeps it below 2^31)
+    // (at least four ticks a CTA: each on a unit has one of its tiles)
+    const int ctas = max(1, min(T >> 2, int(gridDim.x) - dec_tall_ctas(s_tall, T, a.b * a.Hkv * args.own_tiles, gridDim.x)));
+    if (report && tid == 0) *args.plan = make_int4(T, ctas, ng, 0);
+    if (int(blockIdx.x) >= ctas) {
+      if (args.tall) pdl_wait();
+      return;
+    }
+    S = int((long long)blockIdx.x * T / ctas);
+    E = int((long long)(blockIdx.x + 1) * T / ctas);
   }
-  const int T = pre[ng + a.b];  // (the host keeps it below 2^31)
-  // (at least four ticks a CTA: each on a unit has one of its tiles)
-  const int ctas = max(1, min(T >> 2, int(gridDim.x) - dec_tall_ctas(s_tall, T, gridDim.x)));
-  if (report && tid == 0) *args.plan = make_int4(T, ctas, ng, 0);
-  if (int(blockIdx.x) >= ctas) {
-    if (args.tall) pdl_wait();
-    return;
-  }
-  const int S = int((long long)blockIdx.x * T / ctas), E = int((long long)(blockIdx.x + 1) * T / ctas);
 
   auto open = [&](Unit& u, int seg) {  // the first unit of the first segment from `seg` on that has ticks
     while (seg < ng && pre[seg + 1] == pre[seg]) ++seg;
@@ -278,6 +313,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   };
   // the range's first unit, and the first of its tiles that is the CTA's
   auto locate = [&](Unit& u, int& t) {
+    if (CLUSTER) {
+      u = unit;
+      t = S;
+      return;
+    }
     int lo = 0, hi = ng + a.b;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -293,6 +333,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   };
   // the next unit; false behind the range
   auto next_unit = [&](Unit& u) {
+    if (CLUSTER) return false;
     u.u0 += u.ticks + kEndTicks;
     if (u.u0 >= E) return false;
     if (++u.rt == u.row_tiles) {
@@ -302,13 +343,50 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     return true;
   };
   // tiles of the unit in the range, from tile t on
-  auto tiles_from = [&](const Unit& u, int t) { return min(u.tiles(), (E - u.u0 + 3) >> 2) - t; };
+  auto tiles_from = [&](const Unit& u, int t) { return CLUSTER ? E - t : min(u.tiles(), (E - u.u0 + 3) >> 2) - t; };
   // Who takes a part of n tiles of a unit: a warp (0 .. 7), four (8, 9), or all (-1).  parts: how many of either kind
   // came before in the range.
   auto owner_of = [&](const Unit& u, int n, int2& parts) {
     if (u.rows - u.row0() > 16) return -1;
+    if (CLUSTER) return kConsumers;
     if (n <= kSoloTiles && E - S > kSoloRange * 4 * n) return parts.x++ % kConsumers;
     return kConsumers + (parts.y++ & 1);
+  };
+  // CLUSTER: the CTA's results lie where the ring was, O as [row][D], then each row's (m, l); the cluster's CTAs each join
+  // a share of the words.
+  auto join_cluster = [&] {
+    cluster_sync();
+    const int size = gridDim.x, words = G * (D / 4), w1 = int((blockIdx.x + 1ll) * words / size);
+    for (int x = int((long long)blockIdx.x * words / size) + tid; x < w1; x += kDecThreads) {
+      const int row = x / (D / 4), c = x - row * (D / 4);
+      float2 ml[kClusterMost];
+      float4 y[kClusterMost];
+      float M = -INFINITY, Ls = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < kClusterMost; ++q) {
+        ml[q] = make_float2(-INFINITY, 0.f);
+        if (q < size) {
+          ml[q] = cluster_ld2(cluster_addr(smem + L::kStage + row * 8, q));
+          y[q] = cluster_ld4(cluster_addr(smem + x * 16, q));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kClusterMost; ++q) M = fmaxf(M, ml[q].x);
+#pragma unroll
+      for (int q = 0; q < kClusterMost; ++q) {
+        const float wt = dec_weight(ml[q].x, M);
+        if (wt == 0.f) continue;
+        Ls = fmaf(ml[q].y, wt, Ls);
+        acc = make_float4(fmaf(y[q].x, wt, acc.x), fmaf(y[q].y, wt, acc.y), fmaf(y[q].z, wt, acc.z), fmaf(y[q].w, wt, acc.w));
+      }
+      const float inv = dec_inverse(Ls);
+      const size_t orow = size_t(unit.r0) * a.Hq + unit.h * G + row;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + 4 * c) =
+          make_uint2(dec_pack(acc.x * inv, acc.y * inv), dec_pack(acc.z * inv, acc.w * inv));
+      if (c == 0 && a.lse) a.lse[orow] = dec_lse(M, Ls);
+    }
+    cluster_sync();  // (no CTA ends while another reads its shared memory)
   };
   __syncthreads();  // (sgroup is not read any more)
 
@@ -337,7 +415,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     auto look = [&](int half) {
       heads[half] = -1;
       while (n <= 0) {  // over a unit's end
-        if (!more || !(more = next_unit(u))) return;
+        more = more && next_unit(u);
+        if (!more) return;
         t = 0;
         n = tiles_from(u, 0);
         entered = false;
@@ -424,6 +503,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
       *abort_flag = 1;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (CLUSTER) join_cluster();
     return;
   }
 
@@ -575,6 +655,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   // Two columns of a row's result (unnormalised, relative to M): out, or a partial result.
   auto put = [&](const Unit& u, int row, int col, bool whole, bool begun, float M, float Ls, float s0, float s1, bool note) {
     const int h = u.h, row0 = u.row0();
+    if (CLUSTER) {
+      *reinterpret_cast<float2*>(smem + (row * D + col) * 4) = make_float2(s0, s1);
+      if (note) *reinterpret_cast<float2*>(smem + L::kStage + row * 8) = make_float2(M, Ls);
+      return;
+    }
     const bool own = u.seg >= ng;
     const int f = row / G;
     const size_t orow = (size_t(u.r0) + f) * a.Hq + h * G + (row - f * G);
@@ -685,7 +770,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   locate(u, t);
   do {
     const int n = tiles_from(u, t);
-    if (n > 0) {
+    if (n > 0 || CLUSTER) {  // (a CTA of a cluster without a tile leaves an empty result)
       const int who = owner_of(u, n, parts);
       if (who < 0) {
         if (u.rows - u.row0() <= 32) work(std::integral_constant<int, 2>{}, u, t, n, who);
@@ -700,7 +785,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     }
     t = 0;
   } while (next_unit(u));
-  if (args.tall) pdl_wait();
+  if (CLUSTER) join_cluster();
+  else if (args.tall) pdl_wait();
 }
 
 // Joins the partial results: a thread a word of four columns of a row.  The rows of a group come in the order of its units,
@@ -818,14 +904,25 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
 template <int D>
 int launch_decode(const DecodeArgs& args, int sms, cudaStream_t stream) {
   const DecodeParams& p = args.p;
+  if (p.num_groups == 0 && args.own_tiles == 1) {
+    const long long units = (long long)p.b * p.Hkv;
+    const int size = cluster_of(units, sms);
+    constexpr int tile = DecSmem<D>::kTile, smem = DecSmem<D>::kScan;
+    if ((long long)size * kClusterTiles * tile >= p.max_seq_len && size > 0) {
+      if (cudaFuncSetAttribute(decode_attention_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return SPEC_ERR_LAUNCH;
+      return launch_cluster(decode_attention_kernel<D, true>, size, dim3(size, unsigned(units)), dim3(kDecThreads), smem, stream, args) == cudaSuccess
+                 ? SPEC_OK
+                 : SPEC_ERR_LAUNCH;
+    }
+  }
   const size_t smem = DecSmem<D>::bytes(p.b, p.num_groups);
-  if (cudaFuncSetAttribute(decode_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(decode_attention_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            int(DecSmem<D>::bytes(kDecodeMaxB, kDecodeMaxB))) != cudaSuccess)  // (the most, so that calls of two threads agree)
     return SPEC_ERR_LAUNCH;
   const int grid = sms < kDecMaxCtas ? sms : kDecMaxCtas;
   if (args.tall)
     if (const int rc = launch_decode_tall(args, sms, stream)) return rc;
-  if (launch_pdl(decode_attention_kernel<D>, dim3(grid), dim3(kDecThreads), smem, stream, args) != cudaSuccess) return SPEC_ERR_LAUNCH;
+  if (launch_pdl(decode_attention_kernel<D, false>, dim3(grid), dim3(kDecThreads), smem, stream, args) != cudaSuccess) return SPEC_ERR_LAUNCH;
   constexpr int rows = kJoinThreads / (D / 4);
   const unsigned blocks = unsigned((size_t(p.b) * p.Hq + rows - 1) / rows);
   return launch_pdl(decode_join_kernel<D>, dim3(blocks), dim3(kJoinThreads), 0, stream, args) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;

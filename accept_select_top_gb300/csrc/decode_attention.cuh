@@ -34,13 +34,14 @@ constexpr int kDecTallRows = 256;  // query rows of one of its units
 constexpr int kDecTallEnd = 2;     // what a unit's end costs there in the division of the work, in tiles
 
 // The two kernels of a call run side by side: of `ctas` SMs the tcgen05 kernel takes so many, by the ticks of both (one
-// of its tiles takes as long as so many of the other's ticks), and the rest of its CTAs leave at once, so that the other
-// kernel's, launched behind them, find their SMs free.
-constexpr int kDecTallCost = 4;
-__device__ __forceinline__ int dec_tall_ctas(int tall, int flat, int ctas) {
+// of its tiles takes as long as kDecTallCost of the other's ticks, and a unit there, of which a few SMs may have to take
+// hundreds, kDecUnitCost more than its end's), and the rest of its CTAs leave at once, so that the other kernel's, launched
+// behind them, find their SMs free.
+constexpr int kDecTallCost = 4, kDecUnitCost = 2;
+__device__ __forceinline__ int dec_tall_ctas(int tall, int flat, int units, int ctas) {
   if (tall == 0) return 0;
-  const long long cost = (long long)tall * kDecTallCost;
-  const int n = int((cost * ctas + (cost + flat) / 2) / (cost + flat));
+  const long long cost = (long long)tall * kDecTallCost, rest = flat + (long long)units * kDecUnitCost;
+  const int n = int((cost * ctas + (cost + rest) / 2) / (cost + rest));
   return n < 1 || ctas == 1 ? 1 : n > ctas - 1 ? ctas - 1 : n;
 }
 constexpr int kDecTickKeys128 = 16;  // keys of a tick of the other kernel, of D 128 (64: twice as many)

@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
   tc_after();
   const uint32_t tmem = *tmem_holder;
   const int T = pre[ng];
-  const int ctas = min(T, dec_tall_ctas(T, *s_flat, gridDim.x));
+  const int ctas = min(T, dec_tall_ctas(T, *s_flat, a.b * a.Hkv * args.own_tiles, gridDim.x));
   const bool part = int(blockIdx.x) < ctas;
   const int S = part ? int((long long)blockIdx.x * T / ctas) : 0, E = part ? int((blockIdx.x + 1ll) * T / ctas) : 0;
   if (blockIdx.x == 0) {
