@@ -37,8 +37,10 @@ constexpr int kConsumers = 8, kProducers = 4;
 constexpr int kDecThreads = 32 * (kConsumers + kProducers);
 constexpr int kRing = 5;
 // A cluster takes a unit where all of them run at once (a GB300 holds 15 clusters of eight CTAs of a SM each, 36 of four,
-// 76 of two) and a CTA gets at most so many tiles; else the SMs share the work, and a second launch joins it.
-constexpr int kClusterMost = 8, kClusterTiles = 8;
+// 76 of two) and a CTA gets at most so many tiles; else the SMs share the work, and a second launch joins it.  In us, cluster /
+// all SMs, 32 / 8 heads of 128: one request of 1000 tokens 6.5 / 12.4, 8192 (16 tiles a CTA) 13.9 / 17.7, 16384 22.6 / 22.1; eight
+// of 1000 9.4 / 17.5, 2048 (16) 13.8 / 22.0, 4096 27 / 34.
+constexpr int kClusterMost = 8, kClusterTiles = 24;
 inline int cluster_of(long long units, int sms) { return units <= 14 ? 8 : units <= 34 ? 4 : units <= 72 ? 2 : units <= sms ? 1 : 0; }
 constexpr int kOwners = kConsumers + 2;  // who may have a part to itself: a warp, or four of them
 // A part of at most so many tiles, where the CTA's range is so many times longer, goes to one warp.
