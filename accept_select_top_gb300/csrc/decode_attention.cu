@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     if (args.tall && grouped)
       for (int g = tid; g < ng; g += kDecThreads) {
         const int first = sgroup[g], rows = (sgroup[g + 1] - first) * G;
-        if (rows > kDecFlatRows && sbase[first] > 0)
+        if (rows > args.flat_rows && sbase[first] > 0)
           tall += a.Hkv * ((rows + kDecTallRows - 1) / kDecTallRows) * ((sbase[first] + kDecTile - 1) / kDecTile + kDecTallEnd);
       }
     tall = __reduce_add_sync(FULL, tall);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     auto ticks_of = [&](int s) {
       if (s < ng) {
         const int first = grouped ? sgroup[s] : 0, rows = grouped ? (sgroup[s + 1] - first) * G : 0;
-        const bool here = rows > 0 && sbase[first] > 0 && !(args.tall && rows > kDecFlatRows);  // (else it is the tcgen05 kernel's)
+        const bool here = rows > 0 && sbase[first] > 0 && !(args.tall && rows > args.flat_rows);  // (else it is the tcgen05 kernel's)
         return here ? a.Hkv * ((rows + kDecRows - 1) / kDecRows) * (unit_ticks(0, sbase[first]) + kEndTicks) : 0;
       }
       return a.Hkv * args.own_tiles * (unit_ticks(sbase[s - ng], slen[s - ng]) + kEndTicks);
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   int n_sh = 0;
   // what the request shares: the first kernel's partial results, or the tcgen05 kernel's
   Span sh{0, 0};
-  const bool tall = args.tall && all > kDecFlatRows;
+  const bool tall = args.tall && all > args.flat_rows;
   const int size = tall ? kDecTallRows : kDecRows, x0 = x / size * size, rows = min(size, all - x0), xr = x - x0;
   const bool split = tall && rows <= 128;
   if (base > 0) {
@@ -962,7 +962,7 @@ struct DecodeLayout {
   }
 };
 // whether a group of the batch may have more rows than the register kernel takes
-bool may_be_tall(int b, int Hq, int Hkv) { return (long long)b * (Hq / Hkv) > kDecFlatRows; }
+bool may_be_tall(int b, int Hq, int Hkv) { return (long long)b * (Hq / Hkv) > dec_flat_rows(128); }
 
 }  // namespace
 
@@ -976,7 +976,7 @@ int launch_decode_attention(const DecodeParams& p, cudaStream_t stream) {
   // The groups are not known here, but their mean is: where it is far below what the tcgen05 kernel takes, its launch
   // (5 us) is left out, and a large group among small ones takes the other kernel's tiles of 64 rows.
   // (A scale of zero would take the -inf of a key that does not count to NaN there.)
-  const bool tall = p.num_groups > 0 && may_be_tall(p.b, p.Hq, p.Hkv) && (long long)p.b * (p.Hq / p.Hkv) > kDecFlatRows / 2 * (long long)p.num_groups &&
+  const bool tall = p.num_groups > 0 && may_be_tall(p.b, p.Hq, p.Hkv) && (long long)p.b * (p.Hq / p.Hkv) > dec_flat_rows(p.D) / 2 * (long long)p.num_groups &&
                     p.scale != 0.f;
   const DecodeLayout at(p.b, p.Hq, p.D, tall);
   unsigned char* ws = p.partials;
@@ -985,6 +985,7 @@ int launch_decode_attention(const DecodeParams& p, cudaStream_t stream) {
   for (args.shift = 0; (1 << args.shift) < p.page_size; ++args.shift) {
   }
   args.own_tiles = (p.Hq / p.Hkv + kDecRows - 1) / kDecRows;
+  args.flat_rows = dec_flat_rows(p.D);
   args.plan = reinterpret_cast<int4*>(ws);
   args.pre = reinterpret_cast<int*>(ws + at.pre);
   args.member = reinterpret_cast<int4*>(ws + at.member);

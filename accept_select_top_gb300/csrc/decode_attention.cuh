@@ -28,8 +28,10 @@ __device__ __forceinline__ float dec_lse(float m, float l) {
   return l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-// Rows of a group's shared tokens (members times q heads of a kv head) above which the tcgen05 kernel takes them.
-constexpr int kDecFlatRows = 32;
+// Rows of a group's shared tokens (members times q heads of a kv head) above which the tcgen05 kernel takes them.  In us,
+// there / in the other kernel: heads of 128, eight groups of 4096 tokens and 32 rows 50 / 56, 20 rows 47 / 54, two of 16384 and 32
+// rows 47 / 54; heads of 64, 16 groups of 1024 and 24 rows 34 / 29.
+constexpr int dec_flat_rows(int D) { return D == 128 ? 16 : 32; }
 constexpr int kDecTallRows = 256;  // query rows of one of its units
 constexpr int kDecTallEnd = 2;     // what a unit's end costs there in the division of the work, in tiles
 
@@ -63,6 +65,7 @@ struct DecodeArgs {
   DecodeParams p;
   int shift;       // log2(page_size)
   int own_tiles;   // 64-row tiles of a kv head's rows of one request
+  int flat_rows;   // dec_flat_rows
   int4* plan;
   int* pre;        // [groups + b + 1]
   int4* member;    // [b]: {group (-1: none), its first request, its members, tokens shared}

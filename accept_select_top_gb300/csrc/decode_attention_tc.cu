@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
     if (!grouped || g >= ng) return;
     p.r0 = __ldg(a.group_start + g);
     p.rows = (__ldg(a.group_start + g + 1) - p.r0) * G;
-    if (p.rows <= kDecFlatRows) return;
+    if (p.rows <= args.flat_rows) return;
     const int row = __ldg(a.req_pool_idx + p.r0), len = min(max(__ldg(a.seq_lens + p.r0), 0), most);
     if (row < 0 || row >= a.req_rows) return;
     p.shared = dec_shared(__ldg(a.shared_lens + g), len);
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
         }
         const int first = sgroup[lo], rows = (sgroup[lo + 1] - first) * G, s = dec_shared(__ldg(a.shared_lens + lo), len_of(first));
         base = len >= s ? s : 0;
-        if (r == first && s > 0 && rows <= kDecFlatRows) flat += a.Hkv * ((rows + kDecRows - 1) / kDecRows) * (dec_unit_ticks<D>(0, s) + kDecEndTicks);
+        if (r == first && s > 0 && rows <= args.flat_rows) flat += a.Hkv * ((rows + kDecRows - 1) / kDecRows) * (dec_unit_ticks<D>(0, s) + kDecEndTicks);
       }
       flat += a.Hkv * own_tiles * (dec_unit_ticks<D>(base, len) + kDecEndTicks);
     }
