@@ -1042,6 +1042,22 @@ bool table_ok(int b, int page_size, int64_t num_pages, int req_rows, int row_pag
          int64_t(row_pages) * page_size < (int64_t(1) << 31) && int64_t(b) * row_pages < (int64_t(1) << 31);
 }
 
+// Arrays that a call writes, which may lie over none of those that it reads to its end, nor over one another.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+template <size_t N, size_t M>
+bool clash(const Span (&written)[N], const Span (&read)[M]) {
+  for (size_t i = 0; i < N; ++i) {
+    for (size_t k = 0; k < i; ++k)
+      if (overlap(written[i].p, written[i].bytes, written[k].p, written[k].bytes)) return true;
+    for (const Span& r : read)
+      if (overlap(written[i].p, written[i].bytes, r.p, r.bytes)) return true;
+  }
+  return false;
+}
+
 bool vec_slots(const void* slots, int row_w, int page_size) { return page_size % 4 == 0 && row_w % 4 == 0 && aligned(slots, 16); }
 
 }  // namespace
@@ -1056,9 +1072,13 @@ int spec_fork_pages(int b, int page_size, const int32_t* parents, const int32_t*
   if (!table_ok(b, page_size, num_pages, req_rows, row_pages, req_to_token, row_w) || free_cap < 0) return SPEC_ERR_ARG;
   if (b == 0) return SPEC_OK;
   if (!parents || !children || !fork_lens || !share_counts || !n_free || !page_table || !copy_src || !copy_dst ||
-      !n_copies || !n_left || n_copies == n_left || n_copies == n_free || (!free_ids && free_cap > 0))
+      !n_copies || !n_left || n_copies == n_free || (!free_ids && free_cap > 0))
     return SPEC_ERR_ARG;
   if (int rc = check_ws(ws, ws_bytes, kHeaderBytes + counters_bytes(b))) return rc;
+  const size_t row = size_t(b) * 4;
+  const Span written[] = {{copy_src, row}, {copy_dst, row}, {n_copies, 4}, {n_left, 4}};
+  const Span read[] = {{parents, row}, {children, row}, {fork_lens, row}, {free_ids, size_t(free_cap) * 4}};
+  if (clash(written, read)) return SPEC_ERR_ARG;
   note_other(ws);
   const WsView v = ws_view(ws, b);
   ForkParams p{};
@@ -1130,10 +1150,17 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
     return SPEC_ERR_ARG;
   if (b == 0) return SPEC_OK;
   if (!req_pool_idx || !seq_lens || !share_counts || !n_free || !page_table || !new_share_counts || !n_left ||
-      !new_page_table || !n_moves || n_moves == n_left || n_moves == n_free || (req_to_token && !new_req_to_token) ||
+      !new_page_table || !n_moves || n_moves == n_free || (req_to_token && !new_req_to_token) ||
       ((!free_ids || !new_free_ids || !move_src || !move_dst) && free_cap > 0))
     return SPEC_ERR_ARG;
   if (int rc = check_ws(ws, ws_bytes, spec_workspace_size(SPEC_OP_COMPACT_PAGES, b, 1, 1, int(num_pages), 0, 0, 0))) return rc;
+  const size_t row = size_t(b) * 4, list = size_t(free_cap) * 4, counts = size_t(num_pages) * 4;
+  const Span written[] = {{move_src, list}, {move_dst, list}, {n_moves, 4}, {n_left, 4}, {new_free_ids, list}, {new_share_counts, counts}};
+  const Span read[] = {{req_pool_idx, row}, {seq_lens, row}};
+  if (clash(written, read)) return SPEC_ERR_ARG;
+  // (the lists of moves are written while the first list is still read, and read while the counts are written)
+  const Span moves[] = {{move_src, list}, {move_dst, list}}, other[] = {{free_ids, list}, {share_counts, counts}};
+  if (clash(moves, other)) return SPEC_ERR_ARG;
   note_other(ws);
   const WsView v = ws_view(ws, b);
   CompactParams p{};
@@ -1225,8 +1252,11 @@ int spec_decode_attention(int b, int Hq, int Hkv, int D, int page_size, const vo
       (num_groups && (!group_start || !shared_lens)))
     return SPEC_ERR_ARG;
   if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16)) return SPEC_ERR_ARG;
-  // (a request's results are written while another's q is still read)
-  if (overlap(q, (size_t(b - 1) * q_ld + size_t(Hq) * D) * 2, out, size_t(b) * Hq * D * 2)) return SPEC_ERR_ARG;
+  // (a request's results are written while others are still worked on)
+  const Span written[] = {{out, size_t(b) * Hq * D * 2}, {lse, size_t(b) * Hq * 4}};
+  const Span read[] = {{q, (size_t(b - 1) * q_ld + size_t(Hq) * D) * 2}, {req_pool_idx, size_t(b) * 4}, {seq_lens, size_t(b) * 4},
+                       {group_start, size_t(num_groups + 1) * 4}, {shared_lens, size_t(num_groups) * 4}};
+  if (clash(written, read)) return SPEC_ERR_ARG;
   if (int rc = check_ws(ws, ws_bytes, spec_workspace_size(SPEC_OP_DECODE_ATTENTION, b, 1, 1, 1, Hq, Hkv, max_seq_len))) return rc;
   note_other(ws);
   const WsView v = ws_view(ws, b);

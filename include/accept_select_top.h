@@ -593,9 +593,10 @@ int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size
  * and (copy_src[j], copy_dst[j]) = (the parent's page, it) is a pair for
  * spec_copy_pages (arrays of b).  n_copies [1] = those pages, n_left [1] = n_free
  * less them (may be n_free itself).  req_to_token (nullable): entries [0, L) of
- * the child's row.  A parent may have many children; the children are distinct
- * rows, none of them a parent in the call (a child that is its own parent sets
- * SPEC_DEV_INDEX).  A bad length or row leaves its child as it was
+ * the child's row.  A parent may have many children, and L be less than it has;
+ * the children are distinct rows that hold no pages, none of them a parent in the
+ * call (a child that is its own parent sets SPEC_DEV_INDEX).  The written arrays
+ * lie over none of the lists that the call reads (SPEC_ERR_ARG).  A bad length or row leaves its child as it was
  * (SPEC_DEV_LENGTH / SPEC_DEV_INDEX); too short a free list sets SPEC_DEV_SPACE and
  * the call does nothing (n_copies 0, n_left = n_free).  A bad page id gives an entry
  * (and slots) of -1 and SPEC_DEV_INDEX.
@@ -648,7 +649,8 @@ int spec_release_pages(int b, int page_size, const int32_t* req_pool_idx, const 
  * new_share_counts [num_pages] follow the pages.  new_free_ids: the n_left[0] free
  * pages, highest first, so that the lowest are handed out first and a pool cut to
  * N pages drops the first num_pages - N of them.
- * Each output may be its input (n_left may be n_free).  Where the tables are arrays of their own, the old
+ * Each output may be its input (n_left may be n_free); the lists of moves lie over
+ * nothing else, and no output over seq_lens or req_pool_idx (SPEC_ERR_ARG).  Where the tables are arrays of their own, the old
  * ones stay readable, and so do the moved pages until their ids are handed out.
  * A bad id on the free list is passed over (SPEC_DEV_INDEX), one listed twice
  * counts once (SPEC_DEV_INVARIANT), as does a table entry that is on it; a bad table
@@ -675,7 +677,8 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
  * seq_lens[r]-1, the new one's K and V being in the pools already:
  *   out[r, h] = softmax(scale * q.K^T) V,  lse (nullable) = its natural-log
  * sum-exp.  out: [b, Hq, D] bf16, lse: [b, Hq] fp32.  A request without a token
- * gives out 0 and lse -inf.  out does not overlap q (SPEC_ERR_ARG).
+ * gives out 0 and lse -inf.  out and lse lie over none of q, the lengths, rows and
+ * groups, nor over one another (SPEC_ERR_ARG).
  *   Group g: requests group_start[g] .. group_start[g+1]-1 (ascending, [num_groups
  * + 1]; requests before the first and behind the last are in none), whose tables
  * name the same pages for their tokens 0 .. shared_lens[g]-1; these are read
@@ -683,7 +686,8 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
  * tokens through its own row, and so does every one where the first member is
  * shorter.  num_groups 0: both arrays may be NULL.  Group bounds that descend or
  * leave the batch set SPEC_DEV_INDEX, and nothing is shared; a negative shared
- * length, or one above max_seq_len, sets SPEC_DEV_LENGTH.
+ * length, or one above max_seq_len, sets SPEC_DEV_LENGTH.  Requests that share
+ * nothing are best left out of the groups: which kernels run goes by their mean size.
  *   max_seq_len bounds every seq_len (a larger one sets SPEC_DEV_LENGTH and is
  * clamped).  A page id out of range sets SPEC_DEV_INDEX and its keys do not count;
  * a bad table row leaves its request without tokens.  What the pools hold behind a

@@ -162,6 +162,19 @@ def test_members_shorter_than_the_shared_tokens():
     c.check(*c.call())
 
 
+@pytest.mark.parametrize("Hq, Hkv", [(8, 8), (40, 2), (64, 1), (96, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_requests(D, Hq, Hkv):
+    """Units that clusters of every size take, some of them without a token, up to 64 rows."""
+    for b in (1, 4, 9, 30):
+        lens = [(i * 397) % 1500 for i in range(b)]
+        c = Case([], lens, Hq=Hq, Hkv=Hkv, D=D, seed=b)
+        c.check(*c.call())
+    c = Case([], [0], Hq=Hq, Hkv=Hkv, D=D)
+    c.check(*c.call(most=0))
+    c.check(*c.call(most=9000))
+
+
 @pytest.mark.parametrize("b, most", [(1, 1), (1, 40000), (3, 20000), (200, 900), (2048, 70)])
 def test_batches(b, most):
     gen = _gen(b)

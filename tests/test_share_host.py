@@ -18,7 +18,7 @@ def lib():
 
 def _fork(**change):
     a = dict(b=2, ps=16, parents=FAKE, children=FAKE, lens=FAKE, counts=FAKE, pages=10, free=FAKE, cap=8, n_free=FAKE, table=FAKE, rows=4, row_pages=8, slots=None, row_w=0,
-             src=FAKE, dst=FAKE, copies=FAKE + 64, left=FAKE, ws=FAKE, ws_bytes=4096, stream=None)
+             src=FAKE + 128, dst=FAKE + 192, copies=FAKE + 64, left=FAKE + 256, ws=FAKE, ws_bytes=4096, stream=None)
     a.update(change)
     return list(a.values())
 
@@ -30,6 +30,11 @@ def _fork(**change):
     (dict(copies=None), -1), (dict(left=None), -1), (dict(copies=FAKE), -1), (dict(ws=None), -2), (dict(ws=FAKE + 16), -2), (dict(ws_bytes=512), -2), (dict(b=0, parents=None), 0)])
 def test_fork_refusals(lib, change, code):
     assert lib.spec_fork_pages(*_fork(**change)) == code
+
+
+@pytest.mark.parametrize("change", [dict(src=FAKE + 4), dict(dst=FAKE + 28), dict(src=FAKE + 196), dict(copies=FAKE + 196), dict(left=FAKE + 64), dict(left=FAKE + 4), dict(copies=FAKE + 132)])
+def test_fork_refuses_outputs_over_what_it_reads(lib, change):
+    assert lib.spec_fork_pages(*_fork(**change)) == -1
 
 
 def _release(**change):
@@ -58,6 +63,13 @@ def _compact(**change):
     (dict(ws=None), -2), (dict(pages=1 << 22), -2), (dict(b=0, idx=None), 0)])
 def test_compact_refusals(lib, change, code):
     assert lib.spec_compact_pages(*_compact(**change)) == code
+
+
+@pytest.mark.parametrize("change", [dict(src=FAKE + 4140), dict(dst=FAKE), dict(moves=FAKE + 4096), dict(left=FAKE + 4), dict(new_free=FAKE + 4), dict(new_counts=FAKE + 4), dict(src=FAKE + 8196),
+                                    dict(dst=FAKE + 12292), dict(left=FAKE + 64)])
+def test_compact_refuses_outputs_over_what_it_reads(lib, change):
+    apart = dict(idx=FAKE, lens=FAKE, src=FAKE + 4096, dst=FAKE + 4160, moves=FAKE + 64, left=FAKE + 128, free=FAKE + 8192, new_free=FAKE + 8192, counts=FAKE + 12288, new_counts=FAKE + 12288)
+    assert lib.spec_compact_pages(*_compact(**{**apart, **change})) == -1
 
 
 def _copy(hole=None, **change):
