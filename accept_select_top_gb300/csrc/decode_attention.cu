@@ -7,8 +7,8 @@
 // so a group's shared tokens are read once for all its rows.
 //
 // P is rounded to bf16, V's type (half a step 2^-8; with random values out is off by 1.4 times what its own rounding
-// makes it); the sums l and O are fp32.  (P in two bf16 parts, whose products are exact to 2^-16, costs 3 to 11%: the batch
-// below 388 us.)
+// makes it); the sums l and O are fp32.  (P in two bf16 parts, whose products are exact to 2^-16, costs 2 to 11%: the batch
+// below 388 us, not 363.)
 //
 // Bound: the cache's bytes.  A segment is a group's shared tokens (rows: every member's q heads of a kv head) or a
 // request's own tokens; a unit is (segment, kv head, up to 64 rows).  One CTA a SM takes an equal contiguous

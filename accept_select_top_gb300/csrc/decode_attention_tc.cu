@@ -14,8 +14,8 @@
 //   Every piece of a unit leaves an fp32 partial result; decode_attention.cu joins them.
 //   Bound: up to 128 rows the cache's bytes (eight groups of 12 requests, 32768 shared tokens, 32 / 8 heads: 193 us a call,
 // 1.1 GB); 256 rows: shared memory.  S with both operands there reads 6 KB in 32 cycles of the tensor cores, so that a tile
-// is 1280 cycles of products and 256 of the copies' writes; measured 1790, of the 1400 in which it comes from memory (two
-// documents of 65536, 32 requests of 64 / 8 heads each: 132 us, 1.04 PF/s).  K and V in rings of their own, TMA boxes of 16
+// is 1280 cycles of products and 256 of the copies' writes; measured 1790; from memory it comes in 1400 (two documents
+// of 65536 tokens, 32 requests of 64 / 8 heads each: 132 us, 1.04 PF/s).  K and V in rings of their own, TMA boxes of 16
 // keys (what a page holds for certain; 30 GB/s a SM) and Q in TMEM, with one S a group, are slower by 8, 15 and 29%.
 //   Every wait is bounded: on timeout the CTA sets SPEC_DEV_TIMEOUT, stops, drains its copies and MMAs and frees its TMEM.
 #include "common.cuh"
@@ -201,10 +201,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-__device__ __forceinline__ float pow2(int d) {  // 2^d, d clamped to [-126, 127]
-  d = d < -126 ? -126 : d > 127 ? 127 : d;
-  return __uint_as_float(uint32_t(127 + d) << 23);
-}
+// 2^d of a whole number d <= 0; 0 below 2^-126 (as ex2 gives it: a larger factor would leave values of no weight standing)
+__device__ __forceinline__ float pow2(float d) { return d >= -126.f ? __uint_as_float(uint32_t(127 + int(d)) << 23) : 0.f; }
 
 // A place in the tick space: a group's shared tokens, (kv head, row block), tile.
 struct Place {
@@ -658,11 +656,11 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
             for (int i = 0; i < 16; ++i)
               if (bits >> i & 1u) mx = fmaxf(mx, __uint_as_float(v[i]) * xf);
           }
-          // the reference becomes a whole number, so that O and l are multiplied by a power of two, exactly
+          // the reference becomes a whole number, so that O and l are multiplied by a power of two, exactly (or by 0)
           float fac = 1.f;
           if (mx > m + kDecBase) {
             const float mn = ceilf(mx) - kDecBase;
-            fac = m == -INFINITY ? 1.f : pow2(int(fmaxf(m - mn, -126.f)));
+            fac = m == -INFINITY ? 1.f : pow2(m - mn);
             l *= fac;
             m = mn;
           }

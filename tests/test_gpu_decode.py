@@ -230,6 +230,20 @@ def test_values_of_the_types_ends():
     c.check(*c.call())
 
 
+@pytest.mark.parametrize("members", [2, 12])
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_values_of_no_weight(D, members):
+    """Keys whose scores lie hundreds below the others', seen first, with values near the type's largest."""
+    c = Case([(384, [400 + r for r in range(members)])], [500], Hq=4, Hkv=1, D=D)
+    c.q[..., 0] = 8.0
+    for r in (0, members):  # what the group shares, and the request alone
+        at = c.slots_of(r)
+        c.k[at, 0, 0] = 0.0
+        c.k[at[:256], 0, 0] = -400.0
+        c.v[at[:256]] = 2.0 ** 127
+    c.check(*c.call())
+
+
 def test_infinities_and_nans_reach_who_sees_them():
     c = Case([(64, [100, 90])], [80, 70], Hq=4, Hkv=1)
     out, lse = c.call()
