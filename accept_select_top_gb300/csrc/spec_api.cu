@@ -1035,11 +1035,15 @@ int verify_greedy_compact(int b, int n, int S, int V, int dtype, const void* log
 
 namespace {
 
-// What the calls that walk table rows have in common: sizes whose products stay below 2^31.
-bool table_ok(int b, int page_size, int64_t num_pages, int req_rows, int row_pages, const void* slots, int row_w) {
-  return b >= 0 && b <= kAllocMaxB && page_size >= 1 && num_pages >= 1 && req_rows >= 1 && row_pages >= 1 &&
-         (!slots || row_w >= 1) && num_pages <= ((int64_t(1) << 31) - 1) / page_size &&
-         int64_t(row_pages) * page_size < (int64_t(1) << 31) && int64_t(b) * row_pages < (int64_t(1) << 31);
+// What the calls that walk table rows have in common.  kMostPages leaves the sums of an index and a grid's stride below
+// 2^31, kMostPageSize those of the slots that a CTA writes at a time.
+constexpr int64_t kMostPages = int64_t(1) << 30;
+constexpr int kMostPageSize = 1 << 20;
+bool table_ok(int b, int page_size, int64_t num_pages, int free_cap, int req_rows, int row_pages, const void* slots, int row_w) {
+  return b >= 0 && b <= kAllocMaxB && page_size >= 1 && page_size <= kMostPageSize && num_pages >= 1 && num_pages <= kMostPages &&
+         free_cap >= 0 && free_cap <= kMostPages && req_rows >= 1 && row_pages >= 1 && (!slots || row_w >= 1) &&
+         num_pages <= ((int64_t(1) << 31) - 1) / page_size && int64_t(row_pages) * page_size < (int64_t(1) << 31) &&
+         int64_t(b) * row_pages <= kMostPages;
 }
 
 // Arrays that a call writes, which may lie over none of those that it reads to its end, nor over one another.
@@ -1069,7 +1073,7 @@ int spec_fork_pages(int b, int page_size, const int32_t* parents, const int32_t*
                     const int32_t* n_free, int32_t* page_table, int req_rows, int row_pages, int32_t* req_to_token,
                     int row_w, int32_t* copy_src, int32_t* copy_dst, int32_t* n_copies, int32_t* n_left, void* ws,
                     size_t ws_bytes, void* stream) {
-  if (!table_ok(b, page_size, num_pages, req_rows, row_pages, req_to_token, row_w) || free_cap < 0) return SPEC_ERR_ARG;
+  if (!table_ok(b, page_size, num_pages, free_cap, req_rows, row_pages, req_to_token, row_w)) return SPEC_ERR_ARG;
   if (b == 0) return SPEC_OK;
   if (!parents || !children || !fork_lens || !share_counts || !n_free || !page_table || !copy_src || !copy_dst ||
       !n_copies || !n_left || n_copies == n_free || (!free_ids && free_cap > 0))
@@ -1111,7 +1115,7 @@ int spec_release_pages(int b, int page_size, const int32_t* req_pool_idx, const 
                        const int32_t* keep_lens, int32_t* share_counts, int64_t num_pages, int32_t* free_ids,
                        int free_cap, const int32_t* n_free, const int32_t* page_table, int req_rows, int row_pages,
                        int32_t* n_left, void* ws, size_t ws_bytes, void* stream) {
-  if (!table_ok(b, page_size, num_pages, req_rows, row_pages, nullptr, 0) || free_cap < 0) return SPEC_ERR_ARG;
+  if (!table_ok(b, page_size, num_pages, free_cap, req_rows, row_pages, nullptr, 0)) return SPEC_ERR_ARG;
   if (b == 0) return SPEC_OK;
   if (!req_pool_idx || !seq_lens || !share_counts || !n_free || !page_table || !n_left || (!free_ids && free_cap > 0))
     return SPEC_ERR_ARG;
@@ -1146,7 +1150,7 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
                        const int32_t* req_to_token, int row_w, int32_t* new_share_counts, int32_t* new_free_ids,
                        int32_t* n_left, int32_t* new_page_table, int32_t* new_req_to_token, int32_t* move_src,
                        int32_t* move_dst, int32_t* n_moves, void* ws, size_t ws_bytes, void* stream) {
-  if (!table_ok(b, page_size, num_pages, req_rows, row_pages, req_to_token, row_w) || free_cap < 0 || limit < 0)
+  if (!table_ok(b, page_size, num_pages, free_cap, req_rows, row_pages, req_to_token, row_w) || limit < 0)
     return SPEC_ERR_ARG;
   if (b == 0) return SPEC_OK;
   if (!req_pool_idx || !seq_lens || !share_counts || !n_free || !page_table || !new_share_counts || !n_left ||
@@ -1236,7 +1240,7 @@ int spec_decode_attention(int b, int Hq, int Hkv, int D, int page_size, const vo
                           int req_rows, int row_pages, const int32_t* req_pool_idx, const int32_t* seq_lens,
                           int max_seq_len, int num_groups, const int32_t* group_start, const int32_t* shared_lens,
                           float scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
-  if (b < 0 || b > kDecodeMaxB || Hq < 1 || Hkv < 1 || Hq % Hkv || max_seq_len < 0 || num_groups < 0 || num_groups > b)
+  if (b < 0 || b > kDecodeMaxB || Hq < 1 || Hkv < 1 || Hq % Hkv || max_seq_len < 0 || max_seq_len > 1 << 30 || num_groups < 0 || num_groups > b)
     return SPEC_ERR_ARG;
   if ((D != 64 && D != 128) || page_size < 1 || page_size > 128 || (page_size & (page_size - 1))) return SPEC_ERR_UNSUPPORTED;
   if (q_ld < int64_t(Hq) * D || q_ld % 8 || num_slots < page_size || num_slots >= (int64_t(1) << 31) || req_rows < 1 ||

@@ -575,15 +575,15 @@ int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size
  * Requests that share pages: forks, pages given back, copies, compaction.  The
  * pages have no counterpart; parallel samples of a prompt and beams hold the
  * prompt's KV once.  They work on page_table and the free list of
- * spec_alloc_slots (any page_size >= 1) and on the pages of either cache.
+ * spec_alloc_slots (page_size up to 2^20) and on the pages of either cache.
  *
  * share_counts [num_pages] int32, zero-filled once: the holders of a page beyond
  * the first (0 for a free page, too), so spec_alloc_slots and the commits need not
  * know of it.  Only whole pages are shared, and tokens are only appended, so no
  * shared page is written: a request that goes on from the middle of a page it
- * shares (cut back to there, for instance) is forked there first.  The rows of a
- * call hold at most 2^31 - 1 pages (b * row_pages), b <= 16384.  Results do not
- * depend on the order in which a call's threads run.
+ * shares (cut back to there, for instance) is forked there first.  num_pages,
+ * free_cap and the pages of a call's rows (b * row_pages) are at most 2^30, b at
+ * most 16384.  Results do not depend on the order in which a call's threads run.
  *
  * spec_fork_pages -- child r (table row children[r]) starts as the first
  * fork_lens[r] tokens of its parent (table row parents[r]).  With L = fork_lens[r]:
@@ -692,7 +692,7 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
  * clamped).  A page id out of range sets SPEC_DEV_INDEX and its keys do not count;
  * a bad table row leaves its request without tokens.  What the pools hold behind a
  * request's last token is not looked at.  A call's results are always the same
- * bits.  D 64 or 128, b <= 2048, num_groups <= b; the ticks, b * (max_seq_len / 16
+ * bits.  D 64 or 128, b <= 2048, num_groups <= b, max_seq_len <= 2^30; the ticks, b * (max_seq_len / 16
  * + 8) * Hkv * ceil(Hq / Hkv / 64), stay below 2^30.  HBM-bound.
  * ------------------------------------------------------------------------- */
 int spec_decode_attention(int b, int Hq, int Hkv, int D, int page_size, const void* q, int64_t q_ld,

@@ -25,7 +25,8 @@ def _fork(**change):
 
 @pytest.mark.parametrize("change, code", [
     (dict(b=-1), -1), (dict(b=16385), -1), (dict(ps=0), -1), (dict(pages=0), -1), (dict(pages=1 << 28), -1), (dict(pages=(1 << 27)), -1), (dict(row_pages=1 << 27), -1),
-    (dict(row_pages=0), -1), (dict(b=16384, row_pages=1 << 17), -1), (dict(cap=-1), -1), (dict(slots=FAKE, row_w=0), -1), (dict(parents=None), -1), (dict(children=None), -1),
+    (dict(row_pages=0), -1), (dict(b=16384, row_pages=1 << 17), -1), (dict(b=16384, row_pages=(1 << 16) + 1), -1), 
+    (dict(ps=(1 << 20) + 1), -1), (dict(ps=1, pages=(1 << 30) + 1), -1), (dict(cap=(1 << 30) + 1), -1), (dict(cap=-1), -1), (dict(slots=FAKE, row_w=0), -1), (dict(parents=None), -1), (dict(children=None), -1),
     (dict(lens=None), -1), (dict(counts=None), -1), (dict(free=None), -1), (dict(n_free=None), -1), (dict(table=None), -1), (dict(src=None), -1), (dict(dst=None), -1),
     (dict(copies=None), -1), (dict(left=None), -1), (dict(copies=FAKE), -1), (dict(ws=None), -2), (dict(ws=FAKE + 16), -2), (dict(ws_bytes=512), -2), (dict(b=0, parents=None), 0)])
 def test_fork_refusals(lib, change, code):
@@ -44,7 +45,7 @@ def _release(**change):
 
 
 @pytest.mark.parametrize("change, code", [
-    (dict(b=-1), -1), (dict(b=16385), -1), (dict(ps=-3), -1), (dict(pages=0), -1), (dict(rows=0), -1), (dict(cap=-1), -1), (dict(idx=None), -1), (dict(lens=None), -1), (dict(counts=None), -1),
+    (dict(b=-1), -1), (dict(b=16385), -1), (dict(ps=-3), -1), (dict(ps=1 << 21), -1), (dict(cap=(1 << 30) + 1), -1), (dict(b=4096, row_pages=1 << 19, ps=1), -1), (dict(pages=0), -1), (dict(rows=0), -1), (dict(cap=-1), -1), (dict(idx=None), -1), (dict(lens=None), -1), (dict(counts=None), -1),
     (dict(free=None), -1), (dict(n_free=None), -1), (dict(table=None), -1), (dict(left=None), -1), (dict(ws=None), -2), (dict(pages=1 << 20), -2), (dict(b=0, lens=None), 0)])
 def test_release_refusals(lib, change, code):
     assert lib.spec_release_pages(*_release(**change)) == code
@@ -58,7 +59,7 @@ def _compact(**change):
 
 
 @pytest.mark.parametrize("change, code", [
-    (dict(b=-1), -1), (dict(limit=-1), -1), (dict(ps=0), -1), (dict(cap=-1), -1), (dict(slots=FAKE, row_w=64), -1), (dict(counts=None), -1), (dict(free=None), -1), (dict(new_counts=None), -1),
+    (dict(b=-1), -1), (dict(limit=-1), -1), (dict(ps=0), -1), (dict(ps=1 << 21), -1), (dict(cap=(1 << 30) + 1), -1), (dict(ps=1, pages=(1 << 30) + 1), -1), (dict(cap=-1), -1), (dict(slots=FAKE, row_w=64), -1), (dict(counts=None), -1), (dict(free=None), -1), (dict(new_counts=None), -1),
     (dict(new_free=None), -1), (dict(new_table=None), -1), (dict(src=None), -1), (dict(dst=None), -1), (dict(moves=None), -1), (dict(moves=FAKE), -1), (dict(left=None), -1),
     (dict(ws=None), -2), (dict(pages=1 << 22), -2), (dict(b=0, idx=None), 0)])
 def test_compact_refusals(lib, change, code):
