@@ -1165,6 +1165,14 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
   // (the lists of moves are written while the first list is still read, and read while the counts are written)
   const Span moves[] = {{move_src, list}, {move_dst, list}}, other[] = {{free_ids, list}, {share_counts, counts}};
   if (clash(moves, other)) return SPEC_ERR_ARG;
+  // an output may be its input, but not lie over another part of it
+  const size_t table = size_t(req_rows) * row_pages * 4, slots = req_to_token ? size_t(req_rows) * row_w * 4 : 0;
+  const struct {
+    Span from;
+    const void* to;
+  } same[] = {{{share_counts, counts}, new_share_counts}, {{free_ids, list}, new_free_ids}, {{page_table, table}, new_page_table}, {{req_to_token, slots}, new_req_to_token}};
+  for (const auto& x : same)
+    if (x.from.p != x.to && overlap(x.from.p, x.from.bytes, x.to, x.from.bytes)) return SPEC_ERR_ARG;
   note_other(ws);
   const WsView v = ws_view(ws, b);
   CompactParams p{};

@@ -596,10 +596,10 @@ int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size
  * the child's row.  A parent may have many children, and L be less than it has;
  * the children are distinct rows that hold no pages, none of them a parent in the
  * call (a child that is its own parent sets SPEC_DEV_INDEX).  The written arrays
- * lie over none of the lists that the call reads (SPEC_ERR_ARG).  A bad length or row leaves its child as it was
- * (SPEC_DEV_LENGTH / SPEC_DEV_INDEX); too short a free list sets SPEC_DEV_SPACE and
- * the call does nothing (n_copies 0, n_left = n_free).  A bad page id gives an entry
- * (and slots) of -1 and SPEC_DEV_INDEX.
+ * lie over none of the lists that the call reads (SPEC_ERR_ARG).  A bad length or
+ * row leaves its child as it was (SPEC_DEV_LENGTH / SPEC_DEV_INDEX); too short a
+ * free list sets SPEC_DEV_SPACE and the call does nothing (n_copies 0, n_left =
+ * n_free).  A bad page id gives an entry (and slots) of -1 and SPEC_DEV_INDEX.
  * ------------------------------------------------------------------------- */
 int spec_fork_pages(int b, int page_size, const int32_t* parents, const int32_t* children, const int32_t* fork_lens,
                     int32_t* share_counts, int64_t num_pages, const int32_t* free_ids, int free_cap,
@@ -649,8 +649,9 @@ int spec_release_pages(int b, int page_size, const int32_t* req_pool_idx, const 
  * new_share_counts [num_pages] follow the pages.  new_free_ids: the n_left[0] free
  * pages, highest first, so that the lowest are handed out first and a pool cut to
  * N pages drops the first num_pages - N of them.
- * Each output may be its input (n_left may be n_free); the lists of moves lie over
- * nothing else, and no output over seq_lens or req_pool_idx (SPEC_ERR_ARG).  Where the tables are arrays of their own, the old
+ * Each output may be its input (n_left may be n_free), but lie over no other part
+ * of it; the lists of moves lie over nothing else, and no output over seq_lens or
+ * req_pool_idx (SPEC_ERR_ARG).  Where the tables are arrays of their own, the old
  * ones stay readable, and so do the moved pages until their ids are handed out.
  * A bad id on the free list is passed over (SPEC_DEV_INDEX), one listed twice
  * counts once (SPEC_DEV_INVARIANT), as does a table entry that is on it; a bad table
@@ -692,8 +693,9 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
  * clamped).  A page id out of range sets SPEC_DEV_INDEX and its keys do not count;
  * a bad table row leaves its request without tokens.  What the pools hold behind a
  * request's last token is not looked at.  A call's results are always the same
- * bits.  D 64 or 128, b <= 2048, num_groups <= b, max_seq_len <= 2^30; the ticks, b * (max_seq_len / 16
- * + 8) * Hkv * ceil(Hq / Hkv / 64), stay below 2^30.  HBM-bound.
+ * bits.  D 64 or 128, b <= 2048, num_groups <= b, max_seq_len <= 2^30; the ticks,
+ * b * (max_seq_len / 16 + 8) * Hkv * ceil(Hq / Hkv / 64), stay below 2^30.
+ * HBM-bound.
  * ------------------------------------------------------------------------- */
 int spec_decode_attention(int b, int Hq, int Hkv, int D, int page_size, const void* q, int64_t q_ld,
                           const void* k_pool, const void* v_pool, int64_t num_slots, const int32_t* page_table,

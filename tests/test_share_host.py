@@ -73,6 +73,14 @@ def test_compact_refuses_outputs_over_what_it_reads(lib, change):
     assert lib.spec_compact_pages(*_compact(**{**apart, **change})) == -1
 
 
+@pytest.mark.parametrize("change", [dict(new_counts=FAKE + 12288 + 36), dict(new_free=FAKE + 8192 + 28), dict(new_table=FAKE + 16384 + 124), dict(new_table=FAKE + 16384 - 124),
+                                    dict(new_slots=FAKE + 20480 + 512)])
+def test_compact_refuses_outputs_shifted_over_their_inputs(lib, change):
+    same = dict(idx=FAKE, lens=FAKE, src=FAKE + 4096, dst=FAKE + 4160, moves=FAKE + 64, left=FAKE + 128, free=FAKE + 8192, new_free=FAKE + 8192, counts=FAKE + 12288, new_counts=FAKE + 12288,
+                table=FAKE + 16384, new_table=FAKE + 16384, slots=FAKE + 20480, new_slots=FAKE + 20480, row_w=64)
+    assert lib.spec_compact_pages(*_compact(**{**same, **change})) == -1
+
+
 def _copy(hole=None, **change):
     arr = (ctypes.c_void_p * 128)(*[FAKE] * 128)
     odd = (ctypes.c_void_p * 128)(*[FAKE + 8] * 128)
