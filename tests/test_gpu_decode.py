@@ -233,14 +233,16 @@ def test_values_of_the_types_ends():
 @pytest.mark.parametrize("members", [2, 12])
 @pytest.mark.parametrize("D", [64, 128])
 def test_large_values_of_no_weight(D, members):
-    """Keys whose scores lie hundreds below the others', seen first, with values near the type's largest."""
-    c = Case([(384, [400 + r for r in range(members)])], [500], Hq=4, Hkv=1, D=D)
+    """Keys whose scores lie hundreds below the others', seen first, with values near the type's largest.  Low and high
+    keys take turns every 256, so that a CTA that has several tiles meets low ones before high ones wherever it begins."""
+    c = Case([(4096, [4100 + 3 * r for r in range(members)])] * 4, [4096], Hq=32, Hkv=8, D=D)
     c.q[..., 0] = 8.0
-    for r in (0, members):  # what the group shares, and the request alone
+    for r in range(0, c.b, members):  # what each group shares, and the request alone
         at = c.slots_of(r)
-        c.k[at, 0, 0] = 0.0
-        c.k[at[:256], 0, 0] = -400.0
-        c.v[at[:256]] = 2.0 ** 127
+        low = at[(torch.arange(at.numel(), device=DEV) % 512) < 256]
+        c.k[at, :, 0] = 0.0
+        c.k[low, :, 0] = -400.0
+        c.v[low] = 2.0 ** 127
     c.check(*c.call())
 
 
