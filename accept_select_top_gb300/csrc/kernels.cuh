@@ -478,7 +478,6 @@ struct CompactParams {
   int32_t* n_moves;
   uint32_t* error;
   int4* plan;         // {whether there is one, limit, moves, free pages}
-  int2* totals;       // [16]
   uint32_t* bits;     // [ceil(num_pages / 32)] free pages
   int32_t* pre_hole;  // [same] holes and moved pages before each word
   int32_t* pre_live;

@@ -285,9 +285,14 @@ __global__ void __launch_bounds__(kClusterThreads) release_pages_kernel(ReleaseP
 __global__ void __launch_bounds__(kClusterThreads) compact_plan_kernel(CompactParams a) {
   pdl_wait();
   pdl_trigger();
-  __shared__ int wsum[2][kClusterThreads / 32];
+  __shared__ int wsum[3][kClusterThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, me = blockIdx.x;
   const int N = int(a.num_pages), W = (N + 31) / 32;
+  const int gid = me * kClusterThreads + tid;
+  constexpr int kAll = kClusterCtas * kClusterThreads, kAhead = 4;
+  int ahead[kAhead];  // (read before it is known how many of them count)
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) ahead[k] = gid + k * kAll < a.free_cap ? a.free_ids[gid + k * kAll] : -1;
   const int n_free = *a.n_free;
   const bool ok = n_free >= 0 && n_free <= a.free_cap;
   if (!ok) {  // (every CTA of the cluster)
@@ -299,42 +304,39 @@ __global__ void __launch_bounds__(kClusterThreads) compact_plan_kernel(CompactPa
     }
     return;
   }
-  const int gid = me * kClusterThreads + tid;
-  for (int i = gid; i < W; i += kClusterCtas * kClusterThreads) a.bits[i] = 0;
+  for (int i = gid; i < W; i += kAll) a.bits[i] = 0;
   cluster_sync();
-  auto block_sum = [&](int x, int y, int2* to) {
+  // the sums over the CTA's threads, in every thread
+  auto block_sum = [&](int x, int y, int z) {
     x = __reduce_add_sync(0xffffffffu, x);
     y = __reduce_add_sync(0xffffffffu, y);
+    z = __reduce_add_sync(0xffffffffu, z);
     __syncthreads();
     if (lane == 0) {
       wsum[0][w] = x;
       wsum[1][w] = y;
+      wsum[2][w] = z;
     }
     __syncthreads();
-    if (tid == 0) {
-      int2 s = make_int2(0, 0);
-      for (int q = 0; q < kClusterThreads / 32; ++q) {
-        s.x += wsum[0][q];
-        s.y += wsum[1][q];
-      }
-      *to = s;
-    }
+    return make_int3(__reduce_add_sync(0xffffffffu, wsum[0][lane]), __reduce_add_sync(0xffffffffu, wsum[1][lane]),
+                     __reduce_add_sync(0xffffffffu, wsum[2][lane]));
   };
-  int set = 0;
-  for (int i = gid; i < n_free; i += kClusterCtas * kClusterThreads) {
-    const int p = a.free_ids[i];
+  auto mark = [&](int p) {
     if (p < 0 || p >= N) {
       raise_error(a.error, SPEC_DEV_INDEX);
     } else if (atomicOr(a.bits + (p >> 5), 1u << (p & 31)) >> (p & 31) & 1u) {
       raise_error(a.error, SPEC_DEV_INVARIANT);  // listed twice
-    } else {
-      ++set;
     }
-  }
-  block_sum(set, 0, a.totals + me);
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (gid + k * kAll < n_free) mark(ahead[k]);
+  for (int i = gid + kAhead * kAll; i < n_free; i += kAll) mark(a.free_ids[i]);
   cluster_sync();
-  int free_pages = 0;
-  for (int q = 0; q < kClusterCtas; ++q) free_pages += __ldcg(a.totals + q).x;
+  // Each CTA counts for itself what lies in the whole bitmap, which takes less time than another meeting.
+  int set = 0;
+  for (int i = tid; i < W; i += kClusterThreads) set += __popc(__ldcg(a.bits + i));
+  const int free_pages = block_sum(set, 0, 0).x;
   const int live = N - free_pages, limit = int(a.limit > live ? a.limit < N ? a.limit : N : live);
   // words of this CTA; a word's holes below the limit and moved pages from it on
   const int lo = int((long long)W * me / kClusterCtas), hi = int((long long)W * (me + 1) / kClusterCtas);
@@ -346,24 +348,19 @@ __global__ void __launch_bounds__(kClusterThreads) compact_plan_kernel(CompactPa
     hole = f & below;
     moved = ~f & ~below & exists;
   };
-  int holes = 0, moved = 0;
-  for (int i = lo + tid; i < hi; i += kClusterThreads) {
+  int holes = 0, moved = 0, all_moved = 0;
+  for (int i = tid; i < W; i += kClusterThreads) {
     unsigned h, m;
     parts(i, h, m);
-    holes += __popc(h);
-    moved += __popc(m);
-  }
-  block_sum(holes, moved, a.totals + kClusterCtas + me);
-  cluster_sync();
-  int at_hole = 0, at_live = 0, M = 0;
-  for (int q = 0; q < kClusterCtas; ++q) {
-    const int2 c = __ldcg(a.totals + kClusterCtas + q);
-    M += c.y;
-    if (q < me) {
-      at_hole += c.x;
-      at_live += c.y;
+    all_moved += __popc(m);
+    if (i < lo) {
+      holes += __popc(h);
+      moved += __popc(m);
     }
   }
+  const int3 sums = block_sum(holes, moved, all_moved);
+  const int M = sums.z;
+  int at_hole = sums.x, at_live = sums.y;
   if (me == 0 && tid == 0) {
     *a.plan = make_int4(1, limit, M, free_pages);
     *a.n_left = free_pages;
@@ -412,33 +409,45 @@ __global__ void __launch_bounds__(kClusterThreads) compact_plan_kernel(CompactPa
 }
 
 // The tables, slots, counts and the rest of the free list after the plan.  Each value has one thread, so that
-// every output may be its input.
+// every output may be its input.  What the plan does not write is read while it runs: its CTAs let this kernel start once
+// what came before the call is done.
 __global__ void __launch_bounds__(kForkThreads) compact_tables_kernel(CompactParams a) {
-  pdl_wait();
-  pdl_trigger();
   extern __shared__ int pre[];  // [b + 1]
   __shared__ int wsum[kForkThreads / 32];
   __shared__ SlotStage<kForkThreads> stage;
   const int tid = threadIdx.x, N = int(a.num_pages);
-  const bool report = blockIdx.x == 0;
-  const int4 plan = *a.plan;
-  const int limit = plan.y, M = plan.z, free_pages = plan.w;
-  if (!plan.x) return;
-  const int E = scan_counts<kForkThreads>(a.b, pre, wsum, [&](int r) {
+  auto pages_in = [&](int r, bool tell) {
     const int len = a.seq_lens[r], row = a.req_pool_idx[r];
     const bool idx_ok = row >= 0 && row < a.req_rows;
     const bool len_ok = len >= 0 && len <= (long long)a.row_pages * a.page_size && (!a.req_to_token || len <= a.row_w);
-    if (report && !idx_ok) raise_error(a.error, SPEC_DEV_INDEX);
-    if (report && !len_ok) raise_error(a.error, SPEC_DEV_LENGTH);
+    if (tell && !idx_ok) raise_error(a.error, SPEC_DEV_INDEX);
+    if (tell && !len_ok) raise_error(a.error, SPEC_DEV_LENGTH);
     return idx_ok && len_ok ? pages_of(len, a.page_size) : 0;
-  });
+  };
+  const int E = scan_counts<kForkThreads>(a.b, pre, wsum, [&](int r) { return pages_in(r, false); });
+  // of the thread's entry: its place in the row, the row, the request's length, the page
+  int i = 0, row = 0, len = 0, id = -1;
+  auto look = [&](int e) {
+    if (e >= E) return;
+    const int r = row_of_entry(pre, a.b, e);
+    i = e - pre[r];
+    row = a.req_pool_idx[r];
+    len = a.seq_lens[r];
+    id = a.page_table[(long long)row * a.row_pages + i];
+  };
+  look(blockIdx.x * kForkThreads + tid);
+  pdl_wait();
+  pdl_trigger();
+  const int4 plan = *a.plan;
+  const int limit = plan.y, M = plan.z, free_pages = plan.w;
+  if (!plan.x) return;
+  if (blockIdx.x == 0)
+    for (int r = tid; r < a.b; r += kForkThreads) pages_in(r, true);
   for (int e0 = blockIdx.x * kForkThreads; e0 < E; e0 += gridDim.x * kForkThreads) {
-    const int e = e0 + tid;
-    int id = -1, count = 0;
+    const bool on = e0 + tid < E;
+    int count = 0;
     long long first = 0;
-    if (e < E) {
-      const int r = row_of_entry(pre, a.b, e), i = e - pre[r], row = a.req_pool_idx[r];
-      id = a.page_table[(long long)row * a.row_pages + i];
+    if (on) {
       if (id < 0 || id >= N) {
         raise_error(a.error, SPEC_DEV_INDEX);
         id = -1;
@@ -449,10 +458,11 @@ __global__ void __launch_bounds__(kForkThreads) compact_tables_kernel(CompactPar
         else id = a.move_dst[at + __popc(~f & ((1u << (id & 31)) - 1u) & ~((1u << (from & 31)) - 1u))];
       }
       a.new_page_table[(long long)row * a.row_pages + i] = id;
-      count = min(a.page_size, a.seq_lens[r] - i * a.page_size);
+      count = min(a.page_size, len - i * a.page_size);
       first = (long long)row * a.row_w + (long long)i * a.page_size;
     }
     if (a.req_to_token) write_slots<kForkThreads>(stage, a.new_req_to_token, first, id, count, a.page_size, a.vec_slots);
+    look(e0 + gridDim.x * kForkThreads + tid);
   }
   const int stride = gridDim.x * kForkThreads, gid = blockIdx.x * kForkThreads + tid;
   for (int i = gid; i < M; i += stride) {

@@ -1203,7 +1203,6 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
   p.error = v.error;
   const size_t words = align256(size_t(num_pages + 31) / 32 * 4);
   p.plan = reinterpret_cast<int4*>(v.partials);
-  p.totals = reinterpret_cast<int2*>(v.partials + 16);
   p.bits = reinterpret_cast<uint32_t*>(v.partials + 256);
   p.pre_hole = reinterpret_cast<int32_t*>(v.partials + 256 + words);
   p.pre_live = reinterpret_cast<int32_t*>(v.partials + 256 + 2 * words);
