@@ -95,10 +95,10 @@ __global__ void __launch_bounds__(kForkThreads) fork_pages_kernel(ForkParams a) 
 // ---------------------------------------------------------------- release
 
 // The occurrences (request, page) of the call, laid end to end, are cut into contiguous shares, one a CTA of the
-// cluster, in rows of 1024.  note[p] = {times given up, first occurrence of a page that is freed}: cleared, then
-// counted by atomics; a page is freed where more holders than its count give it up.  (The first occurrence takes
-// atomics only where a page is given up more than once.)  Freed pages are pushed in descending order of
-// occurrence: what alloc or fork took in one call goes back to where it was.
+// cluster, in rows of 1024.  note[p] = {times given up, -1 - the occurrence that speaks for the page}: times are counted by
+// atomics, and whoever counts first speaks; a page is freed where more holders than its count give it up, and then its
+// first occurrence speaks (by atomics, only where it is given up more than once).  So each page's count is stored once.
+// Freed pages are pushed in descending order of occurrence: what alloc or fork took in one call goes back to where it was.
 //   The page ids and what is known of them stay in registers for the first kKept rows of a share.
 //   The CTAs meet four times.  Up to 16 are a cluster (16 of them where the device takes such); a call that may hold
 // more occurrences than their registers is a cooperative launch over all SMs, as a SM's scattered accesses to the
@@ -185,28 +185,40 @@ __global__ void __launch_bounds__(kClusterThreads) release_pages_kernel(ReleaseP
         if (p[i] >= 0) fn(lo + (i0 + i) * kClusterThreads + tid, p[i], i0 + i);
     }
   };
-  for_each([&](int, int p, int) { a.note[p] = make_int2(0, INT_MAX); });
+  // (in order, where that takes fewer stores of a warp)
+  if (!CLUSTER && a.num_pages / 8 < E) {
+    for (long long p = me * kClusterThreads + tid; p < a.num_pages; p += ctas * kClusterThreads) a.note[p] = make_int2(0, 0);
+  } else {
+    for_each([&](int, int p, int) { a.note[p].x = 0; });
+  }
   if (!meet()) return;
-  for_each([&](int, int p, int) { atomicAdd(&a.note[p].x, 1); });
+  unsigned speaks = 0, freed = 0;  // bits: of the kept rows
+  for_each([&](int e, int p, int i) {
+    if (atomicAdd(&a.note[p].x, 1) == 0) {
+      a.note[p].y = -1 - e;
+      if (i < kKept) speaks |= 1u << i;
+    }
+  });
   if (!meet()) return;
-  for_each([&](int e, int p, int) {
+  for_each([&](int e, int p, int i) {
     const int times = __ldcg(&a.note[p].x), more = a.share_counts[p];
     if (times > more) {
-      if (times == 1) a.note[p].y = e;
-      else atomicMin(&a.note[p].y, e);
+      if (times > 1) atomicMax(&a.note[p].y, -1 - e);
       if (times > more + 1) raise_error(a.error, SPEC_DEV_INVARIANT);
+      if (i < kKept) freed |= 1u << i;
     }
   });
   if (!meet()) return;
   // counts are not touched before the list is known to have room
   int mine = 0;
-  unsigned freed = 0, stays = 0;  // bits: of the kept rows
   for_each([&](int e, int p, int i) {
-    const int first = __ldcg(&a.note[p].y);
-    mine += first == e;
     if (i < kKept) {
-      if (first == e) freed |= 1u << i;
-      if (first == INT_MAX) stays |= 1u << i;
+      if (!(freed >> i & 1)) return;
+      const bool first = __ldcg(&a.note[p].y) == -1 - e;
+      mine += first;
+      speaks = first ? speaks | 1u << i : speaks & ~(1u << i);
+    } else if (__ldcg(&a.note[p].y) == -1 - e) {
+      mine += __ldcg(&a.note[p].x) > a.share_counts[p];
     }
   });
   mine = __reduce_add_sync(0xffffffffu, mine);
@@ -248,23 +260,19 @@ __global__ void __launch_bounds__(kClusterThreads) release_pages_kernel(ReleaseP
   for (int i = rows - 1; i >= 0; --i) {
     const int e = lo + i * kClusterThreads + tid;
     int p = -1;
-    bool go = false, stay = false;
+    bool go = false;
     if (i < kKept) {
 #pragma unroll
       for (int q = 0; q < kKept; ++q)
         if (q == i) p = kept[q];
-      go = freed >> i & 1;
-      stay = stays >> i & 1;
+      if (!(speaks >> i & 1)) p = -1;
+      go = speaks >> i & freed >> i & 1;
     } else {
       p = page_at(e);
-      if (p >= 0) {
-        const int first = __ldcg(&a.note[p].y);
-        go = first == e;
-        stay = first == INT_MAX;
-      }
+      if (p >= 0 && __ldcg(&a.note[p].y) != -1 - e) p = -1;
+      if (p >= 0) go = __ldcg(&a.note[p].x) > a.share_counts[p];
     }
-    if (go) a.share_counts[p] = 0;
-    if (stay) atomicSub(a.share_counts + p, 1);
+    if (p >= 0) a.share_counts[p] = go ? 0 : a.share_counts[p] - __ldcg(&a.note[p].x);
     if (mine == 0) continue;  // (the CTA frees nothing)
     const unsigned m = __ballot_sync(0xffffffffu, go);
     __syncthreads();

@@ -136,11 +136,11 @@ def test_release_cut_back(b, most):
     c.same()
 
 
-def test_release_of_pages_held_in_one_call_and_outside():
+@pytest.mark.parametrize("b, width, total", [(50, 40, 500), (40, 4500, 5000), (40, 4500, 2000000), (80, 40000, 60000)])
+def test_release_of_pages_held_in_one_call_and_outside(b, width, total):
     """Pages shared among the call's requests and one outside of it, in a random pattern; the same row twice is an error of the caller that is told."""
     ops = _ops()
     gen = _gen(3)
-    b, width, total = 50, 40, 500
     table = torch.randint(0, total, (b, width), generator=gen).tolist()
     lens = torch.randint(0, width * 4 + 1, (b,), generator=gen).tolist()
     held = {}
