@@ -110,18 +110,20 @@ constexpr int kClusterMost = 16;
 constexpr int kReleaseMostCtas = 192;
 constexpr long long kBarrierCycles = 4000000000ll;  // about 2 s: bound of a wait for the other CTAs
 
-// All CTAs of a cooperative launch; what they wrote before is seen after.  arrivals counts to `ctas` once a meeting.
-// False (in every thread) if they do not come.
-__device__ __forceinline__ bool grid_sync(uint32_t* arrivals, uint32_t until, uint32_t* error) {
+// All CTAs of a cooperative launch, for the round-th time (from 1) of `rounds`; what they wrote before is seen after.  The
+// last arrival of the last round takes the counter back to zero.  False (in every thread) if they do not come.
+__device__ __forceinline__ bool grid_sync(uint32_t* arrivals, uint32_t round, uint32_t rounds, uint32_t* error) {
   __shared__ int s_ok;
   __syncthreads();
   if (threadIdx.x == 0) {
-    bool ok = atom_add_acq_rel(arrivals) + 1 >= until;
+    const uint32_t ctas = gridDim.x, before = (round - 1) * ctas;  // (zero is as far from `before` as any count behind it)
+    uint32_t now;
+    asm volatile("atom.inc.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(now) : "l"(arrivals), "r"(rounds * ctas - 1) : "memory");
+    bool ok = now + 1 - before >= ctas;
     const long long start = clock64();
     while (!ok && clock64() - start <= kBarrierCycles) {
-      uint32_t now;
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(arrivals) : "memory");
-      ok = now >= until;
+      ok = now - before >= ctas;
     }
     if (!ok) raise_error(error, SPEC_DEV_TIMEOUT);
     s_ok = ok;
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kClusterThreads) release_pages_kernel(ReleaseP
       cluster_sync();
       return true;
     }
-    return grid_sync(a.counters, ++met * uint32_t(ctas), a.error);
+    return grid_sync(a.counters, ++met, 4, a.error);
   };
   const int E = scan_counts<kClusterThreads>(a.b, pre, wsum, [&](int r) {
     const int len = a.seq_lens[r], keep = a.keep_lens ? a.keep_lens[r] : 0, row = a.req_pool_idx[r];
@@ -171,55 +173,73 @@ __global__ void __launch_bounds__(kClusterThreads) release_pages_kernel(ReleaseP
   int kept[kKept];
 #pragma unroll
   for (int i = 0; i < kKept; ++i) kept[i] = page_at(lo + i * kClusterThreads + tid);
-  // fn(occurrence, page, row) for the thread's pages
-  auto for_each = [&](auto&& fn) {
-#pragma unroll
-    for (int i = 0; i < kKept; ++i)
-      if (kept[i] >= 0) fn(lo + i * kClusterThreads + tid, kept[i], i);
+  // fn(occurrence, page) for the thread's other pages
+  auto for_others = [&](auto&& fn) {
     for (int i0 = kKept; i0 < rows; i0 += kKept) {
       int p[kKept];
 #pragma unroll
       for (int i = 0; i < kKept; ++i) p[i] = page_at(lo + (i0 + i) * kClusterThreads + tid);
 #pragma unroll
       for (int i = 0; i < kKept; ++i)
-        if (p[i] >= 0) fn(lo + (i0 + i) * kClusterThreads + tid, p[i], i0 + i);
+        if (p[i] >= 0) fn(lo + (i0 + i) * kClusterThreads + tid, p[i]);
     }
   };
+  auto occurrence = [&](int i) { return lo + i * kClusterThreads + tid; };
   // (in order, where that takes fewer stores of a warp)
   if (!CLUSTER && a.num_pages / 8 < E) {
     for (long long p = me * kClusterThreads + tid; p < a.num_pages; p += ctas * kClusterThreads) a.note[p] = make_int2(0, 0);
   } else {
-    for_each([&](int, int p, int) { a.note[p].x = 0; });
+#pragma unroll
+    for (int i = 0; i < kKept; ++i)
+      if (kept[i] >= 0) a.note[kept[i]].x = 0;
+    for_others([&](int, int p) { a.note[p].x = 0; });
   }
   if (!meet()) return;
   unsigned speaks = 0, freed = 0;  // bits: of the kept rows
-  for_each([&](int e, int p, int i) {
-    if (atomicAdd(&a.note[p].x, 1) == 0) {
-      a.note[p].y = -1 - e;
-      if (i < kKept) speaks |= 1u << i;
+  int x[kKept], y[kKept];
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) x[i] = kept[i] >= 0 ? atomicAdd(&a.note[kept[i]].x, 1) : 1;
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (x[i] == 0) {
+      a.note[kept[i]].y = -1 - occurrence(i);
+      speaks |= 1u << i;
     }
+  for_others([&](int e, int p) {
+    if (atomicAdd(&a.note[p].x, 1) == 0) a.note[p].y = -1 - e;
   });
   if (!meet()) return;
-  for_each([&](int e, int p, int i) {
-    const int times = __ldcg(&a.note[p].x), more = a.share_counts[p];
-    if (times > more) {
-      if (times > 1) atomicMax(&a.note[p].y, -1 - e);
-      if (times > more + 1) raise_error(a.error, SPEC_DEV_INVARIANT);
-      if (i < kKept) freed |= 1u << i;
-    }
-  });
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    x[i] = kept[i] >= 0 ? __ldcg(&a.note[kept[i]].x) : 0;
+    y[i] = kept[i] >= 0 ? a.share_counts[kept[i]] : 0;
+  }
+  auto give_up = [&](int e, int p, int times, int more) {
+    if (times <= more) return false;
+    if (times > 1) atomicMax(&a.note[p].y, -1 - e);
+    if (times > more + 1) raise_error(a.error, SPEC_DEV_INVARIANT);
+    return true;
+  };
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    if (give_up(occurrence(i), kept[i], x[i], y[i])) freed |= 1u << i;
+    y[i] = max(0, y[i] - x[i]);  // (what its count will be)
+  }
+  for_others([&](int e, int p) { give_up(e, p, __ldcg(&a.note[p].x), a.share_counts[p]); });
   if (!meet()) return;
   // counts are not touched before the list is known to have room
   int mine = 0;
-  for_each([&](int e, int p, int i) {
-    if (i < kKept) {
-      if (!(freed >> i & 1)) return;
-      const bool first = __ldcg(&a.note[p].y) == -1 - e;
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) x[i] = freed >> i & 1 ? __ldcg(&a.note[kept[i]].y) : 0;
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (freed >> i & 1) {
+      const bool first = x[i] == -1 - occurrence(i);
       mine += first;
       speaks = first ? speaks | 1u << i : speaks & ~(1u << i);
-    } else if (__ldcg(&a.note[p].y) == -1 - e) {
-      mine += __ldcg(&a.note[p].x) > a.share_counts[p];
     }
+  for_others([&](int e, int p) {
+    if (__ldcg(&a.note[p].y) == -1 - e) mine += __ldcg(&a.note[p].x) > a.share_counts[p];
   });
   mine = __reduce_add_sync(0xffffffffu, mine);
   __syncthreads();
@@ -246,17 +266,15 @@ __global__ void __launch_bounds__(kClusterThreads) release_pages_kernel(ReleaseP
     at += __reduce_add_sync(0xffffffffu, behind);
     mine = __ldcg(a.totals + me);
   }
-  // the CTA that leaves last puts the counters back to zero
-  if (!CLUSTER && tid == 0 && atom_add_acq_rel(a.counters + 1) == uint32_t(ctas) - 1) {
-    atomicExch(a.counters, 0u);
-    atomicExch(a.counters + 1, 0u);
-  }
   const bool fits = n_free >= 0 && n_free <= a.free_cap && total <= a.free_cap - n_free;
   if (me == 0 && tid == 0) {
     if (!fits) raise_error(a.error, SPEC_DEV_SPACE);
     *a.n_left = fits ? n_free + total : n_free;
   }
   if (!fits) return;
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (speaks >> i & 1) a.share_counts[kept[i]] = y[i];
   for (int i = rows - 1; i >= 0; --i) {
     const int e = lo + i * kClusterThreads + tid;
     int p = -1;
@@ -265,14 +283,15 @@ __global__ void __launch_bounds__(kClusterThreads) release_pages_kernel(ReleaseP
 #pragma unroll
       for (int q = 0; q < kKept; ++q)
         if (q == i) p = kept[q];
-      if (!(speaks >> i & 1)) p = -1;
       go = speaks >> i & freed >> i & 1;
     } else {
       p = page_at(e);
-      if (p >= 0 && __ldcg(&a.note[p].y) != -1 - e) p = -1;
-      if (p >= 0) go = __ldcg(&a.note[p].x) > a.share_counts[p];
+      if (p >= 0 && __ldcg(&a.note[p].y) == -1 - e) {
+        const int times = __ldcg(&a.note[p].x), more = a.share_counts[p];
+        go = times > more;
+        a.share_counts[p] = max(0, more - times);
+      }
     }
-    if (p >= 0) a.share_counts[p] = go ? 0 : a.share_counts[p] - __ldcg(&a.note[p].x);
     if (mine == 0) continue;  // (the CTA frees nothing)
     const unsigned m = __ballot_sync(0xffffffffu, go);
     __syncthreads();
