@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
   int* slen = pre + ng + a.b + 1;
   int* sbase = slen + a.b;
   int* sgroup = reinterpret_cast<int*>(smem);  // (the ring is not in use yet)
+  int* sshared = sgroup + ng + 1;
   __shared__ int wsum[kDecThreads / 32];
   __shared__ int s_bad, s_tall;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
@@ -203,7 +204,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
     E = int((blockIdx.x + 1ll) * tiles / gridDim.x);
     __syncthreads();  // (the barriers)
   } else {
-    for (int g = tid; g <= ng && ng > 0; g += kDecThreads) sgroup[g] = a.group_start[g];
+    for (int g = tid; g <= ng && ng > 0; g += kDecThreads) {
+      sgroup[g] = a.group_start[g];
+      if (g < ng) sshared[g] = a.shared_lens[g];
+    }
     for (int r = tid; r < a.b; r += kDecThreads) {
       int len = a.seq_lens[r];
       const int row = a.req_pool_idx[r];
@@ -234,7 +238,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
           else hi = mid;
         }
         g = lo;
-        const int shared = a.shared_lens[g];
+        const int shared = sshared[g];
         if (report && r == sgroup[g] && (shared < 0 || shared > most)) raise_error(a.error, SPEC_DEV_LENGTH);
         const int s = dec_shared(shared, slen[sgroup[g]]);
         if (slen[r] >= s) base = s;

@@ -51,7 +51,7 @@ struct TallSmem {
   static constexpr int kWords = kMask + kStages * 16;  // TMEM address, abort flag, bad flag, the other kernel's ticks, then a word a warp
   static constexpr int kBytes = kWords + 16 + 4 * (kTallThreads / 32);
   // the ticks before each group are summed up where the ring will be
-  static_assert(4 * (2 * kDecodeMaxB + 2) <= kStages * kStage, "scan space");
+  static_assert(4 * (4 * kDecodeMaxB + 2) <= kStages * kStage, "scan space");
 };
 static_assert(TallSmem<128>::kBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
 
@@ -231,6 +231,8 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
   int* wsum = reinterpret_cast<int*>(sp + L::kWords + 16);
   int* pre = reinterpret_cast<int*>(sp + L::kRing);  // [groups + 1] ticks before each group, until the roles start
   int* sgroup = pre + ng + 1;                        // [groups + 1]
+  int* sshared = sgroup + ng + 1;                    // [groups]
+  int* slen = sshared + ng;                          // [b]
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -267,33 +269,45 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
     const int s = a.group_start[g], e = g < ng ? a.group_start[g + 1] : a.b;
     if (g < ng && (s < 0 || s > e || e > a.b)) *bad = 1;
     sgroup[g] = s;
+    if (g < ng) sshared[g] = a.shared_lens[g];
+  }
+  for (int r = tid; r < a.b; r += kTallThreads) {
+    const int row = a.req_pool_idx[r], len = a.seq_lens[r];
+    slen[r] = row < 0 || row >= a.req_rows ? 0 : min(max(len, 0), most);
   }
   __syncthreads();
   const bool grouped = *bad == 0;  // (the other kernel tells)
-  // (all of it is read again where a role comes to the group)
-  auto group = [&](int g, Place& p) {
-    p.g = g;
-    p.j = p.t = p.tiles = 0;
-    if (!grouped || g >= ng) return;
-    p.r0 = __ldg(a.group_start + g);
-    p.rows = (__ldg(a.group_start + g + 1) - p.r0) * G;
+  auto fill = [&](Place& p, int r0, int members, int shared, auto&& len_of) {
+    p.r0 = r0;
+    p.rows = members * G;
     if (p.rows <= args.flat_rows) return;
-    const int row = __ldg(a.req_pool_idx + p.r0), len = min(max(__ldg(a.seq_lens + p.r0), 0), most);
-    if (row < 0 || row >= a.req_rows) return;
-    p.shared = dec_shared(__ldg(a.shared_lens + g), len);
+    p.shared = dec_shared(shared, len_of(r0));
     p.blocks = (p.rows + kDecTallRows - 1) / kDecTallRows;
     p.tiles = (p.shared + kDecTile - 1) / kDecTile;
+  };
+  auto begin = [&](int g, Place& p) {
+    p.g = g;
+    p.j = p.t = p.tiles = 0;
+    return grouped && g < ng;
+  };
+  // (all of it is read again where a role comes to the group)
+  auto group = [&](int g, Place& p) {
+    if (!begin(g, p)) return;
+    const int r0 = __ldg(a.group_start + g);
+    fill(p, r0, __ldg(a.group_start + g + 1) - r0, __ldg(a.shared_lens + g), [&](int r) {
+      const int row = __ldg(a.req_pool_idx + r), len = __ldg(a.seq_lens + r);
+      return row < 0 || row >= a.req_rows ? 0 : min(max(len, 0), most);
+    });
+  };
+  auto known_group = [&](int g, Place& p) {  // from shared memory
+    if (begin(g, p)) fill(p, sgroup[g], sgroup[g + 1] - sgroup[g], sshared[g], [&](int r) { return slen[r]; });
   };
   auto ticks_of = [&](const Place& p) { return p.tiles ? a.Hkv * p.blocks * (p.tiles + kDecTallEnd) : 0; };
   if (grouped) {  // the other kernel's ticks: each request's own tokens, and what smaller groups share
     const int own_tiles = args.own_tiles;
-    auto len_of = [&](int r) {
-      const int row = __ldg(a.req_pool_idx + r);
-      return row < 0 || row >= a.req_rows ? 0 : min(max(__ldg(a.seq_lens + r), 0), most);
-    };
     int flat = 0;
     for (int r = tid; r < a.b; r += kTallThreads) {
-      const int len = len_of(r);
+      const int len = slen[r];
       int base = 0;
       if (r >= sgroup[0] && r < sgroup[ng]) {
         int lo = 0, hi = ng;
@@ -302,7 +316,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
           if (sgroup[mid] <= r) lo = mid;
           else hi = mid;
         }
-        const int first = sgroup[lo], rows = (sgroup[lo + 1] - first) * G, s = dec_shared(__ldg(a.shared_lens + lo), len_of(first));
+        const int first = sgroup[lo], rows = (sgroup[lo + 1] - first) * G, s = dec_shared(sshared[lo], slen[first]);
         base = len >= s ? s : 0;
         if (r == first && s > 0 && rows <= args.flat_rows) flat += a.Hkv * ((rows + kDecRows - 1) / kDecRows) * (dec_unit_ticks<D>(0, s) + kDecEndTicks);
       }
@@ -316,7 +330,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
     for (int g0 = 0; g0 < ng; g0 += kTallThreads) {
       const int g = g0 + tid;
       Place p;
-      group(g, p);
+      known_group(g, p);
       const int t = ticks_of(p);
       int incl = t;
 #pragma unroll
@@ -356,7 +370,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
       if (pre[mid] <= S) lo = mid;
       else hi = mid;
     }
-    group(lo, start);  // (the last that begins at or before S: it has ticks)
+    known_group(lo, start);  // (the last that begins at or before S: it has ticks)
     const int rem = S - pre[lo];
     start.j = rem / (start.tiles + kDecTallEnd);
     start.t = rem - start.j * (start.tiles + kDecTallEnd);
