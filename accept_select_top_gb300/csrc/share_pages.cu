@@ -11,8 +11,8 @@
 // Bound: latency.  A step's forks and releases are some kB; the chain is lengths -> entries -> counts ->
 // lists, dependent reads of about 1 us each.  What has to agree over the whole call (which of a page's holders
 // gives it up first; how many pages lie before) is agreed within a cluster of CTAs by its barrier, so that a release is one
-// launch and a compaction two.  In us: eight children of 1001 tokens 4 (two million slots of 64 children 9), their release 7;
-// compaction of 17 thousand pages 14.
+// launch and a compaction two.  In us: eight children of 1001 tokens 4 (two million slots of 64 children 9), their release 8;
+// compaction of 17 thousand pages 11.
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(kForkThreads) fork_pages_kernel(ForkParams a) 
 //   The CTAs meet four times.  Up to 16 are a cluster (16 of them where the device takes such); a call that may hold
 // more occurrences than their registers is a cooperative launch over all SMs, as a SM's scattered accesses to the
 // notes, one a cycle, are what a large call costs, and its CTAs meet at a counter.  In us, cluster of 16 / all SMs:
-// 133 thousand pages 47 / 20, 328 thousand of 32 holders each 111 / 39 (its atomics meet at the same words);
-// a few hundred pages: cluster of 8 8, all SMs 13.
+// 133 thousand pages 43 / 19, 328 thousand of 32 holders each 103 / 31 (its atomics meet at the same words);
+// a few hundred pages: cluster of 8 8, all SMs 15 (a cooperative launch by itself costs 7).
 constexpr int kKept = 8;
 constexpr int kClusterMost = 16;
 constexpr int kReleaseMostCtas = 192;
