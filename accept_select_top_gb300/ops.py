@@ -632,15 +632,16 @@ def spec_decode_attention(b: int, Hq: int, Hkv: int, D: int, page_size: int, q, 
     pages (both None: no groups).  lse may be None."""
     dev = _device()
     qp, q_ld = _rows_in(q, Hq, D, b, dev, "q")
-    if k_pool.shape != v_pool.shape or k_pool.dim() != 3 or k_pool.shape[1] != Hkv or k_pool.shape[2] != D:
-        raise SpecError(f"pools: expected [num_slots, {Hkv}, {D}] twice, got {tuple(k_pool.shape)} and {tuple(v_pool.shape)}")
+    pool = k_pool.shape
+    if pool != v_pool.shape or len(pool) != 3 or pool[1] != Hkv or pool[2] != D:
+        raise SpecError(f"pools: expected [num_slots, {Hkv}, {D}] twice, got {tuple(pool)} and {tuple(v_pool.shape)}")
     if (group_start is None) != (shared_lens is None):
         raise SpecError("group_start and shared_lens go together")
     groups = 0 if shared_lens is None else shared_lens.numel()
     rows, row_pages = page_table.shape
     _check(LIB.spec_decode_attention(
         b, Hq, Hkv, D, page_size, qp, q_ld, _in(k_pool, _BF16, 1, dev, "k_pool"), _in(v_pool, _BF16, 1, dev, "v_pool"),
-        k_pool.shape[0], _in(page_table, _I32, 1, dev, "page_table"), rows, row_pages,
+        pool[0], _in(page_table, _I32, 1, dev, "page_table"), rows, row_pages,
         _in(req_pool_idx, _I32, b, dev, "req_pool_idx"), _in(seq_lens, _I32, b, dev, "seq_lens"), max_seq_len, groups,
         None if groups == 0 else _in(group_start, _I32, groups + 1, dev, "group_start"),
         None if groups == 0 else _in(shared_lens, _I32, groups, dev, "shared_lens"), scale,
