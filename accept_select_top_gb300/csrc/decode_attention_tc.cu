@@ -14,9 +14,10 @@
 //   Every piece of a unit leaves an fp32 partial result; decode_attention.cu joins them.
 //   Bound: up to 128 rows the cache's bytes (eight groups of 12 requests, 32768 shared tokens, 32 / 8 heads: 193 us a call,
 // 1.1 GB); 256 rows: shared memory.  S with both operands there reads 6 KB in 32 cycles of the tensor cores, so that a tile
-// is 1280 cycles of products and 256 of the copies' writes; measured 1790; from memory it comes in 1400 (two documents
-// of 65536 tokens, 32 requests of 64 / 8 heads each: 132 us, 1.04 PF/s).  K and V in rings of their own, TMA boxes of 16
-// keys (what a page holds for certain; 30 GB/s a SM) and Q in TMEM, with one S a group, are slower by 8, 15 and 29%.
+// is 1280 cycles of products and 256 of the copies' writes; it takes about 1790, and from memory it comes in 1340 (at the
+// profiler's 1.8 GHz).  Two documents of 65536 tokens, 32 requests of 64 / 8 heads each: 132 us, 1.04 PF/s.  K and V in
+// rings of their own, TMA boxes of 16 keys (what a page holds for certain; 30 GB/s a SM) and Q in TMEM, with one S a
+// group, are slower by 8, 15 and 29%.
 //   Every wait is bounded: on timeout the CTA sets SPEC_DEV_TIMEOUT, stops, drains its copies and MMAs and frees its TMEM.
 #include "common.cuh"
 #include "kernels.cuh"
