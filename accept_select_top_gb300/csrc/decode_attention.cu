@@ -388,8 +388,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
       for (int q = 0; q < kClusterMost; ++q) M = fmaxf(M, ml[q].x);
 #pragma unroll
       for (int q = 0; q < kClusterMost; ++q) {
+        if (ml[q].y == 0.f) continue;  // (a CTA that has seen nothing; one that has counts under any weight, for its NaN)
         const float wt = dec_weight(ml[q].x, M);
-        if (wt == 0.f) continue;
         Ls = fmaf(ml[q].y, wt, Ls);
         acc = make_float4(fmaf(y[q].x, wt, acc.x), fmaf(y[q].y, wt, acc.y), fmaf(y[q].z, wt, acc.z), fmaf(y[q].w, wt, acc.w));
       }
@@ -902,8 +902,8 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     acc = make_float4(acc.x * was, acc.y * was, acc.z * was, acc.w * was);
 #pragma unroll
     for (int k = 0; k < kOnce; ++k) {
+      if (v[k].y == 0.f) continue;  // (a part that has seen nothing: its O may not have been written)
       const float wt = dec_weight(v[k].x, M);
-      if (wt == 0.f) continue;  // (a part that has seen nothing may not have been written)
       Ls = fmaf(v[k].y, wt, Ls);
       acc = make_float4(fmaf(y[k].x, wt, acc.x), fmaf(y[k].y, wt, acc.y), fmaf(y[k].z, wt, acc.z), fmaf(y[k].w, wt, acc.w));
     }

@@ -21,7 +21,8 @@ __device__ __forceinline__ uint32_t dec_pack(float lo, float hi) {
   return r;
 }
 
-// the weight of a partial result of reference m in one of reference M (an empty one has m = -inf)
+// The weight of a partial result of reference m in one of reference M.  An empty one has m = -inf and l = 0, one whose scores
+// are all NaN m = -inf and l NaN: the first is left out where results are joined, the second is not.
 __device__ __forceinline__ float dec_weight(float m, float M) { return m == -INFINITY ? 0.f : exp2f(m - M); }
 __device__ __forceinline__ float dec_inverse(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }
 __device__ __forceinline__ float dec_lse(float m, float l) {
