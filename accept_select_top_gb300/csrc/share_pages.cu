@@ -478,11 +478,14 @@ __global__ void __launch_bounds__(kForkThreads) compact_tables_kernel(CompactPar
       if (id < 0 || id >= N) {
         raise_error(a.error, SPEC_DEV_INDEX);
         id = -1;
-      } else if (id >= limit) {
+      } else {
         const unsigned f = a.bits[id >> 5];
-        const int from = max(limit, id & ~31), at = a.pre_live[id >> 5];
-        if (f >> (id & 31) & 1u) raise_error(a.error, SPEC_DEV_INVARIANT);  // in use, but on the free list
-        else id = a.move_dst[at + __popc(~f & ((1u << (id & 31)) - 1u) & ~((1u << (from & 31)) - 1u))];
+        if (f >> (id & 31) & 1u) {  // in use, but on the free list (below the limit it may be another page's place now)
+          raise_error(a.error, SPEC_DEV_INVARIANT);
+        } else if (id >= limit) {
+          const int from = max(limit, id & ~31), at = a.pre_live[id >> 5];
+          id = a.move_dst[at + __popc(~f & ((1u << (id & 31)) - 1u) & ~((1u << (from & 31)) - 1u))];
+        }
       }
       a.new_page_table[(long long)row * a.row_pages + i] = id;
       count = min(a.page_size, len - i * a.page_size);

@@ -645,7 +645,7 @@ int spec_release_pages(int b, int page_size, const int32_t* req_pool_idx, const 
  * (move_src[i], move_dst[i]), i < n_moves[0], pairs for spec_copy_pages (arrays of
  * free_cap).  The new tables name the new pages: entries [0, ceil(seq_lens[r] /
  * page_size)) of the rows req_pool_idx[r] and, where req_to_token is given, slots
- * [0, seq_lens[r]); every request that holds a page has to be listed.
+ * [0, seq_lens[r]); every request that holds a page has to be listed, once.
  * new_share_counts [num_pages] follow the pages.  new_free_ids: the n_left[0] free
  * pages, highest first, so that the lowest are handed out first and a pool cut to
  * N pages drops the first num_pages - N of them.
@@ -654,9 +654,10 @@ int spec_release_pages(int b, int page_size, const int32_t* req_pool_idx, const 
  * req_pool_idx (SPEC_ERR_ARG).  Where the tables are arrays of their own, the old
  * ones stay readable, and so do the moved pages until their ids are handed out.
  * A bad id on the free list is passed over (SPEC_DEV_INDEX), one listed twice
- * counts once (SPEC_DEV_INVARIANT), as does a table entry that is on it; a bad table
- * entry becomes -1 (SPEC_DEV_INDEX); a bad length or row leaves its row out.  n_free
- * outside [0, free_cap] sets SPEC_DEV_SPACE, and the call does nothing (n_moves 0).
+ * counts once (SPEC_DEV_INVARIANT).  A table entry that is on the free list stays as
+ * it was and sets SPEC_DEV_INVARIANT; a bad table entry becomes -1 (SPEC_DEV_INDEX); a
+ * bad length or row leaves its row out.  n_free outside [0, free_cap] sets
+ * SPEC_DEV_SPACE, and the call does nothing (n_moves 0).
  * Two launches. */
 int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const int32_t* seq_lens, int64_t limit,
                        const int32_t* share_counts, int64_t num_pages, const int32_t* free_ids, int free_cap,
