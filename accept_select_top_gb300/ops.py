@@ -523,11 +523,21 @@ def _slots_in(req_to_token, rows: int, dev: int, what: str):
     return _in(req_to_token, _I32, 1, dev, what), req_to_token.shape[1]
 
 
+def _idle(n_free, n_left, moves, kept, stream):
+    """What the calls behind a fork or a compaction without a request read: no page to copy, and lists as they were (the
+    library leaves every array of an idle call alone)."""
+    with torch.cuda.stream(stream):
+        moves.view(-1)[:1].zero_()
+        for src, dst in [(n_free.view(-1)[:1], n_left)] + kept:
+            if src.data_ptr() != dst.data_ptr():
+                dst.view(-1)[:src.numel()].copy_(src.view(-1))
+
+
 def spec_fork_pages(b: int, page_size: int, parents, children, fork_lens, share_counts, free_ids, n_free, page_table,
                     req_to_token, copy_src, copy_dst, n_copies, n_left, ws: Workspace, stream=None):
     """Children (table rows) that share their parents' whole pages up to fork_lens[r] tokens, with a page of their
     own behind them; see the header.  copy_src, copy_dst and n_copies go to spec_copy_pages.  share_counts has one
-    entry a page of the pool; req_to_token may be None; n_left may be n_free."""
+    entry a page of the pool; req_to_token may be None; n_left may be n_free.  b 0: n_copies becomes 0, n_left n_free."""
     dev = _device()
     rows, row_pages = page_table.shape
     slots, width = _slots_in(req_to_token, rows, dev, "req_to_token")
@@ -538,6 +548,8 @@ def spec_fork_pages(b: int, page_size: int, parents, children, fork_lens, share_
         _in(page_table, _I32, 1, dev, "page_table"), rows, row_pages, slots, width, _in(copy_src, _I32, b, dev, "copy_src"),
         _in(copy_dst, _I32, b, dev, "copy_dst"), _in(n_copies, _I32, 1, dev, "n_copies"), _in(n_left, _I32, 1, dev, "n_left"),
         _workspace_in(ws, dev), ws.nbytes, _raw_stream(stream, dev)), "spec_fork_pages")
+    if b == 0:
+        _idle(n_free, n_left, n_copies, [], stream)
 
 
 def _pool_pages(t: torch.Tensor, page_size: int, dev: int, what: str):
@@ -603,7 +615,8 @@ def spec_compact_pages(b: int, page_size: int, req_pool_idx, seq_lens, limit: in
                        page_table, req_to_token, new_share_counts, new_free_ids, n_left, new_page_table,
                        new_req_to_token, move_src, move_dst, n_moves, ws: Workspace, stream=None):
     """Pages in use moved below `limit` (0: as low as they go): new tables, counts and free list, and the moves for
-    spec_copy_pages.  Every output may be its input; req_to_token and new_req_to_token may be None."""
+    spec_copy_pages.  Every output may be its input; req_to_token and new_req_to_token may be None.  b 0: nothing moves
+    (n_moves 0; the counts and the free list as they were)."""
     dev = _device()
     rows, row_pages = page_table.shape
     if new_page_table.shape != page_table.shape:
@@ -622,6 +635,8 @@ def spec_compact_pages(b: int, page_size: int, req_pool_idx, seq_lens, limit: in
         _in(move_src, _I32, cap, dev, "move_src"), _in(move_dst, _I32, cap, dev, "move_dst"),
         _in(n_moves, _I32, 1, dev, "n_moves"), _workspace_in(ws, dev), ws.nbytes, _raw_stream(stream, dev)),
         "spec_compact_pages")
+    if b == 0:
+        _idle(n_free, n_left, n_moves, [(share_counts, new_share_counts), (free_ids, new_free_ids)], stream)
 
 
 def spec_decode_attention(b: int, Hq: int, Hkv: int, D: int, page_size: int, q, k_pool, v_pool, page_table,

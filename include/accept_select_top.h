@@ -584,6 +584,8 @@ int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size
  * shares (cut back to there, for instance) is forked there first.  num_pages,
  * free_cap and the pages of a call's rows (b * row_pages) are at most 2^30, b at
  * most 16384.  Results do not depend on the order in which a call's threads run.
+ * An idle call (b == 0) leaves n_copies and n_moves as they were, too: the
+ * spec_copy_pages behind it is left out, or its count set to 0 by the caller.
  *
  * spec_fork_pages -- child r (table row children[r]) starts as the first
  * fork_lens[r] tokens of its parent (table row parents[r]).  With L = fork_lens[r]:
