@@ -1046,18 +1046,26 @@ bool table_ok(int b, int page_size, int64_t num_pages, int free_cap, int req_row
          int64_t(b) * row_pages <= kMostPages;
 }
 
-// Arrays that a call writes, which may lie over none of those that it reads to its end, nor over one another.
+// Arrays that a call writes, which may lie over none of those that it reads to its end, nor over one another.  `own`: the
+// one of those read that an array written may be.
 struct Span {
   const void* p;
   size_t bytes;
 };
+struct Out {
+  const void* p;
+  size_t bytes;
+  int own = -1;
+};
 template <size_t N, size_t M>
-bool clash(const Span (&written)[N], const Span (&read)[M]) {
+bool clash(const Out (&written)[N], const Span (&read)[M]) {
+  auto meet = [](const void* a, size_t na, const void* b, size_t nb) { return na && nb && overlap(a, na, b, nb); };
   for (size_t i = 0; i < N; ++i) {
+    const Out& w = written[i];
     for (size_t k = 0; k < i; ++k)
-      if (overlap(written[i].p, written[i].bytes, written[k].p, written[k].bytes)) return true;
-    for (const Span& r : read)
-      if (overlap(written[i].p, written[i].bytes, r.p, r.bytes)) return true;
+      if (meet(w.p, w.bytes, written[k].p, written[k].bytes)) return true;
+    for (size_t k = 0; k < M; ++k)
+      if (meet(w.p, w.bytes, read[k].p, read[k].bytes) && !(int(k) == w.own && w.p == read[k].p)) return true;
   }
   return false;
 }
@@ -1080,7 +1088,7 @@ int spec_fork_pages(int b, int page_size, const int32_t* parents, const int32_t*
     return SPEC_ERR_ARG;
   if (int rc = check_ws(ws, ws_bytes, kHeaderBytes + counters_bytes(b))) return rc;
   const size_t row = size_t(b) * 4;
-  const Span written[] = {{copy_src, row}, {copy_dst, row}, {n_copies, 4}, {n_left, 4}};
+  const Out written[] = {{copy_src, row}, {copy_dst, row}, {n_copies, 4}, {n_left, 4}};
   const Span read[] = {{parents, row}, {children, row}, {fork_lens, row}, {free_ids, size_t(free_cap) * 4}};
   if (clash(written, read)) return SPEC_ERR_ARG;
   note_other(ws);
@@ -1158,21 +1166,15 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
       ((!free_ids || !new_free_ids || !move_src || !move_dst) && free_cap > 0))
     return SPEC_ERR_ARG;
   if (int rc = check_ws(ws, ws_bytes, spec_workspace_size(SPEC_OP_COMPACT_PAGES, b, 1, 1, int(num_pages), 0, 0, 0))) return rc;
-  const size_t row = size_t(b) * 4, list = size_t(free_cap) * 4, counts = size_t(num_pages) * 4;
-  const Span written[] = {{move_src, list}, {move_dst, list}, {n_moves, 4}, {n_left, 4}, {new_free_ids, list}, {new_share_counts, counts}};
-  const Span read[] = {{req_pool_idx, row}, {seq_lens, row}};
+  // The tables' kernel reads while the plan still writes, and its CTAs read while others write.  (Pages of one token: one
+  // array may be both tables, whose entries are then the same.)
+  const size_t row = size_t(b) * 4, list = size_t(free_cap) * 4, counts = size_t(num_pages) * 4, table = size_t(req_rows) * row_pages * 4;
+  const bool one_table = page_size == 1 && req_to_token == page_table && new_req_to_token == new_page_table && row_w == row_pages;
+  const size_t slots = req_to_token && !one_table ? size_t(req_rows) * row_w * 4 : 0;
+  const Span read[] = {{share_counts, counts}, {free_ids, list}, {n_free, 4}, {page_table, table}, {req_to_token, slots}, {req_pool_idx, row}, {seq_lens, row}};
+  const Out written[] = {{new_share_counts, counts, 0}, {new_free_ids, list, 1}, {n_left, 4, 2}, {new_page_table, table, 3}, {new_req_to_token, slots, 4},
+                         {move_src, list}, {move_dst, list}, {n_moves, 4}};
   if (clash(written, read)) return SPEC_ERR_ARG;
-  // (the lists of moves are written while the first list is still read, and read while the counts are written)
-  const Span moves[] = {{move_src, list}, {move_dst, list}}, other[] = {{free_ids, list}, {share_counts, counts}};
-  if (clash(moves, other)) return SPEC_ERR_ARG;
-  // an output may be its input, but not lie over another part of it
-  const size_t table = size_t(req_rows) * row_pages * 4, slots = req_to_token ? size_t(req_rows) * row_w * 4 : 0;
-  const struct {
-    Span from;
-    const void* to;
-  } same[] = {{{share_counts, counts}, new_share_counts}, {{free_ids, list}, new_free_ids}, {{page_table, table}, new_page_table}, {{req_to_token, slots}, new_req_to_token}};
-  for (const auto& x : same)
-    if (x.from.p != x.to && overlap(x.from.p, x.from.bytes, x.to, x.from.bytes)) return SPEC_ERR_ARG;
   note_other(ws);
   const WsView v = ws_view(ws, b);
   CompactParams p{};
@@ -1264,7 +1266,7 @@ int spec_decode_attention(int b, int Hq, int Hkv, int D, int page_size, const vo
     return SPEC_ERR_ARG;
   if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16)) return SPEC_ERR_ARG;
   // (a request's results are written while others are still worked on)
-  const Span written[] = {{out, size_t(b) * Hq * D * 2}, {lse, size_t(b) * Hq * 4}};
+  const Out written[] = {{out, size_t(b) * Hq * D * 2}, {lse, size_t(b) * Hq * 4}};
   const Span read[] = {{q, (size_t(b - 1) * q_ld + size_t(Hq) * D) * 2}, {req_pool_idx, size_t(b) * 4}, {seq_lens, size_t(b) * 4},
                        {group_start, size_t(num_groups + 1) * 4}, {shared_lens, size_t(num_groups) * 4}};
   if (clash(written, read)) return SPEC_ERR_ARG;

@@ -652,8 +652,8 @@ int spec_release_pages(int b, int page_size, const int32_t* req_pool_idx, const 
  * pages, highest first, so that the lowest are handed out first and a pool cut to
  * N pages drops the first num_pages - N of them.
  * Each output may be its input (n_left may be n_free), but lie over no other part
- * of it; the lists of moves lie over nothing else, and no output over seq_lens or
- * req_pool_idx (SPEC_ERR_ARG).  Where the tables are arrays of their own, the old
+ * of it, nor over another input or output (SPEC_ERR_ARG; with pages of one token, one
+ * array may be both tables).  Where the tables are arrays of their own, the old
  * ones stay readable, and so do the moved pages until their ids are handed out.
  * A bad id on the free list is passed over (SPEC_DEV_INDEX), one listed twice
  * counts once (SPEC_DEV_INVARIANT).  A table entry that is on the free list stays as
