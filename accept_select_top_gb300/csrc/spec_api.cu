@@ -1087,9 +1087,11 @@ int spec_fork_pages(int b, int page_size, const int32_t* parents, const int32_t*
       !n_copies || !n_left || n_copies == n_free || (!free_ids && free_cap > 0))
     return SPEC_ERR_ARG;
   if (int rc = check_ws(ws, ws_bytes, kHeaderBytes + counters_bytes(b))) return rc;
-  const size_t row = size_t(b) * 4;
-  const Out written[] = {{copy_src, row}, {copy_dst, row}, {n_copies, 4}, {n_left, 4}};
-  const Span read[] = {{parents, row}, {children, row}, {fork_lens, row}, {free_ids, size_t(free_cap) * 4}};
+  // (pages of one token: one array may be both tables, whose entries are then the same)
+  const bool one_table = page_size == 1 && req_to_token == page_table && row_w == row_pages;
+  const size_t row = size_t(b) * 4, table = size_t(req_rows) * row_pages * 4, slots = req_to_token && !one_table ? size_t(req_rows) * row_w * 4 : 0;
+  const Span read[] = {{parents, row}, {children, row}, {fork_lens, row}, {free_ids, size_t(free_cap) * 4}, {n_free, 4}};
+  const Out written[] = {{share_counts, size_t(num_pages) * 4}, {page_table, table}, {req_to_token, slots}, {copy_src, row}, {copy_dst, row}, {n_copies, 4}, {n_left, 4, 4}};
   if (clash(written, read)) return SPEC_ERR_ARG;
   note_other(ws);
   const WsView v = ws_view(ws, b);

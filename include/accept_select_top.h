@@ -597,11 +597,12 @@ int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size
  * less them (may be n_free itself).  req_to_token (nullable): entries [0, L) of
  * the child's row.  A parent may have many children, and L be less than it has;
  * the children are distinct rows that hold no pages, none of them a parent in the
- * call (a child that is its own parent sets SPEC_DEV_INDEX).  The written arrays
- * lie over none of the lists that the call reads (SPEC_ERR_ARG).  A bad length or
- * row leaves its child as it was (SPEC_DEV_LENGTH / SPEC_DEV_INDEX); too short a
- * free list sets SPEC_DEV_SPACE and the call does nothing (n_copies 0, n_left =
- * n_free).  A bad page id gives an entry (and slots) of -1 and SPEC_DEV_INDEX.
+ * call (a child that is its own parent sets SPEC_DEV_INDEX).  The written arrays,
+ * the tables and counts among them, lie over none of the lists that the call reads,
+ * nor over one another (SPEC_ERR_ARG; with pages of one token, one array may be both
+ * tables).  A bad length or row leaves its child as it was (SPEC_DEV_LENGTH /
+ * SPEC_DEV_INDEX); too short a free list sets SPEC_DEV_SPACE and the call
+ * does nothing (n_copies 0, n_left = n_free).  A bad page id gives an entry (and slots) of -1 and SPEC_DEV_INDEX.
  * ------------------------------------------------------------------------- */
 int spec_fork_pages(int b, int page_size, const int32_t* parents, const int32_t* children, const int32_t* fork_lens,
                     int32_t* share_counts, int64_t num_pages, const int32_t* free_ids, int free_cap,

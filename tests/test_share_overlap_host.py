@@ -59,3 +59,37 @@ def test_compaction_refuses_overlaps(lib, written, other):
                         [BASE, BASE + 256, BASE + 512, BASE + 768, BASE + 1024, BASE + 2048, BASE + 4096, BASE + 8192, BASE + 8448, BASE + 8704])), **APART}
     for at in (where[other], where[other] + BYTES[other] - 4, where[other] - BYTES[written] + 4):
         assert lib.spec_compact_pages(*_compact(**{**APART, written: at})) == REFUSED
+
+
+FORK = dict(parents=BASE, children=BASE + 256, lens=BASE + 512, counts=BASE + 1024, free=BASE + 2048, n_free=BASE + 2304, table=BASE + 4096, slots=BASE + 8192, src=BASE + 12288, dst=BASE + 12544,
+            copies=BASE + 12800, left=BASE + 13056)
+FORK_BYTES = dict(parents=8, children=8, lens=8, counts=40, free=32, n_free=4, table=128, slots=2048, src=8, dst=8, copies=4, left=4)
+FORK_WRITTEN = ["counts", "table", "slots", "src", "dst", "copies", "left"]
+
+
+def _fork(**change):
+    """Two children, 10 pages of 16, a list of 8, tables of 4 rows of 8 pages and 128 slots."""
+    a = dict(b=2, ps=16, parents=0, children=0, lens=0, counts=0, pages=10, free=0, cap=8, n_free=0, table=0, rows=4, row_pages=8, slots=0, row_w=128, src=0, dst=0, copies=0, left=0, ws=BASE + (1 << 20),
+             ws_bytes=1 << 20, stream=None)
+    a.update({**FORK, **change})
+    return list(a.values())
+
+
+def test_forks_are_accepted(lib):
+    assert lib.spec_fork_pages(*_fork()) == LAUNCH
+    assert lib.spec_fork_pages(*_fork(left=FORK["n_free"])) == LAUNCH
+    assert lib.spec_fork_pages(*_fork(slots=None, row_w=0)) == LAUNCH
+    assert lib.spec_fork_pages(*_fork(cap=0, free=None)) == LAUNCH
+    assert lib.spec_fork_pages(*_fork(children=BASE, lens=BASE)) == LAUNCH  # (what is only read may be one array)
+    assert lib.spec_fork_pages(*_fork(src=BASE + 8, dst=BASE + 16, copies=BASE + 24, left=BASE + 28)) == LAUNCH
+    one = dict(ps=1, slots=FORK["table"], row_w=8)  # pages of one token: the page table is the slot table
+    assert lib.spec_fork_pages(*_fork(**one)) == LAUNCH
+    assert lib.spec_fork_pages(*_fork(**{**one, "row_w": 16})) == REFUSED
+    assert lib.spec_fork_pages(*_fork(**{**one, "ps": 2})) == REFUSED
+
+
+@pytest.mark.parametrize("written, other", [(w, o) for w in FORK_WRITTEN for o in FORK_BYTES if w != o])
+def test_fork_refuses_overlaps(lib, written, other):
+    for at in (FORK[other], FORK[other] + FORK_BYTES[other] - 4, FORK[other] - FORK_BYTES[written] + 4):
+        want = LAUNCH if (written, other) == ("left", "n_free") else REFUSED
+        assert lib.spec_fork_pages(*_fork(**{written: at})) == want
