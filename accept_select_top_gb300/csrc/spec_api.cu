@@ -1130,6 +1130,10 @@ int spec_release_pages(int b, int page_size, const int32_t* req_pool_idx, const 
   if (!req_pool_idx || !seq_lens || !share_counts || !n_free || !page_table || !n_left || (!free_ids && free_cap > 0))
     return SPEC_ERR_ARG;
   if (int rc = check_ws(ws, ws_bytes, spec_workspace_size(SPEC_OP_RELEASE_PAGES, b, 1, 1, int(num_pages), 0, 0, 0))) return rc;
+  const size_t row = size_t(b) * 4;
+  const Span read[] = {{req_pool_idx, row}, {seq_lens, row}, {keep_lens, row}, {n_free, 4}, {page_table, size_t(req_rows) * row_pages * 4}};
+  const Out written[] = {{share_counts, size_t(num_pages) * 4}, {free_ids, size_t(free_cap) * 4}, {n_left, 4, 3}};
+  if (clash(written, read)) return SPEC_ERR_ARG;
   note_other(ws);
   const WsView v = ws_view(ws, b);
   ReleaseParams p{};

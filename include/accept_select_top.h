@@ -602,7 +602,8 @@ int spec_verify_attention_q8(int b, int n, int Hq, int Hkv, int D, int page_size
  * nor over one another (SPEC_ERR_ARG; with pages of one token, one array may be both
  * tables).  A bad length or row leaves its child as it was (SPEC_DEV_LENGTH /
  * SPEC_DEV_INDEX); too short a free list sets SPEC_DEV_SPACE and the call
- * does nothing (n_copies 0, n_left = n_free).  A bad page id gives an entry (and slots) of -1 and SPEC_DEV_INDEX.
+ * does nothing (n_copies 0, n_left = n_free).  A bad page id gives an entry (and
+ * slots) of -1 and SPEC_DEV_INDEX.
  * ------------------------------------------------------------------------- */
 int spec_fork_pages(int b, int page_size, const int32_t* parents, const int32_t* children, const int32_t* fork_lens,
                     int32_t* share_counts, int64_t num_pages, const int32_t* free_ids, int free_cap,
@@ -631,7 +632,8 @@ int spec_copy_pages(int num_layers, int64_t page_bytes, int scale_bytes, void* c
  * in the order in which they are first given up (request order, then page order),
  * are pushed last one first, so that what one spec_alloc_slots or spec_fork_pages
  * took goes back to where it was.  free_ids is changed behind its n_free[0] entries;
- * n_left [1] = the new count (may be n_free itself).  Table rows keep their
+ * n_left [1] = the new count (may be n_free itself).  The counts, the free list and
+ * n_left lie over nothing else of the call (SPEC_ERR_ARG).  Table rows keep their
  * entries.  A bad length or row leaves its request out (SPEC_DEV_LENGTH /
  * SPEC_DEV_INDEX), a bad page id its page; a page given up more often than it is
  * held is freed once and sets SPEC_DEV_INVARIANT.  Pages that do not fit into

@@ -93,3 +93,28 @@ def test_fork_refuses_overlaps(lib, written, other):
     for at in (FORK[other], FORK[other] + FORK_BYTES[other] - 4, FORK[other] - FORK_BYTES[written] + 4):
         want = LAUNCH if (written, other) == ("left", "n_free") else REFUSED
         assert lib.spec_fork_pages(*_fork(**{written: at})) == want
+
+
+RELEASE = dict(idx=BASE, lens=BASE + 256, keep=BASE + 512, counts=BASE + 1024, free=BASE + 2048, n_free=BASE + 2304, table=BASE + 4096, left=BASE + 8192)
+RELEASE_BYTES = dict(idx=8, lens=8, keep=8, counts=40, free=32, n_free=4, table=128, left=4)
+
+
+def _release(**change):
+    a = dict(b=2, ps=16, idx=0, lens=0, keep=0, counts=0, pages=10, free=0, cap=8, n_free=0, table=0, rows=4, row_pages=8, left=0, ws=BASE + (1 << 20), ws_bytes=1 << 20, stream=None)
+    a.update({**RELEASE, **change})
+    return list(a.values())
+
+
+def test_releases_are_accepted(lib):
+    assert lib.spec_release_pages(*_release()) == LAUNCH
+    assert lib.spec_release_pages(*_release(left=RELEASE["n_free"])) == LAUNCH
+    assert lib.spec_release_pages(*_release(keep=None)) == LAUNCH
+    assert lib.spec_release_pages(*_release(keep=RELEASE["lens"])) == LAUNCH
+    assert lib.spec_release_pages(*_release(cap=0, free=None)) == LAUNCH
+
+
+@pytest.mark.parametrize("written, other", [(w, o) for w in ("counts", "free", "left") for o in RELEASE_BYTES if w != o])
+def test_release_refuses_overlaps(lib, written, other):
+    for at in (RELEASE[other], RELEASE[other] + RELEASE_BYTES[other] - 4, RELEASE[other] - RELEASE_BYTES[written] + 4):
+        want = LAUNCH if (written, other) == ("left", "n_free") else REFUSED
+        assert lib.spec_release_pages(*_release(**{written: at})) == want
