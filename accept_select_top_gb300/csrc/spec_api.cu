@@ -1274,7 +1274,7 @@ int spec_decode_attention(int b, int Hq, int Hkv, int D, int page_size, const vo
   // (a request's results are written while others are still worked on)
   const Out written[] = {{out, size_t(b) * Hq * D * 2}, {lse, size_t(b) * Hq * 4}};
   const Span read[] = {{q, (size_t(b - 1) * q_ld + size_t(Hq) * D) * 2}, {req_pool_idx, size_t(b) * 4}, {seq_lens, size_t(b) * 4},
-                       {group_start, size_t(num_groups + 1) * 4}, {shared_lens, size_t(num_groups) * 4}};
+                       {page_table, size_t(req_rows) * row_pages * 4}, {group_start, size_t(num_groups + 1) * 4}, {shared_lens, size_t(num_groups) * 4}};
   if (clash(written, read)) return SPEC_ERR_ARG;
   if (int rc = check_ws(ws, ws_bytes, spec_workspace_size(SPEC_OP_DECODE_ATTENTION, b, 1, 1, 1, Hq, Hkv, max_seq_len))) return rc;
   note_other(ws);

@@ -684,8 +684,8 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
  * seq_lens[r]-1, the new one's K and V being in the pools already:
  *   out[r, h] = softmax(scale * q.K^T) V,  lse (nullable) = its natural-log
  * sum-exp.  out: [b, Hq, D] bf16, lse: [b, Hq] fp32.  A request without a token
- * gives out 0 and lse -inf.  out and lse lie over none of q, the lengths, rows and
- * groups, nor over one another (SPEC_ERR_ARG).
+ * gives out 0 and lse -inf.  out and lse lie over none of q, the table, the lengths,
+ * rows and groups, nor over one another (SPEC_ERR_ARG).
  *   Group g: requests group_start[g] .. group_start[g+1]-1 (ascending, [num_groups
  * + 1]; requests before the first and behind the last are in none), whose tables
  * name the same pages for their tokens 0 .. shared_lens[g]-1; these are read

@@ -118,3 +118,22 @@ def test_release_refuses_overlaps(lib, written, other):
     for at in (RELEASE[other], RELEASE[other] + RELEASE_BYTES[other] - 4, RELEASE[other] - RELEASE_BYTES[written] + 4):
         want = LAUNCH if (written, other) == ("left", "n_free") else REFUSED
         assert lib.spec_release_pages(*_release(**{written: at})) == want
+
+
+DECODE = dict(q=BASE, table=BASE + 8192, idx=BASE + 16384, lens=BASE + 16640, start=BASE + 16896, shared=BASE + 17152, out=BASE + 20480, lse=BASE + 32768)
+DECODE_BYTES = dict(q=2 * 2 * 1024, table=128, idx=8, lens=8, start=8, shared=4, out=2 * 8 * 128 * 2, lse=2 * 8 * 4)
+
+
+def _decode(**change):
+    a = dict(b=2, Hq=8, Hkv=2, D=128, ps=16, q=0, q_ld=1024, k=BASE + (1 << 20), v=BASE + (2 << 20), slots=160, table=0, rows=4, row_pages=8, idx=0, lens=0, most=100, groups=1, start=0, shared=0, scale=0.1,
+             out=0, lse=0, ws=BASE + (16 << 20), ws_bytes=1 << 28, stream=None)
+    a.update({**DECODE, **change})
+    return list(a.values())
+
+
+@pytest.mark.parametrize("written, other", [(w, o) for w in ("out", "lse") for o in DECODE_BYTES if w != o])
+def test_decode_refuses_overlaps(lib, written, other):
+    assert lib.spec_decode_attention(*_decode()) == LAUNCH
+    step = 16 if written == "out" else 4  # (its alignment)
+    for at in (DECODE[other], DECODE[other] - DECODE_BYTES[written] + step, DECODE[other] + (DECODE_BYTES[other] - 1) // step * step):
+        assert lib.spec_decode_attention(*_decode(**{written: at})) == REFUSED
