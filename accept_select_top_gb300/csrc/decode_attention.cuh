@@ -11,9 +11,10 @@ constexpr int kDecRows = 64;    // query rows of a unit
 constexpr int kDecMaxCtas = 192;  // upper bound of a grid of one CTA a SM; sizes the fragment slots
 
 // P at a row's maximum when its reference is set, and how far the maximum may grow before it is set again: P stays below
-// 2^-24, so the sums of any number of values that 32 bits count stay below the largest of them.  (What that costs:
-// products below 2^-126, of values below 2^-94.)
-constexpr float kDecBase = -32.f, kDecLazy = 8.f;
+// 2^-32, so the sums of the 2^30 values that a request may have stay below a quarter of the largest of them.  (What that costs:
+// products below 2^-126, of values below 2^-86.)
+constexpr float kDecBase = -40.f, kDecLazy = 8.f;
+constexpr float kDecUnit = 1099511627776.f;  // 2^-kDecBase
 
 __device__ __forceinline__ uint32_t dec_pack(float lo, float hi) {
   uint32_t r;
@@ -25,8 +26,9 @@ __device__ __forceinline__ uint32_t dec_pack(float lo, float hi) {
 // are all NaN m = -inf and l NaN: the first is left out where results are joined, the second is not.
 __device__ __forceinline__ float dec_weight(float m, float M) { return m == -INFINITY ? 0.f : exp2f(m - M); }
 __device__ __forceinline__ float dec_inverse(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }
+// (l is brought back to the weights' own scale first, where a row's largest is 1: the logarithm's rounding is then that of its sum)
 __device__ __forceinline__ float dec_lse(float m, float l) {
-  return l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  return l > 0.f || l != l ? ((m + kDecBase) + log2f(l * kDecUnit)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Rows of a group's shared tokens (members times q heads of a kv head) above which the tcgen05 kernel takes them.  In us,

@@ -10,7 +10,7 @@
 //   12, 13    issue S = Q K^T (M 128, N 64, K D) of groups 0, 1; 14, 15: O += P V (A = P from TMEM)
 // TMEM: O0 O1 | two S buffers a group; P (bf16, two to a column) takes the place of its S, so that the scores of
 // the next tile are computed, and the products of the last one added up, while a tile's softmax runs.
-//   P is taken against a reference that moves only when a tile's sum of P passes 2^-24 (kDecBase).
+//   P is taken against a reference that moves only when a tile's sum of P passes 2^-32 (kDecBase, kDecLazy).
 //   Every piece of a unit leaves an fp32 partial result; decode_attention.cu joins them.
 //   Bound: up to 128 rows the cache's bytes (eight groups of 12 requests, 32768 shared tokens, 32 / 8 heads: 193 us a call,
 // 1.1 GB); 256 rows: shared memory.  S with both operands there reads 6 KB in 32 cycles of the tensor cores, so that a tile
@@ -32,7 +32,7 @@ constexpr int kRows = 128;
 constexpr int kTallThreads = 16 * 32;
 constexpr int kMostStages = 10;
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s: bound of every wait
-constexpr float kSumMost = 5.9604644775390625e-08f;  // 2^-24
+constexpr float kSumMost = 2.3283064365386963e-10f;  // 2^(kDecBase + kDecLazy)
 __host__ __device__ constexpr uint32_t col_o(int w) { return 128u * uint32_t(w); }
 __host__ __device__ constexpr uint32_t col_s(int w, int b) { return 256u + 128u * uint32_t(w) + 64u * uint32_t(b); }
 
