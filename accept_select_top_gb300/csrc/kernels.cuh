@@ -445,7 +445,7 @@ struct ReleaseParams {
   int req_rows, row_pages;
   int32_t* n_left;
   uint32_t* error;
-  uint32_t* counters;  // two
+  uint32_t* counters;  // two: CTAs that came to the meetings, and that left
   int* totals;         // a CTA each
   int2* note;          // [num_pages]
 };

@@ -110,26 +110,33 @@ constexpr int kClusterMost = 16;
 constexpr int kReleaseMostCtas = 192;
 constexpr long long kBarrierCycles = 4000000000ll;  // about 2 s: bound of a wait for the other CTAs
 
-// All CTAs of a cooperative launch, for the round-th time (from 1) of `rounds`; what they wrote before is seen after.  The
-// last arrival of the last round takes the counter back to zero.  False (in every thread) if they do not come.
-__device__ __forceinline__ bool grid_sync(uint32_t* arrivals, uint32_t round, uint32_t rounds, uint32_t* error) {
+// All CTAs of a cooperative launch, for the round-th time (from 1); what they wrote before is seen after.  False (in every
+// thread) if they do not come.
+__device__ __forceinline__ bool grid_sync(uint32_t* arrivals, uint32_t round, uint32_t* error) {
   __shared__ int s_ok;
   __syncthreads();
   if (threadIdx.x == 0) {
-    const uint32_t ctas = gridDim.x, before = (round - 1) * ctas;  // (zero is as far from `before` as any count behind it)
-    uint32_t now;
-    asm volatile("atom.inc.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(now) : "l"(arrivals), "r"(rounds * ctas - 1) : "memory");
-    bool ok = now + 1 - before >= ctas;
+    const uint32_t want = round * gridDim.x;
+    bool ok = int(atom_add_acq_rel(arrivals) + 1 - want) >= 0;
     const long long start = clock64();
     while (!ok && clock64() - start <= kBarrierCycles) {
+      uint32_t now;
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(arrivals) : "memory");
-      ok = now - before >= ctas;
+      ok = int(now - want) >= 0;
     }
     if (!ok) raise_error(error, SPEC_DEV_TIMEOUT);
     s_ok = ok;
   }
   __syncthreads();
   return s_ok;
+}
+// Each CTA, once, behind its last meeting: the last of them takes the arrivals back to zero, wherever the meetings ended (the
+// count of those that left wraps by itself).
+__device__ __forceinline__ void grid_leave(uint32_t* counters) {
+  if (threadIdx.x != 0) return;
+  uint32_t before;
+  asm volatile("atom.inc.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(before) : "l"(counters + 1), "r"(gridDim.x - 1) : "memory");
+  if (before == gridDim.x - 1) atomicExch(counters, 0u);
 }
 
 template <bool CLUSTER>
@@ -147,7 +154,9 @@ __global__ void __launch_bounds__(kClusterThreads) release_pages_kernel(ReleaseP
       cluster_sync();
       return true;
     }
-    return grid_sync(a.counters, ++met, 4, a.error);
+    const bool all = grid_sync(a.counters, ++met, a.error);
+    if (!all || met == 4) grid_leave(a.counters);
+    return all;
   };
   const int E = scan_counts<kClusterThreads>(a.b, pre, wsum, [&](int r) {
     const int len = a.seq_lens[r], keep = a.keep_lens ? a.keep_lens[r] : 0, row = a.req_pool_idx[r];

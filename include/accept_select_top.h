@@ -42,6 +42,8 @@
  *   - Indices read from device arrays are bounds-checked on the device; a bad
  *     one sets a bit in the workspace error word and the access is skipped (no
  *     trap).  spec_last_error() reads and clears that word.
+ *     SPEC_DEV_TIMEOUT: what the call was to write is not whole, and the workspace is
+ *     zero-filled (spec_workspace_init) before it serves another call.
  *   - Tree arrays use -1 for "none"; a verify row is the flattened index
  *     b*n + i of request b's tree node i [ACCEPT section 3].
  *   - Limits: 1 <= k <= 16, k <= V, 1 <= n <= 64, n - 1 <= k + (S-1)*k*k,
