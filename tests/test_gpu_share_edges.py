@@ -1,7 +1,8 @@
-"""Page sharing on the GPU where its lists are at odds with one another."""
+"""Page sharing on the GPU where its lists are at odds with one another, and with as many requests as a call takes."""
 import pytest
 
-from tests.test_gpu_share import _ops, _ws, i32
+from tests import share_reference as R
+from tests.test_gpu_share import Cache, _ops, _ws, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +33,31 @@ def test_compaction_tells_of_entries_on_the_free_list(in_place):
     # a limit above every page: nothing is moved, and an entry on the list is told all the same
     assert compact([[0, 7, -1], [5, 2, -1]], [8, 8], limit=8) == (0, [[0, 7, -1], [5, 2, -1]])
     assert compact([[0, 4, -1], [5, 2, -1]], [8, 8], limit=8) == (ops.DEV_INVARIANT, [[0, 4, -1], [5, 2, -1]])
+
+
+def test_the_most_requests_of_a_call():
+    """16384 children of two prompts, grown by nothing, given back one half at a time; a compaction that lists them all."""
+    ops = _ops()
+    n, page = 16384, 8
+    c = Cache(page, [20, 9], n + 2, 4, n + 3)
+    ws = _ws(ops, ops.OP_FORK_PAGES, ops.OP_RELEASE_PAGES, ops.OP_COMPACT_PAGES, b=n, pages=c.total)
+    r = c.rows
+    lens = [(20, 17, 8)[i % 3] if i % 5 else 9 for i in range(n)]
+    c.fork(ws, [r[0] if i % 5 else r[1] for i in range(n)], r[2:], lens)
+    assert ws.last_error() == 0
+    c.same()
+    c.release(ws, r[2:n // 2], lens[:n // 2 - 2])
+    assert ws.last_error() == 0
+    c.same()
+    rows, held = r[:2] + r[n // 2:], [20, 9] + lens[n // 2 - 2:]  # (fewer than a call takes)
+    src, dst, moves = (i32([-5] * c.total) for _ in range(3))
+    t = c.t
+    ops.spec_compact_pages(len(rows), page, i32(rows), i32(held), 0, t["counts"], t["free"], t["n"], t["table"], None, t["counts"], t["free"], t["n"], t["table"], None, src, dst, moves, ws)
+    assert ws.last_error() == 0
+    want, c.n_free = R.compact(page, rows, held, 0, c.counts, c.free, c.n_free, c.table)
+    c.same()
+    assert moves.tolist()[0] == len(want) and list(zip(src.tolist(), dst.tolist()))[:len(want)] == want
+    c.release(ws, rows, held)
+    assert ws.last_error() == 0
+    c.same()
+    assert c.n_free == c.total
