@@ -639,7 +639,9 @@ int spec_copy_pages(int num_layers, int64_t page_bytes, int scale_bytes, void* c
  * entries.  A bad length or row leaves its request out (SPEC_DEV_LENGTH /
  * SPEC_DEV_INDEX), a bad page id its page; a page given up more often than it is
  * held is freed once and sets SPEC_DEV_INVARIANT.  Pages that do not fit into
- * free_cap set SPEC_DEV_SPACE, and the call does nothing. */
+ * free_cap set SPEC_DEV_SPACE, and the call does nothing.  A call whose rows have room
+ * for more than 131072 pages (b * row_pages) goes over all SMs, however few it gives
+ * up: a few pages then take 15 to 17 us, not 8. */
 int spec_release_pages(int b, int page_size, const int32_t* req_pool_idx, const int32_t* seq_lens,
                        const int32_t* keep_lens, int32_t* share_counts, int64_t num_pages, int32_t* free_ids,
                        int free_cap, const int32_t* n_free, const int32_t* page_table, int req_rows, int row_pages,
@@ -695,15 +697,26 @@ int spec_compact_pages(int b, int page_size, const int32_t* req_pool_idx, const 
  * tokens through its own row, and so does every one where the first member is
  * shorter.  num_groups 0: both arrays may be NULL.  Group bounds that descend or
  * leave the batch set SPEC_DEV_INDEX, and nothing is shared; a negative shared
- * length, or one above max_seq_len, sets SPEC_DEV_LENGTH.  Requests that share
- * nothing are best left out of the groups: which kernels run goes by their mean size.
- *   max_seq_len bounds every seq_len (a larger one sets SPEC_DEV_LENGTH and is
- * clamped).  A page id out of range sets SPEC_DEV_INDEX and its keys do not count;
- * a bad table row leaves its request without tokens.  What the pools hold behind a
- * request's last token is not looked at.  A call's results are always the same
- * bits.  D 64 or 128, b <= 2048, num_groups <= b, max_seq_len <= 2^30; the ticks,
+ * length, or one above max_seq_len or what a table row holds, sets SPEC_DEV_LENGTH.
+ * Which kernels run goes by b / num_groups, as the groups themselves are on the device:
+ * requests that share nothing are best left out of the groups, and a call of many of
+ * them beside a few that share a little is quicker without groups (200 alone and a
+ * pair, 1024 tokens each, 512 of the pair's shared: 154 us with its group, 145 without).
+ *   max_seq_len and what a table row holds bound every seq_len (a larger one sets
+ * SPEC_DEV_LENGTH and is clamped).  A close max_seq_len is quicker where requests are
+ * few and short: without groups, and up to 64 q heads a kv head, as many pairs of a
+ * request and a kv head as there are SMs are one launch as long as max_seq_len is at
+ * most 24 tiles (of 64 keys; heads of 64: of 128) for each CTA of a pair (8 up to 14
+ * pairs, 4 up to 34, 2 up to 72, else 1).  One request of 1001 tokens takes 6.2 us so,
+ * 12.6 with a max_seq_len of 131072.
+ *   A page id out of range sets SPEC_DEV_INDEX and its keys do not count; a bad table
+ * row leaves its request without tokens.  What the pools hold behind a request's last
+ * token is not looked at.  A NaN in what a request sees (q, K, V) comes out of it.  A
+ * call's results are always the same bits.  D 64 or 128, b <= 2048, num_groups <= b,
+ * max_seq_len <= 2^30; the ticks,
  * b * (max_seq_len / 16 + 8) * Hkv * ceil(Hq / Hkv / 64), stay below 2^30.
- * HBM-bound.
+ * The workspace has 13 MB and 1 KB for each row of q; where b * Hq / Hkv is above 16,
+ * 64 MB and 2 KB, whether there are groups or not.  HBM-bound.
  * ------------------------------------------------------------------------- */
 int spec_decode_attention(int b, int Hq, int Hkv, int D, int page_size, const void* q, int64_t q_ld,
                           const void* k_pool, const void* v_pool, int64_t num_slots, const int32_t* page_table,
