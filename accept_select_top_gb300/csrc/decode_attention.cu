@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_attention_kernel(const 
       for (int q = 0; q < kClusterMost; ++q) M = fmaxf(M, ml[q].x);
 #pragma unroll
       for (int q = 0; q < kClusterMost; ++q) {
-        if (ml[q].y == 0.f) continue;  // (a CTA that has seen nothing; one that has counts under any weight, for its NaN)
+        if (q >= size) break;
         const float wt = dec_weight(ml[q].x, M);
         Ls = fmaf(ml[q].y, wt, Ls);
         acc = make_float4(fmaf(y[q].x, wt, acc.x), fmaf(y[q].y, wt, acc.y), fmaf(y[q].z, wt, acc.z), fmaf(y[q].w, wt, acc.w));
@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     float4 y[kOnce];
 #pragma unroll
     for (int k = 0; k < kOnce; ++k) {
-      v[k] = make_float2(-INFINITY, 0.f);
+      v[k] = make_float2(-INFINITY, kDecNone);
       if (q0 + k < np) {
         const Part p = part(q0 + k);
         v[k] = __ldcg(p.ml);
@@ -902,7 +902,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     acc = make_float4(acc.x * was, acc.y * was, acc.z * was, acc.w * was);
 #pragma unroll
     for (int k = 0; k < kOnce; ++k) {
-      if (v[k].y == 0.f) continue;  // (a part that has seen nothing: its O may not have been written)
+      if (v[k].y < 0.f) continue;
       const float wt = dec_weight(v[k].x, M);
       Ls = fmaf(v[k].y, wt, Ls);
       acc = make_float4(fmaf(y[k].x, wt, acc.x), fmaf(y[k].y, wt, acc.y), fmaf(y[k].z, wt, acc.z), fmaf(y[k].w, wt, acc.w));

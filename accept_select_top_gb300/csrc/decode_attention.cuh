@@ -22,8 +22,10 @@ __device__ __forceinline__ uint32_t dec_pack(float lo, float hi) {
   return r;
 }
 
-// The weight of a partial result of reference m in one of reference M.  An empty one has m = -inf and l = 0, one whose scores
-// are all NaN m = -inf and l NaN: the first is left out where results are joined, the second is not.
+// The weight of a partial result of reference m in one of reference M.  One that has seen nothing, or only scores of -inf or
+// NaN, has m = -inf and the weight 0; it counts all the same where results are joined, for the NaN that its l or O may hold.  Only
+// one whose O was not written is left out: its l is kDecNone.
+constexpr float kDecNone = -1.f;
 __device__ __forceinline__ float dec_weight(float m, float M) { return m == -INFINITY ? 0.f : exp2f(m - M); }
 __device__ __forceinline__ float dec_inverse(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }
 // (l is brought back to the weights' own scale first, where a row's largest is 1: the logarithm's rounding is then that of its sum)

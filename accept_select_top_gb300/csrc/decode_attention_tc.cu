@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(kTallThreads, 1) decode_attention_tc_kernel(co
         tc_before();
         mbar_arrive(bar(kOFree0 + w));  // the next piece may write O
       }
-      if (valid) *pm = make_float2(m, l);  // (without a tile: m = -inf, and its O is not read)
+      if (valid) *pm = make_float2(m, mine ? l : kDecNone);  // (without a tile: its O is not read)
       p = pn;
       f = fn;
       n = nn;

@@ -102,3 +102,42 @@ def test_a_value_of_nan_under_a_small_weight(groups, alone, D):
     same = torch.ones(c.b, c.Hq, D, dtype=torch.bool, device=out.device)
     same[r, :half, 9] = False
     assert torch.equal(out[same], clean[0][same]) and torch.equal(lse, clean[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("groups, alone", [
+    ([], [1001]), ([], [64, 9000] + [40] * 99), ([], [7 * 64 + 1]), ([], [7 * 128 + 1]), ([(64, [65, 70])], []), ([(640, [641] + [700] * 11)], []), ([(2048, [2049] + [2100] * 39)], [])])
+def test_a_value_of_nan_under_no_weight(groups, alone, D):
+    """The last key's scores are -inf: a weight of 0, and 0 times NaN is NaN, in 64 bits too.  A finite value there is without effect."""
+    c = Case(groups, alone, D=D, seed=7)
+    r = 1 if len(alone) > 1 else 0
+    at = c.slots_of(r)[-1]
+    c.q[r, :, 0] = 8.0
+    c.k[at, :, 0] = -math.inf
+    clean = c.call()
+    c.check(*clean)
+    c.v[at, 0, 9] = math.nan
+    out, lse = c.call()
+    half = c.Hq // c.Hkv
+    assert out[r, :half, 9].isnan().all()
+    same = torch.ones(c.b, c.Hq, D, dtype=torch.bool, device=out.device)
+    same[r, :half, 9] = False
+    assert torch.equal(out[same], clean[0][same]) and torch.equal(lse, clean[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("groups, alone", [([], [449]), ([], [64, 9000] + [40] * 99), ([(64, [65, 70])], []), ([(640, [641] + [700] * 11)], [])])
+def test_scores_of_minus_infinity_only(groups, alone, D):
+    """No key of one request has any weight: out 0 and lse -inf, as without a token."""
+    c = Case(groups, alone, D=D, seed=7)
+    r = 1 if len(alone) > 1 else 0
+    c.q[r, :, 0] = -8.0
+    others = c.call()
+    keep = c.k.clone()
+    c.k[c.slots_of(r), :, 0] = math.inf
+    out, lse = c.call()
+    assert (out[r] == 0).all() and (lse[r] == -math.inf).all()
+    c.k = keep
+    if not groups:
+        rest = [x for x in range(c.b) if x != r]
+        assert torch.equal(out[rest], others[0][rest]) and torch.equal(lse[rest], others[1][rest])
